@@ -1,8 +1,10 @@
-"""Build ``libdlrm_sparse.so`` in-tree with nvcc for sm_100a.
+"""Build ``libdlrm_sparse.so`` and ``libdlrm_tokens.so`` in-tree with nvcc for sm_100a.
 
 ``python -m dlrm_embedding_bag_b200.build`` (or ``__graft_entry__.build()``)
-compiles every ``csrc/*.cu`` to an object in parallel and links the shared
-library next to this file. nvcc cross-compiles, so no GPU is needed.
+compiles every ``csrc/*.cu`` (the stage and its MLP layers) and every
+``csrc/tokens/*.cu`` (the token-level operators and the 8-bit layers) to an
+object in parallel and links the two shared libraries next to this file. nvcc
+cross-compiles, so no GPU is needed.
 """
 from __future__ import annotations
 
@@ -15,9 +17,11 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
+CSRC_TOKENS = os.path.join(CSRC, "tokens")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libdlrm_sparse.so")
+LIB_TOKENS = os.path.join(HERE, "libdlrm_tokens.so")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -26,7 +30,7 @@ FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler",
 
 
 def _compile(src: str, verbose: bool) -> str:
-    obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
+    obj = os.path.join(BUILD_DIR, os.path.relpath(src, CSRC).replace(os.sep, "_") + ".o")
     cmd = [NVCC, *ARCH, *FLAGS, "-c", src, "-o", obj]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
@@ -38,28 +42,41 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB):
+def _sources(d: str):
+    return [p for p in glob.glob(os.path.join(d, "*")) if os.path.isfile(p)]
+
+
+def _stale(lib: str, dirs) -> bool:
+    if not os.path.exists(lib):
         return True
-    t = os.path.getmtime(LIB)
-    deps = glob.glob(os.path.join(CSRC, "*")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    t = os.path.getmtime(lib)
+    deps = [p for d in dirs for p in _sources(d)] + glob.glob(os.path.join(INCLUDE, "*.h"))
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the CUDA library if any source is newer; return its path."""
-    if not force and not _stale():
-        return LIB
-    os.makedirs(BUILD_DIR, exist_ok=True)
-    srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
-    with cf.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
-        objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
-    tmp = LIB + f".tmp{os.getpid()}"
+def _link(lib: str, objs) -> None:
+    tmp = lib + f".tmp{os.getpid()}"
     cmd = [NVCC, *ARCH, "-shared", "-Xcompiler", "-fPIC", "-o", tmp, *objs, "-cudart", "static"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
-    os.replace(tmp, LIB)
+    os.replace(tmp, lib)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """Compile each CUDA library any of whose sources is newer; return the stage's path."""
+    # the token library includes headers of the stage's sources
+    todo = [(lib, d) for lib, d, deps in ((LIB, CSRC, [CSRC]),
+                                          (LIB_TOKENS, CSRC_TOKENS, [CSRC, CSRC_TOKENS]))
+            if force or _stale(lib, deps)]
+    if not todo:
+        return LIB
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    srcs = [(lib, src) for lib, d in todo for src in sorted(glob.glob(os.path.join(d, "*.cu")))]
+    with cf.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
+        objs = list(ex.map(lambda s: _compile(s[1], verbose), srcs))
+    for lib, _ in todo:
+        _link(lib, [o for (n, _), o in zip(srcs, objs) if n == lib])
     return LIB
 
 

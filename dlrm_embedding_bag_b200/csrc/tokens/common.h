@@ -1,0 +1,90 @@
+// What the kernels of libdlrm_tokens.so share: host-side bookkeeping, and
+// loads and stores of the two element types through f32.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "dlrm_sparse.h"
+
+namespace dlrm {
+
+// Records a failed CUDA call for dlrm_tokens_last_cuda_error(); DLRM_ERR_CUDA.
+int cuda_fail(cudaError_t e);
+// Counts kernel launches of this library (dlrm_tokens_launch_count).
+void note_launch(int n = 1);
+// SMs of the current device (0 and a recorded error if it cannot be asked).
+int sm_count_current();
+// cuTensorMapEncodeTiled, looked up once through the runtime (null if absent).
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_tiled();
+
+inline bool is_aligned(const void* p, uintptr_t a) {
+  return (reinterpret_cast<uintptr_t>(p) % a) == 0;
+}
+inline bool known_dtype(int d) { return d == DLRM_TABLE_F32 || d == DLRM_TABLE_BF16; }
+inline int dtype_size(int d) { return d == DLRM_TABLE_BF16 ? 2 : 4; }
+// Rows that 128-bit accesses can walk: base and pitch are whole 16-byte units.
+inline bool rows16(const void* p, int64_t ld, int elem) {
+  return is_aligned(p, 16) && (ld * elem) % 16 == 0;
+}
+
+// Elements of one 128-bit access.
+template <class T>
+constexpr int kVecOf = 16 / static_cast<int>(sizeof(T));
+
+// VEC consecutive elements (VEC > 1: one aligned 128-bit load), widened to f32.
+template <class T, int VEC>
+__device__ __forceinline__ void load_f32(const T* p, float (&v)[VEC]) {
+  if constexpr (VEC == 1) {
+    v[0] = static_cast<float>(*p);
+  } else if constexpr (sizeof(T) == 4) {
+    static_assert(VEC == 4, "one 128-bit load");
+    const float4 r = *reinterpret_cast<const float4*>(p);
+    v[0] = r.x, v[1] = r.y, v[2] = r.z, v[3] = r.w;
+  } else {
+    static_assert(VEC == 8, "one 128-bit load");
+    const uint4 r = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
+  return static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(lo))) |
+         (static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(hi))) << 16);
+}
+
+// VEC values rounded to T (nearest even) at p; VEC > 1: p is aligned to
+// min(16, VEC * sizeof(T)) bytes.
+template <class T, int VEC>
+__device__ __forceinline__ void store_f32(T* p, const float (&v)[VEC]) {
+  if constexpr (VEC == 1) {
+    if constexpr (sizeof(T) == 4)
+      *p = v[0];
+    else
+      *p = __float2bfloat16_rn(v[0]);
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 4)
+      *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+  } else if constexpr (VEC == 4) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]));
+  } else {
+    static_assert(VEC == 8, "one 128-bit store");
+    *reinterpret_cast<uint4*>(p) = make_uint4(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]),
+                                              bf16x2_bits(v[4], v[5]), bf16x2_bits(v[6], v[7]));
+  }
+}
+
+}  // namespace dlrm

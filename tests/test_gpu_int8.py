@@ -1,0 +1,335 @@
+"""The 8-bit rows, the norm in front of them and the 8-bit layer on the GPU, against 64 bits.
+
+Bounds, with u = 2^-24 (half a step of f32). Of a level v = y / s: h = x + r,
+t = h w, 127 / A, the lift and two products round once each, and A carries the
+same two roundings as t: at most 8 u relative, |v| <= 127, so a rounded level
+lies within 1/2 + 127 * 8 u of the exact one. Of a scale: the squares' sum of K
+terms is within (K + 3) u (all terms positive), its root within half of that;
+the mean, eps, the root, A, the product and the division round once each: at
+most ((K + 3) / 2 + 8) u. Of a layer: the sum is exact, its conversion, two
+products and the addition round once each; a rounding to bf16 is 2^-8.
+"""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+F32, BF16 = torch.float32, torch.bfloat16
+DT = dict(f32=F32, bf16=BF16)
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def int8():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    from dlrm_embedding_bag_b200 import int8 as _int8
+
+    return _int8
+
+
+def _gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def _normal(g, rows, cols, dtype=F32, pitch=None, std=1.0):
+    pitch = cols if pitch is None else pitch
+    buf = torch.full((rows, pitch), float("nan"), device=DEV, dtype=dtype)
+    buf[:, :cols] = torch.empty((rows, cols), device=DEV).normal_(0, std, generator=g).to(dtype)
+    return buf[:, :cols]
+
+
+def _check_rows(q, scale, y, K, what=""):
+    """(q, scale) against the exact rows y (64 bits)."""
+    s = y.abs().amax(1) / 127.0
+    assert ((scale.double() - s).abs() <= ((K + 3) / 2 + 8) * U * s).all(), what
+    live = s > 0
+    v = y[live] / s[live][:, None]
+    assert ((q[live].double() - v).abs() <= 0.5 + 127 * 8 * U).all(), what
+    assert (q[~live] == 0).all() and (q.to(torch.int16).abs() <= 127).all(), what
+
+
+SHAPES = [(1, 1), (1, 8), (3, 7), (2, 16), (5, 100), (33, 128), (17, 250), (8, 512), (4, 1000),
+          (3, 1024), (2, 2048), (7, 4096), (2, 4104), (2, 5000), (1, 8192), (2, 16384),
+          (1, 40000), (1, 131072), (3000, 24), (700, 130)]
+
+
+@pytest.mark.parametrize("M,K", SHAPES)
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_quantize_rows(int8, M, K, dt):
+    g = _gen(M + K)
+    x = _normal(g, M, K, DT[dt], std=3.0)
+    q, s = int8.quantize_rows(x)
+    assert q.dtype == torch.int8 and q.shape == (M, K) and s.shape == (M,)
+    _check_rows(q, s, x.double(), K)
+
+
+@pytest.mark.parametrize("M,K", SHAPES)
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("residual,weight", [(True, True), (False, True), (True, False)])
+def test_rms_norm(int8, M, K, dt, residual, weight):
+    g = _gen(M + K)
+    x = _normal(g, M, K, DT[dt])
+    r = _normal(g, M, K, DT[dt], std=2.0) if residual else None
+    w = torch.empty(K, device=DEV).normal_(1, 0.3, generator=g) if weight else None
+    q, s, h = int8.rms_norm_int8(x, w, residual=r, eps=1e-5)
+    hd = x.double() + (r.double() if residual else 0.0)
+    y = hd / torch.sqrt(hd.square().mean(1, keepdim=True) + np.float64(np.float32(1e-5)))
+    _check_rows(q, s, y * (w.double() if weight else 1.0), K)
+    if residual:
+        assert torch.equal(h, (x.float() + r.float()).to(DT[dt]))
+    else:
+        assert h is None
+
+
+@pytest.mark.parametrize("pitch", [104, 112, 101, 100])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("K", [100, 96, 97])
+def test_norm_strides_in_place_and_what_is_left_alone(int8, pitch, dt, K):
+    g = _gen(pitch + K)
+    M = 19
+    x = _normal(g, M, K, DT[dt], pitch)
+    r = _normal(g, M, K, DT[dt], pitch)
+    w = torch.empty(K, device=DEV).normal_(1, 0.3, generator=g)
+    want = (x.float() + r.float()).to(DT[dt])
+    hd = x.double() + r.double()
+    buf = torch.full((M + 1, 128), 99, device=DEV, dtype=torch.int8)
+    scales = torch.full((M + 1,), -1.0, device=DEV)
+    q, s, h = int8.rms_norm_int8(x, w, residual=r, out=buf[:M, :K], scale_out=scales[:M],
+                                 residual_out=r)
+    assert h is r and torch.equal(r, want)
+    y = hd / torch.sqrt(hd.square().mean(1, keepdim=True) + 1e-6) * w.double()
+    _check_rows(q, s, y, K)
+    assert (buf[:, K:] == 99).all() and (buf[M] == 99).all() and float(scales[M]) == -1.0
+    base = torch.as_strided(r, (M, pitch), (pitch, 1))
+    assert torch.isnan(base[:, K:].float()).all()
+
+
+@pytest.mark.parametrize("K", [64, 4096, 20000])
+def test_rows_of_zeros_tiny_huge_and_not_finite(int8, K):
+    g = _gen(K)
+    x = _normal(g, 9, K)
+    x[0] = 0.0
+    x[1] *= 1e-30            # squares vanish
+    x[2] *= 1e25             # squares leave f32
+    x[3, K // 2] = float("inf")
+    x[4, K - 1] = float("nan")
+    x[5, 0] = -float("inf")
+    x[6] = 0.0
+    x[6, K - 1] = 1e-44      # a subnormal alone
+    x[7] = torch.finfo(F32).max
+    for eps in (0.0, 1e-6):
+        q, s, _ = int8.rms_norm_int8(x, eps=eps)
+        bad = torch.tensor([3, 4, 5], device=DEV)
+        assert torch.isnan(s[bad]).all() and (q[bad] == 0).all()
+        assert torch.isnan(int8.dequantize_rows(q, s)[bad]).all()
+        good = torch.tensor([0, 1, 2, 7, 8], device=DEV)
+        y = x[good].double()
+        y = y / torch.sqrt(y.square().mean(1, keepdim=True) + np.float64(np.float32(eps))
+                           + (y == 0).all(1, keepdim=True))
+        _check_rows(q[good], s[good], y, K, f"eps={eps}")
+        assert int(q[6, K - 1]) == 127 and (q[6, :K - 1] == 0).all()
+        if eps == 0.0:  # a row with one value: its norm is sqrt(K)
+            assert abs(float(s[6]) * 127 - K ** 0.5) <= K ** 0.5 * 64 * U
+    q, s = int8.quantize_rows(x)
+    good = torch.tensor([0, 1, 2, 7, 8], device=DEV)
+    _check_rows(q[good], s[good], x[good].double(), K)
+    assert torch.isnan(s[3:6]).all() and int(q[6, K - 1]) == 127
+
+
+def test_values_of_rows(int8):
+    g = _gen(4)
+    for M, K in ((1, 1), (5, 16), (40, 100), (3, 4099)):
+        q, s = int8.quantize_rows(_normal(g, M, K))
+        exact = q.double() * s.double()[:, None]
+        for dt in (F32, BF16):
+            v = int8.dequantize_rows(q, s, dtype=dt)
+            half = torch.finfo(dt).eps / 2
+            assert ((v.double() - exact).abs() <= (half + U) * exact.abs()).all()
+
+
+def test_empty_batches(int8):
+    x = torch.empty((0, 32), device=DEV)
+    q, s = int8.quantize_rows(x)
+    assert q.shape == (0, 32) and s.shape == (0,)
+    w, ws = int8.quantize_rows(torch.ones((5, 32), device=DEV))
+    assert int8.linear_int8(q, s, w, ws).shape == (0, 5)
+    assert int8.dequantize_rows(q, s).shape == (0, 32)
+
+
+# ------------------------------------------------------------------------- layer
+
+
+def _ints(g, rows, cols, lo=-127, hi=127, extra=0):
+    pitch = (cols + 15) // 16 * 16 + extra
+    buf = torch.full((rows, pitch), 77, device=DEV, dtype=torch.int8)
+    buf[:, :cols] = torch.randint(lo, hi + 1, (rows, cols), device=DEV, generator=g).to(torch.int8)
+    return buf[:, :cols]
+
+
+def _check_layer(y, xq, xs, wq, ws, bias, act, rows=None):
+    if rows is not None:
+        y, xq, xs = y[rows], xq[rows], xs[rows]
+    acc = xq.double() @ wq.double().T  # exact: below 2^53
+    z = acc * xs.double()[:, None] * ws.double()
+    mag = z.abs()
+    if bias is not None:
+        z, mag = z + bias.double(), mag + bias.double().abs()
+    tol = 5 * U * mag
+    if act == "relu":
+        z = z.clamp(min=0)
+    elif act == "sigmoid":
+        z = 1 / (1 + torch.exp(-z))
+        # slope at most 1/4; the exponential, the sum and the quotient: a few steps more
+        tol = tol / 4 + 8 * U * z
+    half = torch.finfo(y.dtype).eps / 2 if y.dtype != F32 else 0.0
+    tol = tol * (1 + half) + half * z.abs()
+    err = (y.double() - z).abs()
+    assert (err <= tol).all(), float((err - tol).max())
+
+
+def _layer(int8, M, N, K, act="none", bias=True, dt=F32, seed=0, extra=0, rows=None, out=None):
+    g = _gen(M * 7 + N * 3 + K + seed)
+    xq, wq = _ints(g, M, K, extra=extra), _ints(g, N, K, lo=-128, extra=extra)
+    xs = torch.empty(M, device=DEV).uniform_(0.001, 0.1, generator=g)
+    ws = torch.empty(N, device=DEV).uniform_(0.001, 0.1, generator=g) / K ** 0.5
+    b = torch.empty(N, device=DEV).normal_(0, 0.5, generator=g) if bias else None
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    y = int8.linear_int8(xq, xs, wq, ws, b, act, out_dtype=dt, out=out, status=status)
+    assert int(status) == 0
+    _check_layer(y, xq, xs, wq, ws, b, act, rows)
+    return y
+
+
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 5, 8, 9, 16, 17, 31, 33, 64, 65, 100, 129, 257])
+@pytest.mark.parametrize("N,K", [(1, 1), (7, 16), (64, 64), (130, 100), (33, 129), (300, 592),
+                                 (128, 1000)])
+def test_linear_shapes(int8, M, N, K):
+    _layer(int8, M, N, K, dt=F32 if (M + N) % 2 else BF16)
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "sigmoid"])
+@pytest.mark.parametrize("M", [1, 6, 200])
+@pytest.mark.parametrize("bias", [True, False])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_linear_activations_and_types(int8, act, M, bias, dt):
+    _layer(int8, M, 150, 200, act=act, bias=bias, dt=DT[dt])
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 4096, 4096), (4, 5000, 2100), (20, 2048, 8192),
+                                   (2048, 592, 512), (1000, 1000, 1000), (5000, 512, 592),
+                                   (300, 9000, 272), (4096, 4096, 256), (3001, 2999, 1037)])
+def test_linear_larger(int8, M, N, K):
+    rows = torch.from_numpy(np.random.default_rng(M).choice(M, min(M, 200), replace=False)).to(DEV)
+    _layer(int8, M, N, K, act="relu", rows=rows, dt=BF16)
+    _layer(int8, M, N, K, rows=rows)
+
+
+@pytest.mark.parametrize("M", [1, 40, 300])
+@pytest.mark.parametrize("K", [131071, 60000])
+def test_linear_longest_sums_are_exact(int8, M, K):
+    """All products 2^14: the largest sum that int32 has to hold."""
+    xq = int8.int8_empty(M, K)
+    wq = int8.int8_empty(3, K)
+    xq.fill_(-128)
+    wq.fill_(-128)
+    wq[1].fill_(127)
+    ones = torch.ones(M, device=DEV)
+    y = int8.linear_int8(xq, ones, wq, torch.ones(3, device=DEV))
+    want = torch.tensor([K * 16384, -K * 16256, K * 16384], dtype=torch.float64)
+    assert torch.equal(y.cpu(), want.float().expand(M, 3))
+
+
+@pytest.mark.parametrize("M", [1, 5, 90, 400])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_linear_pitches_and_what_is_left_alone(int8, M, dt):
+    for N, pitch, offset in ((100, 100, 0), (100, 112, 0), (100, 111, 0), (99, 128, 3),
+                             (260, 264, 1)):
+        buf = torch.full(((M + 1) * pitch + offset,), float("nan"), device=DEV, dtype=DT[dt])
+        rows = buf[offset:].view(M + 1, pitch)
+        _layer(int8, M, N, 200, act="relu", dt=DT[dt], extra=32, out=rows[:M, :N])
+        rows[:M, :N] = float("nan")
+        assert torch.isnan(buf.float()).all()
+
+
+def test_linear_one_row_of_any_pitch(int8):
+    """The pitch of a single row (of x, or of w) is never used to find another."""
+    g = _gen(8)
+    xq = torch.randint(-127, 128, (1, 37), device=DEV, generator=g).to(torch.int8)
+    wq = torch.randint(-127, 128, (1, 37), device=DEV, generator=g).to(torch.int8)
+    y = int8.linear_int8(xq, torch.ones(1, device=DEV), wq, torch.ones(1, device=DEV))
+    assert float(y) == float(xq.double() @ wq.double().T)
+
+
+def test_linear_scales_that_are_not_finite(int8):
+    """A row that could not be rounded (scale NaN, levels 0) stays NaN, through ReLU too."""
+    xq = torch.zeros((3, 16), dtype=torch.int8, device=DEV)
+    xs = torch.tensor([1.0, float("nan"), 0.0], device=DEV)
+    wq = torch.ones((20, 16), dtype=torch.int8, device=DEV)
+    for act in ("none", "relu", "sigmoid"):
+        y = int8.linear_int8(xq, xs, wq, torch.ones(20, device=DEV), None, act)
+        assert torch.isnan(y[1]).all() and not torch.isnan(y[[0, 2]]).any()
+
+
+def test_streams_and_graphs(int8):
+    """The norm and the layer captured together and replayed with new inputs."""
+    g = _gen(12)
+    for M in (1, 50, 300):
+        x = _normal(g, M, 512, BF16)
+        r = _normal(g, M, 512, BF16)
+        w = torch.ones(512, device=DEV)
+        wq, ws = int8.quantize_rows(_normal(g, 256, 512))
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            q, s, _ = int8.rms_norm_int8(x, w, residual=r)
+            y = int8.linear_int8(q, s, wq, ws)
+        side.synchronize()
+        _check_layer(y, q, s, wq, ws, None, "none")
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            q, s, _ = int8.rms_norm_int8(x, w, residual=r)
+            y = int8.linear_int8(q, s, wq, ws)
+        x.mul_(-3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        hd = x.double() + r.double()
+        _check_rows(q, s, hd / torch.sqrt(hd.square().mean(1, keepdim=True) + 1e-6), 512)
+        _check_layer(y, q, s, wq, ws, None, "none")
+
+
+def test_refusals(int8):
+    from dlrm_embedding_bag_b200.tokens import TokensError
+
+    q = torch.zeros((4, 32), dtype=torch.int8, device=DEV)
+    s = torch.ones(4, device=DEV)
+    with pytest.raises(ValueError, match="w_q must be"):
+        int8.linear_int8(q, s, q[:, :16], s)
+    with pytest.raises(ValueError, match="x_scale"):
+        int8.linear_int8(q, s[:3], q, s)
+    with pytest.raises(TypeError, match="int8"):
+        int8.linear_int8(q.to(torch.uint8), s, q, s)
+    with pytest.raises(TokensError, match="DLRM_ERR_ALIGN"):
+        int8.linear_int8(q[:, 1:17], s, q[:, :16], s)
+    with pytest.raises(TokensError, match="DLRM_ERR_ALIGN"):
+        odd = torch.zeros((4, 24), dtype=torch.int8, device=DEV)
+        int8.linear_int8(odd, s, odd, s)
+    with pytest.raises(TokensError, match="DLRM_ERR_SHAPE"):
+        long = torch.zeros((1, 131072), dtype=torch.int8, device=DEV)
+        int8.linear_int8(long, s[:1], long, s[:1])
+    x = torch.zeros((4, 32), device=DEV)
+    with pytest.raises(ValueError, match="residual must be"):
+        int8.rms_norm_int8(x, residual=x.to(BF16))
+    with pytest.raises(ValueError, match="weight"):
+        int8.rms_norm_int8(x, s)
+    with pytest.raises(ValueError, match="residual_out needs"):
+        int8.rms_norm_int8(x, residual_out=x)
+    with pytest.raises(TokensError, match="DLRM_ERR_ARG"):
+        int8.rms_norm_int8(x, eps=-1.0)
+    with pytest.raises(ValueError, match="overlap"):
+        int8.quantize_rows(x[:1].expand(4, 32))
