@@ -1,88 +1,546 @@
 // The layer on 8-bit integers (declared in dlrm_int8.h):
 // y[m][n] = act(x_scale[m] * w_scale[n] * sum_k x[m][k] w[n][k] + bias[n]).
+//
+// The weights take the tensor cores' M side and the tokens their N side, so an
+// accumulator lane is an output channel and a column a token: the scale and
+// the bias of a channel stay in its lane's registers, the 32 lanes of a warp
+// write 32 neighbouring channels of one token (whole sectors at any pitch, no
+// staging), and few tokens make a narrow tile instead of a mostly empty one.
+//
+// Ten warps a CTA, as in the bf16 layer (linear.cu): one thread streams 128-byte
+// K blocks of both operands into a shared-memory ring with 2-D TMA loads, one
+// issues tcgen05.mma.kind::i8 (K = 32 each, int32 sums in TMEM, two
+// accumulators), eight warps drain a finished accumulator while the next tile's
+// products fill the other. Three forms:
+//   - one CTA walks 128-channel x BN-token tiles;
+//   - CTA pairs (cta_group::2) walk 256 x 256 tiles, each CTA loading its 128
+//     channels and half of the tokens;
+//   - few tiles: a cluster of S CTAs shares one tile, each summing a stretch of
+//     K; the int32 parts meet through distributed shared memory (exact, so the
+//     split changes no bit).
+// Every wait is bounded; one that runs out sets DLRM_FLAG_TIMEOUT in the
+// optional status word, and the CTA still frees its tensor memory and exits.
 #include <algorithm>
+#include <atomic>
 #include <climits>
+#include <cstring>
 
 #include "common.h"
 #include "dlrm_int8.h"
+#include "tcgen05_common.cuh"
 
 namespace dlrm {
 namespace {
 
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kBM = 128;  // channels of a CTA's tile
+constexpr int kBK = 128;  // bytes of K per stage: one 128-byte swizzle row
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr long long kWaitLimit = 200000000LL;  // clock cycles, about 0.1 s
+constexpr int kMaxDevices = 64;                // devices whose launch set-up is cached
+
 struct LinArgs {
-  const int8_t* x;
-  const int8_t* w;
   const float* x_scale;
   const float* w_scale;
   const float* bias;
   void* y;
-  int64_t ldx, ldw, ldy;
-  int M, N, K;
+  int64_t ldy;
+  int M, N;
+  int nkb;                       // K blocks
+  int tiles_m, tiles_n, tiles;   // token tiles, channel tiles
   int act, y_bf16;
   int32_t* status;
 };
 
-__device__ __forceinline__ float activate(float x, int act) {
-  if (act == DLRM_ACT_RELU) return x > 0.f ? x : (x != x ? x : 0.f);
-  if (act == DLRM_ACT_SIGMOID) return __fdiv_rn(1.f, __fadd_rn(1.f, expf(-x)));
+struct alignas(64) LinMaps {
+  CUtensorMap w, x;
+};
+
+template <int BN, bool PAIR>
+struct Ring {
+  static constexpr int kW = kBM * kBK;
+  static constexpr int kX = (PAIR ? BN / 2 : BN) * kBK;
+  static constexpr int kStage = kW + kX;
+  // as many stages as fit in about 192 KB, at most 8
+  static constexpr int kStages = (192 * 1024 / kStage) < 8 ? (192 * 1024 / kStage) : 8;
+  static constexpr int kScales = kStages * kStage;  // x_scale of a tile, a slice per warp
+  static constexpr int kBars = kScales + kEpiWarps * (BN / 2 < 32 ? 32 : BN / 2) * 4;
+  static constexpr int kTotal = kBars + (2 * kStages + 5) * 8 + 8 + 1024;  // + alignment
+  static_assert(kTotal <= 227 * 1024, "shared memory of one CTA");
+};
+
+// Instruction descriptor of tcgen05.mma.kind::i8 with signed 8-bit A and B, both
+// K-major, wrapping int32 sums, dense, shape M x N: D format S32 (bits 4-5 = 2),
+// A and B signed (7-9 = 1, 10-12 = 1), N >> 3 (17-22), M >> 4 (24-28).
+__host__ __device__ constexpr uint32_t idesc_s8_s32(int M, int N) {
+  return (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T for one K = 32 step of 8-bit integers.
+template <int CG>
+__device__ __forceinline__ void tc_mma_s8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                          uint32_t idesc, uint32_t accumulate) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ uint32_t load_cluster_u32(uint32_t cluster_addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+
+template <int ACT>
+__device__ __forceinline__ float activate(float x) {
+  if constexpr (ACT == DLRM_ACT_RELU) return x < 0.f ? 0.f : x;  // NaN stays NaN
+  if constexpr (ACT == DLRM_ACT_SIGMOID) return __fdiv_rn(1.f, __fadd_rn(1.f, expf(-x)));
   return x;
 }
 
-__device__ __forceinline__ float finish(const LinArgs& a, int acc, float xs, float ws, float b) {
-  return activate(__fadd_rn(static_cast<float>(acc) * xs * ws, b), a.act);
+// An output channel's constants and its column of y.
+struct Channel {
+  float ws, b;
+  bool live;
+};
+
+template <int ACT, class Out>
+__device__ __forceinline__ void put(const LinArgs& a, const Channel& ch, int n, int m, int sum,
+                                    float xs) {
+  const float v =
+      activate<ACT>(__fadd_rn(__fmul_rn(__fmul_rn(static_cast<float>(sum), xs), ch.ws), ch.b));
+  Out* p = static_cast<Out*>(a.y) + static_cast<int64_t>(m) * a.ldy + n;
+  if constexpr (sizeof(Out) == 4)
+    *p = v;
+  else
+    *p = __float2bfloat16_rn(v);
 }
 
-// 64 x 64 outputs a block, 4 x 4 a thread, four products an instruction.
-constexpr int kTile = 64, kStepK = 64;
-
-// 16 bytes of row r at column k, zero past the row's K columns.
-__device__ __forceinline__ int4 row_bytes(const int8_t* p, int64_t ld, int r, int rows, int k,
-                                          int K) {
-  if (r >= rows || k >= K) return make_int4(0, 0, 0, 0);
-  const int8_t* s = p + static_cast<int64_t>(r) * ld + k;
-  if (k + 16 <= K) return *reinterpret_cast<const int4*>(s);
-  uint32_t w[4] = {0, 0, 0, 0};
-  for (int i = 0; i < K - k; ++i)
-    w[i / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(s[i])) << (8 * (i % 4));
-  return make_int4(w[0], w[1], w[2], w[3]);
-}
-
-__global__ void __launch_bounds__(256) linear_tile_kernel(const LinArgs a) {
-  __shared__ int xs[kTile][kStepK / 4 + 1], ws[kTile][kStepK / 4 + 1];
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  const int m0 = blockIdx.y * kTile, n0 = blockIdx.x * kTile;
-  int acc[4][4] = {};
-  const int r = threadIdx.x / 4, kq = threadIdx.x % 4;
-  for (int k0 = 0; k0 < a.K; k0 += kStepK) {
-    const int4 xv = row_bytes(a.x, a.ldx, m0 + r, a.M, k0 + kq * 16, a.K);
-    const int4 wv = row_bytes(a.w, a.ldw, n0 + r, a.N, k0 + kq * 16, a.K);
-    __syncthreads();
-    xs[r][kq * 4] = xv.x, xs[r][kq * 4 + 1] = xv.y, xs[r][kq * 4 + 2] = xv.z,
-    xs[r][kq * 4 + 3] = xv.w;
-    ws[r][kq * 4] = wv.x, ws[r][kq * 4 + 1] = wv.y, ws[r][kq * 4 + 2] = wv.z,
-    ws[r][kq * 4 + 3] = wv.w;
-    __syncthreads();
-#pragma unroll 4
-    for (int k = 0; k < kStepK / 4; ++k)
+// One warp's share of a finished accumulator: 32 channels (its TMEM lanes),
+// tokens m0 + c for the columns c of [c0, c1).
+template <int ACT, class Out>
+__device__ __forceinline__ void drain(const LinArgs& a, const Channel& ch, int n, int m0,
+                                      const float* xs, uint32_t tmem, int c0, int c1) {
+  for (int c = c0; c < c1 && m0 + c < a.M; c += 32) {
+    float v[32];
+    tmem_ld_32x32b_x32(tmem + c, v);
+    const int left = a.M - (m0 + c);
+    const float4* s = reinterpret_cast<const float4*>(xs + (c - c0));
+    if (!ch.live) {
+      // a channel past N: nothing to write
+    } else if (left >= 32) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 8; ++i) {
+        const float4 f = s[i];
+        put<ACT, Out>(a, ch, n, m0 + c + 4 * i, __float_as_int(v[4 * i]), f.x);
+        put<ACT, Out>(a, ch, n, m0 + c + 4 * i + 1, __float_as_int(v[4 * i + 1]), f.y);
+        put<ACT, Out>(a, ch, n, m0 + c + 4 * i + 2, __float_as_int(v[4 * i + 2]), f.z);
+        put<ACT, Out>(a, ch, n, m0 + c + 4 * i + 3, __float_as_int(v[4 * i + 3]), f.w);
+      }
+    } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc[i][j] = __dp4a(xs[ty + 16 * i][k], ws[tx + 16 * j][k], acc[i][j]);
-  }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-      if (m >= a.M || n >= a.N) continue;
-      const float v = finish(a, acc[i][j], a.x_scale[m], a.w_scale[n],
-                             a.bias != nullptr ? a.bias[n] : 0.f);
-      if (a.y_bf16)
-        static_cast<__nv_bfloat16*>(a.y)[m * a.ldy + n] = __float2bfloat16_rn(v);
-      else
-        static_cast<float*>(a.y)[m * a.ldy + n] = v;
+      for (int i = 0; i < 32; ++i)
+        if (i < left) put<ACT, Out>(a, ch, n, m0 + c + i, __float_as_int(v[i]), xs[c - c0 + i]);
     }
+    __syncwarp();  // the next load takes the whole warp
+  }
+}
+
+// Calls f with the activation and the output type as types.
+template <class F>
+__device__ __forceinline__ void by_kind(const LinArgs& a, F f) {
+  if (a.y_bf16) {
+    if (a.act == DLRM_ACT_RELU)
+      f.template run<DLRM_ACT_RELU, __nv_bfloat16>();
+    else if (a.act == DLRM_ACT_SIGMOID)
+      f.template run<DLRM_ACT_SIGMOID, __nv_bfloat16>();
+    else
+      f.template run<DLRM_ACT_NONE, __nv_bfloat16>();
+  } else {
+    if (a.act == DLRM_ACT_RELU)
+      f.template run<DLRM_ACT_RELU, float>();
+    else if (a.act == DLRM_ACT_SIGMOID)
+      f.template run<DLRM_ACT_SIGMOID, float>();
+    else
+      f.template run<DLRM_ACT_NONE, float>();
+  }
+}
+
+struct DrainCall {
+  const LinArgs& a;
+  const Channel& ch;
+  int n, m0;
+  const float* xs;
+  uint32_t tmem;
+  int c0, c1;
+  template <int ACT, class Out>
+  __device__ __forceinline__ void run() const {
+    drain<ACT, Out>(a, ch, n, m0, xs, tmem, c0, c1);
+  }
+};
+
+// The cluster's parts of a tile, kept as [column][channel] int32 at the start
+// of each CTA's ring, summed over its S CTAs for columns [c0, c1).
+struct JoinCall {
+  const LinArgs& a;
+  int n0, m0, S, c0, c1, ew, lane;
+  uint32_t smem;
+  template <int ACT, class Out>
+  __device__ __forceinline__ void run() const {
+    // (column, 32 channels) a warp and step
+    for (int t = ew; t < (c1 - c0) * 4; t += kEpiWarps) {
+      const int c = c0 + t / 4, r = (t & 3) * 32 + lane;
+      const int m = m0 + c, n = n0 + r;
+      if (m >= a.M || n >= a.N) continue;
+      int sum = 0;
+      for (int k = 0; k < S; ++k)
+        sum += static_cast<int>(load_cluster_u32(map_to_cta(smem + (c * kBM + r) * 4, k)));
+      Channel ch;
+      ch.ws = __ldg(a.w_scale + n);
+      ch.b = a.bias != nullptr ? __ldg(a.bias + n) : 0.f;
+      put<ACT, Out>(a, ch, n, m, sum, __ldg(a.x_scale + m));
+    }
+  }
+};
+
+// Tile t -> (token tile, channel tile): bands of 8 token tiles, so that the CTAs
+// at work at one time read few different rows of either operand.
+__device__ __forceinline__ void tile_at(const LinArgs& a, int t, int& tm, int& tn) {
+  constexpr int kBand = 8;
+  const int per_band = kBand * a.tiles_n;
+  const int band = t / per_band, in = t % per_band;
+  const int height = min(kBand, a.tiles_m - band * kBand);
+  tm = band * kBand + in % height;
+  tn = in / height;
+}
+
+// SPLIT: the cluster's CTAs share one tile (and there is one tile per cluster).
+template <int BN, bool PAIR, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_int8_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinArgs args) {
+  static_assert(!(PAIR && SPLIT), "a pair shares a tile's channels, not its K");
+  using R = Ring<BN, PAIR>;
+  constexpr int CG = PAIR ? 2 : 1;
+  constexpr int kUnitN = CG * kBM;                          // channels of a unit's tile
+  constexpr uint32_t kCols = 2 * BN < 32 ? 32 : 2 * BN;     // two accumulators
+  constexpr int kWarpCols = BN / 2 < 32 ? 32 : BN / 2;      // columns an epilogue warp drains
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + R::kBars);
+  uint64_t* empty = full + R::kStages;
+  uint64_t* acc_full = empty + R::kStages;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* mma_done = acc_empty + 2;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = (PAIR || SPLIT) ? cluster_ctarank() : 0u;
+  const int S = SPLIT ? static_cast<int>(gridDim.x / cluster_count_x()) : 1;
+  const int unit0 = (PAIR || SPLIT) ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
+  const int unit_step =
+      (PAIR || SPLIT) ? static_cast<int>(cluster_count_x()) : static_cast<int>(gridDim.x);
+  // this CTA's stretch of K blocks
+  const int kb_begin = SPLIT ? static_cast<int>(static_cast<int64_t>(args.nkb) * rank / S) : 0;
+  const int kb_end = SPLIT ? static_cast<int>(static_cast<int64_t>(args.nkb) * (rank + 1) / S) : args.nkb;
+
+  if (warp == 1) {
+    tmem_alloc<CG>(tslot, kCols);
+    tmem_relinquish<CG>();
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < R::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], CG * kEpiWarps);
+    }
+    mbar_init(mma_done, 1);
+    mbar_init_fence();
+  }
+  tc_fence_before_sync();
+  if constexpr (PAIR)
+    cluster_sync();  // both CTAs' barriers exist before either signals the other's
+  else
+    __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tslot;
+  // The kernel after this one may be scheduled; it waits for this grid's
+  // results before it reads them. Likewise here: everything below may come
+  // from the kernel before (the levels, the scales), so every role waits.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  bool timed_out = false;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int g = 0;
+      for (int t = unit0; t < args.tiles && !timed_out; t += unit_step) {
+        int tm, tn;
+        tile_at(args, t, tm, tn);
+        const int n0 = tn * kUnitN + (PAIR ? static_cast<int>(rank) * kBM : 0);
+        const int m0 = tm * BN + (PAIR ? static_cast<int>(rank) * (BN / 2) : 0);
+        for (int kb = kb_begin; kb < kb_end; ++kb, ++g) {
+          const int s = g % R::kStages;
+          if (g >= R::kStages &&
+              !mbar_wait_bounded(&empty[s], ((g / R::kStages) - 1) & 1, kWaitLimit)) {
+            timed_out = true;
+            break;
+          }
+          uint8_t* sw = smem + s * R::kStage;
+          uint8_t* sx = sw + R::kW;
+          if constexpr (PAIR) {
+            // both CTAs' bytes are counted on the issuer's barrier, which only
+            // its producer arms
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * R::kStage);
+            const uint32_t fb = map_to_cta(smem_u32(&full[s]), 0);
+            tma_load_2d_pair(sw, &maps.w, fb, kb * kBK, n0);
+            tma_load_2d_pair(sx, &maps.x, fb, kb * kBK, m0);
+          } else {
+            mbar_arrive_expect_tx(&full[s], R::kStage);
+            tma_load_2d(sw, &maps.w, &full[s], kb * kBK, n0);
+            tma_load_2d(sx, &maps.x, &full[s], kb * kBK, m0);
+          }
+        }
+      }
+      if (timed_out && rank == 0) {
+        // this CTA's copies in flight land before it leaves
+        for (int i = max(0, g - R::kStages); i < g; ++i)
+          (void)mbar_wait_bounded(&full[i % R::kStages], (i / R::kStages) & 1, kWaitLimit);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && (!PAIR || rank == 0)) {
+      constexpr uint32_t idesc = idesc_s8_s32(kUnitN, BN);
+      int g = 0, j = 0;
+      for (int t = unit0; t < args.tiles && !timed_out; t += unit_step, ++j) {
+        const int b = j & 1;
+        if (j >= 2 && !mbar_wait_bounded(&acc_empty[b], ((j >> 1) - 1) & 1, kWaitLimit)) {
+          timed_out = true;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t acc = tmem + static_cast<uint32_t>(b * BN);
+        for (int kb = kb_begin; kb < kb_end; ++kb, ++g) {
+          const int s = g % R::kStages;
+          if (!mbar_wait_bounded(&full[s], (g / R::kStages) & 1, kWaitLimit)) {
+            timed_out = true;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t sw = smem_u32(smem + s * R::kStage);
+          const uint32_t sx = sw + R::kW;
+#pragma unroll
+          for (int k = 0; k < kBK / 32; ++k)
+            tc_mma_s8<CG>(acc, sdesc_k_sw128(sw + k * 32), sdesc_k_sw128(sx + k * 32), idesc,
+                          (kb > kb_begin || k > 0) ? 1u : 0u);
+          if constexpr (PAIR)
+            tc_commit_pair_both(&empty[s]);
+          else
+            tc_commit<CG>(&empty[s]);
+        }
+        if constexpr (PAIR)
+          tc_commit_pair_both(&acc_full[b]);
+        else
+          tc_commit<CG>(&acc_full[b]);
+      }
+      // every MMA has completed before this CTA or its peer can leave
+      tc_commit<CG>(mma_done);
+      if (!mbar_wait_bounded(mma_done, 0, kWaitLimit)) timed_out = true;
+    }
+  } else {
+    const int ew = warp - 2, quarter = warp & 3;
+    const int c_begin = (ew >> 2) * kWarpCols;
+    const int c_end = min(BN, c_begin + kWarpCols);
+    float* xs = reinterpret_cast<float*>(smem + R::kScales) + ew * kWarpCols;
+    int j = 0;
+    for (int t = unit0; t < args.tiles; t += unit_step, ++j) {
+      const int b = j & 1;
+      int tm, tn;
+      tile_at(args, t, tm, tn);
+      const int m0 = tm * BN;
+      const int n = tn * kUnitN + (PAIR ? static_cast<int>(rank) * kBM : 0) + quarter * 32 + lane;
+      Channel ch = {0.f, 0.f, n < args.N};
+      if constexpr (!SPLIT) {
+        if (ch.live) {
+          ch.ws = __ldg(args.w_scale + n);
+          ch.b = args.bias != nullptr ? __ldg(args.bias + n) : 0.f;
+        }
+        __syncwarp();  // the slice's readers of the tile before are done
+        for (int c = c_begin + lane; c < c_end; c += 32)
+          xs[c - c_begin] = m0 + c < args.M ? __ldg(args.x_scale + m0 + c) : 0.f;
+        __syncwarp();
+      }
+      if (!__all_sync(kFull, mbar_wait_bounded(&acc_full[b], (j >> 1) & 1, kWaitLimit))) {
+        timed_out = true;
+        break;
+      }
+      tc_fence_after_sync();
+      const uint32_t tq =
+          tmem + static_cast<uint32_t>(b * BN) + (static_cast<uint32_t>(quarter * 32) << 16);
+      if constexpr (SPLIT) {
+        // all products are done: the ring is free for this CTA's part
+        int* part = reinterpret_cast<int*>(smem);
+        for (int c = c_begin; c < c_end; c += 32) {
+          float v[32];
+          tmem_ld_32x32b_x32(tq + c, v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            part[(c + i) * kBM + quarter * 32 + lane] = __float_as_int(v[i]);
+        }
+      } else {
+        by_kind(args, DrainCall{args, ch, n, m0, xs, tq, c_begin, c_end});
+      }
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR)
+          mbar_arrive_remote(map_to_cta(smem_u32(&acc_empty[b]), 0));
+        else
+          mbar_arrive(&acc_empty[b]);
+      }
+    }
+  }
+  if (timed_out && args.status != nullptr) atomicOr(args.status, DLRM_FLAG_TIMEOUT);
+  if constexpr (SPLIT) {
+    cluster_sync();  // every CTA's part is in its shared memory
+    if (warp >= 2) {
+      int tm, tn;
+      tile_at(args, unit0, tm, tn);
+      const int c0 = BN * static_cast<int>(rank) / S, c1 = BN * static_cast<int>(rank + 1) / S;
+      by_kind(args, JoinCall{args, tn * kBM, tm * BN, S, c0, c1, warp - 2, lane, smem_u32(smem)});
+    }
+  }
+  tc_fence_before_sync();
+  if constexpr (PAIR || SPLIT)
+    cluster_sync();  // no CTA leaves while another may still use its memory
+  else
+    __syncthreads();
+  tc_fence_after_sync();
+  if (warp == 1) tmem_dealloc<CG>(tmem, kCols);
+}
+
+// 2-D map of an int8 matrix {K, rows} with the given pitch, box {128, box_rows},
+// 128-byte swizzle; elements past the matrix read as zero.
+cudaError_t encode_int8(CUtensorMap* map, const int8_t* base, int64_t K, int64_t rows, int64_t ld,
+                        int box_rows) {
+  const EncodeTiledFn enc = encode_tiled();
+  if (enc == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
+  const cuuint32_t box[2] = {kBK, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<int8_t*>(base), dims,
+                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+struct Operands {
+  const int8_t* x;
+  const int8_t* w;
+  int64_t ldx, ldw, K;
+};
+
+// split: CTAs of a tile's cluster (SPLIT), else 1.
+template <int BN, bool PAIR, bool SPLIT>
+cudaError_t run_linear(const Operands& op, LinArgs args, int sms, int split, cudaStream_t stream) {
+  auto* fn = &linear_int8_kernel<BN, PAIR, SPLIT>;
+  constexpr int smem = Ring<BN, PAIR>::kTotal;
+  constexpr int kUnitN = (PAIR ? 2 : 1) * kBM;
+  LinMaps maps;
+  cudaError_t e = encode_int8(&maps.w, op.w, op.K, args.N, op.ldw, kBM);
+  if (e == cudaSuccess)
+    e = encode_int8(&maps.x, op.x, op.K, args.M, op.ldx, PAIR ? BN / 2 : BN);
+  if (e != cudaSuccess) return e;
+  // Per device, the instance's shared-memory size is set and (pairs) the
+  // resident cluster count asked for once: 0 = not yet, else that count + 1.
+  static std::atomic<int> prepared[kMaxDevices];
+  int dev = -1;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  const bool cacheable = dev >= 0 && dev < kMaxDevices;
+  const int cached = cacheable ? prepared[dev].load(std::memory_order_acquire) : 0;
+  if (cached == 0) {
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  args.tiles_m = (args.M + BN - 1) / BN;
+  args.tiles_n = (args.N + kUnitN - 1) / kUnitN;
+  const int64_t tiles = static_cast<int64_t>(args.tiles_m) * args.tiles_n;
+  if (tiles > INT_MAX || static_cast<int64_t>(args.tiles_n) * 8 > INT_MAX)
+    return cudaErrorInvalidValue;
+  args.tiles = static_cast<int>(tiles);
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int64_t grid = std::min<int64_t>(tiles, sms);
+  int fit = cached > 0 ? cached - 1 : 0;
+  if constexpr (PAIR || SPLIT) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = PAIR ? 2 : split;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  if constexpr (PAIR) {
+    int pairs = sms / 2;
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+    if (cached == 0 && cudaOccupancyMaxActiveClusters(&fit, fn, &cfg) != cudaSuccess) {
+      (void)cudaGetLastError();
+      fit = 0;
+    }
+    if (fit > 0) pairs = std::min(pairs, fit);
+    grid = 2 * std::min<int64_t>(tiles, pairs);
+  }
+  if constexpr (SPLIT) grid = tiles * split;
+  if (cacheable && cached == 0) prepared[dev].store(fit + 1, std::memory_order_release);
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  return cudaLaunchKernelEx(&cfg, fn, maps, args);
+}
+
+// The widest token tile whose tiles still cover every SM; with fewer tokens
+// than that, a tile about as wide as they are, shared by a cluster along K if
+// its tiles leave SMs idle.
+cudaError_t launch_linear(const Operands& op, const LinArgs& args, int sms, cudaStream_t s) {
+  const int64_t tn = (args.N + kBM - 1) / kBM;
+  auto tiles = [&](int bn) { return (static_cast<int64_t>(args.M) + bn - 1) / bn * tn; };
+  if (args.M > 128 && tiles(256) >= sms) {
+    const int64_t pairs = (static_cast<int64_t>(args.M) + 255) / 256 *
+                          ((static_cast<int64_t>(args.N) + 255) / 256);
+    if (pairs >= sms / 2) return run_linear<256, true, false>(op, args, sms, 1, s);
+    return run_linear<256, false, false>(op, args, sms, 1, s);
+  }
+  if (args.M > 64 && tiles(128) >= sms) return run_linear<128, false, false>(op, args, sms, 1, s);
+  const int bn = args.M <= 32 ? 32 : 64;
+  int split = 1;
+  while (split < 8 && tiles(bn) * split * 2 <= sms && args.nkb >= split * 4) split *= 2;
+  if (split > 1)
+    return bn == 32 ? run_linear<32, false, true>(op, args, sms, split, s)
+                    : run_linear<64, false, true>(op, args, sms, split, s);
+  return bn == 32 ? run_linear<32, false, false>(op, args, sms, 1, s)
+                  : run_linear<64, false, false>(op, args, sms, 1, s);
 }
 
 }  // namespace
@@ -96,7 +554,9 @@ int dlrm_linear_int8(const int8_t* x, int64_t ldx, const float* x_scale, const i
                      dlrm_stream_t stream) {
   using namespace dlrm;
   if (act < DLRM_ACT_NONE || act > DLRM_ACT_SIGMOID || !known_dtype(y_dtype)) return DLRM_ERR_ARG;
-  if (M < 0 || M > INT_MAX || N < 1 || N > INT_MAX || K < 1 || K > DLRM_INT8_MAX_K)
+  // room above M and N for the last tile's end
+  if (M < 0 || M > INT_MAX - 1024 || N < 1 || N > INT_MAX - 1024 || K < 1 ||
+      K > DLRM_INT8_MAX_K)
     return DLRM_ERR_SHAPE;
   if (ldx < K || ldw < K || ldy < N) return DLRM_ERR_SHAPE;
   if (w == nullptr || w_scale == nullptr) return DLRM_ERR_NULL;
@@ -106,28 +566,22 @@ int dlrm_linear_int8(const int8_t* x, int64_t ldx, const float* x_scale, const i
       !is_aligned(y, dtype_size(y_dtype)) || !is_aligned(status_dev, 4))
     return DLRM_ERR_ALIGN;
   if (M == 0) return DLRM_OK;
+  const int sms = sm_count_current();
+  if (sms == 0) return DLRM_ERR_CUDA;
   LinArgs a = {};
-  a.x = x;
-  a.w = w;
   a.x_scale = x_scale;
   a.w_scale = w_scale;
   a.bias = bias;
   a.y = y;
-  a.ldx = ldx;
-  a.ldw = ldw;
   a.ldy = ldy;
   a.M = static_cast<int>(M);
   a.N = static_cast<int>(N);
-  a.K = static_cast<int>(K);
+  a.nkb = static_cast<int>((K + kBK - 1) / kBK);
   a.act = act;
   a.y_bf16 = y_dtype == DLRM_TABLE_BF16;
   a.status = status_dev;
-  const int64_t mt = (M + kTile - 1) / kTile;
-  if (mt > 65535) return DLRM_ERR_SHAPE;
-  linear_tile_kernel<<<dim3(static_cast<unsigned>((N + kTile - 1) / kTile),
-                            static_cast<unsigned>(mt)),
-                       256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
-  const cudaError_t e = cudaGetLastError();
+  const Operands op = {x, w, ldx, ldw, K};
+  const cudaError_t e = launch_linear(op, a, sms, reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e);
   note_launch();
   return DLRM_OK;

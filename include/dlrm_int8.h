@@ -79,7 +79,7 @@ DLRM_API int dlrm_dequantize_int8(const int8_t* q, int64_t ldq, const float* sca
  * are applied in f32 and the result is rounded once.
  * Requirements (DLRM_ERR_SHAPE / DLRM_ERR_ALIGN otherwise): M >= 0 (with
  * M == 0 nothing is enqueued), N >= 1, 1 <= K <= DLRM_INT8_MAX_K, M and N <
- * 2^31; ldx, ldw >= K and ldy >= N; ldx and ldw multiples of 16 and x, w
+ * 2^31 - 1024; ldx, ldw >= K and ldy >= N; ldx and ldw multiples of 16 and x, w
  * 16-byte aligned (the TMA loads); the others aligned to their elements.
  * Columns past K of x and w are never used.
  */
