@@ -15,43 +15,54 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import ops
 from .mlp import ACTS
-from .tokens import _call, _flat, _pitch, _rows, _status, _tensor
+from .tokens import _call, _code, _flat, _lib, _on, _pitch, _status
 
 MAX_K = 131071
+
+_norm = _lib.dlrm_rms_norm_int8
+_quantize = _lib.dlrm_quantize_int8
+_dequantize = _lib.dlrm_dequantize_int8
+_linear = _lib.dlrm_linear_int8
 
 
 def int8_empty(rows: int, cols: int, device="cuda") -> torch.Tensor:
     """A ``(rows, cols)`` int8 view whose row pitch is ``cols`` rounded up to 16."""
-    return torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.int8, device=device)[:, :cols]
+    t = torch.empty((rows, (cols + 15) // 16 * 16), dtype=torch.int8, device=device)
+    return t if cols % 16 == 0 else t[:, :cols]
 
 
-def _int8(t: torch.Tensor, name: str, device: torch.device) -> Tuple[int, int]:
-    """(pointer, row pitch) of an int8 matrix."""
-    _tensor(t, name, device)
+def _int8(t: torch.Tensor, name: str, index: int) -> Tuple[int, int, int]:
+    """(rows, columns, row pitch) of an int8 matrix."""
+    _on(t, name, index)
     if t.dtype != torch.int8:
         raise TypeError(f"{name} must be torch.int8 (got {t.dtype})")
-    return t.data_ptr(), _pitch(t, name)
+    return _pitch(t, name)
 
 
-def _scales(t: torch.Tensor, name: str, n: int, device: torch.device) -> int:
-    p = _flat(t, name, torch.float32, device)
+def _scales(t: torch.Tensor, name: str, n: int, index: int) -> int:
+    p = _flat(t, name, torch.float32, index)
     if t.numel() != n:
         raise ValueError(f"{name} must have {n} elements (got {t.numel()})")
     return p
 
 
-def _outputs(x, out, scale_out):
-    M, K = x.shape
+def _outputs(x, M, K, out, scale_out, index):
+    """(out, scale_out, out's pitch): the 8-bit matrix and its scales, made where not given."""
     if out is None:
-        out = int8_empty(M, K, x.device)
-    if out.shape != x.shape:
-        raise ValueError(f"out must be ({M}, {K}) (got {tuple(out.shape)})")
+        pitch = (K + 15) // 16 * 16
+        out = x.new_empty((M, pitch), dtype=torch.int8)
+        if pitch != K:
+            out = out[:, :K]
+    else:
+        rows, cols, pitch = _int8(out, "out", index)
+        if rows != M or cols != K:
+            raise ValueError(f"out must be ({M}, {K}) (got {tuple(out.shape)})")
     if scale_out is None:
-        scale_out = torch.empty(M, dtype=torch.float32, device=x.device)
-    pq, ldq = _int8(out, "out", x.device)
-    return out, scale_out, pq, ldq, _scales(scale_out, "scale_out", M, x.device)
+        scale_out = x.new_empty(M, dtype=torch.float32)
+    else:
+        _scales(scale_out, "scale_out", M, index)
+    return out, scale_out, pitch
 
 
 def quantize_rows(x: torch.Tensor, *, out: Optional[torch.Tensor] = None,
@@ -59,10 +70,12 @@ def quantize_rows(x: torch.Tensor, *, out: Optional[torch.Tensor] = None,
     """``(q, scale)`` of an f32 or bf16 ``(M, K)`` matrix: ``scale = max|row| / 127`` and
     ``q = row / scale`` rounded to nearest even. For weights ``(N, K)`` this is
     one scale for each output channel."""
-    px, xd, ldx = _rows(x, "x")
-    M, K = x.shape
-    out, scale_out, pq, ldq, ps = _outputs(x, out, scale_out)
-    _call("dlrm_quantize_int8", x.device, px, ldx, xd, M, K, pq, ldq, ps)
+    index = _on(x, "x")
+    xd = _code(x, "x")
+    M, K, ldx = _pitch(x, "x")
+    out, scale_out, ldq = _outputs(x, M, K, out, scale_out, index)
+    _call(_quantize, "dlrm_quantize_int8", index, x.data_ptr(), ldx, xd, M, K, out.data_ptr(),
+          ldq, scale_out.data_ptr())
     return out, scale_out
 
 
@@ -78,24 +91,30 @@ def rms_norm_int8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
     ``x`` into ``residual_out`` (which may be ``residual`` itself) or a new tensor,
     and is None without a residual.
     """
-    px, xd, ldx = _rows(x, "x")
-    M, K = x.shape
-    dev = x.device
+    index = _on(x, "x")
+    xd = _code(x, "x")
+    M, K, ldx = _pitch(x, "x")
     pr, ldr, ph, ldh = None, 0, None, 0
     if residual is not None:
+        _on(residual, "residual", index)
         if residual.dtype != x.dtype or residual.shape != x.shape:
             raise ValueError(f"residual must be {x.dtype} ({M}, {K})")
-        pr, _, ldr = _rows(residual, "residual", dev)
+        pr, ldr = residual.data_ptr(), _pitch(residual, "residual")[2]
         if residual_out is None:
-            residual_out = torch.empty((M, K), dtype=x.dtype, device=dev)
-        if residual_out.dtype != x.dtype or residual_out.shape != x.shape:
-            raise ValueError(f"residual_out must be {x.dtype} ({M}, {K})")
-        ph, _, ldh = _rows(residual_out, "residual_out", dev)
+            residual_out = x.new_empty((M, K))
+            ldh = K
+        else:
+            _on(residual_out, "residual_out", index)
+            if residual_out.dtype != x.dtype or residual_out.shape != x.shape:
+                raise ValueError(f"residual_out must be {x.dtype} ({M}, {K})")
+            ldh = _pitch(residual_out, "residual_out")[2]
+        ph = residual_out.data_ptr()
     elif residual_out is not None:
         raise ValueError("residual_out needs residual")
-    pw = _scales(weight, "weight", K, dev) if weight is not None else None
-    out, scale_out, pq, ldq, ps = _outputs(x, out, scale_out)
-    _call("dlrm_rms_norm_int8", dev, px, ldx, pr, ldr, xd, pw, M, K, eps, ph, ldh, pq, ldq, ps)
+    pw = _scales(weight, "weight", K, index) if weight is not None else None
+    out, scale_out, ldq = _outputs(x, M, K, out, scale_out, index)
+    _call(_norm, "dlrm_rms_norm_int8", index, x.data_ptr(), ldx, pr, ldr, xd, pw, M, K, eps, ph,
+          ldh, out.data_ptr(), ldq, scale_out.data_ptr())
     return out, scale_out, residual_out
 
 
@@ -103,16 +122,19 @@ def dequantize_rows(q: torch.Tensor, scale: torch.Tensor, *,
                     dtype: torch.dtype = torch.float32,
                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The values of a matrix in 8 bits, ``q * scale[:, None]``, rounded once to ``dtype``."""
-    _tensor(q, "q", None)
-    M, K = q.shape
-    pq, ldq = _int8(q, "q", q.device)
-    ps = _scales(scale, "scale", M, q.device)
+    index = _on(q, "q")
+    M, K, ldq = _int8(q, "q", index)
+    ps = _scales(scale, "scale", M, index)
     if out is None:
-        out = torch.empty((M, K), dtype=dtype, device=q.device)
-    if out.shape != q.shape:
-        raise ValueError(f"out must be ({M}, {K}) (got {tuple(out.shape)})")
-    po, od, ldo = _rows(out, "out", q.device)
-    _call("dlrm_dequantize_int8", q.device, pq, ldq, ps, M, K, po, od, ldo)
+        out = q.new_empty((M, K), dtype=dtype)
+        ldo = K
+    else:
+        _on(out, "out", index)
+        if out.shape != (M, K):
+            raise ValueError(f"out must be ({M}, {K}) (got {tuple(out.shape)})")
+        ldo = _pitch(out, "out")[2]
+    _call(_dequantize, "dlrm_dequantize_int8", index, q.data_ptr(), ldq, ps, M, K,
+          out.data_ptr(), _code(out, "out"), ldo)
     return out
 
 
@@ -126,31 +148,34 @@ def linear_int8(x_q: torch.Tensor, x_scale: torch.Tensor, w_q: torch.Tensor,
     ``x_q`` ``(M, K)`` and ``w_q`` ``(N, K)`` are int8 matrices (pitch a multiple of 16),
     ``x_scale`` ``(M,)`` and ``w_scale`` ``(N,)`` f32 (one scale for each token and
     each output channel), ``bias`` ``(N,)`` f32 or None. The sum over K is exact;
-    ``K`` is at most 131071. The result is f32 or bf16 (``out_dtype``).
+    ``K`` is at most 131071. The result is f32 or bf16: ``out``, or a new tensor of
+    ``out_dtype``. ``status`` (one int32) gets ``FLAG_TIMEOUT`` OR-ed in if a wait of
+    the kernel ran out.
     """
-    if act not in ACTS:
+    code = ACTS.get(act)
+    if code is None:
         raise ValueError(f"act must be one of {sorted(ACTS)}")
-    _tensor(x_q, "x_q", None)
-    dev = x_q.device
-    px, ldx = _int8(x_q, "x_q", dev)
-    pw, ldw = _int8(w_q, "w_q", dev)
-    M, K = x_q.shape
-    N = w_q.shape[0]
-    if w_q.shape[1] != K:
+    index = _on(x_q, "x_q")
+    M, K, ldx = _int8(x_q, "x_q", index)
+    N, kw, ldw = _int8(w_q, "w_q", index)
+    if kw != K:
         raise ValueError(f"w_q must be (N, {K})")
-    pxs = _scales(x_scale, "x_scale", M, dev)
-    pws = _scales(w_scale, "w_scale", N, dev)
-    pb = _scales(bias, "bias", N, dev) if bias is not None else None
+    pxs = _scales(x_scale, "x_scale", M, index)
+    pws = _scales(w_scale, "w_scale", N, index)
+    pb = _scales(bias, "bias", N, index) if bias is not None else None
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=dev)
-    if tuple(out.shape) != (M, N):
-        raise ValueError(f"out must be ({M}, {N}) (got {tuple(out.shape)})")
-    po, od, ldo = _rows(out, "out", dev)
+        out = x_q.new_empty((M, N), dtype=out_dtype)
+        ldo = N
+    else:
+        _on(out, "out", index)
+        if out.shape != (M, N):
+            raise ValueError(f"out must be ({M}, {N}) (got {tuple(out.shape)})")
+        ldo = _pitch(out, "out")[2]
     # a single row's pitch is not used to find another one: its own length will do
     if M == 1:
         ldx = (ldx + 15) // 16 * 16
     if N == 1:
         ldw = (ldw + 15) // 16 * 16
-    _call("dlrm_linear_int8", dev, px, ldx, pxs, pw, ldw, pws, pb, M, N, K, ACTS[act], po, od, ldo,
-          _status(status, dev))
+    _call(_linear, "dlrm_linear_int8", index, x_q.data_ptr(), ldx, pxs, w_q.data_ptr(), ldw, pws,
+          pb, M, N, K, code, out.data_ptr(), _code(out, "out"), ldo, _status(status, index))
     return out

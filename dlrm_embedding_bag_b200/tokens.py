@@ -62,6 +62,9 @@ def load_library(path: str = LIBRARY) -> ctypes.CDLL:
 
 
 _lib = load_library()
+_lookup = _lib.dlrm_embedding_lookup
+_grad = _lib.dlrm_embedding_grad
+_scratch_bytes = _lib.dlrm_embedding_grad_scratch_bytes
 
 
 class TokensError(ops.DlrmError):
@@ -76,50 +79,62 @@ class TokensError(ops.DlrmError):
         self.status = status
 
 
-def _call(name: str, device: torch.device, *args) -> None:
-    """Call the C entry point ``name`` on ``device`` and its current stream."""
-    fn = getattr(_lib, name)
-    index = device.index
-    if index == torch.cuda.current_device():
-        rc = fn(*args, torch.cuda.current_stream().cuda_stream)
+# The raw handle of a device's current stream, without a Stream object around it
+# (which alone costs 3 us a call).
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_get_device = torch._C._cuda_getDevice
+
+
+def _call(fn, name: str, index: int, *args) -> None:
+    """Call the C entry point ``fn`` on device ``index`` and its current stream."""
+    if index == _get_device():
+        rc = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
-            rc = fn(*args, torch.cuda.current_stream().cuda_stream)
+            rc = fn(*args, _raw_stream(index))
     if rc != 0:
         raise TokensError(rc, name)
 
 
-def _tensor(t: torch.Tensor, name: str, device: Optional[torch.device]) -> None:
+def _on(t: torch.Tensor, name: str, index: Optional[int] = None) -> int:
+    """The device index of a CUDA tensor, which has to be ``index`` if that is given."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    at = t.get_device()
+    if at < 0 or not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device (got {t.device})")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device} (got {t.device})")
+    if index is not None and at != index:
+        raise ValueError(f"{name} must be on cuda:{index} (got {t.device})")
+    return at
 
 
-def _rows(t: torch.Tensor, name: str, device: Optional[torch.device] = None) -> Tuple[int, int, int]:
-    """(pointer, dtype code, row pitch) of a 2-D f32 or bf16 tensor with unit column stride."""
-    _tensor(t, name, device)
+def _pitch(t: torch.Tensor, name: str) -> Tuple[int, int, int]:
+    """(rows, columns, row pitch) of a 2-D tensor with unit column stride."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must be 2-D with unit column stride")
+    rows, cols = shape
+    pitch, step = t.stride()
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name} must be 2-D with unit column stride")
+    if rows <= 1:
+        # the pitch of a single row says nothing (and may be smaller than the row)
+        pitch = max(pitch, cols)
+    elif pitch < cols:
+        raise ValueError(f"{name}'s rows must not overlap")
+    return rows, cols, pitch
+
+
+def _code(t: torch.Tensor, name: str) -> int:
     code = ops.TABLE_DTYPES.get(t.dtype)
     if code is None:
         raise TypeError(f"{name} must be float32 or bfloat16 (got {t.dtype})")
-    return t.data_ptr(), code, _pitch(t, name)
+    return code
 
 
-def _pitch(t: torch.Tensor, name: str) -> int:
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be 2-D with unit column stride")
-    # the pitch of a single row says nothing (and may be smaller than the row)
-    pitch = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
-    if t.shape[0] > 1 and pitch < t.shape[1]:
-        raise ValueError(f"{name}'s rows must not overlap")
-    return pitch
-
-
-def _flat(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device) -> int:
-    """Pointer of a contiguous tensor of ``dtype`` on ``device``."""
-    _tensor(t, name, device)
+def _flat(t: torch.Tensor, name: str, dtype: torch.dtype, index: int) -> int:
+    """Pointer of a contiguous tensor of ``dtype`` on device ``index``."""
+    _on(t, name, index)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
     if not t.is_contiguous():
@@ -127,12 +142,12 @@ def _flat(t: torch.Tensor, name: str, dtype: torch.dtype, device: torch.device) 
     return t.data_ptr()
 
 
-def _status(status: Optional[torch.Tensor], device: torch.device) -> Optional[int]:
+def _status(status: Optional[torch.Tensor], index: int) -> Optional[int]:
     if status is None:
         return None
     if status.numel() != 1:
         raise ValueError("status must have one element")
-    return _flat(status, "status", torch.int32, device)
+    return _flat(status, "status", torch.int32, index)
 
 
 def _padding(padding_idx: Optional[int], rows: int) -> int:
@@ -156,31 +171,35 @@ def embedding_lookup(table: torch.Tensor, ids: torch.Tensor, *, scale: float = 1
     ``out`` may be given as ``(ids.numel(), D)`` rows with a pitch, or as a
     contiguous tensor of the result's shape.
     """
-    pw, wd, ldw = _rows(table, "table")
-    rows, D = table.shape
-    dev = table.device
-    pi = _flat(ids, "ids", torch.int32, dev)
+    index = _on(table, "table")
+    wd = _code(table, "table")
+    rows, D, ldw = _pitch(table, "table")
+    pi = _flat(ids, "ids", torch.int32, index)
     T = ids.numel()
     if out is None:
-        out = torch.empty((*ids.shape, D), dtype=out_dtype or table.dtype, device=dev)
-        result = out
+        out = table.new_empty((*ids.shape, D), dtype=out_dtype)
+        po, od, ldo = out.data_ptr(), _code(out, "out_dtype"), D
     else:
-        result = out
+        _on(out, "out", index)
+        od = _code(out, "out")
         if out_dtype is not None and out.dtype != out_dtype:
             raise TypeError(f"out must be {out_dtype} (got {out.dtype})")
-    if out.shape == (*ids.shape, D) and out.is_contiguous():
-        out = out.view(T, D) if T else out.reshape(0, D)
-    if tuple(out.shape) != (T, D):
-        raise ValueError(f"out must be {(*ids.shape, D)} or {(T, D)} (got {tuple(out.shape)})")
-    po, od, ldo = _rows(out, "out", dev)
-    _call("dlrm_embedding_lookup", dev, pw, wd, ldw, rows, D, pi, T, scale,
-          _padding(padding_idx, rows), po, od, ldo, _status(status, dev))
-    return result
+        if out.shape == (*ids.shape, D) and out.is_contiguous():
+            ldo = D
+        elif out.shape == (T, D):
+            ldo = _pitch(out, "out")[2]
+        else:
+            raise ValueError(f"out must be {(*ids.shape, D)} (contiguous) or {(T, D)} "
+                             f"(got {tuple(out.shape)})")
+        po = out.data_ptr()
+    _call(_lookup, "dlrm_embedding_lookup", index, table.data_ptr(), wd, ldw, rows, D, pi, T,
+          scale, _padding(padding_idx, rows), po, od, ldo, _status(status, index))
+    return out
 
 
 def embedding_grad_scratch_bytes(T: int, rows: int, D: int) -> int:
     """Bytes of scratch that :func:`embedding_grad` needs for ``T`` ids."""
-    n = _lib.dlrm_embedding_grad_scratch_bytes(T, rows, D)
+    n = _scratch_bytes(T, rows, D)
     if n < 0:
         raise TokensError(n, "dlrm_embedding_grad_scratch_bytes")
     return n
@@ -209,28 +228,37 @@ def embedding_grad(grad: torch.Tensor, ids: torch.Tensor, num_rows: int, *, L: i
     of at least :func:`embedding_grad_scratch_bytes` bytes; by default one is
     taken from torch's allocator for the call.
     """
-    pg, gd, ldg = _rows(grad, "grad")
-    dev = grad.device
-    pi = _flat(ids, "ids", torch.int32, dev)
-    T, D = ids.numel(), grad.shape[1]
-    if L < 1 or T % L != 0 or grad.shape[0] != T // L:
-        raise ValueError(f"grad must have ids.numel() / L = {T} / {L} rows (got {grad.shape[0]})")
+    index = _on(grad, "grad")
+    gd = _code(grad, "grad")
+    n, D, ldg = _pitch(grad, "grad")
+    pi = _flat(ids, "ids", torch.int32, index)
+    T = ids.numel()
+    if L < 1 or T % L != 0 or n != T // L:
+        raise ValueError(f"grad must have ids.numel() / L = {T} / {L} rows (got {n})")
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = torch.empty((num_rows, D), dtype=dtype or grad.dtype, device=dev)
-    elif dtype is not None and out.dtype != dtype:
-        raise TypeError(f"out must be {dtype} (got {out.dtype})")
-    if tuple(out.shape) != (num_rows, D):
-        raise ValueError(f"out must be ({num_rows}, {D}) (got {tuple(out.shape)})")
-    po, od, ldo = _rows(out, "out", dev)
-    need = embedding_grad_scratch_bytes(T, num_rows, D)
+        out = grad.new_empty((num_rows, D), dtype=dtype)
+        od, ldo = _code(out, "dtype"), D
+    else:
+        _on(out, "out", index)
+        od = _code(out, "out")
+        if dtype is not None and out.dtype != dtype:
+            raise TypeError(f"out must be {dtype} (got {out.dtype})")
+        if out.shape != (num_rows, D):
+            raise ValueError(f"out must be ({num_rows}, {D}) (got {tuple(out.shape)})")
+        ldo = _pitch(out, "out")[2]
+    room = _scratch_bytes(T, num_rows, D)
+    if room < 0:
+        raise TokensError(room, "dlrm_embedding_grad")
     if scratch is None:
-        scratch = torch.empty(need, dtype=torch.uint8, device=dev)
-    ps = _flat(scratch, "scratch", torch.uint8, dev)
-    _call("dlrm_embedding_grad", dev, pg, gd, ldg, pi, T, L, num_rows, D, scale,
-          _padding(padding_idx, num_rows), po, od, ldo, 1 if accumulate else 0, ps,
-          scratch.numel(), _status(status, dev))
+        scratch = grad.new_empty(room, dtype=torch.uint8)
+        ps = scratch.data_ptr()
+    else:
+        ps, room = _flat(scratch, "scratch", torch.uint8, index), scratch.numel()
+    _call(_grad, "dlrm_embedding_grad", index, grad.data_ptr(), gd, ldg, pi, T, L, num_rows, D,
+          scale, _padding(padding_idx, num_rows), out.data_ptr(), od, ldo,
+          1 if accumulate else 0, ps, room, _status(status, index))
     return out
 
 
