@@ -224,25 +224,32 @@ __global__ void __launch_bounds__(kSortThreads) sort_move_kernel(const SortArgs 
 // Gradient, step 2: sums over runs of equal ids.
 //
 // The sorted tokens are cut into chunks; a group of G lanes sums a chunk's rows
-// (a window of G * VEC columns of them) run by run in sorted order. A run that
-// lies inside its chunk is written at once. One that crosses a border leaves
-// an f32 partial sum: slot 0 of the chunk if it began before the chunk, slot 1
-// if it begins in it and goes on; the join kernel adds those up in order.
+// (a window of G * VEC columns of them) run by run in sorted order, eight rows
+// in flight. A run that lies inside its chunk is written at once. One that
+// crosses a border leaves parts, which meet in two levels: the groups of a
+// block, whose chunks follow each other, in shared memory; then blocks through
+// one f32 row each for a run that came in from the left (slot 0) and one that
+// goes out to the right (slot 1), added up by the join kernel. The order of
+// every sum is fixed by the sizes.
 
 constexpr int kSumThreads = 256;
 constexpr int kSumInFlight = 8;
 constexpr int kJoinWarps = 8;
+constexpr int kJoinCols = 128;  // columns of a join block: four a lane
 
 struct SumArgs {
   const void* grad;
   int64_t ldg;
   const uint2* sorted;
-  float* part;  // [chunk][2][Dp]
+  float* part;  // [block of chunks][2][Dp]
   int64_t Dp;
   void* out;
   int64_t ldo;
   int T, L, rows, D;
-  int chunk, nchunks, windows;
+  int chunk;      // tokens of a group, a multiple of kSumInFlight
+  int per_block;  // tokens of a block
+  int nblocks;    // of a window
+  int windows;
   float scale;
   int out_bf16, accumulate;
 };
@@ -273,19 +280,24 @@ __device__ __forceinline__ void put_row(const SumArgs& a, uint32_t row, int c,
 
 template <class In, int VEC, int G>
 __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
-  const int q = threadIdx.x % G, base = (threadIdx.x & 31) / G * G;
-  const int64_t unit = (static_cast<int64_t>(blockIdx.x) * kSumThreads + threadIdx.x) / G;
-  const bool idle = unit >= static_cast<int64_t>(a.nchunks) * a.windows;
-  const int chunk = idle ? 0 : static_cast<int>(unit / a.windows);
-  const int c = (static_cast<int>(unit % a.windows) * G + q) * VEC;
-  const bool cols = c < a.D && !idle;
-  const int64_t begin = static_cast<int64_t>(chunk) * a.chunk;
-  const int n = idle ? 0 : static_cast<int>(min(static_cast<int64_t>(a.chunk), a.T - begin));
+  constexpr int NG = kSumThreads / G;  // groups, with chunks that follow each other
+  constexpr int U = G < kSumInFlight ? G : kSumInFlight;
+  __shared__ float head[NG][G * VEC], tail[NG][G * VEC];
+  __shared__ uint32_t first[NG], last[NG];
+  const int q = threadIdx.x % G, g = threadIdx.x / G, base = (threadIdx.x & 31) / G * G;
+  const int block = blockIdx.x / a.windows;
+  const int c = (static_cast<int>(blockIdx.x % a.windows) * G + q) * VEC;
+  const bool cols = c < a.D;
+  const int64_t begin = static_cast<int64_t>(block) * a.per_block + static_cast<int64_t>(g) * a.chunk;
+  const int n = static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(a.chunk), a.T - begin)));
   const In* grad = static_cast<const In*>(a.grad);
   const uint32_t none = a.rows;
-  float* part = a.part + static_cast<int64_t>(chunk) * 2 * a.Dp + c;
   const uint32_t left = (n > 0 && begin > 0) ? a.sorted[begin - 1].x : none;
   const uint32_t right = (n > 0 && begin + n < a.T) ? a.sorted[begin + n].x : none;
+  if (q == 0) {
+    first[g] = n > 0 ? a.sorted[begin].x : none;
+    last[g] = n > 0 ? a.sorted[begin + n - 1].x : none;
+  }
   float acc[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
@@ -300,8 +312,7 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
       row = p.y / static_cast<uint32_t>(a.L);
     }
     const int steps = min(G, a.chunk - j0);
-    for (int u0 = 0; u0 < steps; u0 += (G < kSumInFlight ? G : kSumInFlight)) {
-      constexpr int U = G < kSumInFlight ? G : kSumInFlight;
+    for (int u0 = 0; u0 < steps; u0 += U) {
       float v[U][VEC];
       uint32_t k[U];
 #pragma unroll
@@ -317,11 +328,11 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
       for (int u = 0; u < U; ++u) {
         if (k[u] != cur) {
           // the run before this token ends here
-          if (cur != none && cols) {
-            if (inside)
+          if (cur != none) {
+            if (!inside)
+              store_f32<float, VEC>(&head[g][q * VEC], acc);
+            else if (cols)
               put_row<VEC>(a, cur, c, acc);
-            else
-              store_f32<float, VEC>(part, acc);
           }
           inside = k[u] != left || j0 + u0 + u > 0;
           cur = k[u];
@@ -333,81 +344,135 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
       }
     }
   }
-  if (cur != none && cols) {
+  const bool out_right = cur != none && cur == right;  // the last run goes on
+  if (cur != none) {
     if (!inside)
-      store_f32<float, VEC>(part, acc);
-    else if (cur == right)
-      store_f32<float, VEC>(part + a.Dp, acc);
-    else
+      store_f32<float, VEC>(&head[g][q * VEC], acc);
+    else if (out_right)
+      store_f32<float, VEC>(&tail[g][q * VEC], acc);
+    else if (cols)
       put_row<VEC>(a, cur, c, acc);
   }
+  // the last group's lanes alone know whether the block's last run goes on
+  const bool block_goes_on = __syncthreads_or(g == NG - 1 && out_right);
+  auto goes_on = [&](int j) {  // group j's last run does not end with it
+    return j + 1 < NG ? last[j] != none && last[j] == first[j + 1] : block_goes_on;
+  };
+  auto one_run = [&](int j) { return first[j] == last[j] && goes_on(j); };
+  float* part = a.part + static_cast<int64_t>(block) * 2 * a.Dp + c;
+  if (inside && out_right) {
+    // a run that begins in this group: its parts to the right
+    bool open = true;
+    int j = g + 1;
+    for (; j < NG && open; ++j) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) acc[e] += head[j][q * VEC + e];
+      open = one_run(j);
+    }
+    if (cols) {
+      if (open)
+        store_f32<float, VEC>(part + a.Dp, acc);
+      else
+        put_row<VEC>(a, cur, c, acc);
+    }
+  }
+  if (g == 0 && n > 0 && first[0] != none && first[0] == left) {
+    // the run that came in from the block before
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) acc[e] = head[0][q * VEC + e];
+    for (int j = 0; j + 1 < NG && one_run(j); ++j) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) acc[e] += head[j + 1][q * VEC + e];
+    }
+    if (cols) store_f32<float, VEC>(part, acc);
+  }
 }
 
-// The runs that begin in a chunk and go on past its end: their partial sums,
-// added in order by a block.
+// The runs that begin in a block of chunks and go on past its end: their parts,
+// added by the warps of a block in turn, for a window of columns.
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const SumArgs a) {
-  __shared__ float sums[kJoinWarps][32];
+  __shared__ float4 sums[kJoinWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int i = blockIdx.x; i < a.nchunks - 1; i += gridDim.x) {
-    const int64_t begin = static_cast<int64_t>(i) * a.chunk, end = begin + a.chunk;
-    const uint32_t key = a.sorted[end - 1].x;
-    if (key == static_cast<uint32_t>(a.rows) || a.sorted[end].x != key) continue;
-    if (begin > 0 && a.sorted[begin - 1].x == key) continue;
-    // the first sorted token past the run
-    int64_t lo = end + 1, hi = a.T;
-    while (lo < hi) {
-      const int64_t mid = (lo + hi) / 2;
-      if (a.sorted[mid].x == key)
-        lo = mid + 1;
-      else
-        hi = mid;
+  const int i = blockIdx.x;
+  const int c = blockIdx.y * kJoinCols + lane * 4;
+  const int64_t begin = static_cast<int64_t>(i) * a.per_block, end = begin + a.per_block;
+  const uint32_t key = a.sorted[end - 1].x;
+  const uint32_t next = a.sorted[end].x;
+  const uint32_t before = begin > 0 ? a.sorted[begin - 1].x : a.rows;
+  if (key == static_cast<uint32_t>(a.rows) || next != key || before == key) return;
+  // the first sorted token past the run
+  int64_t lo = end + 1, hi = a.T;
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) / 2;
+    if (a.sorted[mid].x == key)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  const int to = static_cast<int>((lo - 1) / a.per_block);
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (c < a.Dp) {
+#pragma unroll 4
+    for (int m = i + warp; m <= to; m += kJoinWarps) {
+      const float4 p = *reinterpret_cast<const float4*>(
+          a.part + (static_cast<int64_t>(m) * 2 + (m == i ? 1 : 0)) * a.Dp + c);
+      s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
     }
-    const int last = static_cast<int>((lo - 1) / a.chunk);
-    for (int c0 = 0; c0 < a.D; c0 += 32) {
-      const int c = c0 + lane;
-      float s = 0.f;
-      if (c < a.D) {
-        for (int m = i + warp; m <= last; m += kJoinWarps)
-          s += a.part[(static_cast<int64_t>(m) * 2 + (m == i ? 1 : 0)) * a.Dp + c];
-      }
-      sums[warp][lane] = s;
-      __syncthreads();
-      if (warp == 0 && c < a.D) {
-        float v[1] = {0.f};
-        for (int w = 0; w < kJoinWarps; ++w) v[0] += sums[w][lane];
-        put_row<1>(a, key, c, v);
-      }
-      __syncthreads();
+  }
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0) {
+    for (int w = 1; w < kJoinWarps; ++w) {
+      const float4 p = sums[w][lane];
+      s.x += p.x, s.y += p.y, s.z += p.z, s.w += p.w;
+    }
+    const float v[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float one[1] = {v[e]};
+      if (c + e < a.D) put_row<1>(a, key, c + e, one);
     }
   }
 }
 
+// The sums, then the runs that cross blocks. Launched kernels are added to n.
 template <class In, int VEC, int G>
-cudaError_t run_sum(SumArgs a, cudaStream_t stream) {
+cudaError_t run_sum(SumArgs a, int& n, cudaStream_t stream) {
   a.windows = (a.D + G * VEC - 1) / (G * VEC);
-  const int64_t threads = static_cast<int64_t>(a.nchunks) * a.windows * G;
-  const int64_t blocks = (threads + kSumThreads - 1) / kSumThreads;
+  a.per_block = a.chunk * (kSumThreads / G);
+  a.nblocks = static_cast<int>((static_cast<int64_t>(a.T) + a.per_block - 1) / a.per_block);
+  const int64_t blocks = static_cast<int64_t>(a.nblocks) * a.windows;
   if (blocks > INT_MAX) return cudaErrorInvalidValue;
   sum_kernel<In, VEC, G><<<static_cast<unsigned>(blocks), kSumThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  ++n;
+  if (a.nblocks > 1) {
+    const dim3 grid(a.nblocks - 1, (a.D + kJoinCols - 1) / kJoinCols);
+    if (grid.y > 65535) return cudaErrorInvalidValue;
+    join_kernel<<<grid, kJoinWarps * 32, 0, stream>>>(a);
+    e = cudaGetLastError();
+    ++n;
+  }
+  return e;
 }
 
 template <class In>
-cudaError_t run_sum_shape(const SumArgs& a, bool vec, cudaStream_t stream) {
+cudaError_t run_sum_shape(const SumArgs& a, bool vec, int& n, cudaStream_t stream) {
   constexpr int V = kVecOf<In>;
-  if (!vec) return run_sum<In, 1, 32>(a, stream);
+  if (!vec) return run_sum<In, 1, 32>(a, n, stream);
   const int chunks = a.D / V;
-  if (chunks <= 4) return run_sum<In, V, 4>(a, stream);
-  if (chunks <= 8) return run_sum<In, V, 8>(a, stream);
-  if (chunks <= 16) return run_sum<In, V, 16>(a, stream);
-  return run_sum<In, V, 32>(a, stream);
+  if (chunks <= 4) return run_sum<In, V, 4>(a, n, stream);
+  if (chunks <= 8) return run_sum<In, V, 8>(a, n, stream);
+  if (chunks <= 16) return run_sum<In, V, 16>(a, n, stream);
+  return run_sum<In, V, 32>(a, n, stream);
 }
 
 // Sizes of a gradient's scratch, and where its parts lie.
 struct GradPlan {
   int sort_blocks, per, passes, bits;
-  int chunk, nchunks;
-  int64_t Dp;
+  int chunk;
+  int64_t nblocks, Dp;
   int64_t pairs[2], counts, part, bytes;  // byte offsets, and the sum
 };
 
@@ -421,16 +486,13 @@ GradPlan plan_grad(int64_t T, int64_t rows, int64_t D) {
   per = std::max<int64_t>(1, (per + kSortThreads - 1) / kSortThreads) * kSortThreads;
   p.per = static_cast<int>(per);
   p.sort_blocks = static_cast<int>((T + per - 1) / per);
-  // a chunk's tokens: 16 rows a group when the tokens are few, more when there
-  // are more than the groups of a full GPU; by T and D alone, so that the order
-  // of a sum does not depend on pointers or types. A multiple of 32 (or 16):
-  // the sum kernel takes up to 8 tokens a step and sees the end of a run only
-  // in a step's tokens, which may not reach past the chunk.
-  const int64_t even = (T * D / (int64_t{148} * 2048 * 4) + 31) / 32 * 32;
-  p.chunk = T * D < int64_t{148} * 2048 * 4 * 16
-                ? 16
-                : static_cast<int>(std::min<int64_t>(256, std::max<int64_t>(32, even)));
-  p.nchunks = static_cast<int>((T + p.chunk - 1) / p.chunk);
+  // a group's tokens: as few as are in flight at once while that fills the
+  // GPU's threads, more when there are more; by T and D alone
+  const int64_t even = T * D / (int64_t{148} * 1024 * 4) / kSumInFlight * kSumInFlight;
+  p.chunk = static_cast<int>(std::min<int64_t>(256, std::max<int64_t>(kSumInFlight, even)));
+  // blocks of chunks, at most: 32 lanes a group are the widest
+  const int64_t per_block = static_cast<int64_t>(p.chunk) * (kSumThreads / 32);
+  p.nblocks = (T + per_block - 1) / per_block;
   p.Dp = (D + 7) / 8 * 8;
   int64_t at = 0;
   auto take = [&at](int64_t bytes) {
@@ -441,14 +503,14 @@ GradPlan plan_grad(int64_t T, int64_t rows, int64_t D) {
   p.pairs[0] = take(T * 8);
   p.pairs[1] = take(T * 8);
   p.counts = take(static_cast<int64_t>(p.sort_blocks) * kRadix * 4);
-  p.part = take(static_cast<int64_t>(p.nchunks) * 2 * p.Dp * 4);
+  p.part = take(p.nblocks * 2 * p.Dp * 4);
   p.bytes = at;
   return p;
 }
 
 bool grad_sizes_ok(int64_t T, int64_t rows, int64_t D) {
   return T >= 0 && T <= INT_MAX && rows >= 1 && rows <= INT_MAX - 1 && D >= 1 &&
-         D <= INT_MAX - 1024;
+         D <= (1 << 22);
 }
 
 int clear_status(int32_t* status, cudaStream_t stream) {
@@ -572,20 +634,15 @@ int dlrm_embedding_grad(const void* grad, int grad_dtype, int64_t ldg, const int
   a.rows = static_cast<int>(rows);
   a.D = static_cast<int>(D);
   a.chunk = p.chunk;
-  a.nchunks = p.nchunks;
   a.scale = scale;
   a.out_bf16 = out_dtype == DLRM_TABLE_BF16;
   a.accumulate = accumulate ? 1 : 0;
   const bool vec = D % (16 / es) == 0 && rows16(grad, ldg, es) && rows16(out, ldo, os);
-  e = grad_dtype == DLRM_TABLE_F32 ? run_sum_shape<float>(a, vec, s)
-                                   : run_sum_shape<__nv_bfloat16>(a, vec, s);
+  int n = 2 * p.passes;
+  e = grad_dtype == DLRM_TABLE_F32 ? run_sum_shape<float>(a, vec, n, s)
+                                   : run_sum_shape<__nv_bfloat16>(a, vec, n, s);
   if (e != cudaSuccess) return cuda_fail(e);
-  note_launch(2 * p.passes + 1);
-  if (p.nchunks > 1) {
-    join_kernel<<<std::min(p.nchunks - 1, 148 * 8), kJoinWarps * 32, 0, s>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e);
-    note_launch();
-  }
+  note_launch(n);
   return DLRM_OK;
 }
 

@@ -36,7 +36,7 @@ extern "C" {
 /*
  * dlrm_embedding_lookup -- Y[t, :] = scale * W[ids[t], :], t < T.
  *   table       dev (rows, ldw) of table_dtype; columns [0, D) are used.
- *   rows        1 .. 2^31 - 2.
+ *   rows        1 .. 2^31 - 2; D is 1 .. 2^22.
  *   ids         dev int32 (T,); may be NULL iff T == 0.
  *   T           0 .. 2^31 - 1; with T == 0 nothing is enqueued (but the status
  *               word is cleared).
@@ -62,7 +62,8 @@ DLRM_API int64_t dlrm_embedding_grad_scratch_bytes(int64_t T, int64_t rows, int6
 /*
  * dlrm_embedding_grad -- out[r, :] = scale * sum_{t: ids[t] == r} grad[t / L, :].
  * The tokens are sorted by id (stable), and the rows of equal ids are summed in
- * f32 in an order that depends on T and D alone: equal inputs give equal bits.
+ * f32 in an order that the sizes, types and alignments fix: equal calls give
+ * equal bits.
  *   grad        dev (T / L, ldg) of grad_dtype; columns [0, D) are used. May be
  *               NULL iff T == 0.
  *   ids         dev int32 (T,); may be NULL iff T == 0.
