@@ -39,25 +39,41 @@ inline bool rows16(const void* p, int64_t ld, int elem) {
 template <class T>
 constexpr int kVecOf = 16 / static_cast<int>(sizeof(T));
 
-// VEC consecutive elements (VEC > 1: one aligned 128-bit load), widened to f32.
+// VEC elements as they lie in memory: one (VEC 1) or a whole 128-bit access.
 template <class T, int VEC>
-__device__ __forceinline__ void load_f32(const T* p, float (&v)[VEC]) {
+struct RawOf {
+  using type = uint4;
+  static_assert(VEC == kVecOf<T>, "one 128-bit access");
+};
+template <class T>
+struct RawOf<T, 1> {
+  using type = T;
+};
+template <class T, int VEC>
+using Raw = typename RawOf<T, VEC>::type;
+
+// ... widened to f32 (a bf16 value is the upper half of an f32).
+template <class T, int VEC>
+__device__ __forceinline__ void widen(const Raw<T, VEC>& r, float (&v)[VEC]) {
   if constexpr (VEC == 1) {
-    v[0] = static_cast<float>(*p);
-  } else if constexpr (sizeof(T) == 4) {
-    static_assert(VEC == 4, "one 128-bit load");
-    const float4 r = *reinterpret_cast<const float4*>(p);
-    v[0] = r.x, v[1] = r.y, v[2] = r.z, v[3] = r.w;
+    v[0] = static_cast<float>(r);
   } else {
-    static_assert(VEC == 8, "one 128-bit load");
-    const uint4 r = *reinterpret_cast<const uint4*>(p);
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      if constexpr (sizeof(T) == 4) {
+        v[i] = __uint_as_float(w[i]);
+      } else {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
     }
   }
+}
+
+template <class T, int VEC>
+__device__ __forceinline__ void load_f32(const T* p, float (&v)[VEC]) {
+  widen<T, VEC>(*reinterpret_cast<const Raw<T, VEC>*>(p), v);
 }
 
 __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {

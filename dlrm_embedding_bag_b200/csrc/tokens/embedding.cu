@@ -1,15 +1,18 @@
 // Embedding rows by token id, and the table's gradient by sorted tokens
 // (declared in dlrm_tokens.h).
 #include <algorithm>
+#include <atomic>
 #include <climits>
 
 #include "common.h"
 #include "dlrm_tokens.h"
+#include "tma_common.cuh"
 
 namespace dlrm {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
+constexpr int kMaxDevices = 64;  // devices whose launch set-up is cached
 
 // ---------------------------------------------------------------------------
 // Lookup: Y[t] = scale * W[ids[t]].
@@ -89,18 +92,104 @@ cudaError_t run_lookup_shape(const LookupArgs& a, bool vec, cudaStream_t stream)
 }
 
 // ---------------------------------------------------------------------------
+// Gradient: zeros for the rows that no token names.
+//
+// A dense gradient is mostly writes, and the sort in front of the sums leaves
+// the memory idle; so every row is zeroed by blocks that ride along with the
+// sort's, and the named rows are written over later.
+
+struct FillArgs {
+  char* out;      // null: nothing to fill
+  int64_t rows;   // of row_bytes each, pitch bytes apart
+  int64_t row_bytes, pitch;
+};
+
+// Bulk (TMA, non-tensor) copy of `bytes` bytes of this CTA's shared memory (a
+// multiple of 16; both addresses 16-byte aligned) to global memory, tracked by
+// the thread's bulk groups.
+__device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst),
+               "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+}
+
+constexpr int kZeroBytes = 16 << 10;  // of a bulk store
+
+// Part `part` of `parts` of the zeros, by THREADS threads. zeros: kZeroBytes of
+// shared memory, 16-byte aligned, for this alone.
+template <int THREADS>
+__device__ void fill_zeros(const FillArgs& f, int part, int parts, uint8_t* zeros) {
+  const int64_t first = static_cast<int64_t>(part) * THREADS + threadIdx.x;
+  const int64_t step = static_cast<int64_t>(parts) * THREADS;
+  if (f.pitch == f.row_bytes) {
+    // one stretch of bytes: bulk stores of a block of zeros between its
+    // unaligned ends (a thread's own 16-byte stores reached 4.3 TB/s, these
+    // are bound by the memory)
+    const int64_t bytes = f.rows * f.row_bytes;
+    const int64_t lead = min(bytes, static_cast<int64_t>(-reinterpret_cast<intptr_t>(f.out) & 15));
+    const int64_t mid = (bytes - lead) & ~int64_t{15};
+    for (int i = threadIdx.x; i < kZeroBytes / 16; i += THREADS)
+      reinterpret_cast<uint4*>(zeros)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int64_t at = static_cast<int64_t>(part) * kZeroBytes; at < mid;
+           at += static_cast<int64_t>(parts) * kZeroBytes)
+        bulk_s2g(f.out + lead + at, zeros,
+                 static_cast<uint32_t>(min(static_cast<int64_t>(kZeroBytes), mid - at)));
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
+    if (first < lead) f.out[first] = 0;
+    if (first < bytes - lead - mid) f.out[lead + mid + first] = 0;
+  } else {
+    // rows apart from each other, a warp each: whole 16-byte units, or the
+    // 2 bytes that every element has at least
+    const bool wide = ((reinterpret_cast<intptr_t>(f.out) | f.row_bytes | f.pitch) & 15) == 0;
+    const int64_t per_row = f.row_bytes / (wide ? 16 : 2);
+    for (int64_t r = first / 32; r < f.rows; r += step / 32) {
+      char* row = f.out + r * f.pitch;
+      for (int64_t c = threadIdx.x % 32; c < per_row; c += 32) {
+        if (wide)
+          reinterpret_cast<uint4*>(row)[c] = make_uint4(0, 0, 0, 0);
+        else
+          reinterpret_cast<uint16_t*>(row)[c] = 0;
+      }
+    }
+  }
+}
+
+// No tokens at all: the zeros alone.
+__global__ void __launch_bounds__(1024) fill_kernel(const FillArgs f) {
+  __shared__ __align__(16) uint8_t zeros[kZeroBytes];
+  fill_zeros<1024>(f, blockIdx.x, gridDim.x, zeros);
+}
+
+// ---------------------------------------------------------------------------
 // Gradient, step 1: the tokens sorted by id, stable.
 //
 // Least-significant-digit radix sort of (key, token) pairs with digits of at
-// most 8 bits over the bits that `rows` needs. A pass is two kernels: every
-// block counts the digits of its stretch of pairs, then every block adds up
-// the counts of all digits and of the blocks before it, and moves its pairs.
-// Padding and out-of-range ids take the key `rows` and so come last.
+// most 8 bits over the bits that `rows` needs. Padding and out-of-range ids
+// take the key `rows` and so come last. Up to kClusterSort tokens one cluster
+// of CTAs sorts in shared memory, all passes in one launch; more take two
+// launches a pass: every block counts the digits of its stretch of pairs, then
+// every block adds up the counts of all digits and of the blocks before it,
+// and moves its pairs. Either way a block first brings a tile of pairs into
+// digit order in its own shared memory, so that neighbouring threads write
+// neighbouring places: moving the pairs straight from registers, a store of
+// scattered 8-byte pairs a warp, took 1.5 us a pair of a thread and pass.
 
-constexpr int kSortThreads = 1024;
-constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kRadix = 256;
-constexpr int kSortMaxBlocks = 148;
+constexpr int kCountThreads = 1024;
+constexpr int kCountLoads = 4;  // pairs a thread loads at once
+constexpr int kMoveThreads = 512;
+constexpr int kMoveItems = 16;  // pairs of a thread in a tile
+constexpr int kMoveTile = kMoveThreads * kMoveItems;
+constexpr int kSortMaxBlocks = 296;  // two move blocks an SM
+constexpr int kClusterThreads = 1024;
+constexpr int kClusterSize = 8;       // CTAs
+constexpr int kClusterMaxItems = 8;  // pairs of a thread
+constexpr int64_t kClusterSort = int64_t{kClusterSize} * kClusterThreads * kClusterMaxItems;
 
 struct SortArgs {
   const int32_t* ids;  // first pass: the tokens' ids; later passes read `in`
@@ -109,11 +198,15 @@ struct SortArgs {
   uint32_t* counts;  // [block][kRadix]
   int T, rows, pad;
   int shift, bits;
-  int per;  // pairs of a block, a multiple of kSortThreads
+  int passes;  // of the cluster sort
+  int per;     // pairs of a block, a multiple of kMoveTile
+  int blocks;  // that sort; the others fill
+  FillArgs fill;
+  int fill_part, fill_parts;  // the first filling block's part, and of how many
   int32_t* status;
 };
 
-__device__ __forceinline__ uint2 sort_pair(const SortArgs& a, int i) {
+__device__ __forceinline__ uint2 sort_pair(const SortArgs& a, int64_t i) {
   if (a.ids == nullptr) return a.in[i];
   const int r = __ldg(a.ids + i);
   const bool in = static_cast<unsigned>(r) < static_cast<unsigned>(a.rows);
@@ -121,103 +214,366 @@ __device__ __forceinline__ uint2 sort_pair(const SortArgs& a, int i) {
   return make_uint2(key, static_cast<uint32_t>(i));
 }
 
-__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(const SortArgs a) {
+__device__ __forceinline__ void flag_bad_id(const SortArgs& a, int64_t i) {
+  if (a.ids != nullptr && a.status != nullptr &&
+      static_cast<unsigned>(__ldg(a.ids + i)) >= static_cast<unsigned>(a.rows))
+    atomicOr(a.status, DLRM_FLAG_INDEX_OOB);
+}
+
+// The live lanes of the warp whose digit is this lane's (for a live lane): a vote
+// for each of the digit's bits. (The match instruction takes the warp's
+// distinct digits one after another.)
+__device__ __forceinline__ unsigned same_digit(uint32_t digit, bool live, int bits) {
+  unsigned peers = __ballot_sync(kFull, live);
+#pragma unroll
+  for (int b = 0; b < 8; ++b) {
+    if (b < bits) {
+      const bool set = (digit >> b) & 1;
+      const unsigned votes = __ballot_sync(kFull, set);
+      peers &= set ? votes : ~votes;
+    }
+  }
+  return peers;
+}
+
+// Exclusive sums over the digits, for the threads below kRadix; every thread of
+// the block takes part. Holds a barrier.
+__device__ __forceinline__ uint32_t digits_before(uint32_t n, uint32_t* warp_sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t scan = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t m = __shfl_up_sync(kFull, scan, o);
+    if (lane >= o) scan += m;
+  }
+  if (threadIdx.x < kRadix && lane == 31) warp_sum[warp] = scan;
+  __syncthreads();
+  if (threadIdx.x < kRadix)
+    for (int w = 0; w < warp; ++w) scan += warp_sum[w];
+  return scan - n;
+}
+
+template <int THREADS, int ITEMS>
+struct TileSmem {
+  static constexpr int kWarps = THREADS / 32;
+  static constexpr int kParts = THREADS / kRadix;  // threads of a digit
+  static constexpr int kWarpsOfPart = kWarps / kParts;
+  uint2 pairs[THREADS * ITEMS];  // the tile in digit order
+  uint32_t at[kWarps][kRadix];
+  uint32_t parts[kParts][kRadix];
+  uint32_t start[kRadix];  // a digit's first place in `pairs`
+  uint32_t warp_sum[kRadix / 32];
+};
+
+// Brings a tile of pairs (a warp's ITEMS * 32 pairs follow each other, `n` of the
+// tile are live) into digit order in sm.pairs, stable. Returns the count of
+// digit threadIdx.x for the threads below kRadix. Ends with a barrier.
+template <int THREADS, int ITEMS>
+__device__ __forceinline__ uint32_t order_tile(TileSmem<THREADS, ITEMS>& sm,
+                                               const uint2 (&pair)[ITEMS], int n, int shift,
+                                               int bits) {
+  using S = TileSmem<THREADS, ITEMS>;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int own = warp * 32 * ITEMS + lane;
+  const uint32_t mask = (1u << bits) - 1;
+  // a pair's place among its warp's pairs of the same digit
+  uint32_t among[ITEMS];
+#pragma unroll
+  for (int d = lane; d < kRadix; d += 32) sm.at[warp][d] = 0;
+  __syncwarp();
+#pragma unroll
+  for (int u = 0; u < ITEMS; ++u) {
+    const bool live = own + u * 32 < n;
+    const uint32_t digit = (pair[u].x >> shift) & mask;
+    const unsigned peers = same_digit(digit, live, bits);
+    among[u] = live ? sm.at[warp][digit] + __popc(peers & ((1u << lane) - 1)) : 0;
+    __syncwarp();
+    if (live && lane == __ffs(peers) - 1) sm.at[warp][digit] += __popc(peers);
+    __syncwarp();
+  }
+  __syncthreads();
+  // ... among the tile's warps: kWarpsOfPart of them a thread, then the threads of a digit
+  const int d = tid % kRadix, part = tid / kRadix;
+  uint32_t sum = 0;
+#pragma unroll
+  for (int w = 0; w < S::kWarpsOfPart; ++w) {
+    uint32_t& c = sm.at[part * S::kWarpsOfPart + w][d];
+    const uint32_t m = c;
+    c = sum;
+    sum += m;
+  }
+  sm.parts[part][d] = sum;
+  __syncthreads();
+  uint32_t count = 0;
+#pragma unroll
+  for (int k = 0; k < S::kParts; ++k) count += sm.parts[k][d];
+  // ... and after the smaller digits
+  uint32_t place = digits_before(count, sm.warp_sum);
+  if (part == 0) {
+    sm.start[d] = place;
+#pragma unroll
+    for (int k = 0; k < S::kParts; ++k) {
+      const uint32_t m = sm.parts[k][d];
+      sm.parts[k][d] = place;
+      place += m;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < ITEMS; ++u) {
+    if (own + u * 32 < n) {
+      const uint32_t digit = (pair[u].x >> shift) & mask;
+      sm.pairs[sm.parts[warp / S::kWarpsOfPart][digit] + sm.at[warp][digit] + among[u]] = pair[u];
+    }
+  }
+  __syncthreads();
+  return count;
+}
+
+__global__ void __launch_bounds__(kCountThreads) sort_count_kernel(const SortArgs a) {
+  __shared__ __align__(16) uint8_t zeros[kZeroBytes];
+  if (static_cast<int>(blockIdx.x) >= a.blocks) {
+    fill_zeros<kCountThreads>(a.fill, a.fill_part + blockIdx.x - a.blocks, a.fill_parts, zeros);
+    return;
+  }
   __shared__ uint32_t cnt[kRadix];
   const int tid = threadIdx.x, lane = tid & 31;
   if (tid < kRadix) cnt[tid] = 0;
   __syncthreads();
   const int64_t begin = static_cast<int64_t>(blockIdx.x) * a.per;
+  const int64_t end = min(begin + a.per, static_cast<int64_t>(a.T));
   const uint32_t mask = (1u << a.bits) - 1;
-  for (int64_t i0 = begin; i0 < begin + a.per; i0 += kSortThreads) {
-    const int64_t i = i0 + tid;
-    const bool live = i < a.T;
-    uint32_t digit = kRadix;  // of no pair
-    if (live) {
-      if (a.ids != nullptr && a.status != nullptr &&
-          static_cast<unsigned>(__ldg(a.ids + i)) >= static_cast<unsigned>(a.rows))
-        atomicOr(a.status, DLRM_FLAG_INDEX_OOB);
-      digit = (sort_pair(a, static_cast<int>(i)).x >> a.shift) & mask;
+  for (int64_t i0 = begin; i0 < end; i0 += kCountThreads * kCountLoads) {
+    uint32_t digit[kCountLoads];
+#pragma unroll
+    for (int u = 0; u < kCountLoads; ++u) {
+      const int64_t i = i0 + u * kCountThreads + tid;
+      digit[u] = kRadix;  // of no pair
+      if (i < end) {
+        flag_bad_id(a, i);
+        digit[u] = (sort_pair(a, i).x >> a.shift) & mask;
+      }
     }
-    const unsigned peers = __match_any_sync(kFull, digit);
-    if (live && lane == __ffs(peers) - 1) atomicAdd(&cnt[digit], __popc(peers));
+#pragma unroll
+    for (int u = 0; u < kCountLoads; ++u) {
+      const unsigned peers = same_digit(digit[u], digit[u] != kRadix, a.bits);
+      if (digit[u] != kRadix && lane == __ffs(peers) - 1) atomicAdd(&cnt[digit[u]], __popc(peers));
+    }
   }
   __syncthreads();
   if (tid < kRadix) a.counts[static_cast<int64_t>(blockIdx.x) * kRadix + tid] = cnt[tid];
 }
 
-__global__ void __launch_bounds__(kSortThreads) sort_move_kernel(const SortArgs a) {
-  __shared__ uint32_t at[kSortWarps][kRadix];  // a warp's next place for each digit
-  __shared__ uint32_t total[kSortThreads / kRadix][kRadix], before[kSortThreads / kRadix][kRadix];
-  __shared__ uint32_t warp_sum[kRadix / 32];
+struct MoveSmem {
+  TileSmem<kMoveThreads, kMoveItems> tile;
+  uint32_t total[kMoveThreads / kRadix][kRadix], before[kMoveThreads / kRadix][kRadix];
+  uint32_t place[kRadix];  // a digit's next place in the output
+};
+
+__global__ void __launch_bounds__(kMoveThreads, 2) sort_move_kernel(const SortArgs a) {
+  extern __shared__ __align__(16) uint8_t sort_smem[];
+  if (static_cast<int>(blockIdx.x) >= a.blocks) {
+    static_assert(sizeof(MoveSmem) >= kZeroBytes, "room for the zeros");
+    fill_zeros<kMoveThreads>(a.fill, a.fill_part + blockIdx.x - a.blocks, a.fill_parts, sort_smem);
+    return;
+  }
+  auto& sm = *reinterpret_cast<MoveSmem*>(sort_smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t mask = (1u << a.bits) - 1;
-  for (int d = lane; d < kRadix; d += 32) at[warp][d] = 0;
-  __syncwarp();
-  // every warp counts the digits of its own stretch of pairs
-  const int per_warp = a.per / kSortWarps;
-  const int64_t begin = static_cast<int64_t>(blockIdx.x) * a.per + warp * per_warp;
-  for (int j = 0; j < per_warp; j += 32) {
-    const int64_t i = begin + j + lane;
-    const bool live = i < a.T;
-    const uint32_t digit = live ? (sort_pair(a, static_cast<int>(i)).x >> a.shift) & mask : kRadix;
-    const unsigned peers = __match_any_sync(kFull, digit);
-    if (live && lane == __ffs(peers) - 1) at[warp][digit] += __popc(peers);
-    __syncwarp();
-  }
   // digit d: pairs in all blocks, and in the blocks before this one
   const int d = tid % kRadix, part = tid / kRadix;
-  uint32_t all = 0, mine = 0;
-  for (int b = part; b < static_cast<int>(gridDim.x); b += kSortThreads / kRadix) {
-    const uint32_t n = a.counts[static_cast<int64_t>(b) * kRadix + d];
-    all += n;
-    mine += b < static_cast<int>(blockIdx.x) ? n : 0;
+  uint32_t all = 0, place = 0;
+#pragma unroll 8
+  for (int b = part; b < a.blocks; b += kMoveThreads / kRadix) {
+    const uint32_t c = a.counts[static_cast<int64_t>(b) * kRadix + d];
+    all += c;
+    place += b < static_cast<int>(blockIdx.x) ? c : 0;
   }
-  total[part][d] = all;
-  before[part][d] = mine;
+  sm.total[part][d] = all;
+  sm.before[part][d] = place;
   __syncthreads();
-  uint32_t place = 0, scan = 0;
-  if (tid < kRadix) {
-    all = 0;
-    for (int p = 0; p < kSortThreads / kRadix; ++p) {
-      all += total[p][d];
-      place += before[p][d];
-    }
-    scan = all;
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t n = __shfl_up_sync(kFull, scan, o);
-      if (lane >= o) scan += n;
-    }
-    if (lane == 31) warp_sum[warp] = scan;
+  all = place = 0;
+#pragma unroll
+  for (int p = 0; p < kMoveThreads / kRadix; ++p) {
+    all += sm.total[p][d];
+    place += sm.before[p][d];
   }
-  __syncthreads();
-  if (tid < kRadix) {
-    for (int w = 0; w < warp; ++w) scan += warp_sum[w];
-    place += scan - all;
-    for (int w = 0; w < kSortWarps; ++w) {
-      const uint32_t n = at[w][d];
-      at[w][d] = place;
-      place += n;
+  place += digits_before(all, sm.tile.warp_sum);
+  if (tid < kRadix) sm.place[d] = place;
+  const int64_t begin = static_cast<int64_t>(blockIdx.x) * a.per;
+  const int64_t end = min(begin + a.per, static_cast<int64_t>(a.T));
+  for (int64_t i0 = begin; i0 < end; i0 += kMoveTile) {
+    const int n = static_cast<int>(min(static_cast<int64_t>(kMoveTile), end - i0));
+    uint2 pair[kMoveItems];
+#pragma unroll
+    for (int u = 0; u < kMoveItems; ++u) {
+      const int i = (warp * kMoveItems + u) * 32 + lane;
+      pair[u] = make_uint2(0, 0);
+      if (i < n) pair[u] = sort_pair(a, i0 + i);
+    }
+    __syncthreads();  // the tile before has left, its digits' places are set
+    const uint32_t count = order_tile(sm.tile, pair, n, a.shift, a.bits);
+    for (int k = tid; k < n; k += kMoveThreads) {
+      const uint2 p = sm.tile.pairs[k];
+      const uint32_t digit = (p.x >> a.shift) & mask;
+      a.out[sm.place[digit] + (k - sm.tile.start[digit])] = p;
+    }
+    __syncthreads();
+    if (tid < kRadix) sm.place[tid] += count;
+  }
+}
+
+__device__ __forceinline__ uint32_t load_cluster_u32(uint32_t cluster_addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ void store_cluster_pair(uint32_t cluster_addr, uint2 p) {
+  asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(cluster_addr), "r"(p.x), "r"(p.y)
+               : "memory");
+}
+
+template <int ITEMS>
+struct ClusterSmem {
+  TileSmem<kClusterThreads, ITEMS> tile;
+  uint2 arrived[kClusterThreads * ITEMS];  // this CTA's stretch of the pairs after a pass
+  uint32_t total[kRadix];                  // its count of each digit, read by the others
+  uint32_t place[kRadix];
+};
+
+// The first cluster sorts: each of its CTAs owns a stretch of the pairs, a tile.
+// The other clusters fill.
+template <int ITEMS>
+__global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(const SortArgs a) {
+  extern __shared__ __align__(16) uint8_t sort_smem[];
+  // the sums' blocks may be scheduled now (they wait for this grid's end)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (blockIdx.x >= kClusterSize) {
+    static_assert(sizeof(ClusterSmem<ITEMS>) >= kZeroBytes, "room for the zeros");
+    fill_zeros<kClusterThreads>(a.fill, blockIdx.x - kClusterSize, a.fill_parts, sort_smem);
+    return;
+  }
+  auto& sm = *reinterpret_cast<ClusterSmem<ITEMS>*>(sort_smem);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = static_cast<int>(cluster_ctarank());
+  constexpr int kStretch = kClusterThreads * ITEMS;
+  const int own = warp * 32 * ITEMS + lane;  // the thread's first pair in the stretch
+  const int n = max(0, min(kStretch, a.T - rank * kStretch));
+  const uint32_t mask = (1u << a.bits) - 1;
+  uint2 pair[ITEMS];
+#pragma unroll
+  for (int u = 0; u < ITEMS; ++u) {
+    pair[u] = make_uint2(0, 0);
+    if (own + u * 32 < n) {
+      pair[u] = sort_pair(a, rank * kStretch + own + u * 32);
+      flag_bad_id(a, rank * kStretch + own + u * 32);
     }
   }
-  __syncthreads();
-  for (int j = 0; j < per_warp; j += 32) {
-    const int64_t i = begin + j + lane;
-    const bool live = i < a.T;
-    uint2 pair = make_uint2(0, 0);
-    uint32_t digit = kRadix;
-    if (live) {
-      pair = sort_pair(a, static_cast<int>(i));
-      digit = (pair.x >> a.shift) & mask;
+  for (int p = 0; p < a.passes; ++p) {
+    const int shift = p * a.bits;
+    const uint32_t count = order_tile(sm.tile, pair, n, shift, a.bits);
+    if (tid < kRadix) sm.total[tid] = count;
+    cluster_sync();
+    // a digit's first place: after the smaller digits, and after the CTAs before
+    uint32_t all = 0, place = 0;
+    if (tid < kRadix) {
+      const uint32_t addr = smem_u32(&sm.total[tid]);
+#pragma unroll
+      for (int r = 0; r < kClusterSize; ++r) {
+        const uint32_t c = load_cluster_u32(map_to_cta(addr, r));
+        all += c;
+        place += r < rank ? c : 0;
+      }
     }
-    const unsigned peers = __match_any_sync(kFull, digit);
-    if (live) {
-      const uint32_t to = at[warp][digit] + __popc(peers & ((1u << lane) - 1));
-      a.out[to] = pair;
+    place += digits_before(all, sm.tile.warp_sum);
+    if (tid < kRadix) sm.place[tid] = place;
+    __syncthreads();
+    const bool final_pass = p + 1 == a.passes;
+    for (int k = tid; k < n; k += kClusterThreads) {
+      const uint2 v = sm.tile.pairs[k];
+      const uint32_t digit = (v.x >> shift) & mask;
+      const uint32_t to = sm.place[digit] + (k - sm.tile.start[digit]);
+      if (final_pass)
+        a.out[to] = v;
+      else
+        store_cluster_pair(map_to_cta(smem_u32(&sm.arrived[to % kStretch]), to / kStretch), v);
     }
-    __syncwarp();
-    if (live && lane == __ffs(peers) - 1) at[warp][digit] += __popc(peers);
-    __syncwarp();
+    // the pairs have arrived, and nobody reads this CTA's counts any more
+    cluster_sync();
+    if (!final_pass) {
+#pragma unroll
+      for (int u = 0; u < ITEMS; ++u) pair[u] = sm.arrived[own + u * 32];
+    }
   }
+}
+
+// Sorts up to kClusterSort tokens of `ids` into a.out and zeroes a.fill.
+template <int ITEMS>
+cudaError_t run_cluster_sort(SortArgs& a, cudaStream_t stream) {
+  auto* fn = &sort_cluster_kernel<ITEMS>;
+  constexpr int smem = sizeof(ClusterSmem<ITEMS>);
+  // Per device, the shared-memory size is set and the resident cluster count
+  // asked for once: 0 = not yet, else that count + 1.
+  static std::atomic<int> prepared[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool cacheable = dev >= 0 && dev < kMaxDevices;
+  const int cached = cacheable ? prepared[dev].load(std::memory_order_acquire) : 0;
+  int fit = cached - 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kClusterThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kClusterSize;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cached == 0) {
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(16 * kClusterSize);
+    if ((e = cudaOccupancyMaxActiveClusters(&fit, fn, &cfg)) != cudaSuccess) return e;
+    if (cacheable) prepared[dev].store(fit + 1, std::memory_order_release);
+  }
+  // Clusters that fill, each 64 KB at least: not more than run beside the one
+  // that sorts (another would wait for that one to end: 60 instead of 43 us at
+  // 32768 tokens and 256 MB of zeros).
+  int fillers = 0;
+  if (a.fill.out != nullptr) {
+    const int64_t bytes = a.fill.rows * a.fill.row_bytes;
+    fillers = static_cast<int>(std::min<int64_t>(std::max(1, fit - 1),
+                                                 bytes / (kClusterSize * (64 << 10)) + 1));
+  }
+  a.fill_parts = fillers * kClusterSize;
+  cfg.gridDim = dim3((fillers + 1) * kClusterSize);
+  return cudaLaunchKernelEx(&cfg, fn, a);
+}
+
+// Sorts more tokens, two launches a pass, between the two buffers of pairs; the
+// zeros are shared out evenly over the launches. a.out ends as the sorted one.
+cudaError_t run_grid_sort(SortArgs& a, uint2* const (&pairs)[2], cudaStream_t stream) {
+  constexpr int smem = sizeof(MoveSmem);
+  cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&sort_move_kernel),
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int fillers = a.fill.out != nullptr ? 148 : 0;
+  a.fill_parts = 2 * a.passes * fillers;
+  for (int i = 0; i < a.passes; ++i) {
+    a.out = pairs[i & 1];
+    a.shift = i * a.bits;
+    a.fill_part = 2 * i * fillers;
+    sort_count_kernel<<<a.blocks + fillers, kCountThreads, 0, stream>>>(a);
+    a.fill_part += fillers;
+    sort_move_kernel<<<a.blocks + fillers, kMoveThreads, smem, stream>>>(a);
+    a.ids = nullptr;
+    a.in = a.out;
+  }
+  return cudaGetLastError();
 }
 
 // ---------------------------------------------------------------------------
@@ -278,25 +634,37 @@ __device__ __forceinline__ void put_row(const SumArgs& a, uint32_t row, int c,
   }
 }
 
+template <int VEC, int G>
+struct alignas(16) SumSmem {
+  static constexpr int kGroups = kSumThreads / G;
+  float head[kGroups][G * VEC];  // a group's part of a run that began before it
+  uint32_t first[kGroups], last[kGroups];
+};
+
+// The block's sums over the sorted tokens [lo, hi), `chunk` of them a group (a
+// multiple of kSumInFlight), for window `window` of the columns. part: this
+// block's two rows for the runs that cross [lo, hi), or null if none does.
 template <class In, int VEC, int G>
-__global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
-  constexpr int NG = kSumThreads / G;  // groups, with chunks that follow each other
+__device__ __forceinline__ void sum_block(const SumArgs& a, SumSmem<VEC, G>& sm,
+                                          const uint2* sorted, int64_t lo, int64_t hi, int chunk,
+                                          int window, float* part) {
+  constexpr int NG = SumSmem<VEC, G>::kGroups;
   constexpr int U = G < kSumInFlight ? G : kSumInFlight;
-  __shared__ float head[NG][G * VEC], tail[NG][G * VEC];
-  __shared__ uint32_t first[NG], last[NG];
+  auto& head = sm.head;
+  auto& first = sm.first;
+  auto& last = sm.last;
   const int q = threadIdx.x % G, g = threadIdx.x / G, base = (threadIdx.x & 31) / G * G;
-  const int block = blockIdx.x / a.windows;
-  const int c = (static_cast<int>(blockIdx.x % a.windows) * G + q) * VEC;
+  const int c = (window * G + q) * VEC;
   const bool cols = c < a.D;
-  const int64_t begin = static_cast<int64_t>(block) * a.per_block + static_cast<int64_t>(g) * a.chunk;
-  const int n = static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(a.chunk), a.T - begin)));
+  const int64_t begin = lo + static_cast<int64_t>(g) * chunk;
+  const int n = static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(chunk), hi - begin)));
   const In* grad = static_cast<const In*>(a.grad);
   const uint32_t none = a.rows;
-  const uint32_t left = (n > 0 && begin > 0) ? a.sorted[begin - 1].x : none;
-  const uint32_t right = (n > 0 && begin + n < a.T) ? a.sorted[begin + n].x : none;
+  const uint32_t left = (n > 0 && begin > 0) ? sorted[begin - 1].x : none;
+  const uint32_t right = (n > 0 && begin + n < a.T) ? sorted[begin + n].x : none;
   if (q == 0) {
-    first[g] = n > 0 ? a.sorted[begin].x : none;
-    last[g] = n > 0 ? a.sorted[begin + n - 1].x : none;
+    first[g] = n > 0 ? sorted[begin].x : none;
+    last[g] = n > 0 ? sorted[begin + n - 1].x : none;
   }
   float acc[VEC];
 #pragma unroll
@@ -304,25 +672,24 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
   uint32_t cur = none;  // key of the run being summed; none before the first
   bool inside = false;  // it began in this chunk
   // every lane of the warp takes the same number of steps: shuffles span it
-  for (int j0 = 0; j0 < a.chunk; j0 += G) {
+  for (int j0 = 0; j0 < chunk; j0 += G) {
     uint32_t key = none, row = 0;
     if (j0 + q < n) {
-      const uint2 p = a.sorted[begin + j0 + q];
+      const uint2 p = sorted[begin + j0 + q];
       key = p.x;
       row = p.y / static_cast<uint32_t>(a.L);
     }
-    const int steps = min(G, a.chunk - j0);
+    const int steps = min(G, chunk - j0);
     for (int u0 = 0; u0 < steps; u0 += U) {
-      float v[U][VEC];
+      Raw<In, VEC> raw[U];
       uint32_t k[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         k[u] = __shfl_sync(kFull, key, base + u0 + u);
         const uint32_t r = __shfl_sync(kFull, row, base + u0 + u);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) v[u][e] = 0.f;
+        raw[u] = Raw<In, VEC>();
         if (k[u] != none && cols)
-          load_f32<In, VEC>(grad + static_cast<int64_t>(r) * a.ldg + c, v[u]);
+          raw[u] = *reinterpret_cast<const Raw<In, VEC>*>(grad + static_cast<int64_t>(r) * a.ldg + c);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -339,8 +706,10 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
 #pragma unroll
           for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
         }
+        float v[VEC];
+        widen<In, VEC>(raw[u], v);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) acc[e] += v[u][e];
+        for (int e = 0; e < VEC; ++e) acc[e] += v[e];
       }
     }
   }
@@ -348,9 +717,7 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
   if (cur != none) {
     if (!inside)
       store_f32<float, VEC>(&head[g][q * VEC], acc);
-    else if (out_right)
-      store_f32<float, VEC>(&tail[g][q * VEC], acc);
-    else if (cols)
+    else if (!out_right && cols)
       put_row<VEC>(a, cur, c, acc);
   }
   // the last group's lanes alone know whether the block's last run goes on
@@ -359,7 +726,6 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
     return j + 1 < NG ? last[j] != none && last[j] == first[j + 1] : block_goes_on;
   };
   auto one_run = [&](int j) { return first[j] == last[j] && goes_on(j); };
-  float* part = a.part + static_cast<int64_t>(block) * 2 * a.Dp + c;
   if (inside && out_right) {
     // a run that begins in this group: its parts to the right
     bool open = true;
@@ -371,7 +737,7 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
     }
     if (cols) {
       if (open)
-        store_f32<float, VEC>(part + a.Dp, acc);
+        store_f32<float, VEC>(part + a.Dp + c, acc);
       else
         put_row<VEC>(a, cur, c, acc);
     }
@@ -384,8 +750,20 @@ __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) acc[e] += head[j + 1][q * VEC + e];
     }
-    if (cols) store_f32<float, VEC>(part, acc);
+    if (cols) store_f32<float, VEC>(part + c, acc);
   }
+}
+
+template <class In, int VEC, int G>
+__global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
+  __shared__ SumSmem<VEC, G> sm;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the sort (and the zeros) are done
+  const int block = blockIdx.x / a.windows;
+  const int64_t lo = static_cast<int64_t>(block) * a.per_block;
+  sum_block<In, VEC, G>(a, sm, a.sorted, lo, min(lo + a.per_block, static_cast<int64_t>(a.T)),
+                        a.chunk, blockIdx.x % a.windows,
+                        a.part + static_cast<int64_t>(block) * 2 * a.Dp);
 }
 
 // The runs that begin in a block of chunks and go on past its end: their parts,
@@ -395,21 +773,22 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const SumArgs a) 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int i = blockIdx.x;
   const int c = blockIdx.y * kJoinCols + lane * 4;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the sums are done
   const int64_t begin = static_cast<int64_t>(i) * a.per_block, end = begin + a.per_block;
   const uint32_t key = a.sorted[end - 1].x;
   const uint32_t next = a.sorted[end].x;
   const uint32_t before = begin > 0 ? a.sorted[begin - 1].x : a.rows;
   if (key == static_cast<uint32_t>(a.rows) || next != key || before == key) return;
-  // the first sorted token past the run
-  int64_t lo = end + 1, hi = a.T;
-  while (lo < hi) {
-    const int64_t mid = (lo + hi) / 2;
-    if (a.sorted[mid].x == key)
-      lo = mid + 1;
-    else
-      hi = mid;
+  // the last block that the run reaches: block m is reached if its first key
+  // is the run's, and those blocks follow each other
+  int to = i + 1;
+  for (int m0 = i + 2; m0 < a.nblocks; m0 += kJoinWarps * 32) {
+    const int m = m0 + threadIdx.x;
+    const bool reached = m < a.nblocks && a.sorted[static_cast<int64_t>(m) * a.per_block].x == key;
+    const int n = __syncthreads_count(reached);
+    to += n;
+    if (n < kJoinWarps * 32) break;
   }
-  const int to = static_cast<int>((lo - 1) / a.per_block);
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (c < a.Dp) {
 #pragma unroll 4
@@ -435,37 +814,188 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const SumArgs a) 
   }
 }
 
-// The sums, then the runs that cross blocks. Launched kernels are added to n.
-template <class In, int VEC, int G>
-cudaError_t run_sum(SumArgs a, int& n, cudaStream_t stream) {
-  a.windows = (a.D + G * VEC - 1) / (G * VEC);
-  a.per_block = a.chunk * (kSumThreads / G);
-  a.nblocks = static_cast<int>((static_cast<int64_t>(a.T) + a.per_block - 1) / a.per_block);
-  const int64_t blocks = static_cast<int64_t>(a.nblocks) * a.windows;
-  if (blocks > INT_MAX) return cudaErrorInvalidValue;
-  sum_kernel<In, VEC, G><<<static_cast<unsigned>(blocks), kSumThreads, 0, stream>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  ++n;
-  if (a.nblocks > 1) {
-    const dim3 grid(a.nblocks - 1, (a.D + kJoinCols - 1) / kJoinCols);
-    if (grid.y > 65535) return cudaErrorInvalidValue;
-    join_kernel<<<grid, kJoinWarps * 32, 0, stream>>>(a);
-    e = cudaGetLastError();
-    ++n;
+// Few tokens: all of the gradient in one launch, and no scratch. Every block
+// ranks the tokens by counting the smaller keys (T^2 comparisons, kSmallTokens
+// bounds them to about 2 us of a block) and takes a stretch of the sorted tokens
+// that begins and ends with whole runs, for one window of columns; the zeros of
+// the rows that no token names are shared out over all blocks, by a bitmap of
+// the named rows in a block's share.
+
+constexpr int kSmallTokens = 512;
+constexpr int64_t kSmallZeros = 16 << 20;  // bytes of the gradient, at most
+constexpr int kMapWords = 256;             // of the bitmap: rows / 32 at a time
+
+struct SmallArgs {
+  SumArgs sum;  // T, rows, ...: `sorted` and `part` are not used
+  const int32_t* ids;
+  int pad;
+  FillArgs fill;
+  int elem;   // bytes of an element of the gradient
+  int parts;  // of the tokens
+  int32_t* status;
+};
+
+// Block `part` of `parts`: its share of the rows, without those in keys[0, T).
+__device__ void fill_unnamed(const FillArgs& f, const uint32_t* keys, int T, int elem, int part,
+                             int parts, uint32_t* map) {
+  const int64_t begin = f.rows * part / parts, end = f.rows * (part + 1) / parts;
+  const bool wide = ((reinterpret_cast<intptr_t>(f.out) | f.row_bytes | f.pitch) & 15) == 0;
+  const uint32_t unit = wide ? 16 : elem;
+  const uint32_t per_row = static_cast<uint32_t>(f.row_bytes / unit);
+  for (int64_t r0 = begin; r0 < end; r0 += kMapWords * 32) {
+    const int n = static_cast<int>(min(end - r0, static_cast<int64_t>(kMapWords * 32)));
+    __syncthreads();
+    for (int i = threadIdx.x; i < kMapWords; i += kSumThreads) map[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < T; i += kSumThreads) {
+      const int64_t r = static_cast<int64_t>(keys[i]) - r0;
+      if (r >= 0 && r < n) atomicOr(&map[r / 32], 1u << (r % 32));
+    }
+    __syncthreads();
+    const int64_t units = static_cast<int64_t>(n) * per_row;
+    for (int64_t u = threadIdx.x; u < units; u += kSumThreads) {
+      const uint32_t r = static_cast<uint32_t>(static_cast<uint32_t>(u) / per_row);
+      if (map[r / 32] & (1u << (r % 32))) continue;
+      char* p = f.out + (r0 + r) * f.pitch + static_cast<int64_t>(u - static_cast<int64_t>(r) * per_row) * unit;
+      if (wide)
+        *reinterpret_cast<uint4*>(p) = make_uint4(0, 0, 0, 0);
+      else if (elem == 4)
+        *reinterpret_cast<uint32_t*>(p) = 0;
+      else
+        *reinterpret_cast<uint16_t*>(p) = 0;
+    }
   }
-  return e;
 }
 
-template <class In>
-cudaError_t run_sum_shape(const SumArgs& a, bool vec, int& n, cudaStream_t stream) {
+template <class In, int VEC, int G>
+__global__ void __launch_bounds__(kSumThreads) small_kernel(const SmallArgs a) {
+  __shared__ SumSmem<VEC, G> sm;
+  __shared__ __align__(16) uint32_t keys[kSmallTokens];
+  __shared__ uint2 sorted[kSmallTokens];
+  __shared__ uint32_t map[kMapWords];
+  __shared__ int lo, hi;
+  const int tid = threadIdx.x, T = a.sum.T;
+  const uint32_t none = a.sum.rows;
+  for (int i = tid; i < kSmallTokens; i += kSumThreads) {
+    uint32_t key = 0xffffffffu;  // past the tokens: larger than any key
+    if (i < T) {
+      const int r = __ldg(a.ids + i);
+      const bool in = static_cast<unsigned>(r) < none;
+      if (!in && a.status != nullptr && blockIdx.x == 0)
+        atomicOr(a.status, DLRM_FLAG_INDEX_OOB);
+      key = (in && r != a.pad) ? r : none;
+    }
+    keys[i] = key;
+  }
+  const int part = blockIdx.x / a.sum.windows;
+  if (tid == 0) lo = hi = T;
+  __syncthreads();
+  if (part < a.parts) {
+    for (int i = tid; i < T; i += kSumThreads) {
+      const uint32_t key = keys[i];
+      int place = 0;
+      for (int j = 0; j < T; j += 4) {
+        const uint4 k = *reinterpret_cast<const uint4*>(&keys[j]);
+        // equal keys: the earlier token first
+        place += (k.x < key || (k.x == key && j < i)) + (k.y < key || (k.y == key && j + 1 < i)) +
+                 (k.z < key || (k.z == key && j + 2 < i)) + (k.w < key || (k.w == key && j + 3 < i));
+      }
+      sorted[place] = make_uint2(key, static_cast<uint32_t>(i));
+    }
+    __syncthreads();
+    // the part's first and last token, moved on to the next run's beginning
+    const int from = static_cast<int>(static_cast<int64_t>(T) * part / a.parts);
+    const int to = static_cast<int>(static_cast<int64_t>(T) * (part + 1) / a.parts);
+    for (int i = tid; i < T; i += kSumThreads)
+      if (i == 0 || sorted[i].x != sorted[i - 1].x) {
+        if (i >= from) atomicMin(&lo, i);
+        if (i >= to) atomicMin(&hi, i);
+      }
+    __syncthreads();
+    const int per = (hi - lo + SumSmem<VEC, G>::kGroups - 1) / SumSmem<VEC, G>::kGroups;
+    const int chunk = (per + kSumInFlight - 1) / kSumInFlight * kSumInFlight;
+    if (hi > lo)
+      sum_block<In, VEC, G>(a.sum, sm, sorted, lo, hi, chunk, blockIdx.x % a.sum.windows, nullptr);
+  }
+  if (a.fill.out != nullptr)
+    fill_unnamed(a.fill, keys, T, a.elem, blockIdx.x, gridDim.x, map);
+}
+
+// A kernel that may be scheduled while the one before it ends, and waits for it.
+template <class... P, class... A>
+cudaError_t launch_after(void (*fn)(P...), dim3 grid, int threads, cudaStream_t stream,
+                         const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
+// The sums, then the runs that cross blocks. Launched kernels are added to n.
+struct SumLaunch {
+  SumArgs a;
+  int n;
+  cudaStream_t stream;
+  template <class In, int VEC, int G>
+  cudaError_t run() {
+    a.windows = (a.D + G * VEC - 1) / (G * VEC);
+    a.per_block = a.chunk * (kSumThreads / G);
+    a.nblocks = static_cast<int>((static_cast<int64_t>(a.T) + a.per_block - 1) / a.per_block);
+    const int64_t blocks = static_cast<int64_t>(a.nblocks) * a.windows;
+    if (blocks > INT_MAX) return cudaErrorInvalidValue;
+    cudaError_t e = launch_after(&sum_kernel<In, VEC, G>, dim3(static_cast<unsigned>(blocks)),
+                                 kSumThreads, stream, a);
+    if (e != cudaSuccess) return e;
+    ++n;
+    if (a.nblocks > 1) {
+      const dim3 grid(a.nblocks - 1, (a.D + kJoinCols - 1) / kJoinCols);
+      e = launch_after(&join_kernel, grid, kJoinWarps * 32, stream, a);
+      ++n;
+    }
+    return e;
+  }
+};
+
+// All of it in one launch, for few tokens.
+struct SmallLaunch {
+  SmallArgs a;
+  cudaStream_t stream;
+  template <class In, int VEC, int G>
+  cudaError_t run() {
+    a.sum.windows = (a.sum.D + G * VEC - 1) / (G * VEC);
+    constexpr int per_block = kSumThreads / G * kSumInFlight;  // tokens in flight
+    a.parts = (a.sum.T + per_block - 1) / per_block;
+    // blocks: for the sums, and 32 KB of zeros each
+    int64_t blocks = static_cast<int64_t>(a.parts) * a.sum.windows;
+    if (a.fill.out != nullptr)
+      blocks = std::max(blocks, std::min<int64_t>(592, a.fill.rows * a.fill.row_bytes / (32 << 10)));
+    small_kernel<In, VEC, G><<<static_cast<unsigned>(blocks), kSumThreads, 0, stream>>>(a);
+    return cudaGetLastError();
+  }
+};
+
+// The lanes of a group, by the row's length.
+template <class In, class F>
+cudaError_t by_shape(int D, bool vec, F& f) {
   constexpr int V = kVecOf<In>;
-  if (!vec) return run_sum<In, 1, 32>(a, n, stream);
-  const int chunks = a.D / V;
-  if (chunks <= 4) return run_sum<In, V, 4>(a, n, stream);
-  if (chunks <= 8) return run_sum<In, V, 8>(a, n, stream);
-  if (chunks <= 16) return run_sum<In, V, 16>(a, n, stream);
-  return run_sum<In, V, 32>(a, n, stream);
+  if (!vec) return f.template run<In, 1, 32>();
+  const int chunks = D / V;
+  if (chunks <= 4) return f.template run<In, V, 4>();
+  if (chunks <= 8) return f.template run<In, V, 8>();
+  if (chunks <= 16) return f.template run<In, V, 16>();
+  return f.template run<In, V, 32>();
+}
+
+template <class F>
+cudaError_t by_type(int dtype, int D, bool vec, F& f) {
+  return dtype == DLRM_TABLE_F32 ? by_shape<float>(D, vec, f)
+                                 : by_shape<__nv_bfloat16>(D, vec, f);
 }
 
 // Sizes of a gradient's scratch, and where its parts lie.
@@ -483,13 +1013,13 @@ GradPlan plan_grad(int64_t T, int64_t rows, int64_t D) {
   p.passes = (key_bits + 7) / 8;
   p.bits = (key_bits + p.passes - 1) / p.passes;
   int64_t per = (T + kSortMaxBlocks - 1) / kSortMaxBlocks;
-  per = std::max<int64_t>(1, (per + kSortThreads - 1) / kSortThreads) * kSortThreads;
+  per = std::max<int64_t>(1, (per + kMoveTile - 1) / kMoveTile) * kMoveTile;
   p.per = static_cast<int>(per);
   p.sort_blocks = static_cast<int>((T + per - 1) / per);
   // a group's tokens: as few as are in flight at once while that fills the
   // GPU's threads, more when there are more; by T and D alone
-  const int64_t even = T * D / (int64_t{148} * 1024 * 4) / kSumInFlight * kSumInFlight;
-  p.chunk = static_cast<int>(std::min<int64_t>(256, std::max<int64_t>(kSumInFlight, even)));
+  const int64_t even = T * D / (int64_t{148} * 4096 * 4) / kSumInFlight * kSumInFlight;
+  p.chunk = static_cast<int>(std::min<int64_t>(64, std::max<int64_t>(kSumInFlight, even)));
   // blocks of chunks, at most: 32 lanes a group are the widest
   const int64_t per_block = static_cast<int64_t>(p.chunk) * (kSumThreads / 32);
   p.nblocks = (T + per_block - 1) / per_block;
@@ -593,39 +1123,25 @@ int dlrm_embedding_grad(const void* grad, int grad_dtype, int64_t ldg, const int
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int rc = clear_status(status_dev, s);
   if (rc != DLRM_OK) return rc;
+  FillArgs fill = {};
   if (!accumulate) {
-    const cudaError_t e = cudaMemset2DAsync(out, static_cast<size_t>(ldo) * os, 0,
-                                            static_cast<size_t>(D) * os, rows, s);
+    fill.out = static_cast<char*>(out);
+    fill.rows = rows;
+    fill.row_bytes = D * os;
+    fill.pitch = ldo * os;
+  }
+  if (T == 0) {
+    if (accumulate) return DLRM_OK;
+    fill_kernel<<<148, 1024, 0, s>>>(fill);
+    const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e);
+    note_launch();
+    return DLRM_OK;
   }
-  if (T == 0) return DLRM_OK;
-
-  char* mem = static_cast<char*>(scratch);
-  SortArgs sa = {};
-  sa.ids = ids;
-  sa.counts = reinterpret_cast<uint32_t*>(mem + p.counts);
-  sa.T = static_cast<int>(T);
-  sa.rows = static_cast<int>(rows);
-  sa.pad = static_cast<int>(padding_idx);
-  sa.bits = p.bits;
-  sa.per = p.per;
-  sa.status = status_dev;
-  for (int i = 0; i < p.passes; ++i) {
-    sa.out = reinterpret_cast<uint2*>(mem + p.pairs[i & 1]);
-    sa.shift = i * p.bits;
-    sort_count_kernel<<<p.sort_blocks, kSortThreads, 0, s>>>(sa);
-    sort_move_kernel<<<p.sort_blocks, kSortThreads, 0, s>>>(sa);
-    sa.ids = nullptr;
-    sa.in = sa.out;
-  }
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e);
 
   SumArgs a = {};
   a.grad = grad;
   a.ldg = ldg;
-  a.sorted = sa.out;
-  a.part = reinterpret_cast<float*>(mem + p.part);
   a.Dp = p.Dp;
   a.out = out;
   a.ldo = ldo;
@@ -638,11 +1154,54 @@ int dlrm_embedding_grad(const void* grad, int grad_dtype, int64_t ldg, const int
   a.out_bf16 = out_dtype == DLRM_TABLE_BF16;
   a.accumulate = accumulate ? 1 : 0;
   const bool vec = D % (16 / es) == 0 && rows16(grad, ldg, es) && rows16(out, ldo, os);
-  int n = 2 * p.passes;
-  e = grad_dtype == DLRM_TABLE_F32 ? run_sum_shape<float>(a, vec, n, s)
-                                   : run_sum_shape<__nv_bfloat16>(a, vec, n, s);
+  cudaError_t e;
+  if (T <= kSmallTokens && (accumulate || rows * D * os <= kSmallZeros)) {
+    SmallLaunch f = {};
+    f.a.sum = a;
+    f.a.ids = ids;
+    f.a.pad = static_cast<int>(padding_idx);
+    f.a.fill = fill;
+    f.a.elem = os;
+    f.a.status = status_dev;
+    f.stream = s;
+    if ((e = by_type(grad_dtype, a.D, vec, f)) != cudaSuccess) return cuda_fail(e);
+    note_launch();
+    return DLRM_OK;
+  }
+
+  char* mem = static_cast<char*>(scratch);
+  SortArgs sa = {};
+  sa.ids = ids;
+  sa.counts = reinterpret_cast<uint32_t*>(mem + p.counts);
+  sa.T = static_cast<int>(T);
+  sa.rows = static_cast<int>(rows);
+  sa.pad = static_cast<int>(padding_idx);
+  sa.bits = p.bits;
+  sa.passes = p.passes;
+  sa.per = p.per;
+  sa.blocks = p.sort_blocks;
+  sa.fill = fill;
+  sa.status = status_dev;
+  uint2* const pairs[2] = {reinterpret_cast<uint2*>(mem + p.pairs[0]),
+                           reinterpret_cast<uint2*>(mem + p.pairs[1])};
+  sa.out = pairs[0];
+  int n = 1;
+  if (T <= kClusterSort) {
+    const int64_t items = (T + kClusterSize * kClusterThreads - 1) / (kClusterSize * kClusterThreads);
+    e = items <= 1   ? run_cluster_sort<1>(sa, s)
+        : items <= 2 ? run_cluster_sort<2>(sa, s)
+        : items <= 4 ? run_cluster_sort<4>(sa, s)
+                     : run_cluster_sort<8>(sa, s);
+  } else {
+    e = run_grid_sort(sa, pairs, s);
+    n = 2 * p.passes;
+  }
   if (e != cudaSuccess) return cuda_fail(e);
-  note_launch(n);
+  a.sorted = sa.out;
+  a.part = reinterpret_cast<float*>(mem + p.part);
+  SumLaunch f = {a, n, s};
+  if ((e = by_type(grad_dtype, a.D, vec, f)) != cudaSuccess) return cuda_fail(e);
+  note_launch(f.n);
   return DLRM_OK;
 }
 
