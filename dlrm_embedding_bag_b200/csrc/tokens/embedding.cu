@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <atomic>
 #include <climits>
+#include <cstddef>
 
 #include "common.h"
 #include "dlrm_tokens.h"
@@ -115,20 +116,20 @@ __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t by
 
 constexpr int kZeroBytes = 16 << 10;  // of a bulk store
 
-// Part `part` of `parts` of the zeros, by THREADS threads. zeros: kZeroBytes of
-// shared memory, 16-byte aligned, for this alone.
-template <int THREADS>
-__device__ void fill_zeros(const FillArgs& f, int part, int parts, uint8_t* zeros) {
-  const int64_t first = static_cast<int64_t>(part) * THREADS + threadIdx.x;
-  const int64_t step = static_cast<int64_t>(parts) * THREADS;
+// Part `part` of `parts` of the zeros, by the whole block. One stretch of bytes
+// goes out as bulk stores of a block of zeros, which one thread issues and which
+// run on by themselves until fill_end: a sort's blocks fill while they sort.
+// (A thread's own 16-byte stores, one after another, reached 6.0 TB/s, these
+// 6.4.) zeros: kZeroBytes of shared memory, 16-byte aligned, for this alone.
+__device__ void fill_begin(const FillArgs& f, int part, int parts, uint8_t* zeros) {
+  const int threads = blockDim.x;
+  const int64_t first = static_cast<int64_t>(part) * threads + threadIdx.x;
+  const int64_t step = static_cast<int64_t>(parts) * threads;
   if (f.pitch == f.row_bytes) {
-    // one stretch of bytes: bulk stores of a block of zeros between its
-    // unaligned ends (a thread's own 16-byte stores reached 4.3 TB/s, these
-    // are bound by the memory)
     const int64_t bytes = f.rows * f.row_bytes;
     const int64_t lead = min(bytes, static_cast<int64_t>(-reinterpret_cast<intptr_t>(f.out) & 15));
     const int64_t mid = (bytes - lead) & ~int64_t{15};
-    for (int i = threadIdx.x; i < kZeroBytes / 16; i += THREADS)
+    for (int i = threadIdx.x; i < kZeroBytes / 16; i += threads)
       reinterpret_cast<uint4*>(zeros)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
     __syncthreads();
@@ -138,8 +139,8 @@ __device__ void fill_zeros(const FillArgs& f, int part, int parts, uint8_t* zero
         bulk_s2g(f.out + lead + at, zeros,
                  static_cast<uint32_t>(min(static_cast<int64_t>(kZeroBytes), mid - at)));
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-      asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
+    // the unaligned ends
     if (first < lead) f.out[first] = 0;
     if (first < bytes - lead - mid) f.out[lead + mid + first] = 0;
   } else {
@@ -159,10 +160,16 @@ __device__ void fill_zeros(const FillArgs& f, int part, int parts, uint8_t* zero
   }
 }
 
+// The zeros that this block began are written.
+__device__ __forceinline__ void fill_end() {
+  if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
 // No tokens at all: the zeros alone.
 __global__ void __launch_bounds__(1024) fill_kernel(const FillArgs f) {
   __shared__ __align__(16) uint8_t zeros[kZeroBytes];
-  fill_zeros<1024>(f, blockIdx.x, gridDim.x, zeros);
+  fill_begin(f, blockIdx.x, gridDim.x, zeros);
+  fill_end();
 }
 
 // ---------------------------------------------------------------------------
@@ -180,12 +187,9 @@ __global__ void __launch_bounds__(1024) fill_kernel(const FillArgs f) {
 // scattered 8-byte pairs a warp, took 1.5 us a pair of a thread and pass.
 
 constexpr int kRadix = 256;
-constexpr int kCountThreads = 1024;
-constexpr int kCountLoads = 4;  // pairs a thread loads at once
-constexpr int kMoveThreads = 512;
-constexpr int kMoveItems = 16;  // pairs of a thread in a tile
-constexpr int kMoveTile = kMoveThreads * kMoveItems;
-constexpr int kSortMaxBlocks = 296;  // two move blocks an SM
+constexpr int kSortThreads = 512;  // of a block that counts or moves
+constexpr int kSortItems = 16;     // pairs of a thread, at most, in a tile
+constexpr int kSortMaxBlocks = 296;  // two blocks an SM
 constexpr int kClusterThreads = 1024;
 constexpr int kClusterSize = 8;       // CTAs
 constexpr int kClusterMaxItems = 8;  // pairs of a thread
@@ -199,10 +203,10 @@ struct SortArgs {
   int T, rows, pad;
   int shift, bits;
   int passes;  // of the cluster sort
-  int per;     // pairs of a block, a multiple of kMoveTile
-  int blocks;  // that sort; the others fill
+  int per;     // pairs of a block, a multiple of its tile
+  int blocks;  // that sort; the grid may have more, which only fill
   FillArgs fill;
-  int fill_part, fill_parts;  // the first filling block's part, and of how many
+  int fill_part, fill_parts;  // the first block's part of the zeros, and of how many
   int32_t* status;
 };
 
@@ -258,7 +262,7 @@ struct TileSmem {
   static constexpr int kWarps = THREADS / 32;
   static constexpr int kParts = THREADS / kRadix;  // threads of a digit
   static constexpr int kWarpsOfPart = kWarps / kParts;
-  uint2 pairs[THREADS * ITEMS];  // the tile in digit order
+  alignas(16) uint2 pairs[THREADS * ITEMS];  // the tile in digit order
   uint32_t at[kWarps][kRadix];
   uint32_t parts[kParts][kRadix];
   uint32_t start[kRadix];  // a digit's first place in `pairs`
@@ -330,97 +334,123 @@ __device__ __forceinline__ uint32_t order_tile(TileSmem<THREADS, ITEMS>& sm,
   return count;
 }
 
-__global__ void __launch_bounds__(kCountThreads) sort_count_kernel(const SortArgs a) {
+__global__ void __launch_bounds__(kSortThreads, 2) sort_count_kernel(const SortArgs a) {
   __shared__ __align__(16) uint8_t zeros[kZeroBytes];
-  if (static_cast<int>(blockIdx.x) >= a.blocks) {
-    fill_zeros<kCountThreads>(a.fill, a.fill_part + blockIdx.x - a.blocks, a.fill_parts, zeros);
-    return;
-  }
   __shared__ uint32_t cnt[kRadix];
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x;
   if (tid < kRadix) cnt[tid] = 0;
-  __syncthreads();
-  const int64_t begin = static_cast<int64_t>(blockIdx.x) * a.per;
-  const int64_t end = min(begin + a.per, static_cast<int64_t>(a.T));
-  const uint32_t mask = (1u << a.bits) - 1;
-  for (int64_t i0 = begin; i0 < end; i0 += kCountThreads * kCountLoads) {
-    uint32_t digit[kCountLoads];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the pass before is done
+  if (a.fill.out != nullptr) fill_begin(a.fill, a.fill_part + blockIdx.x, a.fill_parts, zeros);
+  if (static_cast<int>(blockIdx.x) < a.blocks) {
+    __syncthreads();
+    const int64_t begin = static_cast<int64_t>(blockIdx.x) * a.per;
+    const int64_t end = min(begin + a.per, static_cast<int64_t>(a.T));
+    const uint32_t mask = (1u << a.bits) - 1;
+    constexpr int kLoads = 4;  // pairs a thread loads at once
+    for (int64_t i0 = begin; i0 < end; i0 += kSortThreads * kLoads) {
+      uint32_t digit[kLoads];
 #pragma unroll
-    for (int u = 0; u < kCountLoads; ++u) {
-      const int64_t i = i0 + u * kCountThreads + tid;
-      digit[u] = kRadix;  // of no pair
-      if (i < end) {
-        flag_bad_id(a, i);
-        digit[u] = (sort_pair(a, i).x >> a.shift) & mask;
+      for (int u = 0; u < kLoads; ++u) {
+        const int64_t i = i0 + u * kSortThreads + tid;
+        digit[u] = kRadix;  // of no pair
+        if (i < end) {
+          flag_bad_id(a, i);
+          digit[u] = (sort_pair(a, i).x >> a.shift) & mask;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) {
+        // a warp whose digits are all the same (one frequent id) adds once
+        const bool same = __all_sync(kFull, digit[u] == __shfl_sync(kFull, digit[u], 0));
+        if (digit[u] != kRadix && (!same || (tid & 31) == 0))
+          atomicAdd(&cnt[digit[u]], same ? 32 : 1);
       }
     }
-#pragma unroll
-    for (int u = 0; u < kCountLoads; ++u) {
-      const unsigned peers = same_digit(digit[u], digit[u] != kRadix, a.bits);
-      if (digit[u] != kRadix && lane == __ffs(peers) - 1) atomicAdd(&cnt[digit[u]], __popc(peers));
-    }
+    __syncthreads();
+    if (tid < kRadix) a.counts[static_cast<int64_t>(blockIdx.x) * kRadix + tid] = cnt[tid];
   }
-  __syncthreads();
-  if (tid < kRadix) a.counts[static_cast<int64_t>(blockIdx.x) * kRadix + tid] = cnt[tid];
+  if (a.fill.out != nullptr) fill_end();
 }
 
+template <int ITEMS>
 struct MoveSmem {
-  TileSmem<kMoveThreads, kMoveItems> tile;
-  uint32_t total[kMoveThreads / kRadix][kRadix], before[kMoveThreads / kRadix][kRadix];
+  TileSmem<kSortThreads, ITEMS> tile;
+  uint8_t zeros[kZeroBytes];
   uint32_t place[kRadix];  // a digit's next place in the output
 };
 
-__global__ void __launch_bounds__(kMoveThreads, 2) sort_move_kernel(const SortArgs a) {
+template <int ITEMS>
+__global__ void __launch_bounds__(kSortThreads, 2) sort_move_kernel(const SortArgs a) {
   extern __shared__ __align__(16) uint8_t sort_smem[];
-  if (static_cast<int>(blockIdx.x) >= a.blocks) {
-    static_assert(sizeof(MoveSmem) >= kZeroBytes, "room for the zeros");
-    fill_zeros<kMoveThreads>(a.fill, a.fill_part + blockIdx.x - a.blocks, a.fill_parts, sort_smem);
-    return;
-  }
-  auto& sm = *reinterpret_cast<MoveSmem*>(sort_smem);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t mask = (1u << a.bits) - 1;
-  // digit d: pairs in all blocks, and in the blocks before this one
-  const int d = tid % kRadix, part = tid / kRadix;
-  uint32_t all = 0, place = 0;
+  auto& sm = *reinterpret_cast<MoveSmem<ITEMS>*>(sort_smem);
+  static_assert(offsetof(MoveSmem<ITEMS>, zeros) % 16 == 0, "bulk stores");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the counts are there
+  if (a.fill.out != nullptr) fill_begin(a.fill, a.fill_part + blockIdx.x, a.fill_parts, sm.zeros);
+  if (static_cast<int>(blockIdx.x) < a.blocks) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t mask = (1u << a.bits) - 1;
+    constexpr int kTile = kSortThreads * ITEMS;
+    const int64_t begin = static_cast<int64_t>(blockIdx.x) * a.per;
+    const int64_t end = min(begin + a.per, static_cast<int64_t>(a.T));
+    uint2 pair[ITEMS];
+    auto load = [&](int64_t i0) {
+#pragma unroll
+      for (int u = 0; u < ITEMS; ++u) {
+        const int64_t i = i0 + (warp * ITEMS + u) * 32 + lane;
+        pair[u] = make_uint2(0, 0);
+        if (i < end) pair[u] = sort_pair(a, i);
+      }
+    };
+    load(begin);
+    // pairs of each digit in all blocks and in the blocks before this one: four
+    // digits a thread, every eighth block
+    {
+      const int d4 = tid % (kRadix / 4), part = tid / (kRadix / 4);
+      const uint4* counts = reinterpret_cast<const uint4*>(a.counts) + d4;
+      uint4 all = make_uint4(0, 0, 0, 0), mine = all;
 #pragma unroll 8
-  for (int b = part; b < a.blocks; b += kMoveThreads / kRadix) {
-    const uint32_t c = a.counts[static_cast<int64_t>(b) * kRadix + d];
-    all += c;
-    place += b < static_cast<int>(blockIdx.x) ? c : 0;
-  }
-  sm.total[part][d] = all;
-  sm.before[part][d] = place;
-  __syncthreads();
-  all = place = 0;
-#pragma unroll
-  for (int p = 0; p < kMoveThreads / kRadix; ++p) {
-    all += sm.total[p][d];
-    place += sm.before[p][d];
-  }
-  place += digits_before(all, sm.tile.warp_sum);
-  if (tid < kRadix) sm.place[d] = place;
-  const int64_t begin = static_cast<int64_t>(blockIdx.x) * a.per;
-  const int64_t end = min(begin + a.per, static_cast<int64_t>(a.T));
-  for (int64_t i0 = begin; i0 < end; i0 += kMoveTile) {
-    const int n = static_cast<int>(min(static_cast<int64_t>(kMoveTile), end - i0));
-    uint2 pair[kMoveItems];
-#pragma unroll
-    for (int u = 0; u < kMoveItems; ++u) {
-      const int i = (warp * kMoveItems + u) * 32 + lane;
-      pair[u] = make_uint2(0, 0);
-      if (i < n) pair[u] = sort_pair(a, i0 + i);
-    }
-    __syncthreads();  // the tile before has left, its digits' places are set
-    const uint32_t count = order_tile(sm.tile, pair, n, a.shift, a.bits);
-    for (int k = tid; k < n; k += kMoveThreads) {
-      const uint2 p = sm.tile.pairs[k];
-      const uint32_t digit = (p.x >> a.shift) & mask;
-      a.out[sm.place[digit] + (k - sm.tile.start[digit])] = p;
+      for (int b = part; b < a.blocks; b += 8) {
+        const uint4 c = counts[static_cast<int64_t>(b) * (kRadix / 4)];
+        all.x += c.x, all.y += c.y, all.z += c.z, all.w += c.w;
+        if (b < static_cast<int>(blockIdx.x))
+          mine.x += c.x, mine.y += c.y, mine.z += c.z, mine.w += c.w;
+      }
+      // the tile's pairs come later
+      static_assert(sizeof(sm.tile.pairs) >= 2 * 8 * kRadix * 4, "room for the sums");
+      uint4* sums = reinterpret_cast<uint4*>(sm.tile.pairs);
+      sums[part * (kRadix / 4) + d4] = all;
+      sums[(8 + part) * (kRadix / 4) + d4] = mine;
     }
     __syncthreads();
-    if (tid < kRadix) sm.place[tid] += count;
+    uint32_t all = 0, place = 0;
+    if (tid < kRadix) {
+      const uint32_t* sums = reinterpret_cast<const uint32_t*>(sm.tile.pairs);
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        all += sums[p * kRadix + tid];
+        place += sums[(8 + p) * kRadix + tid];
+      }
+    }
+    place += digits_before(all, sm.tile.warp_sum);
+    if (tid < kRadix) sm.place[tid] = place;
+    for (int64_t i0 = begin; i0 < end; i0 += kTile) {
+      const int n = static_cast<int>(min(static_cast<int64_t>(kTile), end - i0));
+      if (i0 > begin) load(i0);
+      __syncthreads();  // the tile before has left, its digits' places are set
+      const uint32_t count = order_tile(sm.tile, pair, n, a.shift, a.bits);
+#pragma unroll 4
+      for (int k = tid; k < n; k += kSortThreads) {
+        const uint2 p = sm.tile.pairs[k];
+        const uint32_t digit = (p.x >> a.shift) & mask;
+        a.out[sm.place[digit] + (k - sm.tile.start[digit])] = p;
+      }
+      __syncthreads();
+      if (tid < kRadix) sm.place[tid] += count;
+    }
   }
+  if (a.fill.out != nullptr) fill_end();
 }
 
 __device__ __forceinline__ uint32_t load_cluster_u32(uint32_t cluster_addr) {
@@ -450,7 +480,8 @@ __global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(const 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (blockIdx.x >= kClusterSize) {
     static_assert(sizeof(ClusterSmem<ITEMS>) >= kZeroBytes, "room for the zeros");
-    fill_zeros<kClusterThreads>(a.fill, blockIdx.x - kClusterSize, a.fill_parts, sort_smem);
+    fill_begin(a.fill, blockIdx.x - kClusterSize, a.fill_parts, sort_smem);
+    fill_end();
     return;
   }
   auto& sm = *reinterpret_cast<ClusterSmem<ITEMS>*>(sort_smem);
@@ -554,26 +585,61 @@ cudaError_t run_cluster_sort(SortArgs& a, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, fn, a);
 }
 
+// A kernel that may be scheduled while the one before it ends, and waits for it.
+template <class... P, class... A>
+cudaError_t launch_after(void (*fn)(P...), dim3 grid, int threads, int smem,
+                         cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, args...);
+}
+
 // Sorts more tokens, two launches a pass, between the two buffers of pairs; the
 // zeros are shared out evenly over the launches. a.out ends as the sorted one.
+template <int ITEMS>
 cudaError_t run_grid_sort(SortArgs& a, uint2* const (&pairs)[2], cudaStream_t stream) {
-  constexpr int smem = sizeof(MoveSmem);
-  cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(&sort_move_kernel),
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  constexpr int smem = sizeof(MoveSmem<ITEMS>);
+  auto* move = &sort_move_kernel<ITEMS>;
+  static std::atomic<bool> prepared[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const int fillers = a.fill.out != nullptr ? 148 : 0;
-  a.fill_parts = 2 * a.passes * fillers;
+  const bool cacheable = dev >= 0 && dev < kMaxDevices;
+  if (!cacheable || !prepared[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(move),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    if (cacheable) prepared[dev].store(true, std::memory_order_release);
+  }
+  // blocks enough to keep the memory busy with zeros
+  const int grid = a.fill.out != nullptr ? std::max(a.blocks, 148) : a.blocks;
+  a.fill_parts = 2 * a.passes * grid;
   for (int i = 0; i < a.passes; ++i) {
     a.out = pairs[i & 1];
     a.shift = i * a.bits;
-    a.fill_part = 2 * i * fillers;
-    sort_count_kernel<<<a.blocks + fillers, kCountThreads, 0, stream>>>(a);
-    a.fill_part += fillers;
-    sort_move_kernel<<<a.blocks + fillers, kMoveThreads, smem, stream>>>(a);
+    a.fill_part = 2 * i * grid;
+    // the first launch waits for all that came before it on the stream
+    if (i == 0) {
+      sort_count_kernel<<<grid, kSortThreads, 0, stream>>>(a);
+      e = cudaGetLastError();
+    } else {
+      e = launch_after(&sort_count_kernel, dim3(grid), kSortThreads, 0, stream, a);
+    }
+    if (e != cudaSuccess) return e;
+    a.fill_part += grid;
+    if ((e = launch_after(move, dim3(grid), kSortThreads, smem, stream, a)) != cudaSuccess) return e;
     a.ids = nullptr;
     a.in = a.out;
   }
-  return cudaGetLastError();
+  return cudaSuccess;
 }
 
 // ---------------------------------------------------------------------------
@@ -921,22 +987,6 @@ __global__ void __launch_bounds__(kSumThreads) small_kernel(const SmallArgs a) {
     fill_unnamed(a.fill, keys, T, a.elem, blockIdx.x, gridDim.x, map);
 }
 
-// A kernel that may be scheduled while the one before it ends, and waits for it.
-template <class... P, class... A>
-cudaError_t launch_after(void (*fn)(P...), dim3 grid, int threads, cudaStream_t stream,
-                         const A&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fn, args...);
-}
-
 // The sums, then the runs that cross blocks. Launched kernels are added to n.
 struct SumLaunch {
   SumArgs a;
@@ -950,12 +1000,12 @@ struct SumLaunch {
     const int64_t blocks = static_cast<int64_t>(a.nblocks) * a.windows;
     if (blocks > INT_MAX) return cudaErrorInvalidValue;
     cudaError_t e = launch_after(&sum_kernel<In, VEC, G>, dim3(static_cast<unsigned>(blocks)),
-                                 kSumThreads, stream, a);
+                                 kSumThreads, 0, stream, a);
     if (e != cudaSuccess) return e;
     ++n;
     if (a.nblocks > 1) {
       const dim3 grid(a.nblocks - 1, (a.D + kJoinCols - 1) / kJoinCols);
-      e = launch_after(&join_kernel, grid, kJoinWarps * 32, stream, a);
+      e = launch_after(&join_kernel, grid, kJoinWarps * 32, 0, stream, a);
       ++n;
     }
     return e;
@@ -1000,7 +1050,7 @@ cudaError_t by_type(int dtype, int D, bool vec, F& f) {
 
 // Sizes of a gradient's scratch, and where its parts lie.
 struct GradPlan {
-  int sort_blocks, per, passes, bits;
+  int sort_blocks, per, items, passes, bits;
   int chunk;
   int64_t nblocks, Dp;
   int64_t pairs[2], counts, part, bytes;  // byte offsets, and the sum
@@ -1012,8 +1062,15 @@ GradPlan plan_grad(int64_t T, int64_t rows, int64_t D) {
   while ((rows >> key_bits) != 0) ++key_bits;
   p.passes = (key_bits + 7) / 8;
   p.bits = (key_bits + p.passes - 1) / p.passes;
-  int64_t per = (T + kSortMaxBlocks - 1) / kSortMaxBlocks;
-  per = std::max<int64_t>(1, (per + kMoveTile - 1) / kMoveTile) * kMoveTile;
+  // tiles that give about two blocks an SM while one tile a block will do (4608
+  // pairs: up to 1.36 M tokens), whole tiles of 8192 pairs a block beyond
+  const int64_t share = (T + kSortMaxBlocks - 1) / kSortMaxBlocks;
+  p.items = share <= kSortThreads * 4   ? 4
+            : share <= kSortThreads * 6 ? 6
+            : share <= kSortThreads * 9 ? 9
+                                        : kSortItems;
+  const int64_t tile = kSortThreads * p.items;
+  const int64_t per = std::max<int64_t>(1, (share + tile - 1) / tile) * tile;
   p.per = static_cast<int>(per);
   p.sort_blocks = static_cast<int>((T + per - 1) / per);
   // a group's tokens: as few as are in flight at once while that fills the
@@ -1193,7 +1250,10 @@ int dlrm_embedding_grad(const void* grad, int grad_dtype, int64_t ldg, const int
         : items <= 4 ? run_cluster_sort<4>(sa, s)
                      : run_cluster_sort<8>(sa, s);
   } else {
-    e = run_grid_sort(sa, pairs, s);
+    e = p.items == 4   ? run_grid_sort<4>(sa, pairs, s)
+        : p.items == 6 ? run_grid_sort<6>(sa, pairs, s)
+        : p.items == 9 ? run_grid_sort<9>(sa, pairs, s)
+                       : run_grid_sort<kSortItems>(sa, pairs, s);
     n = 2 * p.passes;
   }
   if (e != cudaSuccess) return cuda_fail(e);

@@ -172,6 +172,7 @@ GRADS = [  # T, rows, D
     (777, 40, 1000), (5000, 100000, 36), (333, 50, 129), (150, 20, 4100), (30000, 17, 64),
     (150001, 70001, 4), (170001, 3000, 128), (400007, 900, 100), (31000, 70, 4100),
     (511, 64, 64), (512, 40000, 100), (512, 2000000, 4), (513, 64, 64), (300, 9000, 1000),
+    (700001, 900000, 4), (1000003, 70, 4), (1600001, 20000, 4),
     (8192, 300, 8), (8193, 70000, 8), (20000, 5, 16), (65536, 3000, 8), (65537, 3000, 8),
 ]
 
