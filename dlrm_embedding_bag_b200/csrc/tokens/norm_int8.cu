@@ -16,7 +16,7 @@ namespace dlrm {
 namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kNormThreads = 256;
+constexpr int kNormThreads = 512;  // of a row that does not fit registers
 constexpr uint32_t kInfBits = 0x7f800000u;
 
 struct NormArgs {
@@ -32,15 +32,16 @@ struct NormArgs {
   int norm;  // 0: the rows as they are (rstd = 1)
 };
 
-// Sum and largest bit pattern over the block; every thread gets both.
+// Sum and largest bit pattern over the THREADS threads of a row: a warp, or the
+// whole block. Every thread gets both.
 template <int THREADS>
-__device__ __forceinline__ void block_sum_max(float& sum, uint32_t& top) {
-  __shared__ float sums[THREADS / 32];
-  __shared__ uint32_t tops[THREADS / 32];
+__device__ __forceinline__ void row_sum_max(float& sum, uint32_t& top) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
   top = __reduce_max_sync(kFull, top);
   if constexpr (THREADS > 32) {
+    __shared__ float sums[THREADS / 32];
+    __shared__ uint32_t tops[THREADS / 32];
     __syncthreads();  // an earlier call's values have been read
     if ((threadIdx.x & 31) == 0) {
       sums[threadIdx.x >> 5] = sum;
@@ -60,7 +61,14 @@ __device__ __forceinline__ void block_sum_max(float& sum, uint32_t& top) {
 // |t|'s bits: as unsigned numbers they order like |t|, infinities and NaNs last.
 __device__ __forceinline__ uint32_t abs_bits(float t) { return __float_as_uint(t) & 0x7fffffffu; }
 
-// A row's factors: q = rint(t * pre * inv).
+// max(|t|, top), NaN if either is.
+__device__ __forceinline__ float max_abs(float top, float t) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(top), "f"(fabsf(t)));
+  return r;
+}
+
+// A row's factors: its levels are t * pre * inv, rounded.
 struct Levels {
   float pre, inv;
 };
@@ -75,9 +83,11 @@ __device__ __forceinline__ Levels levels_of(uint32_t top) {
   return f;
 }
 
-__device__ __forceinline__ int8_t level(float t, Levels f) {
-  // f.inv is 0 for a row of zeros and for one with a NaN or an infinity: 0
-  return f.inv == 0.f ? 0 : static_cast<int8_t>(__float2int_rn(t * f.pre * f.inv));
+// t * inv rounded to the nearest whole number, ties to even, in the low byte:
+// added to 1.5 * 2^23, where a step of f32 is 1, in one fused rounding. (The
+// conversion instruction runs at an eighth of this rate.)
+__device__ __forceinline__ uint32_t level_bits(float t, float inv) {
+  return __float_as_uint(__fmaf_rn(t, inv, 12582912.f));
 }
 
 // Chunk of VEC elements of a row at column c: h = x + residual.
@@ -109,17 +119,22 @@ __device__ __forceinline__ void load_weight(const NormArgs& a, int c, float (&w)
 }
 
 template <int VEC>
-__device__ __forceinline__ void store_levels(int8_t* p, const float (&t)[VEC], Levels f) {
+__device__ __forceinline__ void store_levels(int8_t* p, float (&t)[VEC], Levels f) {
+  if (f.pre != 1.f) {  // the same for the whole row
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) t[e] *= f.pre;
+  }
+  // inv is 0 for a row of zeros, and for one with a NaN or an infinity
+  const bool none = f.inv == 0.f;
   if constexpr (VEC == 1) {
-    *p = level(t[0], f);
+    *p = none ? 0 : static_cast<int8_t>(level_bits(t[0], f.inv) & 0xff);
   } else {
     uint32_t w[VEC / 4];
 #pragma unroll
     for (int i = 0; i < VEC / 4; ++i) {
-      w[i] = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        w[i] |= static_cast<uint32_t>(static_cast<uint8_t>(level(t[4 * i + e], f))) << (8 * e);
+      const uint32_t lo = __byte_perm(level_bits(t[4 * i], f.inv), level_bits(t[4 * i + 1], f.inv), 0x0040);
+      const uint32_t hi = __byte_perm(level_bits(t[4 * i + 2], f.inv), level_bits(t[4 * i + 3], f.inv), 0x0040);
+      w[i] = none ? 0u : __byte_perm(lo, hi, 0x5410);
     }
     if constexpr (VEC == 4)
       *reinterpret_cast<uint32_t*>(p) = w[0];
@@ -129,31 +144,22 @@ __device__ __forceinline__ void store_levels(int8_t* p, const float (&t)[VEC], L
 }
 
 // The squares of a row left the range of f32 (or vanished in it) although the
-// row itself did not: its scale from squares of h / max|h|. Reads the row
-// again, before anything of it is written.
-template <class T, int VEC, int THREADS>
-__device__ float far_scale(const NormArgs& a, int64_t m, uint32_t top) {
-  float none = 0.f, sum = 0.f;
+// row itself did not: its scale from squares of h / max|h|. `each` calls its
+// argument with every h of the thread.
+template <int THREADS, class Each>
+__device__ float far_scale(const NormArgs& a, uint32_t top, Each each) {
+  float sum = 0.f;
   uint32_t hbits = 0;
-  for (int c = threadIdx.x * VEC; c < a.K; c += THREADS * VEC) {
-    float h[VEC];
-    load_h<T, VEC>(a, m, c, h);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) hbits = max(hbits, abs_bits(h[e]));
-  }
-  block_sum_max<THREADS>(none, hbits);
+  each([&](float h) { hbits = max(hbits, abs_bits(h)); });
+  row_sum_max<THREADS>(sum, hbits);
   const float big = __uint_as_float(hbits);
-  for (int c = threadIdx.x * VEC; c < a.K; c += THREADS * VEC) {
-    float h[VEC];
-    load_h<T, VEC>(a, m, c, h);
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const float s = __fdiv_rn(h[e], big);
-      sum += s * s;
-    }
-  }
+  sum = 0.f;
+  each([&](float h) {
+    const float s = __fdiv_rn(h, big);
+    sum += s * s;
+  });
   uint32_t unused = 0;
-  block_sum_max<THREADS>(sum, unused);
+  row_sum_max<THREADS>(sum, unused);
   const double mean = static_cast<double>(big) * big * (static_cast<double>(sum) / a.K) + a.eps;
   return static_cast<float>(static_cast<double>(__uint_as_float(top)) / sqrt(mean) / 127.0);
 }
@@ -170,13 +176,80 @@ __device__ __forceinline__ float scale_of(const NormArgs& a, float sum, uint32_t
   return __fdiv_rn(__fmul_rn(A, __frsqrt_rn(mean)), 127.f);
 }
 
-// A block for each row, which it reads twice (the second time from L2): any
-// row length.
+// Rows that fit the registers of TPR threads (a warp, or a block), CH chunks of VEC
+// elements each: read once, 128 bits a load. Bound by the memory: 16384 rows of
+// 4096 bf16 with a residual move 470 MB.
+template <class T, int VEC, int TPR, int CH>
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
+    norm_row_kernel(const NormArgs a) {
+  constexpr int kRows = TPR < 128 ? 128 / TPR : 1;  // rows of a block
+  const int64_t m = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / TPR;
+  if (m >= a.M) return;  // whole warps, and only where a row is a warp's
+  const int q = threadIdx.x % TPR;
+  // all of the row's loads first
+  Raw<T, VEC> xs[CH], rs[CH];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = (i * TPR + q) * VEC;
+    xs[i] = rs[i] = Raw<T, VEC>();
+    if (c < a.K) {
+      xs[i] = *reinterpret_cast<const Raw<T, VEC>*>(static_cast<const T*>(a.x) + m * a.ldx + c);
+      if (a.residual != nullptr)
+        rs[i] = *reinterpret_cast<const Raw<T, VEC>*>(static_cast<const T*>(a.residual) + m * a.ldr + c);
+    }
+  }
+  float h[CH][VEC];
+  float sum = 0.f, most = 0.f;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = (i * TPR + q) * VEC;
+    float r[VEC];
+    widen<T, VEC>(xs[i], h[i]);
+    widen<T, VEC>(rs[i], r);
+    if (c < a.K) {
+      float w[VEC];
+      load_weight<VEC>(a, c, w);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        if (a.residual != nullptr) h[i][e] += r[e];
+        sum += h[i][e] * h[i][e];
+        most = max_abs(most, h[i][e] * w[e]);
+      }
+    }
+  }
+  uint32_t top = __float_as_uint(most);
+  row_sum_max<TPR>(sum, top);
+  bool far;
+  float s = scale_of(a, sum, top, far);
+  if (far)
+    s = far_scale<TPR>(a, top, [&](auto f) {
+#pragma unroll
+      for (int i = 0; i < CH; ++i)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) f(h[i][e]);  // past the row: 0
+    });
+  if (q == 0) a.scale[m] = s;
+  const Levels f = levels_of(top);
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = (i * TPR + q) * VEC;
+    if (c < a.K) {
+      if (a.h_out != nullptr) store_f32<T, VEC>(static_cast<T*>(a.h_out) + m * a.ldh + c, h[i]);
+      float w[VEC];
+      load_weight<VEC>(a, c, w);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) w[e] *= h[i][e];
+      store_levels<VEC>(a.q + m * a.ldq + c, w, f);
+    }
+  }
+}
+
+// Longer rows, and rows that 128-bit accesses cannot walk: a block for each row,
+// which it reads twice (the second time from L2).
 template <class T, int VEC>
 __global__ void __launch_bounds__(kNormThreads) norm_loop_kernel(const NormArgs a) {
   for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
-    float sum = 0.f;
-    uint32_t top = 0;
+    float sum = 0.f, most = 0.f;
     for (int c = threadIdx.x * VEC; c < a.K; c += kNormThreads * VEC) {
       float h[VEC], w[VEC];
       load_h<T, VEC>(a, m, c, h);
@@ -184,13 +257,22 @@ __global__ void __launch_bounds__(kNormThreads) norm_loop_kernel(const NormArgs 
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         sum += h[e] * h[e];
-        top = max(top, abs_bits(h[e] * w[e]));
+        most = max_abs(most, h[e] * w[e]);
       }
     }
-    block_sum_max<kNormThreads>(sum, top);
+    uint32_t top = __float_as_uint(most);
+    row_sum_max<kNormThreads>(sum, top);
     bool far;
     float s = scale_of(a, sum, top, far);
-    if (far) s = far_scale<T, VEC, kNormThreads>(a, m, top);
+    if (far)  // reads the row again, before anything of it is written
+      s = far_scale<kNormThreads>(a, top, [&](auto f) {
+        for (int c = threadIdx.x * VEC; c < a.K; c += kNormThreads * VEC) {
+          float h[VEC];
+          load_h<T, VEC>(a, m, c, h);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) f(h[e]);
+        }
+      });
     if (threadIdx.x == 0) a.scale[m] = s;
     const Levels f = levels_of(top);
     for (int c = threadIdx.x * VEC; c < a.K; c += kNormThreads * VEC) {
@@ -206,10 +288,35 @@ __global__ void __launch_bounds__(kNormThreads) norm_loop_kernel(const NormArgs 
 }
 
 template <class T, int VEC>
-cudaError_t run_norm(const NormArgs& a, cudaStream_t stream) {
+cudaError_t run_loop(const NormArgs& a, cudaStream_t stream) {
   const int64_t blocks = std::min<int64_t>(a.M, 148 * 64);
   norm_loop_kernel<T, VEC><<<static_cast<unsigned>(blocks), kNormThreads, 0, stream>>>(a);
   return cudaGetLastError();
+}
+
+template <class T, int TPR, int CH>
+cudaError_t run_row(const NormArgs& a, cudaStream_t stream) {
+  constexpr int kThreads = TPR < 128 ? 128 : TPR, kRows = kThreads / TPR;
+  const int64_t blocks = (static_cast<int64_t>(a.M) + kRows - 1) / kRows;
+  norm_row_kernel<T, kVecOf<T>, TPR, CH>
+      <<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+// Four chunks a thread where rows are many (a row's loads all in flight, many
+// rows an SM); one where they are few and a row's latency is what counts.
+template <class T>
+cudaError_t run_norm(const NormArgs& a, bool vec, cudaStream_t stream) {
+  if (!vec) return run_loop<T, 1>(a, stream);
+  const int chunks = a.K / kVecOf<T>;
+  const bool few = a.M <= 148 * 4;
+  if (chunks <= 32) return run_row<T, 32, 1>(a, stream);
+  if (chunks <= 128) return few ? run_row<T, 128, 1>(a, stream) : run_row<T, 32, 4>(a, stream);
+  if (chunks <= 512) return few ? run_row<T, 512, 1>(a, stream) : run_row<T, 128, 4>(a, stream);
+  if (chunks <= 1024) return few ? run_row<T, 1024, 1>(a, stream) : run_row<T, 256, 4>(a, stream);
+  if (chunks <= 2048) return run_row<T, 512, 4>(a, stream);
+  if (chunks <= 4096) return run_row<T, 1024, 4>(a, stream);
+  return run_loop<T, kVecOf<T>>(a, stream);
 }
 
 int norm_rows(const NormArgs& a, int dtype, cudaStream_t stream) {
@@ -222,9 +329,9 @@ int norm_rows(const NormArgs& a, int dtype, cudaStream_t stream) {
   using B = __nv_bfloat16;
   cudaError_t e;
   if (dtype == DLRM_TABLE_F32)
-    e = vec ? run_norm<float, 4>(a, stream) : run_norm<float, 1>(a, stream);
+    e = run_norm<float>(a, vec, stream);
   else
-    e = vec ? run_norm<B, 8>(a, stream) : run_norm<B, 1>(a, stream);
+    e = run_norm<B>(a, vec, stream);
   if (e != cudaSuccess) return cuda_fail(e);
   note_launch();
   return DLRM_OK;
@@ -240,25 +347,29 @@ int check_rows(const void* x, int64_t ldx, int dtype, int64_t M, int64_t K, cons
   return DLRM_OK;
 }
 
-// y = q * scale: a block walks rows, VEC columns a thread.
+// y = q * scale: a block walks rows, VEC columns a thread (16: one 128-bit load).
 template <class T, int VEC>
 __global__ void __launch_bounds__(256)
     dequant_kernel(const int8_t* q, int64_t ldq, const float* scale, int M, int K, T* y,
                    int64_t ldy) {
   for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
     const float s = __ldg(scale + m);
-    for (int c = threadIdx.x * VEC; c < K; c += 256 * VEC) {
-      float v[VEC];
+    for (int c = threadIdx.x * VEC; c < K; c += blockDim.x * VEC) {
       if constexpr (VEC == 1) {
-        v[0] = static_cast<float>(q[m * ldq + c]) * s;
+        const float v[1] = {static_cast<float>(q[m * ldq + c]) * s};
+        store_f32<T, 1>(y + m * ldy + c, v);
       } else {
-        const uint2 r = __ldg(reinterpret_cast<const uint2*>(q + m * ldq + c));
-        const uint32_t w[2] = {r.x, r.y};
+        const uint4 r = __ldg(reinterpret_cast<const uint4*>(q + m * ldq + c));
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          v[e] = static_cast<float>(static_cast<int8_t>(w[e / 4] >> (8 * (e % 4)))) * s;
+        for (int i = 0; i < 2; ++i) {
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            v[e] = static_cast<float>(static_cast<int8_t>(w[2 * i + e / 4] >> (8 * (e % 4)))) * s;
+          store_f32<T, 8>(y + m * ldy + c + 8 * i, v);
+        }
       }
-      store_f32<T, VEC>(y + m * ldy + c, v);
     }
   }
 }
@@ -267,13 +378,15 @@ template <class T>
 cudaError_t run_dequant(const int8_t* q, int64_t ldq, const float* scale, int64_t M, int64_t K,
                         T* y, int64_t ldy, cudaStream_t stream) {
   const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(M, 148 * 64));
-  const bool vec = K % 8 == 0 && is_aligned(q, 8) && ldq % 8 == 0 && rows16(y, ldy, sizeof(T));
+  const bool vec = K % 16 == 0 && is_aligned(q, 16) && ldq % 16 == 0 && rows16(y, ldy, sizeof(T));
+  const int64_t per_row = vec ? K / 16 : K;
+  const int threads = static_cast<int>(std::min<int64_t>(256, (per_row + 31) / 32 * 32));
   if (vec)
-    dequant_kernel<T, 8><<<blocks, 256, 0, stream>>>(q, ldq, scale, static_cast<int>(M),
-                                                     static_cast<int>(K), y, ldy);
+    dequant_kernel<T, 16><<<blocks, threads, 0, stream>>>(q, ldq, scale, static_cast<int>(M),
+                                                          static_cast<int>(K), y, ldy);
   else
-    dequant_kernel<T, 1><<<blocks, 256, 0, stream>>>(q, ldq, scale, static_cast<int>(M),
-                                                     static_cast<int>(K), y, ldy);
+    dequant_kernel<T, 1><<<blocks, threads, 0, stream>>>(q, ldq, scale, static_cast<int>(M),
+                                                         static_cast<int>(K), y, ldy);
   return cudaGetLastError();
 }
 
