@@ -103,4 +103,24 @@ __device__ __forceinline__ void store_f32(T* p, const float (&v)[VEC]) {
   }
 }
 
+// The same, for values that nobody reads soon: they leave L2 first, before what
+// is read again.
+template <class T, int VEC>
+__device__ __forceinline__ void store_f32_once(T* p, const float (&v)[VEC]) {
+  if constexpr (VEC == 1) {
+    store_f32<T, 1>(p, v);
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < VEC; i += 4)
+      __stcs(reinterpret_cast<float4*>(p + i), make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
+  } else if constexpr (VEC == 4) {
+    __stcs(reinterpret_cast<uint2*>(p),
+           make_uint2(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3])));
+  } else {
+    __stcs(reinterpret_cast<uint4*>(p),
+           make_uint4(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]),
+                      bf16x2_bits(v[4], v[5]), bf16x2_bits(v[6], v[7])));
+  }
+}
+
 }  // namespace dlrm

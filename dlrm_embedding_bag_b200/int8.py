@@ -15,8 +15,10 @@ from typing import Optional, Tuple
 
 import torch
 
+from . import ops
 from .mlp import ACTS
-from .tokens import _call, _code, _flat, _lib, _on, _pitch, _status
+from .tokens import (_call, _code, _empty, _empty_vector, _flat, _lib, _on, _pitch,
+                     _status)
 
 MAX_K = 131071
 
@@ -51,7 +53,7 @@ def _outputs(x, M, K, out, scale_out, index):
     """(out, scale_out, out's pitch): the 8-bit matrix and its scales, made where not given."""
     if out is None:
         pitch = (K + 15) // 16 * 16
-        out = x.new_empty((M, pitch), dtype=torch.int8)
+        out = _empty(M, pitch, torch.int8, index)
         if pitch != K:
             out = out[:, :K]
     else:
@@ -59,7 +61,7 @@ def _outputs(x, M, K, out, scale_out, index):
         if rows != M or cols != K:
             raise ValueError(f"out must be ({M}, {K}) (got {tuple(out.shape)})")
     if scale_out is None:
-        scale_out = x.new_empty(M, dtype=torch.float32)
+        scale_out = _empty_vector(M, torch.float32, index)
     else:
         _scales(scale_out, "scale_out", M, index)
     return out, scale_out, pitch
@@ -101,7 +103,7 @@ def rms_norm_int8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
             raise ValueError(f"residual must be {x.dtype} ({M}, {K})")
         pr, ldr = residual.data_ptr(), _pitch(residual, "residual")[2]
         if residual_out is None:
-            residual_out = x.new_empty((M, K))
+            residual_out = _empty(M, K, x.dtype, index)
             ldh = K
         else:
             _on(residual_out, "residual_out", index)
@@ -126,15 +128,17 @@ def dequantize_rows(q: torch.Tensor, scale: torch.Tensor, *,
     M, K, ldq = _int8(q, "q", index)
     ps = _scales(scale, "scale", M, index)
     if out is None:
-        out = q.new_empty((M, K), dtype=dtype)
-        ldo = K
+        od, ldo = ops.TABLE_DTYPES.get(dtype), K
+        if od is None:
+            raise TypeError(f"dtype must be float32 or bfloat16 (got {dtype})")
+        out = _empty(M, K, dtype, index)
     else:
         _on(out, "out", index)
         if out.shape != (M, K):
             raise ValueError(f"out must be ({M}, {K}) (got {tuple(out.shape)})")
-        ldo = _pitch(out, "out")[2]
+        od, ldo = _code(out, "out"), _pitch(out, "out")[2]
     _call(_dequantize, "dlrm_dequantize_int8", index, q.data_ptr(), ldq, ps, M, K,
-          out.data_ptr(), _code(out, "out"), ldo)
+          out.data_ptr(), od, ldo)
     return out
 
 
@@ -164,18 +168,20 @@ def linear_int8(x_q: torch.Tensor, x_scale: torch.Tensor, w_q: torch.Tensor,
     pws = _scales(w_scale, "w_scale", N, index)
     pb = _scales(bias, "bias", N, index) if bias is not None else None
     if out is None:
-        out = x_q.new_empty((M, N), dtype=out_dtype)
-        ldo = N
+        od, ldo = ops.TABLE_DTYPES.get(out_dtype), N
+        if od is None:
+            raise TypeError(f"out_dtype must be float32 or bfloat16 (got {out_dtype})")
+        out = _empty(M, N, out_dtype, index)
     else:
         _on(out, "out", index)
         if out.shape != (M, N):
             raise ValueError(f"out must be ({M}, {N}) (got {tuple(out.shape)})")
-        ldo = _pitch(out, "out")[2]
+        od, ldo = _code(out, "out"), _pitch(out, "out")[2]
     # a single row's pitch is not used to find another one: its own length will do
     if M == 1:
         ldx = (ldx + 15) // 16 * 16
     if N == 1:
         ldw = (ldw + 15) // 16 * 16
     _call(_linear, "dlrm_linear_int8", index, x_q.data_ptr(), ldx, pxs, w_q.data_ptr(), ldw, pws,
-          pb, M, N, K, code, out.data_ptr(), _code(out, "out"), ldo, _status(status, index))
+          pb, M, N, K, code, out.data_ptr(), od, ldo, _status(status, index))
     return out
