@@ -18,12 +18,16 @@ constexpr int kMaxDevices = 64;  // devices whose launch set-up is cached
 // ---------------------------------------------------------------------------
 // Lookup: Y[t] = scale * W[ids[t]].
 //
-// G lanes walk one row, VEC elements each per step; a group takes kRowsInFlight
-// tokens at a time, so that as many row loads are in the air before the first
-// is used. No arithmetic to speak of: bound by the bytes of the rows read and
-// written.
+// G lanes take a window of G * VEC columns of kRowsInFlight tokens' rows, all
+// loads in the air before the first is used. No arithmetic to speak of: bound by
+// the bytes of the rows. Y is written past the cache's order of use, which keeps
+// frequent rows in L2. Measured on B200, 1310720 tokens of 512-byte rows under a
+// power law of 1.2 (671 MB written): 135 us; with 256 threads a block 141, 512
+// threads 148, two rows in flight 147, ordinary stores 4 us more; 16383 tokens
+// of 2000-byte rows: 10.3 us (6.4 TB/s), 15.8 where a group walks all windows
+// of its rows instead.
 
-constexpr int kLookupThreads = 256;
+constexpr int kLookupThreads = 128;
 constexpr int kRowsInFlight = 4;
 
 struct LookupArgs {
@@ -33,6 +37,7 @@ struct LookupArgs {
   void* out;
   int64_t ldo;
   int rows, D, T, pad;
+  int windows;  // of G * VEC columns
   float scale;
   int32_t* status;
 };
@@ -42,8 +47,9 @@ __global__ void __launch_bounds__(kLookupThreads) lookup_kernel(const LookupArgs
   const In* W = static_cast<const In*>(a.table);
   Out* Y = static_cast<Out*>(a.out);
   const int q = threadIdx.x % G;
-  const int64_t group = (static_cast<int64_t>(blockIdx.x) * kLookupThreads + threadIdx.x) / G;
-  const int64_t t0 = group * kRowsInFlight;
+  const int64_t unit = (static_cast<int64_t>(blockIdx.x) * kLookupThreads + threadIdx.x) / G;
+  const int64_t t0 = unit / a.windows * kRowsInFlight;
+  const int c = (static_cast<int>(unit % a.windows) * G + q) * VEC;
   int id[kRowsInFlight];
 #pragma unroll
   for (int u = 0; u < kRowsInFlight; ++u) {
@@ -55,28 +61,32 @@ __global__ void __launch_bounds__(kLookupThreads) lookup_kernel(const LookupArgs
       id[u] = (in && r != a.pad) ? r : a.rows;  // `rows`: a row of zeros
     }
   }
-  for (int c = q * VEC; c < a.D; c += G * VEC) {
-    float v[kRowsInFlight][VEC];
+  if (c >= a.D) return;
+  Raw<In, VEC> raw[kRowsInFlight];
 #pragma unroll
-    for (int u = 0; u < kRowsInFlight; ++u) {
+  for (int u = 0; u < kRowsInFlight; ++u) {
+    raw[u] = Raw<In, VEC>();
+    if (id[u] >= 0 && id[u] < a.rows)
+      raw[u] = __ldg(reinterpret_cast<const Raw<In, VEC>*>(W + static_cast<int64_t>(id[u]) * a.ldw + c));
+  }
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) v[u][e] = 0.f;
-      if (id[u] >= 0 && id[u] < a.rows) {
-        load_f32<In, VEC>(W + static_cast<int64_t>(id[u]) * a.ldw + c, v[u]);
+  for (int u = 0; u < kRowsInFlight; ++u) {
+    if (id[u] >= 0) {
+      float v[VEC];
+      widen<In, VEC>(raw[u], v);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) v[u][e] *= a.scale;
-      }
+      for (int e = 0; e < VEC; ++e) v[e] = id[u] < a.rows ? v[e] * a.scale : 0.f;
+      store_f32_once<Out, VEC>(Y + (t0 + u) * a.ldo + c, v);
     }
-#pragma unroll
-    for (int u = 0; u < kRowsInFlight; ++u)
-      if (id[u] >= 0) store_f32<Out, VEC>(Y + (t0 + u) * a.ldo + c, v[u]);
   }
 }
 
 template <class In, class Out, int VEC, int G>
-cudaError_t run_lookup(const LookupArgs& a, cudaStream_t stream) {
-  constexpr int per_block = kLookupThreads / G * kRowsInFlight;
-  const int64_t blocks = (static_cast<int64_t>(a.T) + per_block - 1) / per_block;
+cudaError_t run_lookup(LookupArgs a, cudaStream_t stream) {
+  a.windows = (a.D + G * VEC - 1) / (G * VEC);
+  const int64_t units = (static_cast<int64_t>(a.T) + kRowsInFlight - 1) / kRowsInFlight * a.windows;
+  const int64_t blocks = (units * G + kLookupThreads - 1) / kLookupThreads;
+  if (blocks > INT_MAX) return cudaErrorInvalidValue;
   lookup_kernel<In, Out, VEC, G><<<static_cast<unsigned>(blocks), kLookupThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
