@@ -434,6 +434,122 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) tmem_dealloc<CG>(tmem, kCols);
 }
 
+// Few tokens: a warp for each R output channels, four products an instruction,
+// the weights read once with 128-bit loads past L1 (which the tokens' rows,
+// read by every warp, keep), eight in flight a lane. Bound by reading the
+// weights, with about 2 us for a launch's latencies around it. Measured on B200
+// in a graph, 16 MB of weights from HBM, against the cluster form below: one
+// token 5.1 (R = 1, K = 4096; 3.3 TB/s) and 7.9 us, two 6.4 and 8.0, four 8.0
+// and 8.3, eight 11.1 and 8.9; 8192 channels of K = 2048 with R = 2: one 5.1
+// and 7.6, four 5.8 and 8.1. R = 2 is slower at K = 4096 (6.9 us), R = 1 at K =
+// 2048 (5.6 us).
+constexpr int kVecThreads = 256;
+constexpr int kFewTokens = 4;
+
+struct VecArgs {
+  LinArgs lin;
+  const int8_t* x;
+  const int8_t* w;
+  int64_t ldx, ldw;
+  int K;
+};
+
+__device__ __forceinline__ uint4 load_once(const int8_t* p) {
+  uint4 r;
+  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+      : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+      : "l"(p));
+  return r;
+}
+
+__device__ __forceinline__ int dot16(const uint4& a, const uint4& b, int s) {
+  s = __dp4a(static_cast<int>(a.x), static_cast<int>(b.x), s);
+  s = __dp4a(static_cast<int>(a.y), static_cast<int>(b.y), s);
+  s = __dp4a(static_cast<int>(a.z), static_cast<int>(b.z), s);
+  return __dp4a(static_cast<int>(a.w), static_cast<int>(b.w), s);
+}
+
+template <int MT, int R, int ACT, class Out>
+__device__ __forceinline__ void put_sums(const VecArgs& a, int n0, const int (&acc)[R][MT]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+      if (lane == r * MT + m && n0 + r < a.lin.N && m < a.lin.M) {
+        const int n = n0 + r;
+        const Channel ch = {__ldg(a.lin.w_scale + n),
+                            a.lin.bias != nullptr ? __ldg(a.lin.bias + n) : 0.f, true};
+        put<ACT, Out>(a.lin, ch, n, m, acc[r][m], __ldg(a.lin.x_scale + m));
+      }
+}
+
+template <int MT, int R>
+struct PutCall {
+  const VecArgs& a;
+  int n0;
+  const int (&acc)[R][MT];
+  template <int ACT, class Out>
+  __device__ __forceinline__ void run() const {
+    put_sums<MT, R, ACT, Out>(a, n0, acc);
+  }
+};
+
+template <int MT, int R>
+__global__ void __launch_bounds__(kVecThreads) linear_few_kernel(const VecArgs a) {
+  static_assert(MT * R <= 32, "a lane for each output");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31;
+  const int n0 = (blockIdx.x * (kVecThreads / 32) + (threadIdx.x >> 5)) * R;
+  if (n0 >= a.lin.N) return;
+  const int8_t* w[R];
+  const int8_t* x[MT];
+#pragma unroll
+  for (int r = 0; r < R; ++r) w[r] = a.w + min(n0 + r, a.lin.N - 1) * a.ldw;
+#pragma unroll
+  for (int m = 0; m < MT; ++m) x[m] = a.x + min(m, a.lin.M - 1) * a.ldx;
+  int acc[R][MT] = {};
+  constexpr int U = 8 / R;  // K steps in flight
+  const int whole = a.K / 16 * 16;
+  for (int k0 = lane * 16; k0 < whole; k0 += 512 * U) {
+    uint4 wv[U][R];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        wv[u][r] = make_uint4(0, 0, 0, 0);
+        if (k0 + u * 512 < whole) wv[u][r] = load_once(w[r] + k0 + u * 512);
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      uint4 xv[MT];
+      const int k = min(k0 + u * 512, whole - 16);  // past the end: against zeros
+#pragma unroll
+      for (int m = 0; m < MT; ++m) xv[m] = __ldg(reinterpret_cast<const uint4*>(x[m] + k));
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int r = 0; r < R; ++r) acc[r][m] = dot16(wv[u][r], xv[m], acc[r][m]);
+    }
+  }
+  // the last K % 16 columns, one a lane
+  if (whole + lane < a.K) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int v = __ldg(w[r] + whole + lane);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) acc[r][m] += v * __ldg(x[m] + whole + lane);
+    }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int m = 0; m < MT; ++m) acc[r][m] = __reduce_add_sync(kFull, acc[r][m]);
+  by_kind(a.lin, PutCall<MT, R>{a, n0, acc});
+}
+
 // 2-D map of an int8 matrix {K, rows} with the given pitch, box {128, box_rows},
 // 128-byte swizzle; elements past the matrix read as zero.
 cudaError_t encode_int8(CUtensorMap* map, const int8_t* base, int64_t K, int64_t rows, int64_t ld,
@@ -520,10 +636,32 @@ cudaError_t run_linear(const Operands& op, LinArgs args, int sms, int split, cud
   return cudaLaunchKernelEx(&cfg, fn, maps, args);
 }
 
+template <int MT, int R>
+cudaError_t run_few(const Operands& op, const LinArgs& args, cudaStream_t stream) {
+  const VecArgs a = {args, op.x, op.w, op.ldx, op.ldw, static_cast<int>(op.K)};
+  constexpr int kChannels = kVecThreads / 32 * R;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((args.N + kChannels - 1) / kChannels);
+  cfg.blockDim = dim3(kVecThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, &linear_few_kernel<MT, R>, a);
+}
+
 // The widest token tile whose tiles still cover every SM; with fewer tokens
 // than that, a tile about as wide as they are, shared by a cluster along K if
 // its tiles leave SMs idle.
 cudaError_t launch_linear(const Operands& op, const LinArgs& args, int sms, cudaStream_t s) {
+  if (args.M <= kFewTokens) {
+    const bool two = op.K <= 2048;  // channels a warp
+    if (args.M == 1) return two ? run_few<1, 2>(op, args, s) : run_few<1, 1>(op, args, s);
+    if (args.M == 2) return two ? run_few<2, 2>(op, args, s) : run_few<2, 1>(op, args, s);
+    return two ? run_few<4, 2>(op, args, s) : run_few<4, 1>(op, args, s);
+  }
   const int64_t tn = (args.N + kBM - 1) / kBM;
   auto tiles = [&](int bn) { return (static_cast<int64_t>(args.M) + bn - 1) / bn * tn; };
   if (args.M > 128 && tiles(256) >= sms) {
