@@ -98,9 +98,12 @@ __device__ __forceinline__ void tc_mma_s8(uint32_t d_tmem, uint64_t adesc, uint6
         : "memory");
 }
 
-__device__ __forceinline__ uint32_t load_cluster_u32(uint32_t cluster_addr) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr) : "memory");
+__device__ __forceinline__ uint4 load_cluster_v4(uint32_t cluster_addr) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
   return v;
 }
 
@@ -117,23 +120,30 @@ struct Channel {
   bool live;
 };
 
+// One output from its int32 sum, the same in every form of the layer: two
+// roundings, the sum's own and a product's, then one fused with the bias.
 template <int ACT, class Out>
-__device__ __forceinline__ void put(const LinArgs& a, const Channel& ch, int n, int m, int sum,
-                                    float xs) {
-  const float v =
-      activate<ACT>(__fadd_rn(__fmul_rn(__fmul_rn(static_cast<float>(sum), xs), ch.ws), ch.b));
-  Out* p = static_cast<Out*>(a.y) + static_cast<int64_t>(m) * a.ldy + n;
+__device__ __forceinline__ void put_at(Out* p, const Channel& ch, int sum, float xs) {
+  const float v = activate<ACT>(__fmaf_rn(__fmul_rn(static_cast<float>(sum), xs), ch.ws, ch.b));
   if constexpr (sizeof(Out) == 4)
     *p = v;
   else
     *p = __float2bfloat16_rn(v);
 }
 
+template <int ACT, class Out>
+__device__ __forceinline__ void put(const LinArgs& a, const Channel& ch, int n, int m, int sum,
+                                    float xs) {
+  put_at<ACT>(static_cast<Out*>(a.y) + static_cast<int64_t>(m) * a.ldy + n, ch, sum, xs);
+}
+
 // One warp's share of a finished accumulator: 32 channels (its TMEM lanes),
-// tokens m0 + c for the columns c of [c0, c1).
+// tokens m0 + c for the columns c of [c0, c1). The address walks from token to
+// token: a 64-bit product for each made it 19 instructions an element.
 template <int ACT, class Out>
 __device__ __forceinline__ void drain(const LinArgs& a, const Channel& ch, int n, int m0,
                                       const float* xs, uint32_t tmem, int c0, int c1) {
+  Out* p = static_cast<Out*>(a.y) + static_cast<int64_t>(m0 + c0) * a.ldy + n;
   for (int c = c0; c < c1 && m0 + c < a.M; c += 32) {
     float v[32];
     tmem_ld_32x32b_x32(tmem + c, v);
@@ -145,15 +155,21 @@ __device__ __forceinline__ void drain(const LinArgs& a, const Channel& ch, int n
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float4 f = s[i];
-        put<ACT, Out>(a, ch, n, m0 + c + 4 * i, __float_as_int(v[4 * i]), f.x);
-        put<ACT, Out>(a, ch, n, m0 + c + 4 * i + 1, __float_as_int(v[4 * i + 1]), f.y);
-        put<ACT, Out>(a, ch, n, m0 + c + 4 * i + 2, __float_as_int(v[4 * i + 2]), f.z);
-        put<ACT, Out>(a, ch, n, m0 + c + 4 * i + 3, __float_as_int(v[4 * i + 3]), f.w);
+        put_at<ACT>(p, ch, __float_as_int(v[4 * i]), f.x);
+        p += a.ldy;
+        put_at<ACT>(p, ch, __float_as_int(v[4 * i + 1]), f.y);
+        p += a.ldy;
+        put_at<ACT>(p, ch, __float_as_int(v[4 * i + 2]), f.z);
+        p += a.ldy;
+        put_at<ACT>(p, ch, __float_as_int(v[4 * i + 3]), f.w);
+        p += a.ldy;
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (i < left) put<ACT, Out>(a, ch, n, m0 + c + i, __float_as_int(v[i]), xs[c - c0 + i]);
+      for (int i = 0; i < 32; ++i) {
+        if (i < left) put_at<ACT>(p, ch, __float_as_int(v[i]), xs[c - c0 + i]);
+        p += a.ldy;
+      }
     }
     __syncwarp();  // the next load takes the whole warp
   }
@@ -193,25 +209,53 @@ struct DrainCall {
 };
 
 // The cluster's parts of a tile, kept as [column][channel] int32 at the start
-// of each CTA's ring, summed over its S CTAs for columns [c0, c1).
+// of each CTA's ring, summed over its S CTAs for columns [c0, c1): a column's
+// 128 channels a warp, four a lane, the loads of eight parts in flight. (One
+// 4-byte load after another, an earlier form, took 5 us of a 10 us layer.)
+template <int S>
 struct JoinCall {
   const LinArgs& a;
-  int n0, m0, S, c0, c1, ew, lane;
+  int n0, m0, c0, c1, ew, lane;
   uint32_t smem;
   template <int ACT, class Out>
   __device__ __forceinline__ void run() const {
-    // (column, 32 channels) a warp and step
-    for (int t = ew; t < (c1 - c0) * 4; t += kEpiWarps) {
-      const int c = c0 + t / 4, r = (t & 3) * 32 + lane;
-      const int m = m0 + c, n = n0 + r;
-      if (m >= a.M || n >= a.N) continue;
-      int sum = 0;
-      for (int k = 0; k < S; ++k)
-        sum += static_cast<int>(load_cluster_u32(map_to_cta(smem + (c * kBM + r) * 4, k)));
-      Channel ch;
-      ch.ws = __ldg(a.w_scale + n);
-      ch.b = a.bias != nullptr ? __ldg(a.bias + n) : 0.f;
-      put<ACT, Out>(a, ch, n, m, sum, __ldg(a.x_scale + m));
+    constexpr int kCols = 8 / S;  // columns at a time
+    const int n = n0 + lane * 4;
+    Channel ch[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      ch[e] = {0.f, 0.f, n + e < a.N};
+      if (ch[e].live) {
+        ch[e].ws = __ldg(a.w_scale + n + e);
+        ch[e].b = a.bias != nullptr ? __ldg(a.bias + n + e) : 0.f;
+      }
+    }
+    for (int cb = c0 + ew * kCols; cb < c1; cb += kEpiWarps * kCols) {
+      uint4 v[kCols][S];
+      float xs[kCols];
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) {
+        const bool live = cb + i < c1 && m0 + cb + i < a.M;
+        xs[i] = live ? __ldg(a.x_scale + m0 + cb + i) : 0.f;
+#pragma unroll
+        for (int k = 0; k < S; ++k) {
+          v[i][k] = make_uint4(0, 0, 0, 0);
+          if (live) v[i][k] = load_cluster_v4(map_to_cta(smem + ((cb + i) * kBM + lane * 4) * 4, k));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kCols; ++i) {
+        if (cb + i >= c1 || m0 + cb + i >= a.M) break;
+        uint4 t = v[i][0];
+#pragma unroll
+        for (int k = 1; k < S; ++k)
+          t.x += v[i][k].x, t.y += v[i][k].y, t.z += v[i][k].z, t.w += v[i][k].w;
+        const uint32_t sums[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (ch[e].live)
+            put<ACT, Out>(a, ch[e], n + e, m0 + cb + i, static_cast<int>(sums[e]), xs[i]);
+      }
     }
   }
 };
@@ -227,10 +271,11 @@ __device__ __forceinline__ void tile_at(const LinArgs& a, int t, int& tm, int& t
   tn = in / height;
 }
 
-// SPLIT: the cluster's CTAs share one tile (and there is one tile per cluster).
-template <int BN, bool PAIR, bool SPLIT>
+// S > 1: the S CTAs of a cluster share one tile (and there is one tile a cluster).
+template <int BN, bool PAIR, int S>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_int8_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinArgs args) {
+  constexpr bool SPLIT = S > 1;
   static_assert(!(PAIR && SPLIT), "a pair shares a tile's channels, not its K");
   using R = Ring<BN, PAIR>;
   constexpr int CG = PAIR ? 2 : 1;
@@ -248,7 +293,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tslot = reinterpret_cast<uint32_t*>(mma_done + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = (PAIR || SPLIT) ? cluster_ctarank() : 0u;
-  const int S = SPLIT ? static_cast<int>(gridDim.x / cluster_count_x()) : 1;
   const int unit0 = (PAIR || SPLIT) ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
   const int unit_step =
       (PAIR || SPLIT) ? static_cast<int>(cluster_count_x()) : static_cast<int>(gridDim.x);
@@ -422,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int tm, tn;
       tile_at(args, unit0, tm, tn);
       const int c0 = BN * static_cast<int>(rank) / S, c1 = BN * static_cast<int>(rank + 1) / S;
-      by_kind(args, JoinCall{args, tn * kBM, tm * BN, S, c0, c1, warp - 2, lane, smem_u32(smem)});
+      by_kind(args, JoinCall<S>{args, tn * kBM, tm * BN, c0, c1, warp - 2, lane, smem_u32(smem)});
     }
   }
   tc_fence_before_sync();
@@ -573,10 +617,10 @@ struct Operands {
   int64_t ldx, ldw, K;
 };
 
-// split: CTAs of a tile's cluster (SPLIT), else 1.
-template <int BN, bool PAIR, bool SPLIT>
-cudaError_t run_linear(const Operands& op, LinArgs args, int sms, int split, cudaStream_t stream) {
-  auto* fn = &linear_int8_kernel<BN, PAIR, SPLIT>;
+template <int BN, bool PAIR, int S>
+cudaError_t run_linear(const Operands& op, LinArgs args, int sms, cudaStream_t stream) {
+  constexpr bool SPLIT = S > 1;
+  auto* fn = &linear_int8_kernel<BN, PAIR, S>;
   constexpr int smem = Ring<BN, PAIR>::kTotal;
   constexpr int kUnitN = (PAIR ? 2 : 1) * kBM;
   LinMaps maps;
@@ -615,7 +659,7 @@ cudaError_t run_linear(const Operands& op, LinArgs args, int sms, int split, cud
   int fit = cached > 0 ? cached - 1 : 0;
   if constexpr (PAIR || SPLIT) {
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = PAIR ? 2 : split;
+    attr[1].val.clusterDim.x = PAIR ? 2 : S;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
@@ -630,7 +674,7 @@ cudaError_t run_linear(const Operands& op, LinArgs args, int sms, int split, cud
     if (fit > 0) pairs = std::min(pairs, fit);
     grid = 2 * std::min<int64_t>(tiles, pairs);
   }
-  if constexpr (SPLIT) grid = tiles * split;
+  if constexpr (SPLIT) grid = tiles * S;
   if (cacheable && cached == 0) prepared[dev].store(fit + 1, std::memory_order_release);
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   return cudaLaunchKernelEx(&cfg, fn, maps, args);
@@ -652,9 +696,34 @@ cudaError_t run_few(const Operands& op, const LinArgs& args, cudaStream_t stream
   return cudaLaunchKernelEx(&cfg, &linear_few_kernel<MT, R>, a);
 }
 
-// The widest token tile whose tiles still cover every SM; with fewer tokens
-// than that, a tile about as wide as they are, shared by a cluster along K if
-// its tiles leave SMs idle.
+// The forms of the tensor-core kernel, with what they take on a B200 in us: a K
+// block of 128 bytes of a tile (`step`; a narrow tile's is bound by the latency
+// of its loads) and the draining of an accumulator (`drain`, which the next
+// tile's products overlap). Fitted to 15 forms at 18 shapes: the choice by them
+// was the fastest or within 4 % of it at all of these.
+struct Form {
+  int bn;
+  bool pair;
+  int split;
+  double step, drain;
+  cudaError_t (*run)(const Operands&, LinArgs, int, cudaStream_t);
+};
+const Form kForms[] = {
+    {32, false, 1, 0.30, 0.1, run_linear<32, false, 1>},
+    {32, false, 2, 0.30, 0.1, run_linear<32, false, 2>},
+    {32, false, 4, 0.30, 0.1, run_linear<32, false, 4>},
+    {64, false, 1, 0.31, 0.4, run_linear<64, false, 1>},
+    {64, false, 2, 0.31, 0.4, run_linear<64, false, 2>},
+    {64, false, 4, 0.31, 0.4, run_linear<64, false, 4>},
+    {128, false, 1, 0.33, 1.5, run_linear<128, false, 1>},
+    {128, false, 2, 0.33, 1.5, run_linear<128, false, 2>},
+    {128, false, 4, 0.33, 1.5, run_linear<128, false, 4>},
+    {256, false, 1, 0.42, 3.7, run_linear<256, false, 1>},
+    {256, true, 1, 0.42, 3.1, run_linear<256, true, 1>},
+};
+
+// Few tokens take the kernel for them; the others the form that takes the least
+// time by the figures above.
 cudaError_t launch_linear(const Operands& op, const LinArgs& args, int sms, cudaStream_t s) {
   if (args.M <= kFewTokens) {
     const bool two = op.K <= 2048;  // channels a warp
@@ -662,23 +731,25 @@ cudaError_t launch_linear(const Operands& op, const LinArgs& args, int sms, cuda
     if (args.M == 2) return two ? run_few<2, 2>(op, args, s) : run_few<2, 1>(op, args, s);
     return two ? run_few<4, 2>(op, args, s) : run_few<4, 1>(op, args, s);
   }
-  const int64_t tn = (args.N + kBM - 1) / kBM;
-  auto tiles = [&](int bn) { return (static_cast<int64_t>(args.M) + bn - 1) / bn * tn; };
-  if (args.M > 128 && tiles(256) >= sms) {
-    const int64_t pairs = (static_cast<int64_t>(args.M) + 255) / 256 *
-                          ((static_cast<int64_t>(args.N) + 255) / 256);
-    if (pairs >= sms / 2) return run_linear<256, true, false>(op, args, sms, 1, s);
-    return run_linear<256, false, false>(op, args, sms, 1, s);
+  Form best = {};
+  double least = 0;
+  for (const Form& f : kForms) {
+    const int64_t channels = f.pair ? 2 * kBM : kBM;
+    const int64_t tiles = (static_cast<int64_t>(args.M) + f.bn - 1) / f.bn *
+                          ((static_cast<int64_t>(args.N) + channels - 1) / channels);
+    // a cluster's CTAs run at the same time, and each has two K blocks at least
+    if (f.split > 1 && (tiles * f.split > 128 || args.nkb < 2 * f.split)) continue;
+    const int64_t units = f.pair ? sms / 2 : sms;
+    const int64_t rounds = (tiles + units - 1) / units;
+    const double main = static_cast<double>(args.nkb) / f.split * f.step;
+    const double us = rounds * std::max(main, f.drain) + std::min(main, f.drain) +
+                      (f.split > 1 ? 1.7 : 0.0);
+    if (best.run == nullptr || us < least) {
+      best = f;
+      least = us;
+    }
   }
-  if (args.M > 64 && tiles(128) >= sms) return run_linear<128, false, false>(op, args, sms, 1, s);
-  const int bn = args.M <= 32 ? 32 : 64;
-  int split = 1;
-  while (split < 8 && tiles(bn) * split * 2 <= sms && args.nkb >= split * 4) split *= 2;
-  if (split > 1)
-    return bn == 32 ? run_linear<32, false, true>(op, args, sms, split, s)
-                    : run_linear<64, false, true>(op, args, sms, split, s);
-  return bn == 32 ? run_linear<32, false, false>(op, args, sms, 1, s)
-                  : run_linear<64, false, false>(op, args, sms, 1, s);
+  return best.run(op, args, sms, s);
 }
 
 }  // namespace
