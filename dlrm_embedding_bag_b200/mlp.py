@@ -7,12 +7,15 @@ library's tcgen05 kernel. bf16 tensors are ``torch.bfloat16``
 views whose row pitch is a multiple of 8 elements (16 bytes), as the layer's
 TMA loads require; :func:`bf16_empty` makes such buffers.
 
-Two arithmetics are offered (``mode``). ``"f32"`` (the default) is the pages' own: f32
+Three arithmetics are offered (``mode``). ``"f32"`` (the default) is the pages' own: f32
 activations times bf16 (or f32) weights with f32 results, through
 ``dlrm_linear_f32a``; each f32 activation travels between layers as three
 bf16 planes that sum to it exactly (:func:`planes_empty`,
 :func:`split_bf16x3`). ``"bf16"`` rounds activations to bf16 (one plane,
-``dlrm_linear_bf16``), a third of the tensor work.
+``dlrm_linear_bf16``), a third of the tensor work. ``"int8"`` rounds the rows of
+activations to 8-bit integers in front of every layer, with one scale for each
+row and for each output channel of the weights (:mod:`.int8`), half of the
+bytes of ``"bf16"`` at twice its tensor rate.
 
 A DLRMv1 forward (:func:`dlrm_forward`) is: bottom MLP on the dense features
 -> ``dense`` (B, D); the sparse stage (pooled embeddings and the interaction
@@ -202,20 +205,62 @@ class MLP:
     ``(N,)`` f32, ``act`` one of ``"none" | "relu" | "sigmoid"``. In ``"bf16"``
     mode activations between layers are bf16; in ``"f32"`` mode they are f32,
     carried as three exact bf16 planes, and the input is given as planes.
+
+    In ``"int8"`` mode ``w`` is a pair ``(w_q, w_scale)`` (:func:`int8_layers` makes
+    them from weights) and the input an f32 or bf16 matrix. The rows in front of
+    each layer are rounded to 8 bits (:func:`.int8.quantize_rows`) or, where
+    ``norms[i]`` is given (f32 ``(K,)``), normed and rounded
+    (:func:`.int8.rms_norm_int8`). Layers with a norm that follow each other at
+    one width form a residual stack: the norm in front of layer i reads the sum
+    of the sum before it and layer i-1's output. Activations between layers are
+    bf16: what an 8-bit level (2^-8 of its row's maximum) is rounded from need
+    not be finer.
     """
 
     def __init__(self, layers: Sequence[Tuple[torch.Tensor, torch.Tensor, str]],
-                 mode: str = "f32"):
+                 mode: str = "f32", *,
+                 norms: Optional[Sequence[Optional[torch.Tensor]]] = None, eps: float = 1e-6):
         if not layers:
             raise ValueError("an MLP needs at least one layer")
-        if mode not in ("bf16", "f32"):
-            raise ValueError("mode must be 'bf16' or 'f32'")
+        if mode not in ("bf16", "f32", "int8"):
+            raise ValueError("mode must be 'bf16', 'f32' or 'int8'")
+        if norms is not None and mode != "int8":
+            raise ValueError("norms need mode 'int8'")
+        if norms is not None and len(norms) != len(layers):
+            raise ValueError(f"norms must have {len(layers)} entries")
+        if mode == "int8" and any(isinstance(w, torch.Tensor) for w, _, _ in layers):
+            raise ValueError("an int8 layer's weights are (w_q, w_scale): see int8_layers")
         self.layers: List[Tuple[torch.Tensor, torch.Tensor, str]] = list(layers)
         self.mode = mode
+        self.norms = list(norms) if norms is not None else [None] * len(self.layers)
+        self.eps = eps
 
     @property
     def out_features(self) -> int:
-        return self.layers[-1][0].shape[0]
+        w = self.layers[-1][0]
+        return (w[0] if self.mode == "int8" else w).shape[0]
+
+    def _forward_int8(self, x, last_f32: bool, last_bf16: bool, keep: bool):
+        from . import int8
+
+        inputs = []
+        h, total = x, None  # total: the residual stack's running sum
+        n = len(self.layers)
+        for i, ((w_q, w_scale), b, act) in enumerate(self.layers):
+            if self.norms[i] is None:
+                q, s = int8.quantize_rows(h)
+                total = None
+            elif total is not None and total.shape == h.shape and total.dtype == h.dtype:
+                q, s, total = int8.rms_norm_int8(h, self.norms[i], residual=total, eps=self.eps)
+            else:
+                q, s, _ = int8.rms_norm_int8(h, self.norms[i], eps=self.eps)
+                total = h
+            inputs.append((q, s))
+            dtype = torch.float32 if i == n - 1 and last_f32 else torch.bfloat16
+            h = int8.linear_int8(q, s, w_q, w_scale, b, act, out_dtype=dtype)
+        y32 = h if last_f32 else None
+        y_n = None if not last_bf16 else to_bf16(h) if last_f32 else h
+        return ((y32, y_n), inputs) if keep else (y32, y_n)
 
     def forward(self, x: torch.Tensor, *, a_hi: Optional[torch.Tensor] = None,
                 last_f32: bool = True, last_bf16: bool = False, keep: bool = False):
@@ -224,8 +269,14 @@ class MLP:
 
         Returns ``(y_f32, y_next)`` of the last layer -- ``y_next`` is its bf16
         output (``"bf16"``) or its planes (``"f32"``) when ``last_bf16`` is set
-        -- plus the list of every layer's inputs when ``keep`` is set.
+        -- plus the list of every layer's inputs when ``keep`` is set. In
+        ``"int8"`` mode ``x`` is an f32 or bf16 matrix, ``a_hi`` is not taken,
+        ``y_next`` is bf16 and a layer's input is its ``(q, scale)``.
         """
+        if self.mode == "int8":
+            if a_hi is not None:
+                raise ValueError("int8 layers take one input: a row has one scale")
+            return self._forward_int8(x, last_f32, last_bf16, keep)
         inputs = []
         h, hi = x, a_hi
         n = len(self.layers)
@@ -242,6 +293,14 @@ class MLP:
         return ((y32, y_n), inputs) if keep else (y32, y_n)
 
 
+def int8_layers(layers: Sequence[Tuple[torch.Tensor, torch.Tensor, str]]):
+    """Layers ``(w, bias, act)`` with f32 or bf16 weights ``(N, K)`` as ``"int8"`` layers:
+    the weights rounded to 8 bits with one scale for each output channel."""
+    from . import int8
+
+    return [(int8.quantize_rows(w), b, act) for w, b, act in layers]
+
+
 def dlrm_forward(bottom: MLP, top: MLP, dense_x: torch.Tensor, weights: Sequence[torch.Tensor],
                  indices: torch.Tensor, offsets: torch.Tensor, L: int, *, keep: bool = False):
     """DLRMv1 forward: CTR ``(B, 1)`` f32 from the dense features and the tables.
@@ -251,11 +310,20 @@ def dlrm_forward(bottom: MLP, top: MLP, dense_x: torch.Tensor, weights: Sequence
     bf16; top MLP with ``[dense | z]`` as its split first-layer input.
     ``"f32"`` MLPs: ``dense_x`` is f32 and every activation stays f32: the
     bottom MLP's output goes to the interaction as f32 and to the top MLP as
-    its exact planes, and z is split into planes. With ``keep`` it also
-    returns a dict of the intermediate tensors.
+    its exact planes, and z is split into planes. ``"int8"`` MLPs: ``dense_x`` is
+    f32 or bf16, and the sparse stage writes the rows ``[dense | z]`` that the top
+    MLP rounds to 8 bits. With ``keep`` it also returns a dict of the
+    intermediate tensors.
     """
     if bottom.mode != top.mode:
         raise ValueError("the bottom and top MLPs must use the same mode")
+    if bottom.mode == "int8":
+        dense32, _ = bottom.forward(dense_x)
+        pooled, z = ops.sparse_interact(weights, indices, offsets, dense32, L, concat_dense=True)
+        (ctr, _), top_inputs = top.forward(z, keep=True)
+        if keep:
+            return ctr, dict(dense32=dense32, pooled=pooled, z=z, top_inputs=top_inputs)
+        return ctr
     if bottom.mode == "f32":
         x_in = split_bf16x3(dense_x)
         dense32, dense_next = bottom.forward(x_in, last_f32=True, last_bf16=True)

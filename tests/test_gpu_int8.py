@@ -303,6 +303,153 @@ def test_streams_and_graphs(int8):
         _check_layer(y, q, s, wq, ws, None, "none")
 
 
+# ------------------------------------------------------------------ whole networks
+
+
+def _weights(g, widths):
+    out = []
+    for k, n in zip(widths, widths[1:]):
+        w = torch.empty((n, k), device=DEV).normal_(0, k ** -0.5, generator=g)
+        out.append((w, torch.empty(n, device=DEV).normal_(0, 0.1, generator=g), "relu"))
+    return out
+
+
+@pytest.mark.parametrize("M", [1, 3, 70, 500])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_mlp_of_int8_layers(int8, M, dt):
+    """Every layer of a network against 64 bits on the inputs that the kernels gave it:
+    plain rounding, a norm, and a residual stack of three normed layers."""
+    from dlrm_embedding_bag_b200 import mlp
+
+    g = _gen(M)
+    widths = [200, 96, 96, 96, 96, 33]
+    layers = mlp.int8_layers(_weights(g, widths))
+    norms = [None] + [torch.empty(96, device=DEV).normal_(1, 0.2, generator=g) for _ in range(4)]
+    net = mlp.MLP(layers, mode="int8", norms=norms, eps=1e-5)
+    assert net.out_features == 33
+    x = _normal(g, M, 200, DT[dt])
+    (y32, y16), inputs = net.forward(x, last_bf16=True, keep=True)
+    h, total = x, None
+    for i, (((wq, ws), b, act), (q, s)) in enumerate(zip(layers, inputs)):
+        rows = h.double()
+        if norms[i] is not None:
+            if total is not None:
+                rows = rows + total.double()
+                total = rows.float().to(BF16)  # the running sum, rounded once
+            else:
+                total = h
+            rows = rows / torch.sqrt(rows.square().mean(1, keepdim=True)
+                                     + np.float64(np.float32(1e-5))) * norms[i].double()
+        _check_rows(q, s, rows, rows.shape[1], f"layer {i}")
+        last = i == len(layers) - 1
+        h = y32 if last else int8.linear_int8(q, s, wq, ws, b, act, out_dtype=BF16)
+        _check_layer(h, q, s, wq, ws, b, act)
+    assert y32.shape == (M, 33) and torch.equal(y16.float(), y32.to(BF16).float())
+    y, none = net.forward(x)
+    assert none is None and torch.equal(y, y32)
+    none, yb = net.forward(x, last_f32=False, last_bf16=True)
+    assert none is None and yb.dtype == BF16 and torch.equal(yb.float(), y32.to(BF16).float())
+
+
+def test_dlrm_forward_in_int8(int8):
+    """The whole forward on 8-bit layers: each stage against 64 bits on its own
+    inputs, and the captured graph against the eager call."""
+    from dlrm_embedding_bag_b200 import mlp, ops
+
+    g = _gen(77)
+    B, F, N, D, L = 300, 5, 400, 32, 4
+    P = (F + 1) * F // 2
+    bottom = mlp.MLP(mlp.int8_layers(_weights(g, [13, 64, D])), mode="int8")
+    tops = _weights(g, [D + P, 48, 1])
+    tops[-1] = (*tops[-1][:2], "sigmoid")
+    top = mlp.MLP(mlp.int8_layers(tops), mode="int8")
+    tables = [torch.empty((N, D), device=DEV).normal_(0, 0.3, generator=g) for _ in range(F)]
+    idx = torch.randint(0, N, (F, B * L), device=DEV, generator=g).to(torch.int32)
+    off = (torch.arange(B, device=DEV, dtype=torch.int32) * L).repeat(F, 1).contiguous()
+    x = _normal(g, B, 13).abs()
+    ctr, t = mlp.dlrm_forward(bottom, top, x, tables, idx, off, L, keep=True)
+    assert ctr.shape == (B, 1) and ((ctr > 0) & (ctr < 1)).all()
+    assert torch.equal(t["z"][:, :D], t["dense32"])
+    dense, pooled = t["dense32"].double(), t["pooled"].double()
+    v = torch.cat([dense[:, None], pooled], 1)
+    i, j = torch.tril_indices(F + 1, F + 1, -1, device=DEV)
+    dots = (v[:, i] * v[:, j]).sum(2)
+    bound = (v[:, i] * v[:, j]).abs().sum(2)
+    assert ((t["z"][:, D:].double() - dots).abs() <= 1e-5 * bound + 1e-30).all()
+    q, s = t["top_inputs"][0]
+    _check_rows(q, s, t["z"].double(), D + P)
+    q, s = t["top_inputs"][1]
+    (wq, ws), b, act = top.layers[1]
+    _check_layer(ctr, q, s, wq, ws, b, act)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        again = mlp.dlrm_forward(bottom, top, x, tables, idx, off, L)
+    x.mul_(0.5)
+    idx.copy_((idx + 7) % N)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(again, mlp.dlrm_forward(bottom, top, x, tables, idx, off, L))
+    assert not torch.equal(again, ctr)
+    with pytest.raises(ValueError, match="same mode"):
+        mlp.dlrm_forward(bottom, mlp.MLP([(tables[0].to(BF16), None, "none")], mode="bf16"), x,
+                         tables, idx, off, L)
+    assert ops.launch_count() > 0
+
+
+def test_mlp_refusals(int8):
+    from dlrm_embedding_bag_b200 import mlp
+
+    w = torch.zeros((8, 16), device=DEV)
+    layers = [(w, None, "none")]
+    with pytest.raises(ValueError, match="w_q, w_scale"):
+        mlp.MLP(layers, mode="int8")
+    with pytest.raises(ValueError, match="mode must be"):
+        mlp.MLP(layers, mode="int4")
+    with pytest.raises(ValueError, match="norms need"):
+        mlp.MLP(layers, norms=[None])
+    with pytest.raises(ValueError, match="1 entries"):
+        mlp.MLP(mlp.int8_layers(layers), mode="int8", norms=[None, None])
+    net = mlp.MLP(mlp.int8_layers(layers), mode="int8")
+    with pytest.raises(ValueError, match="one input"):
+        net.forward(torch.zeros((4, 8), device=DEV), a_hi=torch.zeros((4, 8), device=DEV))
+
+
+def test_lookup_norm_layer_and_gradient_together(int8):
+    """A step over token histories: rows looked up with a scale, normed into 8
+    bits, multiplied; and the table's gradient from the rows' own gradients, each
+    against 64 bits on the inputs that it was given."""
+    from dlrm_embedding_bag_b200 import tokens
+
+    g = _gen(5)
+    N, D, out = 500, 256, 64
+    table = _normal(g, N, D, BF16, std=0.1)
+    ids = torch.randint(0, N, (20, 30), device=DEV, generator=g).to(torch.int32)
+    ids[:, 25:] = 0  # padding
+    wq, ws = int8.quantize_rows(_normal(g, out, D, std=D ** -0.5))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        rows = tokens.embedding_lookup(table, ids, scale=16.0, padding_idx=0).view(-1, D)
+        q, s, h = int8.rms_norm_int8(rows, residual=rows)
+        y = int8.linear_int8(q, s, wq, ws)
+        grad = tokens.embedding_grad(rows, ids, N, scale=16.0, padding_idx=0)
+    side.synchronize()
+    want = table[ids.view(-1).long()].float() * 16.0
+    want[ids.view(-1) == 0] = 0
+    assert torch.equal(rows, want.to(BF16))
+    hd = 2 * rows.double()
+    _check_rows(q, s, hd / torch.sqrt(hd.square().mean(1, keepdim=True) + 1e-6), D)
+    assert torch.equal(h, rows * 2) and (q[ids.view(-1) == 0] == 0).all()
+    _check_layer(y, q, s, wq, ws, None, "none")
+    ref = torch.zeros((N, D), dtype=torch.float64, device=DEV)
+    mag = torch.zeros_like(ref)
+    ref.index_add_(0, ids.view(-1).long(), rows.double() * 16)
+    mag.index_add_(0, ids.view(-1).long(), rows.double().abs() * 16)
+    ref[0] = mag[0] = 0
+    tol = 60 * U * mag + 2.0 ** -8 * ref.abs() * (1 + 2.0 ** -8)
+    assert ((grad.double() - ref).abs() <= tol).all()
+
+
 def test_refusals(int8):
     from dlrm_embedding_bag_b200.tokens import TokensError
 
