@@ -831,7 +831,8 @@ __device__ __forceinline__ void sum_block(const SumArgs& a, SumSmem<VEC, G>& sm,
 template <class In, int VEC, int G>
 __global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
   __shared__ SumSmem<VEC, G> sm;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // only the join may be scheduled early: it waits before it reads anything
+  if (a.nblocks > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the sort (and the zeros) are done
   const int block = blockIdx.x / a.windows;
   const int64_t lo = static_cast<int64_t>(block) * a.per_block;

@@ -323,10 +323,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tslot;
-  // The kernel after this one may be scheduled; it waits for this grid's
-  // results before it reads them. Likewise here: everything below may come
-  // from the kernel before (the levels, the scales), so every role waits.
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // Everything below may come from the kernel before (the levels, the scales),
+  // so every role waits for its end. This grid lets none start before its own
+  // end: the bf16 layers read their bias without waiting.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   bool timed_out = false;
 
@@ -542,8 +541,7 @@ struct PutCall {
 template <int MT, int R>
 __global__ void __launch_bounds__(kVecThreads) linear_few_kernel(const VecArgs a) {
   static_assert(MT * R <= 32, "a lane for each output");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // as in the kernel above
   const int lane = threadIdx.x & 31;
   const int n0 = (blockIdx.x * (kVecThreads / 32) + (threadIdx.x >> 5)) * R;
   if (n0 >= a.lin.N) return;

@@ -7,6 +7,10 @@ plus half a step of the output's type, eps / 2.
 """
 from __future__ import annotations
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -292,7 +296,7 @@ def test_grad_of_sum_pooled_bags(tokens, B, L, N, D, F):
     assert abs(total - float(change.sum())) <= tol
 
 
-@pytest.mark.parametrize("T", [50, 5000])
+@pytest.mark.parametrize("T", [50, 5000, 70000])
 def test_grad_streams_scratch_and_graphs(tokens, T):
     """On a stream of its own, with the caller's scratch, captured and replayed
     with new inputs, next to another captured call with its own scratch."""
@@ -327,6 +331,67 @@ def test_grad_streams_scratch_and_graphs(tokens, T):
     torch.cuda.synchronize()
     for grad, ids, out, _ in calls:
         _check_grad(out, grad, ids, N)
+
+
+@pytest.mark.parametrize("T", [300, 6000, 90000])
+def test_grads_at_the_same_time(tokens, T):
+    """Calls that overlap on four streams, each with the scratch that torch gives it."""
+    g = _gen(T)
+    N, D = 5000, 40
+    calls = []
+    for k in range(4):
+        grad, _ = _matrix(g, T, D, F32)
+        calls.append((grad, torch.from_numpy(_ids(k, T, N, "skew")).to(DEV), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(3):
+        for grad, ids, stream in calls:
+            with torch.cuda.stream(stream):
+                outs.append(tokens.embedding_grad(grad, ids, N))
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        grad, ids, _ = calls[i % 4]
+        _check_grad(out, grad, ids, N)
+        assert _same_bits(out, outs[i % 4])
+
+
+def test_first_calls_under_capture():
+    """In a new process every operator's first call may be a captured one: their
+    set-up makes no call that a capture forbids."""
+    code = """
+import torch
+from dlrm_embedding_bag_b200 import int8, tokens
+dev = "cuda"
+x = torch.randn(70000, 32, device=dev); ids = torch.randint(0, 900, (70000,), device=dev).int()
+w = torch.zeros(4096, 512, dtype=torch.int8, device=dev); ws = torch.ones(4096, device=dev)
+torch.cuda.synchronize()
+outs = []
+side = torch.cuda.Stream()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph, stream=side):
+    for T in (100, 3000, 12000, 20000, 40000, 66000):
+        outs.append(tokens.embedding_grad(x[:T], ids[:T], 900))
+        outs.append(tokens.embedding_lookup(x, ids[:T]))
+    for M in (1, 2, 4, 16, 64, 128, 600, 3000):
+        q, s, _ = int8.rms_norm_int8(x[:16 * M].view(M, 512))
+        outs.append(int8.linear_int8(q, s, w, ws, out_dtype=torch.bfloat16))
+w.copy_(torch.randint(-9, 9, w.shape, device=dev).to(torch.int8))
+graph.replay()
+torch.cuda.synchronize()
+i = 0
+for T in (100, 3000, 12000, 20000, 40000, 66000):
+    assert torch.equal(outs[i], tokens.embedding_grad(x[:T], ids[:T], 900)), T
+    assert torch.equal(outs[i + 1], x[ids[:T].long()]), T
+    i += 2
+for M in (1, 2, 4, 16, 64, 128, 600, 3000):
+    q, s, _ = int8.rms_norm_int8(x[:16 * M].view(M, 512))
+    assert torch.equal(outs[i], int8.linear_int8(q, s, w, ws, out_dtype=torch.bfloat16)), M
+    i += 1
+print("ok")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stderr[-2000:]
 
 
 def test_grad_refusals(tokens):

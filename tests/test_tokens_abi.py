@@ -194,3 +194,35 @@ def test_python_checks(tokens):
         int8.linear_int8(cpu.to(torch.int8), cpu[0], cpu.to(torch.int8), cpu[0], act="gelu")
     q = int8.int8_empty(3, 17, "cpu")
     assert q.shape == (3, 17) and q.stride() == (32, 1)
+
+
+def test_calls_run_on_their_tensors_device(tokens, monkeypatch):
+    """A call on a device that is not current is made with that device current, on
+    its stream; a failed one raises with the library's status."""
+    seen, current = [], [0]
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.old, current[0] = current[0], self.index
+
+        def __exit__(self, *exc):
+            current[0] = self.old
+
+    monkeypatch.setattr(tokens, "_get_device", lambda: current[0])
+    monkeypatch.setattr(tokens, "_raw_stream", lambda index: 1000 + index)
+    monkeypatch.setattr(tokens.torch.cuda, "device", Device)
+
+    def entry(a, stream):
+        seen.append((a, stream, current[0]))
+        return -2 if a == 7 else 0
+
+    tokens._call(entry, "entry", 0, 5)
+    tokens._call(entry, "entry", 1, 6)
+    assert seen == [(5, 1000, 0), (6, 1001, 1)] and current == [0]
+    with pytest.raises(tokens.TokensError, match="entry: DLRM_ERR_SHAPE") as e:
+        tokens._call(entry, "entry", 1, 7)
+    assert e.value.status == -2 and current == [0]
+    assert isinstance(e.value, tokens.ops.DlrmError)
