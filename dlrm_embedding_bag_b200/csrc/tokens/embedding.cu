@@ -828,11 +828,12 @@ __device__ __forceinline__ void sum_block(const SumArgs& a, SumSmem<VEC, G>& sm,
   }
 }
 
-template <class In, int VEC, int G>
-__global__ void __launch_bounds__(kSumThreads) sum_kernel(const SumArgs a) {
+// JOIN: the join kernel follows, and may be scheduled early (it waits before it
+// reads anything; what else may follow is not known to).
+template <class In, int VEC, int G, bool JOIN>
+__global__ void __launch_bounds__(kSumThreads, 4) sum_kernel(const SumArgs a) {
   __shared__ SumSmem<VEC, G> sm;
-  // only the join may be scheduled early: it waits before it reads anything
-  if (a.nblocks > 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if constexpr (JOIN) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the sort (and the zeros) are done
   const int block = blockIdx.x / a.windows;
   const int64_t lo = static_cast<int64_t>(block) * a.per_block;
@@ -1032,8 +1033,9 @@ struct SumLaunch {
     a.nblocks = static_cast<int>((static_cast<int64_t>(a.T) + a.per_block - 1) / a.per_block);
     const int64_t blocks = static_cast<int64_t>(a.nblocks) * a.windows;
     if (blocks > INT_MAX) return cudaErrorInvalidValue;
-    cudaError_t e = launch_after(&sum_kernel<In, VEC, G>, dim3(static_cast<unsigned>(blocks)),
-                                 kSumThreads, 0, stream, a);
+    cudaError_t e = launch_after(
+        a.nblocks > 1 ? &sum_kernel<In, VEC, G, true> : &sum_kernel<In, VEC, G, false>,
+        dim3(static_cast<unsigned>(blocks)), kSumThreads, 0, stream, a);
     if (e != cudaSuccess) return e;
     ++n;
     if (a.nblocks > 1) {
