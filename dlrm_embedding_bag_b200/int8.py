@@ -17,8 +17,7 @@ import torch
 
 from . import ops
 from .mlp import ACTS
-from .tokens import (_call, _code, _empty, _empty_vector, _flat, _lib, _on, _pitch,
-                     _status)
+from .tokens import _call, _empty, _empty_vector, _flat, _lib, _matrix, _on, _pitch, _status
 
 MAX_K = 131071
 
@@ -34,10 +33,11 @@ def int8_empty(rows: int, cols: int, device="cuda") -> torch.Tensor:
     return t if cols % 16 == 0 else t[:, :cols]
 
 
-def _int8(t: torch.Tensor, name: str, index: int) -> Tuple[int, int, int]:
+def _int8(t: torch.Tensor, name: str, index: Optional[int]) -> Tuple[int, int, int]:
     """(rows, columns, row pitch) of an int8 matrix."""
-    _on(t, name, index)
-    if t.dtype != torch.int8:
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is torch.int8) or \
+            (index is not None and t.get_device() != index):
+        _on(t, name, index)
         raise TypeError(f"{name} must be torch.int8 (got {t.dtype})")
     return _pitch(t, name)
 
@@ -72,12 +72,10 @@ def quantize_rows(x: torch.Tensor, *, out: Optional[torch.Tensor] = None,
     """``(q, scale)`` of an f32 or bf16 ``(M, K)`` matrix: ``scale = max|row| / 127`` and
     ``q = row / scale`` rounded to nearest even. For weights ``(N, K)`` this is
     one scale for each output channel."""
-    index = _on(x, "x")
-    xd = _code(x, "x")
-    M, K, ldx = _pitch(x, "x")
+    index, xd, M, K, ldx = _matrix(x, "x")
     out, scale_out, ldq = _outputs(x, M, K, out, scale_out, index)
-    _call(_quantize, "dlrm_quantize_int8", index, x.data_ptr(), ldx, xd, M, K, out.data_ptr(),
-          ldq, scale_out.data_ptr())
+    _call(_quantize, "dlrm_quantize_int8", index,
+          (x.data_ptr(), ldx, xd, M, K, out.data_ptr(), ldq, scale_out.data_ptr()))
     return out, scale_out
 
 
@@ -93,9 +91,7 @@ def rms_norm_int8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
     ``x`` into ``residual_out`` (which may be ``residual`` itself) or a new tensor,
     and is None without a residual.
     """
-    index = _on(x, "x")
-    xd = _code(x, "x")
-    M, K, ldx = _pitch(x, "x")
+    index, xd, M, K, ldx = _matrix(x, "x")
     pr, ldr, ph, ldh = None, 0, None, 0
     if residual is not None:
         _on(residual, "residual", index)
@@ -115,8 +111,9 @@ def rms_norm_int8(x: torch.Tensor, weight: Optional[torch.Tensor] = None, *,
         raise ValueError("residual_out needs residual")
     pw = _scales(weight, "weight", K, index) if weight is not None else None
     out, scale_out, ldq = _outputs(x, M, K, out, scale_out, index)
-    _call(_norm, "dlrm_rms_norm_int8", index, x.data_ptr(), ldx, pr, ldr, xd, pw, M, K, eps, ph,
-          ldh, out.data_ptr(), ldq, scale_out.data_ptr())
+    _call(_norm, "dlrm_rms_norm_int8", index,
+          (x.data_ptr(), ldx, pr, ldr, xd, pw, M, K, eps, ph, ldh, out.data_ptr(), ldq,
+           scale_out.data_ptr()))
     return out, scale_out, residual_out
 
 
@@ -124,8 +121,8 @@ def dequantize_rows(q: torch.Tensor, scale: torch.Tensor, *,
                     dtype: torch.dtype = torch.float32,
                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The values of a matrix in 8 bits, ``q * scale[:, None]``, rounded once to ``dtype``."""
-    index = _on(q, "q")
-    M, K, ldq = _int8(q, "q", index)
+    M, K, ldq = _int8(q, "q", None)
+    index = q.get_device()
     ps = _scales(scale, "scale", M, index)
     if out is None:
         od, ldo = ops.TABLE_DTYPES.get(dtype), K
@@ -133,12 +130,11 @@ def dequantize_rows(q: torch.Tensor, scale: torch.Tensor, *,
             raise TypeError(f"dtype must be float32 or bfloat16 (got {dtype})")
         out = _empty(M, K, dtype, index)
     else:
-        _on(out, "out", index)
-        if out.shape != (M, K):
+        _, od, rows, cols, ldo = _matrix(out, "out", index)
+        if rows != M or cols != K:
             raise ValueError(f"out must be ({M}, {K}) (got {tuple(out.shape)})")
-        od, ldo = _code(out, "out"), _pitch(out, "out")[2]
-    _call(_dequantize, "dlrm_dequantize_int8", index, q.data_ptr(), ldq, ps, M, K,
-          out.data_ptr(), od, ldo)
+    _call(_dequantize, "dlrm_dequantize_int8", index,
+          (q.data_ptr(), ldq, ps, M, K, out.data_ptr(), od, ldo))
     return out
 
 
@@ -159,8 +155,8 @@ def linear_int8(x_q: torch.Tensor, x_scale: torch.Tensor, w_q: torch.Tensor,
     code = ACTS.get(act)
     if code is None:
         raise ValueError(f"act must be one of {sorted(ACTS)}")
-    index = _on(x_q, "x_q")
-    M, K, ldx = _int8(x_q, "x_q", index)
+    M, K, ldx = _int8(x_q, "x_q", None)
+    index = x_q.get_device()
     N, kw, ldw = _int8(w_q, "w_q", index)
     if kw != K:
         raise ValueError(f"w_q must be (N, {K})")
@@ -173,15 +169,15 @@ def linear_int8(x_q: torch.Tensor, x_scale: torch.Tensor, w_q: torch.Tensor,
             raise TypeError(f"out_dtype must be float32 or bfloat16 (got {out_dtype})")
         out = _empty(M, N, out_dtype, index)
     else:
-        _on(out, "out", index)
-        if out.shape != (M, N):
+        _, od, rows, cols, ldo = _matrix(out, "out", index)
+        if rows != M or cols != N:
             raise ValueError(f"out must be ({M}, {N}) (got {tuple(out.shape)})")
-        od, ldo = _code(out, "out"), _pitch(out, "out")[2]
     # a single row's pitch is not used to find another one: its own length will do
     if M == 1:
         ldx = (ldx + 15) // 16 * 16
     if N == 1:
         ldw = (ldw + 15) // 16 * 16
-    _call(_linear, "dlrm_linear_int8", index, x_q.data_ptr(), ldx, pxs, w_q.data_ptr(), ldw, pws,
-          pb, M, N, K, code, out.data_ptr(), od, ldo, _status(status, index))
+    _call(_linear, "dlrm_linear_int8", index,
+          (x_q.data_ptr(), ldx, pxs, w_q.data_ptr(), ldw, pws, pb, M, N, K, code, out.data_ptr(),
+           od, ldo, _status(status, index)))
     return out

@@ -103,7 +103,7 @@ def _empty_vector(n: int, dtype: torch.dtype, index: int) -> torch.Tensor:
     return torch.empty(n, dtype=dtype, device=torch.device("cuda", index))
 
 
-def _call(fn, name: str, index: int, *args) -> None:
+def _call(fn, name: str, index: int, args: tuple) -> None:
     """Call the C entry point ``fn`` on device ``index`` and its current stream."""
     if index == _get_device():
         rc = fn(*args, _raw_stream(index))
@@ -114,16 +114,17 @@ def _call(fn, name: str, index: int, *args) -> None:
         raise TokensError(rc, name)
 
 
-def _on(t: torch.Tensor, name: str, index: Optional[int] = None) -> int:
-    """The device index of a CUDA tensor, which has to be ``index`` if that is given."""
+# The checks below run in front of every call: each first asks whether all is well
+# and looks for what is not only then.
+
+def _on(t: torch.Tensor, name: str, index: Optional[int]) -> None:
+    """Raises unless ``t`` is a CUDA tensor (on device ``index`` if that is given)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    at = t.get_device()
-    if at < 0 or not t.is_cuda:
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device (got {t.device})")
-    if index is not None and at != index:
+    if index is not None and t.get_device() != index:
         raise ValueError(f"{name} must be on cuda:{index} (got {t.device})")
-    return at
 
 
 def _pitch(t: torch.Tensor, name: str) -> Tuple[int, int, int]:
@@ -132,6 +133,8 @@ def _pitch(t: torch.Tensor, name: str) -> Tuple[int, int, int]:
     if len(shape) != 2:
         raise ValueError(f"{name} must be 2-D with unit column stride")
     rows, cols = shape
+    if t.is_contiguous():
+        return rows, cols, cols
     pitch, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{name} must be 2-D with unit column stride")
@@ -143,21 +146,26 @@ def _pitch(t: torch.Tensor, name: str) -> Tuple[int, int, int]:
     return rows, cols, pitch
 
 
-def _code(t: torch.Tensor, name: str) -> int:
+def _matrix(t: torch.Tensor, name: str, index: Optional[int] = None):
+    """(device index, dtype code, rows, columns, row pitch) of an f32 or bf16 matrix."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda) or \
+            (index is not None and t.get_device() != index):
+        _on(t, name, index)
     code = ops.TABLE_DTYPES.get(t.dtype)
     if code is None:
         raise TypeError(f"{name} must be float32 or bfloat16 (got {t.dtype})")
-    return code
+    return (t.get_device(), code, *_pitch(t, name))
 
 
 def _flat(t: torch.Tensor, name: str, dtype: torch.dtype, index: int) -> int:
     """Pointer of a contiguous tensor of ``dtype`` on device ``index``."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == index \
+            and t.dtype is dtype and t.is_contiguous():
+        return t.data_ptr()
     _on(t, name, index)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _status(status: Optional[torch.Tensor], index: int) -> Optional[int]:
@@ -189,9 +197,7 @@ def embedding_lookup(table: torch.Tensor, ids: torch.Tensor, *, scale: float = 1
     ``out`` may be given as ``(ids.numel(), D)`` rows with a pitch, or as a
     contiguous tensor of the result's shape.
     """
-    index = _on(table, "table")
-    wd = _code(table, "table")
-    rows, D, ldw = _pitch(table, "table")
+    index, wd, rows, D, ldw = _matrix(table, "table")
     pi = _flat(ids, "ids", torch.int32, index)
     T = ids.numel()
     if out is None:
@@ -205,9 +211,9 @@ def embedding_lookup(table: torch.Tensor, ids: torch.Tensor, *, scale: float = 1
             out = out.view(*ids.shape, D)
     else:
         _on(out, "out", index)
-        od = _code(out, "out")
-        if out_dtype is not None and out.dtype != out_dtype:
-            raise TypeError(f"out must be {out_dtype} (got {out.dtype})")
+        od = ops.TABLE_DTYPES.get(out.dtype)
+        if od is None or (out_dtype is not None and out.dtype != out_dtype):
+            raise TypeError(f"out must be {out_dtype or 'float32 or bfloat16'} (got {out.dtype})")
         if out.shape == (*ids.shape, D) and out.is_contiguous():
             ldo = D
         elif out.shape == (T, D):
@@ -216,8 +222,9 @@ def embedding_lookup(table: torch.Tensor, ids: torch.Tensor, *, scale: float = 1
             raise ValueError(f"out must be {(*ids.shape, D)} (contiguous) or {(T, D)} "
                              f"(got {tuple(out.shape)})")
         po = out.data_ptr()
-    _call(_lookup, "dlrm_embedding_lookup", index, table.data_ptr(), wd, ldw, rows, D, pi, T,
-          scale, _padding(padding_idx, rows), po, od, ldo, _status(status, index))
+    _call(_lookup, "dlrm_embedding_lookup", index,
+          (table.data_ptr(), wd, ldw, rows, D, pi, T, scale, _padding(padding_idx, rows), po, od,
+           ldo, _status(status, index)))
     return out
 
 
@@ -252,9 +259,7 @@ def embedding_grad(grad: torch.Tensor, ids: torch.Tensor, num_rows: int, *, L: i
     of at least :func:`embedding_grad_scratch_bytes` bytes; by default one is
     taken from torch's allocator for the call.
     """
-    index = _on(grad, "grad")
-    gd = _code(grad, "grad")
-    n, D, ldg = _pitch(grad, "grad")
+    index, gd, n, D, ldg = _matrix(grad, "grad")
     pi = _flat(ids, "ids", torch.int32, index)
     T = ids.numel()
     if L < 1 or T % L != 0 or n != T // L:
@@ -270,13 +275,11 @@ def embedding_grad(grad: torch.Tensor, ids: torch.Tensor, num_rows: int, *, L: i
             raise ValueError(f"num_rows must be at least 1 (got {num_rows})")
         out = _empty(num_rows, D, dtype, index)
     else:
-        _on(out, "out", index)
-        od = _code(out, "out")
+        _, od, out_rows, out_cols, ldo = _matrix(out, "out", index)
         if dtype is not None and out.dtype != dtype:
             raise TypeError(f"out must be {dtype} (got {out.dtype})")
-        if out.shape != (num_rows, D):
+        if out_rows != num_rows or out_cols != D:
             raise ValueError(f"out must be ({num_rows}, {D}) (got {tuple(out.shape)})")
-        ldo = _pitch(out, "out")[2]
     room = _scratch_bytes(T, num_rows, D)
     if room < 0:
         raise TokensError(room, "dlrm_embedding_grad")
@@ -285,9 +288,10 @@ def embedding_grad(grad: torch.Tensor, ids: torch.Tensor, num_rows: int, *, L: i
         ps = scratch.data_ptr()
     else:
         ps, room = _flat(scratch, "scratch", torch.uint8, index), scratch.numel()
-    _call(_grad, "dlrm_embedding_grad", index, grad.data_ptr(), gd, ldg, pi, T, L, num_rows, D,
-          scale, _padding(padding_idx, num_rows), out.data_ptr(), od, ldo,
-          1 if accumulate else 0, ps, room, _status(status, index))
+    _call(_grad, "dlrm_embedding_grad", index,
+          (grad.data_ptr(), gd, ldg, pi, T, L, num_rows, D, scale,
+           _padding(padding_idx, num_rows), out.data_ptr(), od, ldo, 1 if accumulate else 0, ps,
+           room, _status(status, index)))
     return out
 
 

@@ -219,10 +219,10 @@ def test_calls_run_on_their_tensors_device(tokens, monkeypatch):
         seen.append((a, stream, current[0]))
         return -2 if a == 7 else 0
 
-    tokens._call(entry, "entry", 0, 5)
-    tokens._call(entry, "entry", 1, 6)
+    tokens._call(entry, "entry", 0, (5,))
+    tokens._call(entry, "entry", 1, (6,))
     assert seen == [(5, 1000, 0), (6, 1001, 1)] and current == [0]
     with pytest.raises(tokens.TokensError, match="entry: DLRM_ERR_SHAPE") as e:
-        tokens._call(entry, "entry", 1, 7)
+        tokens._call(entry, "entry", 1, (7,))
     assert e.value.status == -2 and current == [0]
     assert isinstance(e.value, tokens.ops.DlrmError)
