@@ -831,7 +831,8 @@ __device__ __forceinline__ void sum_block(const SumArgs& a, SumSmem<VEC, G>& sm,
 // JOIN: the join kernel follows, and may be scheduled early (it waits before it
 // reads anything; what else may follow is not known to).
 template <class In, int VEC, int G, bool JOIN>
-__global__ void __launch_bounds__(kSumThreads, 4) sum_kernel(const SumArgs a) {
+__global__ void __launch_bounds__(kSumThreads, sizeof(In) == 2 && VEC > 1 ? 4 : 3)
+    sum_kernel(const SumArgs a) {
   __shared__ SumSmem<VEC, G> sm;
   if constexpr (JOIN) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the sort (and the zeros) are done
