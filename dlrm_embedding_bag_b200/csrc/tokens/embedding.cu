@@ -175,11 +175,26 @@ __device__ __forceinline__ void fill_end() {
   if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
-// No tokens at all: the zeros alone.
-__global__ void __launch_bounds__(1024) fill_kernel(const FillArgs f) {
-  __shared__ __align__(16) uint8_t zeros[kZeroBytes];
+// The zeros alone, behind a cluster sort and at the same time: a block for each
+// SM that the sort leaves. An SM writes about 60 GB/s of bulk stores however
+// many blocks share it, so the blocks must not: each asks for half of the shared
+// memory. 256 MB take 40 us so, the memory's rate; with 148 small blocks, some
+// of them two on an SM, 59 us, where most had ended after 32. (Fill blocks in
+// clusters of the sort's own launch took 41 or 45 us, by how many clusters the
+// GPU at hand keeps resident.)
+constexpr int kFillThreads = 64;
+constexpr int kFillSmem = 116 << 10;
+
+__global__ void __launch_bounds__(kFillThreads) fill_kernel(const FillArgs f) {
+  extern __shared__ __align__(16) uint8_t zeros[];
+  static_assert(kFillSmem >= kZeroBytes, "room for the zeros");
+  // the sums' blocks may be scheduled now (they wait for this grid's end)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   fill_begin(f, blockIdx.x, gridDim.x, zeros);
   fill_end();
+  // The sort in front is still at work, perhaps: this grid ends after it, so that
+  // what waits for the zeros has the sorted tokens too.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -479,27 +494,24 @@ struct ClusterSmem {
   uint2 arrived[kClusterThreads * ITEMS];  // this CTA's stretch of the pairs after a pass
   uint32_t total[kRadix];                  // its count of each digit, read by the others
   uint32_t place[kRadix];
+  alignas(16) uint8_t zeros[kZeroBytes];
 };
 
-// The first cluster sorts: each of its CTAs owns a stretch of the pairs, a tile.
-// The other clusters fill.
+// One cluster sorts: each of its CTAs owns a stretch of the pairs, a tile. Few
+// zeros it writes itself.
 template <int ITEMS>
 __global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(const SortArgs a) {
   extern __shared__ __align__(16) uint8_t sort_smem[];
-  // the sums' blocks may be scheduled now (they wait for this grid's end)
+  // the fill's or the sums' blocks may be scheduled now: these wait for this
+  // grid's end, those have nothing to do with it before theirs
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (blockIdx.x >= kClusterSize) {
-    static_assert(sizeof(ClusterSmem<ITEMS>) >= kZeroBytes, "room for the zeros");
-    fill_begin(a.fill, blockIdx.x - kClusterSize, a.fill_parts, sort_smem);
-    fill_end();
-    return;
-  }
   auto& sm = *reinterpret_cast<ClusterSmem<ITEMS>*>(sort_smem);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(cluster_ctarank());
   constexpr int kStretch = kClusterThreads * ITEMS;
   const int own = warp * 32 * ITEMS + lane;  // the thread's first pair in the stretch
   const int n = max(0, min(kStretch, a.T - rank * kStretch));
+  if (a.fill.out != nullptr) fill_begin(a.fill, rank, kClusterSize, sm.zeros);
   const uint32_t mask = (1u << a.bits) - 1;
   uint2 pair[ITEMS];
 #pragma unroll
@@ -546,56 +558,10 @@ __global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(const 
       for (int u = 0; u < ITEMS; ++u) pair[u] = sm.arrived[own + u * 32];
     }
   }
+  if (a.fill.out != nullptr) fill_end();
 }
 
-// Sorts up to kClusterSort tokens of `ids` into a.out and zeroes a.fill.
-template <int ITEMS>
-cudaError_t run_cluster_sort(SortArgs& a, cudaStream_t stream) {
-  auto* fn = &sort_cluster_kernel<ITEMS>;
-  constexpr int smem = sizeof(ClusterSmem<ITEMS>);
-  // Per device, the shared-memory size is set and the resident cluster count
-  // asked for once: 0 = not yet, else that count + 1.
-  static std::atomic<int> prepared[kMaxDevices];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const bool cacheable = dev >= 0 && dev < kMaxDevices;
-  const int cached = cacheable ? prepared[dev].load(std::memory_order_acquire) : 0;
-  int fit = cached - 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kClusterThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kClusterSize;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cached == 0) {
-    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    cfg.gridDim = dim3(16 * kClusterSize);
-    if ((e = cudaOccupancyMaxActiveClusters(&fit, fn, &cfg)) != cudaSuccess) return e;
-    if (cacheable) prepared[dev].store(fit + 1, std::memory_order_release);
-  }
-  // Clusters that fill, each 64 KB at least: not more than run beside the one
-  // that sorts (another would wait for that one to end: 60 instead of 43 us at
-  // 32768 tokens and 256 MB of zeros).
-  int fillers = 0;
-  if (a.fill.out != nullptr) {
-    const int64_t bytes = a.fill.rows * a.fill.row_bytes;
-    fillers = static_cast<int>(std::min<int64_t>(std::max(1, fit - 1),
-                                                 bytes / (kClusterSize * (64 << 10)) + 1));
-  }
-  a.fill_parts = fillers * kClusterSize;
-  cfg.gridDim = dim3((fillers + 1) * kClusterSize);
-  return cudaLaunchKernelEx(&cfg, fn, a);
-}
-
-// A kernel that may be scheduled while the one before it ends, and waits for it.
+// A kernel that may be scheduled while the one before it is at work.
 template <class... P, class... A>
 cudaError_t launch_after(void (*fn)(P...), dim3 grid, int threads, int smem,
                          cudaStream_t stream, const A&... args) {
@@ -612,6 +578,63 @@ cudaError_t launch_after(void (*fn)(P...), dim3 grid, int threads, int smem,
   return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
+// A kernel's dynamic shared memory, set once per device (`prepared` is its own).
+template <class K>
+cudaError_t allow_smem(K* fn, int bytes, std::atomic<bool> (&prepared)[kMaxDevices]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool cacheable = dev >= 0 && dev < kMaxDevices;
+  if (cacheable && prepared[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && cacheable) prepared[dev].store(true, std::memory_order_release);
+  return e;
+}
+
+// The zeros behind what was launched last (a cluster sort, or nothing of ours).
+cudaError_t run_fill(const FillArgs& f, int blocks, cudaStream_t stream) {
+  static std::atomic<bool> prepared[kMaxDevices];
+  const cudaError_t e = allow_smem(&fill_kernel, kFillSmem, prepared);
+  if (e != cudaSuccess) return e;
+  return launch_after(&fill_kernel, dim3(blocks), kFillThreads, kFillSmem, stream, f);
+}
+
+// Zeros that the cluster sort writes itself, in about the time that it sorts;
+// more go to a kernel beside it.
+constexpr int64_t kClusterZeros = 4 << 20;
+
+// Sorts up to kClusterSort tokens of `ids` into a.out and zeroes a.fill. Launched
+// kernels are added to n.
+template <int ITEMS>
+cudaError_t run_cluster_sort(SortArgs& a, int sms, int& n, cudaStream_t stream) {
+  auto* fn = &sort_cluster_kernel<ITEMS>;
+  constexpr int smem = sizeof(ClusterSmem<ITEMS>);
+  static_assert(smem <= 227 * 1024, "shared memory of one CTA");
+  static std::atomic<bool> prepared[kMaxDevices];
+  cudaError_t e = allow_smem(fn, smem, prepared);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kClusterSize);
+  cfg.blockDim = dim3(kClusterThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = kClusterSize;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const FillArgs fill = a.fill;
+  const bool beside = fill.out != nullptr && fill.rows * fill.row_bytes > kClusterZeros;
+  if (beside) a.fill.out = nullptr;
+  ++n;
+  if ((e = cudaLaunchKernelEx(&cfg, fn, a)) != cudaSuccess || !beside) return e;
+  ++n;
+  return run_fill(fill, std::max(1, sms - kClusterSize), stream);
+}
+
 // Sorts more tokens, two launches a pass, between the two buffers of pairs; the
 // zeros are shared out evenly over the launches. a.out ends as the sorted one.
 template <int ITEMS>
@@ -619,16 +642,8 @@ cudaError_t run_grid_sort(SortArgs& a, uint2* const (&pairs)[2], cudaStream_t st
   constexpr int smem = sizeof(MoveSmem<ITEMS>);
   auto* move = &sort_move_kernel<ITEMS>;
   static std::atomic<bool> prepared[kMaxDevices];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  cudaError_t e = allow_smem(move, smem, prepared);
   if (e != cudaSuccess) return e;
-  const bool cacheable = dev >= 0 && dev < kMaxDevices;
-  if (!cacheable || !prepared[dev].load(std::memory_order_acquire)) {
-    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(move),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    if (cacheable) prepared[dev].store(true, std::memory_order_release);
-  }
   // blocks enough to keep the memory busy with zeros
   const int grid = a.fill.out != nullptr ? std::max(a.blocks, 148) : a.blocks;
   a.fill_parts = 2 * a.passes * grid;
@@ -1216,6 +1231,8 @@ int dlrm_embedding_grad(const void* grad, int grad_dtype, int64_t ldg, const int
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int rc = clear_status(status_dev, s);
   if (rc != DLRM_OK) return rc;
+  const int sms = sm_count_current();
+  if (sms == 0) return DLRM_ERR_CUDA;
   FillArgs fill = {};
   if (!accumulate) {
     fill.out = static_cast<char*>(out);
@@ -1225,8 +1242,7 @@ int dlrm_embedding_grad(const void* grad, int grad_dtype, int64_t ldg, const int
   }
   if (T == 0) {
     if (accumulate) return DLRM_OK;
-    fill_kernel<<<148, 1024, 0, s>>>(fill);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e = run_fill(fill, sms, s);
     if (e != cudaSuccess) return cuda_fail(e);
     note_launch();
     return DLRM_OK;
@@ -1278,13 +1294,13 @@ int dlrm_embedding_grad(const void* grad, int grad_dtype, int64_t ldg, const int
   uint2* const pairs[2] = {reinterpret_cast<uint2*>(mem + p.pairs[0]),
                            reinterpret_cast<uint2*>(mem + p.pairs[1])};
   sa.out = pairs[0];
-  int n = 1;
+  int n = 0;
   if (T <= kClusterSort) {
     const int64_t items = (T + kClusterSize * kClusterThreads - 1) / (kClusterSize * kClusterThreads);
-    e = items <= 1   ? run_cluster_sort<1>(sa, s)
-        : items <= 2 ? run_cluster_sort<2>(sa, s)
-        : items <= 4 ? run_cluster_sort<4>(sa, s)
-                     : run_cluster_sort<8>(sa, s);
+    e = items <= 1   ? run_cluster_sort<1>(sa, sms, n, s)
+        : items <= 2 ? run_cluster_sort<2>(sa, sms, n, s)
+        : items <= 4 ? run_cluster_sort<4>(sa, sms, n, s)
+                     : run_cluster_sort<8>(sa, sms, n, s);
   } else {
     e = p.items == 4   ? run_grid_sort<4>(sa, pairs, s)
         : p.items == 6 ? run_grid_sort<6>(sa, pairs, s)
