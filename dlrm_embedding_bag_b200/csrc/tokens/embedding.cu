@@ -106,8 +106,9 @@ cudaError_t run_lookup_shape(const LookupArgs& a, bool vec, cudaStream_t stream)
 // Gradient: zeros for the rows that no token names.
 //
 // A dense gradient is mostly writes, and the sort in front of the sums leaves
-// the memory idle; so every row is zeroed by blocks that ride along with the
-// sort's, and the named rows are written over later.
+// the memory idle; so every row is zeroed while the tokens are sorted (by a warp
+// of the sort's own blocks, or a kernel beside it), and the named rows are
+// written over later.
 
 struct FillArgs {
   char* out;      // null: nothing to fill
@@ -126,41 +127,40 @@ __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t by
 
 constexpr int kZeroBytes = 16 << 10;  // of a bulk store
 
-// Part `part` of `parts` of the zeros, by the whole block. One stretch of bytes
-// goes out as bulk stores of a block of zeros, which one thread issues and which
-// run on by themselves until fill_end: a sort's blocks fill while they sort.
-// (A thread's own 16-byte stores, one after another, reached 6.0 TB/s, these
-// 6.4.) zeros: kZeroBytes of shared memory, 16-byte aligned, for this alone.
-__device__ void fill_begin(const FillArgs& f, int part, int parts, uint8_t* zeros) {
-  const int threads = blockDim.x;
-  const int64_t first = static_cast<int64_t>(part) * threads + threadIdx.x;
-  const int64_t step = static_cast<int64_t>(parts) * threads;
+// Part `part` of `parts` of the zeros, by one whole warp. One stretch of bytes goes
+// out as bulk stores of a block of zeros, which one lane issues; it waits where
+// the SM's queue of them is full, so the warp has nothing else to do meanwhile.
+// zeros: kZeroBytes of shared memory, 16-byte aligned, for this alone. The warp
+// has to call fill_done before it ends.
+__device__ void fill_zeros(const FillArgs& f, int part, int parts, uint8_t* zeros) {
+  const int lane = threadIdx.x & 31;
   if (f.pitch == f.row_bytes) {
     const int64_t bytes = f.rows * f.row_bytes;
     const int64_t lead = min(bytes, static_cast<int64_t>(-reinterpret_cast<intptr_t>(f.out) & 15));
     const int64_t mid = (bytes - lead) & ~int64_t{15};
-    for (int i = threadIdx.x; i < kZeroBytes / 16; i += threads)
+    for (int i = lane; i < kZeroBytes / 16; i += 32)
       reinterpret_cast<uint4*>(zeros)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
-    __syncthreads();
-    if (threadIdx.x == 0) {
+    __syncwarp();
+    if (lane == 0) {
       for (int64_t at = static_cast<int64_t>(part) * kZeroBytes; at < mid;
            at += static_cast<int64_t>(parts) * kZeroBytes)
         bulk_s2g(f.out + lead + at, zeros,
                  static_cast<uint32_t>(min(static_cast<int64_t>(kZeroBytes), mid - at)));
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
-    // the unaligned ends
-    if (first < lead) f.out[first] = 0;
-    if (first < bytes - lead - mid) f.out[lead + mid + first] = 0;
+    if (part == 0) {  // the unaligned ends
+      if (lane < lead) f.out[lane] = 0;
+      if (lane < bytes - lead - mid) f.out[lead + mid + lane] = 0;
+    }
   } else {
-    // rows apart from each other, a warp each: whole 16-byte units, or the
-    // 2 bytes that every element has at least
+    // rows apart from each other: whole 16-byte units, or the 2 bytes that every
+    // element has at least
     const bool wide = ((reinterpret_cast<intptr_t>(f.out) | f.row_bytes | f.pitch) & 15) == 0;
     const int64_t per_row = f.row_bytes / (wide ? 16 : 2);
-    for (int64_t r = first / 32; r < f.rows; r += step / 32) {
+    for (int64_t r = part; r < f.rows; r += parts) {
       char* row = f.out + r * f.pitch;
-      for (int64_t c = threadIdx.x % 32; c < per_row; c += 32) {
+      for (int64_t c = lane; c < per_row; c += 32) {
         if (wide)
           reinterpret_cast<uint4*>(row)[c] = make_uint4(0, 0, 0, 0);
         else
@@ -170,9 +170,9 @@ __device__ void fill_begin(const FillArgs& f, int part, int parts, uint8_t* zero
   }
 }
 
-// The zeros that this block began are written.
-__device__ __forceinline__ void fill_end() {
-  if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+// The zeros that this warp began are written.
+__device__ __forceinline__ void fill_done() {
+  if ((threadIdx.x & 31) == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // The zeros alone, behind a cluster sort and at the same time: a block for each
@@ -182,7 +182,7 @@ __device__ __forceinline__ void fill_end() {
 // of them two on an SM, 59 us, where most had ended after 32. (Fill blocks in
 // clusters of the sort's own launch took 41 or 45 us, by how many clusters the
 // GPU at hand keeps resident.)
-constexpr int kFillThreads = 64;
+constexpr int kFillThreads = 32;
 constexpr int kFillSmem = 116 << 10;
 
 __global__ void __launch_bounds__(kFillThreads) fill_kernel(const FillArgs f) {
@@ -190,8 +190,8 @@ __global__ void __launch_bounds__(kFillThreads) fill_kernel(const FillArgs f) {
   static_assert(kFillSmem >= kZeroBytes, "room for the zeros");
   // the sums' blocks may be scheduled now (they wait for this grid's end)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  fill_begin(f, blockIdx.x, gridDim.x, zeros);
-  fill_end();
+  fill_zeros(f, blockIdx.x, gridDim.x, zeros);
+  fill_done();
   // The sort in front is still at work, perhaps: this grid ends after it, so that
   // what waits for the zeros has the sorted tokens too.
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -265,8 +265,15 @@ __device__ __forceinline__ unsigned same_digit(uint32_t digit, bool live, int bi
   return peers;
 }
 
-// Exclusive sums over the digits, for the threads below kRadix; every thread of
-// the block takes part. Holds a barrier.
+// A barrier of the THREADS threads that sort (a warp more may be filling).
+template <int THREADS>
+__device__ __forceinline__ void sort_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
+
+// Exclusive sums over the digits, for the threads below kRadix; every thread that
+// sorts takes part. Holds a barrier.
+template <int THREADS>
 __device__ __forceinline__ uint32_t digits_before(uint32_t n, uint32_t* warp_sum) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t scan = n;
@@ -276,7 +283,7 @@ __device__ __forceinline__ uint32_t digits_before(uint32_t n, uint32_t* warp_sum
     if (lane >= o) scan += m;
   }
   if (threadIdx.x < kRadix && lane == 31) warp_sum[warp] = scan;
-  __syncthreads();
+  sort_sync<THREADS>();
   if (threadIdx.x < kRadix)
     for (int w = 0; w < warp; ++w) scan += warp_sum[w];
   return scan - n;
@@ -320,7 +327,7 @@ __device__ __forceinline__ uint32_t order_tile(TileSmem<THREADS, ITEMS>& sm,
     if (live && lane == __ffs(peers) - 1) sm.at[warp][digit] += __popc(peers);
     __syncwarp();
   }
-  __syncthreads();
+  sort_sync<THREADS>();
   // ... among the tile's warps: kWarpsOfPart of them a thread, then the threads of a digit
   const int d = tid % kRadix, part = tid / kRadix;
   uint32_t sum = 0;
@@ -332,12 +339,12 @@ __device__ __forceinline__ uint32_t order_tile(TileSmem<THREADS, ITEMS>& sm,
     sum += m;
   }
   sm.parts[part][d] = sum;
-  __syncthreads();
+  sort_sync<THREADS>();
   uint32_t count = 0;
 #pragma unroll
   for (int k = 0; k < S::kParts; ++k) count += sm.parts[k][d];
   // ... and after the smaller digits
-  uint32_t place = digits_before(count, sm.warp_sum);
+  uint32_t place = digits_before<THREADS>(count, sm.warp_sum);
   if (part == 0) {
     sm.start[d] = place;
 #pragma unroll
@@ -347,7 +354,7 @@ __device__ __forceinline__ uint32_t order_tile(TileSmem<THREADS, ITEMS>& sm,
       place += m;
     }
   }
-  __syncthreads();
+  sort_sync<THREADS>();
 #pragma unroll
   for (int u = 0; u < ITEMS; ++u) {
     if (own + u * 32 < n) {
@@ -355,47 +362,49 @@ __device__ __forceinline__ uint32_t order_tile(TileSmem<THREADS, ITEMS>& sm,
       sm.pairs[sm.parts[warp / S::kWarpsOfPart][digit] + sm.at[warp][digit] + among[u]] = pair[u];
     }
   }
-  __syncthreads();
+  sort_sync<THREADS>();
   return count;
 }
 
-__global__ void __launch_bounds__(kSortThreads, 2) sort_count_kernel(const SortArgs a) {
+__global__ void __launch_bounds__(kSortThreads + 32, 2) sort_count_kernel(const SortArgs a) {
   __shared__ __align__(16) uint8_t zeros[kZeroBytes];
   __shared__ uint32_t cnt[kRadix];
   const int tid = threadIdx.x;
-  if (tid < kRadix) cnt[tid] = 0;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the pass before is done
-  if (a.fill.out != nullptr) fill_begin(a.fill, a.fill_part + blockIdx.x, a.fill_parts, zeros);
-  if (static_cast<int>(blockIdx.x) < a.blocks) {
-    __syncthreads();
-    const int64_t begin = static_cast<int64_t>(blockIdx.x) * a.per;
-    const int64_t end = min(begin + a.per, static_cast<int64_t>(a.T));
-    const uint32_t mask = (1u << a.bits) - 1;
-    constexpr int kLoads = 4;  // pairs a thread loads at once
-    for (int64_t i0 = begin; i0 < end; i0 += kSortThreads * kLoads) {
-      uint32_t digit[kLoads];
+  if (tid >= kSortThreads) {
+    fill_zeros(a.fill, a.fill_part + blockIdx.x, a.fill_parts, zeros);
+    fill_done();
+    return;
+  }
+  if (static_cast<int>(blockIdx.x) >= a.blocks) return;
+  if (tid < kRadix) cnt[tid] = 0;
+  sort_sync<kSortThreads>();
+  const int64_t begin = static_cast<int64_t>(blockIdx.x) * a.per;
+  const int64_t end = min(begin + a.per, static_cast<int64_t>(a.T));
+  const uint32_t mask = (1u << a.bits) - 1;
+  constexpr int kLoads = 4;  // pairs a thread loads at once
+  for (int64_t i0 = begin; i0 < end; i0 += kSortThreads * kLoads) {
+    uint32_t digit[kLoads];
 #pragma unroll
-      for (int u = 0; u < kLoads; ++u) {
-        const int64_t i = i0 + u * kSortThreads + tid;
-        digit[u] = kRadix;  // of no pair
-        if (i < end) {
-          flag_bad_id(a, i);
-          digit[u] = (sort_pair(a, i).x >> a.shift) & mask;
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < kLoads; ++u) {
-        // a warp whose digits are all the same (one frequent id) adds once
-        const bool same = __all_sync(kFull, digit[u] == __shfl_sync(kFull, digit[u], 0));
-        if (digit[u] != kRadix && (!same || (tid & 31) == 0))
-          atomicAdd(&cnt[digit[u]], same ? 32 : 1);
+    for (int u = 0; u < kLoads; ++u) {
+      const int64_t i = i0 + u * kSortThreads + tid;
+      digit[u] = kRadix;  // of no pair
+      if (i < end) {
+        flag_bad_id(a, i);
+        digit[u] = (sort_pair(a, i).x >> a.shift) & mask;
       }
     }
-    __syncthreads();
-    if (tid < kRadix) a.counts[static_cast<int64_t>(blockIdx.x) * kRadix + tid] = cnt[tid];
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      // a warp whose digits are all the same (one frequent id) adds once
+      const bool same = __all_sync(kFull, digit[u] == __shfl_sync(kFull, digit[u], 0));
+      if (digit[u] != kRadix && (!same || (tid & 31) == 0))
+        atomicAdd(&cnt[digit[u]], same ? 32 : 1);
+    }
   }
-  if (a.fill.out != nullptr) fill_end();
+  sort_sync<kSortThreads>();
+  if (tid < kRadix) a.counts[static_cast<int64_t>(blockIdx.x) * kRadix + tid] = cnt[tid];
 }
 
 template <int ITEMS>
@@ -406,13 +415,17 @@ struct MoveSmem {
 };
 
 template <int ITEMS>
-__global__ void __launch_bounds__(kSortThreads, 2) sort_move_kernel(const SortArgs a) {
+__global__ void __launch_bounds__(kSortThreads + 32, 2) sort_move_kernel(const SortArgs a) {
   extern __shared__ __align__(16) uint8_t sort_smem[];
   auto& sm = *reinterpret_cast<MoveSmem<ITEMS>*>(sort_smem);
   static_assert(offsetof(MoveSmem<ITEMS>, zeros) % 16 == 0, "bulk stores");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the counts are there
-  if (a.fill.out != nullptr) fill_begin(a.fill, a.fill_part + blockIdx.x, a.fill_parts, sm.zeros);
+  if (threadIdx.x >= kSortThreads) {
+    fill_zeros(a.fill, a.fill_part + blockIdx.x, a.fill_parts, sm.zeros);
+    fill_done();
+    return;
+  }
   if (static_cast<int>(blockIdx.x) < a.blocks) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t mask = (1u << a.bits) - 1;
@@ -448,7 +461,7 @@ __global__ void __launch_bounds__(kSortThreads, 2) sort_move_kernel(const SortAr
       sums[part * (kRadix / 4) + d4] = all;
       sums[(8 + part) * (kRadix / 4) + d4] = mine;
     }
-    __syncthreads();
+    sort_sync<kSortThreads>();
     uint32_t all = 0, place = 0;
     if (tid < kRadix) {
       const uint32_t* sums = reinterpret_cast<const uint32_t*>(sm.tile.pairs);
@@ -458,12 +471,12 @@ __global__ void __launch_bounds__(kSortThreads, 2) sort_move_kernel(const SortAr
         place += sums[(8 + p) * kRadix + tid];
       }
     }
-    place += digits_before(all, sm.tile.warp_sum);
+    place += digits_before<kSortThreads>(all, sm.tile.warp_sum);
     if (tid < kRadix) sm.place[tid] = place;
     for (int64_t i0 = begin; i0 < end; i0 += kTile) {
       const int n = static_cast<int>(min(static_cast<int64_t>(kTile), end - i0));
       if (i0 > begin) load(i0);
-      __syncthreads();  // the tile before has left, its digits' places are set
+      sort_sync<kSortThreads>();  // the tile before has left, its digits' places are set
       const uint32_t count = order_tile(sm.tile, pair, n, a.shift, a.bits);
 #pragma unroll 4
       for (int k = tid; k < n; k += kSortThreads) {
@@ -471,11 +484,10 @@ __global__ void __launch_bounds__(kSortThreads, 2) sort_move_kernel(const SortAr
         const uint32_t digit = (p.x >> a.shift) & mask;
         a.out[sm.place[digit] + (k - sm.tile.start[digit])] = p;
       }
-      __syncthreads();
+      sort_sync<kSortThreads>();
       if (tid < kRadix) sm.place[tid] += count;
     }
   }
-  if (a.fill.out != nullptr) fill_end();
 }
 
 __device__ __forceinline__ uint32_t load_cluster_u32(uint32_t cluster_addr) {
@@ -511,7 +523,6 @@ __global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(const 
   constexpr int kStretch = kClusterThreads * ITEMS;
   const int own = warp * 32 * ITEMS + lane;  // the thread's first pair in the stretch
   const int n = max(0, min(kStretch, a.T - rank * kStretch));
-  if (a.fill.out != nullptr) fill_begin(a.fill, rank, kClusterSize, sm.zeros);
   const uint32_t mask = (1u << a.bits) - 1;
   uint2 pair[ITEMS];
 #pragma unroll
@@ -522,6 +533,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(const 
       flag_bad_id(a, rank * kStretch + own + u * 32);
     }
   }
+  if (a.fill.out != nullptr && warp == 0) fill_zeros(a.fill, rank, kClusterSize, sm.zeros);
   for (int p = 0; p < a.passes; ++p) {
     const int shift = p * a.bits;
     const uint32_t count = order_tile(sm.tile, pair, n, shift, a.bits);
@@ -538,7 +550,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(const 
         place += r < rank ? c : 0;
       }
     }
-    place += digits_before(all, sm.tile.warp_sum);
+    place += digits_before<kClusterThreads>(all, sm.tile.warp_sum);
     if (tid < kRadix) sm.place[tid] = place;
     __syncthreads();
     const bool final_pass = p + 1 == a.passes;
@@ -558,7 +570,7 @@ __global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(const 
       for (int u = 0; u < ITEMS; ++u) pair[u] = sm.arrived[own + u * 32];
     }
   }
-  if (a.fill.out != nullptr) fill_end();
+  if (a.fill.out != nullptr && warp == 0) fill_done();
 }
 
 // A kernel that may be scheduled while the one before it is at work.
@@ -600,9 +612,9 @@ cudaError_t run_fill(const FillArgs& f, int blocks, cudaStream_t stream) {
   return launch_after(&fill_kernel, dim3(blocks), kFillThreads, kFillSmem, stream, f);
 }
 
-// Zeros that the cluster sort writes itself, in about the time that it sorts;
-// more go to a kernel beside it.
-constexpr int64_t kClusterZeros = 4 << 20;
+// Zeros that the cluster sort writes itself, 16 bulk stores a CTA; more go to a
+// kernel beside it.
+constexpr int64_t kClusterZeros = int64_t{kClusterSize} * 16 * kZeroBytes;
 
 // Sorts up to kClusterSort tokens of `ids` into a.out and zeroes a.fill. Launched
 // kernels are added to n.
@@ -646,6 +658,7 @@ cudaError_t run_grid_sort(SortArgs& a, uint2* const (&pairs)[2], cudaStream_t st
   if (e != cudaSuccess) return e;
   // blocks enough to keep the memory busy with zeros
   const int grid = a.fill.out != nullptr ? std::max(a.blocks, 148) : a.blocks;
+  const int threads = a.fill.out != nullptr ? kSortThreads + 32 : kSortThreads;
   a.fill_parts = 2 * a.passes * grid;
   for (int i = 0; i < a.passes; ++i) {
     a.out = pairs[i & 1];
@@ -653,14 +666,14 @@ cudaError_t run_grid_sort(SortArgs& a, uint2* const (&pairs)[2], cudaStream_t st
     a.fill_part = 2 * i * grid;
     // the first launch waits for all that came before it on the stream
     if (i == 0) {
-      sort_count_kernel<<<grid, kSortThreads, 0, stream>>>(a);
+      sort_count_kernel<<<grid, threads, 0, stream>>>(a);
       e = cudaGetLastError();
     } else {
-      e = launch_after(&sort_count_kernel, dim3(grid), kSortThreads, 0, stream, a);
+      e = launch_after(&sort_count_kernel, dim3(grid), threads, 0, stream, a);
     }
     if (e != cudaSuccess) return e;
     a.fill_part += grid;
-    if ((e = launch_after(move, dim3(grid), kSortThreads, smem, stream, a)) != cudaSuccess) return e;
+    if ((e = launch_after(move, dim3(grid), threads, smem, stream, a)) != cudaSuccess) return e;
     a.ids = nullptr;
     a.in = a.out;
   }
