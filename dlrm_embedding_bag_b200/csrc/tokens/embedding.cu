@@ -127,12 +127,14 @@ __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t by
 
 constexpr int kZeroBytes = 16 << 10;  // of a bulk store
 
-// Part `part` of `parts` of the zeros, by one whole warp. One stretch of bytes goes
+// Parts part, part + apart, .. (`count` of them) of `parts` of the zeros, by one
+// whole warp. One stretch of bytes goes
 // out as bulk stores of a block of zeros, which one lane issues; it waits where
 // the SM's queue of them is full, so the warp has nothing else to do meanwhile.
 // zeros: kZeroBytes of shared memory, 16-byte aligned, for this alone. The warp
 // has to call fill_done before it ends.
-__device__ void fill_zeros(const FillArgs& f, int part, int parts, uint8_t* zeros) {
+__device__ void fill_zeros(const FillArgs& f, int part, int parts, uint8_t* zeros, int count = 1,
+                           int apart = 0) {
   const int lane = threadIdx.x & 31;
   if (f.pitch == f.row_bytes) {
     const int64_t bytes = f.rows * f.row_bytes;
@@ -143,10 +145,11 @@ __device__ void fill_zeros(const FillArgs& f, int part, int parts, uint8_t* zero
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      for (int64_t at = static_cast<int64_t>(part) * kZeroBytes; at < mid;
-           at += static_cast<int64_t>(parts) * kZeroBytes)
-        bulk_s2g(f.out + lead + at, zeros,
-                 static_cast<uint32_t>(min(static_cast<int64_t>(kZeroBytes), mid - at)));
+      for (int k = 0; k < count; ++k)
+        for (int64_t at = static_cast<int64_t>(part + k * apart) * kZeroBytes; at < mid;
+             at += static_cast<int64_t>(parts) * kZeroBytes)
+          bulk_s2g(f.out + lead + at, zeros,
+                   static_cast<uint32_t>(min(static_cast<int64_t>(kZeroBytes), mid - at)));
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
     if (part == 0) {  // the unaligned ends
@@ -158,15 +161,16 @@ __device__ void fill_zeros(const FillArgs& f, int part, int parts, uint8_t* zero
     // element has at least
     const bool wide = ((reinterpret_cast<intptr_t>(f.out) | f.row_bytes | f.pitch) & 15) == 0;
     const int64_t per_row = f.row_bytes / (wide ? 16 : 2);
-    for (int64_t r = part; r < f.rows; r += parts) {
-      char* row = f.out + r * f.pitch;
-      for (int64_t c = lane; c < per_row; c += 32) {
-        if (wide)
-          reinterpret_cast<uint4*>(row)[c] = make_uint4(0, 0, 0, 0);
-        else
-          reinterpret_cast<uint16_t*>(row)[c] = 0;
+    for (int k = 0; k < count; ++k)
+      for (int64_t r = part + k * apart; r < f.rows; r += parts) {
+        char* row = f.out + r * f.pitch;
+        for (int64_t c = lane; c < per_row; c += 32) {
+          if (wide)
+            reinterpret_cast<uint4*>(row)[c] = make_uint4(0, 0, 0, 0);
+          else
+            reinterpret_cast<uint16_t*>(row)[c] = 0;
+        }
       }
-    }
   }
 }
 
@@ -215,6 +219,10 @@ constexpr int kRadix = 256;
 constexpr int kSortThreads = 512;  // of a block that counts or moves
 constexpr int kSortItems = 16;     // pairs of a thread, at most, in a tile
 constexpr int kSortMaxBlocks = 296;  // two blocks an SM
+// A move takes more than twice as long as a count (19 and 8 us at 1.3 M pairs) and
+// writes more of the zeros meanwhile: 512 MB of them, in all 271 us with equal
+// parts, 263 with two of three in the moves, 258 with three of four.
+constexpr int kMoveParts = 3, kPassParts = kMoveParts + 1;
 constexpr int kClusterThreads = 1024;
 constexpr int kClusterSize = 8;       // CTAs
 constexpr int kClusterMaxItems = 8;  // pairs of a thread
@@ -422,7 +430,7 @@ __global__ void __launch_bounds__(kSortThreads + 32, 2) sort_move_kernel(const S
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the counts are there
   if (threadIdx.x >= kSortThreads) {
-    fill_zeros(a.fill, a.fill_part + blockIdx.x, a.fill_parts, sm.zeros);
+    fill_zeros(a.fill, a.fill_part + blockIdx.x, a.fill_parts, sm.zeros, kMoveParts, gridDim.x);
     fill_done();
     return;
   }
@@ -659,11 +667,11 @@ cudaError_t run_grid_sort(SortArgs& a, uint2* const (&pairs)[2], cudaStream_t st
   // blocks enough to keep the memory busy with zeros
   const int grid = a.fill.out != nullptr ? std::max(a.blocks, 148) : a.blocks;
   const int threads = a.fill.out != nullptr ? kSortThreads + 32 : kSortThreads;
-  a.fill_parts = 2 * a.passes * grid;
+  a.fill_parts = kPassParts * a.passes * grid;
   for (int i = 0; i < a.passes; ++i) {
     a.out = pairs[i & 1];
     a.shift = i * a.bits;
-    a.fill_part = 2 * i * grid;
+    a.fill_part = kPassParts * i * grid;
     // the first launch waits for all that came before it on the stream
     if (i == 0) {
       sort_count_kernel<<<grid, threads, 0, stream>>>(a);
