@@ -696,28 +696,29 @@ cudaError_t run_few(const Operands& op, const LinArgs& args, cudaStream_t stream
 
 // The forms of the tensor-core kernel, with what they take on a B200 in us: a K
 // block of 128 bytes of a tile (`step`; a narrow tile's is bound by the latency
-// of its loads) and the draining of an accumulator (`drain`, which the next
-// tile's products overlap). Fitted to 15 forms at 18 shapes: the choice by them
-// was the fastest or within 4 % of it at all of these.
+// of its loads), what a tile takes besides (`tile`), the least that a tile takes
+// (`least`: its drain), and the joining of a cluster's parts (`join`). Fitted to
+// all forms at 27 shapes from 5 x 512 x 512 to 65536 x 512 x 592 in a graph; the
+// choice was the fastest form, or within 5 % of it, at 26 of them.
 struct Form {
   int bn;
   bool pair;
   int split;
-  double step, drain;
+  double step, tile, least, join;
   cudaError_t (*run)(const Operands&, LinArgs, int, cudaStream_t);
 };
 const Form kForms[] = {
-    {32, false, 1, 0.30, 0.1, run_linear<32, false, 1>},
-    {32, false, 2, 0.30, 0.1, run_linear<32, false, 2>},
-    {32, false, 4, 0.30, 0.1, run_linear<32, false, 4>},
-    {64, false, 1, 0.31, 0.4, run_linear<64, false, 1>},
-    {64, false, 2, 0.31, 0.4, run_linear<64, false, 2>},
-    {64, false, 4, 0.31, 0.4, run_linear<64, false, 4>},
-    {128, false, 1, 0.33, 1.5, run_linear<128, false, 1>},
-    {128, false, 2, 0.33, 1.5, run_linear<128, false, 2>},
-    {128, false, 4, 0.33, 1.5, run_linear<128, false, 4>},
-    {256, false, 1, 0.42, 3.7, run_linear<256, false, 1>},
-    {256, true, 1, 0.42, 3.1, run_linear<256, true, 1>},
+    {32, false, 1, 0.285, 0.5, 0.0, 0.0, run_linear<32, false, 1>},
+    {32, false, 2, 0.285, 0.5, 0.0, 1.5, run_linear<32, false, 2>},
+    {32, false, 4, 0.285, 0.5, 0.0, 2.2, run_linear<32, false, 4>},
+    {64, false, 1, 0.290, 0.7, 0.0, 0.0, run_linear<64, false, 1>},
+    {64, false, 2, 0.290, 0.7, 0.0, 1.7, run_linear<64, false, 2>},
+    {64, false, 4, 0.290, 0.7, 0.0, 2.4, run_linear<64, false, 4>},
+    {128, false, 1, 0.280, 1.2, 2.0, 0.0, run_linear<128, false, 1>},
+    {128, false, 2, 0.280, 1.2, 2.0, 2.7, run_linear<128, false, 2>},
+    {128, false, 4, 0.280, 1.2, 2.0, 3.0, run_linear<128, false, 4>},
+    {256, false, 1, 0.320, 2.3, 3.6, 0.0, run_linear<256, false, 1>},
+    {256, true, 1, 0.310, 2.2, 3.7, 0.0, run_linear<256, true, 1>},
 };
 
 // Few tokens take the kernel for them; the others the form that takes the least
@@ -739,9 +740,8 @@ cudaError_t launch_linear(const Operands& op, const LinArgs& args, int sms, cuda
     if (f.split > 1 && (tiles * f.split > 128 || args.nkb < 2 * f.split)) continue;
     const int64_t units = f.pair ? sms / 2 : sms;
     const int64_t rounds = (tiles + units - 1) / units;
-    const double main = static_cast<double>(args.nkb) / f.split * f.step;
-    const double us = rounds * std::max(main, f.drain) + std::min(main, f.drain) +
-                      (f.split > 1 ? 1.7 : 0.0);
+    const double us =
+        rounds * std::max(f.least, f.step * args.nkb / f.split + f.tile) + f.join;
     if (best.run == nullptr || us < least) {
       best = f;
       least = us;
