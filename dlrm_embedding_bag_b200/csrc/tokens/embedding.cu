@@ -128,11 +128,10 @@ __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t by
 constexpr int kZeroBytes = 16 << 10;  // of a bulk store
 
 // Parts part, part + apart, .. (`count` of them) of `parts` of the zeros, by one
-// whole warp. One stretch of bytes goes
-// out as bulk stores of a block of zeros, which one lane issues; it waits where
-// the SM's queue of them is full, so the warp has nothing else to do meanwhile.
-// zeros: kZeroBytes of shared memory, 16-byte aligned, for this alone. The warp
-// has to call fill_done before it ends.
+// whole warp. One stretch of bytes goes out as bulk stores of a block of zeros,
+// which one lane issues; it waits where the SM's queue of them is full, so the
+// warp has nothing else to do meanwhile. zeros: kZeroBytes of shared memory,
+// 16-byte aligned, for this alone. The warp has to call fill_done before it ends.
 __device__ void fill_zeros(const FillArgs& f, int part, int parts, uint8_t* zeros, int count = 1,
                            int apart = 0) {
   const int lane = threadIdx.x & 31;
@@ -612,12 +611,15 @@ cudaError_t allow_smem(K* fn, int bytes, std::atomic<bool> (&prepared)[kMaxDevic
   return e;
 }
 
-// The zeros behind what was launched last (a cluster sort, or nothing of ours).
-cudaError_t run_fill(const FillArgs& f, int blocks, cudaStream_t stream) {
+// The zeros: beside the cluster sort that was launched last (the one before them
+// that they may not wait for), or behind all that is on the stream.
+cudaError_t run_fill(const FillArgs& f, int blocks, bool beside, cudaStream_t stream) {
   static std::atomic<bool> prepared[kMaxDevices];
   const cudaError_t e = allow_smem(&fill_kernel, kFillSmem, prepared);
   if (e != cudaSuccess) return e;
-  return launch_after(&fill_kernel, dim3(blocks), kFillThreads, kFillSmem, stream, f);
+  if (beside) return launch_after(&fill_kernel, dim3(blocks), kFillThreads, kFillSmem, stream, f);
+  fill_kernel<<<blocks, kFillThreads, kFillSmem, stream>>>(f);
+  return cudaGetLastError();
 }
 
 // Zeros that the cluster sort writes itself, 16 bulk stores a CTA; more go to a
@@ -652,7 +654,7 @@ cudaError_t run_cluster_sort(SortArgs& a, int sms, int& n, cudaStream_t stream) 
   ++n;
   if ((e = cudaLaunchKernelEx(&cfg, fn, a)) != cudaSuccess || !beside) return e;
   ++n;
-  return run_fill(fill, std::max(1, sms - kClusterSize), stream);
+  return run_fill(fill, std::max(1, sms - kClusterSize), true, stream);
 }
 
 // Sorts more tokens, two launches a pass, between the two buffers of pairs; the
@@ -1263,7 +1265,7 @@ int dlrm_embedding_grad(const void* grad, int grad_dtype, int64_t ldg, const int
   }
   if (T == 0) {
     if (accumulate) return DLRM_OK;
-    const cudaError_t e = run_fill(fill, sms, s);
+    const cudaError_t e = run_fill(fill, sms, false, s);
     if (e != cudaSuccess) return cuda_fail(e);
     note_launch();
     return DLRM_OK;

@@ -333,6 +333,28 @@ def test_grad_streams_scratch_and_graphs(tokens, T):
         _check_grad(out, grad, ids, N)
 
 
+@pytest.mark.parametrize("T", [0, 40, 3000, 100000])
+def test_grad_waits_for_what_writes_its_output(tokens, T):
+    """A bf16 layer lets the kernel behind it start before it ends: a gradient into
+    the layer's own output still comes after it, and a layer on the gradient after that."""
+    from dlrm_embedding_bag_b200 import mlp
+
+    g = _gen(T + 7)
+    rows, D = 60000, 64
+    a, _ = _matrix(g, rows, 512, BF16)
+    w, _ = _matrix(g, D, 512, BF16)
+    grad, _ = _matrix(g, T, D, F32)
+    ids = torch.from_numpy(_ids(T, T, rows, "skew")).to(DEV)
+    out = torch.empty((rows, D), device=DEV)
+    for _ in range(3):
+        mlp.linear_bf16(a, w, None, "none", out_f32=out)
+        tokens.embedding_grad(grad, ids, rows, out=out)
+        seen = mlp.to_bf16(out)
+        torch.cuda.synchronize()
+        _check_grad(out, grad, ids, rows)
+        assert _same_bits(seen, out.to(BF16))
+
+
 @pytest.mark.parametrize("T", [300, 6000, 90000])
 def test_grads_at_the_same_time(tokens, T):
     """Calls that overlap on four streams, each with the scratch that torch gives it."""
