@@ -1165,7 +1165,9 @@ GradPlan plan_grad(int64_t T, int64_t rows, int64_t D) {
   p.pairs[1] = take(T * 8);
   p.counts = take(static_cast<int64_t>(p.sort_blocks) * kRadix * 4);
   p.part = take(p.nblocks * 2 * p.Dp * 4);
-  p.bytes = at;
+  // the one-launch form (for f32 and accumulating or not, so that the size alone
+  // decides) keeps everything in shared memory
+  p.bytes = T <= kSmallTokens && rows * D <= kSmallZeros / 4 ? 0 : at;
   return p;
 }
 
@@ -1250,7 +1252,7 @@ int dlrm_embedding_grad(const void* grad, int grad_dtype, int64_t ldg, const int
     return DLRM_ERR_ALIGN;
   const GradPlan p = plan_grad(T, rows, D);
   if (scratch_bytes < p.bytes) return DLRM_ERR_SCRATCH;
-  if (T > 0 && scratch == nullptr) return DLRM_ERR_NULL;
+  if (p.bytes > 0 && scratch == nullptr) return DLRM_ERR_NULL;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int rc = clear_status(status_dev, s);
   if (rc != DLRM_OK) return rc;

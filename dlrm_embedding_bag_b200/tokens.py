@@ -15,6 +15,7 @@ its rows may be further apart (a column slice of a wider buffer).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -228,8 +229,9 @@ def embedding_lookup(table: torch.Tensor, ids: torch.Tensor, *, scale: float = 1
     return out
 
 
+@functools.lru_cache(maxsize=256)
 def embedding_grad_scratch_bytes(T: int, rows: int, D: int) -> int:
-    """Bytes of scratch that :func:`embedding_grad` needs for ``T`` ids."""
+    """Bytes of scratch that :func:`embedding_grad` needs for ``T`` ids (may be 0)."""
     n = _scratch_bytes(T, rows, D)
     if n < 0:
         raise TokensError(n, "dlrm_embedding_grad_scratch_bytes")
@@ -264,6 +266,7 @@ def embedding_grad(grad: torch.Tensor, ids: torch.Tensor, num_rows: int, *, L: i
     T = ids.numel()
     if L < 1 or T % L != 0 or n != T // L:
         raise ValueError(f"grad must have ids.numel() / L = {T} / {L} rows (got {n})")
+    room = embedding_grad_scratch_bytes(T, num_rows, D)  # refuses what the sizes rule out
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
@@ -271,8 +274,6 @@ def embedding_grad(grad: torch.Tensor, ids: torch.Tensor, num_rows: int, *, L: i
         od, ldo = ops.TABLE_DTYPES.get(dtype), D
         if od is None:
             raise TypeError(f"dtype must be float32 or bfloat16 (got {dtype})")
-        if num_rows < 1:
-            raise ValueError(f"num_rows must be at least 1 (got {num_rows})")
         out = _empty(num_rows, D, dtype, index)
     else:
         _, od, out_rows, out_cols, ldo = _matrix(out, "out", index)
@@ -280,12 +281,11 @@ def embedding_grad(grad: torch.Tensor, ids: torch.Tensor, num_rows: int, *, L: i
             raise TypeError(f"out must be {dtype} (got {out.dtype})")
         if out_rows != num_rows or out_cols != D:
             raise ValueError(f"out must be ({num_rows}, {D}) (got {tuple(out.shape)})")
-    room = _scratch_bytes(T, num_rows, D)
-    if room < 0:
-        raise TokensError(room, "dlrm_embedding_grad")
+    ps = None
     if scratch is None:
-        scratch = _empty_vector(room, torch.uint8, index)
-        ps = scratch.data_ptr()
+        if room:
+            scratch = _empty_vector(room, torch.uint8, index)
+            ps = scratch.data_ptr()
     else:
         ps, room = _flat(scratch, "scratch", torch.uint8, index), scratch.numel()
     _call(_grad, "dlrm_embedding_grad", index,

@@ -55,7 +55,8 @@ DLRM_API int dlrm_embedding_lookup(const void* table, int table_dtype, int64_t l
                                    int64_t padding_idx, void* out, int out_dtype, int64_t ldo,
                                    int32_t* status_dev, dlrm_stream_t stream);
 
-/* Bytes of scratch that dlrm_embedding_grad needs for these sizes (a multiple
+/* Bytes of scratch that dlrm_embedding_grad needs for these sizes (0 for few
+ * tokens into a small table, else a multiple
  * of 16), or a negative dlrm_status_t for sizes that it refuses. */
 DLRM_API int64_t dlrm_embedding_grad_scratch_bytes(int64_t T, int64_t rows, int64_t D);
 
@@ -78,7 +79,8 @@ DLRM_API int64_t dlrm_embedding_grad_scratch_bytes(int64_t T, int64_t rows, int6
  *               and out the table itself: one sparse SGD step).
  *   scratch     dev, 16-byte aligned, of at least
  *               dlrm_embedding_grad_scratch_bytes(T, rows, D) bytes
- *               (DLRM_ERR_SCRATCH otherwise); its contents need not be set. Calls
+ *               (DLRM_ERR_SCRATCH otherwise; NULL if that is 0); its contents
+ *               need not be set. Calls
  *               whose work overlaps on the GPU must not share it.
  *   status_dev  as for dlrm_embedding_lookup; an id outside [0, rows) adds
  *               nothing.

@@ -432,7 +432,10 @@ def test_grad_refusals(tokens):
     with pytest.raises(TypeError, match="float32 or bfloat16"):
         tokens.embedding_grad(grad.half(), ids, 4)
     with pytest.raises(tokens.TokensError, match="DLRM_ERR_SCRATCH"):
-        tokens.embedding_grad(grad, ids, 4, scratch=torch.empty(16, dtype=torch.uint8, device=DEV))
+        tokens.embedding_grad(grad.repeat(200, 1), ids.repeat(200), 4,
+                              scratch=torch.empty(16, dtype=torch.uint8, device=DEV))
+    with pytest.raises(tokens.TokensError, match="DLRM_ERR_SHAPE"):
+        tokens.embedding_grad(grad, ids, 2 ** 31, out=None, accumulate=False)
     with pytest.raises(ValueError, match="out must be"):
         tokens.embedding_grad(grad, ids, 4, out=torch.zeros((5, 8), device=DEV))
     with pytest.raises(ValueError, match="unit column stride"):

@@ -90,7 +90,7 @@ def test_lookup_refusals(tokens):
 
 
 def test_grad_refusals(tokens):
-    def call(grad=A, gd=0, ldg=8, ids=W, T=4, L=1, rows=10, D=8, pad=-1, out=Y, od=0, ldo=8,
+    def call(grad=A, gd=0, ldg=8, ids=W, T=602, L=1, rows=10, D=8, pad=-1, out=Y, od=0, ldo=8,
              scratch=S, room=1 << 30, st=None):
         return tokens._lib.dlrm_embedding_grad(grad, gd, ldg, ids, T, L, rows, D, 1.0, pad, out,
                                                od, ldo, 0, scratch, room, st, None)
@@ -98,14 +98,14 @@ def test_grad_refusals(tokens):
     for kw in (dict(grad=None), dict(ids=None), dict(out=None), dict(scratch=None)):
         assert call(**kw) == NULL, kw
     for kw in (dict(rows=0), dict(rows=BIG - 1), dict(D=0), dict(T=-1), dict(T=BIG), dict(ldg=7),
-               dict(ldo=7), dict(L=0), dict(L=3)):
+               dict(ldo=7), dict(L=0), dict(L=3), dict(L=-1)):
         assert call(**kw) == SHAPE, kw
     for kw in (dict(gd=2), dict(od=-1), dict(pad=-2), dict(pad=10)):
         assert call(**kw) == ARG, kw
     for kw in (dict(grad=A + 2), dict(out=Y + 2), dict(ids=W + 2), dict(st=S + 2),
                dict(scratch=S + 8)):
         assert call(**kw) == ALIGN, kw
-    need = tokens.embedding_grad_scratch_bytes(4, 10, 8)
+    need = tokens.embedding_grad_scratch_bytes(602, 10, 8)
     assert need > 0 and need % 16 == 0
     assert call(room=need - 1) == SCRATCH
     assert tokens.launch_count() == 0
@@ -114,7 +114,10 @@ def test_grad_refusals(tokens):
 def test_scratch_sizes(tokens):
     small = tokens.embedding_grad_scratch_bytes(1000, 5000, 64)
     assert small >= 1000 * 8
-    assert tokens.embedding_grad_scratch_bytes(0, 1, 1) >= 0
+    assert tokens.embedding_grad_scratch_bytes(0, 1, 1) == 0
+    assert tokens.embedding_grad_scratch_bytes(512, 1000, 64) == 0
+    assert tokens.embedding_grad_scratch_bytes(512, 1 << 20, 64) > 512 * 8
+    assert tokens.embedding_grad_scratch_bytes(513, 1000, 64) > 513 * 8
     # the largest token list: its size does not leave 64 bits
     assert tokens.embedding_grad_scratch_bytes(BIG - 1, BIG - 2, 4096) > (BIG - 1) * 8
     for bad in ((-1, 5, 5), (BIG, 5, 5), (5, 0, 5), (5, BIG - 1, 5), (5, 5, 0)):
