@@ -87,8 +87,8 @@ cudaError_t run_lookup(LookupArgs a, cudaStream_t stream) {
   const int64_t units = (static_cast<int64_t>(a.T) + kRowsInFlight - 1) / kRowsInFlight * a.windows;
   const int64_t blocks = (units * G + kLookupThreads - 1) / kLookupThreads;
   if (blocks > INT_MAX) return cudaErrorInvalidValue;
-  lookup_kernel<In, Out, VEC, G><<<static_cast<unsigned>(blocks), kLookupThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch(&lookup_kernel<In, Out, VEC, G>, dim3(static_cast<unsigned>(blocks)),
+                kLookupThreads, 0, false, stream, a);
 }
 
 template <class In, class Out>
@@ -580,23 +580,6 @@ __global__ void __launch_bounds__(kClusterThreads, 1) sort_cluster_kernel(const 
   if (a.fill.out != nullptr && warp == 0) fill_done();
 }
 
-// A kernel that may be scheduled while the one before it is at work.
-template <class... P, class... A>
-cudaError_t launch_after(void (*fn)(P...), dim3 grid, int threads, int smem,
-                         cudaStream_t stream, const A&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, fn, args...);
-}
-
 // A kernel's dynamic shared memory, set once per device (`prepared` is its own).
 template <class K>
 cudaError_t allow_smem(K* fn, int bytes, std::atomic<bool> (&prepared)[kMaxDevices]) {
@@ -617,9 +600,7 @@ cudaError_t run_fill(const FillArgs& f, int blocks, bool beside, cudaStream_t st
   static std::atomic<bool> prepared[kMaxDevices];
   const cudaError_t e = allow_smem(&fill_kernel, kFillSmem, prepared);
   if (e != cudaSuccess) return e;
-  if (beside) return launch_after(&fill_kernel, dim3(blocks), kFillThreads, kFillSmem, stream, f);
-  fill_kernel<<<blocks, kFillThreads, kFillSmem, stream>>>(f);
-  return cudaGetLastError();
+  return launch(&fill_kernel, dim3(blocks), kFillThreads, kFillSmem, beside, stream, f);
 }
 
 // Zeros that the cluster sort writes itself, 16 bulk stores a CTA; more go to a
@@ -675,15 +656,10 @@ cudaError_t run_grid_sort(SortArgs& a, uint2* const (&pairs)[2], cudaStream_t st
     a.shift = i * a.bits;
     a.fill_part = kPassParts * i * grid;
     // the first launch waits for all that came before it on the stream
-    if (i == 0) {
-      sort_count_kernel<<<grid, threads, 0, stream>>>(a);
-      e = cudaGetLastError();
-    } else {
-      e = launch_after(&sort_count_kernel, dim3(grid), threads, 0, stream, a);
-    }
-    if (e != cudaSuccess) return e;
+    if ((e = launch(&sort_count_kernel, dim3(grid), threads, 0, i > 0, stream, a)) != cudaSuccess)
+      return e;
     a.fill_part += grid;
-    if ((e = launch_after(move, dim3(grid), threads, smem, stream, a)) != cudaSuccess) return e;
+    if ((e = launch(move, dim3(grid), threads, smem, true, stream, a)) != cudaSuccess) return e;
     a.ids = nullptr;
     a.in = a.out;
   }
@@ -1072,14 +1048,14 @@ struct SumLaunch {
     a.nblocks = static_cast<int>((static_cast<int64_t>(a.T) + a.per_block - 1) / a.per_block);
     const int64_t blocks = static_cast<int64_t>(a.nblocks) * a.windows;
     if (blocks > INT_MAX) return cudaErrorInvalidValue;
-    cudaError_t e = launch_after(
-        a.nblocks > 1 ? &sum_kernel<In, VEC, G, true> : &sum_kernel<In, VEC, G, false>,
-        dim3(static_cast<unsigned>(blocks)), kSumThreads, 0, stream, a);
+    cudaError_t e =
+        launch(a.nblocks > 1 ? &sum_kernel<In, VEC, G, true> : &sum_kernel<In, VEC, G, false>,
+               dim3(static_cast<unsigned>(blocks)), kSumThreads, 0, true, stream, a);
     if (e != cudaSuccess) return e;
     ++n;
     if (a.nblocks > 1) {
       const dim3 grid(a.nblocks - 1, (a.D + kJoinCols - 1) / kJoinCols);
-      e = launch_after(&join_kernel, grid, kJoinWarps * 32, 0, stream, a);
+      e = launch(&join_kernel, grid, kJoinWarps * 32, 0, true, stream, a);
       ++n;
     }
     return e;
@@ -1099,8 +1075,8 @@ struct SmallLaunch {
     int64_t blocks = static_cast<int64_t>(a.parts) * a.sum.windows;
     if (a.fill.out != nullptr)
       blocks = std::max(blocks, std::min<int64_t>(592, a.fill.rows * a.fill.row_bytes / (32 << 10)));
-    small_kernel<In, VEC, G><<<static_cast<unsigned>(blocks), kSumThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch(&small_kernel<In, VEC, G>, dim3(static_cast<unsigned>(blocks)), kSumThreads, 0,
+                  false, stream, a);
   }
 };
 

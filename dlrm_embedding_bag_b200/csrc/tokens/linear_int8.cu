@@ -682,16 +682,8 @@ template <int MT, int R>
 cudaError_t run_few(const Operands& op, const LinArgs& args, cudaStream_t stream) {
   const VecArgs a = {args, op.x, op.w, op.ldx, op.ldw, static_cast<int>(op.K)};
   constexpr int kChannels = kVecThreads / 32 * R;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((args.N + kChannels - 1) / kChannels);
-  cfg.blockDim = dim3(kVecThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, &linear_few_kernel<MT, R>, a);
+  return launch(&linear_few_kernel<MT, R>, dim3((args.N + kChannels - 1) / kChannels), kVecThreads,
+                0, true, stream, a);
 }
 
 // The forms of the tensor-core kernel, with what they take on a B200 in us: a K

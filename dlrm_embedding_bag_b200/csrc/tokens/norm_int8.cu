@@ -290,17 +290,16 @@ __global__ void __launch_bounds__(kNormThreads) norm_loop_kernel(const NormArgs 
 template <class T, int VEC>
 cudaError_t run_loop(const NormArgs& a, cudaStream_t stream) {
   const int64_t blocks = std::min<int64_t>(a.M, 148 * 64);
-  norm_loop_kernel<T, VEC><<<static_cast<unsigned>(blocks), kNormThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch(&norm_loop_kernel<T, VEC>, dim3(static_cast<unsigned>(blocks)), kNormThreads, 0,
+                false, stream, a);
 }
 
 template <class T, int TPR, int CH>
 cudaError_t run_row(const NormArgs& a, cudaStream_t stream) {
   constexpr int kThreads = TPR < 128 ? 128 : TPR, kRows = kThreads / TPR;
   const int64_t blocks = (static_cast<int64_t>(a.M) + kRows - 1) / kRows;
-  norm_row_kernel<T, kVecOf<T>, TPR, CH>
-      <<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch(&norm_row_kernel<T, kVecOf<T>, TPR, CH>, dim3(static_cast<unsigned>(blocks)),
+                kThreads, 0, false, stream, a);
 }
 
 // Four chunks a thread where rows are many (a row's loads all in flight, many
@@ -381,13 +380,8 @@ cudaError_t run_dequant(const int8_t* q, int64_t ldq, const float* scale, int64_
   const bool vec = K % 16 == 0 && is_aligned(q, 16) && ldq % 16 == 0 && rows16(y, ldy, sizeof(T));
   const int64_t per_row = vec ? K / 16 : K;
   const int threads = static_cast<int>(std::min<int64_t>(256, (per_row + 31) / 32 * 32));
-  if (vec)
-    dequant_kernel<T, 16><<<blocks, threads, 0, stream>>>(q, ldq, scale, static_cast<int>(M),
-                                                          static_cast<int>(K), y, ldy);
-  else
-    dequant_kernel<T, 1><<<blocks, threads, 0, stream>>>(q, ldq, scale, static_cast<int>(M),
-                                                         static_cast<int>(K), y, ldy);
-  return cudaGetLastError();
+  return launch(vec ? &dequant_kernel<T, 16> : &dequant_kernel<T, 1>, dim3(blocks), threads, 0,
+                false, stream, q, ldq, scale, static_cast<int>(M), static_cast<int>(K), y, ldy);
 }
 
 }  // namespace
