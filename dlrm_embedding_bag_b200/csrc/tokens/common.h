@@ -48,16 +48,18 @@ inline bool is_aligned(const void* p, uintptr_t a) {
 }
 inline bool known_dtype(int d) { return d == DLRM_TABLE_F32 || d == DLRM_TABLE_BF16; }
 inline int dtype_size(int d) { return d == DLRM_TABLE_BF16 ? 2 : 4; }
-// Rows that 128-bit accesses can walk: base and pitch are whole 16-byte units.
-inline bool rows16(const void* p, int64_t ld, int elem) {
-  return is_aligned(p, 16) && (ld * elem) % 16 == 0;
+// Rows of `cols` columns that accesses of v elements (16 bytes at most each) can
+// walk: base, pitch and length are whole multiples of them.
+inline bool rows_by(const void* p, int64_t ld, int elem, int v) {
+  const int bytes = v * elem < 16 ? v * elem : 16;
+  return is_aligned(p, bytes) && ld % v == 0;
 }
 
 // Elements of one 128-bit access.
 template <class T>
 constexpr int kVecOf = 16 / static_cast<int>(sizeof(T));
 
-// VEC elements as they lie in memory: one (VEC 1) or a whole 128-bit access.
+// VEC elements as they lie in memory: one, a pair, or a whole 128-bit access.
 template <class T, int VEC>
 struct RawOf {
   using type = uint4;
@@ -67,6 +69,14 @@ template <class T>
 struct RawOf<T, 1> {
   using type = T;
 };
+template <>
+struct RawOf<float, 2> {
+  using type = uint2;
+};
+template <>
+struct RawOf<__nv_bfloat16, 2> {
+  using type = uint32_t;
+};
 template <class T, int VEC>
 using Raw = typename RawOf<T, VEC>::type;
 
@@ -75,6 +85,12 @@ template <class T, int VEC>
 __device__ __forceinline__ void widen(const Raw<T, VEC>& r, float (&v)[VEC]) {
   if constexpr (VEC == 1) {
     v[0] = static_cast<float>(r);
+  } else if constexpr (VEC == 2 && sizeof(T) == 4) {
+    v[0] = __uint_as_float(r.x);
+    v[1] = __uint_as_float(r.y);
+  } else if constexpr (VEC == 2) {
+    v[0] = __uint_as_float(r << 16);
+    v[1] = __uint_as_float(r & 0xffff0000u);
   } else {
     const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -99,45 +115,37 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
          (static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(hi))) << 16);
 }
 
-// VEC values rounded to T (nearest even) at p; VEC > 1: p is aligned to
-// min(16, VEC * sizeof(T)) bytes.
-template <class T, int VEC>
+// VEC values rounded to T (nearest even) at p, aligned to min(16, VEC *
+// sizeof(T)) bytes. ONCE: nobody reads them soon; they leave L2 first, before what
+// is read again.
+template <class T, int VEC, bool ONCE = false>
 __device__ __forceinline__ void store_f32(T* p, const float (&v)[VEC]) {
+  auto put = [](auto* at, auto value) {
+    if constexpr (ONCE)
+      __stcs(at, value);
+    else
+      *at = value;
+  };
   if constexpr (VEC == 1) {
     if constexpr (sizeof(T) == 4)
-      *p = v[0];
+      put(p, v[0]);
     else
-      *p = __float2bfloat16_rn(v[0]);
+      put(reinterpret_cast<unsigned short*>(p), __bfloat16_as_ushort(__float2bfloat16_rn(v[0])));
+  } else if constexpr (VEC == 2) {
+    if constexpr (sizeof(T) == 4)
+      put(reinterpret_cast<float2*>(p), make_float2(v[0], v[1]));
+    else
+      put(reinterpret_cast<unsigned int*>(p), bf16x2_bits(v[0], v[1]));
   } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
     for (int i = 0; i < VEC; i += 4)
-      *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+      put(reinterpret_cast<float4*>(p + i), make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
   } else if constexpr (VEC == 4) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]));
+    put(reinterpret_cast<uint2*>(p), make_uint2(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3])));
   } else {
     static_assert(VEC == 8, "one 128-bit store");
-    *reinterpret_cast<uint4*>(p) = make_uint4(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]),
-                                              bf16x2_bits(v[4], v[5]), bf16x2_bits(v[6], v[7]));
-  }
-}
-
-// The same, for values that nobody reads soon: they leave L2 first, before what
-// is read again.
-template <class T, int VEC>
-__device__ __forceinline__ void store_f32_once(T* p, const float (&v)[VEC]) {
-  if constexpr (VEC == 1) {
-    store_f32<T, 1>(p, v);
-  } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-    for (int i = 0; i < VEC; i += 4)
-      __stcs(reinterpret_cast<float4*>(p + i), make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]));
-  } else if constexpr (VEC == 4) {
-    __stcs(reinterpret_cast<uint2*>(p),
-           make_uint2(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3])));
-  } else {
-    __stcs(reinterpret_cast<uint4*>(p),
-           make_uint4(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]),
-                      bf16x2_bits(v[4], v[5]), bf16x2_bits(v[6], v[7])));
+    put(reinterpret_cast<uint4*>(p), make_uint4(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]),
+                                                bf16x2_bits(v[4], v[5]), bf16x2_bits(v[6], v[7])));
   }
 }
 

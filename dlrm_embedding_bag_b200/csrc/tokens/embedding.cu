@@ -42,14 +42,14 @@ struct LookupArgs {
   int32_t* status;
 };
 
-template <class In, class Out, int VEC, int G>
+template <class In, class Out, int VEC, int G, int E>
 __global__ void __launch_bounds__(kLookupThreads) lookup_kernel(const LookupArgs a) {
   const In* W = static_cast<const In*>(a.table);
   Out* Y = static_cast<Out*>(a.out);
   const int q = threadIdx.x % G;
   const int64_t unit = (static_cast<int64_t>(blockIdx.x) * kLookupThreads + threadIdx.x) / G;
   const int64_t t0 = unit / a.windows * kRowsInFlight;
-  const int c = (static_cast<int>(unit % a.windows) * G + q) * VEC;
+  const int c0 = (static_cast<int>(unit % a.windows) * G * E + q) * VEC;
   int id[kRowsInFlight];
 #pragma unroll
   for (int u = 0; u < kRowsInFlight; ++u) {
@@ -61,46 +61,85 @@ __global__ void __launch_bounds__(kLookupThreads) lookup_kernel(const LookupArgs
       id[u] = (in && r != a.pad) ? r : a.rows;  // `rows`: a row of zeros
     }
   }
-  if (c >= a.D) return;
-  Raw<In, VEC> raw[kRowsInFlight];
+  Raw<In, VEC> raw[kRowsInFlight][E];
 #pragma unroll
   for (int u = 0; u < kRowsInFlight; ++u) {
-    raw[u] = Raw<In, VEC>();
-    if (id[u] >= 0 && id[u] < a.rows)
-      raw[u] = __ldg(reinterpret_cast<const Raw<In, VEC>*>(W + static_cast<int64_t>(id[u]) * a.ldw + c));
+    const In* row = W + static_cast<int64_t>(id[u]) * a.ldw + c0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      raw[u][e] = Raw<In, VEC>();
+      if (id[u] >= 0 && id[u] < a.rows && c0 + e * G * VEC < a.D)
+        raw[u][e] = __ldg(reinterpret_cast<const Raw<In, VEC>*>(row + e * G * VEC));
+    }
   }
 #pragma unroll
   for (int u = 0; u < kRowsInFlight; ++u) {
-    if (id[u] >= 0) {
-      float v[VEC];
-      widen<In, VEC>(raw[u], v);
+    Out* row = Y + (t0 + u) * a.ldo + c0;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) v[e] = id[u] < a.rows ? v[e] * a.scale : 0.f;
-      store_f32_once<Out, VEC>(Y + (t0 + u) * a.ldo + c, v);
+    for (int e = 0; e < E; ++e) {
+      float v[VEC];
+      widen<In, VEC>(raw[u][e], v);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) v[k] = id[u] < a.rows ? v[k] * a.scale : 0.f;
+      if (id[u] >= 0 && c0 + e * G * VEC < a.D)
+        store_f32<Out, VEC, true>(row + e * G * VEC, v);
     }
   }
 }
 
-template <class In, class Out, int VEC, int G>
-cudaError_t run_lookup(LookupArgs a, cudaStream_t stream) {
-  a.windows = (a.D + G * VEC - 1) / (G * VEC);
-  const int64_t units = (static_cast<int64_t>(a.T) + kRowsInFlight - 1) / kRowsInFlight * a.windows;
-  const int64_t blocks = (units * G + kLookupThreads - 1) / kLookupThreads;
-  if (blocks > INT_MAX) return cudaErrorInvalidValue;
-  return launch(&lookup_kernel<In, Out, VEC, G>, dim3(static_cast<unsigned>(blocks)),
-                kLookupThreads, 0, false, stream, a);
+// The lanes of a group, and the accesses of a lane (E of them, G apart), by the
+// row's length: 128-bit accesses where rows allow them, else pairs, else single
+// elements, four a lane where the row is longer than a warp.
+template <class In, class F>
+cudaError_t by_shape(int D, int vec, F& f) {
+  constexpr int V = kVecOf<In>;
+  const int chunks = D / vec;
+  if (vec == V) {
+    if (chunks <= 4) return f.template run<In, V, 4, 1>();
+    if (chunks <= 8) return f.template run<In, V, 8, 1>();
+    if (chunks <= 16) return f.template run<In, V, 16, 1>();
+    return f.template run<In, V, 32, 1>();
+  }
+  if (vec == 2) {
+    if (chunks <= 16) return f.template run<In, 2, 16, 1>();
+    if (chunks <= 32) return f.template run<In, 2, 32, 1>();
+    return f.template run<In, 2, 32, 4>();
+  }
+  if (chunks <= 16) return f.template run<In, 1, 16, 1>();
+  if (chunks <= 32) return f.template run<In, 1, 32, 1>();
+  return f.template run<In, 1, 32, 4>();
 }
 
-template <class In, class Out>
-cudaError_t run_lookup_shape(const LookupArgs& a, bool vec, cudaStream_t stream) {
-  constexpr int V = kVecOf<In>;
-  if (!vec) return run_lookup<In, Out, 1, 32>(a, stream);
-  const int chunks = a.D / V;
-  if (chunks <= 4) return run_lookup<In, Out, V, 4>(a, stream);
-  if (chunks <= 8) return run_lookup<In, Out, V, 8>(a, stream);
-  if (chunks <= 16) return run_lookup<In, Out, V, 16>(a, stream);
-  return run_lookup<In, Out, V, 32>(a, stream);
+template <class F>
+cudaError_t by_type(int dtype, int D, int vec, F& f) {
+  return dtype == DLRM_TABLE_F32 ? by_shape<float>(D, vec, f)
+                                 : by_shape<__nv_bfloat16>(D, vec, f);
 }
+
+// Elements of an access that both matrices' rows allow.
+int common_vec(const void* in, int64_t ldi, int in_size, const void* out, int64_t ldo,
+               int out_size, int64_t D) {
+  for (int v : {16 / in_size, 2})
+    if (D % v == 0 && rows_by(in, ldi, in_size, v) && rows_by(out, ldo, out_size, v)) return v;
+  return 1;
+}
+
+template <class Out>
+struct LookupLaunch {
+  LookupArgs a;
+  cudaStream_t stream;
+  template <class In, int VEC, int G, int E>
+  cudaError_t run() {
+    constexpr int kWindow = G * E * VEC;
+    a.windows = (a.D + kWindow - 1) / kWindow;
+    const int64_t units =
+        (static_cast<int64_t>(a.T) + kRowsInFlight - 1) / kRowsInFlight * a.windows;
+    const int64_t blocks = (units * G + kLookupThreads - 1) / kLookupThreads;
+    if (blocks > INT_MAX) return cudaErrorInvalidValue;
+    return launch(&lookup_kernel<In, Out, VEC, G, E>, dim3(static_cast<unsigned>(blocks)),
+                  kLookupThreads, 0, false, stream, a);
+  }
+};
 
 // ---------------------------------------------------------------------------
 // Gradient: zeros for the rows that no token names.
@@ -722,28 +761,27 @@ __device__ __forceinline__ void put_row(const SumArgs& a, uint32_t row, int c,
   }
 }
 
-template <int VEC, int G>
+template <int VEC, int G, int E>
 struct alignas(16) SumSmem {
   static constexpr int kGroups = kSumThreads / G;
-  float head[kGroups][G * VEC];  // a group's part of a run that began before it
+  float head[kGroups][E][G * VEC];  // a group's part of a run that began before it
   uint32_t first[kGroups], last[kGroups];
 };
 
 // The block's sums over the sorted tokens [lo, hi), `chunk` of them a group (a
 // multiple of kSumInFlight), for window `window` of the columns. part: this
 // block's two rows for the runs that cross [lo, hi), or null if none does.
-template <class In, int VEC, int G>
-__device__ __forceinline__ void sum_block(const SumArgs& a, SumSmem<VEC, G>& sm,
+template <class In, int VEC, int G, int E>
+__device__ __forceinline__ void sum_block(const SumArgs& a, SumSmem<VEC, G, E>& sm,
                                           const uint2* sorted, int64_t lo, int64_t hi, int chunk,
                                           int window, float* part) {
-  constexpr int NG = SumSmem<VEC, G>::kGroups;
+  constexpr int NG = SumSmem<VEC, G, E>::kGroups;
   constexpr int U = G < kSumInFlight ? G : kSumInFlight;
-  auto& head = sm.head;
   auto& first = sm.first;
   auto& last = sm.last;
   const int q = threadIdx.x % G, g = threadIdx.x / G, base = (threadIdx.x & 31) / G * G;
-  const int c = (window * G + q) * VEC;
-  const bool cols = c < a.D;
+  const int c0 = (window * G * E + q) * VEC;  // the lane's columns: c0 + e * G * VEC ..
+  auto live = [&](int e) { return c0 + e * G * VEC < a.D; };
   const int64_t begin = lo + static_cast<int64_t>(g) * chunk;
   const int n = static_cast<int>(max(int64_t{0}, min(static_cast<int64_t>(chunk), hi - begin)));
   const In* grad = static_cast<const In*>(a.grad);
@@ -754,9 +792,34 @@ __device__ __forceinline__ void sum_block(const SumArgs& a, SumSmem<VEC, G>& sm,
     first[g] = n > 0 ? sorted[begin].x : none;
     last[g] = n > 0 ? sorted[begin + n - 1].x : none;
   }
-  float acc[VEC];
+  float acc[E][VEC];
+  auto clear = [&] {
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+    for (int e = 0; e < E; ++e)
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) acc[e][k] = 0.f;
+  };
+  auto keep_head = [&] {
+#pragma unroll
+    for (int e = 0; e < E; ++e) store_f32<float, VEC>(&sm.head[g][e][q * VEC], acc[e]);
+  };
+  auto add_head = [&](int j) {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) acc[e][k] += sm.head[j][e][q * VEC + k];
+  };
+  auto put_rows = [&](uint32_t row) {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (live(e)) put_row<VEC>(a, row, c0 + e * G * VEC, acc[e]);
+  };
+  auto put_part = [&](float* to) {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (live(e)) store_f32<float, VEC>(to + c0 + e * G * VEC, acc[e]);
+  };
+  clear();
   uint32_t cur = none;  // key of the run being summed; none before the first
   bool inside = false;  // it began in this chunk
   // every lane of the warp takes the same number of steps: shuffles span it
@@ -769,15 +832,19 @@ __device__ __forceinline__ void sum_block(const SumArgs& a, SumSmem<VEC, G>& sm,
     }
     const int steps = min(G, chunk - j0);
     for (int u0 = 0; u0 < steps; u0 += U) {
-      Raw<In, VEC> raw[U];
+      Raw<In, VEC> raw[U][E];
       uint32_t k[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         k[u] = __shfl_sync(kFull, key, base + u0 + u);
         const uint32_t r = __shfl_sync(kFull, row, base + u0 + u);
-        raw[u] = Raw<In, VEC>();
-        if (k[u] != none && cols)
-          raw[u] = *reinterpret_cast<const Raw<In, VEC>*>(grad + static_cast<int64_t>(r) * a.ldg + c);
+        const In* from = grad + static_cast<int64_t>(r) * a.ldg + c0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          raw[u][e] = Raw<In, VEC>();
+          if (k[u] != none && live(e))
+            raw[u][e] = *reinterpret_cast<const Raw<In, VEC>*>(from + e * G * VEC);
+        }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -785,28 +852,30 @@ __device__ __forceinline__ void sum_block(const SumArgs& a, SumSmem<VEC, G>& sm,
           // the run before this token ends here
           if (cur != none) {
             if (!inside)
-              store_f32<float, VEC>(&head[g][q * VEC], acc);
-            else if (cols)
-              put_row<VEC>(a, cur, c, acc);
+              keep_head();
+            else
+              put_rows(cur);
           }
           inside = k[u] != left || j0 + u0 + u > 0;
           cur = k[u];
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+          clear();
         }
-        float v[VEC];
-        widen<In, VEC>(raw[u], v);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) acc[e] += v[e];
+        for (int e = 0; e < E; ++e) {
+          float v[VEC];
+          widen<In, VEC>(raw[u][e], v);
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) acc[e][i] += v[i];
+        }
       }
     }
   }
   const bool out_right = cur != none && cur == right;  // the last run goes on
   if (cur != none) {
     if (!inside)
-      store_f32<float, VEC>(&head[g][q * VEC], acc);
-    else if (!out_right && cols)
-      put_row<VEC>(a, cur, c, acc);
+      keep_head();
+    else if (!out_right)
+      put_rows(cur);
   }
   // the last group's lanes alone know whether the block's last run goes on
   const bool block_goes_on = __syncthreads_or(g == NG - 1 && out_right);
@@ -817,42 +886,35 @@ __device__ __forceinline__ void sum_block(const SumArgs& a, SumSmem<VEC, G>& sm,
   if (inside && out_right) {
     // a run that begins in this group: its parts to the right
     bool open = true;
-    int j = g + 1;
-    for (; j < NG && open; ++j) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) acc[e] += head[j][q * VEC + e];
+    for (int j = g + 1; j < NG && open; ++j) {
+      add_head(j);
       open = one_run(j);
     }
-    if (cols) {
-      if (open)
-        store_f32<float, VEC>(part + a.Dp + c, acc);
-      else
-        put_row<VEC>(a, cur, c, acc);
-    }
+    if (open)
+      put_part(part + a.Dp);
+    else
+      put_rows(cur);
   }
   if (g == 0 && n > 0 && first[0] != none && first[0] == left) {
     // the run that came in from the block before
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) acc[e] = head[0][q * VEC + e];
-    for (int j = 0; j + 1 < NG && one_run(j); ++j) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) acc[e] += head[j + 1][q * VEC + e];
-    }
-    if (cols) store_f32<float, VEC>(part + c, acc);
+    clear();
+    add_head(0);
+    for (int j = 0; j + 1 < NG && one_run(j); ++j) add_head(j + 1);
+    put_part(part);
   }
 }
 
 // JOIN: the join kernel follows, and may be scheduled early (it waits before it
 // reads anything; what else may follow is not known to).
-template <class In, int VEC, int G, bool JOIN>
-__global__ void __launch_bounds__(kSumThreads, sizeof(In) == 2 && VEC > 1 ? 4 : 3)
+template <class In, int VEC, int G, int E, bool JOIN>
+__global__ void __launch_bounds__(kSumThreads, sizeof(In) == 2 && VEC > 2 ? 4 : 3)
     sum_kernel(const SumArgs a) {
-  __shared__ SumSmem<VEC, G> sm;
+  __shared__ SumSmem<VEC, G, E> sm;
   if constexpr (JOIN) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the sort (and the zeros) are done
   const int block = blockIdx.x / a.windows;
   const int64_t lo = static_cast<int64_t>(block) * a.per_block;
-  sum_block<In, VEC, G>(a, sm, a.sorted, lo, min(lo + a.per_block, static_cast<int64_t>(a.T)),
+  sum_block<In, VEC, G, E>(a, sm, a.sorted, lo, min(lo + a.per_block, static_cast<int64_t>(a.T)),
                         a.chunk, blockIdx.x % a.windows,
                         a.part + static_cast<int64_t>(block) * 2 * a.Dp);
 }
@@ -982,9 +1044,9 @@ __device__ void fill_unnamed(const FillArgs& f, const uint32_t* keys, int T, int
   }
 }
 
-template <class In, int VEC, int G>
+template <class In, int VEC, int G, int E>
 __global__ void __launch_bounds__(kSumThreads) small_kernel(const SmallArgs a) {
-  __shared__ SumSmem<VEC, G> sm;
+  __shared__ SumSmem<VEC, G, E> sm;
   __shared__ __align__(16) uint32_t keys[kSmallTokens];
   __shared__ uint2 sorted[kSmallTokens];
   __shared__ uint32_t map[kMapWords];
@@ -1027,10 +1089,12 @@ __global__ void __launch_bounds__(kSumThreads) small_kernel(const SmallArgs a) {
         if (i >= to) atomicMin(&hi, i);
       }
     __syncthreads();
-    const int per = (hi - lo + SumSmem<VEC, G>::kGroups - 1) / SumSmem<VEC, G>::kGroups;
+    constexpr int kGroups = SumSmem<VEC, G, E>::kGroups;
+    const int per = (hi - lo + kGroups - 1) / kGroups;
     const int chunk = (per + kSumInFlight - 1) / kSumInFlight * kSumInFlight;
     if (hi > lo)
-      sum_block<In, VEC, G>(a.sum, sm, sorted, lo, hi, chunk, blockIdx.x % a.sum.windows, nullptr);
+      sum_block<In, VEC, G, E>(a.sum, sm, sorted, lo, hi, chunk, blockIdx.x % a.sum.windows,
+                               nullptr);
   }
   if (a.fill.out != nullptr)
     fill_unnamed(a.fill, keys, T, a.elem, blockIdx.x, gridDim.x, map);
@@ -1041,15 +1105,16 @@ struct SumLaunch {
   SumArgs a;
   int n;
   cudaStream_t stream;
-  template <class In, int VEC, int G>
+  template <class In, int VEC, int G, int E>
   cudaError_t run() {
-    a.windows = (a.D + G * VEC - 1) / (G * VEC);
+    constexpr int kWindow = G * E * VEC;
+    a.windows = (a.D + kWindow - 1) / kWindow;
     a.per_block = a.chunk * (kSumThreads / G);
     a.nblocks = static_cast<int>((static_cast<int64_t>(a.T) + a.per_block - 1) / a.per_block);
     const int64_t blocks = static_cast<int64_t>(a.nblocks) * a.windows;
     if (blocks > INT_MAX) return cudaErrorInvalidValue;
     cudaError_t e =
-        launch(a.nblocks > 1 ? &sum_kernel<In, VEC, G, true> : &sum_kernel<In, VEC, G, false>,
+        launch(a.nblocks > 1 ? &sum_kernel<In, VEC, G, E, true> : &sum_kernel<In, VEC, G, E, false>,
                dim3(static_cast<unsigned>(blocks)), kSumThreads, 0, true, stream, a);
     if (e != cudaSuccess) return e;
     ++n;
@@ -1066,37 +1131,20 @@ struct SumLaunch {
 struct SmallLaunch {
   SmallArgs a;
   cudaStream_t stream;
-  template <class In, int VEC, int G>
+  template <class In, int VEC, int G, int E>
   cudaError_t run() {
-    a.sum.windows = (a.sum.D + G * VEC - 1) / (G * VEC);
+    constexpr int kWindow = G * E * VEC;
+    a.sum.windows = (a.sum.D + kWindow - 1) / kWindow;
     constexpr int per_block = kSumThreads / G * kSumInFlight;  // tokens in flight
     a.parts = (a.sum.T + per_block - 1) / per_block;
     // blocks: for the sums, and 32 KB of zeros each
     int64_t blocks = static_cast<int64_t>(a.parts) * a.sum.windows;
     if (a.fill.out != nullptr)
       blocks = std::max(blocks, std::min<int64_t>(592, a.fill.rows * a.fill.row_bytes / (32 << 10)));
-    return launch(&small_kernel<In, VEC, G>, dim3(static_cast<unsigned>(blocks)), kSumThreads, 0,
+    return launch(&small_kernel<In, VEC, G, E>, dim3(static_cast<unsigned>(blocks)), kSumThreads, 0,
                   false, stream, a);
   }
 };
-
-// The lanes of a group, by the row's length.
-template <class In, class F>
-cudaError_t by_shape(int D, bool vec, F& f) {
-  constexpr int V = kVecOf<In>;
-  if (!vec) return f.template run<In, 1, 32>();
-  const int chunks = D / V;
-  if (chunks <= 4) return f.template run<In, V, 4>();
-  if (chunks <= 8) return f.template run<In, V, 8>();
-  if (chunks <= 16) return f.template run<In, V, 16>();
-  return f.template run<In, V, 32>();
-}
-
-template <class F>
-cudaError_t by_type(int dtype, int D, bool vec, F& f) {
-  return dtype == DLRM_TABLE_F32 ? by_shape<float>(D, vec, f)
-                                 : by_shape<__nv_bfloat16>(D, vec, f);
-}
 
 // Sizes of a gradient's scratch, and where its parts lie.
 struct GradPlan {
@@ -1193,15 +1241,15 @@ int dlrm_embedding_lookup(const void* table, int table_dtype, int64_t ldw, int64
   a.pad = static_cast<int>(padding_idx);
   a.scale = scale;
   a.status = status_dev;
-  const bool vec = D % (16 / es) == 0 && rows16(table, ldw, es) && rows16(out, ldo, os);
-  using B = __nv_bfloat16;
+  const int vec = common_vec(table, ldw, es, out, ldo, os, D);
   cudaError_t e;
-  if (table_dtype == DLRM_TABLE_F32)
-    e = out_dtype == DLRM_TABLE_F32 ? run_lookup_shape<float, float>(a, vec, s)
-                                    : run_lookup_shape<float, B>(a, vec, s);
-  else
-    e = out_dtype == DLRM_TABLE_F32 ? run_lookup_shape<B, float>(a, vec, s)
-                                    : run_lookup_shape<B, B>(a, vec, s);
+  if (out_dtype == DLRM_TABLE_F32) {
+    LookupLaunch<float> f = {a, s};
+    e = by_type(table_dtype, a.D, vec, f);
+  } else {
+    LookupLaunch<__nv_bfloat16> f = {a, s};
+    e = by_type(table_dtype, a.D, vec, f);
+  }
   if (e != cudaSuccess) return cuda_fail(e);
   note_launch();
   return DLRM_OK;
@@ -1265,7 +1313,7 @@ int dlrm_embedding_grad(const void* grad, int grad_dtype, int64_t ldg, const int
   a.scale = scale;
   a.out_bf16 = out_dtype == DLRM_TABLE_BF16;
   a.accumulate = accumulate ? 1 : 0;
-  const bool vec = D % (16 / es) == 0 && rows16(grad, ldg, es) && rows16(out, ldo, os);
+  const int vec = common_vec(grad, ldg, es, out, ldo, os, D);
   cudaError_t e;
   if (T <= kSmallTokens && (accumulate || rows * D * os <= kSmallZeros)) {
     SmallLaunch f = {};

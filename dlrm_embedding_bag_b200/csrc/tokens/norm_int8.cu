@@ -320,9 +320,9 @@ cudaError_t run_norm(const NormArgs& a, bool vec, cudaStream_t stream) {
 
 int norm_rows(const NormArgs& a, int dtype, cudaStream_t stream) {
   const int es = dtype_size(dtype), V = 16 / es;
-  const bool vec = a.K % V == 0 && rows16(a.x, a.ldx, es) &&
-                   (a.residual == nullptr || rows16(a.residual, a.ldr, es)) &&
-                   (a.h_out == nullptr || rows16(a.h_out, a.ldh, es)) &&
+  const bool vec = a.K % V == 0 && rows_by(a.x, a.ldx, es, V) &&
+                   (a.residual == nullptr || rows_by(a.residual, a.ldr, es, V)) &&
+                   (a.h_out == nullptr || rows_by(a.h_out, a.ldh, es, V)) &&
                    (a.weight == nullptr || is_aligned(a.weight, 16)) && is_aligned(a.q, V) &&
                    a.ldq % V == 0;
   using B = __nv_bfloat16;
@@ -377,7 +377,7 @@ template <class T>
 cudaError_t run_dequant(const int8_t* q, int64_t ldq, const float* scale, int64_t M, int64_t K,
                         T* y, int64_t ldy, cudaStream_t stream) {
   const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(M, 148 * 64));
-  const bool vec = K % 16 == 0 && is_aligned(q, 16) && ldq % 16 == 0 && rows16(y, ldy, sizeof(T));
+  const bool vec = K % 16 == 0 && is_aligned(q, 16) && ldq % 16 == 0 && rows_by(y, ldy, sizeof(T), 8);
   const int64_t per_row = vec ? K / 16 : K;
   const int threads = static_cast<int>(std::min<int64_t>(256, (per_row + 31) / 32 * 32));
   return launch(vec ? &dequant_kernel<T, 16> : &dequant_kernel<T, 1>, dim3(blocks), threads, 0,

@@ -67,7 +67,7 @@ def _same_bits(a, b):
 LOOKUPS = [  # T, rows, D
     (1, 1, 1), (1, 10, 4), (3, 7, 8), (5, 100, 16), (64, 1000, 16), (33, 50, 24), (1000, 300, 64),
     (257, 90, 100), (129, 33, 129), (77, 40, 1000), (4099, 999, 128), (20, 10, 4100),
-    (70000, 50, 12),
+    (70000, 50, 12), (500, 90, 18), (500, 90, 34), (500, 90, 130), (300, 90, 515), (301, 90, 2),
 ]
 
 
@@ -88,7 +88,8 @@ def test_lookup(tokens, T, rows, D, dt, odt):
     assert _same_bits(out, ref.to(IDS[odt]))
 
 
-@pytest.mark.parametrize("pitch,offset", [(128, 0), (104, 0), (103, 0), (104, 4), (100, 1)])
+@pytest.mark.parametrize("pitch,offset", [(128, 0), (104, 0), (103, 0), (104, 4), (100, 1),
+                                          (102, 0), (102, 2), (102, 1)])
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_lookup_strides_and_what_is_left_alone(tokens, pitch, offset, dt):
     g = _gen(pitch + offset)
@@ -175,7 +176,8 @@ GRADS = [  # T, rows, D
     (1023, 255, 24), (1024, 256, 32), (1025, 257, 12), (4096, 65535, 16), (4097, 65536, 128),
     (777, 40, 1000), (5000, 100000, 36), (333, 50, 129), (150, 20, 4100), (30000, 17, 64),
     (150001, 70001, 4), (170001, 3000, 128), (400007, 900, 100), (31000, 70, 4100),
-    (511, 64, 64), (512, 40000, 100), (512, 2000000, 4), (513, 64, 64), (300, 9000, 1000),
+    (900, 200, 18), (900, 200, 33), (2000, 300, 130), (2000, 300, 131), (300, 90, 515),
+    (40000, 300, 258), (511, 64, 64), (512, 40000, 100), (512, 2000000, 4), (513, 64, 64), (300, 9000, 1000),
     (700001, 900000, 4), (1000003, 70, 4), (1600001, 20000, 4),
     (8192, 300, 8), (8193, 70000, 8), (20000, 5, 16), (65536, 3000, 8), (65537, 3000, 8),
 ]
@@ -250,7 +252,8 @@ def test_grad_accumulates_into_the_rows_that_tokens_name(tokens, T, odt):
 
 @pytest.mark.parametrize("T", [40, 4400])
 @pytest.mark.parametrize("pitch,offset,dt", [(64, 0, "f32"), (41, 0, "f32"), (40, 1, "f32"),
-                                             (64, 0, "bf16"), (44, 0, "bf16"), (40, 3, "bf16")])
+                                             (64, 0, "bf16"), (44, 0, "bf16"), (40, 3, "bf16"),
+                                             (42, 0, "f32"), (42, 2, "bf16"), (42, 1, "bf16")])
 @pytest.mark.parametrize("accumulate", [False, True])
 def test_grad_strides_and_what_is_left_alone(tokens, T, pitch, offset, dt, accumulate):
     g = _gen(pitch)
