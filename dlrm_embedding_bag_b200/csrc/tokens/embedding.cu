@@ -88,26 +88,27 @@ __global__ void __launch_bounds__(kLookupThreads) lookup_kernel(const LookupArgs
 }
 
 // The lanes of a group, and the accesses of a lane (E of them, G apart), by the
-// row's length: 128-bit accesses where rows allow them, else pairs, else single
-// elements, four a lane where the row is longer than a warp.
+// row's length: 128-bit accesses where rows allow them, else VEC = 2 or 1 elements
+// and more accesses a lane.
+template <class In, int VEC, class F>
+cudaError_t by_narrow(int chunks, F& f) {
+  if (chunks <= 16) return f.template run<In, VEC, 8, 2>();
+  if (chunks <= 32) return f.template run<In, VEC, 8, 4>();
+  if (chunks <= 64) return f.template run<In, VEC, 16, 4>();
+  if (chunks > 128 && chunks <= 256) return f.template run<In, VEC, 32, 8>();
+  return f.template run<In, VEC, 32, 4>();
+}
+
 template <class In, class F>
 cudaError_t by_shape(int D, int vec, F& f) {
   constexpr int V = kVecOf<In>;
   const int chunks = D / vec;
-  if (vec == V) {
-    if (chunks <= 4) return f.template run<In, V, 4, 1>();
-    if (chunks <= 8) return f.template run<In, V, 8, 1>();
-    if (chunks <= 16) return f.template run<In, V, 16, 1>();
-    return f.template run<In, V, 32, 1>();
-  }
-  if (vec == 2) {
-    if (chunks <= 16) return f.template run<In, 2, 16, 1>();
-    if (chunks <= 32) return f.template run<In, 2, 32, 1>();
-    return f.template run<In, 2, 32, 4>();
-  }
-  if (chunks <= 16) return f.template run<In, 1, 16, 1>();
-  if (chunks <= 32) return f.template run<In, 1, 32, 1>();
-  return f.template run<In, 1, 32, 4>();
+  if (vec == 1) return by_narrow<In, 1>(chunks, f);
+  if (vec == 2) return by_narrow<In, 2>(chunks, f);
+  if (chunks <= 4) return f.template run<In, V, 4, 1>();
+  if (chunks <= 8) return f.template run<In, V, 8, 1>();
+  if (chunks <= 16) return f.template run<In, V, 16, 1>();
+  return f.template run<In, V, 32, 1>();
 }
 
 template <class F>
@@ -776,7 +777,8 @@ __device__ __forceinline__ void sum_block(const SumArgs& a, SumSmem<VEC, G, E>& 
                                           const uint2* sorted, int64_t lo, int64_t hi, int chunk,
                                           int window, float* part) {
   constexpr int NG = SumSmem<VEC, G, E>::kGroups;
-  constexpr int U = G < kSumInFlight ? G : kSumInFlight;
+  // rows in flight: eight, or four of eight accesses a lane
+  constexpr int U = G < kSumInFlight ? G : E >= 8 ? kSumInFlight / 2 : kSumInFlight;
   auto& first = sm.first;
   auto& last = sm.last;
   const int q = threadIdx.x % G, g = threadIdx.x / G, base = (threadIdx.x & 31) / G * G;
