@@ -109,6 +109,9 @@ __device__ __forceinline__ void load_weight(const NormArgs& a, int c, float (&w)
     for (int e = 0; e < VEC; ++e) w[e] = 1.f;
   } else if constexpr (VEC == 1) {
     w[0] = __ldg(a.weight + c);
+  } else if constexpr (VEC == 2) {
+    const float2 v = __ldg(reinterpret_cast<const float2*>(a.weight + c));
+    w[0] = v.x, w[1] = v.y;
   } else {
 #pragma unroll
     for (int e = 0; e < VEC; e += 4) {
@@ -128,6 +131,10 @@ __device__ __forceinline__ void store_levels(int8_t* p, float (&t)[VEC], Levels 
   const bool none = f.inv == 0.f;
   if constexpr (VEC == 1) {
     *p = none ? 0 : static_cast<int8_t>(level_bits(t[0], f.inv) & 0xff);
+  } else if constexpr (VEC == 2) {
+    const uint32_t both =
+        __byte_perm(level_bits(t[0], f.inv), level_bits(t[1], f.inv), 0x0040);
+    *reinterpret_cast<uint16_t*>(p) = none ? 0 : static_cast<uint16_t>(both);
   } else {
     uint32_t w[VEC / 4];
 #pragma unroll
@@ -177,8 +184,8 @@ __device__ __forceinline__ float scale_of(const NormArgs& a, float sum, uint32_t
 }
 
 // Rows that fit the registers of TPR threads (a warp, or a block), CH chunks of VEC
-// elements each: read once, 128 bits a load. Bound by the memory: 16384 rows of
-// 4096 bf16 with a residual move 470 MB.
+// elements each: read once, 128 bits a load where rows allow that. Bound by the
+// memory: 16384 rows of 4096 bf16 with a residual move 470 MB in 73 us.
 template <class T, int VEC, int TPR, int CH>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
     norm_row_kernel(const NormArgs a) {
@@ -244,8 +251,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
   }
 }
 
-// Longer rows, and rows that 128-bit accesses cannot walk: a block for each row,
-// which it reads twice (the second time from L2).
+// Longer rows: a block for each row, which it reads twice (the second time from L2).
 template <class T, int VEC>
 __global__ void __launch_bounds__(kNormThreads) norm_loop_kernel(const NormArgs a) {
   for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
@@ -294,37 +300,59 @@ cudaError_t run_loop(const NormArgs& a, cudaStream_t stream) {
                 false, stream, a);
 }
 
-template <class T, int TPR, int CH>
+template <class T, int VEC, int TPR, int CH>
 cudaError_t run_row(const NormArgs& a, cudaStream_t stream) {
   constexpr int kThreads = TPR < 128 ? 128 : TPR, kRows = kThreads / TPR;
   const int64_t blocks = (static_cast<int64_t>(a.M) + kRows - 1) / kRows;
-  return launch(&norm_row_kernel<T, kVecOf<T>, TPR, CH>, dim3(static_cast<unsigned>(blocks)),
+  return launch(&norm_row_kernel<T, VEC, TPR, CH>, dim3(static_cast<unsigned>(blocks)),
                 kThreads, 0, false, stream, a);
+}
+
+// Rows that 128-bit accesses cannot walk: pairs or single elements, eight a thread.
+// (30000 rows with a residual and their values written out, f32: 260 us in the
+// loop below, here 98 at 1002 columns and 111 at 1001; bf16 253, 91 and 113.)
+template <class T, int VEC>
+cudaError_t run_narrow(const NormArgs& a, cudaStream_t stream) {
+  const int chunks = a.K / VEC;
+  if (chunks <= 128) return run_row<T, VEC, 32, 4>(a, stream);
+  if (chunks <= 256) return run_row<T, VEC, 32, 8>(a, stream);
+  if (chunks <= 1024) return run_row<T, VEC, 128, 8>(a, stream);
+  if (chunks <= 2048) return run_row<T, VEC, 256, 8>(a, stream);
+  if (chunks <= 4096) return run_row<T, VEC, 512, 8>(a, stream);
+  if (chunks <= 8192) return run_row<T, VEC, 1024, 8>(a, stream);
+  return run_loop<T, VEC>(a, stream);
 }
 
 // Four chunks a thread where rows are many (a row's loads all in flight, many
 // rows an SM); one where they are few and a row's latency is what counts.
 template <class T>
-cudaError_t run_norm(const NormArgs& a, bool vec, cudaStream_t stream) {
-  if (!vec) return run_loop<T, 1>(a, stream);
-  const int chunks = a.K / kVecOf<T>;
+cudaError_t run_norm(const NormArgs& a, int vec, cudaStream_t stream) {
+  constexpr int V = kVecOf<T>;
+  if (vec == 1) return run_narrow<T, 1>(a, stream);
+  if (vec == 2) return run_narrow<T, 2>(a, stream);
+  const int chunks = a.K / V;
   const bool few = a.M <= 148 * 4;
-  if (chunks <= 32) return run_row<T, 32, 1>(a, stream);
-  if (chunks <= 128) return few ? run_row<T, 128, 1>(a, stream) : run_row<T, 32, 4>(a, stream);
-  if (chunks <= 512) return few ? run_row<T, 512, 1>(a, stream) : run_row<T, 128, 4>(a, stream);
-  if (chunks <= 1024) return few ? run_row<T, 1024, 1>(a, stream) : run_row<T, 256, 4>(a, stream);
-  if (chunks <= 2048) return run_row<T, 512, 4>(a, stream);
-  if (chunks <= 4096) return run_row<T, 1024, 4>(a, stream);
-  return run_loop<T, kVecOf<T>>(a, stream);
+  if (chunks <= 32) return run_row<T, V, 32, 1>(a, stream);
+  if (chunks <= 128) return few ? run_row<T, V, 128, 1>(a, stream) : run_row<T, V, 32, 4>(a, stream);
+  if (chunks <= 512)
+    return few ? run_row<T, V, 512, 1>(a, stream) : run_row<T, V, 128, 4>(a, stream);
+  if (chunks <= 1024)
+    return few ? run_row<T, V, 1024, 1>(a, stream) : run_row<T, V, 256, 4>(a, stream);
+  if (chunks <= 2048) return run_row<T, V, 512, 4>(a, stream);
+  if (chunks <= 4096) return run_row<T, V, 1024, 4>(a, stream);
+  return run_loop<T, V>(a, stream);
 }
 
 int norm_rows(const NormArgs& a, int dtype, cudaStream_t stream) {
-  const int es = dtype_size(dtype), V = 16 / es;
-  const bool vec = a.K % V == 0 && rows_by(a.x, a.ldx, es, V) &&
-                   (a.residual == nullptr || rows_by(a.residual, a.ldr, es, V)) &&
-                   (a.h_out == nullptr || rows_by(a.h_out, a.ldh, es, V)) &&
-                   (a.weight == nullptr || is_aligned(a.weight, 16)) && is_aligned(a.q, V) &&
-                   a.ldq % V == 0;
+  const int es = dtype_size(dtype);
+  // elements of an access that every row allows
+  int vec = 1;
+  for (int v : {2, 16 / es})
+    if (a.K % v == 0 && rows_by(a.x, a.ldx, es, v) &&
+        (a.residual == nullptr || rows_by(a.residual, a.ldr, es, v)) &&
+        (a.h_out == nullptr || rows_by(a.h_out, a.ldh, es, v)) &&
+        is_aligned(a.weight, v == 2 ? 8 : 16) && rows_by(a.q, a.ldq, 1, v))
+      vec = v;
   using B = __nv_bfloat16;
   cudaError_t e;
   if (dtype == DLRM_TABLE_F32)
@@ -346,19 +374,19 @@ int check_rows(const void* x, int64_t ldx, int dtype, int64_t M, int64_t K, cons
   return DLRM_OK;
 }
 
-// y = q * scale: a block walks rows, VEC columns a thread (16: one 128-bit load).
+// y = q * scale: a block walks rows. VEC 16: one 128-bit load a thread; else four
+// accesses of VEC columns a thread, a block's width apart.
 template <class T, int VEC>
 __global__ void __launch_bounds__(256)
     dequant_kernel(const int8_t* q, int64_t ldq, const float* scale, int M, int K, T* y,
                    int64_t ldy) {
   for (int64_t m = blockIdx.x; m < M; m += gridDim.x) {
     const float s = __ldg(scale + m);
-    for (int c = threadIdx.x * VEC; c < K; c += blockDim.x * VEC) {
-      if constexpr (VEC == 1) {
-        const float v[1] = {static_cast<float>(q[m * ldq + c]) * s};
-        store_f32<T, 1>(y + m * ldy + c, v);
-      } else {
-        const uint4 r = __ldg(reinterpret_cast<const uint4*>(q + m * ldq + c));
+    const int8_t* from = q + m * ldq;
+    T* to = y + m * ldy;
+    if constexpr (VEC == 16) {
+      for (int c = threadIdx.x * 16; c < K; c += blockDim.x * 16) {
+        const uint4 r = __ldg(reinterpret_cast<const uint4*>(from + c));
         const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -366,7 +394,32 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             v[e] = static_cast<float>(static_cast<int8_t>(w[2 * i + e / 4] >> (8 * (e % 4)))) * s;
-          store_f32<T, 8>(y + m * ldy + c + 8 * i, v);
+          store_f32<T, 8>(to + c + 8 * i, v);
+        }
+      }
+    } else {
+      const int step = blockDim.x * VEC;
+      for (int c0 = threadIdx.x * VEC; c0 < K; c0 += 4 * step) {
+        uint32_t r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = c0 + i * step;
+          r[i] = 0;
+          if (c < K) {
+            if constexpr (VEC == 2)
+              r[i] = __ldg(reinterpret_cast<const unsigned short*>(from + c));
+            else
+              r[i] = static_cast<uint8_t>(__ldg(from + c));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = c0 + i * step;
+          float v[VEC];
+#pragma unroll
+          for (int e = 0; e < VEC; ++e)
+            v[e] = static_cast<float>(static_cast<int8_t>(r[i] >> (8 * e))) * s;
+          if (c < K) store_f32<T, VEC>(to + c, v);
         }
       }
     }
@@ -377,11 +430,16 @@ template <class T>
 cudaError_t run_dequant(const int8_t* q, int64_t ldq, const float* scale, int64_t M, int64_t K,
                         T* y, int64_t ldy, cudaStream_t stream) {
   const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(M, 148 * 64));
-  const bool vec = K % 16 == 0 && is_aligned(q, 16) && ldq % 16 == 0 && rows_by(y, ldy, sizeof(T), 8);
-  const int64_t per_row = vec ? K / 16 : K;
+  int vec = 1;
+  for (int v : {2, 16})
+    if (K % v == 0 && rows_by(q, ldq, 1, v) && rows_by(y, ldy, sizeof(T), v)) vec = v;
+  const int64_t per_row = vec == 16 ? K / 16 : (K / vec + 3) / 4;
   const int threads = static_cast<int>(std::min<int64_t>(256, (per_row + 31) / 32 * 32));
-  return launch(vec ? &dequant_kernel<T, 16> : &dequant_kernel<T, 1>, dim3(blocks), threads, 0,
-                false, stream, q, ldq, scale, static_cast<int>(M), static_cast<int>(K), y, ldy);
+  auto* fn = vec == 16  ? &dequant_kernel<T, 16>
+             : vec == 2 ? &dequant_kernel<T, 2>
+                        : &dequant_kernel<T, 1>;
+  return launch(fn, dim3(blocks), threads, 0, false, stream, q, ldq, scale, static_cast<int>(M),
+                static_cast<int>(K), y, ldy);
 }
 
 }  // namespace

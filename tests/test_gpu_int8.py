@@ -56,7 +56,8 @@ def _check_rows(q, scale, y, K, what=""):
 
 SHAPES = [(1, 1), (1, 8), (3, 7), (2, 16), (5, 100), (33, 128), (17, 250), (8, 512), (4, 1000),
           (3, 1024), (2, 2048), (7, 4096), (2, 4104), (2, 5000), (1, 8192), (2, 16384),
-          (1, 40000), (1, 131072), (3000, 24), (700, 130)]
+          (1, 40000), (1, 131072), (3000, 24), (700, 130), (9, 2), (6, 129), (5, 255), (4, 1026),
+          (3, 2046), (3, 2049), (2, 4097), (2, 8193), (2, 8194), (1, 16386), (1, 20001)]
 
 
 @pytest.mark.parametrize("M,K", SHAPES)
@@ -87,7 +88,7 @@ def test_rms_norm(int8, M, K, dt, residual, weight):
         assert h is None
 
 
-@pytest.mark.parametrize("pitch", [104, 112, 101, 100])
+@pytest.mark.parametrize("pitch", [104, 112, 101, 100, 102])
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("K", [100, 96, 97])
 def test_norm_strides_in_place_and_what_is_left_alone(int8, pitch, dt, K):
@@ -110,7 +111,7 @@ def test_norm_strides_in_place_and_what_is_left_alone(int8, pitch, dt, K):
     assert torch.isnan(base[:, K:].float()).all()
 
 
-@pytest.mark.parametrize("K", [64, 4096, 20000])
+@pytest.mark.parametrize("K", [64, 4096, 20000, 66, 1001, 20001])
 def test_rows_of_zeros_tiny_huge_and_not_finite(int8, K):
     g = _gen(K)
     x = _normal(g, 9, K)
@@ -144,7 +145,7 @@ def test_rows_of_zeros_tiny_huge_and_not_finite(int8, K):
 
 def test_values_of_rows(int8):
     g = _gen(4)
-    for M, K in ((1, 1), (5, 16), (40, 100), (3, 4099)):
+    for M, K in ((1, 1), (5, 16), (40, 100), (3, 4099), (7, 1026), (2, 2), (300, 33)):
         q, s = int8.quantize_rows(_normal(g, M, K))
         exact = q.double() * s.double()[:, None]
         for dt in (F32, BF16):
