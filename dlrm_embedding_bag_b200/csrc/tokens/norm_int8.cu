@@ -48,13 +48,12 @@ __device__ __forceinline__ void row_sum_max(float& sum, uint32_t& top) {
       tops[threadIdx.x >> 5] = top;
     }
     __syncthreads();
-    sum = 0.f;
-    top = 0;
+    // every warp adds the warps' sums, in the same order
+    const int w = threadIdx.x & (THREADS / 32 - 1);
+    sum = sums[w];
+    top = __reduce_max_sync(kFull, tops[w]);
 #pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) {
-      sum += sums[w];
-      top = max(top, tops[w]);
-    }
+    for (int o = THREADS / 64; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
   }
 }
 
@@ -171,23 +170,34 @@ __device__ float far_scale(const NormArgs& a, uint32_t top, Each each) {
   return static_cast<float>(static_cast<double>(__uint_as_float(top)) / sqrt(mean) / 127.0);
 }
 
-// The scale of a row from its sum of squares and the bits of max|t|.
-// far: the caller has to take far_scale instead.
-__device__ __forceinline__ float scale_of(const NormArgs& a, float sum, uint32_t top, bool& far) {
-  far = false;
+// Whether a row's scale has to be far_scale's: the mean of its squares, which are
+// finite numbers or more, is above f32 or so small that squares have vanished.
+__device__ __forceinline__ bool is_far(const NormArgs& a, float sum, uint32_t top) {
+  if (!a.norm || top == 0 || top >= kInfBits) return false;
+  return !(sum + a.eps <= FLT_MAX) || __fmaf_rn(a.eps, static_cast<float>(a.K), sum) < 1e-30f * a.K;
+}
+
+// The scale of any other row, from its sum of squares and the bits of max|t|. Two
+// divisions and a root: one thread's work, since the levels do not need it.
+__device__ __forceinline__ float scale_of(const NormArgs& a, float sum, uint32_t top) {
   if (top >= kInfBits) return __uint_as_float(0x7fc00000u);
   const float A = __uint_as_float(top);
   if (!a.norm || top == 0) return __fdiv_rn(A, 127.f);
   const float mean = __fadd_rn(__fdiv_rn(sum, static_cast<float>(a.K)), a.eps);
-  far = !(mean <= FLT_MAX) || mean < 1e-30f;
   return __fdiv_rn(__fmul_rn(A, __frsqrt_rn(mean)), 127.f);
 }
+
+// Blocks of an SM that the compiler leaves registers for. Three of 512 threads in place
+// of two, where that takes no spills worth naming: the work between a row's barriers is
+// what its time goes into (8665 rows of 6924 f32: 86 us with two, 70 with three).
+template <int VEC, int TPR, int CH, bool RES>
+constexpr int kBlocksAnSM = !RES && TPR == 512 && CH > 1 && VEC * CH <= 16 ? 3 : 1;
 
 // Rows that fit the registers of TPR threads (a warp, or a block), CH chunks of VEC
 // elements each: read once, 128 bits a load where rows allow that. Bound by the
 // memory: 16384 rows of 4096 bf16 with a residual move 470 MB in 73 us.
-template <class T, int VEC, int TPR, int CH>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
+template <class T, int VEC, int TPR, int CH, bool RES>
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, kBlocksAnSM<VEC, TPR, CH, RES>)
     norm_row_kernel(const NormArgs a) {
   constexpr int kRows = TPR < 128 ? 128 / TPR : 1;  // rows of a block
   const int64_t m = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / TPR;
@@ -201,7 +211,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
     xs[i] = rs[i] = Raw<T, VEC>();
     if (c < a.K) {
       xs[i] = *reinterpret_cast<const Raw<T, VEC>*>(static_cast<const T*>(a.x) + m * a.ldx + c);
-      if (a.residual != nullptr)
+      if constexpr (RES)
         rs[i] = *reinterpret_cast<const Raw<T, VEC>*>(static_cast<const T*>(a.residual) + m * a.ldr + c);
     }
   }
@@ -210,15 +220,18 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = (i * TPR + q) * VEC;
-    float r[VEC];
     widen<T, VEC>(xs[i], h[i]);
-    widen<T, VEC>(rs[i], r);
+    if constexpr (RES) {
+      float r[VEC];
+      widen<T, VEC>(rs[i], r);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) h[i][e] += r[e];
+    }
     if (c < a.K) {
       float w[VEC];
       load_weight<VEC>(a, c, w);
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        if (a.residual != nullptr) h[i][e] += r[e];
         sum += h[i][e] * h[i][e];
         most = max_abs(most, h[i][e] * w[e]);
       }
@@ -226,8 +239,8 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
   }
   uint32_t top = __float_as_uint(most);
   row_sum_max<TPR>(sum, top);
-  bool far;
-  float s = scale_of(a, sum, top, far);
+  const bool far = is_far(a, sum, top);  // the same for the whole row
+  float s = 0.f;
   if (far)
     s = far_scale<TPR>(a, top, [&](auto f) {
 #pragma unroll
@@ -235,7 +248,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) f(h[i][e]);  // past the row: 0
     });
-  if (q == 0) a.scale[m] = s;
+  if (q == 0) a.scale[m] = far ? s : scale_of(a, sum, top);
   const Levels f = levels_of(top);
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
@@ -268,8 +281,8 @@ __global__ void __launch_bounds__(kNormThreads) norm_loop_kernel(const NormArgs 
     }
     uint32_t top = __float_as_uint(most);
     row_sum_max<kNormThreads>(sum, top);
-    bool far;
-    float s = scale_of(a, sum, top, far);
+    const bool far = is_far(a, sum, top);
+    float s = 0.f;
     if (far)  // reads the row again, before anything of it is written
       s = far_scale<kNormThreads>(a, top, [&](auto f) {
         for (int c = threadIdx.x * VEC; c < a.K; c += kNormThreads * VEC) {
@@ -279,7 +292,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_loop_kernel(const NormArgs 
           for (int e = 0; e < VEC; ++e) f(h[e]);
         }
       });
-    if (threadIdx.x == 0) a.scale[m] = s;
+    if (threadIdx.x == 0) a.scale[m] = far ? s : scale_of(a, sum, top);
     const Levels f = levels_of(top);
     for (int c = threadIdx.x * VEC; c < a.K; c += kNormThreads * VEC) {
       float h[VEC], w[VEC];
@@ -304,8 +317,9 @@ template <class T, int VEC, int TPR, int CH>
 cudaError_t run_row(const NormArgs& a, cudaStream_t stream) {
   constexpr int kThreads = TPR < 128 ? 128 : TPR, kRows = kThreads / TPR;
   const int64_t blocks = (static_cast<int64_t>(a.M) + kRows - 1) / kRows;
-  return launch(&norm_row_kernel<T, VEC, TPR, CH>, dim3(static_cast<unsigned>(blocks)),
-                kThreads, 0, false, stream, a);
+  auto* fn = a.residual != nullptr ? &norm_row_kernel<T, VEC, TPR, CH, true>
+                                   : &norm_row_kernel<T, VEC, TPR, CH, false>;
+  return launch(fn, dim3(static_cast<unsigned>(blocks)), kThreads, 0, false, stream, a);
 }
 
 // Rows that 128-bit accesses cannot walk: pairs or single elements, eight a thread.
@@ -406,7 +420,9 @@ __global__ void __launch_bounds__(256)
           const int c = c0 + i * step;
           r[i] = 0;
           if (c < K) {
-            if constexpr (VEC == 2)
+            if constexpr (VEC == 4)
+              r[i] = __ldg(reinterpret_cast<const uint32_t*>(from + c));
+            else if constexpr (VEC == 2)
               r[i] = __ldg(reinterpret_cast<const unsigned short*>(from + c));
             else
               r[i] = static_cast<uint8_t>(__ldg(from + c));
@@ -431,11 +447,12 @@ cudaError_t run_dequant(const int8_t* q, int64_t ldq, const float* scale, int64_
                         T* y, int64_t ldy, cudaStream_t stream) {
   const unsigned blocks = static_cast<unsigned>(std::min<int64_t>(M, 148 * 64));
   int vec = 1;
-  for (int v : {2, 16})
+  for (int v : {2, 4, 16})
     if (K % v == 0 && rows_by(q, ldq, 1, v) && rows_by(y, ldy, sizeof(T), v)) vec = v;
   const int64_t per_row = vec == 16 ? K / 16 : (K / vec + 3) / 4;
   const int threads = static_cast<int>(std::min<int64_t>(256, (per_row + 31) / 32 * 32));
   auto* fn = vec == 16  ? &dequant_kernel<T, 16>
+             : vec == 4 ? &dequant_kernel<T, 4>
              : vec == 2 ? &dequant_kernel<T, 2>
                         : &dequant_kernel<T, 1>;
   return launch(fn, dim3(blocks), threads, 0, false, stream, q, ldq, scale, static_cast<int>(M),
