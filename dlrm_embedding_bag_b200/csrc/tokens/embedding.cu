@@ -18,14 +18,16 @@ constexpr int kMaxDevices = 64;  // devices whose launch set-up is cached
 // ---------------------------------------------------------------------------
 // Lookup: Y[t] = scale * W[ids[t]].
 //
-// G lanes take a window of G * VEC columns of kRowsInFlight tokens' rows, all
+// G lanes take a window of G * E * VEC columns of kRowsInFlight tokens' rows, all
 // loads in the air before the first is used. No arithmetic to speak of: bound by
-// the bytes of the rows. Y is written past the cache's order of use, which keeps
-// frequent rows in L2. Measured on B200, 1310720 tokens of 512-byte rows under a
-// power law of 1.2 (671 MB written): 135 us; with 256 threads a block 141, 512
-// threads 148, two rows in flight 147, ordinary stores 4 us more; 16383 tokens
-// of 2000-byte rows: 10.3 us (6.4 TB/s), 15.8 where a group walks all windows
-// of its rows instead.
+// the bytes of the rows, or, where 128-bit accesses cannot walk them, by the number
+// of accesses. Y is written past the cache's order of use, which keeps frequent
+// rows in L2. Measured on B200, 1310720 tokens of 512-byte rows under a power law
+// of 1.2 (671 MB written): 119 us, of 2000-byte rows, 16383 tokens: 10.2 us
+// (6.4 TB/s), 15.8 where a group walks all windows of its rows instead. More
+// threads a block (256, 512) cost 6 and 13 us of the first, two rows in flight 12,
+// ordinary stores 4. 60000 rows of 1001 f32, single elements: 76 us with four
+// accesses a lane (6.3 TB/s), bf16 58; of 1002, pairs: 74 and 41.
 
 constexpr int kLookupThreads = 128;
 constexpr int kRowsInFlight = 4;
@@ -1175,7 +1177,7 @@ GradPlan plan_grad(int64_t T, int64_t rows, int64_t D) {
   p.sort_blocks = static_cast<int>((T + per - 1) / per);
   // a group's tokens: as few as are in flight at once while that fills the
   // GPU's threads, more when there are more; by T and D alone. (16383 x 1000
-  // takes 36.0 us with 8 tokens, 33.9 with 16, 36.4 with 24; 32768 x 64 51.3,
+  // takes 36 us with 8 tokens, 34 with 16, 36 with 24; 32768 x 64 51.3,
   // 51.7 and 53.3.)
   const int64_t even = T * D / (int64_t{148} * 2048 * 4) / kSumInFlight + 1;
   p.chunk = static_cast<int>(std::min<int64_t>(64, even * kSumInFlight));

@@ -187,11 +187,16 @@ __device__ __forceinline__ float scale_of(const NormArgs& a, float sum, uint32_t
   return __fdiv_rn(__fmul_rn(A, __frsqrt_rn(mean)), 127.f);
 }
 
-// Blocks of an SM that the compiler leaves registers for. Three of 512 threads in place
-// of two, where that takes no spills worth naming: the work between a row's barriers is
-// what its time goes into (8665 rows of 6924 f32: 86 us with two, 70 with three).
+// Blocks of an SM that the compiler leaves registers for: 1280 threads of narrow rows,
+// and three blocks of 512 in place of two, where that spills a few registers at most.
+// The work around a row's barriers is what its time goes into, and other rows cover it
+// (8665 rows of 6924 f32: 86 us with two blocks, 70 with three; 30000 of 1002 bf16 with
+// their values written out 88 us, as the compiler chooses, and 82).
 template <int VEC, int TPR, int CH, bool RES>
-constexpr int kBlocksAnSM = !RES && TPR == 512 && CH > 1 && VEC * CH <= 16 ? 3 : 1;
+constexpr int kBlocksAnSM = CH == 1 || VEC * CH > 16 ? 1
+                            : TPR == 512             ? (RES ? 2 : 3)
+                            : TPR < 512              ? 1280 / (TPR < 128 ? 128 : TPR)
+                                                     : 1;
 
 // Rows that fit the registers of TPR threads (a warp, or a block), CH chunks of VEC
 // elements each: read once, 128 bits a load where rows allow that. Bound by the
@@ -324,7 +329,7 @@ cudaError_t run_row(const NormArgs& a, cudaStream_t stream) {
 
 // Rows that 128-bit accesses cannot walk: pairs or single elements, eight a thread.
 // (30000 rows with a residual and their values written out, f32: 260 us in the
-// loop below, here 98 at 1002 columns and 111 at 1001; bf16 253, 91 and 113.)
+// loop below, here 101 at 1002 columns and 113 at 1001; bf16 253, 94 and 107.)
 template <class T, int VEC>
 cudaError_t run_narrow(const NormArgs& a, cudaStream_t stream) {
   const int chunks = a.K / VEC;
@@ -333,7 +338,13 @@ cudaError_t run_narrow(const NormArgs& a, cudaStream_t stream) {
   if (chunks <= 1024) return run_row<T, VEC, 128, 8>(a, stream);
   if (chunks <= 2048) return run_row<T, VEC, 256, 8>(a, stream);
   if (chunks <= 4096) return run_row<T, VEC, 512, 8>(a, stream);
-  if (chunks <= 8192) return run_row<T, VEC, 1024, 8>(a, stream);
+  // 1024 threads leave an SM one block, whose barriers nothing covers: 6000 rows of
+  // 6001 took 173 to 192 us with eight elements a thread, 123 to 153 with 512 and 16.
+  if constexpr (VEC == 1) {
+    if (chunks <= 8192) return run_row<T, VEC, 512, 16>(a, stream);
+  } else {
+    if (chunks <= 8192) return run_row<T, VEC, 1024, 8>(a, stream);
+  }
   return run_loop<T, VEC>(a, stream);
 }
 

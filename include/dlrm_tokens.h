@@ -47,8 +47,8 @@ extern "C" {
  *               is OR-ed in if an id lies outside [0, rows). Such an id reads
  *               nothing and its row of Y is zero, with or without a status word.
  * ldw, ldo >= D. Pointers are aligned to their element size; rows whose base
- * and pitch are multiples of 16 bytes use 128-bit accesses, others scalar ones
- * with the same results.
+ * and pitch are multiples of 16 bytes use 128-bit accesses, others those of two
+ * elements or one, with the same results.
  */
 DLRM_API int dlrm_embedding_lookup(const void* table, int table_dtype, int64_t ldw, int64_t rows,
                                    int64_t D, const int32_t* ids, int64_t T, float scale,

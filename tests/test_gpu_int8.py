@@ -143,6 +143,19 @@ def test_rows_of_zeros_tiny_huge_and_not_finite(int8, K):
     assert torch.isnan(s[3:6]).all() and int(q[6, K - 1]) == 127
 
 
+@pytest.mark.parametrize("K", [5, 64, 1000, 6924, 20001])
+def test_eps_that_leaves_f32_with_the_squares(int8, K):
+    # the mean of the squares and eps are finite, their sum is not
+    x = _normal(_gen(K), 6, K).clamp(-8, 8) * 1e19 / 8
+    x[1] = 1.5e19
+    x[2] *= 1e-19
+    for eps in (3e38, 1e-29, 1e-31):
+        q, s, _ = int8.rms_norm_int8(x, eps=eps)
+        y = x.double()
+        y = y / torch.sqrt(y.square().mean(1, keepdim=True) + np.float64(np.float32(eps)))
+        _check_rows(q, s, y, K, f"eps={eps}")
+
+
 def test_values_of_rows(int8):
     g = _gen(4)
     for M, K in ((1, 1), (5, 16), (40, 100), (3, 4099), (7, 1026), (2, 2), (300, 33)):
