@@ -230,11 +230,13 @@ __device__ __forceinline__ void fill_done() {
 constexpr int kFillThreads = 32;
 constexpr int kFillSmem = 116 << 10;
 
+// BESIDE: the sums follow, and their blocks may be scheduled early (they wait for this
+// grid's end; what follows zeros alone may not).
+template <bool BESIDE>
 __global__ void __launch_bounds__(kFillThreads) fill_kernel(const FillArgs f) {
   extern __shared__ __align__(16) uint8_t zeros[];
   static_assert(kFillSmem >= kZeroBytes, "room for the zeros");
-  // the sums' blocks may be scheduled now (they wait for this grid's end)
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if constexpr (BESIDE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   fill_zeros(f, blockIdx.x, gridDim.x, zeros);
   fill_done();
   // The sort in front is still at work, perhaps: this grid ends after it, so that
@@ -638,11 +640,12 @@ cudaError_t allow_smem(K* fn, int bytes, std::atomic<bool> (&prepared)[kMaxDevic
 
 // The zeros: beside the cluster sort that was launched last (the one before them
 // that they may not wait for), or behind all that is on the stream.
-cudaError_t run_fill(const FillArgs& f, int blocks, bool beside, cudaStream_t stream) {
+template <bool BESIDE>
+cudaError_t run_fill(const FillArgs& f, int blocks, cudaStream_t stream) {
   static std::atomic<bool> prepared[kMaxDevices];
-  const cudaError_t e = allow_smem(&fill_kernel, kFillSmem, prepared);
+  const cudaError_t e = allow_smem(&fill_kernel<BESIDE>, kFillSmem, prepared);
   if (e != cudaSuccess) return e;
-  return launch(&fill_kernel, dim3(blocks), kFillThreads, kFillSmem, beside, stream, f);
+  return launch(&fill_kernel<BESIDE>, dim3(blocks), kFillThreads, kFillSmem, BESIDE, stream, f);
 }
 
 // Zeros that the cluster sort writes itself, 16 bulk stores a CTA; more go to a
@@ -677,7 +680,7 @@ cudaError_t run_cluster_sort(SortArgs& a, int sms, int& n, cudaStream_t stream) 
   ++n;
   if ((e = cudaLaunchKernelEx(&cfg, fn, a)) != cudaSuccess || !beside) return e;
   ++n;
-  return run_fill(fill, std::max(1, sms - kClusterSize), true, stream);
+  return run_fill<true>(fill, std::max(1, sms - kClusterSize), stream);
 }
 
 // Sorts more tokens, two launches a pass, between the two buffers of pairs; the
@@ -1297,7 +1300,7 @@ int dlrm_embedding_grad(const void* grad, int grad_dtype, int64_t ldg, const int
   }
   if (T == 0) {
     if (accumulate) return DLRM_OK;
-    const cudaError_t e = run_fill(fill, sms, false, s);
+    const cudaError_t e = run_fill<false>(fill, sms, s);
     if (e != cudaSuccess) return cuda_fail(e);
     note_launch();
     return DLRM_OK;

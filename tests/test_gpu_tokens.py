@@ -358,6 +358,30 @@ def test_grad_waits_for_what_writes_its_output(tokens, T):
         assert _same_bits(seen, out.to(BF16))
 
 
+@pytest.mark.parametrize("T", [0, 5, 600, 70000])
+def test_a_layer_waits_for_a_gradient_that_is_its_bias(tokens, T):
+    """A bf16 layer reads its bias before it waits for the kernel in front, which so must
+    not let it start early: the bias here is the last row of a gradient."""
+    from dlrm_embedding_bag_b200 import mlp
+
+    g = _gen(T + 11)
+    rows, D = 300000, 128
+    a, _ = _matrix(g, 256, 64, BF16)
+    w, _ = _matrix(g, D, 64, BF16)
+    grad, _ = _matrix(g, T, D, F32)
+    ids = torch.full((T,), rows - 1, dtype=torch.int32, device=DEV)
+    ids[: T // 2] = 3
+    out = torch.empty((rows, D), device=DEV)
+    for k in range(3):
+        out.fill_(float(k + 5))
+        tokens.embedding_grad(grad, ids, rows, out=out)
+        seen, _ = mlp.linear_bf16(a, w, out[rows - 1])
+        torch.cuda.synchronize()
+        _check_grad(out, grad, ids, rows)
+        again, _ = mlp.linear_bf16(a, w, out[rows - 1].clone())
+        assert _same_bits(seen, again)
+
+
 @pytest.mark.parametrize("T", [300, 6000, 90000])
 def test_grads_at_the_same_time(tokens, T):
     """Calls that overlap on four streams, each with the scratch that torch gives it."""
