@@ -187,16 +187,18 @@ __device__ __forceinline__ float scale_of(const NormArgs& a, float sum, uint32_t
   return __fdiv_rn(__fmul_rn(A, __frsqrt_rn(mean)), 127.f);
 }
 
-// Blocks of an SM that the compiler leaves registers for: 1280 threads of narrow rows,
-// and three blocks of 512 in place of two, where that spills a few registers at most.
-// The work around a row's barriers is what its time goes into, and other rows cover it
-// (8665 rows of 6924 f32: 86 us with two blocks, 70 with three; 30000 of 1002 bf16 with
-// their values written out 88 us, as the compiler chooses, and 82).
+// Blocks of an SM that the compiler leaves registers for, where it would take some
+// more: the work around a row's barriers is what its time goes into, and other rows
+// cover it. 16 elements a thread: 1280 threads an SM, or 1536 of rows that take 512
+// (8665 rows of 6924 f32: 86 us with 1024, 70 so). 32 elements: 1024 threads (8000
+// rows of 8192 bf16 with their values written out: 103 us as the compiler chooses, 96
+// so), but with a residual the loads that all the registers keep in flight are worth
+// more (16384 rows of 4096: 116 us, and 123).
 template <int VEC, int TPR, int CH, bool RES>
-constexpr int kBlocksAnSM = CH == 1 || VEC * CH > 16 ? 1
-                            : TPR == 512             ? (RES ? 2 : 3)
-                            : TPR < 512              ? 1280 / (TPR < 128 ? 128 : TPR)
-                                                     : 1;
+constexpr int kBlocksAnSM = CH == 1 || TPR > 512 ? 1
+                            : VEC * CH > 16      ? (RES ? 1 : 1024 / (TPR < 128 ? 128 : TPR))
+                            : TPR == 512         ? (RES ? 2 : 3)
+                                                 : 1280 / (TPR < 128 ? 128 : TPR);
 
 // Rows that fit the registers of TPR threads (a warp, or a block), CH chunks of VEC
 // elements each: read once, 128 bits a load where rows allow that. Bound by the
