@@ -179,6 +179,7 @@ GRADS = [  # T, rows, D
     (900, 200, 18), (900, 200, 33), (2000, 300, 130), (2000, 300, 131), (300, 90, 515),
     (40000, 300, 258), (511, 64, 64), (512, 40000, 100), (512, 2000000, 4), (513, 64, 64), (300, 9000, 1000),
     (700001, 900000, 4), (1000003, 70, 4), (1600001, 20000, 4),
+    (337, 286356, 9), (64, 100000, 18), (20, 1192, 54),
     (8192, 300, 8), (8193, 70000, 8), (20000, 5, 16), (65536, 3000, 8), (65537, 3000, 8),
 ]
 
