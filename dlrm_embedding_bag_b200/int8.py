@@ -172,8 +172,8 @@ def linear_int8(x_q: torch.Tensor, x_scale: torch.Tensor, w_q: torch.Tensor,
         _, od, rows, cols, ldo = _matrix(out, "out", index)
         if rows != M or cols != N:
             raise ValueError(f"out must be ({M}, {N}) (got {tuple(out.shape)})")
-    # a single row's pitch is not used to find another one: its own length will do
-    if M == 1:
+    # the pitch of a single row, or of none, is not used to find another: a length will do
+    if M <= 1:
         ldx = (ldx + 15) // 16 * 16
     if N == 1:
         ldw = (ldw + 15) // 16 * 16

@@ -176,6 +176,26 @@ def test_empty_batches(int8):
     assert int8.dequantize_rows(q, s).shape == (0, 32)
 
 
+@pytest.mark.parametrize("K", [1, 32, 33, 592, 1001])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_empty_batches_of_any_width(int8, K, dt):
+    """Through the norm, the layer and a network: no rows in, no rows out."""
+    from dlrm_embedding_bag_b200 import mlp
+
+    x = torch.empty((0, K), device=DEV, dtype=DT[dt])
+    w, ws = int8.quantize_rows(torch.ones((5, K), device=DEV))
+    for q, s, h in ((*int8.quantize_rows(x), None),
+                    int8.rms_norm_int8(x, torch.ones(K, device=DEV), residual=x)):
+        assert q.shape == (0, K) and s.shape == (0,)
+        assert h is None or (h.shape == (0, K) and h.dtype == x.dtype)
+        assert int8.linear_int8(q, s, w, ws, ws, "relu", out_dtype=x.dtype).shape == (0, 5)
+        # a buffer of the binding's own making, as a caller keeps it between batches
+        assert int8.linear_int8(int8.int8_empty(0, K), s, w, ws).shape == (0, 5)
+    net = mlp.MLP(mlp.int8_layers(_weights(_gen(1), [K, 37, 3])), mode="int8")
+    y32, y16 = net.forward(x, last_bf16=True)
+    assert y32.shape == (0, 3) and y16.shape == (0, 3)
+
+
 # ------------------------------------------------------------------------- layer
 
 
