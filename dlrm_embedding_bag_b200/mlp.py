@@ -62,6 +62,8 @@ def to_bf16(x: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor
     if out is None:
         out = bf16_empty(rows, cols, x.device)
     py, ldy = _pitched(out, "out", torch.bfloat16)
+    if rows == 0:  # nothing to round, and no pointers for the entry point
+        return out
     ops._check(ops._lib.dlrm_f32_to_bf16(px, ldx, rows, cols, py, ldy, ops._stream()),
                "dlrm_f32_to_bf16")
     return out
