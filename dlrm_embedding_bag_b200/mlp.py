@@ -214,9 +214,11 @@ class MLP:
     ``norms[i]`` is given (f32 ``(K,)``), normed and rounded
     (:func:`.int8.rms_norm_int8`). Layers with a norm that follow each other at
     one width form a residual stack: the norm in front of layer i reads the sum
-    of the sum before it and layer i-1's output. Activations between layers are
-    bf16: what an 8-bit level (2^-8 of its row's maximum) is rounded from need
-    not be finer.
+    of the sum before it and layer i-1's output. The first sum is the first of
+    these layers' input. A stack's last output does not have the sum added.
+    Activations between layers, and the sums, are bf16 (an f32 input of a stack is
+    rounded as its first sum): what an 8-bit level (2^-8 of its row's maximum) is
+    rounded from need not be finer.
     """
 
     def __init__(self, layers: Sequence[Tuple[torch.Tensor, torch.Tensor, str]],
@@ -252,11 +254,14 @@ class MLP:
             if self.norms[i] is None:
                 q, s = int8.quantize_rows(h)
                 total = None
-            elif total is not None and total.shape == h.shape and total.dtype == h.dtype:
+            elif total is not None and total.shape == h.shape:
                 q, s, total = int8.rms_norm_int8(h, self.norms[i], residual=total, eps=self.eps)
             else:
                 q, s, _ = int8.rms_norm_int8(h, self.norms[i], eps=self.eps)
-                total = h
+                total = None
+                # a stack goes on by widths alone: its sum has the activations' type at once
+                if i + 1 < n and self.norms[i + 1] is not None and w_q.shape[0] == h.shape[1]:
+                    total = h if h.dtype == torch.bfloat16 else to_bf16(h)
             inputs.append((q, s))
             dtype = torch.float32 if i == n - 1 and last_f32 else torch.bfloat16
             h = int8.linear_int8(q, s, w_q, w_scale, b, act, out_dtype=dtype)

@@ -385,6 +385,34 @@ def test_mlp_of_int8_layers(int8, M, dt):
     assert none is None and yb.dtype == BF16 and torch.equal(yb.float(), y32.to(BF16).float())
 
 
+@pytest.mark.parametrize("M", [0, 1, 70])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("widths", [[96] * 5, [40, 40, 40, 33, 33, 33]])
+def test_residual_stack_that_begins_with_the_input(int8, M, dt, widths):
+    """Norms on every layer: the stack starts at the input, whatever the input's type.
+    Where widths change it starts again."""
+    from dlrm_embedding_bag_b200 import mlp
+
+    g = _gen(M + len(widths))
+    layers = mlp.int8_layers(_weights(g, widths))
+    norms = [torch.empty(k, device=DEV).normal_(1, 0.2, generator=g) for k in widths[:-1]]
+    net = mlp.MLP(layers, mode="int8", norms=norms)
+    x = _normal(g, M, widths[0], DT[dt])
+    (y, _), inputs = net.forward(x, keep=True)
+    assert y.shape == (M, widths[-1])
+    h, total = x, None
+    for i, (((wq, ws), b, act), (q, s)) in enumerate(zip(layers, inputs)):
+        rows = h.double()
+        if total is not None and total.shape == h.shape:
+            rows = rows + total.double()
+        total = rows.float().to(BF16)  # the running sum, rounded once
+        rows = rows / torch.sqrt(rows.square().mean(1, keepdim=True)
+                                 + np.float64(np.float32(1e-6))) * norms[i].double()
+        if M:
+            _check_rows(q, s, rows, rows.shape[1], f"layer {i}")
+        h = int8.linear_int8(q, s, wq, ws, b, act, out_dtype=BF16)
+
+
 def test_dlrm_forward_in_int8(int8):
     """The whole forward on 8-bit layers: each stage against 64 bits on its own
     inputs, and the captured graph against the eager call."""

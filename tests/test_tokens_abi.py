@@ -229,3 +229,35 @@ def test_calls_run_on_their_tensors_device(tokens, monkeypatch):
         tokens._call(entry, "entry", 1, (7,))
     assert e.value.status == -2 and current == [0]
     assert isinstance(e.value, tokens.ops.DlrmError)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("last_f32", [True, False])
+def test_residual_stack_does_not_depend_on_the_inputs_type(tokens, monkeypatch, dtype, last_f32):
+    """Which norms of an 8-bit network read a residual, and which: by widths alone."""
+    from dlrm_embedding_bag_b200 import int8, mlp
+
+    calls = []
+
+    def norm(x, weight=None, *, residual=None, eps=1e-6):
+        assert residual is None or residual.dtype == x.dtype
+        calls.append(None if residual is None else residual.float().sum().item())
+        total = None if residual is None else x + residual
+        return x, torch.ones(x.shape[0]), total
+
+    def linear(q, s, w_q, w_scale, bias, act, *, out_dtype):
+        # every layer doubles its input's first columns
+        return (2 * q.float()[:, :1]).expand(-1, w_q.shape[0]).to(out_dtype)
+
+    monkeypatch.setattr(int8, "rms_norm_int8", norm)
+    monkeypatch.setattr(int8, "linear_int8", linear)
+    monkeypatch.setattr(mlp, "to_bf16", lambda t: t.to(torch.bfloat16))
+    layers = [((torch.zeros((n, k), dtype=torch.int8), torch.ones(n)), None, "none")
+              for k, n in ((8, 8), (8, 8), (8, 8), (8, 4), (4, 4), (4, 2))]
+    net = mlp.MLP(layers, mode="int8", norms=[torch.ones(k) for k in (8, 8, 8, 8, 4, 4)])
+    y32, y16 = net.forward(torch.ones((1, 8), dtype=dtype), last_f32=last_f32,
+                           last_bf16=not last_f32)
+    # sums before it: 1; 1 + 2; 3 + 4; then four columns wide, from 16 on
+    assert calls == [None, 8 * 1.0, 8 * 3.0, 8 * 7.0, None, 4 * 16.0]
+    y = y32 if last_f32 else y16
+    assert y.dtype == (torch.float32 if last_f32 else torch.bfloat16) and (y == 64).all()
