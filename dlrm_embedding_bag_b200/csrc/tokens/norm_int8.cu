@@ -18,6 +18,9 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kNormThreads = 512;  // of a row that does not fit registers
 constexpr uint32_t kInfBits = 0x7f800000u;
+// Below this, a largest value of f32 has others of its row that count among the
+// subnormals, and 127 over it leaves f32.
+constexpr float kTiny = 1e-30f;
 
 struct NormArgs {
   const void* x;
@@ -57,8 +60,14 @@ __device__ __forceinline__ void row_sum_max(float& sum, uint32_t& top) {
   }
 }
 
-// |t|'s bits: as unsigned numbers they order like |t|, infinities and NaNs last.
-__device__ __forceinline__ uint32_t abs_bits(float t) { return __float_as_uint(t) & 0x7fffffffu; }
+// Whether any of the row's threads says so.
+template <int THREADS>
+__device__ __forceinline__ bool row_any(bool mine) {
+  if constexpr (THREADS > 32)
+    return __syncthreads_or(mine);
+  else
+    return __any_sync(kFull, mine);
+}
 
 // max(|t|, top), NaN if either is.
 __device__ __forceinline__ float max_abs(float top, float t) {
@@ -77,7 +86,7 @@ struct Levels {
 __device__ __forceinline__ Levels levels_of(uint32_t top) {
   const float A = __uint_as_float(top);
   Levels f;
-  f.pre = A < 1e-30f ? 0x1p100f : 1.f;
+  f.pre = A < kTiny ? 0x1p100f : 1.f;
   f.inv = (top == 0 || top >= kInfBits) ? 0.f : __fdiv_rn(127.f, A * f.pre);
   return f;
 }
@@ -149,31 +158,88 @@ __device__ __forceinline__ void store_levels(int8_t* p, float (&t)[VEC], Levels 
   }
 }
 
-// The squares of a row left the range of f32 (or vanished in it) although the
-// row itself did not: its scale from squares of h / max|h|. `each` calls its
-// argument with every h of the thread.
-template <int THREADS, class Each>
-__device__ float far_scale(const NormArgs& a, uint32_t top, Each each) {
-  float sum = 0.f;
-  uint32_t hbits = 0;
-  each([&](float h) { hbits = max(hbits, abs_bits(h)); });
-  row_sum_max<THREADS>(sum, hbits);
-  const float big = __uint_as_float(hbits);
-  sum = 0.f;
-  each([&](float h) {
-    const float s = __fdiv_rn(h, big);
-    sum += s * s;
-  });
-  uint32_t unused = 0;
-  row_sum_max<THREADS>(sum, unused);
-  const double mean = static_cast<double>(big) * big * (static_cast<double>(sum) / a.K) + a.eps;
-  return static_cast<float>(static_cast<double>(__uint_as_float(top)) / sqrt(mean) / 127.0);
+// Sum, maximum and whether any is set, over the THREADS threads of a row, which all get them.
+template <int THREADS>
+__device__ __forceinline__ void row_join_f64(double& sum, double& top, bool& any) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    sum += __shfl_xor_sync(kFull, sum, o);
+    top = fmax(top, __shfl_xor_sync(kFull, top, o));
+  }
+  any = __any_sync(kFull, any);
+  if constexpr (THREADS > 32) {
+    __shared__ double sums[THREADS / 32], tops[THREADS / 32];
+    __syncthreads();  // an earlier row's values have been read
+    if ((threadIdx.x & 31) == 0) {
+      sums[threadIdx.x >> 5] = sum;
+      tops[threadIdx.x >> 5] = top;
+    }
+    any = __syncthreads_or(any);
+    sum = top = 0.0;
+    for (int w = 0; w < THREADS / 32; ++w) {
+      sum += sums[w];
+      top = fmax(top, tops[w]);
+    }
+  }
 }
 
-// Whether a row's scale has to be far_scale's: the mean of its squares, which are
-// finite numbers or more, is above f32 or so small that squares have vanished.
-__device__ __forceinline__ bool is_far(const NormArgs& a, float sum, uint32_t top) {
-  if (!a.norm || top == 0 || top >= kInfBits) return false;
+// A row in 64 bits, from memory (nothing of it may have been written before): where
+// squares or products with the weight leave the range of f32 or vanish in it although
+// the normed row need not. In 64 bits neither does: factors of 2^-149 to 2^128.
+template <class T, int THREADS>
+__device__ __forceinline__ void row_in_f64(const NormArgs& a, int64_t m) {
+  const int q = threadIdx.x % THREADS;
+  auto load = [&](int c, double& t) {
+    float h[1], w[1];
+    load_h<T, 1>(a, m, c, h);
+    load_weight<1>(a, c, w);
+    t = static_cast<double>(h[0]) * w[0];
+    return h[0];
+  };
+  double sum = 0.0, top = 0.0;
+  bool bad = false;  // a NaN or an infinity
+  for (int c = q; c < a.K; c += THREADS) {
+    double t;
+    const double h = load(c, t);
+    sum += h * h;
+    top = fmax(top, fabs(t));
+    bad |= !(fabs(t) <= DBL_MAX);
+  }
+  row_join_f64<THREADS>(sum, top, bad);
+  const bool none = bad || top == 0.0;
+  if (q == 0)
+    a.scale[m] = bad     ? __uint_as_float(0x7fc00000u)
+                 : none  ? 0.f
+                         : static_cast<float>(top / sqrt(sum / a.K + a.eps) / 127.0);
+  const double inv = none ? 0.0 : 127.0 / top;
+  for (int c = q; c < a.K; c += THREADS) {
+    double t;
+    const float h[1] = {load(c, t)};
+    if (a.h_out != nullptr) store_f32<T, 1>(static_cast<T*>(a.h_out) + m * a.ldh + c, h);
+    a.q[m * a.ldq + c] = none ? 0 : static_cast<int8_t>(__double2int_rn(t * inv));
+  }
+}
+
+// ... where a block has the row: as a call, with the arguments by value, since its code
+// inside a kernel costs the kernel's other rows their registers (6000 rows of 6001 with
+// a residual: 106 us so, 162 inside, 170 with the arguments by reference; rows of a
+// warp lose nothing by it inside, and 45 against 37 us by a call, 60000 of 250 bf16).
+template <class T, int THREADS>
+__device__ __noinline__ void block_row_in_f64(const NormArgs a, int64_t m) {
+  row_in_f64<T, THREADS>(a, m);
+}
+
+// Whether a row is row_in_f64's: the mean of its squares, which are finite numbers or
+// more, is above f32 or so small that squares have vanished; or its products with the
+// weight have left f32, or are so small that some may have vanished. A row of zeros is
+// not: `zeros` tells, asked only where squares and products are all zero.
+template <class Zeros>
+__device__ __forceinline__ bool is_far(const NormArgs& a, float sum, uint32_t top, Zeros zeros) {
+  if (!a.norm) return false;
+  if (top >= kInfBits) return a.weight != nullptr;
+  if (top == 0 && sum == 0.f) return a.weight != nullptr && !zeros();
+  if (a.weight != nullptr && __uint_as_float(top) < kTiny) return true;
+  if (top == 0) return false;
   return !(sum + a.eps <= FLT_MAX) || __fmaf_rn(a.eps, static_cast<float>(a.K), sum) < 1e-30f * a.K;
 }
 
@@ -246,16 +312,22 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, kBlocksAnSM<VEC, TPR, C
   }
   uint32_t top = __float_as_uint(most);
   row_sum_max<TPR>(sum, top);
-  const bool far = is_far(a, sum, top);  // the same for the whole row
-  float s = 0.f;
-  if (far)
-    s = far_scale<TPR>(a, top, [&](auto f) {
+  const bool far = is_far(a, sum, top, [&] {
+    bool any = false;
 #pragma unroll
-      for (int i = 0; i < CH; ++i)
+    for (int i = 0; i < CH; ++i)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) f(h[i][e]);  // past the row: 0
-    });
-  if (q == 0) a.scale[m] = far ? s : scale_of(a, sum, top);
+      for (int e = 0; e < VEC; ++e) any |= h[i][e] != 0.f;  // past the row: 0
+    return !row_any<TPR>(any);
+  });
+  if (far) {  // the same for the whole row
+    if constexpr (TPR > 32)
+      block_row_in_f64<T, TPR>(a, m);
+    else
+      row_in_f64<T, TPR>(a, m);
+    return;
+  }
+  if (q == 0) a.scale[m] = scale_of(a, sum, top);
   const Levels f = levels_of(top);
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
@@ -273,7 +345,8 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, kBlocksAnSM<VEC, TPR, C
 
 // Longer rows: a block for each row, which it reads twice (the second time from L2).
 template <class T, int VEC>
-__global__ void __launch_bounds__(kNormThreads) norm_loop_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(kNormThreads)
+    norm_loop_kernel(const NormArgs a) {
   for (int64_t m = blockIdx.x; m < a.M; m += gridDim.x) {
     float sum = 0.f, most = 0.f;
     for (int c = threadIdx.x * VEC; c < a.K; c += kNormThreads * VEC) {
@@ -288,18 +361,21 @@ __global__ void __launch_bounds__(kNormThreads) norm_loop_kernel(const NormArgs 
     }
     uint32_t top = __float_as_uint(most);
     row_sum_max<kNormThreads>(sum, top);
-    const bool far = is_far(a, sum, top);
-    float s = 0.f;
-    if (far)  // reads the row again, before anything of it is written
-      s = far_scale<kNormThreads>(a, top, [&](auto f) {
-        for (int c = threadIdx.x * VEC; c < a.K; c += kNormThreads * VEC) {
-          float h[VEC];
-          load_h<T, VEC>(a, m, c, h);
+    const bool far = is_far(a, sum, top, [&] {
+      bool any = false;
+      for (int c = threadIdx.x * VEC; c < a.K; c += kNormThreads * VEC) {
+        float h[VEC];
+        load_h<T, VEC>(a, m, c, h);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) f(h[e]);
-        }
-      });
-    if (threadIdx.x == 0) a.scale[m] = far ? s : scale_of(a, sum, top);
+        for (int e = 0; e < VEC; ++e) any |= h[e] != 0.f;
+      }
+      return !row_any<kNormThreads>(any);
+    });
+    if (far) {
+      block_row_in_f64<T, kNormThreads>(a, m);
+      continue;
+    }
+    if (threadIdx.x == 0) a.scale[m] = scale_of(a, sum, top);
     const Levels f = levels_of(top);
     for (int c = threadIdx.x * VEC; c < a.K; c += kNormThreads * VEC) {
       float h[VEC], w[VEC];

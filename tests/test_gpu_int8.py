@@ -156,6 +156,58 @@ def test_eps_that_leaves_f32_with_the_squares(int8, K):
         _check_rows(q, s, y, K, f"eps={eps}")
 
 
+@pytest.mark.parametrize("K", [5, 64, 1000, 1001, 4096, 6924, 20000, 20001])
+@pytest.mark.parametrize("M", [9, 700])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [1.0, 1e20, 1e-20, 1e-35])
+@pytest.mark.parametrize("residual", [False, True])
+def test_products_with_the_weight_that_leave_f32(int8, K, M, dt, size, residual):
+    """Finite rows, weights and normed rows, with h * weight above f32's largest value
+    or among its subnormals and zeros: q and scale hold y all the same. (x and residual
+    do not overlap, so h is exact. A scale among f32's subnormals is off by half of
+    their step, 2^-150, besides.)"""
+    g = _gen(K + M)
+    w = torch.empty(K, device=DEV).normal_(1, 0.3, generator=g) * size
+    w[K // 2] = 0.0
+    x = _normal(g, M, K).clamp(-4, 4)
+    for i, f in enumerate((8e37, 1e30, 1e-10, 1e-25, 1e-30, 1e-38)):
+        x[i] *= f
+    x[6] = 0.0
+    x[7] = 0.0
+    x[7, 1] = 3e5        # one value, at a weight
+    x[8] = 0.0
+    x[8, K // 2] = 2.0   # ... and where the weight is zero
+    x = x.to(DT[dt])
+    r = None
+    if residual:
+        odd = torch.arange(K, device=DEV) % 2 == 1
+        r = torch.where(odd, x, torch.zeros_like(x))
+        x = torch.where(odd, torch.zeros_like(x), x)
+    h = x.double() + (r.double() if residual else 0.0)
+    for eps in (0.0, 1e-6):
+        q, s, total = int8.rms_norm_int8(x, w, residual=r, eps=eps)
+        y = h / torch.sqrt(h.square().mean(1, keepdim=True) + np.float64(np.float32(eps))
+                           + (h == 0).all(1, keepdim=True))
+        y = y * w.double()
+        exact = y.abs().amax(1) / 127.0
+        assert ((s.double() - exact).abs() <= ((K + 3) / 2 + 8) * U * exact + 2.0 ** -149).all()
+        live = exact > 0
+        v = y[live] / exact[live][:, None]
+        assert ((q[live].double() - v).abs() <= 0.5 + 127 * 8 * U).all()
+        assert (q[~live] == 0).all() and (s[~live] == 0).all()
+        if residual:
+            assert torch.equal(total.double(), h)
+    if residual:  # the sum over its own residual: a row is read before it is written
+        q2, s2, h2 = int8.rms_norm_int8(x, w, residual=r, residual_out=r, eps=1e-6)
+        assert h2 is r and torch.equal(r.double(), h)
+        assert torch.equal(q2, q) and torch.equal(s2, s)
+    x[0, K - 1] = float("inf")
+    x[1, 0] = float("nan")
+    x[2, K // 2] = -float("inf")
+    q, s, _ = int8.rms_norm_int8(x, w)
+    assert torch.isnan(s[:3]).all() and (q[:3] == 0).all() and not torch.isnan(s[3:]).any()
+
+
 def test_values_of_rows(int8):
     g = _gen(4)
     for M, K in ((1, 1), (5, 16), (40, 100), (3, 4099), (7, 1026), (2, 2), (300, 33)):
