@@ -19,7 +19,8 @@
 //     K; the int32 parts meet through distributed shared memory (exact, so the
 //     split changes no bit).
 // Every wait is bounded; one that runs out sets DLRM_FLAG_TIMEOUT in the
-// optional status word, and the CTA still frees its tensor memory and exits.
+// optional status word, and the CTA still lets its loads land, frees its tensor
+// memory and exits.
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -27,6 +28,7 @@
 
 #include "common.h"
 #include "dlrm_int8.h"
+#include "ring_landing.h"
 #include "tcgen05_common.cuh"
 
 namespace dlrm {
@@ -102,6 +104,21 @@ __device__ __forceinline__ uint4 load_cluster_v4(uint32_t cluster_addr) {
   uint4 v;
   asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
+  return v;
+}
+
+// A word of a CTA of the cluster that orders nothing else, by its shared::cluster
+// address (its own shared::cta address is one).
+__device__ __forceinline__ void store_cluster_u32(uint32_t cluster_addr, uint32_t v) {
+  asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t load_cluster_u32(uint32_t cluster_addr) {
+  uint32_t v;
+  asm volatile("ld.relaxed.cluster.shared::cluster.u32 %0, [%1];"
+               : "=r"(v)
                : "r"(cluster_addr)
                : "memory");
   return v;
@@ -291,6 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* mma_done = acc_empty + 2;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  uint32_t* other_steps = tslot + 1;  // of a pair's second producer, told at its end
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = (PAIR || SPLIT) ? cluster_ctarank() : 0u;
   const int unit0 = (PAIR || SPLIT) ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
@@ -315,6 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(mma_done, 1);
     mbar_init_fence();
+    if constexpr (PAIR) *other_steps = ~0u;
   }
   tc_fence_before_sync();
   if constexpr (PAIR)
@@ -360,11 +379,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (timed_out && rank == 0) {
-        // this CTA's copies in flight land before it leaves
-        for (int i = max(0, g - R::kStages); i < g; ++i)
-          (void)mbar_wait_bounded(&full[i % R::kStages], (i / R::kStages) & 1, kWaitLimit);
-      }
+      // no load is in flight once this CTA leaves, whoever gave up
+      land_loads<R::kStages, PAIR>(
+          !PAIR || rank == 0, timed_out, g,
+          [&](int s, uint32_t parity) { (void)mbar_wait_bounded(&full[s], parity, kWaitLimit); },
+          [&](int s) { mbar_arrive_expect_tx(&full[s], R::kStage); },
+          [&](int steps) {
+            store_cluster_u32(map_to_cta(smem_u32(other_steps), 0), static_cast<uint32_t>(steps));
+          },
+          [&] {
+            // the other producer takes a step more for each stage at most, and gives up
+            const long long t0 = clock64();
+            int steps;
+            do {
+              steps = static_cast<int>(load_cluster_u32(smem_u32(other_steps)));
+            } while (steps < 0 && clock64() - t0 < (R::kStages + 2) * kWaitLimit);
+            return steps;
+          });
     }
   } else if (warp == 1) {
     if (lane == 0 && (!PAIR || rank == 0)) {
