@@ -243,8 +243,8 @@ struct JoinCall {
     for (int e = 0; e < 4; ++e) {
       ch[e] = {0.f, 0.f, n + e < a.N};
       if (ch[e].live) {
-        ch[e].ws = __ldg(a.w_scale + n + e);
-        ch[e].b = a.bias != nullptr ? __ldg(a.bias + n + e) : 0.f;
+        ch[e].ws = a.w_scale[n + e];
+        ch[e].b = a.bias != nullptr ? a.bias[n + e] : 0.f;
       }
     }
     for (int cb = c0 + ew * kCols; cb < c1; cb += kEpiWarps * kCols) {
@@ -253,7 +253,7 @@ struct JoinCall {
 #pragma unroll
       for (int i = 0; i < kCols; ++i) {
         const bool live = cb + i < c1 && m0 + cb + i < a.M;
-        xs[i] = live ? __ldg(a.x_scale + m0 + cb + i) : 0.f;
+        xs[i] = live ? a.x_scale[m0 + cb + i] : 0.f;
 #pragma unroll
         for (int k = 0; k < S; ++k) {
           v[i][k] = make_uint4(0, 0, 0, 0);
@@ -342,9 +342,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = *tslot;
-  // Everything below may come from the kernel before (the levels, the scales),
-  // so every role waits for its end. This grid lets none start before its own
-  // end: the bf16 layers read their bias without waiting.
+  // Everything below may come from the kernel before (the levels, the scales), which
+  // may still be at work, so every role waits for its end. The loads behind the wait
+  // are ordinary ones: those of the read-only path (__ldg, .nc) may be moved in front
+  // of it, and ask that nothing writes the memory while this kernel runs. This grid lets
+  // none start before its own end: the bf16 layers read their bias without waiting.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   bool timed_out = false;
 
@@ -451,12 +453,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       Channel ch = {0.f, 0.f, n < args.N};
       if constexpr (!SPLIT) {
         if (ch.live) {
-          ch.ws = __ldg(args.w_scale + n);
-          ch.b = args.bias != nullptr ? __ldg(args.bias + n) : 0.f;
+          ch.ws = args.w_scale[n];
+          ch.b = args.bias != nullptr ? args.bias[n] : 0.f;
         }
         __syncwarp();  // the slice's readers of the tile before are done
         for (int c = c_begin + lane; c < c_end; c += 32)
-          xs[c - c_begin] = m0 + c < args.M ? __ldg(args.x_scale + m0 + c) : 0.f;
+          xs[c - c_begin] = m0 + c < args.M ? args.x_scale[m0 + c] : 0.f;
         __syncwarp();
       }
       if (!__all_sync(kFull, mbar_wait_bounded(&acc_full[b], (j >> 1) & 1, kWaitLimit))) {
@@ -530,9 +532,10 @@ struct VecArgs {
 
 __device__ __forceinline__ uint4 load_once(const int8_t* p) {
   uint4 r;
-  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-      : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-      : "l"(p));
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p)
+               : "memory");
   return r;
 }
 
@@ -552,9 +555,9 @@ __device__ __forceinline__ void put_sums(const VecArgs& a, int n0, const int (&a
     for (int m = 0; m < MT; ++m)
       if (lane == r * MT + m && n0 + r < a.lin.N && m < a.lin.M) {
         const int n = n0 + r;
-        const Channel ch = {__ldg(a.lin.w_scale + n),
-                            a.lin.bias != nullptr ? __ldg(a.lin.bias + n) : 0.f, true};
-        put<ACT, Out>(a.lin, ch, n, m, acc[r][m], __ldg(a.lin.x_scale + m));
+        const Channel ch = {a.lin.w_scale[n],
+                            a.lin.bias != nullptr ? a.lin.bias[n] : 0.f, true};
+        put<ACT, Out>(a.lin, ch, n, m, acc[r][m], a.lin.x_scale[m]);
       }
 }
 
@@ -599,7 +602,7 @@ __global__ void __launch_bounds__(kVecThreads) linear_few_kernel(const VecArgs a
       uint4 xv[MT];
       const int k = min(k0 + u * 512, whole - 16);  // past the end: against zeros
 #pragma unroll
-      for (int m = 0; m < MT; ++m) xv[m] = __ldg(reinterpret_cast<const uint4*>(x[m] + k));
+      for (int m = 0; m < MT; ++m) xv[m] = *reinterpret_cast<const uint4*>(x[m] + k);
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -610,9 +613,9 @@ __global__ void __launch_bounds__(kVecThreads) linear_few_kernel(const VecArgs a
   if (whole + lane < a.K) {
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int v = __ldg(w[r] + whole + lane);
+      const int v = w[r][whole + lane];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) acc[r][m] += v * __ldg(x[m] + whole + lane);
+      for (int m = 0; m < MT; ++m) acc[r][m] += v * x[m][whole + lane];
     }
   }
   __syncwarp();

@@ -389,6 +389,38 @@ def test_streams_and_graphs(int8):
         _check_layer(y, q, s, wq, ws, None, "none")
 
 
+@pytest.mark.parametrize("M", [1, 2, 4, 20, 300, 2000])
+@pytest.mark.parametrize("N,K", [(256, 512), (700, 4096)])
+def test_layer_waits_for_what_the_kernel_before_it_writes(int8, M, N, K):
+    """A bf16 layer lets the kernel behind it start before it ends: an 8-bit layer whose
+    scales and bias are the last rows of its output gets them all the same, and so for
+    weights and rows that a rounding has just written."""
+    from dlrm_embedding_bag_b200 import mlp
+
+    g = _gen(M + N + K)
+    rows, width = 60000, max(M, N)
+    a, b = _normal(g, rows, 64, BF16), _normal(g, width, 64, BF16)
+    y = torch.empty((rows, width), device=DEV)
+    w, x = _normal(g, N, K), _normal(g, M, K)
+    wq, xq = int8.int8_empty(N, K), int8.int8_empty(M, K)
+    scale = torch.empty(max(M, N), device=DEV)
+    for k in range(3):
+        y.fill_(float("nan"))
+        wq.fill_(99)
+        xq.fill_(77)
+        a.mul_(-0.5)
+        w.mul_(-0.5)
+        int8.quantize_rows(x, out=xq, scale_out=scale[:M])
+        int8.quantize_rows(w, out=wq, scale_out=scale[:N])
+        mlp.linear_bf16(a, b, out_f32=y)
+        got = int8.linear_int8(xq, y[-1, :M], wq, y[-2, :N], y[-3, :N])
+        int8.quantize_rows(w, out=wq, scale_out=scale[:N])
+        again = int8.linear_int8(xq, y[-1, :M], wq, y[-2, :N], y[-3, :N])
+        torch.cuda.synchronize()
+        _check_layer(got, xq, y[-1, :M].clone(), wq, y[-2, :N].clone(), y[-3, :N].clone(), "none")
+        assert torch.equal(got, again)
+
+
 # ------------------------------------------------------------------ whole networks
 
 
