@@ -51,3 +51,16 @@ def test_kernels_that_start_early_read_nothing_through_the_read_only_path():
     assert len(early) >= 4
     for k in early:
         assert "__ldg" not in k
+
+
+def test_tensor_memory_loads_are_waited_for_in_their_own_statement():
+    """Registers that a tcgen05.ld fills arrive with its wait: no statement may come between."""
+    found = 0
+    for path in glob.glob(os.path.join(os.path.dirname(TOKENS), "*.cu*")) + SOURCES:
+        for volatile, text in _asm_statements(_code(path)):
+            if "tcgen05.ld." in text:
+                found += 1
+                assert volatile and "tcgen05.wait::ld" in text and '"memory"' in text, path
+            else:
+                assert "tcgen05.wait::ld" not in text, path
+    assert found >= 1
