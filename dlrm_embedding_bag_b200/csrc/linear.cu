@@ -41,6 +41,7 @@
 
 #include "dlrm_mlp.h"
 #include "launch.h"
+#include "ring_landing.h"
 #include "tcgen05_common.cuh"
 
 namespace dlrm {
@@ -244,6 +245,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* mma_done = acc_empty + 2;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(mma_done + 1);
+  uint32_t* other_steps = tslot + 1;  // of a pair's second producer, told at its end
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // CTA pairs: rank in the pair (0 = the MMA issuer), pair index and count
   const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
@@ -267,6 +269,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
     mbar_init(mma_done, 1);
     mbar_init_fence();
+    if constexpr (PAIR) *other_steps = ~0u;
   }
   tc_fence_before_sync();
   if constexpr (PAIR)
@@ -325,6 +328,13 @@ __global__ void __launch_bounds__(kLinThreads, 1)
           }
         }
       }
+      // no load is in flight once this CTA leaves, whoever gave up
+      land_loads<L::kStages, PAIR>(
+          rank == 0, timed_out, g,
+          [&](int s, uint32_t parity) { (void)mbar_wait_bounded(&full[s], parity, kLinWaitLimit); },
+          [&](int s) { mbar_arrive_expect_tx(&full[s], L::kStage); },
+          [&](int steps) { tell_steps(other_steps, steps); },
+          [&] { return told_steps(other_steps, (L::kStages + 2) * kLinWaitLimit); });
     }
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {

@@ -125,4 +125,28 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
+// A pair's second producer tells the first how many steps it issued, at its end, by a
+// word of the first one's shared memory at `word`'s offset, which is set to ~0 before.
+// It orders nothing else.
+__device__ __forceinline__ void tell_steps(uint32_t* word, int steps) {
+  asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], %1;" ::"r"(
+                   map_to_cta(smem_u32(word), 0)),
+               "r"(steps)
+               : "memory");
+}
+// ... and the first, in its own shared memory, waits for that number: negative if it was
+// not told within about `limit` clock cycles. (The second takes a step more for each
+// stage at most once the first has stopped, and then gives up as well.)
+__device__ __forceinline__ int told_steps(const uint32_t* word, long long limit) {
+  const long long t0 = clock64();
+  int steps;
+  do {
+    asm volatile("ld.relaxed.cluster.shared::cluster.u32 %0, [%1];"
+                 : "=r"(steps)
+                 : "r"(smem_u32(word))
+                 : "memory");
+  } while (steps < 0 && clock64() - t0 < limit);
+  return steps;
+}
+
 }  // namespace dlrm

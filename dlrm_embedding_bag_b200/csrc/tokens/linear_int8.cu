@@ -109,21 +109,6 @@ __device__ __forceinline__ uint4 load_cluster_v4(uint32_t cluster_addr) {
   return v;
 }
 
-// A word of a CTA of the cluster that orders nothing else, by its shared::cluster
-// address (its own shared::cta address is one).
-__device__ __forceinline__ void store_cluster_u32(uint32_t cluster_addr, uint32_t v) {
-  asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr), "r"(v)
-               : "memory");
-}
-__device__ __forceinline__ uint32_t load_cluster_u32(uint32_t cluster_addr) {
-  uint32_t v;
-  asm volatile("ld.relaxed.cluster.shared::cluster.u32 %0, [%1];"
-               : "=r"(v)
-               : "r"(cluster_addr)
-               : "memory");
-  return v;
-}
-
 template <int ACT>
 __device__ __forceinline__ float activate(float x) {
   if constexpr (ACT == DLRM_ACT_RELU) return x < 0.f ? 0.f : x;  // NaN stays NaN
@@ -386,18 +371,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           !PAIR || rank == 0, timed_out, g,
           [&](int s, uint32_t parity) { (void)mbar_wait_bounded(&full[s], parity, kWaitLimit); },
           [&](int s) { mbar_arrive_expect_tx(&full[s], R::kStage); },
-          [&](int steps) {
-            store_cluster_u32(map_to_cta(smem_u32(other_steps), 0), static_cast<uint32_t>(steps));
-          },
-          [&] {
-            // the other producer takes a step more for each stage at most, and gives up
-            const long long t0 = clock64();
-            int steps;
-            do {
-              steps = static_cast<int>(load_cluster_u32(smem_u32(other_steps)));
-            } while (steps < 0 && clock64() - t0 < (R::kStages + 2) * kWaitLimit);
-            return steps;
-          });
+          [&](int steps) { tell_steps(other_steps, steps); },
+          [&] { return told_steps(other_steps, (R::kStages + 2) * kWaitLimit); });
     }
   } else if (warp == 1) {
     if (lane == 0 && (!PAIR || rank == 0)) {

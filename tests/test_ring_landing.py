@@ -102,8 +102,9 @@ def test_all_loads_land_wherever_a_role_gives_up(tmp_path):
     assert int(r.stdout) > 10000
 
 
-@pytest.mark.parametrize("kernel", ["tokens/linear_int8.cu"])
-def test_the_layers_producer_ends_so(kernel):
+@pytest.mark.parametrize("kernel,leader", [("tokens/linear_int8.cu", "!PAIR || rank == 0"),
+                                           ("linear.cu", "rank == 0")])
+def test_the_layers_producer_ends_so(kernel, leader):
     """Every producer calls it, whatever happened: not under a condition on a give-up."""
     src = open(os.path.join(CSRC, kernel)).read()
     body = src[src.index("if (warp == 0) {"):src.index("} else if (warp == 1) {")]
@@ -111,4 +112,6 @@ def test_the_layers_producer_ends_so(kernel):
     # directly in the producer thread's block: two levels deep, behind the loop over tiles
     depth = body[:call].count("{") - body[:call].count("}")
     assert depth == 2
-    assert re.search(r"!PAIR \|\| rank == 0, timed_out, g,", body[call:])
+    assert re.search(r"\(\s*" + re.escape(leader) + r", timed_out, g,", body[call:])
+    # ranks other than 0 without a pair: only where a cluster splits a tile along K
+    assert ("SPLIT" in src) == ("!PAIR" in leader)
