@@ -521,29 +521,25 @@ __device__ __forceinline__ int dot16(const uint4& a, const uint4& b, int s) {
   return __dp4a(static_cast<int>(a.w), static_cast<int>(b.w), s);
 }
 
-template <int MT, int R, int ACT, class Out>
-__device__ __forceinline__ void put_sums(const VecArgs& a, int n0, const int (&acc)[R][MT]) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int r = 0; r < R; ++r)
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-      if (lane == r * MT + m && n0 + r < a.lin.N && m < a.lin.M) {
-        const int n = n0 + r;
-        const Channel ch = {a.lin.w_scale[n],
-                            a.lin.bias != nullptr ? a.lin.bias[n] : 0.f, true};
-        put<ACT, Out>(a.lin, ch, n, m, acc[r][m], a.lin.x_scale[m]);
-      }
-}
+// A lane's output of the R * MT, if it has one.
+struct FewOut {
+  Channel ch;
+  int n, m;
+  float xs;
+};
 
 template <int MT, int R>
 struct PutCall {
   const VecArgs& a;
-  int n0;
+  const FewOut& out;
   const int (&acc)[R][MT];
   template <int ACT, class Out>
   __device__ __forceinline__ void run() const {
-    put_sums<MT, R, ACT, Out>(a, n0, acc);
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < R * MT; ++i)
+      if ((threadIdx.x & 31) == i) sum = acc[i / MT][i % MT];
+    if (out.ch.live) put<ACT, Out>(a.lin, out.ch, out.n, out.m, sum, out.xs);
   }
 };
 
@@ -593,12 +589,20 @@ __global__ void __launch_bounds__(kVecThreads) linear_few_kernel(const VecArgs a
       for (int m = 0; m < MT; ++m) acc[r][m] += v * x[m][whole + lane];
     }
   }
+  // the lane's scales and bias, on their way while the sums are joined; every lane
+  // loads some, without a branch
+  const int i = min(lane, R * MT - 1);
+  FewOut out = {{0.f, 0.f, lane < R * MT && n0 + i / MT < a.lin.N && i % MT < a.lin.M},
+                min(n0 + i / MT, a.lin.N - 1), min(i % MT, a.lin.M - 1), 0.f};
+  out.ch.ws = a.lin.w_scale[out.n];
+  if (a.lin.bias != nullptr) out.ch.b = a.lin.bias[out.n];
+  out.xs = a.lin.x_scale[out.m];
   __syncwarp();
 #pragma unroll
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int m = 0; m < MT; ++m) acc[r][m] = __reduce_add_sync(kFull, acc[r][m]);
-  by_kind(a.lin, PutCall<MT, R>{a, n0, acc});
+  by_kind(a.lin, PutCall<MT, R>{a, out, acc});
 }
 
 // 2-D map of an int8 matrix {K, rows} with the given pitch, box {128, box_rows},
