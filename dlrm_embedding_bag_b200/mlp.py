@@ -69,6 +69,12 @@ def to_bf16(x: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor
     return out
 
 
+def _to_bf16_there(x: torch.Tensor) -> torch.Tensor:
+    """:func:`to_bf16` on x's device, where the 8-bit layers around it run, current or not."""
+    with torch.cuda.device_of(x):
+        return to_bf16(x)
+
+
 def linear_bf16(a_lo: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor] = None,
                 act: str = "none", *, a_hi: Optional[torch.Tensor] = None, f32: bool = True,
                 bf16: bool = False, out_f32: Optional[torch.Tensor] = None,
@@ -261,12 +267,12 @@ class MLP:
                 total = None
                 # a stack goes on by widths alone: its sum has the activations' type at once
                 if i + 1 < n and self.norms[i + 1] is not None and w_q.shape[0] == h.shape[1]:
-                    total = h if h.dtype == torch.bfloat16 else to_bf16(h)
+                    total = h if h.dtype == torch.bfloat16 else _to_bf16_there(h)
             inputs.append((q, s))
             dtype = torch.float32 if i == n - 1 and last_f32 else torch.bfloat16
             h = int8.linear_int8(q, s, w_q, w_scale, b, act, out_dtype=dtype)
         y32 = h if last_f32 else None
-        y_n = None if not last_bf16 else to_bf16(h) if last_f32 else h
+        y_n = None if not last_bf16 else _to_bf16_there(h) if last_f32 else h
         return ((y32, y_n), inputs) if keep else (y32, y_n)
 
     def forward(self, x: torch.Tensor, *, a_hi: Optional[torch.Tensor] = None,

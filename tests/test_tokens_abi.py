@@ -261,3 +261,39 @@ def test_residual_stack_does_not_depend_on_the_inputs_type(tokens, monkeypatch, 
     assert calls == [None, 8 * 1.0, 8 * 3.0, 8 * 7.0, None, 4 * 16.0]
     y = y32 if last_f32 else y16
     assert y.dtype == (torch.float32 if last_f32 else torch.bfloat16) and (y == 64).all()
+
+
+def test_a_networks_rounding_runs_where_its_layers_do(tokens, monkeypatch):
+    """to_bf16 takes the current device's stream: MLP(mode="int8"), whose other calls run on
+    their tensors' device, makes that one current around it."""
+    from dlrm_embedding_bag_b200 import int8, mlp
+
+    inside, seen = [], []
+
+    class DeviceOf:
+        def __init__(self, t):
+            self.t = t
+
+        def __enter__(self):
+            inside.append(self.t)
+
+        def __exit__(self, *exc):
+            inside.pop()
+
+    def to_bf16(t):
+        seen.append(len(inside) == 1 and inside[0] is t)
+        return t.to(torch.bfloat16)
+
+    def norm(x, weight=None, *, residual=None, eps=1e-6):
+        return x, torch.ones(x.shape[0]), residual
+
+    monkeypatch.setattr(mlp.torch.cuda, "device_of", DeviceOf)
+    monkeypatch.setattr(mlp, "to_bf16", to_bf16)
+    monkeypatch.setattr(int8, "rms_norm_int8", norm)
+    monkeypatch.setattr(int8, "linear_int8",
+                        lambda q, s, w, ws, b, act, *, out_dtype: q.to(out_dtype))
+    layers = [((torch.zeros((8, 8), dtype=torch.int8), torch.ones(8)), None, "none")] * 2
+    net = mlp.MLP(layers, mode="int8", norms=[torch.ones(8)] * 2)
+    _, y16 = net.forward(torch.ones((2, 8)), last_bf16=True)
+    # the stack's first sum, and the last output's rounding
+    assert y16.dtype == torch.bfloat16 and seen == [True, True]
