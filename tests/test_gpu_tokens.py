@@ -197,6 +197,64 @@ def test_grad(tokens, T, rows, D, dt, kind):
     assert _same_bits(out, tokens.embedding_grad(grad, ids, rows, scale=0.3))
 
 
+@pytest.mark.parametrize("T,rows,D", [(400, 30, 64), (513, 40, 16), (8193, 300, 40), (30000, 17, 64),
+                                      (65536, 3000, 12), (65537, 64, 130), (150001, 70001, 4),
+                                      (170001, 3000, 128), (400007, 900, 100), (31000, 70, 4100),
+                                      (40000, 300, 258), (50001, 40, 33), (1000003, 70, 4),
+                                      (1310720, 100000, 16), (1600001, 20000, 4)])
+@pytest.mark.parametrize("dt,odt", [("f32", "f32"), ("bf16", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("kind", ["uniform", "skew", "one", "ends"])
+def test_grad_of_whole_numbers_is_exact(tokens, T, rows, D, dt, odt, kind):
+    """Whole numbers of at most 8: every partial sum is below 2^24 and exact in any order, so
+    no part of a long run can be lost, doubled or misplaced unseen. Each token's row is
+    another one, and one column counts the tokens."""
+    assert 8 * T < 2 ** 24
+    g = _gen(T + rows)
+    grad = torch.randint(-8, 9, (T, D), device=DEV, generator=g).to(IDS[dt])
+    grad[:, D // 2] = 1.0
+    ids = torch.from_numpy(_ids(T + 1, T, rows, kind)).to(DEV)
+    want = torch.zeros((rows, D), device=DEV, dtype=torch.float64)
+    want.index_add_(0, ids.long(), grad.double())
+    out = tokens.embedding_grad(grad, ids, rows, dtype=IDS[odt])
+    assert torch.equal(out, want.to(IDS[odt]))  # rounded once
+    # added to a table of whole numbers, with padding: one step of the sparse update
+    pad = int(torch.mode(ids).values) if kind != "one" else None
+    table = torch.randint(-100, 101, (rows, D), device=DEV, generator=g).float()
+    sums = want.clone()
+    if pad is not None:
+        sums[pad] = 0.0
+    after = (table.double() - 2.0 * sums).float()
+    assert 2 * 8 * T + 100 < 2 ** 25  # a sum's double and the table's value: even or small
+    small = (2.0 * sums).abs().amax(1) + 100 < 2 ** 24
+    tokens.embedding_grad(grad, ids, rows, scale=-2.0, padding_idx=pad, out=table, accumulate=True)
+    assert torch.equal(table[small], after[small])
+
+
+@pytest.mark.parametrize("T", [300, 3000, 70000])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_grad_past_32_bit_offsets(tokens, T, accumulate):
+    """A gradient of more than 2^31 elements (and, of many tokens, from as many): its last
+    rows are written, and all that no token names."""
+    rows, D = 70_000, 32768  # 2.3e9 elements
+    out = torch.empty((rows, D), dtype=BF16, device=DEV)
+    out.fill_(3.0 if accumulate else float("nan"))
+    grad = torch.ones((T, D), dtype=BF16, device=DEV)
+    ids = torch.arange(T, device=DEV, dtype=torch.int32) * 7 % 1000
+    ids[-5:] = torch.tensor([65535, 65536, rows - 2, rows - 1, rows - 1], device=DEV)
+    grad[-1] = 2.0
+    tokens.embedding_grad(grad, ids, rows, out=out, accumulate=accumulate)
+    base = 3.0 if accumulate else 0.0
+    want = torch.zeros(rows, device=DEV)
+    want.index_add_(0, ids.long(), grad[:, 0].float())
+    want = (want + base).to(BF16)
+    assert float(want[rows - 1]) == base + 3.0
+    for c in (0, 1, 4097, D - 1):
+        assert torch.equal(out[:, c], want)
+    # every element, in slices that leave room
+    for r in range(0, rows, 10_000):
+        assert bool((out[r:r + 10_000] == want[r:r + 10_000, None]).all())
+
+
 @pytest.mark.parametrize("dt,odt", [("f32", "bf16"), ("bf16", "f32")])
 @pytest.mark.parametrize("T,D", [(900, 64), (9000, 60), (500, 7)])
 def test_grad_types_and_padding(tokens, T, D, dt, odt):
