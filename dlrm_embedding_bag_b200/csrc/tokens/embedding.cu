@@ -156,7 +156,21 @@ struct FillArgs {
   char* out;      // null: nothing to fill
   int64_t rows;   // of row_bytes each, pitch bytes apart
   int64_t row_bytes, pitch;
+  int unit;  // bytes of the widest store that every row allows: 16, 8, 4 or 2
+
+  bool apart() const { return pitch != row_bytes; }
 };
+
+__device__ __forceinline__ void put_zeros(char* p, int unit) {
+  if (unit == 16)
+    *reinterpret_cast<uint4*>(p) = make_uint4(0, 0, 0, 0);
+  else if (unit == 8)
+    *reinterpret_cast<uint2*>(p) = make_uint2(0, 0);
+  else if (unit == 4)
+    *reinterpret_cast<uint32_t*>(p) = 0;
+  else
+    *reinterpret_cast<uint16_t*>(p) = 0;
+}
 
 // Bulk (TMA, non-tensor) copy of `bytes` bytes of this CTA's shared memory (a
 // multiple of 16; both addresses 16-byte aligned) to global memory, tracked by
@@ -169,49 +183,32 @@ __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t by
 
 constexpr int kZeroBytes = 16 << 10;  // of a bulk store
 
-// Parts part, part + apart, .. (`count` of them) of `parts` of the zeros, by one
-// whole warp. One stretch of bytes goes out as bulk stores of a block of zeros,
-// which one lane issues; it waits where the SM's queue of them is full, so the
-// warp has nothing else to do meanwhile. zeros: kZeroBytes of shared memory,
-// 16-byte aligned, for this alone. The warp has to call fill_done before it ends.
+// Parts part, part + apart, .. (`count` of them) of `parts` of the zeros of rows without
+// gaps, by one whole warp: bulk stores of a block of zeros, which one lane issues; it
+// waits where the SM's queue of them is full, so the warp has nothing else to do
+// meanwhile. zeros: kZeroBytes of shared memory, 16-byte aligned, for this alone. The
+// warp has to call fill_done before it ends.
 __device__ void fill_zeros(const FillArgs& f, int part, int parts, uint8_t* zeros, int count = 1,
                            int apart = 0) {
   const int lane = threadIdx.x & 31;
-  if (f.pitch == f.row_bytes) {
-    const int64_t bytes = f.rows * f.row_bytes;
-    const int64_t lead = min(bytes, static_cast<int64_t>(-reinterpret_cast<intptr_t>(f.out) & 15));
-    const int64_t mid = (bytes - lead) & ~int64_t{15};
-    for (int i = lane; i < kZeroBytes / 16; i += 32)
-      reinterpret_cast<uint4*>(zeros)[i] = make_uint4(0, 0, 0, 0);
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-      for (int k = 0; k < count; ++k)
-        for (int64_t at = static_cast<int64_t>(part + k * apart) * kZeroBytes; at < mid;
-             at += static_cast<int64_t>(parts) * kZeroBytes)
-          bulk_s2g(f.out + lead + at, zeros,
-                   static_cast<uint32_t>(min(static_cast<int64_t>(kZeroBytes), mid - at)));
-      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-    }
-    if (part == 0) {  // the unaligned ends
-      if (lane < lead) f.out[lane] = 0;
-      if (lane < bytes - lead - mid) f.out[lead + mid + lane] = 0;
-    }
-  } else {
-    // rows apart from each other: whole 16-byte units, or the 2 bytes that every
-    // element has at least
-    const bool wide = ((reinterpret_cast<intptr_t>(f.out) | f.row_bytes | f.pitch) & 15) == 0;
-    const int64_t per_row = f.row_bytes / (wide ? 16 : 2);
+  const int64_t bytes = f.rows * f.row_bytes;
+  const int64_t lead = min(bytes, static_cast<int64_t>(-reinterpret_cast<intptr_t>(f.out) & 15));
+  const int64_t mid = (bytes - lead) & ~int64_t{15};
+  for (int i = lane; i < kZeroBytes / 16; i += 32)
+    reinterpret_cast<uint4*>(zeros)[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
     for (int k = 0; k < count; ++k)
-      for (int64_t r = part + k * apart; r < f.rows; r += parts) {
-        char* row = f.out + r * f.pitch;
-        for (int64_t c = lane; c < per_row; c += 32) {
-          if (wide)
-            reinterpret_cast<uint4*>(row)[c] = make_uint4(0, 0, 0, 0);
-          else
-            reinterpret_cast<uint16_t*>(row)[c] = 0;
-        }
-      }
+      for (int64_t at = static_cast<int64_t>(part + k * apart) * kZeroBytes; at < mid;
+           at += static_cast<int64_t>(parts) * kZeroBytes)
+        bulk_s2g(f.out + lead + at, zeros,
+                 static_cast<uint32_t>(min(static_cast<int64_t>(kZeroBytes), mid - at)));
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+  if (part == 0) {  // the unaligned ends
+    if (lane < lead) f.out[lane] = 0;
+    if (lane < bytes - lead - mid) f.out[lead + mid + lane] = 0;
   }
 }
 
@@ -242,6 +239,24 @@ __global__ void __launch_bounds__(kFillThreads) fill_kernel(const FillArgs f) {
   // The sort in front is still at work, perhaps: this grid ends after it, so that
   // what waits for the zeros has the sorted tokens too.
   asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// The zeros of rows that lie apart from each other (columns of a wider buffer): ordinary
+// stores, `lanes` of them a row at a time, by whole blocks; beside a cluster sort as
+// above, or in front of a longer one. (By the sort's warps and two bytes at a time, an
+// earlier form, a million rows of 64 f32 with gaps took 800 us of a gradient.)
+constexpr int kFillRowThreads = 256;
+
+template <bool BESIDE>
+__global__ void __launch_bounds__(kFillRowThreads) fill_rows_kernel(const FillArgs f, int lanes) {
+  if constexpr (BESIDE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int64_t per_row = f.row_bytes / f.unit;
+  const int at = threadIdx.x / lanes, step = kFillRowThreads / lanes;
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * step + at; r < f.rows;
+       r += static_cast<int64_t>(gridDim.x) * step)
+    for (int64_t c = threadIdx.x % lanes; c < per_row; c += lanes)
+      put_zeros(f.out + r * f.pitch + c * f.unit, f.unit);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // as above
 }
 
 // ---------------------------------------------------------------------------
@@ -639,9 +654,15 @@ cudaError_t allow_smem(K* fn, int bytes, std::atomic<bool> (&prepared)[kMaxDevic
 }
 
 // The zeros: beside the cluster sort that was launched last (the one before them
-// that they may not wait for), or behind all that is on the stream.
+// that they may not wait for), or behind all that is on the stream. blocks: SMs to take.
 template <bool BESIDE>
 cudaError_t run_fill(const FillArgs& f, int blocks, cudaStream_t stream) {
+  if (f.apart()) {
+    int lanes = 1;  // a power of two
+    while (lanes < 32 && lanes < f.row_bytes / f.unit) lanes *= 2;
+    return launch(&fill_rows_kernel<BESIDE>, dim3(blocks * (2048 / kFillRowThreads)),
+                  kFillRowThreads, 0, BESIDE, stream, f, lanes);
+  }
   static std::atomic<bool> prepared[kMaxDevices];
   const cudaError_t e = allow_smem(&fill_kernel<BESIDE>, kFillSmem, prepared);
   if (e != cudaSuccess) return e;
@@ -675,7 +696,8 @@ cudaError_t run_cluster_sort(SortArgs& a, int sms, int& n, cudaStream_t stream) 
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   const FillArgs fill = a.fill;
-  const bool beside = fill.out != nullptr && fill.rows * fill.row_bytes > kClusterZeros;
+  const bool beside =
+      fill.out != nullptr && (fill.apart() || fill.rows * fill.row_bytes > kClusterZeros);
   if (beside) a.fill.out = nullptr;
   ++n;
   if ((e = cudaLaunchKernelEx(&cfg, fn, a)) != cudaSuccess || !beside) return e;
@@ -1016,17 +1038,15 @@ struct SmallArgs {
   const int32_t* ids;
   int pad;
   FillArgs fill;
-  int unit;   // bytes of a store of zeros: 16, 8, 4 or 2, as the rows allow
   int parts;  // of the tokens
   int32_t* status;
 };
 
-// Block `part` of `parts`: its share of the rows, without those in keys[0, T), by
-// stores of `unit` bytes.
-__device__ void fill_unnamed(const FillArgs& f, const uint32_t* keys, int T, int unit, int part,
-                             int parts, uint32_t* map) {
+// Block `part` of `parts`: its share of the rows, without those in keys[0, T).
+__device__ void fill_unnamed(const FillArgs& f, const uint32_t* keys, int T, int part, int parts,
+                             uint32_t* map) {
   const int64_t begin = f.rows * part / parts, end = f.rows * (part + 1) / parts;
-  const uint32_t per_row = static_cast<uint32_t>(f.row_bytes) / unit;
+  const uint32_t per_row = static_cast<uint32_t>(f.row_bytes) / f.unit;
   for (int64_t r0 = begin; r0 < end; r0 += kMapWords * 32) {
     const int n = static_cast<int>(min(end - r0, static_cast<int64_t>(kMapWords * 32)));
     __syncthreads();
@@ -1041,15 +1061,7 @@ __device__ void fill_unnamed(const FillArgs& f, const uint32_t* keys, int T, int
     for (int64_t u = threadIdx.x; u < units; u += kSumThreads) {
       const uint32_t r = static_cast<uint32_t>(static_cast<uint32_t>(u) / per_row);
       if (map[r / 32] & (1u << (r % 32))) continue;
-      char* p = f.out + (r0 + r) * f.pitch + static_cast<int64_t>(u - static_cast<int64_t>(r) * per_row) * unit;
-      if (unit == 16)
-        *reinterpret_cast<uint4*>(p) = make_uint4(0, 0, 0, 0);
-      else if (unit == 8)
-        *reinterpret_cast<uint2*>(p) = make_uint2(0, 0);
-      else if (unit == 4)
-        *reinterpret_cast<uint32_t*>(p) = 0;
-      else
-        *reinterpret_cast<uint16_t*>(p) = 0;
+      put_zeros(f.out + (r0 + r) * f.pitch + (u - static_cast<int64_t>(r) * per_row) * f.unit, f.unit);
     }
   }
 }
@@ -1107,7 +1119,7 @@ __global__ void __launch_bounds__(kSumThreads) small_kernel(const SmallArgs a) {
                                nullptr);
   }
   if (a.fill.out != nullptr)
-    fill_unnamed(a.fill, keys, T, a.unit, blockIdx.x, gridDim.x, map);
+    fill_unnamed(a.fill, keys, T, blockIdx.x, gridDim.x, map);
 }
 
 // The sums, then the runs that cross blocks. Launched kernels are added to n.
@@ -1150,7 +1162,7 @@ struct SmallLaunch {
     // blocks: for the sums, and for the zeros, eight stores a thread
     int64_t blocks = static_cast<int64_t>(a.parts) * a.sum.windows;
     if (a.fill.out != nullptr)
-      blocks = std::max(blocks, std::min<int64_t>(148 * 8, a.fill.rows * a.fill.row_bytes / (8 * kSumThreads * a.unit)));
+      blocks = std::max(blocks, std::min<int64_t>(148 * 8, a.fill.rows * a.fill.row_bytes / (8 * kSumThreads * a.fill.unit)));
     return launch(&small_kernel<In, VEC, G, E>, dim3(static_cast<unsigned>(blocks)), kSumThreads, 0,
                   false, stream, a);
   }
@@ -1300,6 +1312,10 @@ int dlrm_embedding_grad(const void* grad, int grad_dtype, int64_t ldg, const int
     fill.rows = rows;
     fill.row_bytes = D * os;
     fill.pitch = ldo * os;
+    fill.unit = os;
+    for (int u : {4, 8, 16})
+      if (((reinterpret_cast<intptr_t>(fill.out) | fill.row_bytes | fill.pitch) & (u - 1)) == 0)
+        fill.unit = u;
   }
   if (T == 0) {
     if (accumulate) return DLRM_OK;
@@ -1331,10 +1347,6 @@ int dlrm_embedding_grad(const void* grad, int grad_dtype, int64_t ldg, const int
     f.a.ids = ids;
     f.a.pad = static_cast<int>(padding_idx);
     f.a.fill = fill;
-    f.a.unit = os;
-    for (int u : {4, 8, 16})
-      if (((reinterpret_cast<intptr_t>(fill.out) | fill.row_bytes | fill.pitch) & (u - 1)) == 0)
-        f.a.unit = u;
     f.a.status = status_dev;
     f.stream = s;
     if ((e = by_type(grad_dtype, a.D, vec, f)) != cudaSuccess) return cuda_fail(e);
@@ -1366,11 +1378,16 @@ int dlrm_embedding_grad(const void* grad, int grad_dtype, int64_t ldg, const int
         : items <= 4 ? run_cluster_sort<4>(sa, sms, n, s)
                      : run_cluster_sort<8>(sa, sms, n, s);
   } else {
+    if (fill.out != nullptr && fill.apart()) {
+      if ((e = run_fill<false>(fill, sms, s)) != cudaSuccess) return cuda_fail(e);
+      sa.fill.out = nullptr;
+      ++n;
+    }
     e = p.items == 4   ? run_grid_sort<4>(sa, pairs, s)
         : p.items == 6 ? run_grid_sort<6>(sa, pairs, s)
         : p.items == 9 ? run_grid_sort<9>(sa, pairs, s)
                        : run_grid_sort<kSortItems>(sa, pairs, s);
-    n = 2 * p.passes;
+    n += 2 * p.passes;
   }
   if (e != cudaSuccess) return cuda_fail(e);
   a.sorted = sa.out;

@@ -230,6 +230,26 @@ def test_grad_of_whole_numbers_is_exact(tokens, T, rows, D, dt, odt, kind):
     assert torch.equal(table[small], after[small])
 
 
+@pytest.mark.parametrize("T", [0, 5, 4000, 70000])
+@pytest.mark.parametrize("D,pitch,offset", [(64, 128, 0), (64, 65, 0), (64, 66, 1), (3, 4, 0),
+                                            (1, 2, 0), (200, 208, 8), (1000, 1004, 4), (6, 10, 2)])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_grad_into_rows_that_lie_apart(tokens, T, D, pitch, offset, dt):
+    """Columns of a wider buffer: every row is zeroed or written, every gap is left."""
+    g = _gen(T + D)
+    rows = 120000 if D * T < 10 ** 6 else 9000
+    grad = torch.randint(-8, 9, (T, D), device=DEV, generator=g).to(IDS[dt])
+    ids = torch.from_numpy(_ids(T, T, rows, "skew")).to(DEV)
+    buf = torch.full((rows * pitch + offset + 16,), 77.0, device=DEV, dtype=IDS[dt])
+    out = buf[offset:offset + rows * pitch].view(rows, pitch)[:, :D]
+    tokens.embedding_grad(grad, ids, rows, out=out)
+    want = torch.zeros((rows, D), device=DEV, dtype=torch.float64)
+    want.index_add_(0, ids.long(), grad.double())
+    assert torch.equal(out, want.to(IDS[dt]))
+    out.fill_(77.0)
+    assert (buf == 77.0).all()
+
+
 @pytest.mark.parametrize("T", [300, 3000, 70000])
 @pytest.mark.parametrize("accumulate", [False, True])
 def test_grad_past_32_bit_offsets(tokens, T, accumulate):
