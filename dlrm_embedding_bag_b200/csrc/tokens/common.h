@@ -12,6 +12,10 @@
 
 namespace dlrm {
 
+// SMs of a B200. Grids and rules that need not follow the device at hand take this one:
+// sizes of scratch must not depend on it, and a grid-stride loop does as well with it.
+constexpr int kSms = 148;
+
 // Records a failed CUDA call for dlrm_tokens_last_cuda_error(); DLRM_ERR_CUDA.
 int cuda_fail(cudaError_t e);
 // Counts kernel launches of this library (dlrm_tokens_launch_count).
@@ -48,8 +52,8 @@ inline bool is_aligned(const void* p, uintptr_t a) {
 }
 inline bool known_dtype(int d) { return d == DLRM_TABLE_F32 || d == DLRM_TABLE_BF16; }
 inline int dtype_size(int d) { return d == DLRM_TABLE_BF16 ? 2 : 4; }
-// Rows of `cols` columns that accesses of v elements (16 bytes at most each) can
-// walk: base, pitch and length are whole multiples of them.
+// Whether rows' base and pitch allow accesses of v elements (16 bytes at most each);
+// that the rows' length is a multiple of v is the caller's to check.
 inline bool rows_by(const void* p, int64_t ld, int elem, int v) {
   const int bytes = v * elem < 16 ? v * elem : 16;
   return is_aligned(p, bytes) && ld % v == 0;

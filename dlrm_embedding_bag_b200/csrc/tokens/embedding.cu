@@ -23,8 +23,8 @@ constexpr int kMaxDevices = 64;  // devices whose launch set-up is cached
 // the bytes of the rows, or, where 128-bit accesses cannot walk them, by the number
 // of accesses. Y is written past the cache's order of use, which keeps frequent
 // rows in L2. Measured on B200, 1310720 tokens of 512-byte rows under a power law
-// of 1.2 (671 MB written): 119 us, of 2000-byte rows, 16383 tokens: 10.2 us
-// (6.4 TB/s), 15.8 where a group walks all windows of its rows instead. More
+// of 1.2 (671 MB written): 119 to 125 us over several GPUs, of 2000-byte rows, 16383
+// tokens: 10.2 us (6.4 TB/s), 15.8 where a group walks all windows of its rows. More
 // threads a block (256, 512) cost 6 and 13 us of the first, two rows in flight 12,
 // ordinary stores 4. 60000 rows of 1001 f32, single elements: 76 us with four
 // accesses a lane (6.3 TB/s), bf16 58; of 1002, pairs: 74 and 41.
@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kFillRowThreads) fill_rows_kernel(const FillAr
 constexpr int kRadix = 256;
 constexpr int kSortThreads = 512;  // of a block that counts or moves
 constexpr int kSortItems = 16;     // pairs of a thread, at most, in a tile
-constexpr int kSortMaxBlocks = 296;  // two blocks an SM
+constexpr int kSortMaxBlocks = 2 * kSms;
 // A move takes more than twice as long as a count (19 and 8 us at 1.3 M pairs) and
 // writes more of the zeros meanwhile: 512 MB of them, in all 271 us with equal
 // parts, 263 with two of three in the moves, 258 with three of four.
@@ -715,7 +715,7 @@ cudaError_t run_grid_sort(SortArgs& a, uint2* const (&pairs)[2], cudaStream_t st
   cudaError_t e = allow_smem(move, smem, prepared);
   if (e != cudaSuccess) return e;
   // blocks enough to keep the memory busy with zeros
-  const int grid = a.fill.out != nullptr ? std::max(a.blocks, 148) : a.blocks;
+  const int grid = a.fill.out != nullptr ? std::max(a.blocks, kSms) : a.blocks;
   const int threads = a.fill.out != nullptr ? kSortThreads + 32 : kSortThreads;
   a.fill_parts = kPassParts * a.passes * grid;
   for (int i = 0; i < a.passes; ++i) {
@@ -934,7 +934,11 @@ __device__ __forceinline__ void sum_block(const SumArgs& a, SumSmem<VEC, G, E>& 
 }
 
 // JOIN: the join kernel follows, and may be scheduled early (it waits before it
-// reads anything; what else may follow is not known to).
+// reads anything; what else may follow is not known to). Blocks of an SM: four of bf16
+// rows by 128 bits (16383 x 1000 36.8 us with three, 36.0 so, 36 to 56 bytes spilt a
+// thread), three of the others (32768 x 64 f32 49.6 us, 51.1 with four). That rule
+// was fitted to rows of 128-bit accesses: f32 pairs spill 88 to 148 bytes at its 80
+// registers, and two blocks of them have not been measured.
 template <class In, int VEC, int G, int E, bool JOIN>
 __global__ void __launch_bounds__(kSumThreads, sizeof(In) == 2 && VEC > 2 ? 4 : 3)
     sum_kernel(const SumArgs a) {
@@ -1061,7 +1065,8 @@ __device__ void fill_unnamed(const FillArgs& f, const uint32_t* keys, int T, int
     for (int64_t u = threadIdx.x; u < units; u += kSumThreads) {
       const uint32_t r = static_cast<uint32_t>(static_cast<uint32_t>(u) / per_row);
       if (map[r / 32] & (1u << (r % 32))) continue;
-      put_zeros(f.out + (r0 + r) * f.pitch + (u - static_cast<int64_t>(r) * per_row) * f.unit, f.unit);
+      put_zeros(f.out + (r0 + r) * f.pitch + (u - static_cast<int64_t>(r) * per_row) * f.unit,
+                f.unit);
     }
   }
 }
@@ -1162,7 +1167,9 @@ struct SmallLaunch {
     // blocks: for the sums, and for the zeros, eight stores a thread
     int64_t blocks = static_cast<int64_t>(a.parts) * a.sum.windows;
     if (a.fill.out != nullptr)
-      blocks = std::max(blocks, std::min<int64_t>(148 * 8, a.fill.rows * a.fill.row_bytes / (8 * kSumThreads * a.fill.unit)));
+      blocks = std::max(blocks, std::min<int64_t>(
+                                    kSms * 8, a.fill.rows * a.fill.row_bytes /
+                                                  (8 * kSumThreads * a.fill.unit)));
     return launch(&small_kernel<In, VEC, G, E>, dim3(static_cast<unsigned>(blocks)), kSumThreads, 0,
                   false, stream, a);
   }
@@ -1197,7 +1204,7 @@ GradPlan plan_grad(int64_t T, int64_t rows, int64_t D) {
   // GPU's threads, more when there are more; by T and D alone. (16383 x 1000
   // takes 36 us with 8 tokens, 34 with 16, 36 with 24; 32768 x 64 51.3,
   // 51.7 and 53.3.)
-  const int64_t even = T * D / (int64_t{148} * 2048 * 4) / kSumInFlight + 1;
+  const int64_t even = T * D / (int64_t{kSms} * 2048 * 4) / kSumInFlight + 1;
   p.chunk = static_cast<int>(std::min<int64_t>(64, even * kSumInFlight));
   // blocks of chunks, at most: 32 lanes a group are the widest
   const int64_t per_block = static_cast<int64_t>(p.chunk) * (kSumThreads / 32);

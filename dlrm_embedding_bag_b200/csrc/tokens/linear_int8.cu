@@ -4,8 +4,9 @@
 // The weights take the tensor cores' M side and the tokens their N side, so an
 // accumulator lane is an output channel and a column a token: the scale and
 // the bias of a channel stay in its lane's registers, the 32 lanes of a warp
-// write 32 neighbouring channels of one token (whole sectors at any pitch, no
-// staging), and few tokens make a narrow tile instead of a mostly empty one.
+// write 32 neighbouring channels of one token without staging (whole sectors where
+// base and pitch are multiples of 32 bytes, else one more sector a store, two of them
+// in part), and few tokens make a narrow tile instead of a mostly empty one.
 //
 // Ten warps a CTA, as in the bf16 layer (linear.cu): one thread streams 128-byte
 // K blocks of both operands into a shared-memory ring with 2-D TMA loads, one
@@ -493,7 +494,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // token 5.1 (R = 1, K = 4096; 3.3 TB/s) and 7.9 us, two 6.4 and 8.0, four 8.0
 // and 8.3, eight 11.1 and 8.9; 8192 channels of K = 2048 with R = 2: one 5.1
 // and 7.6, four 5.8 and 8.1. R = 2 is slower at K = 4096 (6.9 us), R = 1 at K =
-// 2048 (5.6 us).
+// 2048 (5.6 us). (As first built, from which the rules come. Scales and bias loaded
+// before the sums are joined: one token 5.4 to 5.6, two 6.8, four 7.8, behind a
+// flushed L2 of 16 calls in a graph.)
 constexpr int kVecThreads = 256;
 constexpr int kFewTokens = 4;
 
@@ -700,8 +703,10 @@ cudaError_t run_few(const Operands& op, const LinArgs& args, cudaStream_t stream
 }
 
 // The forms of the tensor-core kernel, with what they take on a B200 in us: a K
-// block of 128 bytes of a tile (`step`; a narrow tile's is bound by the latency
-// of its loads), what a tile takes besides (`tile`), the least that a tile takes
+// block of 128 bytes of a tile (`step`; much the same for 20 and for 48 KB, so it is
+// neither the loads' bytes nor the products but what a stage costs besides: a wait,
+// arming and two loads in one thread, a wait, four products and a commit in another),
+// what a tile takes besides (`tile`), the least that a tile takes
 // (`least`: its drain), and the joining of a cluster's parts (`join`). Fitted to
 // all forms at 27 shapes from 5 x 512 x 512 to 65536 x 512 x 592 in a graph; the
 // choice was the fastest form, or within 5 % of it, at 26 of them.

@@ -147,10 +147,10 @@ def linear_int8(x_q: torch.Tensor, x_scale: torch.Tensor, w_q: torch.Tensor,
 
     ``x_q`` ``(M, K)`` and ``w_q`` ``(N, K)`` are int8 matrices (pitch a multiple of 16),
     ``x_scale`` ``(M,)`` and ``w_scale`` ``(N,)`` f32 (one scale for each token and
-    each output channel), ``bias`` ``(N,)`` f32 or None. The sum over K is exact;
-    ``K`` is at most 131071. The result is f32 or bf16: ``out``, or a new tensor of
-    ``out_dtype``. ``status`` (one int32) gets ``FLAG_TIMEOUT`` OR-ed in if a wait of
-    the kernel ran out.
+    each output channel), ``bias`` ``(N,)`` f32 or None. The sum over K is exact,
+    the scales are applied from left to right in f32; ``K`` is at most 131071. The
+    result is f32 or bf16: ``out``, or a new tensor of ``out_dtype``. ``status`` (one
+    int32) gets ``FLAG_TIMEOUT`` OR-ed in if a wait of the kernel ran out.
     """
     code = ACTS.get(act)
     if code is None:

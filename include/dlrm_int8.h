@@ -10,8 +10,9 @@
  *
  * A row v of K values is held as q (int8) and s (f32): v[k] ~ q[k] * s with
  * s = max|v| / 127 and q[k] = v[k] / s rounded to nearest, ties to even, so
- * |q| <= 127. A row of zeros has s = 0 and q = 0. A row that holds a NaN or an
- * infinity has s = NaN and q = 0: what is computed from it is NaN.
+ * |q| <= 127 (q is that of the unrounded s, also where s is a subnormal of f32 or
+ * below). A row of zeros has s = 0 and q = 0. A row that holds a NaN or an infinity
+ * has s = NaN and q = 0: what is computed from it is NaN.
  *
  * Conventions as in dlrm_tokens.h (the same library, libdlrm_tokens.so).
  */
@@ -42,9 +43,10 @@ extern "C" {
  *             residual's own buffer (same pointer and pitch) or x's.
  *   q         dev int8 (M, ldq); columns past K are left as they were.
  *   scale     dev f32 (M,).
- * The sum h, its squares and the norm are f32 (h is not rounded to dtype
- * before it is normed). M >= 0 (with M == 0 nothing is enqueued), K >= 1,
- * pitches >= K, M and K < 2^31.
+ * The sum h is f32 (it is not rounded to dtype before it is normed; where it
+ * leaves f32 it is an infinity). Squares and products with the weight are f32, and
+ * 64 bits for rows where those would leave f32 or vanish in it. M >= 0 (with
+ * M == 0 nothing is enqueued), K >= 1, pitches >= K, M and K < 2^31.
  */
 DLRM_API int dlrm_rms_norm_int8(const void* x, int64_t ldx, const void* residual, int64_t ldr,
                                 int dtype, const float* weight, int64_t M, int64_t K, float eps,
@@ -76,7 +78,9 @@ DLRM_API int dlrm_dequantize_int8(const int8_t* q, int64_t ldq, const float* sca
  *   status_dev dev int32, or NULL: DLRM_FLAG_TIMEOUT is OR-ed in if a bounded
  *            wait of the kernel ran out (the results are then not valid).
  * The sum over k is exact in int32; the scales, the bias and the activation
- * are applied in f32 and the result is rounded once.
+ * are applied in f32, from left to right (sum * x_scale, times w_scale, plus bias:
+ * a product of the first two that leaves f32 stays infinite whatever w_scale is),
+ * and the result is rounded once.
  * Requirements (DLRM_ERR_SHAPE / DLRM_ERR_ALIGN otherwise): M >= 0 (with
  * M == 0 nothing is enqueued), N >= 1, 1 <= K <= DLRM_INT8_MAX_K, M and N <
  * 2^31 - 1024; ldx, ldw >= K and ldy >= N; ldx and ldw multiples of 16 and x, w

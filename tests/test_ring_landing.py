@@ -17,7 +17,11 @@ MODEL = r"""
 #include "ring_landing.h"
 
 static int checks = 0;
-#define CHECK(c) do { ++checks; if (!(c)) { std::printf("line %d: %s\n", __LINE__, #c); std::exit(1); } } while (0)
+#define CHECK(c) \
+  do { \
+    ++checks; \
+    if (!(c)) { std::printf("line %d: %s\n", __LINE__, #c); std::exit(1); } \
+  } while (0)
 
 // The barriers of a unit's ring: phase i / STAGES of stage i % STAGES belongs to step i.
 template <int STAGES>
