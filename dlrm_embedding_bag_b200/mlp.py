@@ -55,6 +55,12 @@ def _pitched(t: torch.Tensor, name: str, dtype: torch.dtype) -> Tuple[int, int]:
     return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1]))
 
 
+def _room(t: Optional[torch.Tensor], name: str, rows: int, cols: int) -> None:
+    """Raises if an output's last two dimensions have no room for ``(rows, cols)``."""
+    if t is not None and (t.dim() < 2 or t.shape[-2] < rows or t.shape[-1] < cols):
+        raise ValueError(f"{name} must have room for ({rows}, {cols}) (got {tuple(t.shape)})")
+
+
 def to_bf16(x: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Round an f32 ``(rows, cols)`` tensor to bf16 (nearest even) into a pitched buffer."""
     px, ldx = _pitched(x, "x", torch.float32)
@@ -62,6 +68,7 @@ def to_bf16(x: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.Tensor
     if out is None:
         out = bf16_empty(rows, cols, x.device)
     py, ldy = _pitched(out, "out", torch.bfloat16)
+    _room(out, "out", rows, cols)
     if rows == 0:  # nothing to round, and no pointers for the entry point
         return out
     ops._check(ops._lib.dlrm_f32_to_bf16(px, ldx, rows, cols, py, ldy, ops._stream()),
@@ -114,6 +121,8 @@ def linear_bf16(a_lo: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor
     pf, ldf = _pitched(out_f32, "out_f32", torch.float32) if out_f32 is not None else (None, 0)
     pbf, ldbf = (_pitched(out_bf16, "out_bf16", torch.bfloat16) if out_bf16 is not None
                  else (None, 0))
+    _room(out_f32, "out_f32", M, N)
+    _room(out_bf16, "out_bf16", M, N)
     ps = ops._dev(status, "status", torch.int32) if status is not None else None
     ops._check(ops._lib.dlrm_linear_bf16(pa, lda, k_lo, ph, ldh, k_hi, pw, ldw, pb, M, N,
                                          ACTS[act], pf, ldf, pbf, ldbf, ps, ops._stream()),
@@ -148,6 +157,7 @@ def split_bf16x3(x: torch.Tensor, out: Optional[torch.Tensor] = None) -> torch.T
     if out is None:
         out = planes_empty(rows, cols, x.device)
     py, ldy, sp = _planes(out, "out")
+    _room(out, "out", rows, cols)
     ops._check(ops._lib.dlrm_split_f32_bf16x3(px, ldx, rows, cols, py, ldy, sp, ops._stream()),
                "dlrm_split_f32_bf16x3")
     return out
@@ -197,6 +207,8 @@ def linear_f32a(a_lo: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor
         out_planes = planes_empty(M, N, a_lo.device)
     pf, ldf = _pitched(out_f32, "out_f32", torch.float32) if out_f32 is not None else (None, 0)
     pp, ldp, spp = _planes(out_planes, "out_planes") if out_planes is not None else (None, 0, 0)
+    _room(out_f32, "out_f32", M, N)
+    _room(out_planes, "out_planes", M, N)
     ps = ops._dev(status, "status", torch.int32) if status is not None else None
     ops._check(ops._lib.dlrm_linear_f32a(pa, lda, spa, k_lo, ph, ldh, sph, k_hi, pw, ldw, spw,
                                          w_planes, pb, M, N, ACTS[act], pf, ldf, pp, ldp, spp,
