@@ -1,10 +1,11 @@
-"""Build ``libdlrm_sparse.so`` and ``libdlrm_tokens.so`` in-tree with nvcc for sm_100a.
+"""Build the three libraries in-tree with nvcc for sm_100a.
 
 ``python -m dlrm_embedding_bag_b200.build`` (or ``__graft_entry__.build()``)
-compiles every ``csrc/*.cu`` (the stage and its MLP layers) and every
-``csrc/tokens/*.cu`` (the token-level operators and the 8-bit layers) to an
-object in parallel and links the two shared libraries next to this file. nvcc
-cross-compiles, so no GPU is needed.
+compiles every ``csrc/*.cu`` (the stage and its MLP layers), every
+``csrc/tokens/*.cu`` (the token-level operators and the 8-bit layers) and every
+``csrc/narrow/*.cu`` (the optimiser step and the 4-bit layers) to an object in
+parallel and links ``libdlrm_sparse.so``, ``libdlrm_tokens.so`` and
+``libdlrm_narrow.so`` next to this file. nvcc cross-compiles, so no GPU is needed.
 """
 from __future__ import annotations
 
@@ -18,10 +19,12 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 CSRC_TOKENS = os.path.join(CSRC, "tokens")
+CSRC_NARROW = os.path.join(CSRC, "narrow")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libdlrm_sparse.so")
 LIB_TOKENS = os.path.join(HERE, "libdlrm_tokens.so")
+LIB_NARROW = os.path.join(HERE, "libdlrm_narrow.so")
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -65,9 +68,12 @@ def _link(lib: str, objs) -> None:
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile each CUDA library any of whose sources is newer; return the stage's path."""
-    # the token library includes headers of the stage's sources
+    # the other libraries include headers of the stage's sources, the last one also the
+    # token library's
     todo = [(lib, d) for lib, d, deps in ((LIB, CSRC, [CSRC]),
-                                          (LIB_TOKENS, CSRC_TOKENS, [CSRC, CSRC_TOKENS]))
+                                          (LIB_TOKENS, CSRC_TOKENS, [CSRC, CSRC_TOKENS]),
+                                          (LIB_NARROW, CSRC_NARROW,
+                                           [CSRC, CSRC_TOKENS, CSRC_NARROW]))
             if force or _stale(lib, deps)]
     if not todo:
         return LIB

@@ -1,0 +1,884 @@
+// The layer on 4-bit floating point (declared in dlrm_fp4.h):
+// y[m][n] = act(sum_k x[m][k] w[n][k] + bias[n]).
+//
+// tcgen05.mma.kind::mxf4.block_scale: products of e2m1 codes times both blocks'
+// powers of two, K = 64 an instruction, f32 sums in TMEM. The weights take the M side
+// and the tokens the N side, as in the 8-bit layer: a lane is an output channel, and
+// the 32 lanes of a warp store 32 neighbouring channels of one token without staging.
+//
+// Ten warps a CTA: one thread streams 128-byte K blocks (256 elements) of both
+// operands and their scale tiles into a shared-memory ring with TMA loads; one copies
+// a stage's scales into TMEM (tcgen05.cp, which the tensor cores take in order with
+// the products around it, so one set of columns is enough) and issues its four products;
+// eight warps drain a finished accumulator while the next tile's products fill the other.
+//   - CTAs of 128 channels x 64 or 128 tokens; few tiles: a cluster of S of them shares
+//     one tile, each summing a stretch of K, and the f32 parts meet through distributed
+//     shared memory in the order of the ranks.
+//   - CTA pairs (cta_group::2) of 256 channels x 256 tokens. Two accumulators of 256
+//     columns and the scales' 24 do not fit TMEM's 512, so the accumulators share 32
+//     columns: those are drained first, and the next tile's products wait for that.
+//   - up to four tokens: CUDA cores, a warp for each channel (below).
+// Every wait is bounded; one that runs out sets DLRM_FLAG_TIMEOUT in the
+// optional status word, and the CTA still lets its loads land, frees its tensor
+// memory and exits.
+#include <algorithm>
+#include <atomic>
+#include <climits>
+
+#include "fp4_common.cuh"
+#include "ring_landing.h"
+#include "tcgen05_common.cuh"
+#include "tokens/common.h"
+
+namespace dlrm {
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int kBM = 128;            // channels of a CTA's tile
+constexpr int kBK = 128;            // bytes of K per stage: one 128-byte swizzle row
+constexpr int kCols = 2 * kBK;      // elements of K per stage
+constexpr int kStageTiles = kCols / 128;  // scale tiles along K per stage
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr long long kWaitLimit = 200000000LL;  // clock cycles, about 0.1 s
+constexpr int kMaxDevices = 64;                // devices whose launch set-up is cached
+
+struct LinArgs {
+  const float* bias;
+  void* y;
+  int64_t ldy;
+  int M, N, K;
+  int nkb;                       // K blocks
+  int tiles_m, tiles_n, tiles;   // token tiles, channel tiles
+  int act, y_bf16;
+  int32_t* status;
+};
+
+struct alignas(64) LinMaps {
+  CUtensorMap w, x, sw, sx;
+};
+
+// Shared memory and TMEM of a form. BN tokens a tile; a pair's CTA loads half of them, but
+// the scales of all, which each CTA's tensor cores read from its own TMEM.
+template <int BN, bool PAIR>
+struct Ring {
+  static constexpr int kXTiles = BN > 128 ? BN / 128 : 1;  // row tiles of the tokens' scales
+  static constexpr int kW = kBM * kBK;
+  static constexpr int kX = (PAIR ? BN / 2 : BN) * kBK;
+  static constexpr int kSW = kStageTiles * kFp4Tile;
+  static constexpr int kSX = kXTiles * kStageTiles * kFp4Tile;
+  static constexpr int kStage = kW + kX + kSW + kSX;
+  // as many stages as fit in about 200 KB, at most 8
+  static constexpr int kStages = (200 * 1024 / kStage) < 8 ? (200 * 1024 / kStage) : 8;
+  static constexpr int kBars = kStages * kStage;
+  static constexpr int kTotal = kBars + (2 * kStages + 6) * 8 + 8 + 1024;  // + alignment
+  static_assert(kStage % 1024 == 0, "swizzled tiles start on 1024 bytes");
+  static_assert(kTotal <= 227 * 1024, "shared memory of one CTA");
+  // TMEM columns: the second accumulator, the scales, and what both accumulators have
+  // of each other
+  static constexpr int kLap = BN > 128 ? 32 : 0;
+  static constexpr uint32_t kAcc1 = BN - kLap;
+  static constexpr uint32_t kScales = kAcc1 + BN;
+  static constexpr uint32_t kScaleCols = 4 * kStageTiles * (1 + kXTiles);
+  static constexpr uint32_t kNeeded = kScales + kScaleCols;
+  static constexpr uint32_t kTmem = kNeeded <= 256 ? 256 : 512;
+  static_assert(kNeeded <= 512, "tensor memory of one SM");
+};
+
+// Instruction descriptor of tcgen05.mma.kind::mxf4.block_scale with e2m1 A and B, both
+// K-major, UE8M0 scales, dense, K = 64, shape M x N: B's scale bytes (bits 4-5), A and B
+// formats E2M1 (7-9 = 1, 10-12 = 1), N >> 3 (17-22), scales UE8M0 (23 = 1), M >> 4 (24-28),
+// A's scale bytes (29-30). The scale bytes of a product are a pair of a column's
+// four: 0 for the first, 2 for the second.
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, uint32_t pair) {
+  return (pair << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (1u << 23) | (static_cast<uint32_t>(M >> 4) << 24) | (pair << 29);
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T for one K = 64 step of 4-bit elements with scales in TMEM.
+template <int CG>
+__device__ __forceinline__ void tc_mma_fp4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                           uint32_t idesc, uint32_t sa, uint32_t sb,
+                                           uint32_t accumulate) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], "
+        "[%6], p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sa), "r"(sb)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], "
+        "[%6], p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sa), "r"(sb)
+        : "memory");
+}
+
+// A scale tile from shared memory into four columns of TMEM, the same for each warp's
+// 32 lanes (with CG = 2 in both CTAs of the pair, each from its own shared memory).
+template <int CG>
+__device__ __forceinline__ void tc_copy_scales(uint32_t tmem, uint64_t desc) {
+  if constexpr (CG == 2)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
+                 : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
+                 : "memory");
+}
+
+// Shared-memory descriptor of a scale tile: 32 rows of 16 bytes without swizzle, groups of 8
+// rows 128 bytes apart (fields as in sdesc_k_sw128; layout type 0).
+__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(1) << 16;
+  d |= static_cast<uint64_t>(128 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  return d;
+}
+
+// The box of a 3-D tensor map at (x, y, z); as tma_load_2d and tma_load_2d_pair.
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                            int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map,
+                                                 uint32_t bar_cluster, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+__device__ __forceinline__ float4 load_cluster_v4(uint32_t cluster_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
+  return v;
+}
+
+template <int ACT>
+__device__ __forceinline__ float activate(float x) {
+  if constexpr (ACT == DLRM_ACT_RELU) return x < 0.f ? 0.f : x;  // NaN stays NaN
+  if constexpr (ACT == DLRM_ACT_SIGMOID) return __fdiv_rn(1.f, __fadd_rn(1.f, expf(-x)));
+  return x;
+}
+
+template <int ACT, class Out>
+__device__ __forceinline__ void put_at(Out* p, float sum, float bias) {
+  const float v = activate<ACT>(__fadd_rn(sum, bias));
+  if constexpr (sizeof(Out) == 4)
+    *p = v;
+  else
+    *p = __float2bfloat16_rn(v);
+}
+
+// An output channel.
+struct Channel {
+  float b;
+  bool live;
+};
+
+// 32 tokens m0 .. of a lane's channel n, from the registers v.
+template <int ACT, class Out>
+__device__ __forceinline__ void put_32(const LinArgs& a, const Channel& ch, int n, int m0,
+                                       const float (&v)[32]) {
+  if (!ch.live) return;
+  Out* p = static_cast<Out*>(a.y) + static_cast<int64_t>(m0) * a.ldy + n;
+  const int left = a.M - m0;
+  if (left >= 32) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      put_at<ACT>(p, v[i], ch.b);
+      p += a.ldy;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      if (i < left) put_at<ACT>(p, v[i], ch.b);
+      p += a.ldy;
+    }
+  }
+}
+
+// Calls f with the activation and the output type as types.
+template <class F>
+__device__ __forceinline__ void by_kind(const LinArgs& a, F f) {
+  if (a.y_bf16) {
+    if (a.act == DLRM_ACT_RELU)
+      f.template run<DLRM_ACT_RELU, __nv_bfloat16>();
+    else if (a.act == DLRM_ACT_SIGMOID)
+      f.template run<DLRM_ACT_SIGMOID, __nv_bfloat16>();
+    else
+      f.template run<DLRM_ACT_NONE, __nv_bfloat16>();
+  } else {
+    if (a.act == DLRM_ACT_RELU)
+      f.template run<DLRM_ACT_RELU, float>();
+    else if (a.act == DLRM_ACT_SIGMOID)
+      f.template run<DLRM_ACT_SIGMOID, float>();
+    else
+      f.template run<DLRM_ACT_NONE, float>();
+  }
+}
+
+struct PutCall {
+  const LinArgs& a;
+  const Channel& ch;
+  int n, m0;
+  const float (&v)[32];
+  template <int ACT, class Out>
+  __device__ __forceinline__ void run() const {
+    put_32<ACT, Out>(a, ch, n, m0, v);
+  }
+};
+
+// The cluster's parts of a tile, kept as [column][channel] f32 at the start of each CTA's
+// ring, summed in the order of its S CTAs for columns [c0, c1): a column's 128 channels a
+// warp, four a lane, the loads of eight parts in flight.
+template <int S>
+struct JoinCall {
+  const LinArgs& a;
+  int n0, m0, c0, c1, ew, lane;
+  uint32_t smem;
+  template <int ACT, class Out>
+  __device__ __forceinline__ void run() const {
+    constexpr int kAtOnce = 8 / S;  // columns
+    const int n = n0 + lane * 4;
+    float b[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) b[e] = a.bias != nullptr && n + e < a.N ? a.bias[n + e] : 0.f;
+    for (int cb = c0 + ew * kAtOnce; cb < c1; cb += kEpiWarps * kAtOnce) {
+      float4 v[kAtOnce][S];
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i)
+#pragma unroll
+        for (int k = 0; k < S; ++k) {
+          v[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (cb + i < c1 && m0 + cb + i < a.M)
+            v[i][k] = load_cluster_v4(map_to_cta(smem + ((cb + i) * kBM + lane * 4) * 4, k));
+        }
+#pragma unroll
+      for (int i = 0; i < kAtOnce; ++i) {
+        if (cb + i >= c1 || m0 + cb + i >= a.M) break;
+        float4 t = v[i][0];
+#pragma unroll
+        for (int k = 1; k < S; ++k)
+          t.x += v[i][k].x, t.y += v[i][k].y, t.z += v[i][k].z, t.w += v[i][k].w;
+        const float sums[4] = {t.x, t.y, t.z, t.w};
+        Out* p = static_cast<Out*>(a.y) + static_cast<int64_t>(m0 + cb + i) * a.ldy + n;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n + e < a.N) put_at<ACT>(p + e, sums[e], b[e]);
+      }
+    }
+  }
+};
+
+// Tile t -> (token tile, channel tile): bands of 8 token tiles, so that the CTAs
+// at work at one time read few different rows of either operand.
+__device__ __forceinline__ void tile_at(const LinArgs& a, int t, int& tm, int& tn) {
+  constexpr int kBand = 8;
+  const int per_band = kBand * a.tiles_n;
+  const int band = t / per_band, in = t % per_band;
+  const int height = min(kBand, a.tiles_m - band * kBand);
+  tm = band * kBand + in % height;
+  tn = in / height;
+}
+
+// S > 1: the S CTAs of a cluster share one tile (and there is one tile a cluster).
+template <int BN, bool PAIR, int S>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_fp4_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinArgs args) {
+  constexpr bool SPLIT = S > 1;
+  static_assert(!(PAIR && SPLIT), "a pair shares a tile's channels, not its K");
+  using R = Ring<BN, PAIR>;
+  constexpr int CG = PAIR ? 2 : 1;
+  constexpr int kUnitN = CG * kBM;      // channels of a unit's tile
+  constexpr int kWarpCols = BN / 2;     // columns an epilogue warp drains
+  static_assert(kWarpCols % 32 == 0, "whole TMEM loads");
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + R::kBars);
+  uint64_t* empty = full + R::kStages;
+  uint64_t* acc_full = empty + R::kStages;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* mma_done = acc_empty + 2;
+  uint64_t* lap_empty = mma_done + 1;
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(lap_empty + 1);
+  uint32_t* other_steps = tslot + 1;  // of a pair's second producer, told at its end
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = (PAIR || SPLIT) ? cluster_ctarank() : 0u;
+  const int unit0 = (PAIR || SPLIT) ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
+  const int unit_step =
+      (PAIR || SPLIT) ? static_cast<int>(cluster_count_x()) : static_cast<int>(gridDim.x);
+  // this CTA's stretch of K blocks
+  const int kb_begin = SPLIT ? static_cast<int>(static_cast<int64_t>(args.nkb) * rank / S) : 0;
+  const int kb_end = SPLIT ? static_cast<int>(static_cast<int64_t>(args.nkb) * (rank + 1) / S) : args.nkb;
+
+  if (warp == 1) {
+    tmem_alloc<CG>(tslot, R::kTmem);
+    tmem_relinquish<CG>();
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < R::kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], CG * kEpiWarps);
+    }
+    mbar_init(mma_done, 1);
+    mbar_init(lap_empty, CG * kEpiWarps / 2);
+    mbar_init_fence();
+    if constexpr (PAIR) *other_steps = ~0u;
+  }
+  tc_fence_before_sync();
+  if constexpr (PAIR)
+    cluster_sync();  // both CTAs' barriers exist before either signals the other's
+  else
+    __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tslot;
+  // Everything below may come from the kernel before, which may still be at work, so every
+  // role waits for its end. The loads behind the wait are ordinary ones: those of the
+  // read-only path may be moved in front of it.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  bool timed_out = false;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int g = 0;
+      for (int t = unit0; t < args.tiles && !timed_out; t += unit_step) {
+        int tm, tn;
+        tile_at(args, t, tm, tn);
+        const int n0 = tn * kUnitN + (PAIR ? static_cast<int>(rank) * kBM : 0);
+        const int m0 = tm * BN + (PAIR ? static_cast<int>(rank) * (BN / 2) : 0);
+        for (int kb = kb_begin; kb < kb_end; ++kb, ++g) {
+          const int s = g % R::kStages;
+          if (g >= R::kStages &&
+              !mbar_wait_bounded(&empty[s], ((g / R::kStages) - 1) & 1, kWaitLimit)) {
+            timed_out = true;
+            break;
+          }
+          uint8_t* sw = smem + s * R::kStage;
+          uint8_t* sx = sw + R::kW;
+          uint8_t* ssw = sx + R::kX;
+          uint8_t* ssx = ssw + R::kSW;
+          if constexpr (PAIR) {
+            // both CTAs' bytes are counted on the issuer's barrier, which only
+            // its producer arms
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * R::kStage);
+            const uint32_t fb = map_to_cta(smem_u32(&full[s]), 0);
+            tma_load_2d_pair(sw, &maps.w, fb, kb * kBK, n0);
+            tma_load_2d_pair(sx, &maps.x, fb, kb * kBK, m0);
+            tma_load_3d_pair(ssw, &maps.sw, fb, 0, kb * kStageTiles, n0 / 128);
+            tma_load_3d_pair(ssx, &maps.sx, fb, 0, kb * kStageTiles, tm * BN / 128);
+          } else {
+            mbar_arrive_expect_tx(&full[s], R::kStage);
+            tma_load_2d(sw, &maps.w, &full[s], kb * kBK, n0);
+            tma_load_2d(sx, &maps.x, &full[s], kb * kBK, m0);
+            tma_load_3d(ssw, &maps.sw, &full[s], 0, kb * kStageTiles, n0 / 128);
+            tma_load_3d(ssx, &maps.sx, &full[s], 0, kb * kStageTiles, m0 / 128);
+          }
+        }
+      }
+      // no load is in flight once this CTA leaves, whoever gave up
+      land_loads<R::kStages, PAIR>(
+          !PAIR || rank == 0, timed_out, g,
+          [&](int s, uint32_t parity) { (void)mbar_wait_bounded(&full[s], parity, kWaitLimit); },
+          [&](int s) { mbar_arrive_expect_tx(&full[s], R::kStage); },
+          [&](int steps) { tell_steps(other_steps, steps); },
+          [&] { return told_steps(other_steps, (R::kStages + 2) * kWaitLimit); });
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && (!PAIR || rank == 0)) {
+      const uint32_t sa = tmem + R::kScales;
+      const uint32_t sb = sa + 4 * kStageTiles;
+      int g = 0, j = 0;
+      for (int t = unit0; t < args.tiles && !timed_out; t += unit_step, ++j) {
+        const int b = j & 1;
+        if (j >= 2 && !mbar_wait_bounded(&acc_empty[b], ((j >> 1) - 1) & 1, kWaitLimit)) {
+          timed_out = true;
+          break;
+        }
+        if (R::kLap != 0 && j >= 1 && !mbar_wait_bounded(lap_empty, (j - 1) & 1, kWaitLimit)) {
+          timed_out = true;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t acc = tmem + (b != 0 ? R::kAcc1 : 0u);
+        // tokens from the middle of a scale tile on: 32 rows of it are a column
+        int tm, tn;
+        tile_at(args, t, tm, tn);
+        const uint32_t sb_t = sb + static_cast<uint32_t>(tm * BN % 128 / 32);
+        for (int kb = kb_begin; kb < kb_end; ++kb, ++g) {
+          const int s = g % R::kStages;
+          if (!mbar_wait_bounded(&full[s], (g / R::kStages) & 1, kWaitLimit)) {
+            timed_out = true;
+            break;
+          }
+          tc_fence_after_sync();
+          const uint32_t sw = smem_u32(smem + s * R::kStage);
+          const uint32_t sx = sw + R::kW;
+          const uint32_t ssw = sx + R::kX;
+          const uint32_t ssx = ssw + R::kSW;
+#pragma unroll
+          for (int i = 0; i < kStageTiles; ++i) {
+            tc_copy_scales<CG>(sa + 4 * i, sdesc_scales(ssw + i * kFp4Tile));
+#pragma unroll
+            for (int r = 0; r < R::kXTiles; ++r)
+              tc_copy_scales<CG>(sb + 4 * (i * R::kXTiles + r),
+                                 sdesc_scales(ssx + (r * kStageTiles + i) * kFp4Tile));
+          }
+          // products past K would add zeros
+          const int steps = min(4, (args.K - kb * kCols + 63) / 64);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < steps)
+              tc_mma_fp4<CG>(acc, sdesc_k_sw128(sw + k * 32), sdesc_k_sw128(sx + k * 32),
+                             idesc_mxf4(kUnitN, BN, 2 * (k & 1)), sa + 4 * (k >> 1),
+                             sb_t + 4 * (k >> 1) * R::kXTiles,
+                             (kb > kb_begin || k > 0) ? 1u : 0u);
+          if constexpr (PAIR)
+            tc_commit_pair_both(&empty[s]);
+          else
+            tc_commit<CG>(&empty[s]);
+        }
+        if constexpr (PAIR)
+          tc_commit_pair_both(&acc_full[b]);
+        else
+          tc_commit<CG>(&acc_full[b]);
+      }
+      // every MMA has completed before this CTA or its peer can leave
+      tc_commit<CG>(mma_done);
+      if (!mbar_wait_bounded(mma_done, 0, kWaitLimit)) timed_out = true;
+    }
+  } else {
+    const int ew = warp - 2, quarter = warp & 3, half = ew >> 2;
+    auto arrive = [&](uint64_t* bar) {
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR)
+          mbar_arrive_remote(map_to_cta(smem_u32(bar), 0));
+        else
+          mbar_arrive(bar);
+      }
+    };
+    int j = 0;
+    for (int t = unit0; t < args.tiles; t += unit_step, ++j) {
+      const int b = j & 1;
+      int tm, tn;
+      tile_at(args, t, tm, tn);
+      const int m0 = tm * BN;
+      const int n = tn * kUnitN + (PAIR ? static_cast<int>(rank) * kBM : 0) + quarter * 32 + lane;
+      Channel ch = {0.f, n < args.N};
+      if (!SPLIT && ch.live && args.bias != nullptr) ch.b = args.bias[n];
+      if (!__all_sync(kFull, mbar_wait_bounded(&acc_full[b], (j >> 1) & 1, kWaitLimit))) {
+        timed_out = true;
+        break;
+      }
+      tc_fence_after_sync();
+      const uint32_t tq = tmem + (b != 0 ? R::kAcc1 : 0u) + (static_cast<uint32_t>(quarter * 32) << 16);
+      // The columns that the next tile's accumulator has too come first: the last of the
+      // lower accumulator, the first of the upper one.
+      constexpr int kChunks = kWarpCols / 32;
+      const bool lap = R::kLap != 0 && half == 1 - b;
+      const int first = R::kLap != 0 && lap && b == 0 ? kChunks - 1 : 0;
+      for (int i = 0; i < kChunks; ++i) {
+        const int c = half * kWarpCols + (first + i) % kChunks * 32;
+        float v[32];
+        tmem_ld_32x32b_x32(tq + c, v);
+        if (lap && i == 0) arrive(lap_empty);
+        if (i == kChunks - 1) arrive(&acc_empty[b]);
+        if constexpr (SPLIT) {
+          // all products are done: the ring is free for this CTA's part
+          float* part = reinterpret_cast<float*>(smem);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) part[(c + e) * kBM + quarter * 32 + lane] = v[e];
+        } else if (m0 + c < args.M) {
+          by_kind(args, PutCall{args, ch, n, m0 + c, v});
+        }
+        __syncwarp();  // the next load takes the whole warp
+      }
+    }
+  }
+  if (timed_out && args.status != nullptr) atomicOr(args.status, DLRM_FLAG_TIMEOUT);
+  if constexpr (SPLIT) {
+    cluster_sync();  // every CTA's part is in its shared memory
+    if (warp >= 2) {
+      int tm, tn;
+      tile_at(args, unit0, tm, tn);
+      const int c0 = BN * static_cast<int>(rank) / S, c1 = BN * static_cast<int>(rank + 1) / S;
+      by_kind(args, JoinCall<S>{args, tn * kBM, tm * BN, c0, c1, warp - 2, lane, smem_u32(smem)});
+    }
+  }
+  tc_fence_before_sync();
+  if constexpr (PAIR || SPLIT)
+    cluster_sync();  // no CTA leaves while another may still use its memory
+  else
+    __syncthreads();
+  tc_fence_after_sync();
+  if (warp == 1) tmem_dealloc<CG>(tmem, R::kTmem);
+}
+
+// Few tokens: a warp for each channel, a lane for each block of 32 columns. Codes become
+// twice their values as 8-bit integers (a byte permutation looks four up in a register
+// pair), four products an instruction, the block's sum exact in int32 and scaled once.
+// The tokens' codes are looked up once a CTA and kept in shared memory. Channels r and
+// r + 1 of each of a row tile's 32-row groups make a CTA: their scales are whole sectors.
+constexpr int kVecThreads = 256;
+constexpr int kFewTokens = 4;
+constexpr int kPiece = 128;  // blocks of K that a CTA takes at a time: 4 a lane
+
+struct VecArgs {
+  LinArgs lin;
+  const uint8_t* x;
+  const uint8_t* x_scale;
+  const uint8_t* w;
+  const uint8_t* w_scale;
+  int64_t ldx, ldw, block_tiles;
+  int blocks;       // of 32 columns
+  int bytes;        // of a row's codes
+};
+
+// Four codes (16 bits) as twice their values.
+__device__ __forceinline__ uint32_t doubled(uint32_t codes) {
+  const uint32_t at = codes & 0x7777u;
+  const uint32_t pos = __byte_perm(0x03020100u, 0x0c080604u, at);
+  const uint32_t neg = __byte_perm(0xfdfeff00u, 0xf4f8fafcu, at);
+  return __byte_perm(pos, neg, 0x3210u | ((codes >> 1) & 0x4444u));
+}
+
+// 16 bytes of a row's codes from byte `at` on; zeros past its end (rows start on 16 bytes and
+// their pitch is a multiple of it, but what lies past the codes is not theirs).
+__device__ __forceinline__ uint4 load_codes(const uint8_t* row, int at, int bytes) {
+  uint4 r = make_uint4(0, 0, 0, 0);
+  if (at + 16 <= bytes) {
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(row + at)
+                 : "memory");
+  } else if (at < bytes) {
+    uint32_t w[4] = {};
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (at + i < bytes) w[i / 4] |= static_cast<uint32_t>(row[at + i]) << (8 * (i % 4));
+    r = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return r;
+}
+
+template <int MT>
+struct FewCall {
+  const VecArgs& a;
+  int n, lane;
+  const float (&sum)[MT];
+  template <int ACT, class Out>
+  __device__ __forceinline__ void run() const {
+    float mine = 0.f;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+      if (lane == m) mine = sum[m];
+    if (lane < MT && lane < a.lin.M)
+      put_at<ACT>(static_cast<Out*>(a.lin.y) + lane * a.lin.ldy + n, mine,
+                  a.lin.bias != nullptr ? a.lin.bias[n] : 0.f);
+  }
+};
+
+template <int MT>
+__global__ void __launch_bounds__(kVecThreads) linear_few_kernel(const VecArgs a) {
+  // of each token and block: 32 bytes in two planes, and its scale's byte
+  __shared__ uint4 xv[MT][2][kPiece];
+  __shared__ uint8_t xe[MT][kPiece];
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // as in the kernel above
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tile = blockIdx.x / 16;
+  const int r = blockIdx.x % 16 * 2 + (warp & 1) + 32 * (warp >> 1);
+  const int n = tile * 128 + r;
+  const bool live = n < a.lin.N;
+  const uint8_t* w = a.w + static_cast<int64_t>(live ? n : 0) * a.ldw;
+  const uint8_t* ws = a.w_scale + fp4_scale_at(a.block_tiles, live ? n : 0, 0);
+  float acc[MT] = {};
+  constexpr int U = kPiece / 32;
+  for (int b0 = 0; b0 < a.blocks; b0 += kPiece) {
+    uint4 wv[U];
+    uint32_t we[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int b = b0 + u * 32 + lane;
+      wv[u] = make_uint4(0, 0, 0, 0);
+      we[u] = 0;
+      if (live && b < a.blocks) {
+        wv[u] = load_codes(w, b * 16, a.bytes);
+        we[u] = ws[static_cast<int64_t>(b >> 2) * kFp4Tile + (b & 3)];
+      }
+    }
+    __syncthreads();  // the piece before has been read
+    for (int i = threadIdx.x; i < MT * kPiece; i += kVecThreads) {
+      const int m = i / kPiece, p = i % kPiece, b = b0 + p;
+      uint4 c = make_uint4(0, 0, 0, 0);
+      uint32_t e = 0;
+      if (m < a.lin.M && b < a.blocks) {
+        c = load_codes(a.x + m * a.ldx, b * 16, a.bytes);
+        e = a.x_scale[fp4_scale_at(a.block_tiles, m, b)];
+      }
+      xv[m][0][p] = make_uint4(doubled(c.x), doubled(c.x >> 16), doubled(c.y), doubled(c.y >> 16));
+      xv[m][1][p] = make_uint4(doubled(c.z), doubled(c.z >> 16), doubled(c.w), doubled(c.w >> 16));
+      xe[m][p] = static_cast<uint8_t>(e);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int p = u * 32 + lane;
+      const uint32_t c[4] = {wv[u].x, wv[u].y, wv[u].z, wv[u].w};
+      uint32_t d[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d[2 * i] = doubled(c[i]), d[2 * i + 1] = doubled(c[i] >> 16);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        int s = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 x = xv[m][h][p];
+          s = __dp4a(static_cast<int>(d[4 * h]), static_cast<int>(x.x), s);
+          s = __dp4a(static_cast<int>(d[4 * h + 1]), static_cast<int>(x.y), s);
+          s = __dp4a(static_cast<int>(d[4 * h + 2]), static_cast<int>(x.z), s);
+          s = __dp4a(static_cast<int>(d[4 * h + 3]), static_cast<int>(x.w), s);
+        }
+        // The sum is four times that of the values. The scales' product in two halves, so
+        // that no product on the way leaves f32 where the last one does not.
+        const uint32_t ex = xe[m][p], e = we[u] + ex, e1 = max(we[u], ex) == 255u ? 255u : e >> 1;
+        acc[m] += static_cast<float>(s) * 0.25f * fp4_scale_value(e1) * fp4_scale_value(e - (e >> 1));
+      }
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) acc[m] += __shfl_xor_sync(kFull, acc[m], o);
+  if (live) by_kind(a.lin, FewCall<MT>{a, n, lane, acc});
+}
+
+struct Operands {
+  const uint8_t* x;
+  const uint8_t* x_scale;
+  const uint8_t* w;
+  const uint8_t* w_scale;
+  int64_t ldx, ldw, K;
+};
+
+// 2-D map of codes {bytes, rows} with the given pitch, box {128, box_rows}, 128-byte
+// swizzle; bytes past the matrix read as zero.
+cudaError_t encode_codes(CUtensorMap* map, const uint8_t* base, int64_t K, int64_t rows,
+                         int64_t ld, int box_rows) {
+  const EncodeTiledFn enc = encode_tiled();
+  if (enc == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>((K + 1) / 2), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
+  const cuuint32_t box[2] = {kBK, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims,
+                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// 3-D map of scale tiles {128 words, tiles along K, row tiles}, box {128, kStageTiles,
+// row_tiles}; tiles past the matrix read as zero.
+cudaError_t encode_scales(CUtensorMap* map, const uint8_t* base, int64_t K, int64_t rows,
+                          int row_tiles) {
+  const EncodeTiledFn enc = encode_tiled();
+  if (enc == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t kt = static_cast<cuuint64_t>(fp4_block_tiles(K));
+  const cuuint64_t dims[3] = {kFp4Tile / 4, kt, static_cast<cuuint64_t>((rows + 127) / 128)};
+  const cuuint64_t strides[2] = {kFp4Tile, kt * kFp4Tile};
+  const cuuint32_t box[3] = {kFp4Tile / 4, kStageTiles, static_cast<cuuint32_t>(row_tiles)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<uint8_t*>(base), dims,
+                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int BN, bool PAIR, int S>
+cudaError_t run_linear(const Operands& op, LinArgs args, int sms, cudaStream_t stream) {
+  constexpr bool SPLIT = S > 1;
+  using R = Ring<BN, PAIR>;
+  auto* fn = &linear_fp4_kernel<BN, PAIR, S>;
+  constexpr int smem = R::kTotal;
+  constexpr int kUnitN = (PAIR ? 2 : 1) * kBM;
+  LinMaps maps;
+  cudaError_t e = encode_codes(&maps.w, op.w, op.K, args.N, op.ldw, kBM);
+  if (e == cudaSuccess)
+    e = encode_codes(&maps.x, op.x, op.K, args.M, op.ldx, PAIR ? BN / 2 : BN);
+  if (e == cudaSuccess) e = encode_scales(&maps.sw, op.w_scale, op.K, args.N, 1);
+  if (e == cudaSuccess) e = encode_scales(&maps.sx, op.x_scale, op.K, args.M, R::kXTiles);
+  if (e != cudaSuccess) return e;
+  // Per device, the instance's shared-memory size is set and (pairs) the
+  // resident cluster count asked for once: 0 = not yet, else that count + 1.
+  static std::atomic<int> prepared[kMaxDevices];
+  int dev = -1;
+  if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+  const bool cacheable = dev >= 0 && dev < kMaxDevices;
+  const int cached = cacheable ? prepared[dev].load(std::memory_order_acquire) : 0;
+  if (cached == 0) {
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(fn),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  args.tiles_m = (args.M + BN - 1) / BN;
+  args.tiles_n = (args.N + kUnitN - 1) / kUnitN;
+  const int64_t tiles = static_cast<int64_t>(args.tiles_m) * args.tiles_n;
+  if (tiles > INT_MAX || static_cast<int64_t>(args.tiles_n) * 8 > INT_MAX)
+    return cudaErrorInvalidValue;
+  args.tiles = static_cast<int>(tiles);
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int64_t grid = std::min<int64_t>(tiles, sms);
+  int fit = cached > 0 ? cached - 1 : 0;
+  if constexpr (PAIR || SPLIT) {
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = PAIR ? 2 : S;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+  }
+  if constexpr (PAIR) {
+    int pairs = sms / 2;
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
+    if (cached == 0 && cudaOccupancyMaxActiveClusters(&fit, fn, &cfg) != cudaSuccess) {
+      (void)cudaGetLastError();
+      fit = 0;
+    }
+    if (fit > 0) pairs = std::min(pairs, fit);
+    grid = 2 * std::min<int64_t>(tiles, pairs);
+  }
+  if constexpr (SPLIT) grid = tiles * S;
+  if (cacheable && cached == 0) prepared[dev].store(fit + 1, std::memory_order_release);
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  return cudaLaunchKernelEx(&cfg, fn, maps, args);
+}
+
+template <int MT>
+cudaError_t run_few(const Operands& op, const LinArgs& args, cudaStream_t stream) {
+  const VecArgs a = {args, op.x, op.x_scale, op.w, op.w_scale, op.ldx, op.ldw,
+                     fp4_block_tiles(op.K), static_cast<int>((op.K + 31) / 32),
+                     static_cast<int>((op.K + 1) / 2)};
+  return launch(&linear_few_kernel<MT>, dim3(static_cast<unsigned>((args.N + 127) / 128 * 16)),
+                kVecThreads, 0, true, stream, a);
+}
+
+// The forms of the tensor-core kernel, with what they take in us: a stage (256 columns of
+// K), a tile besides, a tile at least (its drain), and the joining of a cluster's parts.
+struct Form {
+  int bn;
+  bool pair;
+  int split;
+  double step, tile, least, join;
+  cudaError_t (*run)(const Operands&, LinArgs, int, cudaStream_t);
+};
+const Form kForms[] = {
+    {64, false, 1, 0.290, 0.7, 0.0, 0.0, run_linear<64, false, 1>},
+    {64, false, 2, 0.290, 0.7, 0.0, 1.7, run_linear<64, false, 2>},
+    {64, false, 4, 0.290, 0.7, 0.0, 2.4, run_linear<64, false, 4>},
+    {128, false, 1, 0.280, 1.2, 2.0, 0.0, run_linear<128, false, 1>},
+    {128, false, 2, 0.280, 1.2, 2.0, 2.7, run_linear<128, false, 2>},
+    {128, false, 4, 0.280, 1.2, 2.0, 3.0, run_linear<128, false, 4>},
+    {256, true, 1, 0.310, 2.2, 3.7, 0.0, run_linear<256, true, 1>},
+};
+
+// Few tokens take the kernel for them; the others the form that takes the least
+// time by the figures above.
+cudaError_t launch_linear(const Operands& op, const LinArgs& args, int sms, cudaStream_t s) {
+  if (args.M <= kFewTokens) {
+    if (args.M == 1) return run_few<1>(op, args, s);
+    if (args.M == 2) return run_few<2>(op, args, s);
+    return run_few<4>(op, args, s);
+  }
+  Form best = {};
+  double least = 0;
+  for (const Form& f : kForms) {
+    const int64_t channels = f.pair ? 2 * kBM : kBM;
+    const int64_t tiles = (static_cast<int64_t>(args.M) + f.bn - 1) / f.bn *
+                          ((static_cast<int64_t>(args.N) + channels - 1) / channels);
+    // a cluster's CTAs run at the same time, and each has two K blocks at least
+    if (f.split > 1 && (tiles * f.split > 128 || args.nkb < 2 * f.split)) continue;
+    const int64_t units = f.pair ? sms / 2 : sms;
+    const int64_t rounds = (tiles + units - 1) / units;
+    const double us =
+        rounds * std::max(f.least, f.step * args.nkb / f.split + f.tile) + f.join;
+    if (best.run == nullptr || us < least) {
+      best = f;
+      least = us;
+    }
+  }
+  return best.run(op, args, sms, s);
+}
+
+}  // namespace
+}  // namespace dlrm
+
+extern "C" {
+
+int dlrm_linear_fp4(const uint8_t* x, int64_t ldx, const uint8_t* x_scale, const uint8_t* w,
+                    int64_t ldw, const uint8_t* w_scale, const float* bias, int64_t M, int64_t N,
+                    int64_t K, int act, void* y, int y_dtype, int64_t ldy, int32_t* status_dev,
+                    dlrm_stream_t stream) {
+  using namespace dlrm;
+  if (act < DLRM_ACT_NONE || act > DLRM_ACT_SIGMOID || !known_dtype(y_dtype)) return DLRM_ERR_ARG;
+  // room above M, N and K for the last tile's end
+  constexpr int64_t kMost = INT_MAX - 1024;
+  if (M < 0 || M > kMost || N < 1 || N > kMost || K < 1 || K > kMost) return DLRM_ERR_SHAPE;
+  if (ldx < (K + 1) / 2 || ldw < (K + 1) / 2 || ldy < N) return DLRM_ERR_SHAPE;
+  if (w == nullptr || w_scale == nullptr) return DLRM_ERR_NULL;
+  if (M > 0 && (x == nullptr || x_scale == nullptr || y == nullptr)) return DLRM_ERR_NULL;
+  if (ldx % 16 != 0 || ldw % 16 != 0 || !is_aligned(x, 16) || !is_aligned(w, 16) ||
+      !is_aligned(x_scale, 16) || !is_aligned(w_scale, 16) || !is_aligned(bias, 4) ||
+      !is_aligned(y, dtype_size(y_dtype)) || !is_aligned(status_dev, 4))
+    return DLRM_ERR_ALIGN;
+  if (M == 0) return DLRM_OK;
+  const int sms = sm_count_current();
+  if (sms == 0) return DLRM_ERR_CUDA;
+  LinArgs a = {};
+  a.bias = bias;
+  a.y = y;
+  a.ldy = ldy;
+  a.M = static_cast<int>(M);
+  a.N = static_cast<int>(N);
+  a.K = static_cast<int>(K);
+  a.nkb = static_cast<int>((K + kCols - 1) / kCols);
+  a.act = act;
+  a.y_bf16 = y_dtype == DLRM_TABLE_BF16;
+  a.status = status_dev;
+  const Operands op = {x, x_scale, w, w_scale, ldx, ldw, K};
+  const auto s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = launch_linear(op, a, sms, s);
+  if (e != cudaSuccess) return cuda_fail(e);
+  note_launch();
+  return DLRM_OK;
+}
+
+}  // extern "C"

@@ -7,7 +7,7 @@ library's tcgen05 kernel. bf16 tensors are ``torch.bfloat16``
 views whose row pitch is a multiple of 8 elements (16 bytes), as the layer's
 TMA loads require; :func:`bf16_empty` makes such buffers.
 
-Three arithmetics are offered (``mode``). ``"f32"`` (the default) is the pages' own: f32
+Four arithmetics are offered (``mode``). ``"f32"`` (the default) is the pages' own: f32
 activations times bf16 (or f32) weights with f32 results, through
 ``dlrm_linear_f32a``; each f32 activation travels between layers as three
 bf16 planes that sum to it exactly (:func:`planes_empty`,
@@ -15,7 +15,9 @@ bf16 planes that sum to it exactly (:func:`planes_empty`,
 ``dlrm_linear_bf16``), a third of the tensor work. ``"int8"`` rounds the rows of
 activations to 8-bit integers in front of every layer, with one scale for each
 row and for each output channel of the weights (:mod:`.int8`), half of the
-bytes of ``"bf16"`` at twice its tensor rate.
+bytes of ``"bf16"`` at twice its tensor rate. ``"fp4"`` rounds them to 4-bit floating
+point with a power of two for every 32 columns (:mod:`.fp4`): a quarter of the bytes
+at four times the rate.
 
 A DLRMv1 forward (:func:`dlrm_forward`) is: bottom MLP on the dense features
 -> ``dense`` (B, D); the sparse stage (pooled embeddings and the interaction
@@ -237,6 +239,10 @@ class MLP:
     Activations between layers, and the sums, are bf16 (an f32 input of a stack is
     rounded as its first sum): what an 8-bit level (2^-8 of its row's maximum) is
     rounded from need not be finer.
+
+    In ``"fp4"`` mode ``w`` is a pair ``(w_q, w_scale)`` too (:func:`fp4_layers`), the
+    input is an f32 or bf16 matrix, and the rows in front of each layer are rounded to 4
+    bits (:func:`.fp4.quantize_rows`); activations between layers are bf16.
     """
 
     def __init__(self, layers: Sequence[Tuple[torch.Tensor, torch.Tensor, str]],
@@ -244,14 +250,14 @@ class MLP:
                  norms: Optional[Sequence[Optional[torch.Tensor]]] = None, eps: float = 1e-6):
         if not layers:
             raise ValueError("an MLP needs at least one layer")
-        if mode not in ("bf16", "f32", "int8"):
-            raise ValueError("mode must be 'bf16', 'f32' or 'int8'")
+        if mode not in ("bf16", "f32", "int8", "fp4"):
+            raise ValueError("mode must be 'bf16', 'f32', 'int8' or 'fp4'")
         if norms is not None and mode != "int8":
             raise ValueError("norms need mode 'int8'")
         if norms is not None and len(norms) != len(layers):
             raise ValueError(f"norms must have {len(layers)} entries")
-        if mode == "int8" and any(isinstance(w, torch.Tensor) for w, _, _ in layers):
-            raise ValueError("an int8 layer's weights are (w_q, w_scale): see int8_layers")
+        if mode in ("int8", "fp4") and any(isinstance(w, torch.Tensor) for w, _, _ in layers):
+            raise ValueError(f"an {mode} layer's weights are (w_q, w_scale): see {mode}_layers")
         self.layers: List[Tuple[torch.Tensor, torch.Tensor, str]] = list(layers)
         self.mode = mode
         self.norms = list(norms) if norms is not None else [None] * len(self.layers)
@@ -260,7 +266,7 @@ class MLP:
     @property
     def out_features(self) -> int:
         w = self.layers[-1][0]
-        return (w[0] if self.mode == "int8" else w).shape[0]
+        return (w[0] if self.mode in ("int8", "fp4") else w).shape[0]
 
     def _forward_int8(self, x, last_f32: bool, last_bf16: bool, keep: bool):
         from . import int8
@@ -287,6 +293,19 @@ class MLP:
         y_n = None if not last_bf16 else _to_bf16_there(h) if last_f32 else h
         return ((y32, y_n), inputs) if keep else (y32, y_n)
 
+    def _forward_fp4(self, x, last_f32: bool, last_bf16: bool, keep: bool):
+        from . import fp4
+
+        inputs, h, n = [], x, len(self.layers)
+        for i, ((w_q, w_scale), b, act) in enumerate(self.layers):
+            q, s = fp4.quantize_rows(h)
+            inputs.append((q, s))
+            dtype = torch.float32 if i == n - 1 and last_f32 else torch.bfloat16
+            h = fp4.linear_fp4(q, s, w_q, w_scale, b, act, out_dtype=dtype)
+        y32 = h if last_f32 else None
+        y_n = None if not last_bf16 else _to_bf16_there(h) if last_f32 else h
+        return ((y32, y_n), inputs) if keep else (y32, y_n)
+
     def forward(self, x: torch.Tensor, *, a_hi: Optional[torch.Tensor] = None,
                 last_f32: bool = True, last_bf16: bool = False, keep: bool = False):
         """Run the layers on ``x`` (and ``a_hi`` for the first layer's split form):
@@ -295,13 +314,17 @@ class MLP:
         Returns ``(y_f32, y_next)`` of the last layer -- ``y_next`` is its bf16
         output (``"bf16"``) or its planes (``"f32"``) when ``last_bf16`` is set
         -- plus the list of every layer's inputs when ``keep`` is set. In
-        ``"int8"`` mode ``x`` is an f32 or bf16 matrix, ``a_hi`` is not taken,
-        ``y_next`` is bf16 and a layer's input is its ``(q, scale)``.
+        ``"int8"`` and ``"fp4"`` modes ``x`` is an f32 or bf16 matrix, ``a_hi`` is not
+        taken, ``y_next`` is bf16 and a layer's input is its ``(q, scale)``.
         """
         if self.mode == "int8":
             if a_hi is not None:
                 raise ValueError("int8 layers take one input: a row has one scale")
             return self._forward_int8(x, last_f32, last_bf16, keep)
+        if self.mode == "fp4":
+            if a_hi is not None:
+                raise ValueError("fp4 layers take one input: scales lie in tiles of its columns")
+            return self._forward_fp4(x, last_f32, last_bf16, keep)
         inputs = []
         h, hi = x, a_hi
         n = len(self.layers)
@@ -326,6 +349,14 @@ def int8_layers(layers: Sequence[Tuple[torch.Tensor, torch.Tensor, str]]):
     return [(int8.quantize_rows(w), b, act) for w, b, act in layers]
 
 
+def fp4_layers(layers: Sequence[Tuple[torch.Tensor, torch.Tensor, str]]):
+    """Layers ``(w, bias, act)`` with f32 or bf16 weights ``(N, K)`` as ``"fp4"`` layers:
+    the weights rounded to 4 bits with a power of two for every 32 columns."""
+    from . import fp4
+
+    return [(fp4.quantize_rows(w), b, act) for w, b, act in layers]
+
+
 def dlrm_forward(bottom: MLP, top: MLP, dense_x: torch.Tensor, weights: Sequence[torch.Tensor],
                  indices: torch.Tensor, offsets: torch.Tensor, L: int, *, keep: bool = False):
     """DLRMv1 forward: CTR ``(B, 1)`` f32 from the dense features and the tables.
@@ -335,14 +366,14 @@ def dlrm_forward(bottom: MLP, top: MLP, dense_x: torch.Tensor, weights: Sequence
     bf16; top MLP with ``[dense | z]`` as its split first-layer input.
     ``"f32"`` MLPs: ``dense_x`` is f32 and every activation stays f32: the
     bottom MLP's output goes to the interaction as f32 and to the top MLP as
-    its exact planes, and z is split into planes. ``"int8"`` MLPs: ``dense_x`` is
-    f32 or bf16, and the sparse stage writes the rows ``[dense | z]`` that the top
-    MLP rounds to 8 bits. With ``keep`` it also returns a dict of the
+    its exact planes, and z is split into planes. ``"int8"`` and ``"fp4"`` MLPs:
+    ``dense_x`` is f32 or bf16, and the sparse stage writes the rows ``[dense | z]``
+    that the top MLP rounds to 8 or 4 bits. With ``keep`` it also returns a dict of the
     intermediate tensors.
     """
     if bottom.mode != top.mode:
         raise ValueError("the bottom and top MLPs must use the same mode")
-    if bottom.mode == "int8":
+    if bottom.mode in ("int8", "fp4"):
         dense32, _ = bottom.forward(dense_x)
         pooled, z = ops.sparse_interact(weights, indices, offsets, dense32, L, concat_dense=True)
         (ctr, _), top_inputs = top.forward(z, keep=True)
