@@ -125,7 +125,8 @@ __device__ __forceinline__ void store4(T* p, int left, const float* v) {
 }
 
 // Four codes as values: e4m3, and the roots' unsigned form (4 bits of exponent, 4 of
-// mantissa): its bits in an f32's exponent and mantissa, whose bias 2^112 corrects.
+// mantissa): its bits in an f32's exponent and mantissa (where a code without exponent is a
+// subnormal number, as the format has it), whose bias 2^112 corrects.
 __device__ __forceinline__ void first_values(uint32_t c, float scale, float* v) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -136,21 +137,36 @@ __device__ __forceinline__ void first_values(uint32_t c, float scale, float* v) 
     v[2 * i + 1] = f.y * scale;
   }
 }
-__device__ __forceinline__ float root_value(uint32_t code, float scale) {
-  return __uint_as_float(code << 19) * 0x1p112f * scale;
+__device__ __forceinline__ void root_values(uint32_t c, float scale, float* r) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t at = i < 3 ? c << (19 - 8 * i) : c >> 5;
+    r[i] = __uint_as_float(at & (0xffu << 19)) * 0x1p112f * scale;
+  }
 }
 
-// x >= 0 as a number of FRAC mantissa bits whose least normal power is 2^LEAST (below it
-// the steps stay as they are there): rounded down after 16 random bits below its last one.
+// x >= 0 as a code of FRAC mantissa bits: times the power of two that brings the format's
+// least normal number to that of f32, its exponent and upper mantissa bits are the code (below
+// it too: f32's subnormal numbers have even steps as the format's have), rounded down
+// after `chance`, random bits below the code's last one, was added.
 template <int FRAC, int LEAST, int TOP>
 __device__ __forceinline__ uint32_t code_of(float x, uint32_t chance) {
-  constexpr float kLeast = LEAST == -6 ? 0x1p-6f : 0x1p-14f;
-  static_assert(LEAST == -6 || LEAST == -14, "kLeast");
-  const bool small = x < kLeast;
-  const uint32_t bits = __float_as_uint(small ? x + kLeast : x) + (chance << (7 - FRAC));
-  const uint32_t code =
-      (bits >> (23 - FRAC)) - (small ? (127 + LEAST) << FRAC : (126 + LEAST) << FRAC);
-  return min(code, static_cast<uint32_t>(TOP));
+  constexpr float kLower = LEAST == -6 ? 0x1p-120f : 0x1p-112f;
+  static_assert(LEAST == -6 || LEAST == -14, "2^(-126 - LEAST)");
+  return min((__float_as_uint(x * kLower) + chance) >> (23 - FRAC), static_cast<uint32_t>(TOP));
+}
+
+// Root and quotient from the function units: within two last places, where an element's
+// step needs no more than that of its own size.
+__device__ __forceinline__ float root_of(float x) {
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float quotient(float a, float b) {
+  float r;
+  asm("div.approx.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
 // bf16 by chance: up with the probability of what is left over. Not a number and infinite
@@ -197,11 +213,9 @@ __device__ __forceinline__ void step_block(const StepArgs& a, const Factors& f, 
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       first_values(mc[h], ms, m + 4 * h);
+      root_values(vc[h], vs, v + 4 * h);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float r = root_value((vc[h] >> (8 * i)) & 0xff, vs);
-        v[4 * h + i] = r * r;
-      }
+      for (int i = 0; i < 4; ++i) v[4 * h + i] *= v[4 * h + i];
     }
   }
   const float keep = __fmaf_rn(-f.lr, t.decay, 1.f);
@@ -211,8 +225,8 @@ __device__ __forceinline__ void step_block(const StepArgs& a, const Factors& f, 
     const float x = g[i] * f.grad_scale;
     m[i] = __fmaf_rn(m[i], f.b1, x * f.b1c);
     v[i] = __fmaf_rn(v[i], f.b2, x * x * f.b2c);
-    r[i] = __fsqrt_rn(v[i]);
-    p[i] = __fmaf_rn(-f.alpha, __fdiv_rn(m[i], __fmaf_rn(r[i], f.root, a.eps)), p[i] * keep);
+    r[i] = root_of(v[i]);
+    p[i] = __fmaf_rn(-f.alpha, quotient(m[i], __fmaf_rn(r[i], f.root, a.eps)), p[i] * keep);
   }
   // a random word for each element
   uint32_t word[8];
@@ -241,19 +255,22 @@ __device__ __forceinline__ void step_block(const StepArgs& a, const Factors& f, 
     const float vinv = vtop != 0 && !vbad ? __fdiv_rn(1.9375f, __uint_as_float(vtop)) : 0.f;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      mc[h] = vc[h] = 0;
+      uint32_t c[4], d[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int k = 4 * h + i;
-        uint32_t c = code_of<3, -6, 126>(fabsf(m[k] * minv), word[k] & 0xffffu);
-        if (m[k] < 0.f && c != 0) c |= 128;
-        if (live) mc[h] |= c << (8 * i);
-        uint32_t d = code_of<4, -14, 255>(r[k] * vinv, word[k] >> 16);
-        if (r[k] > 0.f && d == 0) d = 1;
-        if (!vbad) vc[h] |= d << (8 * i);
+        c[i] = code_of<3, -6, 126>(fabsf(m[k]) * minv, (word[k] & 0xffffu) << 4);
+        d[i] = code_of<4, -14, 255>(r[k] * vinv, (word[k] >> 16) << 3);
+        d[i] = max(d[i], min(__float_as_uint(r[k]), 1u));  // what is not zero stays so
       }
-      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + at + q[h]) = mc[h];
-      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.v) + at + q[h]) = vc[h];
+      const uint32_t signs =
+          __byte_perm(__byte_perm(__float_as_uint(m[4 * h]), __float_as_uint(m[4 * h + 1]), 0x0073),
+                      __byte_perm(__float_as_uint(m[4 * h + 2]), __float_as_uint(m[4 * h + 3]), 0x0073),
+                      0x5410);
+      mc[h] = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24 | (signs & 0x80808080u);
+      vc[h] = d[0] | d[1] << 8 | d[2] << 16 | d[3] << 24;
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + at + q[h]) = live ? mc[h] : 0u;
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.v) + at + q[h]) = vbad ? 0u : vc[h];
     }
     if (lane == 0) {
       const float nan = __uint_as_float(0x7fc00000u);
@@ -354,11 +371,9 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     first_values(mw[i], ms, mf + 4 * i);
+    root_values(vw[i], vs, vf + 4 * i);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float r = root_value((vw[i] >> (8 * k)) & 0xff, vs);
-      vf[4 * i + k] = r * r;
-    }
+    for (int k = 0; k < 4; ++k) vf[4 * i + k] *= vf[4 * i + k];
   }
   constexpr int V = kVecOf<T>;
 #pragma unroll
