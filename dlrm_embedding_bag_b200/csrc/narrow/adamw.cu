@@ -10,6 +10,7 @@
 // that every access of a warp is whole lines (512 bytes of f32, 128 of codes)
 // and a block's largest moment is one warp reduction. Eight warps take a chunk of
 // 2048; CTAs stay and walk over the chunks.
+#include <cfloat>
 #include <cmath>
 #include <climits>
 
@@ -87,94 +88,127 @@ __device__ __forceinline__ uint32_t mixed(uint32_t x) {
   return x ^ (x >> 16);
 }
 
+// Two f32 as the pair that one instruction works on.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair(float lo, float hi) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ Pair both(float v) { return pair(v, v); }
+__device__ __forceinline__ float2 parts(Pair p) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ Pair mul(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // 4 elements at p.
 template <class T, bool ALL>
-__device__ __forceinline__ void load4(const T* p, int left, float* v) {
-  if constexpr (ALL) {
-    if constexpr (sizeof(T) == 4) {
-      const float4 r = *reinterpret_cast<const float4*>(p);
-      v[0] = r.x, v[1] = r.y, v[2] = r.z, v[3] = r.w;
-    } else {
-      const uint2 r = *reinterpret_cast<const uint2*>(p);
-      v[0] = __uint_as_float(r.x << 16), v[1] = __uint_as_float(r.x & 0xffff0000u);
-      v[2] = __uint_as_float(r.y << 16), v[3] = __uint_as_float(r.y & 0xffff0000u);
-    }
+__device__ __forceinline__ void load4(const T* p, int left, Pair* v) {
+  if constexpr (ALL && sizeof(T) == 4) {
+    const float4 r = *reinterpret_cast<const float4*>(p);
+    v[0] = pair(r.x, r.y), v[1] = pair(r.z, r.w);
+  } else if constexpr (ALL) {
+    const uint2 r = *reinterpret_cast<const uint2*>(p);
+    v[0] = pair(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u));
+    v[1] = pair(__uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u));
   } else {
+    float e[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = i < left ? static_cast<float>(p[i]) : 0.f;
+    for (int i = 0; i < 4; ++i) e[i] = i < left ? static_cast<float>(p[i]) : 0.f;
+    v[0] = pair(e[0], e[1]), v[1] = pair(e[2], e[3]);
   }
 }
 
 template <class T, bool ALL>
-__device__ __forceinline__ void store4(T* p, int left, const float* v) {
-  if constexpr (ALL) {
-    if constexpr (sizeof(T) == 4)
-      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    else
-      *reinterpret_cast<uint2*>(p) = make_uint2(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]));
+__device__ __forceinline__ void store4(T* p, int left, const Pair* v) {
+  const float2 a = parts(v[0]), b = parts(v[1]);
+  if constexpr (ALL && sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(a.x, a.y, b.x, b.y);
+  } else if constexpr (ALL) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(bf16x2_bits(a.x, a.y), bf16x2_bits(b.x, b.y));
   } else {
+    const float e[4] = {a.x, a.y, b.x, b.y};
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (i < left) {
-        if constexpr (sizeof(T) == 4)
-          p[i] = v[i];
-        else
-          p[i] = __float2bfloat16_rn(v[i]);
-      }
+      if (i < left) p[i] = static_cast<T>(e[i]);
   }
 }
 
-// Four codes as values: e4m3, and the roots' unsigned form (4 bits of exponent, 4 of
-// mantissa): its bits in an f32's exponent and mantissa (where a code without exponent is a
-// subnormal number, as the format has it), whose bias 2^112 corrects.
-__device__ __forceinline__ void first_values(uint32_t c, float scale, float* v) {
+__device__ __forceinline__ Pair of_halves(uint32_t h) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return pair(f.x, f.y);
+}
+// Four codes as numbers without their scale: e4m3, and the roots' unsigned form (4 bits of
+// exponent, 4 of mantissa), which is a half-precision number without its sign, the
+// exponent's first bit and the mantissa's last six.
+__device__ __forceinline__ void first_values(uint32_t c, Pair* v) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     uint32_t h;
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<unsigned short>(c >> (16 * i))));
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-    v[2 * i] = f.x * scale;
-    v[2 * i + 1] = f.y * scale;
+    v[i] = of_halves(h);
   }
 }
-__device__ __forceinline__ void root_values(uint32_t c, float scale, float* r) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t at = i < 3 ? c << (19 - 8 * i) : c >> 5;
-    r[i] = __uint_as_float(at & (0xffu << 19)) * 0x1p112f * scale;
-  }
+__device__ __forceinline__ void root_values(uint32_t c, Pair* r) {
+  r[0] = of_halves(__byte_perm(c, 0, 0x4140) << 6);
+  r[1] = of_halves(__byte_perm(c, 0, 0x4342) << 6);
 }
 
-// x >= 0 as a code of FRAC mantissa bits: times the power of two that brings the format's
-// least normal number to that of f32, its exponent and upper mantissa bits are the code (below
-// it too: f32's subnormal numbers have even steps as the format's have), rounded down
-// after `chance`, random bits below the code's last one, was added.
-template <int FRAC, int LEAST, int TOP>
-__device__ __forceinline__ uint32_t code_of(float x, uint32_t chance) {
-  constexpr float kLower = LEAST == -6 ? 0x1p-120f : 0x1p-112f;
-  static_assert(LEAST == -6 || LEAST == -14, "2^(-126 - LEAST)");
-  return min((__float_as_uint(x * kLower) + chance) >> (23 - FRAC), static_cast<uint32_t>(TOP));
+// Numbers become codes by their own bits: times the power of two that brings the format's
+// least normal number to that of f32, exponent and upper mantissa are the code (below
+// it too: f32's subnormal numbers have even steps as the format's have). Random bits are added
+// below the code's last one before the rest is cut off. They are less than a step by
+// 2^-16 of one, and the block's largest is above the largest code by 2^-17 of a step at
+// most, so no code is left at its upper end.
+constexpr float kFirstLower = 0x1p-120f, kRootLower = 0x1p-112f;
+// Bits [lo, lo + n) of t as bits [to, to + n).
+__device__ __forceinline__ uint32_t moved(uint32_t t, int lo, int n, int to) {
+  const uint32_t mask = ((1u << n) - 1u) << to;
+  return (lo >= to ? t >> (lo - to) : t << (to - lo)) & mask;
 }
 
-// Root and quotient from the function units: within two last places, where an element's
-// step needs no more than that of its own size.
+// Root and reciprocal from the function units, within two last places: an element's step needs
+// no more of its own size.
+template <bool TINY>
 __device__ __forceinline__ float root_of(float x) {
   float r;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  if constexpr (TINY)
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  else
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ float quotient(float a, float b) {
+__device__ __forceinline__ float reciprocal(float x) {
   float r;
-  asm("div.approx.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// max(|a|, |b|, |c|), NaN if one is.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
-// bf16 by chance: up with the probability of what is left over. Not a number and infinite
-// stay so.
-__device__ __forceinline__ float by_chance(float x, uint32_t chance) {
-  const uint32_t b = __float_as_uint(x);
-  if ((b & 0x7f800000u) == 0x7f800000u) return x;
-  return __uint_as_float((b + chance) & 0xffff0000u);
+// Towards bf16 by chance: what a cut after the upper half makes of it goes up with the
+// probability of what is left over. NaN stays NaN (an infinity has nothing to carry).
+__device__ __forceinline__ float by_chance(float x, uint32_t word) {
+  const float y = __uint_as_float(__float_as_uint(x) + ((word * 0x3C6EF373u) >> 16));
+  return x != x ? x : y;
+}
+__device__ __forceinline__ uint32_t upper_halves(float lo, float hi) {
+  return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
 }
 
 // One block of 256 elements of a tensor by one warp; `left` elements of it are there.
@@ -189,22 +223,22 @@ __device__ __forceinline__ void step_block(const StepArgs& a, const Factors& f, 
   const G* grad = static_cast<const G*>(t.grad) + e0;
   const bool whole = sizeof(P) == 2 && a.master != nullptr;
 
-  float p[8], g[8], m[8], v[8];
+  Pair p[4], g[4], m[4], v[4];
   uint32_t mc[2], vc[2];
-  float ms = 0.f, vs = 0.f;
+  float ms = 1.f, vs = 1.f;  // the scales of what was read
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    load4<G, ALL>(grad + q[h], left - q[h], g + 4 * h);
+    load4<G, ALL>(grad + q[h], left - q[h], g + 2 * h);
     if (whole)
-      load4<float, true>(a.master + at + q[h], 4, p + 4 * h);
+      load4<float, true>(a.master + at + q[h], 4, p + 2 * h);
     else
-      load4<P, ALL>(param + q[h], left - q[h], p + 4 * h);
+      load4<P, ALL>(param + q[h], left - q[h], p + 2 * h);
     if constexpr (BITS == 8) {
       mc[h] = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.m) + at + q[h]);
       vc[h] = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v) + at + q[h]);
     } else {
-      load4<float, true>(static_cast<const float*>(a.m) + at + q[h], 4, m + 4 * h);
-      load4<float, true>(static_cast<const float*>(a.v) + at + q[h], 4, v + 4 * h);
+      load4<float, true>(static_cast<const float*>(a.m) + at + q[h], 4, m + 2 * h);
+      load4<float, true>(static_cast<const float*>(a.v) + at + q[h], 4, v + 2 * h);
     }
   }
   if constexpr (BITS == 8) {
@@ -212,87 +246,111 @@ __device__ __forceinline__ void step_block(const StepArgs& a, const Factors& f, 
     vs = a.v_scale[block];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      first_values(mc[h], ms, m + 4 * h);
-      root_values(vc[h], vs, v + 4 * h);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[4 * h + i] *= v[4 * h + i];
+      first_values(mc[h], m + 2 * h);
+      root_values(vc[h], v + 2 * h);
     }
   }
-  const float keep = __fmaf_rn(-f.lr, t.decay, 1.f);
-  float r[8];
+  const Pair b1 = both(ms * f.b1), b1c = both(f.b1c), b2 = both(vs * vs * f.b2), b2c = both(f.b2c);
+  const Pair scale = both(f.grad_scale), keep = both(__fmaf_rn(-f.lr, t.decay, 1.f));
+  const Pair alpha = both(-f.alpha), root = both(f.root), eps = both(a.eps);
+  Pair r[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float x = g[i] * f.grad_scale;
-    m[i] = __fmaf_rn(m[i], f.b1, x * f.b1c);
-    v[i] = __fmaf_rn(v[i], f.b2, x * x * f.b2c);
-    r[i] = root_of(v[i]);
-    p[i] = __fmaf_rn(-f.alpha, quotient(m[i], __fmaf_rn(r[i], f.root, a.eps)), p[i] * keep);
+  for (int i = 0; i < 4; ++i) {
+    const Pair x = mul(g[i], scale);
+    if constexpr (BITS == 8) v[i] = mul(v[i], v[i]);  // of codes: exact
+    m[i] = fma(m[i], b1, mul(x, b1c));
+    v[i] = fma(v[i], b2, mul(mul(x, b2c), x));
+    const float2 w = parts(v[i]);
+    r[i] = pair(root_of<BITS == 32>(w.x), root_of<BITS == 32>(w.y));
+    const float2 d = parts(fma(r[i], root, eps));
+    p[i] = fma(mul(m[i], pair(reciprocal(d.x), reciprocal(d.y))), alpha, mul(p[i], keep));
   }
   // a random word for each element
   uint32_t word[8];
   if constexpr (BITS == 8 || sizeof(P) == 2) {
-    const uint32_t base = mixed(f.key ^ block);
+    const uint32_t base = mixed(f.key ^ block) + static_cast<uint32_t>(q[0]) * 0x9E3779B9u;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      word[i] = mixed(base + static_cast<uint32_t>(q[i / 4] + i % 4) * 0x9E3779B9u);
+      word[i] = mixed(base + static_cast<uint32_t>(i / 4 * 128 + i % 4) * 0x9E3779B9u);
   }
   if constexpr (BITS == 8) {
     // what lies behind the tensor's end stays zero: its gradient was read as zero
-    uint32_t mtop = 0, vtop = 0;
+    float mf = 0.f, vf = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      mtop = max(mtop, __float_as_uint(fabsf(m[i])));
-      vtop = max(vtop, __float_as_uint(fabsf(r[i])));
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = parts(m[i]), y = parts(r[i]);
+      mf = max_abs(mf, x.x, x.y);
+      vf = max_abs(vf, y.x, y.y);
     }
-    mtop = __reduce_max_sync(kFull, mtop);
-    vtop = __reduce_max_sync(kFull, vtop);
+    // (of numbers that are not negative the bits' order is theirs, and NaN is above all)
+    const uint32_t mtop = __reduce_max_sync(kFull, __float_as_uint(mf));
+    const uint32_t vtop = __reduce_max_sync(kFull, __float_as_uint(vf));
+    mf = __uint_as_float(mtop), vf = __uint_as_float(vtop);
     const bool mbad = mtop >= 0x7f800000u, vbad = vtop >= 0x7f800000u;
-    float mscale = __fdiv_rn(__uint_as_float(mtop), 448.f);
-    const bool live = mscale >= 0x1p-126f && !mbad;
-    const float minv = live ? __fdiv_rn(448.f, __uint_as_float(mtop)) : 0.f;
-    if (!live) mscale = 0.f;
-    const float vscale = __fdiv_rn(__uint_as_float(vtop), 1.9375f);
-    const float vinv = vtop != 0 && !vbad ? __fdiv_rn(1.9375f, __uint_as_float(vtop)) : 0.f;
+    const bool live = mf >= 448.f * 0x1p-126f && !mbad;
+    const Pair minv = both(live ? __fdividef(448.f, mf) : 0.f), mlow = both(kFirstLower);
+    const Pair vinv = both(vtop != 0 && !vbad ? __fdividef(1.9375f, vf) : 0.f), vlow = both(kRootLower);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint32_t c[4], d[4];
+      uint32_t x[4], signs[2];
+      mc[h] = vc[h] = 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int k = 4 * h + i;
-        c[i] = code_of<3, -6, 126>(fabsf(m[k]) * minv, (word[k] & 0xffffu) << 4);
-        d[i] = code_of<4, -14, 255>(r[k] * vinv, (word[k] >> 16) << 3);
-        d[i] = max(d[i], min(__float_as_uint(r[k]), 1u));  // what is not zero stays so
+      for (int i = 0; i < 2; ++i) {
+        const float2 y = parts(mul(mul(m[2 * h + i], minv), mlow));
+        const float2 z = parts(mul(mul(r[2 * h + i], vinv), vlow));
+        x[2 * i] = __float_as_uint(y.x), x[2 * i + 1] = __float_as_uint(y.y);
+        signs[i] = __byte_perm(x[2 * i], x[2 * i + 1], 0x0073);
+        const uint32_t w0 = word[4 * h + 2 * i], w1 = word[4 * h + 2 * i + 1];
+        mc[h] |= moved(x[2 * i] + ((w0 & 0xffffu) << 4), 20, 7, 16 * i) |
+                 moved(x[2 * i + 1] + ((w1 & 0xffffu) << 4), 20, 7, 16 * i + 8);
+        vc[h] |= moved(__float_as_uint(z.x) + ((w0 >> 16) << 3), 19, 8, 16 * i) |
+                 moved(__float_as_uint(z.y) + ((w1 >> 16) << 3), 19, 8, 16 * i + 8);
       }
-      const uint32_t signs =
-          __byte_perm(__byte_perm(__float_as_uint(m[4 * h]), __float_as_uint(m[4 * h + 1]), 0x0073),
-                      __byte_perm(__float_as_uint(m[4 * h + 2]), __float_as_uint(m[4 * h + 3]), 0x0073),
-                      0x5410);
-      mc[h] = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24 | (signs & 0x80808080u);
-      vc[h] = d[0] | d[1] << 8 | d[2] << 16 | d[3] << 24;
+      mc[h] |= __byte_perm(signs[0], signs[1], 0x5410) & 0x80808080u;
+      // A root that is not zero stays so: a look at each only where one of four codes is zero.
+      if ((vc[h] - 0x01010101u) & ~vc[h] & 0x80808080u) {
+        const float2 y = parts(r[2 * h]), z = parts(r[2 * h + 1]);
+        if (y.x > 0.f && (vc[h] & 0xffu) == 0) vc[h] |= 1u;
+        if (y.y > 0.f && (vc[h] & 0xff00u) == 0) vc[h] |= 1u << 8;
+        if (z.x > 0.f && (vc[h] & 0xff0000u) == 0) vc[h] |= 1u << 16;
+        if (z.y > 0.f && (vc[h] & 0xff000000u) == 0) vc[h] |= 1u << 24;
+      }
       *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + at + q[h]) = live ? mc[h] : 0u;
       *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.v) + at + q[h]) = vbad ? 0u : vc[h];
     }
     if (lane == 0) {
       const float nan = __uint_as_float(0x7fc00000u);
-      a.m_scale[block] = mbad ? nan : mscale;
-      a.v_scale[block] = vbad ? nan : vscale;
+      a.m_scale[block] = mbad ? nan : live ? mf * (1.f / 448.f) : 0.f;
+      a.v_scale[block] = vbad ? nan : vf * (1.f / 1.9375f);
     }
   } else {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      store4<float, true>(static_cast<float*>(a.m) + at + q[h], 4, m + 4 * h);
-      store4<float, true>(static_cast<float*>(a.v) + at + q[h], 4, v + 4 * h);
+      store4<float, true>(static_cast<float*>(a.m) + at + q[h], 4, m + 2 * h);
+      store4<float, true>(static_cast<float*>(a.v) + at + q[h], 4, v + 2 * h);
     }
   }
-  if (whole) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) store4<float, true>(a.master + at + q[h], 4, p + 4 * h);
-  } else if constexpr (sizeof(P) == 2) {
+  for (int h = 0; h < 2; ++h) {
+    if (whole) {
+      store4<float, true>(a.master + at + q[h], 4, p + 2 * h);
+    } else if constexpr (sizeof(P) == 2) {
+      const float2 y = parts(p[2 * h]), z = parts(p[2 * h + 1]);
+      const uint32_t* w = word + 4 * h;
+      const uint2 b = make_uint2(upper_halves(by_chance(y.x, w[0]), by_chance(y.y, w[1])),
+                                 upper_halves(by_chance(z.x, w[2]), by_chance(z.y, w[3])));
+      if constexpr (ALL) {
+        *reinterpret_cast<uint2*>(param + q[h]) = b;
+      } else {
+        uint16_t* at_p = reinterpret_cast<uint16_t*>(param + q[h]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = by_chance(p[i], (word[i] * 0x3C6EF373u) >> 16);
+        for (int i = 0; i < 4; ++i)
+          if (q[h] + i < left) at_p[i] = static_cast<uint16_t>((i < 2 ? b.x : b.y) >> (16 * (i % 2)));
+      }
+      continue;
+    }
+    store4<P, ALL>(param + q[h], left - q[h], p + 2 * h);
   }
-#pragma unroll
-  for (int h = 0; h < 2; ++h) store4<P, ALL>(param + q[h], left - q[h], p + 4 * h);
 }
 
 template <int BITS, class P, class G>
@@ -336,14 +394,17 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   const int warp = threadIdx.x >> 5;
   int ti = 0;
   for (int c = blockIdx.x; c < a.chunks; c += gridDim.x) {
-    // the last tensor that starts at c or before it
-    int hi = a.n;
-    while (hi - ti > 1) {
-      const int mid = (ti + hi) >> 1;
-      if (a.t[mid].first <= c)
-        ti = mid;
-      else
-        hi = mid;
+    // the last tensor that starts at c or before it: near the last one, but for the first chunk
+    if (c == static_cast<int>(blockIdx.x)) {
+      for (int hi = a.n; hi - ti > 1;) {
+        const int mid = (ti + hi) >> 1;
+        if (a.t[mid].first <= c)
+          ti = mid;
+        else
+          hi = mid;
+      }
+    } else {
+      while (ti + 1 < a.n && a.t[ti + 1].first <= c) ++ti;
     }
     const Tensor& t = a.t[ti];
     const int64_t e0 = static_cast<int64_t>(c - t.first) * kChunk + warp * kBlock;
@@ -368,12 +429,20 @@ __global__ void __launch_bounds__(256)
   const float ms = m_scale[at / kBlock], vs = v_scale[at / kBlock];
   const uint32_t mw[4] = {mc.x, mc.y, mc.z, mc.w}, vw[4] = {vc.x, vc.y, vc.z, vc.w};
   float mf[16], vf[16];
+  const Pair mp = both(ms), vp = both(vs);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    first_values(mw[i], ms, mf + 4 * i);
-    root_values(vw[i], vs, vf + 4 * i);
+    Pair x[2], y[2];
+    first_values(mw[i], x);
+    root_values(vw[i], y);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) vf[4 * i + k] *= vf[4 * i + k];
+    for (int k = 0; k < 2; ++k) {
+      const float2 first = parts(mul(x[k], mp));
+      y[k] = mul(y[k], vp);
+      const float2 second = parts(mul(y[k], y[k]));
+      mf[4 * i + 2 * k] = first.x, mf[4 * i + 2 * k + 1] = first.y;
+      vf[4 * i + 2 * k] = second.x, vf[4 * i + 2 * k + 1] = second.y;
+    }
   }
   constexpr int V = kVecOf<T>;
 #pragma unroll
@@ -398,7 +467,7 @@ int dlrm_adamw_step(int64_t n, void* const* params, const void* const* grads,
   if (n < 0 || n > INT_MAX) return DLRM_ERR_SHAPE;
   if (bits != 8 && bits != 32) return DLRM_ERR_ARG;
   if (!(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1)) return DLRM_ERR_ARG;
-  if (!(static_cast<float>(eps) > 0.f) || !std::isfinite(static_cast<float>(eps)))
+  if (!(static_cast<float>(eps) >= FLT_MIN) || !std::isfinite(static_cast<float>(eps)))
     return DLRM_ERR_ARG;
   if (lr_dev == nullptr && !std::isfinite(lr)) return DLRM_ERR_ARG;
   if (step == nullptr) return DLRM_ERR_NULL;

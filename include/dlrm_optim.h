@@ -26,7 +26,8 @@
  * (to nearest, beta2 = 0.999 would hold the second moment where it is). A root that is
  * not zero is not stored as zero. A block that holds a NaN or an infinity
  * gets the scale NaN and codes 0: the moments of the block's elements are NaN from the
- * next step on. First moments of a block whose largest is below 448 * 2^-126 are dropped.
+ * next step on. First moments of a block whose largest is below 448 * 2^-126 are dropped,
+ * and second moments below 2^-126 are zero.
  *
  * The random bits are a hash of `seed`, the step and the element's place in the
  * arena: equal calls give equal bits.
@@ -70,7 +71,7 @@ extern "C" {
  *   step           dev int32[2]: steps taken so far, and a word of the call's own that
  *                  is zero between calls. t = step[0] + 1; the call writes it back.
  *   lr             learning rate, finite; lr_dev (dev f32) is taken instead if it is not NULL.
- *   beta1, beta2   in [0, 1); eps: positive in f32, finite.
+ *   beta1, beta2   in [0, 1); eps: a normal positive number of f32.
  *   grad_scale_dev dev f32 that every gradient is multiplied with (a clipping
  *                  coefficient), or NULL for 1.
  * The arenas and the parameters of one call must not be used by another call at the same
