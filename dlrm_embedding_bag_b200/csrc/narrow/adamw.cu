@@ -8,8 +8,10 @@
 //
 // A warp takes a block of 256 elements, a lane four neighbours in either half, so
 // that every access of a warp is whole lines (512 bytes of f32, 128 of codes)
-// and a block's largest moment is one warp reduction. Eight warps take a chunk of
-// 2048; CTAs stay and walk over the chunks.
+// and a block's largest moment is one warp reduction. Four warps take a chunk of 1024.
+// CTAs stay, and chunks are handed out in order by a counter: walking with a fixed
+// stride, CTAs drift apart and memory sees a wider and wider window of addresses (10^6 x
+// 64 f32 with 32-bit moments 294 us, with 8-bit ones 178; by tickets 262 and 156).
 #include <cfloat>
 #include <cmath>
 #include <climits>
@@ -24,11 +26,11 @@ namespace {
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kBlock = DLRM_ADAMW_BLOCK;
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kChunk = kWarps * kBlock;
 constexpr int kMaxTensors = 96;  // of one launch: their 40 bytes each fit the classic 4 KB of arguments
-constexpr int kCtasPerSm = 4;
+constexpr int kCtasPerSm = 8;
 
 enum TensorFlags { kParamBf16 = 1, kGradBf16 = 2, kAligned = 4 };
 
@@ -64,7 +66,7 @@ struct Factors {
   float b1, b1c, b2, b2c;  // the decays of the moments and what is left to 1
   float lr, alpha, root;   // alpha = lr / (1 - b1^t), root = 1 / sqrt(1 - b2^t)
   float grad_scale;
-  uint32_t key;  // of this step's random numbers
+  uint32_t t, key;         // the step's number, and the key of its random numbers
 };
 
 // b^t by squaring, in 64 bits: a few of their roundings off.
@@ -172,10 +174,19 @@ __device__ __forceinline__ void root_values(uint32_t c, Pair* r) {
 // 2^-16 of one, and the block's largest is above the largest code by 2^-17 of a step at
 // most, so no code is left at its upper end.
 constexpr float kFirstLower = 0x1p-120f, kRootLower = 0x1p-112f;
-// Bits [lo, lo + n) of t as bits [to, to + n).
-__device__ __forceinline__ uint32_t moved(uint32_t t, int lo, int n, int to) {
-  const uint32_t mask = ((1u << n) - 1u) << to;
-  return (lo >= to ? t >> (lo - to) : t << (to - lo)) & mask;
+// bits + (the low or the high 16 bits of a random word, times UNIT): one dot product of
+// halves and bytes, off the pipe of shifts and logic, which is the busiest here.
+template <int UNIT>
+__device__ __forceinline__ uint32_t plus_low(uint32_t word, uint32_t bits) {
+  return __dp2a_lo(word, static_cast<uint32_t>(UNIT), bits);
+}
+template <int UNIT>
+__device__ __forceinline__ uint32_t plus_high(uint32_t word, uint32_t bits) {
+  return __dp2a_lo(word, static_cast<uint32_t>(UNIT) << 8, bits);
+}
+// The upper bytes of four words.
+__device__ __forceinline__ uint32_t upper_bytes(const uint32_t (&t)[4]) {
+  return __byte_perm(__byte_perm(t[0], t[1], 0x0073), __byte_perm(t[2], t[3], 0x0073), 0x5410);
 }
 
 // Root and reciprocal from the function units, within two last places: an element's step needs
@@ -202,10 +213,9 @@ __device__ __forceinline__ float max_abs(float a, float b, float c) {
 }
 
 // Towards bf16 by chance: what a cut after the upper half makes of it goes up with the
-// probability of what is left over. NaN stays NaN (an infinity has nothing to carry).
+// probability of what is left over. (An infinity has nothing to carry; NaN is not given.)
 __device__ __forceinline__ float by_chance(float x, uint32_t word) {
-  const float y = __uint_as_float(__float_as_uint(x) + ((word * 0x3C6EF373u) >> 16));
-  return x != x ? x : y;
+  return __uint_as_float(plus_high<1>(word * 0x3C6EF373u, __float_as_uint(x)));
 }
 __device__ __forceinline__ uint32_t upper_halves(float lo, float hi) {
   return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
@@ -241,6 +251,14 @@ __device__ __forceinline__ void step_block(const StepArgs& a, const Factors& f, 
       load4<float, true>(static_cast<const float*>(a.v) + at + q[h], 4, v + 2 * h);
     }
   }
+  // a random word for each element, while those are on their way
+  uint32_t word[8];
+  if constexpr (BITS == 8 || sizeof(P) == 2) {
+    const uint32_t base = mixed(f.key ^ block) + static_cast<uint32_t>(q[0]) * 0x9E3779B9u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      word[i] = mixed(base + static_cast<uint32_t>(i / 4 * 128 + i % 4) * 0x9E3779B9u);
+  }
   if constexpr (BITS == 8) {
     ms = a.m_scale[block];
     vs = a.v_scale[block];
@@ -265,14 +283,6 @@ __device__ __forceinline__ void step_block(const StepArgs& a, const Factors& f, 
     const float2 d = parts(fma(r[i], root, eps));
     p[i] = fma(mul(m[i], pair(reciprocal(d.x), reciprocal(d.y))), alpha, mul(p[i], keep));
   }
-  // a random word for each element
-  uint32_t word[8];
-  if constexpr (BITS == 8 || sizeof(P) == 2) {
-    const uint32_t base = mixed(f.key ^ block) + static_cast<uint32_t>(q[0]) * 0x9E3779B9u;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      word[i] = mixed(base + static_cast<uint32_t>(i / 4 * 128 + i % 4) * 0x9E3779B9u);
-  }
   if constexpr (BITS == 8) {
     // what lies behind the tensor's end stays zero: its gradient was read as zero
     float mf = 0.f, vf = 0.f;
@@ -292,21 +302,23 @@ __device__ __forceinline__ void step_block(const StepArgs& a, const Factors& f, 
     const Pair vinv = both(vtop != 0 && !vbad ? __fdividef(1.9375f, vf) : 0.f), vlow = both(kRootLower);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint32_t x[4], signs[2];
-      mc[h] = vc[h] = 0;
+      uint32_t x[4], z[4];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float2 y = parts(mul(mul(m[2 * h + i], minv), mlow));
-        const float2 z = parts(mul(mul(r[2 * h + i], vinv), vlow));
-        x[2 * i] = __float_as_uint(y.x), x[2 * i + 1] = __float_as_uint(y.y);
-        signs[i] = __byte_perm(x[2 * i], x[2 * i + 1], 0x0073);
-        const uint32_t w0 = word[4 * h + 2 * i], w1 = word[4 * h + 2 * i + 1];
-        mc[h] |= moved(x[2 * i] + ((w0 & 0xffffu) << 4), 20, 7, 16 * i) |
-                 moved(x[2 * i + 1] + ((w1 & 0xffffu) << 4), 20, 7, 16 * i + 8);
-        vc[h] |= moved(__float_as_uint(z.x) + ((w0 >> 16) << 3), 19, 8, 16 * i) |
-                 moved(__float_as_uint(z.y) + ((w1 >> 16) << 3), 19, 8, 16 * i + 8);
+        const float2 mx = parts(mul(mul(m[2 * h + i], minv), mlow));
+        const float2 rx = parts(mul(mul(r[2 * h + i], vinv), vlow));
+        x[2 * i] = __float_as_uint(mx.x), x[2 * i + 1] = __float_as_uint(mx.y);
+        z[2 * i] = __float_as_uint(rx.x), z[2 * i + 1] = __float_as_uint(rx.y);
       }
-      mc[h] |= __byte_perm(signs[0], signs[1], 0x5410) & 0x80808080u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        // the code to the top of its word; the sign in front of the first moment's seven bits
+        const uint32_t w = word[4 * h + i];
+        x[i] = (plus_low<16>(w, x[i]) * 16u & 0x7fffffffu) | (x[i] & 0x80000000u);
+        z[i] = plus_high<8>(w, z[i]) * 32u;
+      }
+      mc[h] = upper_bytes(x);
+      vc[h] = upper_bytes(z);
       // A root that is not zero stays so: a look at each only where one of four codes is zero.
       if ((vc[h] - 0x01010101u) & ~vc[h] & 0x80808080u) {
         const float2 y = parts(r[2 * h]), z = parts(r[2 * h + 1]);
@@ -337,8 +349,12 @@ __device__ __forceinline__ void step_block(const StepArgs& a, const Factors& f, 
     } else if constexpr (sizeof(P) == 2) {
       const float2 y = parts(p[2 * h]), z = parts(p[2 * h + 1]);
       const uint32_t* w = word + 4 * h;
-      const uint2 b = make_uint2(upper_halves(by_chance(y.x, w[0]), by_chance(y.y, w[1])),
-                                 upper_halves(by_chance(z.x, w[2]), by_chance(z.y, w[3])));
+      uint2 b = make_uint2(upper_halves(by_chance(y.x, w[0]), by_chance(y.y, w[1])),
+                           upper_halves(by_chance(z.x, w[2]), by_chance(z.y, w[3])));
+      const float top = max_abs(max_abs(0.f, y.x, y.y), z.x, z.y);
+      if (top != top)  // with a NaN among them: by the conversion that keeps it
+        b = make_uint2(upper_halves(y.x != y.x ? y.x : by_chance(y.x, w[0]), y.y != y.y ? y.y : by_chance(y.y, w[1])),
+                       upper_halves(z.x != z.x ? z.x : by_chance(z.x, w[2]), z.y != z.y ? z.y : by_chance(z.y, w[3])));
       if constexpr (ALL) {
         *reinterpret_cast<uint2*>(param + q[h]) = b;
       } else {
@@ -368,6 +384,7 @@ template <int BITS>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     adamw_kernel(const __grid_constant__ StepArgs a) {
   __shared__ Factors shared;
+  __shared__ int next[2];
   if (threadIdx.x == 0) {
     const uint32_t t = static_cast<uint32_t>(a.step[0]) + 1u;
     const double lr = a.lr_dev != nullptr ? static_cast<double>(*a.lr_dev) : a.lr;
@@ -379,42 +396,73 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     shared.alpha = static_cast<float>(lr / (1.0 - power(a.beta1, t)));
     shared.root = static_cast<float>(1.0 / sqrt(1.0 - power(a.beta2, t)));
     shared.grad_scale = a.grad_scale != nullptr ? *a.grad_scale : 1.f;
+    shared.t = t;
     shared.key = mixed(mixed(a.seed + 0x9E3779B9u) ^ t);
-    if (a.last) {
-      // the last CTA to have read the count writes the next one
-      __threadfence();
-      if (atomicAdd(a.step + 1, 1) == static_cast<int>(gridDim.x) - 1) {
-        a.step[1] = 0;
-        a.step[0] = static_cast<int32_t>(t);
-      }
-    }
+    __threadfence();  // the count is read before this CTA draws a ticket
   }
   __syncthreads();
   const Factors f = shared;
   const int warp = threadIdx.x >> 5;
+  // Chunks are handed out in order, by tickets that a CTA draws while it works on the chunk
+  // before: the first chunks are the CTAs' own numbers, and one ticket for each chunk (or
+  // one) is drawn in all, for each CTA learns from its last one that there are no more.
+  const int tickets = max(a.chunks, 1);
   int ti = 0;
-  for (int c = blockIdx.x; c < a.chunks; c += gridDim.x) {
-    // the last tensor that starts at c or before it: near the last one, but for the first chunk
-    if (c == static_cast<int>(blockIdx.x)) {
-      for (int hi = a.n; hi - ti > 1;) {
-        const int mid = (ti + hi) >> 1;
-        if (a.t[mid].first <= c)
-          ti = mid;
-        else
-          hi = mid;
+  for (int c = blockIdx.x, turn = 0;; turn ^= 1) {
+    int ticket = 0;
+    if (threadIdx.x == 0) ticket = atomicAdd(a.step + 1, 1);
+    if (c < a.chunks) {
+      // the last tensor that starts at c or before it: near the last one, but for the first
+      // chunk
+      if (c == static_cast<int>(blockIdx.x)) {
+        for (int hi = a.n; hi - ti > 1;) {
+          const int mid = (ti + hi) >> 1;
+          if (a.t[mid].first <= c)
+            ti = mid;
+          else
+            hi = mid;
+        }
+      } else {
+        while (ti + 1 < a.n && a.t[ti + 1].first <= c) ++ti;
       }
-    } else {
-      while (ti + 1 < a.n && a.t[ti + 1].first <= c) ++ti;
+      const Tensor& t = a.t[ti];
+      const int64_t e0 = static_cast<int64_t>(c - t.first) * kChunk + warp * kBlock;
+      switch (t.flags & (kParamBf16 | kGradBf16)) {
+        case 0: step_warp<BITS, float, float>(a, f, t, e0); break;
+        case kParamBf16: step_warp<BITS, __nv_bfloat16, float>(a, f, t, e0); break;
+        case kGradBf16: step_warp<BITS, float, __nv_bfloat16>(a, f, t, e0); break;
+        default: step_warp<BITS, __nv_bfloat16, __nv_bfloat16>(a, f, t, e0); break;
+      }
     }
-    const Tensor& t = a.t[ti];
-    const int64_t e0 = static_cast<int64_t>(c - t.first) * kChunk + warp * kBlock;
-    switch (t.flags & (kParamBf16 | kGradBf16)) {
-      case 0: step_warp<BITS, float, float>(a, f, t, e0); break;
-      case kParamBf16: step_warp<BITS, __nv_bfloat16, float>(a, f, t, e0); break;
-      case kGradBf16: step_warp<BITS, float, __nv_bfloat16>(a, f, t, e0); break;
-      default: step_warp<BITS, __nv_bfloat16, __nv_bfloat16>(a, f, t, e0); break;
+    if (threadIdx.x == 0) {
+      next[turn] = ticket + static_cast<int>(gridDim.x);
+      if (ticket == tickets - 1) {
+        // every CTA has read the count and drawn its last ticket
+        a.step[1] = 0;
+        if (a.last) a.step[0] = static_cast<int32_t>(f.t);
+      }
     }
+    __syncthreads();
+    c = next[turn];
+    if (c >= a.chunks) break;
   }
+}
+
+// 16 values at p, which starts on 32 bytes: whole sectors a store, past the cache's order of use.
+template <class T>
+__device__ __forceinline__ void store_sectors(T* p, const float* v) {
+  constexpr int kWords = 4 * sizeof(T);
+  uint32_t w[kWords];
+#pragma unroll
+  for (int i = 0; i < kWords; ++i)
+    w[i] = sizeof(T) == 4 ? __float_as_uint(v[i]) : bf16x2_bits(v[2 * i], v[2 * i + 1]);
+#pragma unroll
+  for (int i = 0; i < kWords; i += 8)
+    asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                     reinterpret_cast<uint32_t*>(p) + i),
+                 "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]),
+                 "r"(w[i + 5]), "r"(w[i + 6]), "r"(w[i + 7])
+                 : "memory");
 }
 
 // 8-bit moments as values: 16 elements a thread.
@@ -444,12 +492,8 @@ __global__ void __launch_bounds__(256)
       vf[4 * i + 2 * k] = second.x, vf[4 * i + 2 * k + 1] = second.y;
     }
   }
-  constexpr int V = kVecOf<T>;
-#pragma unroll
-  for (int i = 0; i < 16; i += V) {
-    store_f32<T, V>(m_out + at + i, *reinterpret_cast<const float(*)[V]>(mf + i));
-    store_f32<T, V>(v_out + at + i, *reinterpret_cast<const float(*)[V]>(vf + i));
-  }
+  store_sectors(m_out + at, mf);
+  store_sectors(v_out + at, vf);
 }
 
 }  // namespace
@@ -481,7 +525,7 @@ int dlrm_adamw_step(int64_t n, void* const* params, const void* const* grads,
     if (counts[i] < 0 || counts[i] >= (int64_t{1} << 40)) return DLRM_ERR_SHAPE;
     blocks += (counts[i] + kBlock - 1) / kBlock;
     chunks += (counts[i] + kChunk - 1) / kChunk;
-    if (blocks >= (int64_t{1} << 32) || chunks >= INT_MAX) return DLRM_ERR_SHAPE;
+    if (blocks >= (int64_t{1} << 32) || chunks > (1 << 30)) return DLRM_ERR_SHAPE;
     if (!known_dtype(param_dtypes[i]) || !known_dtype(grad_dtypes[i])) return DLRM_ERR_ARG;
     if (decays != nullptr && !std::isfinite(decays[i])) return DLRM_ERR_ARG;
     if (counts[i] == 0) continue;
@@ -557,7 +601,7 @@ int dlrm_adamw_moments(int64_t count, const void* m, const void* v, const float*
       m_out == nullptr || v_out == nullptr)
     return DLRM_ERR_NULL;
   if (!is_aligned(m, 16) || !is_aligned(v, 16) || !is_aligned(m_scale, 4) ||
-      !is_aligned(v_scale, 4) || !is_aligned(m_out, 16) || !is_aligned(v_out, 16))
+      !is_aligned(v_scale, 4) || !is_aligned(m_out, 32) || !is_aligned(v_out, 32))
     return DLRM_ERR_ALIGN;
   const dim3 grid(static_cast<unsigned>((count / 16 + 255) / 256));
   const auto* mb = static_cast<const uint8_t*>(m);
