@@ -12,6 +12,7 @@
 // CTAs stay, and chunks are handed out in order by a counter: walking with a fixed
 // stride, CTAs drift apart and memory sees a wider and wider window of addresses (10^6 x
 // 64 f32 with 32-bit moments 294 us, with 8-bit ones 178; by tickets 262 and 156).
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 #include <climits>
@@ -19,6 +20,7 @@
 #include <cuda_fp16.h>
 
 #include "dlrm_optim.h"
+#include "sectors.cuh"
 #include "tokens/common.h"
 
 namespace dlrm {
@@ -29,7 +31,11 @@ constexpr int kBlock = DLRM_ADAMW_BLOCK;
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kChunk = kWarps * kBlock;
-constexpr int kMaxTensors = 96;  // of one launch: their 40 bytes each fit the classic 4 KB of arguments
+// Tensors of one launch: 40 bytes each in its arguments, of which 4 KB are room for 96. Few
+// take a launch with room for 16, which is sooner made (a call for 12 tensors 9.3 and 7.4 us
+// of the host's time).
+constexpr int kMaxTensors = 96;
+constexpr int kFewTensors = 16;
 constexpr int kCtasPerSm = 8;
 
 enum TensorFlags { kParamBf16 = 1, kGradBf16 = 2, kAligned = 4 };
@@ -44,8 +50,7 @@ struct Tensor {
   int flags;
 };
 
-struct alignas(16) StepArgs {
-  Tensor t[kMaxTensors];
+struct StepArgs {
   void* m;
   void* v;
   float* m_scale;
@@ -59,6 +64,11 @@ struct alignas(16) StepArgs {
   uint32_t seed;
   int n, chunks;
   int last;  // whether this launch ends the step
+};
+template <int ROOM>
+struct ListArgs {
+  StepArgs step;
+  Tensor t[ROOM];
 };
 
 // What the whole step shares.
@@ -380,9 +390,10 @@ __device__ __forceinline__ void step_warp(const StepArgs& a, const Factors& f, c
     step_block<BITS, P, G, false>(a, f, t, e0, left < kBlock ? static_cast<int>(left) : kBlock);
 }
 
-template <int BITS>
+template <int BITS, int ROOM>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
-    adamw_kernel(const __grid_constant__ StepArgs a) {
+    adamw_kernel(const __grid_constant__ ListArgs<ROOM> args) {
+  const StepArgs& a = args.step;
   __shared__ Factors shared;
   __shared__ int next[2];
   if (threadIdx.x == 0) {
@@ -417,15 +428,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       if (c == static_cast<int>(blockIdx.x)) {
         for (int hi = a.n; hi - ti > 1;) {
           const int mid = (ti + hi) >> 1;
-          if (a.t[mid].first <= c)
+          if (args.t[mid].first <= c)
             ti = mid;
           else
             hi = mid;
         }
       } else {
-        while (ti + 1 < a.n && a.t[ti + 1].first <= c) ++ti;
+        while (ti + 1 < a.n && args.t[ti + 1].first <= c) ++ti;
       }
-      const Tensor& t = a.t[ti];
+      const Tensor& t = args.t[ti];
       const int64_t e0 = static_cast<int64_t>(c - t.first) * kChunk + warp * kBlock;
       switch (t.flags & (kParamBf16 | kGradBf16)) {
         case 0: step_warp<BITS, float, float>(a, f, t, e0); break;
@@ -446,23 +457,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     c = next[turn];
     if (c >= a.chunks) break;
   }
-}
-
-// 16 values at p, which starts on 32 bytes: whole sectors a store, past the cache's order of use.
-template <class T>
-__device__ __forceinline__ void store_sectors(T* p, const float* v) {
-  constexpr int kWords = 4 * sizeof(T);
-  uint32_t w[kWords];
-#pragma unroll
-  for (int i = 0; i < kWords; ++i)
-    w[i] = sizeof(T) == 4 ? __float_as_uint(v[i]) : bf16x2_bits(v[2 * i], v[2 * i + 1]);
-#pragma unroll
-  for (int i = 0; i < kWords; i += 8)
-    asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
-                     reinterpret_cast<uint32_t*>(p) + i),
-                 "r"(w[i]), "r"(w[i + 1]), "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]),
-                 "r"(w[i + 5]), "r"(w[i + 6]), "r"(w[i + 7])
-                 : "memory");
 }
 
 // 8-bit moments as values: 16 elements a thread.
@@ -494,6 +488,16 @@ __global__ void __launch_bounds__(256)
   }
   store_sectors(m_out + at, mf);
   store_sectors(v_out + at, vf);
+}
+
+template <int ROOM>
+cudaError_t launch_step(int bits, const StepArgs& a, const Tensor* t, int sms, cudaStream_t s) {
+  ListArgs<ROOM> args;
+  args.step = a;
+  std::copy(t, t + a.n, args.t);
+  const int grid = std::max(1, std::min(a.chunks, sms * kCtasPerSm));
+  return launch(bits == 8 ? &adamw_kernel<8, ROOM> : &adamw_kernel<32, ROOM>,
+                dim3(static_cast<unsigned>(grid)), kThreads, 0, false, s, args);
 }
 
 }  // namespace
@@ -543,47 +547,44 @@ int dlrm_adamw_step(int64_t n, void* const* params, const void* const* grads,
   }
   const int sms = sm_count_current();
   if (sms == 0) return DLRM_ERR_CUDA;
-  auto* kernel = bits == 8 ? &adamw_kernel<8> : &adamw_kernel<32>;
+  const auto s = static_cast<cudaStream_t>(stream);
+  StepArgs a = {};
+  a.m = m;
+  a.v = v;
+  a.m_scale = m_scale;
+  a.v_scale = v_scale;
+  a.master = master;
+  a.step = step;
+  a.lr_dev = lr_dev;
+  a.grad_scale = grad_scale_dev;
+  a.lr = lr;
+  a.beta1 = beta1;
+  a.beta2 = beta2;
+  a.eps = static_cast<float>(eps);
+  a.seed = seed;
   int64_t i = 0, block = 0;
   do {
-    StepArgs a;
-    a.n = 0;
-    int64_t c = 0;
+    Tensor list[kMaxTensors];
+    a.n = a.chunks = 0;
     for (; i < n && a.n < kMaxTensors; ++i) {
       if (counts[i] == 0) continue;
-      Tensor& t = a.t[a.n++];
+      Tensor& t = list[a.n++];
       t.param = params[i];
       t.grad = grads[i];
       t.count = counts[i];
       t.block0 = static_cast<uint32_t>(block);
-      t.first = static_cast<int>(c);
+      t.first = a.chunks;
       t.decay = decays != nullptr ? decays[i] : 0.f;
       t.flags = (param_dtypes[i] == DLRM_TABLE_BF16 ? kParamBf16 : 0) |
                 (grad_dtypes[i] == DLRM_TABLE_BF16 ? kGradBf16 : 0) |
                 (is_aligned(params[i], 16) && is_aligned(grads[i], 16) ? kAligned : 0);
       block += (counts[i] + kBlock - 1) / kBlock;
-      c += (counts[i] + kChunk - 1) / kChunk;
+      a.chunks += static_cast<int>((counts[i] + kChunk - 1) / kChunk);
     }
     while (i < n && counts[i] == 0) ++i;
-    a.m = m;
-    a.v = v;
-    a.m_scale = m_scale;
-    a.v_scale = v_scale;
-    a.master = master;
-    a.step = step;
-    a.lr_dev = lr_dev;
-    a.grad_scale = grad_scale_dev;
-    a.lr = lr;
-    a.beta1 = beta1;
-    a.beta2 = beta2;
-    a.eps = static_cast<float>(eps);
-    a.seed = seed;
-    a.chunks = static_cast<int>(c);
     a.last = i >= n;
-    const int64_t most = static_cast<int64_t>(sms) * kCtasPerSm;
-    const int grid = static_cast<int>(c < 1 ? 1 : c < most ? c : most);
-    const cudaError_t e = launch(kernel, dim3(static_cast<unsigned>(grid)), kThreads, 0, false,
-                                 static_cast<cudaStream_t>(stream), a);
+    const cudaError_t e = a.n <= kFewTensors ? launch_step<kFewTensors>(bits, a, list, sms, s)
+                                             : launch_step<kMaxTensors>(bits, a, list, sms, s);
     if (e != cudaSuccess) return cuda_fail(e);
     note_launch();
   } while (i < n);

@@ -6,13 +6,15 @@
 // 7/4: an integer addition to its bits. Products with powers of two are exact (where they
 // do not vanish, and then the code is 0), so a code is one rounding of its element.
 //
-// Two forms. Where rows start on 16 bytes a thread takes half a block, 16 elements, in
-// accesses of 16 or 32 bytes, and a block's two threads exchange their maxima. Elsewhere a
-// lane takes one column of several blocks, so that a warp still reads neighbours.
+// A thread takes half a block, 16 elements, and a block's two threads exchange their
+// maxima. Where rows start on 16 bytes it reads them in accesses of 16 or 32 bytes.
+// Elsewhere lanes read neighbouring elements of a row, whole lines, and lay them out in
+// shared memory from where each takes its own 16; values go back the same way.
 #include <algorithm>
 #include <climits>
 
 #include "fp4_common.cuh"
+#include "sectors.cuh"
 #include "tokens/common.h"
 
 namespace dlrm {
@@ -28,8 +30,9 @@ struct QuantArgs {
   uint8_t* scale;
   int64_t ldx, ldq, block_tiles;
   int M, K;
-  int rows, blocks;  // with the scales' padding: multiples of 128 and of 4
-  Divisor by;        // a row's blocks, or kUnits of them
+  int rows;    // with the scales' padding: a multiple of 128
+  int blocks;  // of a row
+  Divisor by;  // what a row is cut into: blocks, or pieces
 };
 
 // A block's scale byte from the bits of its largest magnitude.
@@ -53,81 +56,65 @@ __device__ __forceinline__ uint32_t codes_of(float lo, float hi) {
   return r;
 }
 
-__device__ __forceinline__ void load_32_bytes(const void* p, uint32_t (&w)[8]) {
-  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
-                 "=r"(w[6]), "=r"(w[7])
-               : "l"(p)
-               : "memory");
-}
-
-// BYTES (16 or 32) at a time.
-template <int BYTES, int N>
-__device__ __forceinline__ void load_words(const void* p, uint32_t (&w)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; i += 8) {
-    uint32_t part[8];
-    const char* at = static_cast<const char*>(p) + 4 * i;
-    if constexpr (BYTES == 32) {
-      load_32_bytes(at, part);
-    } else {
-      const uint4 a = reinterpret_cast<const uint4*>(at)[0], b = reinterpret_cast<const uint4*>(at)[1];
-      part[0] = a.x, part[1] = a.y, part[2] = a.z, part[3] = a.w;
-      part[4] = b.x, part[5] = b.y, part[6] = b.z, part[7] = b.w;
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) w[i + k] = part[k];
-  }
-}
-
-// Half a block a thread.
+// 16 elements from p, of which `left` are the row's, as words; what is not reads as zero.
+// BYTES: 16 or 32 at a time.
 template <class T, int BYTES>
-__global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int kWords = 16 * sizeof(T) / 4;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int64_t pair = i >> 1;
-  const int row = static_cast<int>(a.by.of(pair));
-  const int block = static_cast<int>(pair - static_cast<int64_t>(row) * a.blocks);
-  const int half = static_cast<int>(i & 1);
-  const int c = block * 32 + half * 16;
-  const bool live = row < a.M && c < a.K;
-  uint32_t w[kWords] = {};
-  const T* x = static_cast<const T*>(a.x) + row * a.ldx + c;
-  if (live && c + 16 <= a.K) {
-    load_words<BYTES>(x, w);
-  } else if (live) {
-    for (int e = 0; e < 16; ++e)
-      if (c + e < a.K) {
-        // (an index that the compiler knows would keep w in registers; this is one
-        // thread of a row)
-        if constexpr (sizeof(T) == 4) {
+__device__ __forceinline__ void load_half_block(const T* p, int left, uint32_t (&w)[4 * sizeof(T)]) {
+  constexpr int kPieces = sizeof(T);      // of 16 bytes
+  constexpr int kOfPiece = 16 / sizeof(T);  // elements
+  if (BYTES == 32 && left >= 16) {
 #pragma unroll
-          for (int k = 0; k < kWords; ++k)
-            if (k == e) w[k] = __float_as_uint(x[e]);
-        } else {
-          const uint32_t b = reinterpret_cast<const uint16_t*>(x)[e];
-#pragma unroll
-          for (int k = 0; k < kWords; ++k)
-            if (k == e / 2) w[k] |= b << (16 * (e & 1));
-        }
-      }
+    for (int i = 0; i < kPieces; i += 2)
+      load_32_bytes(p + i * kOfPiece, *reinterpret_cast<uint32_t(*)[8]>(w + 4 * i));
+    return;
   }
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i) {
+    const T* at = p + i * kOfPiece;
+    const int in = left - i * kOfPiece;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (in >= kOfPiece) {
+      v = *reinterpret_cast<const uint4*>(at);
+    } else if (in > 0) {
+      uint32_t e[4] = {};
+#pragma unroll
+      for (int k = 0; k < kOfPiece; ++k)
+        if (k < in) {
+          if constexpr (sizeof(T) == 4)
+            e[k] = __float_as_uint(at[k]);
+          else
+            e[k / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(at)[k]) << (16 * (k % 2));
+        }
+      v = make_uint4(e[0], e[1], e[2], e[3]);
+    }
+    w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+  }
+}
+
+// A thread's half block: its words rounded, codes and (a block's first thread) the scale
+// written. Every lane of a warp comes here; in: whether the row has such a block, or a
+// scale tile has it beside the row's.
+template <class T>
+__device__ __forceinline__ void round_half_block(const QuantArgs& a, int row, int block, int half,
+                                                 bool in, const uint32_t (&w)[4 * sizeof(T)]) {
+  constexpr int kWords = 4 * sizeof(T);
+  const int c = block * 32 + half * 16;
   uint32_t top = 0;
   if constexpr (sizeof(T) == 4) {
 #pragma unroll
     for (int k = 0; k < kWords; ++k) top = max(top, w[k] & 0x7fffffffu);
   } else {
-    uint32_t two = 0;
+    uint32_t both = 0;
 #pragma unroll
-    for (int k = 0; k < kWords; ++k) two = __vmaxu2(two, w[k] & 0x7fff7fffu);
-    top = max(two & 0xffff0000u, two << 16);
+    for (int k = 0; k < kWords; ++k) both = __vmaxu2(both, w[k] & 0x7fff7fffu);
+    top = max(both & 0xffff0000u, both << 16);
   }
   top = max(top, __shfl_xor_sync(kFull, top, 1));
+  if (!in) return;
   const uint32_t byte = scale_byte(top);
-  const float inv = byte == 255u ? 0.f : inverse_of(byte);
-  if (row < a.rows && half == 0) a.scale[fp4_scale_at(a.block_tiles, row, block)] = byte;
-  if (!live) return;
+  if (half == 0) a.scale[fp4_scale_at(a.block_tiles, row, block)] = static_cast<uint8_t>(byte);
+  if (row >= a.M || c >= a.K) return;
+  const float inv = inverse_of(byte);
   uint32_t out[2] = {};
   if (byte != 255u) {
 #pragma unroll
@@ -151,86 +138,144 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs a) {
   }
 }
 
-// A column a lane, kUnits blocks of a row a warp.
-constexpr int kUnits = 4;
-
-template <class T>
-__global__ void __launch_bounds__(kThreads) quantize_by_lanes_kernel(const QuantArgs a) {
+template <class T, int BYTES>
+__global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-  const int units = a.blocks / kUnits;  // blocks is a multiple of 4
-  const int row = static_cast<int>(a.by.of(unit));
-  const int block0 = static_cast<int>(unit - static_cast<int64_t>(row) * units) * kUnits;
-  if (row >= a.rows) return;
-  float v[kUnits];
-#pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
-    const int c = (block0 + u) * 32 + lane;
-    v[u] = 0.f;
-    if (row < a.M && c < a.K)
-      v[u] = static_cast<float>((static_cast<const T*>(a.x) + row * a.ldx)[c]);
-  }
-  uint32_t scales = 0;
-#pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
-    const uint32_t top = __reduce_max_sync(kFull, __float_as_uint(fabsf(v[u])));
-    const uint32_t byte = scale_byte(top);
-    scales |= byte << (8 * u);
-    const float mine = byte == 255u ? 0.f : v[u] * inverse_of(byte);
-    const float next = __shfl_down_sync(kFull, mine, 1);
-    const int c = (block0 + u) * 32 + lane;
-    if ((lane & 1) == 0 && row < a.M && c < a.K)
-      (a.q + row * a.ldq)[c / 2] = static_cast<uint8_t>(byte == 255u ? 0u : codes_of(mine, next));
-  }
-  if (lane == 0)
-    *reinterpret_cast<uint32_t*>(a.scale + fp4_scale_at(a.block_tiles, row, block0)) = scales;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  const int64_t two = i >> 1;
+  const int row = static_cast<int>(a.by.of(two));
+  const int block = static_cast<int>(two - static_cast<int64_t>(row) * a.blocks);
+  const int half = static_cast<int>(i & 1);
+  const int c = block * 32 + half * 16;
+  uint32_t w[4 * sizeof(T)] = {};
+  if (row < a.M && c < a.K)
+    load_half_block<T, BYTES>(static_cast<const T*>(a.x) + row * a.ldx + c, a.K - c, w);
+  round_half_block<T>(a, row, block, half, row < a.rows, w);
+  // the last block's thread ends the scale tile's four
+  if (half == 0 && row < a.rows && block == a.blocks - 1)
+    for (int k = block + 1; k & 3; ++k) a.scale[fp4_scale_at(a.block_tiles, row, k)] = 0;
 }
 
-// Back to values: 16 elements a thread, or one where rows do not start on 16 bytes.
+// Where a group of lanes lays a piece of a row out, 16 elements of each lane with 16 bytes
+// between them and the next lane's: 128-bit accesses of neighbouring lanes then meet in no
+// bank (80 or 48 bytes apart).
+template <class T>
+struct Staged {
+  static constexpr int kLane = 16 + 16 / sizeof(T);  // elements
+  T v[32 * kLane];
+  static __device__ __forceinline__ int at(int e) { return e / 16 * kLane + e % 16; }
+};
+
+// G lanes take 16 G columns of a row.
+template <class T, int G>
+__global__ void __launch_bounds__(kThreads) quantize_staged_kernel(const QuantArgs a, int pieces) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  static_assert(G % 8 == 0, "whole scale tiles");
+  __shared__ alignas(16) Staged<T> staged[kThreads / 32];
+  const int lane = threadIdx.x & 31, in = lane % G;
+  const int64_t unit = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / G;
+  const int row = static_cast<int>(a.by.of(unit));
+  const int piece = static_cast<int>(unit - static_cast<int64_t>(row) * pieces);
+  const int c0 = piece * 16 * G;
+  const int left = row < a.M ? a.K - c0 : 0;  // columns of the piece
+  const T* x = static_cast<const T*>(a.x) + row * a.ldx + c0 + in;
+  T v[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) v[j] = j * G + in < left ? x[j * G] : T(0.f);
+  T* mine = staged[threadIdx.x >> 5].v + lane / G * (G * Staged<T>::kLane);
+#pragma unroll
+  for (int j = 0; j < 16; ++j) mine[Staged<T>::at(j * G + in)] = v[j];
+  __syncwarp();
+  uint32_t w[4 * sizeof(T)];
+  const uint4* own = reinterpret_cast<const uint4*>(mine + Staged<T>::at(16 * in));
+#pragma unroll
+  for (int k = 0; k < static_cast<int>(sizeof(T)); ++k) {
+    const uint4 r = own[k];
+    w[4 * k] = r.x, w[4 * k + 1] = r.y, w[4 * k + 2] = r.z, w[4 * k + 3] = r.w;
+  }
+  const int block = piece * (G / 2) + in / 2;
+  round_half_block<T>(a, row, block, in & 1, row < a.rows && block < 4 * a.block_tiles, w);
+}
+
+// Back to values.
 struct DequantArgs {
   const uint8_t* q;
   const uint8_t* scale;
   void* y;
   int64_t ldq, ldy, block_tiles;
-  int M, K, groups;  // of 16 (or 1) elements in a row
-  Divisor by;        // groups
+  int M, K;
+  int groups;  // what a row is cut into: half blocks, or pieces
+  Divisor by;  // groups
 };
 
-__device__ __forceinline__ float value_of(uint32_t code, float scale) {
-  // the sign, then exponent and mantissa as an f32's, whose bias 2^126 corrects
-  return __uint_as_float((code & 8u) << 28 | (code & 7u) << 22) * 0x1p126f * scale;
+// The code in the upper four bits of t, whatever lies below them: its sign, then exponent and
+// mantissa as an f32's, whose bias 2^126 corrects.
+__device__ __forceinline__ float value_of(uint32_t t, float scale) {
+  return __uint_as_float((t & 0x80000000u) | (t >> 6 & 0x01c00000u)) * 0x1p126f * scale;
 }
 
-template <class T>
+template <class T, bool SECTORS>
 __global__ void __launch_bounds__(kThreads) dequantize_kernel(const DequantArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   const int64_t row = a.by.of(i);
   if (row >= a.M) return;
   const int c = static_cast<int>(i - row * a.groups) * 16;
-  const float scale = fp4_scale_value(a.scale[fp4_scale_at(a.block_tiles, static_cast<int>(row), c / 32)]);
+  const float scale =
+      fp4_scale_value(a.scale[fp4_scale_at(a.block_tiles, static_cast<int>(row), c / 32)]);
   const uint2 w = *reinterpret_cast<const uint2*>(a.q + row * a.ldq + c / 2);
   float v[16];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) v[e] = value_of(((e < 8 ? w.x : w.y) >> (4 * (e % 8))) & 15u, scale);
+  for (int e = 0; e < 16; ++e) v[e] = value_of((e < 8 ? w.x : w.y) << (28 - 4 * (e % 8)), scale);
   T* y = static_cast<T*>(a.y) + row * a.ldy + c;
   constexpr int V = kVecOf<T>;
+  if constexpr (SECTORS) {
+    store_sectors(y, v);
+  } else {
 #pragma unroll
-  for (int e = 0; e < 16; e += V) store_f32<T, V>(y + e, *reinterpret_cast<const float(*)[V]>(v + e));
+    for (int e = 0; e < 16; e += V)
+      store_f32<T, V, true>(y + e, *reinterpret_cast<const float(*)[V]>(v + e));
+  }
 }
 
-template <class T>
-__global__ void __launch_bounds__(kThreads) dequantize_one_kernel(const DequantArgs a) {
+template <class T, int G>
+__global__ void __launch_bounds__(kThreads) dequantize_staged_kernel(const DequantArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int64_t row = a.by.of(i);
-  if (row >= a.M) return;
-  const int c = static_cast<int>(i - row * a.groups);
-  const float v[1] = {
-      value_of((a.q[row * a.ldq + c / 2] >> (4 * (c & 1))) & 15u,
-               fp4_scale_value(a.scale[fp4_scale_at(a.block_tiles, static_cast<int>(row), c / 32)]))};
-  store_f32<T, 1>(static_cast<T*>(a.y) + row * a.ldy + c, v);
+  __shared__ alignas(16) Staged<T> staged[kThreads / 32];
+  const int lane = threadIdx.x & 31, in = lane % G;
+  const int64_t unit = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / G;
+  const int64_t row = a.by.of(unit);
+  const int c0 = static_cast<int>(unit - row * a.groups) * 16 * G;
+  const int c = c0 + 16 * in;
+  const int left = row < a.M ? a.K - c0 : 0;
+  uint32_t w[2] = {};
+  float scale = 0.f;
+  if (row < a.M && c < a.K) {
+    scale = fp4_scale_value(a.scale[fp4_scale_at(a.block_tiles, static_cast<int>(row), c / 32)]);
+    const uint8_t* q = a.q + row * a.ldq + c / 2;
+    const int bytes = (a.K - c + 1) / 2;
+    if (bytes >= 8 && (reinterpret_cast<uintptr_t>(q) & 7) == 0) {
+      const uint2 r = *reinterpret_cast<const uint2*>(q);
+      w[0] = r.x, w[1] = r.y;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < bytes) w[k / 4] |= static_cast<uint32_t>(q[k]) << (8 * (k % 4));
+    }
+  }
+  float v[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) v[e] = value_of(w[e / 8] << (28 - 4 * (e % 8)), scale);
+  T* mine = staged[threadIdx.x >> 5].v + lane / G * (G * Staged<T>::kLane);
+  constexpr int V = kVecOf<T>;
+#pragma unroll
+  for (int e = 0; e < 16; e += V)
+    store_f32<T, V>(mine + Staged<T>::at(16 * in) + e, *reinterpret_cast<const float(*)[V]>(v + e));
+  __syncwarp();
+  T* y = static_cast<T*>(a.y) + row * a.ldy + c0 + in;
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+    if (j * G + in < left) y[j * G] = mine[Staged<T>::at(j * G + in)];
 }
 
 constexpr int64_t kMost = INT_MAX - 1024;
@@ -242,33 +287,60 @@ bool fits(int64_t M, int64_t K) {
   return (M + 127) / 128 * fp4_block_tiles(K) <= kMostElements / (128 * 128) && M * K < kMostElements;
 }
 
+unsigned grid_of(int64_t things, int64_t a_block) {
+  return static_cast<unsigned>((things + a_block - 1) / a_block);
+}
+
+template <class T, int G>
+cudaError_t run_staged(QuantArgs a, cudaStream_t s) {
+  const int pieces = (a.blocks + G / 2 - 1) / (G / 2);
+  a.by = Divisor(static_cast<uint32_t>(pieces));
+  return launch(&quantize_staged_kernel<T, G>,
+                dim3(grid_of(static_cast<int64_t>(a.rows) * pieces * G, kThreads)), kThreads, 0,
+                true, s, a, pieces);
+}
+template <class T, int G>
+cudaError_t run_staged(DequantArgs a, cudaStream_t s) {
+  a.groups = (a.K + 16 * G - 1) / (16 * G);
+  a.by = Divisor(static_cast<uint32_t>(a.groups));
+  return launch(&dequantize_staged_kernel<T, G>,
+                dim3(grid_of(static_cast<int64_t>(a.M) * a.groups * G, kThreads)), kThreads, 0,
+                true, s, a);
+}
+// The lanes of a piece: as few as cover a short row, and no more columns past a long one's end than
+// a quarter warp's.
+template <class T, class Args>
+cudaError_t run_staged_by(const Args& a, cudaStream_t s) {
+  const int tail = (a.K - 1) % 512 + 1;
+  if (a.K <= 128 || (a.K < 2048 && tail <= 128)) return run_staged<T, 8>(a, s);
+  if (a.K <= 256 || (a.K < 4096 && tail <= 256)) return run_staged<T, 16>(a, s);
+  return run_staged<T, 32>(a, s);
+}
+
 template <class T>
 cudaError_t run_quantize(QuantArgs a, cudaStream_t s) {
   const int64_t pitch = a.ldx * static_cast<int64_t>(sizeof(T));
-  const int64_t threads = static_cast<int64_t>(a.rows) * a.blocks * 2;
   if (is_aligned(a.x, 16) && (pitch % 16 == 0 || a.M == 1)) {
     a.by = Divisor(static_cast<uint32_t>(a.blocks));
-    const dim3 grid(static_cast<unsigned>((threads + kThreads - 1) / kThreads));
-    if (is_aligned(a.x, 32) && (pitch % 32 == 0 || a.M == 1))
-      return launch(&quantize_kernel<T, 32>, grid, kThreads, 0, true, s, a);
-    return launch(&quantize_kernel<T, 16>, grid, kThreads, 0, true, s, a);
+    const dim3 grid(grid_of(static_cast<int64_t>(a.rows) * a.blocks * 2, kThreads));
+    const bool wide = is_aligned(a.x, 32) && (pitch % 32 == 0 || a.M == 1);
+    return launch(wide ? &quantize_kernel<T, 32> : &quantize_kernel<T, 16>, grid, kThreads, 0, true,
+                  s, a);
   }
-  a.by = Divisor(static_cast<uint32_t>(a.blocks / kUnits));
-  const int64_t warps = static_cast<int64_t>(a.rows) * (a.blocks / kUnits);
-  return launch(&quantize_by_lanes_kernel<T>,
-                dim3(static_cast<unsigned>((warps + kThreads / 32 - 1) / (kThreads / 32))),
-                kThreads, 0, true, s, a);
+  return run_staged_by<T>(a, s);
 }
 
 template <class T>
 cudaError_t run_dequantize(DequantArgs a, cudaStream_t s) {
   const bool wide = is_aligned(a.q, 8) && a.ldq % 8 == 0 && a.K % 16 == 0 &&
                     rows_by(a.y, a.ldy, sizeof(T), kVecOf<T>);
-  a.groups = wide ? a.K / 16 : a.K;
+  if (!wide) return run_staged_by<T>(a, s);
+  a.groups = a.K / 16;
   a.by = Divisor(static_cast<uint32_t>(a.groups));
-  const int64_t blocks = (static_cast<int64_t>(a.M) * a.groups + kThreads - 1) / kThreads;
-  return launch(wide ? &dequantize_kernel<T> : &dequantize_one_kernel<T>,
-                dim3(static_cast<unsigned>(blocks)), kThreads, 0, true, s, a);
+  const int64_t units = static_cast<int64_t>(a.M) * a.groups;
+  const bool sectors = is_aligned(a.y, 32) && a.ldy * sizeof(T) % 32 == 0;
+  return launch(sectors ? &dequantize_kernel<T, true> : &dequantize_kernel<T, false>,
+                dim3(grid_of(units, kThreads)), kThreads, 0, true, s, a);
 }
 
 }  // namespace
@@ -301,7 +373,7 @@ int dlrm_quantize_fp4(const void* x, int64_t ldx, int dtype, int64_t M, int64_t 
   a.M = static_cast<int>(M);
   a.K = static_cast<int>(K);
   a.rows = static_cast<int>((M + 127) / 128 * 128);
-  a.blocks = static_cast<int>(a.block_tiles * 4);
+  a.blocks = static_cast<int>((K + 31) / 32);
   const auto s = static_cast<cudaStream_t>(stream);
   const cudaError_t e =
       dtype == DLRM_TABLE_F32 ? run_quantize<float>(a, s) : run_quantize<__nv_bfloat16>(a, s);

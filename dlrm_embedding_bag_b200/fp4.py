@@ -19,7 +19,8 @@ import torch
 from . import ops
 from .mlp import ACTS
 from .optim import _call, _lib
-from .tokens import _empty, _flat, _matrix, _on, _pitch, _status
+from .tokens import (_empty, _empty_strided_cuda, _flat, _get_device, _matrix, _on, _pitch,
+                     _status)
 
 BLOCK = 32  # columns that share a scale
 
@@ -38,6 +39,14 @@ def fp4_empty(rows: int, cols: int, device="cuda") -> torch.Tensor:
 def scale_shape(rows: int, cols: int) -> Tuple[int, int, int]:
     """Shape of the scale tiles of a ``(rows, cols)`` matrix."""
     return (rows + 127) // 128, (cols + 127) // 128, 512
+
+
+def _empty_tiles(rows: int, cols: int, index: int) -> torch.Tensor:
+    """New scale tiles of a ``(rows, cols)`` matrix on device ``index``."""
+    r, c, n = scale_shape(rows, cols)
+    if _empty_strided_cuda is not None and index == _get_device():
+        return _empty_strided_cuda((r, c, n), (c * n, n, 1), torch.uint8)
+    return torch.empty((r, c, n), dtype=torch.uint8, device=torch.device("cuda", index))
 
 
 def _codes(t: torch.Tensor, name: str, index: Optional[int]) -> Tuple[int, int, int]:
@@ -65,14 +74,16 @@ def quantize_rows(x: torch.Tensor, *, out: Optional[torch.Tensor] = None,
     index, xd, M, K, ldx = _matrix(x, "x")
     width = (K + 1) // 2
     if out is None:
-        out = fp4_empty(M, K, x.device)
         ldq = (width + 15) // 16 * 16
+        out = _empty(M, ldq, torch.uint8, index)
+        if ldq != width:
+            out = out[:, :width]
     else:
         rows, cols, ldq = _codes(out, "out", index)
         if rows != M or cols != width:
             raise ValueError(f"out must be ({M}, {width}) (got {tuple(out.shape)})")
     if scale_out is None:
-        scale_out = torch.empty(scale_shape(M, K), dtype=torch.uint8, device=x.device)
+        scale_out = _empty_tiles(M, K, index)
         ps = scale_out.data_ptr()
     else:
         ps = _tiles(scale_out, "scale_out", M, K, index)

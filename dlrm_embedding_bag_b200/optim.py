@@ -17,9 +17,9 @@ the tensors that an :class:`.mlp.MLP` holds, bf16 weights and f32 biases in one 
 from __future__ import annotations
 
 import ctypes
-import math
 import os
 from array import array
+from operator import attrgetter
 from typing import NamedTuple, Optional, Sequence, Tuple, Union
 
 import torch
@@ -156,21 +156,38 @@ def adamw_state(params: Sequence[torch.Tensor], *, bits: int = 32,
 _CODES = ops.TABLE_DTYPES
 
 
-def _list(tensors: Sequence[torch.Tensor], name: str, index: int):
-    """(pointers, dtype codes, lengths) of contiguous f32 or bf16 tensors on device ``index``."""
-    pointers, codes, counts = array("q"), array("i"), array("q")
-    for t in tensors:
-        code = _CODES.get(t.dtype) if isinstance(t, torch.Tensor) else None
-        if code is None or not t.is_cuda or t.get_device() != index or not t.is_contiguous():
-            i = len(pointers)
-            _on(t, f"{name}[{i}]", index)
-            if code is None:
-                raise TypeError(f"{name}[{i}] must be float32 or bfloat16 (got {t.dtype})")
+_dtype_of, _shape_of = attrgetter("dtype"), attrgetter("shape")
+# methods of the class, which map() calls without a lookup for each tensor
+_device_of, _dense, _pointer, _length = (
+    torch.Tensor.get_device, torch.Tensor.is_contiguous, torch.Tensor.data_ptr, torch.Tensor.numel)
+
+
+def _refuse(tensors, name: str, index: int) -> None:
+    """Raises for the first of ``tensors`` that is not a contiguous f32 or bf16 one there."""
+    for i, t in enumerate(tensors):
+        _on(t, f"{name}[{i}]", index)
+        if t.dtype not in _CODES:
+            raise TypeError(f"{name}[{i}] must be float32 or bfloat16 (got {t.dtype})")
+        if not t.is_contiguous():
             raise ValueError(f"{name}[{i}] must be contiguous")
-        pointers.append(t.data_ptr())
-        codes.append(code)
-        counts.append(t.numel())
-    return pointers, codes, counts
+
+
+def _list(tensors: Sequence[torch.Tensor], name: str, index: int):
+    """(pointers, dtype codes) of contiguous f32 or bf16 tensors on device ``index``.
+
+    Whole lists are asked at once, a third of the time of a loop over the tensors; which
+    one is not right is looked for only then."""
+    try:
+        fine = all(map(_dense, tensors)) and set(map(_device_of, tensors)) <= {index}
+        types = list(map(_dtype_of, tensors))
+        codes = array("i", map(_CODES.__getitem__, types)) if len(set(types)) != 1 else \
+            array("i", (_CODES[types[0]],)) * len(types)
+    except (AttributeError, KeyError, TypeError):
+        fine = False
+    if not fine:
+        _refuse(tensors, name, index)
+        raise ValueError(f"{name} must be contiguous tensors on cuda:{index}")
+    return array("q", map(_pointer, tensors)), codes
 
 
 def _arena(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, n: int, index: int) -> int:
@@ -214,11 +231,12 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], st
     n = len(params)
     if len(grads) != n:
         raise ValueError(f"grads must have {n} entries (got {len(grads)})")
-    pp, pc, counts = _list(params, "params", index)
-    pg, gc, grad_counts = _list(grads, "grads", index)
-    if grad_counts != counts or any(p.shape != g.shape for p, g in zip(params, grads)):
+    pp, pc = _list(params, "params", index)
+    pg, gc = _list(grads, "grads", index)
+    if list(map(_shape_of, params)) != list(map(_shape_of, grads)):
         i = next(i for i in range(n) if params[i].shape != grads[i].shape)
         raise ValueError(f"grads[{i}] must be {tuple(params[i].shape)} (got {tuple(grads[i].shape)})")
+    counts = array("q", map(_length, params))
     total = sum([(c + BLOCK - 1) // BLOCK for c in counts]) * BLOCK
     ps = _flat(state.step, "state.step", torch.int32, index)
     if state.step.numel() != 2:

@@ -225,45 +225,30 @@ def _pretend(optim, monkeypatch):
     return seen
 
 
-class _Device0(torch.Tensor):
-    """A CPU tensor that says it is on device 0."""
-
-    @property
-    def is_cuda(self):
-        return True
-
-    def get_device(self):
-        return 0
-
-
-def _there(t):
-    return t.as_subclass(_Device0)
-
-
 def test_step_lists_are_checked(optim, monkeypatch):
     """What the step's lists have to be, with CPU tensors in place of the device's."""
     seen = _pretend(optim, monkeypatch)
-    params = [_there(torch.zeros((3, 5))), _there(torch.zeros(7, dtype=torch.bfloat16))]
-    grads = [_there(torch.zeros((3, 5))), _there(torch.zeros(7))]
-    zeros = lambda n: _there(torch.zeros(n))  # noqa: E731
-    st = optim.AdamWState(zeros(512), zeros(512), _there(torch.zeros(2, dtype=torch.int32)))
+    params = [torch.zeros((3, 5)), torch.zeros(7, dtype=torch.bfloat16)]
+    grads = [torch.zeros((3, 5)), torch.zeros(7)]
+    zeros = lambda n: torch.zeros(n)  # noqa: E731
+    st = optim.AdamWState(zeros(512), zeros(512), torch.zeros(2, dtype=torch.int32))
     optim.adamw_step(params, grads, st, lr=0.1, weight_decay=(0.5, 0.25))
     name, args = seen.pop()
     assert name == "dlrm_adamw_step" and args[0] == 2 and args[7] == 32
     for bad, match in (
             (dict(grads=grads[:1]), "grads must have 2"),
             (dict(grads=[grads[0], zeros(8)]), r"grads\[1\] must be \(7,\)"),
-            (dict(grads=[_there(torch.zeros((5, 3))), grads[1]]), r"grads\[0\] must be \(3, 5\)"),
-            (dict(grads=[_there(torch.zeros((5, 3)).T), grads[1]]), r"grads\[0\] must be contiguous"),
-            (dict(params=[params[0], _there(torch.zeros(7, dtype=torch.float16))]), r"params\[1\] must be float32"),
+            (dict(grads=[torch.zeros((5, 3)), grads[1]]), r"grads\[0\] must be \(3, 5\)"),
+            (dict(grads=[torch.zeros((5, 3)).T, grads[1]]), r"grads\[0\] must be contiguous"),
+            (dict(params=[params[0], torch.zeros(7, dtype=torch.float16)]), r"params\[1\] must be float32"),
             (dict(st=st._replace(m=zeros(256))), "state.m must have 512"),
             (dict(st=st._replace(v=zeros(768))), "state.v must have 512"),
-            (dict(st=st._replace(step=_there(torch.zeros(1, dtype=torch.int32)))), "two elements"),
+            (dict(st=st._replace(step=torch.zeros(1, dtype=torch.int32))), "two elements"),
             (dict(st=st._replace(master=zeros(22))), "state.master must have 512"),
             (dict(weight_decay=(0.1,)), "weight_decay must have 2"),
             (dict(lr=zeros(2)), "lr must have 1"),
             (dict(grad_scale=zeros(0)), "grad_scale must have 1"),
-            (dict(st=st._replace(m=_there(torch.zeros(512).to(torch.float8_e4m3fn)))), "state.v must be"),
+            (dict(st=st._replace(m=torch.zeros(512).to(torch.float8_e4m3fn))), "state.v must be"),
     ):
         kw = dict(params=params, grads=grads, st=st, lr=0.1)
         kw.update(bad)
