@@ -2,21 +2,27 @@
 // y[m][n] = act(sum_k x[m][k] w[n][k] + bias[n]).
 //
 // tcgen05.mma.kind::mxf4.block_scale: products of e2m1 codes times both blocks'
-// powers of two, K = 64 an instruction, f32 sums in TMEM. The weights take the M side
-// and the tokens the N side, as in the 8-bit layer: a lane is an output channel, and
-// the 32 lanes of a warp store 32 neighbouring channels of one token without staging.
+// powers of two, K = 64 an instruction, f32 sums in TMEM.
 //
-// Ten warps a CTA: one thread streams 128-byte K blocks (256 elements) of both
-// operands and their scale tiles into a shared-memory ring with TMA loads; one copies
-// a stage's scales into TMEM (tcgen05.cp, which the tensor cores take in order with
-// the products around it, so one set of columns is enough) and issues its four products;
-// eight warps drain a finished accumulator while the next tile's products fill the other.
-//   - CTAs of 128 channels x 64 or 128 tokens; few tiles: a cluster of S of them shares
-//     one tile, each summing a stretch of K, and the f32 parts meet through distributed
-//     shared memory in the order of the ranks.
-//   - CTA pairs (cta_group::2) of 256 channels x 256 tokens. Two accumulators of 256
-//     columns and the scales' 24 do not fit TMEM's 512, so the accumulators share 32
-//     columns: those are drained first, and the next tile's products wait for that.
+// Fourteen warps a CTA: one thread streams 128-byte K blocks (256 elements) of both
+// operands and their scale tiles into a shared-memory ring with TMA loads; four warps
+// carry a stage's scales from there into TMEM, two or four stages' ahead; one thread
+// issues a stage's four products; eight warps drain a finished accumulator while the
+// next tile's products fill the other. (tcgen05.cp brings scales to TMEM as well, but in
+// the tensor cores' own queue: a stage's six copies held up its products by 0.15 of 0.63
+// us, 8192^3 284 us instead of CARRIED.)
+//
+// Forms:
+//   - CTAs of 128 channels x 64 or 128 tokens: the weights take the M side, so an
+//     accumulator lane is a channel, few tokens make a narrow tile, and the 32 lanes of a
+//     warp store 32 neighbouring channels of a token at any pitch. Few tiles: a
+//     cluster of S CTAs shares one tile, each summing a stretch of K, and the f32 parts
+//     meet through distributed shared memory in the order of the ranks.
+//   - CTA pairs (cta_group::2) of 256 x 256. Where rows of y start on 16 bytes the
+//     tokens take the M side: a lane then has neighbouring channels of a token, lays
+//     them out in shared memory, and the copy engine writes whole lines. Two accumulators of 256 columns and
+//     the scales do not fit TMEM's 512, so the accumulators share 64 columns: those
+//     are drained first, and the next tile's products wait for that.
 //   - up to four tokens: CUDA cores, a warp for each channel (below).
 // Every wait is bounded; one that runs out sets DLRM_FLAG_TIMEOUT in the
 // optional status word, and the CTA still lets its loads land, frees its tensor
@@ -39,48 +45,59 @@ constexpr int kBK = 128;            // bytes of K per stage: one 128-byte swizzl
 constexpr int kCols = 2 * kBK;      // elements of K per stage
 constexpr int kStageTiles = kCols / 128;  // scale tiles along K per stage
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 64 + 32 * kEpiWarps;
+constexpr int kScaleWarp = 2 + kEpiWarps;  // the first of the four that carry scales
+constexpr int kThreads = 32 * (kScaleWarp + 4);
 constexpr long long kWaitLimit = 200000000LL;  // clock cycles, about 0.1 s
 constexpr int kMaxDevices = 64;                // devices whose launch set-up is cached
 
+// The operand on the M side is a (the weights, or with TOKENS_M the tokens), the other b.
 struct LinArgs {
   const float* bias;
   void* y;
   int64_t ldy;
-  int M, N, K;
+  int na, nb, K;                 // rows of a and of b
   int nkb;                       // K blocks
-  int tiles_m, tiles_n, tiles;   // token tiles, channel tiles
+  int tiles_a, tiles_b, tiles;
   int act, y_bf16;
   int32_t* status;
 };
 
 struct alignas(64) LinMaps {
-  CUtensorMap w, x, sw, sx;
+  CUtensorMap a, b, sa, sb, y;  // y: with TOKENS_M
 };
 
-// Shared memory and TMEM of a form. BN tokens a tile; a pair's CTA loads half of them, but
-// the scales of all, which each CTA's tensor cores read from its own TMEM.
-template <int BN, bool PAIR>
+// Shared memory and TMEM of a form. BN rows of b a tile; a pair's CTA loads half of them,
+// but the scales of all, which each CTA's tensor cores read from its own TMEM.
+// OUT: with room for each epilogue warp's part of y on its way out.
+constexpr int kOutBytes = 4096;  // 32 rows of 128 bytes
+template <int BN, bool PAIR, bool OUT>
 struct Ring {
-  static constexpr int kXTiles = BN > 128 ? BN / 128 : 1;  // row tiles of the tokens' scales
-  static constexpr int kW = kBM * kBK;
-  static constexpr int kX = (PAIR ? BN / 2 : BN) * kBK;
-  static constexpr int kSW = kStageTiles * kFp4Tile;
-  static constexpr int kSX = kXTiles * kStageTiles * kFp4Tile;
-  static constexpr int kStage = kW + kX + kSW + kSX;
-  // as many stages as fit in about 200 KB, at most 8
-  static constexpr int kStages = (200 * 1024 / kStage) < 8 ? (200 * 1024 / kStage) : 8;
-  static constexpr int kBars = kStages * kStage;
-  static constexpr int kTotal = kBars + (2 * kStages + 6) * 8 + 8 + 1024;  // + alignment
+  static constexpr int kBTiles = BN > 128 ? BN / 128 : 1;  // row tiles of b's scales
+  static constexpr int kA = kBM * kBK;
+  static constexpr int kB = (PAIR ? BN / 2 : BN) * kBK;
+  static constexpr int kSA = kStageTiles * kFp4Tile;
+  static constexpr int kSB = kBTiles * kStageTiles * kFp4Tile;
+  static constexpr int kStage = kA + kB + kSA + kSB;
+  // as many stages as fit in about 180 or 200 KB, at most 8
+  static constexpr int kRoom = (OUT ? 180 : 200) * 1024;
+  static constexpr int kStages = kRoom / kStage < 8 ? kRoom / kStage : 8;
+  static constexpr int kOut = kStages * kStage;
+  static constexpr int kBias = kOut + kEpiWarps * kOutBytes;  // a slice of it for each warp
+  static constexpr int kBars = OUT ? kBias + kEpiWarps * (BN / 2) * 4 : kOut;
+  // stages whose scales are in TMEM at a time
+  static constexpr int kCarried = BN > 128 ? 2 : 4;
+  static constexpr int kBarriers = 3 * kStages + kCarried + 6;
+  static constexpr int kTotal = kBars + kBarriers * 8 + 8 + 1024;  // + alignment
   static_assert(kStage % 1024 == 0, "swizzled tiles start on 1024 bytes");
+  static_assert(kStages >= kCarried, "a column set is free when its stage's place is");
   static_assert(kTotal <= 227 * 1024, "shared memory of one CTA");
   // TMEM columns: the second accumulator, the scales, and what both accumulators have
   // of each other
-  static constexpr int kLap = BN > 128 ? 32 : 0;
+  static constexpr int kLap = BN > 128 ? 64 : 0;
   static constexpr uint32_t kAcc1 = BN - kLap;
   static constexpr uint32_t kScales = kAcc1 + BN;
-  static constexpr uint32_t kScaleCols = 4 * kStageTiles * (1 + kXTiles);
-  static constexpr uint32_t kNeeded = kScales + kScaleCols;
+  static constexpr uint32_t kScaleCols = 4 * kStageTiles * (1 + kBTiles);
+  static constexpr uint32_t kNeeded = kScales + kCarried * kScaleCols;
   static constexpr uint32_t kTmem = kNeeded <= 256 ? 256 : 512;
   static_assert(kNeeded <= 512, "tensor memory of one SM");
 };
@@ -118,44 +135,36 @@ __device__ __forceinline__ void tc_mma_fp4(uint32_t d_tmem, uint64_t adesc, uint
         : "memory");
 }
 
-// A scale tile from shared memory into four columns of TMEM, the same for each warp's
-// 32 lanes (with CG = 2 in both CTAs of the pair, each from its own shared memory).
-template <int CG>
-__device__ __forceinline__ void tc_copy_scales(uint32_t tmem, uint64_t desc) {
-  if constexpr (CG == 2)
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
-                 : "memory");
-  else
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
-                 : "memory");
+// The same one of a whole warp's lanes at every call.
+__device__ __forceinline__ bool elected() {
+  uint32_t mine;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(mine));
+  return mine != 0;
 }
 
-// Shared-memory descriptor of a scale tile: 32 rows of 16 bytes without swizzle, groups of 8
-// rows 128 bytes apart (fields as in sdesc_k_sw128; layout type 0).
-__device__ __forceinline__ uint64_t sdesc_scales(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(1) << 16;
-  d |= static_cast<uint64_t>(128 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  return d;
+// N 32-bit columns of the warp's 32 TMEM lanes, from each lane's registers.
+__device__ __forceinline__ void tmem_st_8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
+                   taddr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+               "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// The box of a 3-D tensor map at (x, y, z); as tma_load_2d and tma_load_2d_pair.
+// The box of a 3-D tensor map at (x, y, z), as tma_load_2d.
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar,
                                             int x, int y, int z) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map,
-                                                 uint32_t bar_cluster, int x, int y, int z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
 
@@ -184,30 +193,59 @@ __device__ __forceinline__ void put_at(Out* p, float sum, float bias) {
     *p = __float2bfloat16_rn(v);
 }
 
-// An output channel.
-struct Channel {
-  float b;
-  bool live;
-};
-
-// 32 tokens m0 .. of a lane's channel n, from the registers v.
+// b's rows b0 .. b0 + 31 (tokens) of a lane's row of a (a channel), from the registers v.
 template <int ACT, class Out>
-__device__ __forceinline__ void put_32(const LinArgs& a, const Channel& ch, int n, int m0,
-                                       const float (&v)[32]) {
-  if (!ch.live) return;
-  Out* p = static_cast<Out*>(a.y) + static_cast<int64_t>(m0) * a.ldy + n;
-  const int left = a.M - m0;
+__device__ __forceinline__ void put_tokens(const LinArgs& a, int row, float bias, int b0,
+                                           const float* v) {
+  if (row >= a.na) return;
+  Out* p = static_cast<Out*>(a.y) + static_cast<int64_t>(b0) * a.ldy + row;
+  const int left = a.nb - b0;
   if (left >= 32) {
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-      put_at<ACT>(p, v[i], ch.b);
+      put_at<ACT>(p, v[i], bias);
       p += a.ldy;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-      if (i < left) put_at<ACT>(p, v[i], ch.b);
+      if (i < left) put_at<ACT>(p, v[i], bias);
       p += a.ldy;
+    }
+  }
+}
+
+// b's rows b0 .. b0 + 63 (channels) of 32 rows of a from row0 on (tokens), one a lane: laid
+// out in shared memory as the map's 128-byte swizzle has it, and from there to y by the
+// copy engine, which leaves out what is past y's end. Rows of y start on 16 bytes. bias: of
+// these channels, in shared memory.
+template <int ACT, class Out>
+__device__ __forceinline__ void put_channels(const LinArgs& a, const CUtensorMap* y, uint8_t* out,
+                                             int row0, int b0, int lane, const float* bias,
+                                             float* v) {
+  constexpr int kPiece = 16 / sizeof(Out), kAtOnce = 8 * kPiece;  // columns of 16 and 128 bytes
+  // all of the bias before anything is stored, which a load could not pass
+#pragma unroll
+  for (int i = 0; i < 64; i += 4) {
+    const float4 f = *reinterpret_cast<const float4*>(bias + i);
+    v[i] = activate<ACT>(__fadd_rn(v[i], f.x));
+    v[i + 1] = activate<ACT>(__fadd_rn(v[i + 1], f.y));
+    v[i + 2] = activate<ACT>(__fadd_rn(v[i + 2], f.z));
+    v[i + 3] = activate<ACT>(__fadd_rn(v[i + 3], f.w));
+  }
+#pragma unroll
+  for (int c = 0; c < 64; c += kAtOnce) {
+    if (lane == 0) bulk_wait_read_all();  // the last ones have been read
+    __syncwarp();
+#pragma unroll
+    for (int p = 0; p < 8; ++p)
+      store_f32<Out, kPiece>(reinterpret_cast<Out*>(out + lane * 128 + ((p ^ (lane & 7)) << 4)),
+                             *reinterpret_cast<const float(*)[kPiece]>(v + c + p * kPiece));
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && row0 < a.na && b0 + c < a.nb) {
+      tma_store_2d(y, out, b0 + c, row0);
+      bulk_commit();
     }
   }
 }
@@ -232,14 +270,26 @@ __device__ __forceinline__ void by_kind(const LinArgs& a, F f) {
   }
 }
 
-struct PutCall {
+struct PutTokens {
   const LinArgs& a;
-  const Channel& ch;
-  int n, m0;
-  const float (&v)[32];
+  int row, b0;
+  float bias;
+  const float* v;
   template <int ACT, class Out>
   __device__ __forceinline__ void run() const {
-    put_32<ACT, Out>(a, ch, n, m0, v);
+    put_tokens<ACT, Out>(a, row, bias, b0, v);
+  }
+};
+struct PutChannels {
+  const LinArgs& a;
+  const CUtensorMap* y;
+  uint8_t* out;
+  int row0, b0, lane;
+  const float* bias;
+  float* v;
+  template <int ACT, class Out>
+  __device__ __forceinline__ void run() const {
+    put_channels<ACT, Out>(a, y, out, row0, b0, lane, bias, v);
   }
 };
 
@@ -249,15 +299,15 @@ struct PutCall {
 template <int S>
 struct JoinCall {
   const LinArgs& a;
-  int n0, m0, c0, c1, ew, lane;
+  int a0, b0, c0, c1, ew, lane;
   uint32_t smem;
   template <int ACT, class Out>
   __device__ __forceinline__ void run() const {
     constexpr int kAtOnce = 8 / S;  // columns
-    const int n = n0 + lane * 4;
-    float b[4];
+    const int n = a0 + lane * 4;
+    float bias[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) b[e] = a.bias != nullptr && n + e < a.N ? a.bias[n + e] : 0.f;
+    for (int e = 0; e < 4; ++e) bias[e] = a.bias != nullptr && n + e < a.na ? a.bias[n + e] : 0.f;
     for (int cb = c0 + ew * kAtOnce; cb < c1; cb += kEpiWarps * kAtOnce) {
       float4 v[kAtOnce][S];
 #pragma unroll
@@ -265,54 +315,60 @@ struct JoinCall {
 #pragma unroll
         for (int k = 0; k < S; ++k) {
           v[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (cb + i < c1 && m0 + cb + i < a.M)
+          if (cb + i < c1 && b0 + cb + i < a.nb)
             v[i][k] = load_cluster_v4(map_to_cta(smem + ((cb + i) * kBM + lane * 4) * 4, k));
         }
 #pragma unroll
       for (int i = 0; i < kAtOnce; ++i) {
-        if (cb + i >= c1 || m0 + cb + i >= a.M) break;
+        if (cb + i >= c1 || b0 + cb + i >= a.nb) break;
         float4 t = v[i][0];
 #pragma unroll
         for (int k = 1; k < S; ++k)
           t.x += v[i][k].x, t.y += v[i][k].y, t.z += v[i][k].z, t.w += v[i][k].w;
         const float sums[4] = {t.x, t.y, t.z, t.w};
-        Out* p = static_cast<Out*>(a.y) + static_cast<int64_t>(m0 + cb + i) * a.ldy + n;
+        Out* p = static_cast<Out*>(a.y) + static_cast<int64_t>(b0 + cb + i) * a.ldy + n;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          if (n + e < a.N) put_at<ACT>(p + e, sums[e], b[e]);
+          if (n + e < a.na) put_at<ACT>(p + e, sums[e], bias[e]);
       }
     }
   }
 };
 
-// Tile t -> (token tile, channel tile): bands of 8 token tiles, so that the CTAs
-// at work at one time read few different rows of either operand.
-__device__ __forceinline__ void tile_at(const LinArgs& a, int t, int& tm, int& tn) {
+// Tile t -> (tile of a, tile of b): bands of 8 tiles of b, so that the CTAs at work at one
+// time read few different rows of either operand.
+__device__ __forceinline__ void tile_at(const LinArgs& a, int t, int& ta, int& tb) {
   constexpr int kBand = 8;
-  const int per_band = kBand * a.tiles_n;
+  const int per_band = kBand * a.tiles_a;
   const int band = t / per_band, in = t % per_band;
-  const int height = min(kBand, a.tiles_m - band * kBand);
-  tm = band * kBand + in % height;
-  tn = in / height;
+  const int height = min(kBand, a.tiles_b - band * kBand);
+  tb = band * kBand + in % height;
+  ta = in / height;
 }
 
 // S > 1: the S CTAs of a cluster share one tile (and there is one tile a cluster).
-template <int BN, bool PAIR, int S>
+template <int BN, bool PAIR, int S, bool TOKENS_M>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_fp4_kernel(const __grid_constant__ LinMaps maps, const __grid_constant__ LinArgs args) {
   constexpr bool SPLIT = S > 1;
-  static_assert(!(PAIR && SPLIT), "a pair shares a tile's channels, not its K");
-  using R = Ring<BN, PAIR>;
+  static_assert(!(PAIR && SPLIT), "a pair shares a tile's rows of a, not its K");
+  static_assert(!(TOKENS_M && SPLIT), "parts are joined channel by channel");
+  using R = Ring<BN, PAIR, TOKENS_M>;
   constexpr int CG = PAIR ? 2 : 1;
-  constexpr int kUnitN = CG * kBM;      // channels of a unit's tile
-  constexpr int kWarpCols = BN / 2;     // columns an epilogue warp drains
-  static_assert(kWarpCols % 32 == 0, "whole TMEM loads");
+  constexpr int kUnitA = CG * kBM;                          // rows of a in a unit's tile
+  constexpr int kWarpCols = BN / 2;                         // columns an epilogue warp drains
+  constexpr int kAtOnce = kWarpCols < 64 ? kWarpCols : 64;  // of them at a time
+  static_assert(kAtOnce % 32 == 0, "whole TMEM loads");
+  static_assert(R::kLap == 0 || R::kLap == kAtOnce, "the shared columns are one warp's step");
+  static_assert(!TOKENS_M || kAtOnce == 64, "whole lines of y");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + R::kBars);
-  uint64_t* empty = full + R::kStages;
-  uint64_t* acc_full = empty + R::kStages;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + R::kBars);  // codes are there
+  uint64_t* scales = full + R::kStages;                           // this CTA's scale tiles are
+  uint64_t* empty = scales + R::kStages;
+  uint64_t* carried = empty + R::kStages;                         // scales are in TMEM
+  uint64_t* acc_full = carried + R::kCarried;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* mma_done = acc_empty + 2;
   uint64_t* lap_empty = mma_done + 1;
@@ -334,8 +390,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < R::kStages; ++s) {
       mbar_init(&full[s], 1);
+      mbar_init(&scales[s], 1);
       mbar_init(&empty[s], 1);
     }
+    for (int s = 0; s < R::kCarried; ++s) mbar_init(&carried[s], CG * 4);
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
       mbar_init(&acc_empty[b], CG * kEpiWarps);
@@ -357,15 +415,27 @@ __global__ void __launch_bounds__(kThreads, 1)
   // read-only path may be moved in front of it.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   bool timed_out = false;
+  // a whole warp's arrival, for reads or writes of tensor memory that the issuer of the
+  // products (a pair's first CTA) waits for
+  auto arrive = [&](uint64_t* bar) {
+    tc_fence_before_sync();
+    __syncwarp();
+    if (lane == 0) {
+      if constexpr (PAIR)
+        mbar_arrive_remote(map_to_cta(smem_u32(bar), 0));
+      else
+        mbar_arrive(bar);
+    }
+  };
 
   if (warp == 0) {
     if (lane == 0) {
       int g = 0;
       for (int t = unit0; t < args.tiles && !timed_out; t += unit_step) {
-        int tm, tn;
-        tile_at(args, t, tm, tn);
-        const int n0 = tn * kUnitN + (PAIR ? static_cast<int>(rank) * kBM : 0);
-        const int m0 = tm * BN + (PAIR ? static_cast<int>(rank) * (BN / 2) : 0);
+        int ta, tb;
+        tile_at(args, t, ta, tb);
+        const int a0 = ta * kUnitA + (PAIR ? static_cast<int>(rank) * kBM : 0);
+        const int b0 = tb * BN + (PAIR ? static_cast<int>(rank) * (BN / 2) : 0);
         for (int kb = kb_begin; kb < kb_end; ++kb, ++g) {
           const int s = g % R::kStages;
           if (g >= R::kStages &&
@@ -373,120 +443,159 @@ __global__ void __launch_bounds__(kThreads, 1)
             timed_out = true;
             break;
           }
-          uint8_t* sw = smem + s * R::kStage;
-          uint8_t* sx = sw + R::kW;
-          uint8_t* ssw = sx + R::kX;
-          uint8_t* ssx = ssw + R::kSW;
+          uint8_t* sa = smem + s * R::kStage;
+          uint8_t* sb = sa + R::kA;
+          uint8_t* ssa = sb + R::kB;
+          uint8_t* ssb = ssa + R::kSA;
+          // a CTA's scale tiles are counted on its own barrier
+          mbar_arrive_expect_tx(&scales[s], R::kSA + R::kSB);
+          tma_load_3d(ssa, &maps.sa, &scales[s], 0, kb * kStageTiles, a0 / 128);
+          tma_load_3d(ssb, &maps.sb, &scales[s], 0, kb * kStageTiles, tb * BN / 128);
           if constexpr (PAIR) {
-            // both CTAs' bytes are counted on the issuer's barrier, which only
-            // its producer arms
-            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * R::kStage);
+            // both CTAs' codes are counted on the issuer's barrier, which only its
+            // producer arms
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * (R::kA + R::kB));
             const uint32_t fb = map_to_cta(smem_u32(&full[s]), 0);
-            tma_load_2d_pair(sw, &maps.w, fb, kb * kBK, n0);
-            tma_load_2d_pair(sx, &maps.x, fb, kb * kBK, m0);
-            tma_load_3d_pair(ssw, &maps.sw, fb, 0, kb * kStageTiles, n0 / 128);
-            tma_load_3d_pair(ssx, &maps.sx, fb, 0, kb * kStageTiles, tm * BN / 128);
+            tma_load_2d_pair(sa, &maps.a, fb, kb * kBK, a0);
+            tma_load_2d_pair(sb, &maps.b, fb, kb * kBK, b0);
           } else {
-            mbar_arrive_expect_tx(&full[s], R::kStage);
-            tma_load_2d(sw, &maps.w, &full[s], kb * kBK, n0);
-            tma_load_2d(sx, &maps.x, &full[s], kb * kBK, m0);
-            tma_load_3d(ssw, &maps.sw, &full[s], 0, kb * kStageTiles, n0 / 128);
-            tma_load_3d(ssx, &maps.sx, &full[s], 0, kb * kStageTiles, m0 / 128);
+            mbar_arrive_expect_tx(&full[s], R::kA + R::kB);
+            tma_load_2d(sa, &maps.a, &full[s], kb * kBK, a0);
+            tma_load_2d(sb, &maps.b, &full[s], kb * kBK, b0);
           }
         }
       }
       // no load is in flight once this CTA leaves, whoever gave up
+      land_loads<R::kStages, false>(
+          true, timed_out, g,
+          [&](int s, uint32_t parity) { (void)mbar_wait_bounded(&scales[s], parity, kWaitLimit); },
+          [](int) {}, [](int) {}, [] { return -1; });
       land_loads<R::kStages, PAIR>(
           !PAIR || rank == 0, timed_out, g,
           [&](int s, uint32_t parity) { (void)mbar_wait_bounded(&full[s], parity, kWaitLimit); },
-          [&](int s) { mbar_arrive_expect_tx(&full[s], R::kStage); },
+          [&](int s) { mbar_arrive_expect_tx(&full[s], R::kA + R::kB); },
           [&](int steps) { tell_steps(other_steps, steps); },
           [&] { return told_steps(other_steps, (R::kStages + 2) * kWaitLimit); });
     }
   } else if (warp == 1) {
-    if (lane == 0 && (!PAIR || rank == 0)) {
-      const uint32_t sa = tmem + R::kScales;
-      const uint32_t sb = sa + 4 * kStageTiles;
-      int g = 0, j = 0;
+    // The whole warp walks the stages and one elected lane issues: what the products' operands are
+    // made of is then the same for the warp and stays in its uniform registers (by one
+    // lane alone a stage took WAS cycles, now IS).
+    if (!PAIR || rank == 0) {
+      const uint64_t a_desc = sdesc_k_sw128(smem_u32(smem));
+      const uint64_t b_desc = sdesc_k_sw128(smem_u32(smem) + R::kA);
+      int g = 0, j = 0, s = 0, c = 0;
+      uint32_t s_turn = 0, c_turn = 0;  // parities of the ring's and the column sets' turns
       for (int t = unit0; t < args.tiles && !timed_out; t += unit_step, ++j) {
         const int b = j & 1;
-        if (j >= 2 && !mbar_wait_bounded(&acc_empty[b], ((j >> 1) - 1) & 1, kWaitLimit)) {
+        bool ok = j < 2 || mbar_wait_bounded(&acc_empty[b], ((j >> 1) - 1) & 1, kWaitLimit);
+        if (R::kLap != 0 && ok && j >= 1) ok = mbar_wait_bounded(lap_empty, (j - 1) & 1, kWaitLimit);
+        if (!__all_sync(kFull, ok)) {
           timed_out = true;
           break;
         }
-        if (R::kLap != 0 && j >= 1 && !mbar_wait_bounded(lap_empty, (j - 1) & 1, kWaitLimit)) {
-          timed_out = true;
-          break;
-        }
-        tc_fence_after_sync();
         const uint32_t acc = tmem + (b != 0 ? R::kAcc1 : 0u);
-        // tokens from the middle of a scale tile on: 32 rows of it are a column
-        int tm, tn;
-        tile_at(args, t, tm, tn);
-        const uint32_t sb_t = sb + static_cast<uint32_t>(tm * BN % 128 / 32);
+        // rows of b from the middle of a scale tile on: 32 rows of it are a column
+        int ta, tb;
+        tile_at(args, t, ta, tb);
+        const uint32_t b_col = static_cast<uint32_t>(tb * BN % 128 / 32);
         for (int kb = kb_begin; kb < kb_end; ++kb, ++g) {
-          const int s = g % R::kStages;
-          if (!mbar_wait_bounded(&full[s], (g / R::kStages) & 1, kWaitLimit)) {
+          ok = mbar_wait_bounded(&full[s], s_turn, kWaitLimit) &&
+               mbar_wait_bounded(&carried[c], c_turn, kWaitLimit);
+          if (!__all_sync(kFull, ok)) {
             timed_out = true;
             break;
           }
           tc_fence_after_sync();
-          const uint32_t sw = smem_u32(smem + s * R::kStage);
-          const uint32_t sx = sw + R::kW;
-          const uint32_t ssw = sx + R::kX;
-          const uint32_t ssx = ssw + R::kSW;
-#pragma unroll
-          for (int i = 0; i < kStageTiles; ++i) {
-            tc_copy_scales<CG>(sa + 4 * i, sdesc_scales(ssw + i * kFp4Tile));
-#pragma unroll
-            for (int r = 0; r < R::kXTiles; ++r)
-              tc_copy_scales<CG>(sb + 4 * (i * R::kXTiles + r),
-                                 sdesc_scales(ssx + (r * kStageTiles + i) * kFp4Tile));
-          }
+          const uint64_t ad = a_desc + static_cast<uint32_t>(s * (R::kStage >> 4));
+          const uint64_t bd = b_desc + static_cast<uint32_t>(s * (R::kStage >> 4));
+          const uint32_t ca = tmem + R::kScales + static_cast<uint32_t>(c) * R::kScaleCols;
+          const uint32_t cb = ca + 4 * kStageTiles + b_col;
           // products past K would add zeros
           const int steps = min(4, (args.K - kb * kCols + 63) / 64);
+          if (elected()) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k < steps)
-              tc_mma_fp4<CG>(acc, sdesc_k_sw128(sw + k * 32), sdesc_k_sw128(sx + k * 32),
-                             idesc_mxf4(kUnitN, BN, 2 * (k & 1)), sa + 4 * (k >> 1),
-                             sb_t + 4 * (k >> 1) * R::kXTiles,
-                             (kb > kb_begin || k > 0) ? 1u : 0u);
-          if constexpr (PAIR)
-            tc_commit_pair_both(&empty[s]);
-          else
-            tc_commit<CG>(&empty[s]);
+            for (int k = 0; k < 4; ++k)
+              if (k < steps)
+                tc_mma_fp4<CG>(acc, ad + 2 * k, bd + 2 * k, idesc_mxf4(kUnitA, BN, 2 * (k & 1)),
+                               ca + 4 * (k >> 1), cb + 4 * (k >> 1) * R::kBTiles,
+                               (kb > kb_begin || k > 0) ? 1u : 0u);
+            if constexpr (PAIR)
+              tc_commit_pair_both(&empty[s]);
+            else
+              tc_commit<CG>(&empty[s]);
+          }
+          __syncwarp();
+          if (++s == R::kStages) s = 0, s_turn ^= 1;
+          if (++c == R::kCarried) c = 0, c_turn ^= 1;
         }
-        if constexpr (PAIR)
-          tc_commit_pair_both(&acc_full[b]);
-        else
-          tc_commit<CG>(&acc_full[b]);
+        if (elected()) {
+          if constexpr (PAIR)
+            tc_commit_pair_both(&acc_full[b]);
+          else
+            tc_commit<CG>(&acc_full[b]);
+        }
+        __syncwarp();
       }
       // every MMA has completed before this CTA or its peer can leave
-      tc_commit<CG>(mma_done);
+      if (elected()) tc_commit<CG>(mma_done);
+      __syncwarp();
       if (!mbar_wait_bounded(mma_done, 0, kWaitLimit)) timed_out = true;
+    }
+  } else if (warp >= kScaleWarp) {
+    // A stage's scale tiles: lane i of every warp takes the 16 bytes of rows i, i + 32, i +
+    // 64 and i + 96, four columns of its TMEM lane. A column set is free once the products of
+    // the stage that had it before are done, which is when its place in the ring is.
+    const uint32_t quarter = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    int g = 0;
+    for (int t = unit0; t < args.tiles && !timed_out; t += unit_step) {
+      for (int kb = kb_begin; kb < kb_end; ++kb, ++g) {
+        const int s = g % R::kStages, c = g % R::kCarried, before = g - R::kCarried;
+        bool ok = mbar_wait_bounded(&scales[s], (g / R::kStages) & 1, kWaitLimit);
+        if (ok && before >= 0)
+          ok = mbar_wait_bounded(&empty[before % R::kStages], (before / R::kStages) & 1, kWaitLimit);
+        if (!__all_sync(kFull, ok)) {
+          timed_out = true;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint8_t* tile = smem + s * R::kStage + R::kA + R::kB + lane * 16;
+        const uint32_t to = tmem + quarter + R::kScales + static_cast<uint32_t>(c) * R::kScaleCols;
+        uint32_t r[R::kScaleCols];
+#pragma unroll
+        for (int i = 0; i < kStageTiles * (1 + R::kBTiles); ++i) {
+          // a's tiles along K, then b's: along K, of each its row tiles
+          const int b = i - kStageTiles;
+          const int at = i < kStageTiles ? i : kStageTiles + b % R::kBTiles * kStageTiles + b / R::kBTiles;
+          const uint4 v = *reinterpret_cast<const uint4*>(tile + at * kFp4Tile);
+          r[4 * i] = v.x, r[4 * i + 1] = v.y, r[4 * i + 2] = v.z, r[4 * i + 3] = v.w;
+        }
+#pragma unroll
+        for (int i = 0; i < static_cast<int>(R::kScaleCols); i += 8) tmem_st_8(to + i, r + i);
+        tmem_st_wait();
+        arrive(&carried[c]);
+      }
     }
   } else {
     const int ew = warp - 2, quarter = warp & 3, half = ew >> 2;
-    auto arrive = [&](uint64_t* bar) {
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (PAIR)
-          mbar_arrive_remote(map_to_cta(smem_u32(bar), 0));
-        else
-          mbar_arrive(bar);
-      }
-    };
     int j = 0;
     for (int t = unit0; t < args.tiles; t += unit_step, ++j) {
       const int b = j & 1;
-      int tm, tn;
-      tile_at(args, t, tm, tn);
-      const int m0 = tm * BN;
-      const int n = tn * kUnitN + (PAIR ? static_cast<int>(rank) * kBM : 0) + quarter * 32 + lane;
-      Channel ch = {0.f, n < args.N};
-      if (!SPLIT && ch.live && args.bias != nullptr) ch.b = args.bias[n];
+      int ta, tb;
+      tile_at(args, t, ta, tb);
+      const int b0 = tb * BN;
+      const int row = ta * kUnitA + (PAIR ? static_cast<int>(rank) * kBM : 0) + quarter * 32 + lane;
+      float bias = 0.f;
+      if (!SPLIT && !TOKENS_M && row < args.na && args.bias != nullptr) bias = args.bias[row];
+      float* slice = reinterpret_cast<float*>(smem + R::kBias) + ew * kWarpCols;
+      if constexpr (TOKENS_M) {
+        __syncwarp();  // the slice's readers of the tile before are done
+        for (int c = lane; c < kWarpCols; c += 32) {
+          const int n = b0 + half * kWarpCols + c;
+          slice[c] = args.bias != nullptr && n < args.nb ? args.bias[n] : 0.f;
+        }
+        __syncwarp();
+      }
       if (!__all_sync(kFull, mbar_wait_bounded(&acc_full[b], (j >> 1) & 1, kWaitLimit))) {
         timed_out = true;
         break;
@@ -495,35 +604,46 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t tq = tmem + (b != 0 ? R::kAcc1 : 0u) + (static_cast<uint32_t>(quarter * 32) << 16);
       // The columns that the next tile's accumulator has too come first: the last of the
       // lower accumulator, the first of the upper one.
-      constexpr int kChunks = kWarpCols / 32;
+      constexpr int kSteps = kWarpCols / kAtOnce;
       const bool lap = R::kLap != 0 && half == 1 - b;
-      const int first = R::kLap != 0 && lap && b == 0 ? kChunks - 1 : 0;
-      for (int i = 0; i < kChunks; ++i) {
-        const int c = half * kWarpCols + (first + i) % kChunks * 32;
-        float v[32];
-        tmem_ld_32x32b_x32(tq + c, v);
-        if (lap && i == 0) arrive(lap_empty);
-        if (i == kChunks - 1) arrive(&acc_empty[b]);
-        if constexpr (SPLIT) {
-          // all products are done: the ring is free for this CTA's part
-          float* part = reinterpret_cast<float*>(smem);
+      const int first = lap && b == 0 ? kSteps - 1 : 0;
+      for (int i = 0; i < kSteps; ++i) {
+        const int c = half * kWarpCols + (first + i) % kSteps * kAtOnce;
+        float v[kAtOnce];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) part[(c + e) * kBM + quarter * 32 + lane] = v[e];
-        } else if (m0 + c < args.M) {
-          by_kind(args, PutCall{args, ch, n, m0 + c, v});
+        for (int h = 0; h < kAtOnce; h += 32)
+          tmem_ld_32x32b_x32(tq + c + h, *reinterpret_cast<float(*)[32]>(v + h));
+        if (lap && i == 0) arrive(lap_empty);
+        if (i == kSteps - 1) arrive(&acc_empty[b]);
+if constexpr (TOKENS_M) {
+          by_kind(args, PutChannels{args, &maps.y, smem + R::kOut + ew * kOutBytes, row - lane,
+                                    b0 + c, lane, slice + (c - half * kWarpCols), v});
+        } else {
+#pragma unroll
+          for (int h = 0; h < kAtOnce; h += 32) {
+            if constexpr (SPLIT) {
+              // all products are done: the ring is free for this CTA's part
+              float* part = reinterpret_cast<float*>(smem);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) part[(c + h + e) * kBM + quarter * 32 + lane] = v[h + e];
+            } else if (b0 + c + h < args.nb) {
+              by_kind(args, PutTokens{args, row, b0 + c + h, bias, v + h});
+            }
+          }
         }
         __syncwarp();  // the next load takes the whole warp
       }
     }
+    if (TOKENS_M && lane == 0) bulk_wait_all();
   }
   if (timed_out && args.status != nullptr) atomicOr(args.status, DLRM_FLAG_TIMEOUT);
   if constexpr (SPLIT) {
     cluster_sync();  // every CTA's part is in its shared memory
-    if (warp >= 2) {
-      int tm, tn;
-      tile_at(args, unit0, tm, tn);
+    if (warp >= 2 && warp < kScaleWarp) {
+      int ta, tb;
+      tile_at(args, unit0, ta, tb);
       const int c0 = BN * static_cast<int>(rank) / S, c1 = BN * static_cast<int>(rank + 1) / S;
-      by_kind(args, JoinCall<S>{args, tn * kBM, tm * BN, c0, c1, warp - 2, lane, smem_u32(smem)});
+      by_kind(args, JoinCall<S>{args, ta * kBM, tb * BN, c0, c1, warp - 2, lane, smem_u32(smem)});
     }
   }
   tc_fence_before_sync();
@@ -545,7 +665,7 @@ constexpr int kFewTokens = 4;
 constexpr int kPiece = 128;  // blocks of K that a CTA takes at a time: 4 a lane
 
 struct VecArgs {
-  LinArgs lin;
+  LinArgs lin;      // a: the weights, b: the tokens
   const uint8_t* x;
   const uint8_t* x_scale;
   const uint8_t* w;
@@ -593,7 +713,7 @@ struct FewCall {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
       if (lane == m) mine = sum[m];
-    if (lane < MT && lane < a.lin.M)
+    if (lane < MT && lane < a.lin.nb)
       put_at<ACT>(static_cast<Out*>(a.lin.y) + lane * a.lin.ldy + n, mine,
                   a.lin.bias != nullptr ? a.lin.bias[n] : 0.f);
   }
@@ -609,7 +729,7 @@ __global__ void __launch_bounds__(kVecThreads) linear_few_kernel(const VecArgs a
   const int tile = blockIdx.x / 16;
   const int r = blockIdx.x % 16 * 2 + (warp & 1) + 32 * (warp >> 1);
   const int n = tile * 128 + r;
-  const bool live = n < a.lin.N;
+  const bool live = n < a.lin.na;
   const uint8_t* w = a.w + static_cast<int64_t>(live ? n : 0) * a.ldw;
   const uint8_t* ws = a.w_scale + fp4_scale_at(a.block_tiles, live ? n : 0, 0);
   float acc[MT] = {};
@@ -632,7 +752,7 @@ __global__ void __launch_bounds__(kVecThreads) linear_few_kernel(const VecArgs a
       const int m = i / kPiece, p = i % kPiece, b = b0 + p;
       uint4 c = make_uint4(0, 0, 0, 0);
       uint32_t e = 0;
-      if (m < a.lin.M && b < a.blocks) {
+      if (m < a.lin.nb && b < a.blocks) {
         c = load_codes(a.x + m * a.ldx, b * 16, a.bytes);
         e = a.x_scale[fp4_scale_at(a.block_tiles, m, b)];
       }
@@ -678,7 +798,7 @@ struct Operands {
   const uint8_t* x_scale;
   const uint8_t* w;
   const uint8_t* w_scale;
-  int64_t ldx, ldw, K;
+  int64_t ldx, ldw, M, N, K;
 };
 
 // 2-D map of codes {bytes, rows} with the given pitch, box {128, box_rows}, 128-byte
@@ -716,19 +836,44 @@ cudaError_t encode_scales(CUtensorMap* map, const uint8_t* base, int64_t K, int6
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int BN, bool PAIR, int S>
+// 2-D map of y {N, M}, box {128 bytes, 32 rows}, 128-byte swizzle: a warp's part of it.
+cudaError_t encode_out(CUtensorMap* map, const LinArgs& a, int64_t M, int64_t N) {
+  const EncodeTiledFn enc = encode_tiled();
+  if (enc == nullptr) return cudaErrorNotSupported;
+  const cuuint32_t size = a.y_bf16 ? 2 : 4;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(M)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(a.ldy) * size};
+  const cuuint32_t box[2] = {128 / size, 32};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = enc(map, a.y_bf16 ? CU_TENSOR_MAP_DATA_TYPE_UINT16 : CU_TENSOR_MAP_DATA_TYPE_UINT32,
+                         2, a.y, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int BN, bool PAIR, int S, bool TOKENS_M>
 cudaError_t run_linear(const Operands& op, LinArgs args, int sms, cudaStream_t stream) {
   constexpr bool SPLIT = S > 1;
-  using R = Ring<BN, PAIR>;
-  auto* fn = &linear_fp4_kernel<BN, PAIR, S>;
+  using R = Ring<BN, PAIR, TOKENS_M>;
+  auto* fn = &linear_fp4_kernel<BN, PAIR, S, TOKENS_M>;
   constexpr int smem = R::kTotal;
-  constexpr int kUnitN = (PAIR ? 2 : 1) * kBM;
+  constexpr int kUnitA = (PAIR ? 2 : 1) * kBM;
+  // args come with the weights as a
+  if (TOKENS_M) std::swap(args.na, args.nb);
   LinMaps maps;
-  cudaError_t e = encode_codes(&maps.w, op.w, op.K, args.N, op.ldw, kBM);
+  cudaError_t e = encode_codes(TOKENS_M ? &maps.b : &maps.a, op.w, op.K, op.N, op.ldw,
+                               TOKENS_M ? (PAIR ? BN / 2 : BN) : kBM);
   if (e == cudaSuccess)
-    e = encode_codes(&maps.x, op.x, op.K, args.M, op.ldx, PAIR ? BN / 2 : BN);
-  if (e == cudaSuccess) e = encode_scales(&maps.sw, op.w_scale, op.K, args.N, 1);
-  if (e == cudaSuccess) e = encode_scales(&maps.sx, op.x_scale, op.K, args.M, R::kXTiles);
+    e = encode_codes(TOKENS_M ? &maps.a : &maps.b, op.x, op.K, op.M, op.ldx,
+                     TOKENS_M ? kBM : (PAIR ? BN / 2 : BN));
+  if (e == cudaSuccess)
+    e = encode_scales(TOKENS_M ? &maps.sb : &maps.sa, op.w_scale, op.K, op.N,
+                      TOKENS_M ? R::kBTiles : 1);
+  if (e == cudaSuccess)
+    e = encode_scales(TOKENS_M ? &maps.sa : &maps.sb, op.x_scale, op.K, op.M,
+                      TOKENS_M ? 1 : R::kBTiles);
+  if (TOKENS_M && e == cudaSuccess) e = encode_out(&maps.y, args, op.M, op.N);
   if (e != cudaSuccess) return e;
   // Per device, the instance's shared-memory size is set and (pairs) the
   // resident cluster count asked for once: 0 = not yet, else that count + 1.
@@ -742,10 +887,10 @@ cudaError_t run_linear(const Operands& op, LinArgs args, int sms, cudaStream_t s
                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  args.tiles_m = (args.M + BN - 1) / BN;
-  args.tiles_n = (args.N + kUnitN - 1) / kUnitN;
-  const int64_t tiles = static_cast<int64_t>(args.tiles_m) * args.tiles_n;
-  if (tiles > INT_MAX || static_cast<int64_t>(args.tiles_n) * 8 > INT_MAX)
+  args.tiles_b = (args.nb + BN - 1) / BN;
+  args.tiles_a = (args.na + kUnitA - 1) / kUnitA;
+  const int64_t tiles = static_cast<int64_t>(args.tiles_a) * args.tiles_b;
+  if (tiles > INT_MAX || static_cast<int64_t>(args.tiles_a) * 8 > INT_MAX)
     return cudaErrorInvalidValue;
   args.tiles = static_cast<int>(tiles);
   cudaLaunchConfig_t cfg = {};
@@ -787,7 +932,7 @@ cudaError_t run_few(const Operands& op, const LinArgs& args, cudaStream_t stream
   const VecArgs a = {args, op.x, op.x_scale, op.w, op.w_scale, op.ldx, op.ldw,
                      fp4_block_tiles(op.K), static_cast<int>((op.K + 31) / 32),
                      static_cast<int>((op.K + 1) / 2)};
-  return launch(&linear_few_kernel<MT>, dim3(static_cast<unsigned>((args.N + 127) / 128 * 16)),
+  return launch(&linear_few_kernel<MT>, dim3(static_cast<unsigned>((args.na + 127) / 128 * 16)),
                 kVecThreads, 0, true, stream, a);
 }
 
@@ -801,29 +946,28 @@ struct Form {
   cudaError_t (*run)(const Operands&, LinArgs, int, cudaStream_t);
 };
 const Form kForms[] = {
-    {64, false, 1, 0.290, 0.7, 0.0, 0.0, run_linear<64, false, 1>},
-    {64, false, 2, 0.290, 0.7, 0.0, 1.7, run_linear<64, false, 2>},
-    {64, false, 4, 0.290, 0.7, 0.0, 2.4, run_linear<64, false, 4>},
-    {128, false, 1, 0.280, 1.2, 2.0, 0.0, run_linear<128, false, 1>},
-    {128, false, 2, 0.280, 1.2, 2.0, 2.7, run_linear<128, false, 2>},
-    {128, false, 4, 0.280, 1.2, 2.0, 3.0, run_linear<128, false, 4>},
-    {256, true, 1, 0.310, 2.2, 3.7, 0.0, run_linear<256, true, 1>},
+    {64, false, 1, 0.290, 0.7, 0.0, 0.0, run_linear<64, false, 1, false>},
+    {64, false, 2, 0.290, 0.7, 0.0, 1.7, run_linear<64, false, 2, false>},
+    {64, false, 4, 0.290, 0.7, 0.0, 2.4, run_linear<64, false, 4, false>},
+    {128, false, 1, 0.280, 1.2, 2.0, 0.0, run_linear<128, false, 1, false>},
+    {128, false, 2, 0.280, 1.2, 2.0, 2.7, run_linear<128, false, 2, false>},
+    {128, false, 4, 0.280, 1.2, 2.0, 3.0, run_linear<128, false, 4, false>},
+    {256, true, 1, 0.310, 2.2, 3.7, 0.0, run_linear<256, true, 1, false>},
 };
 
 // Few tokens take the kernel for them; the others the form that takes the least
 // time by the figures above.
 cudaError_t launch_linear(const Operands& op, const LinArgs& args, int sms, cudaStream_t s) {
-  if (args.M <= kFewTokens) {
-    if (args.M == 1) return run_few<1>(op, args, s);
-    if (args.M == 2) return run_few<2>(op, args, s);
+  if (op.M <= kFewTokens) {
+    if (op.M == 1) return run_few<1>(op, args, s);
+    if (op.M == 2) return run_few<2>(op, args, s);
     return run_few<4>(op, args, s);
   }
   Form best = {};
   double least = 0;
   for (const Form& f : kForms) {
     const int64_t channels = f.pair ? 2 * kBM : kBM;
-    const int64_t tiles = (static_cast<int64_t>(args.M) + f.bn - 1) / f.bn *
-                          ((static_cast<int64_t>(args.N) + channels - 1) / channels);
+    const int64_t tiles = (op.M + f.bn - 1) / f.bn * ((op.N + channels - 1) / channels);
     // a cluster's CTAs run at the same time, and each has two K blocks at least
     if (f.split > 1 && (tiles * f.split > 128 || args.nkb < 2 * f.split)) continue;
     const int64_t units = f.pair ? sms / 2 : sms;
@@ -835,6 +979,9 @@ cudaError_t launch_linear(const Operands& op, const LinArgs& args, int sms, cuda
       least = us;
     }
   }
+  const int size = args.y_bf16 ? 2 : 4;
+  if (best.pair && is_aligned(args.y, 16) && args.ldy * size % 16 == 0)
+    return run_linear<256, true, 1, true>(op, args, sms, s);
   return best.run(op, args, sms, s);
 }
 
@@ -866,14 +1013,14 @@ int dlrm_linear_fp4(const uint8_t* x, int64_t ldx, const uint8_t* x_scale, const
   a.bias = bias;
   a.y = y;
   a.ldy = ldy;
-  a.M = static_cast<int>(M);
-  a.N = static_cast<int>(N);
+  a.na = static_cast<int>(N);
+  a.nb = static_cast<int>(M);
   a.K = static_cast<int>(K);
   a.nkb = static_cast<int>((K + kCols - 1) / kCols);
   a.act = act;
   a.y_bf16 = y_dtype == DLRM_TABLE_BF16;
   a.status = status_dev;
-  const Operands op = {x, x_scale, w, w_scale, ldx, ldw, K};
+  const Operands op = {x, x_scale, w, w_scale, ldx, ldw, M, N, K};
   const auto s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = launch_linear(op, a, sms, s);
   if (e != cudaSuccess) return cuda_fail(e);
