@@ -148,7 +148,7 @@ __device__ __forceinline__ void store4(T* p, int left, const Pair* v) {
   if constexpr (ALL && sizeof(T) == 4) {
     *reinterpret_cast<float4*>(p) = make_float4(a.x, a.y, b.x, b.y);
   } else if constexpr (ALL) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(bf16x2_bits(a.x, a.y), bf16x2_bits(b.x, b.y));
+    *reinterpret_cast<uint2*>(p) = make_uint2(bf16_pair(a.x, a.y), bf16_pair(b.x, b.y));
   } else {
     const float e[4] = {a.x, a.y, b.x, b.y};
 #pragma unroll

@@ -6,11 +6,11 @@
 //
 // Fourteen warps a CTA: one thread streams 128-byte K blocks (256 elements) of both
 // operands and their scale tiles into a shared-memory ring with TMA loads; four warps
-// carry a stage's scales from there into TMEM, two or four stages' ahead; one thread
+// carry a stage's scales from there into TMEM, up to four stages ahead; one thread
 // issues a stage's four products; eight warps drain a finished accumulator while the
 // next tile's products fill the other. (tcgen05.cp brings scales to TMEM as well, but in
 // the tensor cores' own queue: a stage's six copies held up its products by 0.15 of 0.63
-// us, 8192^3 284 us instead of CARRIED.)
+// us, 8192^3 284 us where this took 240.)
 //
 // Forms:
 //   - CTAs of 128 channels x 64 or 128 tokens: the weights take the M side, so an
@@ -21,9 +21,9 @@
 //   - CTA pairs (cta_group::2) of 256 x 256. Where rows of y start on 16 bytes the
 //     tokens take the M side: a lane then has neighbouring channels of a token, lays
 //     them out in shared memory, and the copy engine writes whole lines. Two accumulators of 256 columns and
-//     the scales do not fit TMEM's 512, so the accumulators share 64 columns: those
+//     the scales do not fit TMEM's 512, so the accumulators share 128 columns: those
 //     are drained first, and the next tile's products wait for that.
-//   - up to four tokens: CUDA cores, a warp for each channel (below).
+//   - one token: CUDA cores (below).
 // Every wait is bounded; one that runs out sets DLRM_FLAG_TIMEOUT in the
 // optional status word, and the CTA still lets its loads land, frees its tensor
 // memory and exits.
@@ -33,6 +33,7 @@
 
 #include "fp4_common.cuh"
 #include "ring_landing.h"
+#include "sectors.cuh"
 #include "tcgen05_common.cuh"
 #include "tokens/common.h"
 
@@ -50,6 +51,7 @@ constexpr int kThreads = 32 * (kScaleWarp + 4);
 constexpr long long kWaitLimit = 200000000LL;  // clock cycles, about 0.1 s
 constexpr int kMaxDevices = 64;                // devices whose launch set-up is cached
 
+constexpr int kBand = 8;  // tiles of b that are walked together
 // The operand on the M side is a (the weights, or with TOKENS_M the tokens), the other b.
 struct LinArgs {
   const float* bias;
@@ -58,6 +60,7 @@ struct LinArgs {
   int na, nb, K;                 // rows of a and of b
   int nkb;                       // K blocks
   int tiles_a, tiles_b, tiles;
+  Divisor by_band;               // a band's tiles
   int act, y_bf16;
   int32_t* status;
 };
@@ -85,7 +88,7 @@ struct Ring {
   static constexpr int kBias = kOut + kEpiWarps * kOutBytes;  // a slice of it for each warp
   static constexpr int kBars = OUT ? kBias + kEpiWarps * (BN / 2) * 4 : kOut;
   // stages whose scales are in TMEM at a time
-  static constexpr int kCarried = BN > 128 ? 2 : 4;
+  static constexpr int kCarried = 4;
   static constexpr int kBarriers = 3 * kStages + kCarried + 6;
   static constexpr int kTotal = kBars + kBarriers * 8 + 8 + 1024;  // + alignment
   static_assert(kStage % 1024 == 0, "swizzled tiles start on 1024 bytes");
@@ -93,7 +96,7 @@ struct Ring {
   static_assert(kTotal <= 227 * 1024, "shared memory of one CTA");
   // TMEM columns: the second accumulator, the scales, and what both accumulators have
   // of each other
-  static constexpr int kLap = BN > 128 ? 64 : 0;
+  static constexpr int kLap = BN > 128 ? 128 : 0;
   static constexpr uint32_t kAcc1 = BN - kLap;
   static constexpr uint32_t kScales = kAcc1 + BN;
   static constexpr uint32_t kScaleCols = 4 * kStageTiles * (1 + kBTiles);
@@ -200,18 +203,19 @@ __device__ __forceinline__ void put_tokens(const LinArgs& a, int row, float bias
   if (row >= a.na) return;
   Out* p = static_cast<Out*>(a.y) + static_cast<int64_t>(b0) * a.ldy + row;
   const int left = a.nb - b0;
-  if (left >= 32) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      put_at<ACT>(p, v[i], bias);
-      p += a.ldy;
+  for (int i = 0; i < 32; i += 2) {
+    const float lo = activate<ACT>(__fadd_rn(v[i], bias)), hi = activate<ACT>(__fadd_rn(v[i + 1], bias));
+    if constexpr (sizeof(Out) == 4) {
+      if (i < left) p[0] = lo;
+      if (i + 1 < left) p[a.ldy] = hi;
+    } else {
+      const uint32_t both = bf16_pair(lo, hi);
+      uint16_t* at = reinterpret_cast<uint16_t*>(p);
+      if (i < left) at[0] = static_cast<uint16_t>(both);
+      if (i + 1 < left) at[a.ldy] = static_cast<uint16_t>(both >> 16);
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      if (i < left) put_at<ACT>(p, v[i], bias);
-      p += a.ldy;
-    }
+    p += 2 * a.ldy;
   }
 }
 
@@ -239,8 +243,8 @@ __device__ __forceinline__ void put_channels(const LinArgs& a, const CUtensorMap
     __syncwarp();
 #pragma unroll
     for (int p = 0; p < 8; ++p)
-      store_f32<Out, kPiece>(reinterpret_cast<Out*>(out + lane * 128 + ((p ^ (lane & 7)) << 4)),
-                             *reinterpret_cast<const float(*)[kPiece]>(v + c + p * kPiece));
+      store_16_bytes(reinterpret_cast<Out*>(out + lane * 128 + ((p ^ (lane & 7)) << 4)),
+                     v + c + p * kPiece);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0 && row0 < a.na && b0 + c < a.nb) {
@@ -251,8 +255,8 @@ __device__ __forceinline__ void put_channels(const LinArgs& a, const CUtensorMap
 }
 
 // Calls f with the activation and the output type as types.
-template <class F>
-__device__ __forceinline__ void by_kind(const LinArgs& a, F f) {
+template <class Args, class F>
+__device__ __forceinline__ void by_kind(const Args& a, F f) {
   if (a.y_bf16) {
     if (a.act == DLRM_ACT_RELU)
       f.template run<DLRM_ACT_RELU, __nv_bfloat16>();
@@ -335,15 +339,18 @@ struct JoinCall {
   }
 };
 
-// Tile t -> (tile of a, tile of b): bands of 8 tiles of b, so that the CTAs at work at one
+// Tile t -> (tile of a, tile of b): bands of kBand tiles of b, so that the CTAs at work at one
 // time read few different rows of either operand.
 __device__ __forceinline__ void tile_at(const LinArgs& a, int t, int& ta, int& tb) {
-  constexpr int kBand = 8;
-  const int per_band = kBand * a.tiles_a;
-  const int band = t / per_band, in = t % per_band;
+  const int band = static_cast<int>(a.by_band.of(t)), in = t - band * (kBand * a.tiles_a);
   const int height = min(kBand, a.tiles_b - band * kBand);
-  tb = band * kBand + in % height;
-  ta = in / height;
+  if (height == kBand) {
+    tb = band * kBand + in % kBand;
+    ta = in / kBand;
+  } else {
+    tb = band * kBand + in % height;
+    ta = in / height;
+  }
 }
 
 // S > 1: the S CTAs of a cluster share one tile (and there is one tile a cluster).
@@ -359,7 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int kWarpCols = BN / 2;                         // columns an epilogue warp drains
   constexpr int kAtOnce = kWarpCols < 64 ? kWarpCols : 64;  // of them at a time
   static_assert(kAtOnce % 32 == 0, "whole TMEM loads");
-  static_assert(R::kLap == 0 || R::kLap == kAtOnce, "the shared columns are one warp's step");
+  static_assert(R::kLap == 0 || (R::kLap == 2 * kAtOnce && BN == 4 * kAtOnce),
+                "the shared columns are a step of all warps");
   static_assert(!TOKENS_M || kAtOnce == 64, "whole lines of y");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
@@ -399,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&acc_empty[b], CG * kEpiWarps);
     }
     mbar_init(mma_done, 1);
-    mbar_init(lap_empty, CG * kEpiWarps / 2);
+    mbar_init(lap_empty, CG * kEpiWarps);
     mbar_init_fence();
     if constexpr (PAIR) *other_steps = ~0u;
   }
@@ -480,11 +488,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // The whole warp walks the stages and one elected lane issues: what the products' operands are
     // made of is then the same for the warp and stays in its uniform registers (by one
-    // lane alone a stage took WAS cycles, now IS).
+    // lane alone a stage of a pair took 911 cycles, so 680).
     if (!PAIR || rank == 0) {
       const uint64_t a_desc = sdesc_k_sw128(smem_u32(smem));
       const uint64_t b_desc = sdesc_k_sw128(smem_u32(smem) + R::kA);
-      int g = 0, j = 0, s = 0, c = 0;
+      int j = 0, s = 0, c = 0;
       uint32_t s_turn = 0, c_turn = 0;  // parities of the ring's and the column sets' turns
       for (int t = unit0; t < args.tiles && !timed_out; t += unit_step, ++j) {
         const int b = j & 1;
@@ -499,10 +507,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         int ta, tb;
         tile_at(args, t, ta, tb);
         const uint32_t b_col = static_cast<uint32_t>(tb * BN % 128 / 32);
-        for (int kb = kb_begin; kb < kb_end; ++kb, ++g) {
-          ok = mbar_wait_bounded(&full[s], s_turn, kWaitLimit) &&
-               mbar_wait_bounded(&carried[c], c_turn, kWaitLimit);
-          if (!__all_sync(kFull, ok)) {
+        for (int kb = kb_begin; kb < kb_end; ++kb) {
+          if (!__all_sync(kFull, mbar_wait_bounded(&full[s], s_turn, kWaitLimit) &&
+                                     mbar_wait_bounded(&carried[c], c_turn, kWaitLimit))) {
             timed_out = true;
             break;
           }
@@ -578,6 +585,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     const int ew = warp - 2, quarter = warp & 3, half = ew >> 2;
+    // TOKENS_M: a warp's bias of a tile, a few columns a lane, on its way since the tile before
+    constexpr int kMine = kWarpCols / 32;
+    float next[kMine] = {};
+    auto fetch_bias = [&](int t) {
+      if (!TOKENS_M || args.bias == nullptr || t >= args.tiles) return;
+      int ta, tb;
+      tile_at(args, t, ta, tb);
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int c = 32 * i + lane;
+        const int n = tb * BN + (c / kAtOnce * 2 + half) * kAtOnce + c % kAtOnce;
+        next[i] = n < args.nb ? args.bias[n] : 0.f;
+      }
+    };
+    fetch_bias(unit0);
     int j = 0;
     for (int t = unit0; t < args.tiles; t += unit_step, ++j) {
       const int b = j & 1;
@@ -590,11 +612,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* slice = reinterpret_cast<float*>(smem + R::kBias) + ew * kWarpCols;
       if constexpr (TOKENS_M) {
         __syncwarp();  // the slice's readers of the tile before are done
-        for (int c = lane; c < kWarpCols; c += 32) {
-          const int n = b0 + half * kWarpCols + c;
-          slice[c] = args.bias != nullptr && n < args.nb ? args.bias[n] : 0.f;
-        }
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) slice[32 * i + lane] = next[i];
         __syncwarp();
+        fetch_bias(t + unit_step);
       }
       if (!__all_sync(kFull, mbar_wait_bounded(&acc_full[b], (j >> 1) & 1, kWaitLimit))) {
         timed_out = true;
@@ -602,22 +623,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_after_sync();
       const uint32_t tq = tmem + (b != 0 ? R::kAcc1 : 0u) + (static_cast<uint32_t>(quarter * 32) << 16);
-      // The columns that the next tile's accumulator has too come first: the last of the
-      // lower accumulator, the first of the upper one.
+      // A step is 64 columns a warp, those of the two halves of warps next to each other. The
+      // columns that the next tile's accumulator has too come first: the upper ones of the
+      // lower accumulator, the lower ones of the upper one.
       constexpr int kSteps = kWarpCols / kAtOnce;
-      const bool lap = R::kLap != 0 && half == 1 - b;
-      const int first = lap && b == 0 ? kSteps - 1 : 0;
       for (int i = 0; i < kSteps; ++i) {
-        const int c = half * kWarpCols + (first + i) % kSteps * kAtOnce;
+        const int step = kSteps == 2 ? (i + 1 - b) & 1 : i;
+        const int c = (2 * step + half) * kAtOnce;
         float v[kAtOnce];
 #pragma unroll
         for (int h = 0; h < kAtOnce; h += 32)
           tmem_ld_32x32b_x32(tq + c + h, *reinterpret_cast<float(*)[32]>(v + h));
-        if (lap && i == 0) arrive(lap_empty);
+        if (R::kLap != 0 && i == 0) arrive(lap_empty);
         if (i == kSteps - 1) arrive(&acc_empty[b]);
 if constexpr (TOKENS_M) {
           by_kind(args, PutChannels{args, &maps.y, smem + R::kOut + ew * kOutBytes, row - lane,
-                                    b0 + c, lane, slice + (c - half * kWarpCols), v});
+                                    b0 + c, lane, slice + step * kAtOnce, v});
         } else {
 #pragma unroll
           for (int h = 0; h < kAtOnce; h += 32) {
@@ -655,32 +676,57 @@ if constexpr (TOKENS_M) {
   if (warp == 1) tmem_dealloc<CG>(tmem, R::kTmem);
 }
 
-// Few tokens: a warp for each channel, a lane for each block of 32 columns. Codes become
-// twice their values as 8-bit integers (a byte permutation looks four up in a register
-// pair), four products an instruction, the block's sum exact in int32 and scaled once.
-// The tokens' codes are looked up once a CTA and kept in shared memory. Channels r and
-// r + 1 of each of a row tile's 32-row groups make a CTA: their scales are whole sectors.
-constexpr int kVecThreads = 256;
-constexpr int kFewTokens = 4;
-constexpr int kPiece = 128;  // blocks of K that a CTA takes at a time: 4 a lane
+// One token: R channels a warp, a lane for each block of 32 columns, U of them at a time.
+// Codes become twice their values as 8-bit integers (a byte permutation looks four up in a
+// register pair), four products an instruction; a block's sum is exact in int32 and scaled
+// once. The token's codes are looked up once a warp and stay in registers, and all of a
+// warp's weights are on their way before the first is used. Bound by the pipe of those
+// permutations before memory is (4096 x 4096: 5.5 us, 1.4 by its bytes).
+constexpr int kOneThreads = 128;
 
-struct VecArgs {
-  LinArgs lin;      // a: the weights, b: the tokens
+struct OneArgs {
   const uint8_t* x;
   const uint8_t* x_scale;
   const uint8_t* w;
   const uint8_t* w_scale;
-  int64_t ldx, ldw, block_tiles;
-  int blocks;       // of 32 columns
-  int bytes;        // of a row's codes
+  const float* bias;
+  void* y;
+  int64_t ldw, block_tiles;
+  int N;
+  int blocks;  // of 32 columns
+  int bytes;   // of a row's codes
+  int act, y_bf16;
 };
 
-// Four codes (16 bits) as twice their values.
-__device__ __forceinline__ uint32_t doubled(uint32_t codes) {
-  const uint32_t at = codes & 0x7777u;
-  const uint32_t pos = __byte_perm(0x03020100u, 0x0c080604u, at);
-  const uint32_t neg = __byte_perm(0xfdfeff00u, 0xf4f8fafcu, at);
-  return __byte_perm(pos, neg, 0x3210u | ((codes >> 1) & 0x4444u));
+// Eight codes as twice their values.
+__device__ __forceinline__ void doubled(uint32_t codes, uint32_t (&v)[2]) {
+  const uint32_t at = codes & 0x77777777u, sign = 0x32103210u | (codes >> 1 & 0x44444444u);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t pos = __byte_perm(0x03020100u, 0x0c080604u, at >> (16 * h));
+    const uint32_t neg = __byte_perm(0xfdfeff00u, 0xf4f8fafcu, at >> (16 * h));
+    v[h] = __byte_perm(pos, neg, sign >> (16 * h));
+  }
+}
+
+// Four codes' doubled magnitudes; zero where a code's sign bit is set (the permutation then
+// gives the sign of the byte).
+__device__ __forceinline__ uint32_t looked_up(uint32_t codes) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(0x03020100u), "r"(0x0c080604u), "r"(codes));
+  return r;
+}
+
+// sum and less grow by the positive and the negative ones of eight codes times x.
+__device__ __forceinline__ int dot8(uint32_t codes, const uint32_t (&x)[2], int sum, int& less) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t c = codes >> (16 * h);
+    const uint32_t pos = looked_up(c), neg = looked_up(c ^ 0x8888u);
+    sum = __dp4a(static_cast<int>(pos), static_cast<int>(x[h]), sum);
+    less = __dp4a(static_cast<int>(neg), static_cast<int>(x[h]), less);
+  }
+  return sum;
 }
 
 // 16 bytes of a row's codes from byte `at` on; zeros past its end (rows start on 16 bytes and
@@ -702,95 +748,88 @@ __device__ __forceinline__ uint4 load_codes(const uint8_t* row, int at, int byte
   return r;
 }
 
-template <int MT>
-struct FewCall {
-  const VecArgs& a;
-  int n, lane;
-  const float (&sum)[MT];
+struct PutOne {
+  const OneArgs& a;
+  int n;
+  float sum;
   template <int ACT, class Out>
   __device__ __forceinline__ void run() const {
-    float mine = 0.f;
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-      if (lane == m) mine = sum[m];
-    if (lane < MT && lane < a.lin.nb)
-      put_at<ACT>(static_cast<Out*>(a.lin.y) + lane * a.lin.ldy + n, mine,
-                  a.lin.bias != nullptr ? a.lin.bias[n] : 0.f);
+    put_at<ACT>(static_cast<Out*>(a.y) + n, sum, a.bias != nullptr ? a.bias[n] : 0.f);
   }
 };
 
-template <int MT>
-__global__ void __launch_bounds__(kVecThreads) linear_few_kernel(const VecArgs a) {
-  // of each token and block: 32 bytes in two planes, and its scale's byte
-  __shared__ uint4 xv[MT][2][kPiece];
-  __shared__ uint8_t xe[MT][kPiece];
+template <int U, int R>
+__global__ void __launch_bounds__(kOneThreads) linear_one_kernel(const OneArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // as in the kernel above
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int tile = blockIdx.x / 16;
-  const int r = blockIdx.x % 16 * 2 + (warp & 1) + 32 * (warp >> 1);
-  const int n = tile * 128 + r;
-  const bool live = n < a.lin.na;
-  const uint8_t* w = a.w + static_cast<int64_t>(live ? n : 0) * a.ldw;
-  const uint8_t* ws = a.w_scale + fp4_scale_at(a.block_tiles, live ? n : 0, 0);
-  float acc[MT] = {};
-  constexpr int U = kPiece / 32;
-  for (int b0 = 0; b0 < a.blocks; b0 += kPiece) {
-    uint4 wv[U];
-    uint32_t we[U];
+  const int lane = threadIdx.x & 31;
+  const int n0 = (blockIdx.x * (kOneThreads / 32) + (threadIdx.x >> 5)) * R;
+  if (n0 >= a.N) return;
+  const uint8_t* w[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) w[r] = a.w + min(n0 + r, a.N - 1) * a.ldw;
+  // R channels from a multiple of R on are 16 bytes apart in a scale tile, those past N too
+  static_assert(32 % R == 0, "R channels lie in one 32-row group");
+  const uint8_t* ws = a.w_scale + fp4_scale_at(a.block_tiles, n0, 0);
+  float acc[R] = {};
+  uint32_t top = 0;  // the largest scale byte: whether one is NaN
+  for (int b0 = lane; b0 < a.blocks; b0 += 32 * U) {
+    uint4 wv[R][U], xv[U];
+    uint32_t we[R][U], xe[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int b = b0 + u * 32 + lane;
-      wv[u] = make_uint4(0, 0, 0, 0);
-      we[u] = 0;
-      if (live && b < a.blocks) {
-        wv[u] = load_codes(w, b * 16, a.bytes);
-        we[u] = ws[static_cast<int64_t>(b >> 2) * kFp4Tile + (b & 3)];
+      const int b = b0 + u * 32;
+      const bool in = u == 0 || b < a.blocks;
+      const int64_t tile = static_cast<int64_t>(b >> 2) * kFp4Tile + (b & 3);
+      xv[u] = load_codes(a.x, b * 16, a.bytes);
+      xe[u] = in ? a.x_scale[tile] : 0u;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        wv[r][u] = load_codes(w[r], b * 16, a.bytes);
+        we[r][u] = in ? ws[tile + 16 * r] : 0u;
       }
     }
-    __syncthreads();  // the piece before has been read
-    for (int i = threadIdx.x; i < MT * kPiece; i += kVecThreads) {
-      const int m = i / kPiece, p = i % kPiece, b = b0 + p;
-      uint4 c = make_uint4(0, 0, 0, 0);
-      uint32_t e = 0;
-      if (m < a.lin.nb && b < a.blocks) {
-        c = load_codes(a.x + m * a.ldx, b * 16, a.bytes);
-        e = a.x_scale[fp4_scale_at(a.block_tiles, m, b)];
-      }
-      xv[m][0][p] = make_uint4(doubled(c.x), doubled(c.x >> 16), doubled(c.y), doubled(c.y >> 16));
-      xv[m][1][p] = make_uint4(doubled(c.z), doubled(c.z >> 16), doubled(c.w), doubled(c.w >> 16));
-      xe[m][p] = static_cast<uint8_t>(e);
-    }
-    __syncthreads();
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int p = u * 32 + lane;
-      const uint32_t c[4] = {wv[u].x, wv[u].y, wv[u].z, wv[u].w};
-      uint32_t d[8];
+      const uint32_t xc[4] = {xv[u].x, xv[u].y, xv[u].z, xv[u].w};
+      uint32_t x[4][2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) d[2 * i] = doubled(c[i]), d[2 * i + 1] = doubled(c[i] >> 16);
+      for (int i = 0; i < 4; ++i) doubled(xc[i], x[i]);
+      top = max(top, xe[u]);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        int s = 0;
+      for (int r = 0; r < R; ++r) {
+        const uint32_t wc[4] = {wv[r][u].x, wv[r][u].y, wv[r][u].z, wv[r][u].w};
+        int sum = 0, less = 0;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint4 x = xv[m][h][p];
-          s = __dp4a(static_cast<int>(d[4 * h]), static_cast<int>(x.x), s);
-          s = __dp4a(static_cast<int>(d[4 * h + 1]), static_cast<int>(x.y), s);
-          s = __dp4a(static_cast<int>(d[4 * h + 2]), static_cast<int>(x.z), s);
-          s = __dp4a(static_cast<int>(d[4 * h + 3]), static_cast<int>(x.w), s);
-        }
+        for (int i = 0; i < 4; ++i) sum = dot8(wc[i], x[i], sum, less);
         // The sum is four times that of the values. The scales' product in two halves, so
-        // that no product on the way leaves f32 where the last one does not.
-        const uint32_t ex = xe[m][p], e = we[u] + ex, e1 = max(we[u], ex) == 255u ? 255u : e >> 1;
-        acc[m] += static_cast<float>(s) * 0.25f * fp4_scale_value(e1) * fp4_scale_value(e - (e >> 1));
+        // that none on the way leaves f32 where the last does not (a half of 2^-127 is
+        // taken as zero: the product of both vanishes in f32).
+        const uint32_t e = we[r][u] + xe[u], e1 = e >> 1;
+        top = max(top, we[r][u]);
+        acc[r] += static_cast<float>(sum - less) * 0.25f * __uint_as_float(e1 << 23) *
+                  __uint_as_float((e - e1) << 23);
       }
     }
   }
+  top = __reduce_max_sync(kFull, top);
+  if (top == 255u) {
+    // a NaN among the scales (255 + 253 is as well that of two numbers): which of the
+    // channels have one
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
+    for (int r = 0; r < R; ++r)
+      for (int b = lane; b < a.blocks; b += 32)
+        if (a.x_scale[fp4_scale_at(a.block_tiles, 0, b)] == 255u ||
+            a.w_scale[fp4_scale_at(a.block_tiles, min(n0 + r, a.N - 1), b)] == 255u)
+          acc[r] = __uint_as_float(0x7fc00000u);
+  }
+  float mine = 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) acc[m] += __shfl_xor_sync(kFull, acc[m], o);
-  if (live) by_kind(a.lin, FewCall<MT>{a, n, lane, acc});
+  for (int r = 0; r < R; ++r) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) acc[r] += __shfl_xor_sync(kFull, acc[r], o);
+    if (lane == r) mine = acc[r];
+  }
+  if (lane < R && n0 + lane < a.N) by_kind(a, PutOne{a, n0 + lane, mine});
 }
 
 struct Operands {
@@ -890,9 +929,10 @@ cudaError_t run_linear(const Operands& op, LinArgs args, int sms, cudaStream_t s
   args.tiles_b = (args.nb + BN - 1) / BN;
   args.tiles_a = (args.na + kUnitA - 1) / kUnitA;
   const int64_t tiles = static_cast<int64_t>(args.tiles_a) * args.tiles_b;
-  if (tiles > INT_MAX || static_cast<int64_t>(args.tiles_a) * 8 > INT_MAX)
+  if (tiles > INT_MAX || static_cast<int64_t>(args.tiles_a) * kBand > INT_MAX)
     return cudaErrorInvalidValue;
   args.tiles = static_cast<int>(tiles);
+  args.by_band = Divisor(static_cast<uint32_t>(args.tiles_a) * kBand);
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
@@ -927,62 +967,72 @@ cudaError_t run_linear(const Operands& op, LinArgs args, int sms, cudaStream_t s
   return cudaLaunchKernelEx(&cfg, fn, maps, args);
 }
 
-template <int MT>
-cudaError_t run_few(const Operands& op, const LinArgs& args, cudaStream_t stream) {
-  const VecArgs a = {args, op.x, op.x_scale, op.w, op.w_scale, op.ldx, op.ldw,
-                     fp4_block_tiles(op.K), static_cast<int>((op.K + 31) / 32),
-                     static_cast<int>((op.K + 1) / 2)};
-  return launch(&linear_few_kernel<MT>, dim3(static_cast<unsigned>((args.na + 127) / 128 * 16)),
-                kVecThreads, 0, true, stream, a);
+template <int U, int R>
+cudaError_t run_one(const OneArgs& a, cudaStream_t stream) {
+  constexpr int kChannels = kOneThreads / 32 * R;
+  return launch(&linear_one_kernel<U, R>, dim3(static_cast<unsigned>((a.N + kChannels - 1) / kChannels)),
+                kOneThreads, 0, true, stream, a);
 }
 
-// The forms of the tensor-core kernel, with what they take in us: a stage (256 columns of
-// K), a tile besides, a tile at least (its drain), and the joining of a cluster's parts.
+// The forms of the tensor-core kernel, with what they take on a B200 in us besides a launch: a
+// stage of a tile (`step`: 256 columns of K), a tile besides (`tile`), and what comes
+// once (`once`: filling the ring, draining the last tile, joining a cluster's parts). Fitted
+// to all forms at 31 shapes from 2 x 4096 x 4096 to 65536 x 592 -> 512 in a graph, weights
+// from HBM; the choice was the fastest form, or within 3 % of it, at all of them.
 struct Form {
-  int bn;
-  bool pair;
+  int rows_m, rows_n;  // of a tile: channels and tokens
+  int units;           // of 148 SMs that walk tiles: all, or pairs
   int split;
-  double step, tile, least, join;
+  bool lines;          // whether it needs rows of y on 16 bytes
+  double step, tile, once;
   cudaError_t (*run)(const Operands&, LinArgs, int, cudaStream_t);
 };
 const Form kForms[] = {
-    {64, false, 1, 0.290, 0.7, 0.0, 0.0, run_linear<64, false, 1, false>},
-    {64, false, 2, 0.290, 0.7, 0.0, 1.7, run_linear<64, false, 2, false>},
-    {64, false, 4, 0.290, 0.7, 0.0, 2.4, run_linear<64, false, 4, false>},
-    {128, false, 1, 0.280, 1.2, 2.0, 0.0, run_linear<128, false, 1, false>},
-    {128, false, 2, 0.280, 1.2, 2.0, 2.7, run_linear<128, false, 2, false>},
-    {128, false, 4, 0.280, 1.2, 2.0, 3.0, run_linear<128, false, 4, false>},
-    {256, true, 1, 0.310, 2.2, 3.7, 0.0, run_linear<256, true, 1, false>},
+    {128, 64, 1, 1, false, 0.349, 0.6, 0.9, run_linear<64, false, 1, false>},
+    {128, 64, 1, 2, false, 0.328, 1.9, 1.7, run_linear<64, false, 2, false>},
+    {128, 64, 1, 4, false, 0.150, 2.2, 3.0, run_linear<64, false, 4, false>},
+    {128, 128, 1, 1, false, 0.350, 1.3, 0.7, run_linear<128, false, 1, false>},
+    {128, 128, 1, 2, false, 0.331, 2.9, 1.8, run_linear<128, false, 2, false>},
+    {128, 128, 1, 4, false, 0.150, 3.2, 2.8, run_linear<128, false, 4, false>},
+    {256, 256, 2, 1, false, 0.383, 2.6, 0.8, run_linear<256, true, 1, false>},
+    {256, 256, 2, 1, true, 0.371, 1.6, 2.5, run_linear<256, true, 1, true>},
 };
 
-// Few tokens take the kernel for them; the others the form that takes the least
-// time by the figures above.
+// One token and weights of up to 2^25 elements take the kernel for it (16.8 M elements 5.5 us
+// and 7.0 by tensor cores, 33.5 M 10 and 10, 67 M 13.6 and 11.5); the others the form that takes
+// the least time by the figures above.
 cudaError_t launch_linear(const Operands& op, const LinArgs& args, int sms, cudaStream_t s) {
-  if (op.M <= kFewTokens) {
-    if (op.M == 1) return run_few<1>(op, args, s);
-    if (op.M == 2) return run_few<2>(op, args, s);
-    return run_few<4>(op, args, s);
+  if (op.M == 1 && op.N * op.K <= (int64_t{1} << 25)) {
+    const OneArgs a = {op.x, op.x_scale, op.w, op.w_scale, args.bias, args.y, op.ldw,
+                       fp4_block_tiles(op.K), static_cast<int>(op.N),
+                       static_cast<int>((op.K + 31) / 32), static_cast<int>((op.K + 1) / 2),
+                       args.act, args.y_bf16};
+    // Four channels a warp where that leaves four warps an SM (1024 -> 8192 3.2 us, one channel
+    // 5.0; 8192 -> 1024 7.2 and 4.9), and as many blocks a lane as a row has, two or four.
+    const bool many = op.N >= 4 * 4 * sms;
+    if (a.blocks <= 32) return many ? run_one<1, 4>(a, s) : run_one<1, 1>(a, s);
+    if (a.blocks <= 64) return many ? run_one<2, 4>(a, s) : run_one<2, 1>(a, s);
+    return many ? run_one<2, 4>(a, s) : run_one<4, 1>(a, s);
   }
-  Form best = {};
+  const int size = args.y_bf16 ? 2 : 4;
+  const bool lines = is_aligned(args.y, 16) && args.ldy * size % 16 == 0;
+  const Form* best = nullptr;
   double least = 0;
   for (const Form& f : kForms) {
-    const int64_t channels = f.pair ? 2 * kBM : kBM;
-    const int64_t tiles = (op.M + f.bn - 1) / f.bn * ((op.N + channels - 1) / channels);
+    if (f.lines && !lines) continue;
+    const int64_t tiles =
+        (op.M + f.rows_n - 1) / f.rows_n * ((op.N + f.rows_m - 1) / f.rows_m);
     // a cluster's CTAs run at the same time, and each has two K blocks at least
     if (f.split > 1 && (tiles * f.split > 128 || args.nkb < 2 * f.split)) continue;
-    const int64_t units = f.pair ? sms / 2 : sms;
+    const int64_t units = sms / f.units;
     const int64_t rounds = (tiles + units - 1) / units;
-    const double us =
-        rounds * std::max(f.least, f.step * args.nkb / f.split + f.tile) + f.join;
-    if (best.run == nullptr || us < least) {
-      best = f;
+    const double us = rounds * (f.step * args.nkb / f.split + f.tile) + f.once;
+    if (best == nullptr || us < least) {
+      best = &f;
       least = us;
     }
   }
-  const int size = args.y_bf16 ? 2 : 4;
-  if (best.pair && is_aligned(args.y, 16) && args.ldy * size % 16 == 0)
-    return run_linear<256, true, 1, true>(op, args, sms, s);
-  return best.run(op, args, sms, s);
+  return best->run(op, args, sms, s);
 }
 
 }  // namespace

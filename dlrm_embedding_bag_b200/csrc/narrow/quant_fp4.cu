@@ -233,8 +233,7 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const DequantArgs 
     store_sectors(y, v);
   } else {
 #pragma unroll
-    for (int e = 0; e < 16; e += V)
-      store_f32<T, V, true>(y + e, *reinterpret_cast<const float(*)[V]>(v + e));
+    for (int e = 0; e < 16; e += V) store_16_bytes(y + e, v + e);
   }
 }
 
@@ -269,8 +268,7 @@ __global__ void __launch_bounds__(kThreads) dequantize_staged_kernel(const Dequa
   T* mine = staged[threadIdx.x >> 5].v + lane / G * (G * Staged<T>::kLane);
   constexpr int V = kVecOf<T>;
 #pragma unroll
-  for (int e = 0; e < 16; e += V)
-    store_f32<T, V>(mine + Staged<T>::at(16 * in) + e, *reinterpret_cast<const float(*)[V]>(v + e));
+  for (int e = 0; e < 16; e += V) store_16_bytes(mine + Staged<T>::at(16 * in) + e, v + e);
   __syncwarp();
   T* y = static_cast<T*>(a.y) + row * a.ldy + c0 + in;
 #pragma unroll

@@ -1,4 +1,4 @@
-// Accesses of 32 bytes, a whole sector of memory each.
+// Accesses of 32 bytes, a whole sector of memory each, and pairs of bf16 by one conversion.
 #pragma once
 
 #include <cstdint>
@@ -6,6 +6,24 @@
 #include "tokens/common.h"
 
 namespace dlrm {
+
+// Two values rounded to bf16, the first in the lower half. (One instruction at the rate of
+// other arithmetic; conversions one by one run at an eighth of it.)
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// 16 bytes of T from v at p.
+template <class T>
+__device__ __forceinline__ void store_16_bytes(T* p, const float* v) {
+  if constexpr (sizeof(T) == 4)
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  else
+    *reinterpret_cast<uint4*>(p) = make_uint4(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]),
+                                              bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7]));
+}
 
 __device__ __forceinline__ void load_32_bytes(const void* p, uint32_t (&w)[8]) {
   asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -22,7 +40,7 @@ __device__ __forceinline__ void store_sectors(T* p, const float* v) {
   uint32_t w[kWords];
 #pragma unroll
   for (int i = 0; i < kWords; ++i)
-    w[i] = sizeof(T) == 4 ? __float_as_uint(v[i]) : bf16x2_bits(v[2 * i], v[2 * i + 1]);
+    w[i] = sizeof(T) == 4 ? __float_as_uint(v[i]) : bf16_pair(v[2 * i], v[2 * i + 1]);
 #pragma unroll
   for (int i = 0; i < kWords; i += 8) {
     uint32_t* at = reinterpret_cast<uint32_t*>(p) + i;
