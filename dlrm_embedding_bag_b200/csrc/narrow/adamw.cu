@@ -293,8 +293,20 @@ __device__ __forceinline__ void step_block(const StepArgs& a, const Factors& f, 
     const float2 d = parts(fma(r[i], root, eps));
     p[i] = fma(mul(m[i], pair(reciprocal(d.x), reciprocal(d.y))), alpha, mul(p[i], keep));
   }
+  if constexpr (!ALL) {
+    // what lies behind the tensor's end stays zero, whatever the factors are
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = q[i / 2] + i % 2 * 2;
+      const float2 pe = parts(p[i]), me = parts(m[i]), ve = parts(v[i]), re = parts(r[i]);
+      const bool lo = e < left, hi = e + 1 < left;
+      p[i] = pair(lo ? pe.x : 0.f, hi ? pe.y : 0.f);
+      m[i] = pair(lo ? me.x : 0.f, hi ? me.y : 0.f);
+      v[i] = pair(lo ? ve.x : 0.f, hi ? ve.y : 0.f);
+      r[i] = pair(lo ? re.x : 0.f, hi ? re.y : 0.f);
+    }
+  }
   if constexpr (BITS == 8) {
-    // what lies behind the tensor's end stays zero: its gradient was read as zero
     float mf = 0.f, vf = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

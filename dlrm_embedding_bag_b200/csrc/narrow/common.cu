@@ -20,13 +20,18 @@ int cuda_fail(cudaError_t e) {
 void note_launch(int n) { g_launches.fetch_add(n, std::memory_order_relaxed); }
 
 int sm_count_current() {
-  int dev = 0, n = 0;
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> known[kMaxDevices];  // a device's SMs do not change
+  int dev = -1, n = 0;
   cudaError_t e = cudaGetDevice(&dev);
+  const bool cacheable = e == cudaSuccess && dev >= 0 && dev < kMaxDevices;
+  if (cacheable && (n = known[dev].load(std::memory_order_relaxed)) != 0) return n;
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) {
     cuda_fail(e);
     return 0;
   }
+  if (cacheable) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 

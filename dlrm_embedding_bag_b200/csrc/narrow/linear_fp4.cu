@@ -18,7 +18,7 @@
 //     warp store 32 neighbouring channels of a token at any pitch. Few tiles: a
 //     cluster of S CTAs shares one tile, each summing a stretch of K, and the f32 parts
 //     meet through distributed shared memory in the order of the ranks.
-//   - CTA pairs (cta_group::2) of 256 x 256. Where rows of y start on 16 bytes the
+//   - CTA pairs (cta_group::2) of 256 x 256. Where rows of y are whole 16 bytes the
 //     tokens take the M side: a lane then has neighbouring channels of a token, lays
 //     them out in shared memory, and the copy engine writes whole lines. Two accumulators of 256 columns and
 //     the scales do not fit TMEM's 512, so the accumulators share 128 columns: those
@@ -221,7 +221,7 @@ __device__ __forceinline__ void put_tokens(const LinArgs& a, int row, float bias
 
 // b's rows b0 .. b0 + 63 (channels) of 32 rows of a from row0 on (tokens), one a lane: laid
 // out in shared memory as the map's 128-byte swizzle has it, and from there to y by the
-// copy engine, which leaves out what is past y's end. Rows of y start on 16 bytes. bias: of
+// copy engine, which leaves out what is past y's end. Rows of y are whole 16 bytes. bias: of
 // these channels, in shared memory.
 template <int ACT, class Out>
 __device__ __forceinline__ void put_channels(const LinArgs& a, const CUtensorMap* y, uint8_t* out,
@@ -983,7 +983,7 @@ struct Form {
   int rows_m, rows_n;  // of a tile: channels and tokens
   int units;           // of 148 SMs that walk tiles: all, or pairs
   int split;
-  bool lines;          // whether it needs rows of y on 16 bytes
+  bool lines;          // whether it needs rows of y that start and end on 16 bytes
   double step, tile, once;
   cudaError_t (*run)(const Operands&, LinArgs, int, cudaStream_t);
 };
@@ -1015,7 +1015,8 @@ cudaError_t launch_linear(const Operands& op, const LinArgs& args, int sms, cuda
     return many ? run_one<2, 4>(a, s) : run_one<4, 1>(a, s);
   }
   const int size = args.y_bf16 ? 2 : 4;
-  const bool lines = is_aligned(args.y, 16) && args.ldy * size % 16 == 0;
+  // whole 16 bytes of a row: the copy engine's stores were seen to end on those, not on elements
+  const bool lines = is_aligned(args.y, 16) && args.ldy * size % 16 == 0 && op.N * size % 16 == 0;
   const Form* best = nullptr;
   double least = 0;
   for (const Form& f : kForms) {

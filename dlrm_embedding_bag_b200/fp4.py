@@ -55,14 +55,20 @@ def _codes(t: torch.Tensor, name: str, index: Optional[int]) -> Tuple[int, int, 
             (index is not None and t.get_device() != index):
         _on(t, name, index)
         raise TypeError(f"{name} must be torch.uint8 (got {t.dtype})")
+    if t.dim() == 2:  # what fp4_empty makes, without a closer look
+        (rows, cols), (pitch, step) = t.shape, t.stride()
+        if step == 1 and rows > 1 and pitch >= cols:
+            return rows, cols, pitch
     return _pitch(t, name)
 
 
 def _tiles(t: torch.Tensor, name: str, rows: int, cols: int, index: int) -> int:
-    p = _flat(t, name, torch.uint8, index)
-    if t.shape != scale_shape(rows, cols):
-        raise ValueError(f"{name} must be {scale_shape(rows, cols)} (got {tuple(t.shape)})")
-    return p
+    """Pointer of the scale tiles of a ``(rows, cols)`` matrix on device ``index``."""
+    if isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype is torch.uint8 \
+            and t.is_contiguous() and t.shape == ((rows + 127) >> 7, (cols + 127) >> 7, 512):
+        return t.data_ptr()
+    _flat(t, name, torch.uint8, index)
+    raise ValueError(f"{name} must be {scale_shape(rows, cols)} (got {tuple(t.shape)})")
 
 
 def quantize_rows(x: torch.Tensor, *, out: Optional[torch.Tensor] = None,

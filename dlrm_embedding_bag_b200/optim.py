@@ -139,7 +139,7 @@ def adamw_state(params: Sequence[torch.Tensor], *, bits: int = 32,
     at, total = arena_offsets(params)
     step = torch.zeros(2, dtype=torch.int32, device=dev)
     copies = None
-    if master:
+    if master and any(p.dtype == torch.bfloat16 for p in params):
         copies = torch.zeros(total, dtype=torch.float32, device=dev)
         for o, p in zip(at, params):
             if p.dtype == torch.bfloat16:
@@ -191,12 +191,14 @@ def _list(tensors: Sequence[torch.Tensor], name: str, index: int):
 
 
 def _arena(t: Optional[torch.Tensor], name: str, dtype: torch.dtype, n: int, index: int) -> int:
+    """Pointer of a contiguous tensor of ``n`` elements of ``dtype`` on device ``index``."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.numel() == n \
+            and t.get_device() == index and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     if t is None:
         raise ValueError(f"{name} is missing")
-    p = _flat(t, name, dtype, index)
-    if t.numel() != n:
-        raise ValueError(f"{name} must have {n} elements (got {t.numel()})")
-    return p
+    _flat(t, name, dtype, index)
+    raise ValueError(f"{name} must have {n} elements (got {t.numel()})")
 
 
 def _eight_bit(state: AdamWState) -> bool:
@@ -233,14 +235,16 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], st
         raise ValueError(f"grads must have {n} entries (got {len(grads)})")
     pp, pc = _list(params, "params", index)
     pg, gc = _list(grads, "grads", index)
+    if len(set(pp)) != n:  # (empty ones have no address)
+        i = next((i for i in range(n) if pp[i] and pp[i] in pp[:i]), None)
+        if i is not None:
+            raise ValueError(f"params[{i}] is there twice")
     if list(map(_shape_of, params)) != list(map(_shape_of, grads)):
         i = next(i for i in range(n) if params[i].shape != grads[i].shape)
         raise ValueError(f"grads[{i}] must be {tuple(params[i].shape)} (got {tuple(grads[i].shape)})")
     counts = array("q", map(_length, params))
     total = sum([(c + BLOCK - 1) // BLOCK for c in counts]) * BLOCK
-    ps = _flat(state.step, "state.step", torch.int32, index)
-    if state.step.numel() != 2:
-        raise ValueError("state.step must have two elements")
+    ps = _arena(state.step, "state.step", torch.int32, 2, index)
     if _eight_bit(state):
         bits = 8
         pm = _arena(state.m, "state.m", torch.float8_e4m3fn, total, index)

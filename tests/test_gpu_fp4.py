@@ -240,7 +240,8 @@ LAYERS = [(1, 32, 1), (1, 4096, 300), (2, 77, 130), (3, 1000, 257), (4, 5000, 64
           (5, 4096, 512), (17, 2048, 512), (64, 64, 128), (65, 96, 129), (100, 592, 512),
           (128, 8192, 128), (200, 300, 1000), (777, 1001, 1234), (2048, 592, 512), (33, 13, 512),
           (2048, 13, 512), (2048, 256, 1), (1500, 2500, 1700), (4096, 700, 4096),
-          (5000, 1300, 3000), (20000, 64, 300), (260, 520, 20000)]
+          (5000, 1300, 3000), (20000, 64, 300), (260, 520, 20000), (1, 4096, 9000), (1, 2000, 17),
+          (1, 1500, 5001), (1, 9000, 300), (7000, 100, 1001)]
 
 
 @pytest.mark.parametrize("shape", LAYERS, ids=lambda s: "x".join(map(str, s)))
@@ -279,6 +280,18 @@ def test_outputs_with_a_pitch(fp4, m):
         y = fp4.linear_fp4(*ops, "relu", out=buf[:, 5:338])
         assert torch.equal(y, fp4.linear_fp4(*ops, "relu", out_dtype=dtype))
         assert (buf[:, :5] == 9).all() and (buf[:, 338:] == 9).all()
+
+
+@pytest.mark.parametrize("m,n", [(3000, 2000), (3001, 2011), (4000, 1999)])
+def test_large_outputs_with_a_pitch(fp4, m, n):
+    """Tiles on their way out as whole lines stop at the output's last column and row."""
+    g = _gen(16)
+    ops = _layer(fp4, g, m, 300, n, True)
+    for dtype in (F32, BF16):
+        buf = torch.full((m + 5, 2048), 9.0, device=DEV, dtype=dtype)
+        y = fp4.linear_fp4(*ops, "relu", out=buf[:m, 8:8 + n])
+        _check_layer(fp4, y, *ops, "relu")
+        assert (buf[:, :8] == 9).all() and (buf[:, 8 + n:] == 9).all() and (buf[m:] == 9).all()
 
 
 @pytest.mark.parametrize("m", [1, 3, 60, 1000])
@@ -362,6 +375,39 @@ def test_captured_and_replayed(fp4):
             graph.replay()
             want = fp4.linear_fp4(*fp4.quantize_rows(x), w, ws, act="relu")
             assert torch.equal(y, want)
+
+
+def test_first_calls_under_capture():
+    """A process whose first calls are captured: nothing in them that a capture refuses."""
+    import os
+    import subprocess
+    import sys
+
+    code = """
+import torch
+from dlrm_embedding_bag_b200 import fp4, optim
+x = [torch.randn((m, 512), device="cuda") for m in (1, 70, 3000)]
+w = torch.randn((3000, 512), device="cuda")
+p = torch.randn(5000, device="cuda")
+st = optim.adamw_state([p], bits=8)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    wq, ws = fp4.quantize_rows(w)
+    ys = [fp4.linear_fp4(*fp4.quantize_rows(t), wq, ws) for t in x]
+    optim.adamw_step([p], [p.clone()], st, lr=1e-3)
+    v = fp4.dequantize_rows(wq, ws)
+    m = optim.adamw_moments(st)
+g.replay()
+torch.cuda.synchronize()
+for t, y in zip(x, ys):
+    assert torch.equal(y, fp4.linear_fp4(*fp4.quantize_rows(t), wq, ws))
+assert st.step.tolist() == [1, 0]
+print("fine")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "fine", r.stdout + r.stderr
 
 
 def test_at_the_same_time(fp4):

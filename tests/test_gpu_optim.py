@@ -303,6 +303,24 @@ def test_bf16_weights_at_the_ends(optim):
     assert p[2].isnan() and p[5] == 0
 
 
+@pytest.mark.parametrize("bits", [8, 32])
+def test_what_lies_behind_a_tensor_stays_zero(optim, bits):
+    """Also where the clipping coefficient is not a number."""
+    params = [torch.ones(3, device=DEV), torch.ones(700, device=DEV, dtype=BF16)]
+    st = optim.adamw_state(params, bits=bits, master=True)
+    bad = torch.full((1,), float("nan"), device=DEV)
+    optim.adamw_step(params, [torch.ones_like(p) for p in params], st, lr=1e-3, grad_scale=bad)
+    assert all(p.isnan().all() for p in params)
+    for flat in (st.m, st.v, st.master):
+        if flat.dtype == torch.float8_e4m3fn:
+            flat = flat.view(torch.uint8)
+        assert (_padding(optim, params, flat) == 0).all()
+
+
+def test_masters_of_f32_parameters_are_not_made(optim):
+    assert optim.adamw_state([torch.zeros(3, device=DEV)], master=True).master is None
+
+
 # ---- lists, layouts, streams, graphs ------------------------------------------------------
 
 
@@ -368,6 +386,11 @@ def test_refusals_on_the_device(optim):
         optim.adamw_step([p], [p.half()], st, lr=1.0)
     with pytest.raises(ValueError, match="CUDA device"):
         optim.adamw_step([p], [p.cpu()], st, lr=1.0)
+    st2 = optim.adamw_state([p, p])
+    with pytest.raises(ValueError, match=r"params\[1\] is there twice"):
+        optim.adamw_step([p, p], [p.clone(), p.clone()], st2, lr=1.0)
+    with pytest.raises(TypeError, match=r"grads\[0\] must be a torch.Tensor"):
+        optim.adamw_step([p], [None], st, lr=1.0)
     with pytest.raises(optim.NarrowError, match="DLRM_ERR_ARG"):
         optim.adamw_step([p], [p.clone()], st, lr=1.0, eps=0.0)
     with pytest.raises(optim.NarrowError, match="DLRM_ERR_ARG"):

@@ -221,6 +221,9 @@ def _pretend(optim, monkeypatch):
     monkeypatch.setattr(optim, "_flat", lambda t, name, dtype, index: (
         t.data_ptr() if t.dtype == dtype and t.is_contiguous()
         else (_ for _ in ()).throw(TypeError(f"{name} must be {dtype}"))))
+    monkeypatch.setattr(optim, "_arena", lambda t, name, dtype, n, index: (
+        optim._flat(t, name, dtype, index) if t is not None and t.numel() == n
+        else (_ for _ in ()).throw(ValueError(f"{name} must have {n}"))))
     monkeypatch.setattr(optim, "_call", lambda fn, name, index, args: seen.append((name, args)))
     return seen
 
@@ -243,7 +246,7 @@ def test_step_lists_are_checked(optim, monkeypatch):
             (dict(params=[params[0], torch.zeros(7, dtype=torch.float16)]), r"params\[1\] must be float32"),
             (dict(st=st._replace(m=zeros(256))), "state.m must have 512"),
             (dict(st=st._replace(v=zeros(768))), "state.v must have 512"),
-            (dict(st=st._replace(step=torch.zeros(1, dtype=torch.int32))), "two elements"),
+            (dict(st=st._replace(step=torch.zeros(1, dtype=torch.int32))), "state.step must have 2"),
             (dict(st=st._replace(master=zeros(22))), "state.master must have 512"),
             (dict(weight_decay=(0.1,)), "weight_decay must have 2"),
             (dict(lr=zeros(2)), "lr must have 1"),
