@@ -6,9 +6,9 @@
 // value in the launch (up to kMaxTensors of them), so a network's dozens of small
 // tensors are one launch and need no copy in front of it.
 //
-// A warp takes a block of 256 elements, a lane four neighbours in either half, so
-// that every access of a warp is whole lines (512 bytes of f32, 128 of codes)
-// and a block's largest moment is one warp reduction. Four warps take a chunk of 1024.
+// A warp takes a block of 256 elements, a lane eight neighbours, so that its accesses are
+// few and wide (16 bytes of bf16, 8 of codes) and a block's largest moment is one warp
+// reduction. Four warps take a chunk of 1024.
 // CTAs stay, and chunks are handed out in order by a counter: walking with a fixed
 // stride, CTAs drift apart and memory sees a wider and wider window of addresses (10^6 x
 // 64 f32 with 32-bit moments 294 us, with 8-bit ones 178; by tickets 262 and 156).
@@ -124,35 +124,43 @@ __device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
   return r;
 }
 
-// 4 elements at p.
+// 8 elements at p.
 template <class T, bool ALL>
-__device__ __forceinline__ void load4(const T* p, int left, Pair* v) {
+__device__ __forceinline__ void load8(const T* p, int left, Pair* v) {
   if constexpr (ALL && sizeof(T) == 4) {
-    const float4 r = *reinterpret_cast<const float4*>(p);
-    v[0] = pair(r.x, r.y), v[1] = pair(r.z, r.w);
-  } else if constexpr (ALL) {
-    const uint2 r = *reinterpret_cast<const uint2*>(p);
-    v[0] = pair(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u));
-    v[1] = pair(__uint_as_float(r.y << 16), __uint_as_float(r.y & 0xffff0000u));
-  } else {
-    float e[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) e[i] = i < left ? static_cast<float>(p[i]) : 0.f;
-    v[0] = pair(e[0], e[1]), v[1] = pair(e[2], e[3]);
+    for (int i = 0; i < 2; ++i) {
+      const float4 r = reinterpret_cast<const float4*>(p)[i];
+      v[2 * i] = pair(r.x, r.y), v[2 * i + 1] = pair(r.z, r.w);
+    }
+  } else if constexpr (ALL) {
+    const uint4 r = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v[i] = pair(2 * i < left ? static_cast<float>(p[2 * i]) : 0.f,
+                  2 * i + 1 < left ? static_cast<float>(p[2 * i + 1]) : 0.f);
   }
 }
 
 template <class T, bool ALL>
-__device__ __forceinline__ void store4(T* p, int left, const Pair* v) {
-  const float2 a = parts(v[0]), b = parts(v[1]);
-  if constexpr (ALL && sizeof(T) == 4) {
-    *reinterpret_cast<float4*>(p) = make_float4(a.x, a.y, b.x, b.y);
-  } else if constexpr (ALL) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(bf16_pair(a.x, a.y), bf16_pair(b.x, b.y));
-  } else {
-    const float e[4] = {a.x, a.y, b.x, b.y};
+__device__ __forceinline__ void store8(T* p, int left, const Pair* v) {
+  float e[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = parts(v[i]);
+    e[2 * i] = f.x, e[2 * i + 1] = f.y;
+  }
+  if constexpr (ALL) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 16 / sizeof(T)) store_16_bytes(p + i, e + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
       if (i < left) p[i] = static_cast<T>(e[i]);
   }
 }
@@ -236,7 +244,7 @@ template <int BITS, class P, class G, bool ALL>
 __device__ __forceinline__ void step_block(const StepArgs& a, const Factors& f, const Tensor& t,
                                            int64_t e0, int left) {
   const int lane = threadIdx.x & 31;
-  const int q[2] = {lane * 4, 128 + lane * 4};  // the lane's places in the block
+  const int q[2] = {lane * 8, lane * 8 + 4};  // the lane's places in the block
   const uint32_t block = t.block0 + static_cast<uint32_t>(e0 / kBlock);
   const int64_t at = static_cast<int64_t>(block) * kBlock;
   P* param = static_cast<P*>(t.param) + e0;
@@ -246,20 +254,18 @@ __device__ __forceinline__ void step_block(const StepArgs& a, const Factors& f, 
   Pair p[4], g[4], m[4], v[4];
   uint32_t mc[2], vc[2];
   float ms = 1.f, vs = 1.f;  // the scales of what was read
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    load4<G, ALL>(grad + q[h], left - q[h], g + 2 * h);
-    if (whole)
-      load4<float, true>(a.master + at + q[h], 4, p + 2 * h);
-    else
-      load4<P, ALL>(param + q[h], left - q[h], p + 2 * h);
-    if constexpr (BITS == 8) {
-      mc[h] = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.m) + at + q[h]);
-      vc[h] = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(a.v) + at + q[h]);
-    } else {
-      load4<float, true>(static_cast<const float*>(a.m) + at + q[h], 4, m + 2 * h);
-      load4<float, true>(static_cast<const float*>(a.v) + at + q[h], 4, v + 2 * h);
-    }
+  load8<G, ALL>(grad + q[0], left - q[0], g);
+  if (whole)
+    load8<float, true>(a.master + at + q[0], 8, p);
+  else
+    load8<P, ALL>(param + q[0], left - q[0], p);
+  if constexpr (BITS == 8) {
+    const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.m) + at + q[0]);
+    const uint2 y = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.v) + at + q[0]);
+    mc[0] = x.x, mc[1] = x.y, vc[0] = y.x, vc[1] = y.y;
+  } else {
+    load8<float, true>(static_cast<const float*>(a.m) + at + q[0], 8, m);
+    load8<float, true>(static_cast<const float*>(a.v) + at + q[0], 8, v);
   }
   // a random word for each element, while those are on their way
   uint32_t word[8];
@@ -267,7 +273,7 @@ __device__ __forceinline__ void step_block(const StepArgs& a, const Factors& f, 
     const uint32_t base = mixed(f.key ^ block) + static_cast<uint32_t>(q[0]) * 0x9E3779B9u;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      word[i] = mixed(base + static_cast<uint32_t>(i / 4 * 128 + i % 4) * 0x9E3779B9u);
+      word[i] = mixed(base + static_cast<uint32_t>(i) * 0x9E3779B9u);
   }
   if constexpr (BITS == 8) {
     ms = a.m_scale[block];
@@ -297,7 +303,7 @@ __device__ __forceinline__ void step_block(const StepArgs& a, const Factors& f, 
     // what lies behind the tensor's end stays zero, whatever the factors are
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int e = q[i / 2] + i % 2 * 2;
+      const int e = q[0] + 2 * i;
       const float2 pe = parts(p[i]), me = parts(m[i]), ve = parts(v[i]), re = parts(r[i]);
       const bool lo = e < left, hi = e + 1 < left;
       p[i] = pair(lo ? pe.x : 0.f, hi ? pe.y : 0.f);
@@ -349,46 +355,50 @@ __device__ __forceinline__ void step_block(const StepArgs& a, const Factors& f, 
         if (z.x > 0.f && (vc[h] & 0xff0000u) == 0) vc[h] |= 1u << 16;
         if (z.y > 0.f && (vc[h] & 0xff000000u) == 0) vc[h] |= 1u << 24;
       }
-      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.m) + at + q[h]) = live ? mc[h] : 0u;
-      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.v) + at + q[h]) = vbad ? 0u : vc[h];
     }
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.m) + at + q[0]) =
+        live ? make_uint2(mc[0], mc[1]) : make_uint2(0u, 0u);
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v) + at + q[0]) =
+        vbad ? make_uint2(0u, 0u) : make_uint2(vc[0], vc[1]);
     if (lane == 0) {
       const float nan = __uint_as_float(0x7fc00000u);
       a.m_scale[block] = mbad ? nan : live ? mf * (1.f / 448.f) : 0.f;
       a.v_scale[block] = vbad ? nan : vf * (1.f / 1.9375f);
     }
   } else {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      store4<float, true>(static_cast<float*>(a.m) + at + q[h], 4, m + 2 * h);
-      store4<float, true>(static_cast<float*>(a.v) + at + q[h], 4, v + 2 * h);
-    }
+    store8<float, true>(static_cast<float*>(a.m) + at + q[0], 8, m);
+    store8<float, true>(static_cast<float*>(a.v) + at + q[0], 8, v);
   }
+  if (whole) {
+    store8<float, true>(a.master + at + q[0], 8, p);
+  } else if constexpr (sizeof(P) == 2) {
+    uint32_t b[4];
+    float top = 0.f;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if (whole) {
-      store4<float, true>(a.master + at + q[h], 4, p + 2 * h);
-    } else if constexpr (sizeof(P) == 2) {
-      const float2 y = parts(p[2 * h]), z = parts(p[2 * h + 1]);
-      const uint32_t* w = word + 4 * h;
-      uint2 b = make_uint2(upper_halves(by_chance(y.x, w[0]), by_chance(y.y, w[1])),
-                           upper_halves(by_chance(z.x, w[2]), by_chance(z.y, w[3])));
-      const float top = max_abs(max_abs(0.f, y.x, y.y), z.x, z.y);
-      if (top != top)  // with a NaN among them: by the conversion that keeps it
-        b = make_uint2(upper_halves(y.x != y.x ? y.x : by_chance(y.x, w[0]), y.y != y.y ? y.y : by_chance(y.y, w[1])),
-                       upper_halves(z.x != z.x ? z.x : by_chance(z.x, w[2]), z.y != z.y ? z.y : by_chance(z.y, w[3])));
-      if constexpr (ALL) {
-        *reinterpret_cast<uint2*>(param + q[h]) = b;
-      } else {
-        uint16_t* at_p = reinterpret_cast<uint16_t*>(param + q[h]);
+    for (int i = 0; i < 4; ++i) {
+      const float2 y = parts(p[i]);
+      b[i] = upper_halves(by_chance(y.x, word[2 * i]), by_chance(y.y, word[2 * i + 1]));
+      top = max_abs(top, y.x, y.y);
+    }
+    if (top != top) {  // with a NaN among them: by the conversion that keeps it
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (q[h] + i < left) at_p[i] = static_cast<uint16_t>((i < 2 ? b.x : b.y) >> (16 * (i % 2)));
+      for (int i = 0; i < 4; ++i) {
+        const float2 y = parts(p[i]);
+        b[i] = upper_halves(y.x != y.x ? y.x : by_chance(y.x, word[2 * i]),
+                            y.y != y.y ? y.y : by_chance(y.y, word[2 * i + 1]));
       }
-      continue;
     }
-    store4<P, ALL>(param + q[h], left - q[h], p + 2 * h);
+    if constexpr (ALL) {
+      *reinterpret_cast<uint4*>(param + q[0]) = make_uint4(b[0], b[1], b[2], b[3]);
+    } else {
+      uint16_t* at_p = reinterpret_cast<uint16_t*>(param + q[0]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (q[0] + i < left) at_p[i] = static_cast<uint16_t>(b[i / 2] >> (16 * (i % 2)));
+    }
+    return;
   }
+  store8<P, ALL>(param + q[0], left - q[0], p);
 }
 
 template <int BITS, class P, class G>
