@@ -100,30 +100,6 @@ __device__ __forceinline__ uint32_t mixed(uint32_t x) {
   return x ^ (x >> 16);
 }
 
-// Two f32 as the pair that one instruction works on.
-using Pair = unsigned long long;
-__device__ __forceinline__ Pair pair(float lo, float hi) {
-  Pair r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ Pair both(float v) { return pair(v, v); }
-__device__ __forceinline__ float2 parts(Pair p) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(p));
-  return r;
-}
-__device__ __forceinline__ Pair mul(Pair a, Pair b) {
-  Pair r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
-  Pair r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
 // 8 elements at p.
 template <class T, bool ALL>
 __device__ __forceinline__ void load8(const T* p, int left, Pair* v) {
@@ -223,13 +199,6 @@ __device__ __forceinline__ float reciprocal(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// max(|a|, |b|, |c|), NaN if one is.
-__device__ __forceinline__ float max_abs(float a, float b, float c) {
-  float r;
-  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
 // Towards bf16 by chance: what a cut after the upper half makes of it goes up with the
 // probability of what is left over. (An infinity has nothing to carry; NaN is not given.)
 __device__ __forceinline__ float by_chance(float x, uint32_t word) {

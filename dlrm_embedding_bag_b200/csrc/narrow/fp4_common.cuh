@@ -16,12 +16,6 @@ __host__ __device__ inline int64_t fp4_scale_at(int64_t block_tiles, int row, in
          ((row >> 5) & 3) * 4 + (block & 3);
 }
 
-// 2^(E - 127); NaN for 255.
-__device__ __forceinline__ float fp4_scale_value(uint32_t byte) {
-  const uint32_t bits = byte == 255u ? 0x7fc00000u : byte == 0u ? 0x00400000u : byte << 23;
-  return __uint_as_float(bits);
-}
-
 // n / d by a product, for n * d < 2^64: with m = floor(2^64 / d) + 1, n m / 2^64 is
 // above n / d by less than 1 / d.
 struct Divisor {

@@ -46,13 +46,25 @@ __device__ __forceinline__ float inverse_of(uint32_t byte) {
   return __uint_as_float((254u - byte) << 23);
 }
 
-// Two elements as codes, the first in the low half of the byte.
-__device__ __forceinline__ uint32_t codes_of(float lo, float hi) {
-  uint16_t r;
-  asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\t"
-      "mov.b16 %0, {b, 0};\n\t}"
-      : "=h"(r)
-      : "f"(hi), "f"(lo));
+// Eight elements as codes, the first in the lowest four bits.
+__device__ __forceinline__ uint32_t codes_of(const Pair (&x)[4]) {
+  const float2 a = parts(x[0]), b = parts(x[1]), c = parts(x[2]), d = parts(x[3]);
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y), "f"(d.x), "f"(d.y));
+  return r;
+}
+
+// The larger magnitudes of two pairs of bf16, NaN if one is; the signs say nothing.
+__device__ __forceinline__ uint32_t max_abs_bf16(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
 
@@ -99,33 +111,40 @@ __device__ __forceinline__ void round_half_block(const QuantArgs& a, int row, in
                                                  bool in, const uint32_t (&w)[4 * sizeof(T)]) {
   constexpr int kWords = 4 * sizeof(T);
   const int c = block * 32 + half * 16;
-  uint32_t top = 0;
+  uint32_t top;
   if constexpr (sizeof(T) == 4) {
+    float t = 0.f;
 #pragma unroll
-    for (int k = 0; k < kWords; ++k) top = max(top, w[k] & 0x7fffffffu);
+    for (int k = 0; k < kWords; k += 2)
+      t = max_abs(t, __uint_as_float(w[k]), __uint_as_float(w[k + 1]));
+    top = __float_as_uint(t);
   } else {
-    uint32_t both = 0;
+    uint32_t two = w[0];
 #pragma unroll
-    for (int k = 0; k < kWords; ++k) both = __vmaxu2(both, w[k] & 0x7fff7fffu);
-    top = max(both & 0xffff0000u, both << 16);
+    for (int k = 1; k < kWords; ++k) two = max_abs_bf16(two, w[k]);
+    two &= 0x7fff7fffu;
+    top = max(two & 0xffff0000u, two << 16);
   }
   top = max(top, __shfl_xor_sync(kFull, top, 1));
   if (!in) return;
   const uint32_t byte = scale_byte(top);
   if (half == 0) a.scale[fp4_scale_at(a.block_tiles, row, block)] = static_cast<uint8_t>(byte);
   if (row >= a.M || c >= a.K) return;
-  const float inv = inverse_of(byte);
+  const Pair inv = both(inverse_of(byte));
   uint32_t out[2] = {};
   if (byte != 255u) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      float lo, hi;
-      if constexpr (sizeof(T) == 4) {
-        lo = __uint_as_float(w[2 * k]), hi = __uint_as_float(w[2 * k + 1]);
-      } else {
-        lo = __uint_as_float(w[k] << 16), hi = __uint_as_float(w[k] & 0xffff0000u);
+    for (int h = 0; h < 2; ++h) {
+      Pair x[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (sizeof(T) == 4)
+          x[k] = pair(__uint_as_float(w[8 * h + 2 * k]), __uint_as_float(w[8 * h + 2 * k + 1]));
+        else
+          x[k] = pair(__uint_as_float(w[4 * h + k] << 16), __uint_as_float(w[4 * h + k] & 0xffff0000u));
+        x[k] = mul(x[k], inv);
       }
-      out[k / 4] |= codes_of(lo * inv, hi * inv) << (8 * (k % 4));
+      out[h] = codes_of(x);
     }
   }
   uint8_t* q = a.q + row * a.ldq + c / 2;
@@ -208,10 +227,37 @@ struct DequantArgs {
   Divisor by;  // groups
 };
 
-// The code in the upper four bits of t, whatever lies below them: its sign, then exponent and
-// mantissa as an f32's, whose bias 2^126 corrects.
-__device__ __forceinline__ float value_of(uint32_t t, float scale) {
-  return __uint_as_float((t & 0x80000000u) | (t >> 6 & 0x01c00000u)) * 0x1p126f * scale;
+// Sixteen codes (two words) times their scale as T, rounded once, eight words of bf16 or
+// sixteen of f32. Four codes at a time are looked up as bf16 numbers, whose upper and lower
+// bytes are one byte permutation each; the scale is a power of two, so that the
+// product in bf16 is as exact as one in f32.
+template <class T>
+__device__ __forceinline__ void values_of(const uint32_t (&codes)[2], uint32_t byte,
+                                          uint32_t (&v)[4 * sizeof(T)]) {
+  const uint32_t scale_bits = byte == 0u ? 0x00400000u : byte == 255u ? 0x7fc00000u : byte << 23;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t c = codes[i / 2] >> (16 * (i % 2));
+    const uint32_t at = c & 0x7777u;
+    uint32_t signs;  // bytes of 0x80, or 0xff where a code's sign bit is set
+    asm("prmt.b32 %0, %1, %1, %2;" : "=r"(signs) : "r"(0x80808080u), "r"(c));
+    // 0, 0.5, 1, 1.5 and 2, 3, 4, 6
+    const uint32_t hi = __byte_perm(0x3f3f3f00u, 0x40404040u, at) | (signs << 1 & 0x80808080u);
+    const uint32_t lo = __byte_perm(0xc0800000u, 0xc0804000u, at);
+    uint32_t two[2] = {__byte_perm(lo, hi, 0x5140), __byte_perm(lo, hi, 0x7362)};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if constexpr (sizeof(T) == 2) {
+        asm("mul.rn.bf16x2 %0, %1, %2;"
+            : "=r"(v[2 * i + h])
+            : "r"(two[h]), "r"(scale_bits >> 16 | (scale_bits & 0xffff0000u)));
+      } else {
+        const float2 f = parts(mul(pair(__uint_as_float(two[h] << 16), __uint_as_float(two[h] & 0xffff0000u)),
+                                   both(__uint_as_float(scale_bits))));
+        v[4 * i + 2 * h] = __float_as_uint(f.x), v[4 * i + 2 * h + 1] = __float_as_uint(f.y);
+      }
+    }
+  }
 }
 
 template <class T, bool SECTORS>
@@ -221,19 +267,18 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const DequantArgs 
   const int64_t row = a.by.of(i);
   if (row >= a.M) return;
   const int c = static_cast<int>(i - row * a.groups) * 16;
-  const float scale =
-      fp4_scale_value(a.scale[fp4_scale_at(a.block_tiles, static_cast<int>(row), c / 32)]);
-  const uint2 w = *reinterpret_cast<const uint2*>(a.q + row * a.ldq + c / 2);
-  float v[16];
-#pragma unroll
-  for (int e = 0; e < 16; ++e) v[e] = value_of((e < 8 ? w.x : w.y) << (28 - 4 * (e % 8)), scale);
+  const uint32_t byte = a.scale[fp4_scale_at(a.block_tiles, static_cast<int>(row), c / 32)];
+  const uint2 r = *reinterpret_cast<const uint2*>(a.q + row * a.ldq + c / 2);
+  const uint32_t codes[2] = {r.x, r.y};
+  uint32_t v[4 * sizeof(T)];
+  values_of<T>(codes, byte, v);
   T* y = static_cast<T*>(a.y) + row * a.ldy + c;
-  constexpr int V = kVecOf<T>;
   if constexpr (SECTORS) {
-    store_sectors(y, v);
+    store_sector_words(y, v);
   } else {
 #pragma unroll
-    for (int e = 0; e < 16; e += V) store_16_bytes(y + e, v + e);
+    for (int i = 0; i < static_cast<int>(sizeof(T)); ++i)
+      reinterpret_cast<uint4*>(y)[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
   }
 }
 
@@ -247,10 +292,9 @@ __global__ void __launch_bounds__(kThreads) dequantize_staged_kernel(const Dequa
   const int c0 = static_cast<int>(unit - row * a.groups) * 16 * G;
   const int c = c0 + 16 * in;
   const int left = row < a.M ? a.K - c0 : 0;
-  uint32_t w[2] = {};
-  float scale = 0.f;
+  uint32_t w[2] = {}, byte = 0;
   if (row < a.M && c < a.K) {
-    scale = fp4_scale_value(a.scale[fp4_scale_at(a.block_tiles, static_cast<int>(row), c / 32)]);
+    byte = a.scale[fp4_scale_at(a.block_tiles, static_cast<int>(row), c / 32)];
     const uint8_t* q = a.q + row * a.ldq + c / 2;
     const int bytes = (a.K - c + 1) / 2;
     if (bytes >= 8 && (reinterpret_cast<uintptr_t>(q) & 7) == 0) {
@@ -262,13 +306,13 @@ __global__ void __launch_bounds__(kThreads) dequantize_staged_kernel(const Dequa
         if (k < bytes) w[k / 4] |= static_cast<uint32_t>(q[k]) << (8 * (k % 4));
     }
   }
-  float v[16];
-#pragma unroll
-  for (int e = 0; e < 16; ++e) v[e] = value_of(w[e / 8] << (28 - 4 * (e % 8)), scale);
+  uint32_t v[4 * sizeof(T)];
+  values_of<T>(w, byte, v);
   T* mine = staged[threadIdx.x >> 5].v + lane / G * (G * Staged<T>::kLane);
-  constexpr int V = kVecOf<T>;
+  uint4* own = reinterpret_cast<uint4*>(mine + Staged<T>::at(16 * in));
 #pragma unroll
-  for (int e = 0; e < 16; e += V) store_16_bytes(mine + Staged<T>::at(16 * in) + e, v + e);
+  for (int i = 0; i < static_cast<int>(sizeof(T)); ++i)
+    own[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
   __syncwarp();
   T* y = static_cast<T*>(a.y) + row * a.ldy + c0 + in;
 #pragma unroll
