@@ -49,6 +49,9 @@ constexpr int kEpiWarps = 8;
 constexpr int kScaleWarp = 2 + kEpiWarps;  // the first of the four that carry scales
 constexpr int kThreads = 32 * (kScaleWarp + 4);
 constexpr long long kWaitLimit = 200000000LL;  // clock cycles, about 0.1 s
+// What a wait for a whole tile's products may take besides, for each of its stages (which
+// take 300 to 800 cycles): 2^22 stages of a K of 2^30 are more than the limit above.
+constexpr long long kStageLimit = 10000;
 constexpr int kMaxDevices = 64;                // devices whose launch set-up is cached
 
 constexpr int kBand = 8;  // tiles of b that are walked together
@@ -617,7 +620,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         fetch_bias(t + unit_step);
       }
-      if (!__all_sync(kFull, mbar_wait_bounded(&acc_full[b], (j >> 1) & 1, kWaitLimit))) {
+      if (!__all_sync(kFull, mbar_wait_bounded(&acc_full[b], (j >> 1) & 1,
+                                               kWaitLimit + (kb_end - kb_begin) * kStageLimit))) {
         timed_out = true;
         break;
       }
@@ -636,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_32x32b_x32(tq + c + h, *reinterpret_cast<float(*)[32]>(v + h));
         if (R::kLap != 0 && i == 0) arrive(lap_empty);
         if (i == kSteps - 1) arrive(&acc_empty[b]);
-if constexpr (TOKENS_M) {
+        if constexpr (TOKENS_M) {
           by_kind(args, PutChannels{args, &maps.y, smem + R::kOut + ew * kOutBytes, row - lane,
                                     b0 + c, lane, slice + step * kAtOnce, v});
         } else {

@@ -444,6 +444,18 @@ def test_rows_beyond_32_bits(fp4):
         assert torch.equal(fp4.dequantize_rows(one, so, dtype=BF16), v[r:r + 1])
 
 
+def test_a_row_whose_products_take_longer_than_a_wait(fp4):
+    # ones: every partial sum is a multiple of 64 up to 2^30, which f32 holds
+    k = 1 << 30
+    q = torch.full((2, k // 2), 0x22, device=DEV, dtype=torch.uint8)
+    scale = torch.zeros(fp4.scale_shape(2, k), device=DEV, dtype=torch.uint8)
+    scale[:, :, :4] = 127
+    scale[:, :, 16:20] = 127
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    y = fp4.linear_fp4(q, scale, q, scale, status=status)
+    assert status.item() == 0 and (y == float(k)).all()
+
+
 # ---- networks -----------------------------------------------------------------------------------
 
 
