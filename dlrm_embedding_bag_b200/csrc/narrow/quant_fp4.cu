@@ -7,9 +7,13 @@
 // do not vanish, and then the code is 0), so a code is one rounding of its element.
 //
 // A thread takes half a block, 16 elements, and a block's two threads exchange their
-// maxima. Where rows start on 16 bytes it reads them in accesses of 16 or 32 bytes.
-// Elsewhere lanes read neighbouring elements of a row, whole lines, and lay them out in
-// shared memory from where each takes its own 16; values go back the same way.
+// maxima. Where rows start on 16 bytes it reads them in accesses of 16 or 32 bytes (16384 x
+// 4096 bf16 28.8 us of 25.9 by their bytes; values back 28.1 of 25.9). bf16 rows that start
+// anywhere it reads as the 64-bit words around them and moves those down (60000 x 1001 37.7 us of
+// 23.2; by neighbouring elements through shared memory 43.8). f32 rows that start anywhere lanes
+// read by neighbouring elements, whole lines, and lay them out in shared memory from
+// where each takes its own 16 (45.3 us of 41.5); values go back the same way, or in
+// aligned words of the row (below).
 #include <algorithm>
 #include <climits>
 
@@ -26,6 +30,7 @@ constexpr uint32_t kInfBits = 0x7f800000u;
 
 struct QuantArgs {
   const void* x;
+  const void* end;  // behind the last row's last element
   uint8_t* q;
   uint8_t* scale;
   int64_t ldx, ldq, block_tiles;
@@ -103,6 +108,38 @@ __device__ __forceinline__ void load_half_block(const T* p, int left, uint32_t (
   }
 }
 
+// The same of bf16 rows that start anywhere: the five 64-bit words of the matrix around the 16
+// elements (some of them its neighbours' too, from L1), moved down by their start. Where
+// those reach past the matrix, and only there, element by element.
+__device__ __forceinline__ void load_half_block_anywhere(const QuantArgs& a, const __nv_bfloat16* p,
+                                                         int left, uint32_t (&w)[8]) {
+  const uint32_t off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p)) & 7;  // even
+  const uint2* words = reinterpret_cast<const uint2*>(reinterpret_cast<uintptr_t>(p) - off);
+  if (words >= a.x && words + 5 <= a.end) {
+    uint32_t v[10];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+      const uint2 r = words[i];
+      v[2 * i] = r.x, v[2 * i + 1] = r.y;
+    }
+#pragma unroll
+    for (int k = 0; k < 9; ++k) v[k] = off & 4 ? v[k + 1] : v[k];
+    const uint32_t which = off & 2 ? 0x5432 : 0x3210;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) w[k] = __byte_perm(v[k], v[k + 1], which);
+    if (left < 16) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        w[k] &= (2 * k < left ? 0xffffu : 0u) | (2 * k + 1 < left ? 0xffff0000u : 0u);
+    }
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < 16; ++k)
+    if (k < left)
+      w[k / 2] |= static_cast<uint32_t>(reinterpret_cast<const uint16_t*>(p)[k]) << (16 * (k % 2));
+}
+
 // A thread's half block: its words rounded, codes and (a block's first thread) the scale
 // written. Every lane of a warp comes here; in: whether the row has such a block, or a
 // scale tile has it beside the row's.
@@ -157,6 +194,7 @@ __device__ __forceinline__ void round_half_block(const QuantArgs& a, int row, in
   }
 }
 
+// BYTES: of an access that rows allow; 2: bf16 rows that start anywhere.
 template <class T, int BYTES>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -167,8 +205,13 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantArgs a) {
   const int half = static_cast<int>(i & 1);
   const int c = block * 32 + half * 16;
   uint32_t w[4 * sizeof(T)] = {};
-  if (row < a.M && c < a.K)
-    load_half_block<T, BYTES>(static_cast<const T*>(a.x) + row * a.ldx + c, a.K - c, w);
+  if (row < a.M && c < a.K) {
+    const T* p = static_cast<const T*>(a.x) + row * a.ldx + c;
+    if constexpr (BYTES == 2)
+      load_half_block_anywhere(a, p, a.K - c, w);
+    else
+      load_half_block<T, BYTES>(p, a.K - c, w);
+  }
   round_half_block<T>(a, row, block, half, row < a.rows, w);
   // the last block's thread ends the scale tile's four
   if (half == 0 && row < a.rows && block == a.blocks - 1)
@@ -227,14 +270,14 @@ struct DequantArgs {
   Divisor by;  // groups
 };
 
-// Sixteen codes (two words) times their scale as T, rounded once, eight words of bf16 or
-// sixteen of f32. Four codes at a time are looked up as bf16 numbers, whose upper and lower
-// bytes are one byte permutation each; the scale is a power of two, so that the
-// product in bf16 is as exact as one in f32.
-template <class T>
-__device__ __forceinline__ void values_of(const uint32_t (&codes)[2], uint32_t byte,
-                                          uint32_t (&v)[4 * sizeof(T)]) {
-  const uint32_t scale_bits = byte == 0u ? 0x00400000u : byte == 255u ? 0x7fc00000u : byte << 23;
+// What a scale byte stands for, as the bits of f32 (its upper half those of bf16).
+__device__ __forceinline__ uint32_t scale_bits(uint32_t byte) {
+  return byte == 0u ? 0x00400000u : byte == 255u ? 0x7fc00000u : byte << 23;
+}
+
+// Sixteen codes (two words) as pairs of bf16 numbers without their scales: four at a time
+// are looked up, whose upper and lower bytes are one byte permutation each.
+__device__ __forceinline__ void pairs_of(const uint32_t (&codes)[2], uint32_t (&two)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t c = codes[i / 2] >> (16 * (i % 2));
@@ -244,18 +287,31 @@ __device__ __forceinline__ void values_of(const uint32_t (&codes)[2], uint32_t b
     // 0, 0.5, 1, 1.5 and 2, 3, 4, 6
     const uint32_t hi = __byte_perm(0x3f3f3f00u, 0x40404040u, at) | (signs << 1 & 0x80808080u);
     const uint32_t lo = __byte_perm(0xc0800000u, 0xc0804000u, at);
-    uint32_t two[2] = {__byte_perm(lo, hi, 0x5140), __byte_perm(lo, hi, 0x7362)};
+    two[2 * i] = __byte_perm(lo, hi, 0x5140), two[2 * i + 1] = __byte_perm(lo, hi, 0x7362);
+  }
+}
+// Products of two bf16 numbers and powers of two: as exact as in f32.
+__device__ __forceinline__ uint32_t scaled(uint32_t two, uint32_t scales) {
+  uint32_t r;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(two), "r"(scales));
+  return r;
+}
+
+// Sixteen codes times their scale as T, rounded once, eight words of bf16 or sixteen of f32.
+template <class T>
+__device__ __forceinline__ void values_of(const uint32_t (&codes)[2], uint32_t byte,
+                                          uint32_t (&v)[4 * sizeof(T)]) {
+  const uint32_t scale = scale_bits(byte);
+  uint32_t two[8];
+  pairs_of(codes, two);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if constexpr (sizeof(T) == 2) {
-        asm("mul.rn.bf16x2 %0, %1, %2;"
-            : "=r"(v[2 * i + h])
-            : "r"(two[h]), "r"(scale_bits >> 16 | (scale_bits & 0xffff0000u)));
-      } else {
-        const float2 f = parts(mul(pair(__uint_as_float(two[h] << 16), __uint_as_float(two[h] & 0xffff0000u)),
-                                   both(__uint_as_float(scale_bits))));
-        v[4 * i + 2 * h] = __float_as_uint(f.x), v[4 * i + 2 * h + 1] = __float_as_uint(f.y);
-      }
+  for (int i = 0; i < 8; ++i) {
+    if constexpr (sizeof(T) == 2) {
+      v[i] = scaled(two[i], scale >> 16 | scale);
+    } else {
+      const float2 f = parts(mul(pair(__uint_as_float(two[i] << 16), __uint_as_float(two[i] & 0xffff0000u)),
+                                 both(__uint_as_float(scale))));
+      v[2 * i] = __float_as_uint(f.x), v[2 * i + 1] = __float_as_uint(f.y);
     }
   }
 }
@@ -279,6 +335,71 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const DequantArgs 
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(T)); ++i)
       reinterpret_cast<uint4*>(y)[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+  }
+}
+
+// Eight bytes of a row's codes from byte `at` on (a multiple of 8, negative in front of the
+// row). WHOLE: rows start on 8 bytes; what lies between a row's codes and the next one may
+// come with them.
+template <bool WHOLE>
+__device__ __forceinline__ uint2 load_16_codes(const DequantArgs& a, int64_t row, int at) {
+  const int bytes = (a.K + 1) / 2;
+  if (at < 0 || at >= bytes) return make_uint2(0, 0);
+  const uint8_t* q = a.q + row * a.ldq + at;
+  if (WHOLE && (at + 8 <= bytes || row < a.M - 1)) return *reinterpret_cast<const uint2*>(q);
+  uint32_t w[2] = {};
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (at + k < bytes) w[k / 4] |= static_cast<uint32_t>(q[k]) << (8 * (k % 4));
+  return make_uint2(w[0], w[1]);
+}
+
+// bf16 rows that start anywhere: a thread takes the row's part of 32 aligned bytes of y, 16
+// columns that may begin inside a half block and lie in two blocks.
+template <bool WHOLE>
+__global__ void __launch_bounds__(kThreads) dequantize_anywhere_kernel(const DequantArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  const int64_t row = a.by.of(i);
+  if (row >= a.M) return;
+  __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + row * a.ldy;
+  const int before = static_cast<int>(reinterpret_cast<uintptr_t>(y) & 31) / 2;
+  const int c = static_cast<int>(i - row * a.groups) * 16 - before;
+  if (c >= a.K) return;
+  const int c16 = c & ~15;
+  const uint2 lo = load_16_codes<WHOLE>(a, row, c16 / 2);
+  const uint2 hi = load_16_codes<WHOLE>(a, row, c16 / 2 + 8);
+  const int block = c >> 5, cut = 32 - (c & 31);  // columns of the first block
+  const uint32_t b0 = block >= 0 ? a.scale[fp4_scale_at(a.block_tiles, static_cast<int>(row), block)] : 0u;
+  const uint32_t b1 = cut < 16 && c + cut < a.K
+                          ? a.scale[fp4_scale_at(a.block_tiles, static_cast<int>(row), block + 1)]
+                          : 0u;
+  const bool upper = c & 8;
+  const uint32_t x0 = upper ? lo.y : lo.x, x1 = upper ? hi.x : lo.y, x2 = upper ? hi.y : hi.x;
+  const uint32_t codes[2] = {__funnelshift_r(x0, x1, 4 * (c & 7)),
+                             __funnelshift_r(x1, x2, 4 * (c & 7))};
+  uint32_t v[8];
+  pairs_of(codes, v);
+  const uint32_t s0 = scale_bits(b0), s1 = scale_bits(b1);
+  const uint32_t of_first = s0 >> 16 | s0, of_both = s0 >> 16 | s1, of_second = s1 >> 16 | s1;
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    v[k] = scaled(v[k], 2 * k + 1 < cut ? of_first : 2 * k < cut ? of_both : of_second);
+  if (c >= 0 && c + 16 <= a.K) {
+    store_sector_words(y + c, v);
+    return;
+  }
+  // a row's ends: pairs, and the one element that is left over of each
+  const int first = max(-c, 0), last = min(a.K - c, 16);
+  uint32_t* at = reinterpret_cast<uint32_t*>(y + c);
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (2 * k >= first && 2 * k + 2 <= last) at[k] = v[k];
+  uint16_t* one = reinterpret_cast<uint16_t*>(at);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    if (first == 2 * k + 1) one[2 * k + 1] = static_cast<uint16_t>(v[k] >> 16);
+    if (last == 2 * k + 1) one[2 * k] = static_cast<uint16_t>(v[k]);
   }
 }
 
@@ -351,31 +472,54 @@ cudaError_t run_staged(DequantArgs a, cudaStream_t s) {
 }
 // The lanes of a piece: as few as cover a short row, and no more columns past a long one's end than
 // a quarter warp's.
+int lanes_of_piece(int K) {
+  const int tail = (K - 1) % 512 + 1;
+  if (K <= 128 || (K < 2048 && tail <= 128)) return 8;
+  return K <= 256 || (K < 4096 && tail <= 256) ? 16 : 32;
+}
 template <class T, class Args>
 cudaError_t run_staged_by(const Args& a, cudaStream_t s) {
-  const int tail = (a.K - 1) % 512 + 1;
-  if (a.K <= 128 || (a.K < 2048 && tail <= 128)) return run_staged<T, 8>(a, s);
-  if (a.K <= 256 || (a.K < 4096 && tail <= 256)) return run_staged<T, 16>(a, s);
-  return run_staged<T, 32>(a, s);
+  const int lanes = lanes_of_piece(a.K);
+  if (lanes == 8) return run_staged<T, 8>(a, s);
+  return lanes == 16 ? run_staged<T, 16>(a, s) : run_staged<T, 32>(a, s);
 }
 
 template <class T>
 cudaError_t run_quantize(QuantArgs a, cudaStream_t s) {
   const int64_t pitch = a.ldx * static_cast<int64_t>(sizeof(T));
-  if (is_aligned(a.x, 16) && (pitch % 16 == 0 || a.M == 1)) {
-    a.by = Divisor(static_cast<uint32_t>(a.blocks));
-    const dim3 grid(grid_of(static_cast<int64_t>(a.rows) * a.blocks * 2, kThreads));
-    const bool wide = is_aligned(a.x, 32) && (pitch % 32 == 0 || a.M == 1);
-    return launch(wide ? &quantize_kernel<T, 32> : &quantize_kernel<T, 16>, grid, kThreads, 0, true,
-                  s, a);
+  const bool wide = is_aligned(a.x, 16) && (pitch % 16 == 0 || a.M == 1);
+  if constexpr (sizeof(T) == 4) {
+    if (!wide) return run_staged_by<T>(a, s);
   }
-  return run_staged_by<T>(a, s);
+  a.by = Divisor(static_cast<uint32_t>(a.blocks));
+  const dim3 grid(grid_of(static_cast<int64_t>(a.rows) * a.blocks * 2, kThreads));
+  if constexpr (sizeof(T) == 2) {
+    if (!wide) return launch(&quantize_kernel<T, 2>, grid, kThreads, 0, true, s, a);
+  }
+  const bool wider = is_aligned(a.x, 32) && (pitch % 32 == 0 || a.M == 1);
+  return launch(wider ? &quantize_kernel<T, 32> : &quantize_kernel<T, 16>, grid, kThreads, 0, true,
+                s, a);
 }
 
 template <class T>
 cudaError_t run_dequantize(DequantArgs a, cudaStream_t s) {
   const bool wide = is_aligned(a.q, 8) && a.ldq % 8 == 0 && a.K % 16 == 0 &&
                     rows_by(a.y, a.ldy, sizeof(T), kVecOf<T>);
+  if constexpr (sizeof(T) == 2) {
+    // Where the pieces have half as many columns again as the row, a thread for each 32 bytes of
+    // y: 20 M elements by 63 columns 21.9 us (by pieces of 128: 28.1), by 257 18.1 (512: 26.8), by
+    // 13 41.5 (128: 108); but by 200 19.1 (256: 16.4) and by 1001 17.3 (1024: 14.5), for a
+    // row's ends are single stores.
+    const int64_t piece = 16 * lanes_of_piece(a.K);
+    if (!wide && (a.K + piece - 1) / piece * piece * 2 > int64_t{3} * a.K) {
+      a.groups = (a.K + 30) / 16;
+      a.by = Divisor(static_cast<uint32_t>(a.groups));
+      const bool whole = is_aligned(a.q, 8) && a.ldq % 8 == 0;
+      return launch(whole ? &dequantize_anywhere_kernel<true> : &dequantize_anywhere_kernel<false>,
+                    dim3(grid_of(static_cast<int64_t>(a.M) * a.groups, kThreads)), kThreads, 0, true,
+                    s, a);
+    }
+  }
   if (!wide) return run_staged_by<T>(a, s);
   a.groups = a.K / 16;
   a.by = Divisor(static_cast<uint32_t>(a.groups));
@@ -407,6 +551,7 @@ int dlrm_quantize_fp4(const void* x, int64_t ldx, int dtype, int64_t M, int64_t 
   if (!is_aligned(x, dtype_size(dtype)) || !is_aligned(scale, 4)) return DLRM_ERR_ALIGN;
   QuantArgs a = {};
   a.x = x;
+  a.end = static_cast<const uint8_t*>(x) + ((M - 1) * ldx + K) * dtype_size(dtype);
   a.q = q;
   a.scale = scale;
   a.ldx = ldx;

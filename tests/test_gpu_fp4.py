@@ -136,6 +136,31 @@ def test_buffers_that_are_given(fp4, dtype):
             assert (y[:, k:] == 5).all()
 
 
+@pytest.mark.parametrize("k", [1, 15, 16, 31, 47, 250, 513])
+def test_rows_that_start_anywhere(fp4, k):
+    """bf16 rows read and written at every offset from 32 bytes, codes at every offset from 8;
+    what lies beside them is NaN on the way in and stays on the way out."""
+    g = _gen(21)
+    m = 19
+    for start in range(0, 17):
+        pitch = k + start % 5
+        x = _normal(g, m, k, BF16, pitch, start)
+        code, byte = _expect(x)
+        width = (k + 1) // 2
+        qbuf = torch.full((m * (width + start % 3) + start + 1,), 77, device=DEV, dtype=torch.uint8)
+        q = qbuf[start:].as_strided((m, width), (width + start % 3, 1))
+        _, s = fp4.quantize_rows(x, out=q)
+        _check_rows(fp4, x, q, s)
+        ybuf = torch.full((start + m * (k + 3),), 5.0, device=DEV, dtype=BF16)
+        y = ybuf[start:].view(m, k + 3)
+        fp4.dequantize_rows(q, s, k, out=y[:, :k])
+        sign = 1 - 2 * (code >= 8).double()
+        want = sign * LEVELS.to(DEV)[code % 8] * torch.exp2(byte.double() - 127).repeat_interleave(32, 1)[:, :k]
+        assert torch.equal(y[:, :k].double(), want)
+        assert (y[:, k:] == 5).all() and (ybuf[:start] == 5).all()
+        assert (qbuf[:start] == 77).all() and qbuf[-1] == 77
+
+
 def test_every_level_and_every_tie(fp4):
     """Elements at the levels, halfway between them and next to there, at scales far apart."""
     mids = (LEVELS[1:] + LEVELS[:-1]) / 2
