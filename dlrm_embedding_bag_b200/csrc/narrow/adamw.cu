@@ -1,8 +1,9 @@
 // One AdamW step over many tensors (declared in dlrm_optim.h).
 //
-// A step reads and writes every element once and computes some 40 to 70
-// instructions on it, so it is bound by memory: 28 bytes an element for f32 with
-// 32-bit moments, 16 with 8-bit ones, 10 for bf16 with 8-bit ones. Tensors travel as pointers by
+// A step reads and writes every element once: 28 bytes an element for f32 with 32-bit
+// moments, 16 with 8-bit ones, 10 for bf16 with 8-bit ones. Bound by memory (10^6 x 64 in
+// a graph: f32 265 us of 273 by a copy's rate, with 8-bit moments 155 to 162 of 156), but
+// bf16 with 8-bit moments by instructions (148 of 98). Tensors travel as pointers by
 // value in the launch (up to kMaxTensors of them), so a network's dozens of small
 // tensors are one launch and need no copy in front of it.
 //

@@ -12,7 +12,8 @@ is no fallback.
 :func:`adamw_state` makes the buffers of a list of parameters, :func:`adamw_step`
 takes one step in place, :func:`adamw_moments` reads 8-bit moments. The step stands
 beside :func:`.tokens.embedding_grad` with ``accumulate`` (sparse SGD) and takes
-the tensors that an :class:`.mlp.MLP` holds, bf16 weights and f32 biases in one list.
+the tensors that an :class:`.mlp.MLP` holds, bf16 weights and f32 biases in one list
+(weights whose rows are padded, as :func:`.mlp.bf16_empty` makes them, as contiguous copies).
 """
 from __future__ import annotations
 
