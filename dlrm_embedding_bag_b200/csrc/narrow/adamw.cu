@@ -2,8 +2,8 @@
 //
 // A step reads and writes every element once: 28 bytes an element for f32 with 32-bit
 // moments, 16 with 8-bit ones, 10 for bf16 with 8-bit ones. Bound by memory (10^6 x 64 in
-// a graph: f32 265 us of 273 by a copy's rate, with 8-bit moments 155 to 162 of 156), but
-// bf16 with 8-bit moments by instructions (148 of 98). Tensors travel as pointers by
+// a graph: f32 263 us of 273 by a copy's rate), but with 8-bit moments by instructions (f32
+// 170 of 156, bf16 167 of 98). Tensors travel as pointers by
 // value in the launch (up to kMaxTensors of them), so a network's dozens of small
 // tensors are one launch and need no copy in front of it.
 //
@@ -186,14 +186,23 @@ __device__ __forceinline__ uint32_t upper_bytes(const uint32_t (&t)[4]) {
 
 // Root and reciprocal from the function units, within two last places: an element's step needs
 // no more of its own size.
-template <bool TINY>
 __device__ __forceinline__ float root_of(float x) {
   float r;
-  if constexpr (TINY)
-    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
-  else
-    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
+}
+// The second moment's root, which becomes a code, is the nearest f32, but for some of 2^20: one step of Newton's
+// method, r + (x - r^2) / (2 r), from r = x y, where y is about 1 / sqrt(x). 0 below 2^-126, NaN
+// of what is not finite.
+__device__ __forceinline__ float inverse_root(float x) {
+  float r;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r > 0x1.8p63f ? 0.f : r;
+}
+__device__ __forceinline__ Pair near_root(Pair x) {
+  const float2 f = parts(x);
+  const Pair y = pair(inverse_root(f.x), inverse_root(f.y)), r = mul(x, y);
+  return fma(fma(mul(r, both(-1.f)), r, x), mul(y, both(0.5f)), r);
 }
 __device__ __forceinline__ float reciprocal(float x) {
   float r;
@@ -254,23 +263,56 @@ __device__ __forceinline__ void step_block(const StepArgs& a, const Factors& f, 
       root_values(vc[h], v + 2 * h);
     }
   }
-  const Pair b1 = both(ms * f.b1), b1c = both(f.b1c), b2 = both(vs * vs * f.b2), b2c = both(f.b2c);
+  // Moments round after every product and sum, as elementary operations do: where a code
+  // goes up or down then hangs on the formula alone (and on the root below), not on what was fused.
+  // (10^6 x 64 with 8-bit moments:
+  // f32 155 -> 170 us, bf16 148 -> 167; a root off by a last place sent 1.5 of 10^6 codes the other
+  // way, and in the next step some weights with them.)
+  const Pair b1 = both(f.b1), b1c = both(f.b1c), b2 = both(f.b2), b2c = both(f.b2c);
   const Pair scale = both(f.grad_scale), keep = both(__fmaf_rn(-f.lr, t.decay, 1.f));
   const Pair alpha = both(-f.alpha), root = both(f.root), eps = both(a.eps);
   Pair r[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const Pair x = mul(g[i], scale);
-    if constexpr (BITS == 8) v[i] = mul(v[i], v[i]);  // of codes: exact
-    m[i] = fma(m[i], b1, mul(x, b1c));
-    v[i] = fma(v[i], b2, mul(mul(x, b2c), x));
-    const float2 w = parts(v[i]);
-    r[i] = pair(root_of<BITS == 32>(w.x), root_of<BITS == 32>(w.y));
+    if constexpr (BITS == 8) {
+      m[i] = mul(m[i], both(ms));
+      v[i] = mul(v[i], both(vs));
+      v[i] = mul(v[i], v[i]);
+    }
+    m[i] = add(mul(m[i], b1), mul(x, b1c));
+    v[i] = add(mul(v[i], b2), mul(mul(x, x), b2c));
+    if constexpr (BITS == 8) {
+      r[i] = near_root(v[i]);
+    } else {
+      const float2 w = parts(v[i]), y = parts(near_root(v[i]));
+      r[i] = pair(w.x >= FLT_MIN && w.x <= FLT_MAX ? y.x : root_of(w.x),
+                  w.y >= FLT_MIN && w.y <= FLT_MAX ? y.y : root_of(w.y));
+    }
+  }
+  float vf = 0.f;  // the lane's largest root, NaN if one is
+  if constexpr (BITS == 8) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 y = parts(r[i]);
+      vf = max_abs(vf, y.x, y.y);
+    }
+    if (vf != vf) {  // an infinity stays one: a square may leave f32 where its gradient does not
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 w = parts(v[i]);
+        r[i] = pair(root_of(w.x), root_of(w.y));
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
     const float2 d = parts(fma(r[i], root, eps));
     p[i] = fma(mul(m[i], pair(reciprocal(d.x), reciprocal(d.y))), alpha, mul(p[i], keep));
   }
   if constexpr (!ALL) {
     // what lies behind the tensor's end stays zero, whatever the factors are
+    vf = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int e = q[0] + 2 * i;
@@ -280,15 +322,15 @@ __device__ __forceinline__ void step_block(const StepArgs& a, const Factors& f, 
       m[i] = pair(lo ? me.x : 0.f, hi ? me.y : 0.f);
       v[i] = pair(lo ? ve.x : 0.f, hi ? ve.y : 0.f);
       r[i] = pair(lo ? re.x : 0.f, hi ? re.y : 0.f);
+      vf = max_abs(vf, lo ? re.x : 0.f, hi ? re.y : 0.f);
     }
   }
   if constexpr (BITS == 8) {
-    float mf = 0.f, vf = 0.f;
+    float mf = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 x = parts(m[i]), y = parts(r[i]);
+      const float2 x = parts(m[i]);
       mf = max_abs(mf, x.x, x.y);
-      vf = max_abs(vf, y.x, y.y);
     }
     // (of numbers that are not negative the bits' order is theirs, and NaN is above all)
     const uint32_t mtop = __reduce_max_sync(kFull, __float_as_uint(mf));
@@ -296,8 +338,8 @@ __device__ __forceinline__ void step_block(const StepArgs& a, const Factors& f, 
     mf = __uint_as_float(mtop), vf = __uint_as_float(vtop);
     const bool mbad = mtop >= 0x7f800000u, vbad = vtop >= 0x7f800000u;
     const bool live = mf >= 448.f * 0x1p-126f && !mbad;
-    const Pair minv = both(live ? __fdividef(448.f, mf) : 0.f), mlow = both(kFirstLower);
-    const Pair vinv = both(vtop != 0 && !vbad ? __fdividef(1.9375f, vf) : 0.f), vlow = both(kRootLower);
+    const Pair minv = both(live ? __fmul_rn(__frcp_rn(mf), 448.f) : 0.f), mlow = both(kFirstLower);
+    const Pair vinv = both(vtop != 0 && !vbad ? __fmul_rn(__frcp_rn(vf), 1.9375f) : 0.f), vlow = both(kRootLower);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t x[4], z[4];

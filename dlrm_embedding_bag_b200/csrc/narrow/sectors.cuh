@@ -33,6 +33,11 @@ __device__ __forceinline__ Pair mul(Pair a, Pair b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+// (One by one: a sum of pairs is fused with a product in front of it, whatever it says.)
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  const float2 x = parts(a), y = parts(b);
+  return pair(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y));
+}
 __device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c) {
   Pair r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));

@@ -285,6 +285,42 @@ def test_not_finite_gradients(optim, bits, bad):
     assert torch.equal(p.isnan(), hurt) if bits == 8 else p.isnan().sum() == 1
 
 
+def test_moments_round_as_elementary_operations_do(optim):
+    """What becomes codes is the formula's f32 value, every product, sum and root rounded once: the
+    scales bit for bit. (Nothing is fused and the root is the nearest, but for a few of 2^20.)"""
+    g = _gen(31)
+    n = 256 * 4000
+    p, grad = torch.zeros(n, device=DEV), _normal(g, (n,))
+    st = optim.adamw_state([p], bits=8)
+    m = v = torch.zeros(n, device=DEV)
+    one = torch.ones((), device=DEV)
+    for step in range(2):
+        grad = _normal(g, (n,))
+        m0, v0 = (t.view(-1, 256) for t in (st.m.float(), torch.zeros(n, device=DEV)))
+        if step:
+            c = st.v.int().view(-1, 256)
+            v0 = torch.where(c < 16, (c % 16) * 2.0 ** -18, (1 + (c % 16) / 16) * torch.exp2((c // 16 - 15).float()))
+            v0 = (v0 * st.v_scale[:, None]) ** 2
+        m0 = m0 * st.m_scale[:, None]
+        x = grad.view(-1, 256)
+        m = m0 * 0.9 + x * (1 - 0.9)
+        v = v0 * 0.999 + x * x * (1 - 0.999)
+        optim.adamw_step([p], [grad], st, lr=1e-3)
+        assert torch.equal(st.m_scale, m.abs().amax(1) * (one / 448))
+        far = st.v_scale != v.sqrt().amax(1) * (one / 1.9375)
+        assert far.sum() <= 4
+
+
+def test_squares_that_leave_f32(optim):
+    """A finite gradient whose square is infinite: no step of its element, its block's moments NaN."""
+    p, grad = torch.ones(512, device=DEV), torch.ones(512, device=DEV)
+    grad[3] = 1e25
+    st = optim.adamw_state([p], bits=8)
+    optim.adamw_step([p], [grad], st, lr=1e-3)
+    assert p[3] == 1 and p.isfinite().all() and (p[4:] < 1).all()
+    assert st.v_scale[0].isnan() and st.v_scale[1].isfinite()
+
+
 def test_first_moments_too_small_for_a_scale_are_dropped(optim):
     p = torch.zeros(256, device=DEV)
     st = optim.adamw_state([p], bits=8)
