@@ -403,20 +403,26 @@ __global__ void __launch_bounds__(kThreads) dequantize_anywhere_kernel(const Deq
   }
 }
 
+// G lanes take 16 G columns of a row, from one in front of it on where a bf16 row starts
+// between two words, so that all but its ends are stored as words (60000 x 1001
+// 40.1 us, by elements 41.4; 30000 x 1000 19.0 and 21.3).
 template <class T, int G>
 __global__ void __launch_bounds__(kThreads) dequantize_staged_kernel(const DequantArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int kWords = 4 * sizeof(T), kOfWord = 4 / sizeof(T);
   __shared__ alignas(16) Staged<T> staged[kThreads / 32];
   const int lane = threadIdx.x & 31, in = lane % G;
   const int64_t unit = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / G;
   const int64_t row = a.by.of(unit);
-  const int c0 = static_cast<int>(unit - row * a.groups) * 16 * G;
-  const int c = c0 + 16 * in;
+  T* y = static_cast<T*>(a.y) + row * a.ldy;
+  const int before = sizeof(T) == 2 ? static_cast<int>(reinterpret_cast<uintptr_t>(y) >> 1 & 1) : 0;
+  const int c0 = static_cast<int>(unit - row * a.groups) * 16 * G - before;
+  const int c = c0 + before + 16 * in;  // the lane's half block
   const int left = row < a.M ? a.K - c0 : 0;
   uint32_t w[2] = {}, byte = 0;
+  const uint8_t* q = a.q + row * a.ldq + c / 2;
   if (row < a.M && c < a.K) {
     byte = a.scale[fp4_scale_at(a.block_tiles, static_cast<int>(row), c / 32)];
-    const uint8_t* q = a.q + row * a.ldq + c / 2;
     const int bytes = (a.K - c + 1) / 2;
     if (bytes >= 8 && (reinterpret_cast<uintptr_t>(q) & 7) == 0) {
       const uint2 r = *reinterpret_cast<const uint2*>(q);
@@ -427,18 +433,41 @@ __global__ void __launch_bounds__(kThreads) dequantize_staged_kernel(const Dequa
         if (k < bytes) w[k / 4] |= static_cast<uint32_t>(q[k]) << (8 * (k % 4));
     }
   }
-  uint32_t v[4 * sizeof(T)];
-  values_of<T>(w, byte, v);
+  uint32_t v[kWords];
+  if (sizeof(T) == 2 && before != 0) {
+    // the column in front of the half block, and all of that but its last one
+    uint32_t code = 0, other = 0;
+    if (row < a.M && c > 0 && c <= a.K) {
+      code = q[-1] >> 4;
+      other = a.scale[fp4_scale_at(a.block_tiles, static_cast<int>(row), (c - 1) / 32)];
+    }
+    const uint32_t moved[2] = {w[0] << 4 | code, __funnelshift_l(w[0], w[1], 4)};
+    uint32_t two[8];
+    pairs_of(moved, two);
+    const uint32_t scale = scale_bits(byte);
+    v[0] = scaled(two[0], scale_bits(other) >> 16 | scale);
+#pragma unroll
+    for (int k = 1; k < 8; ++k) v[k] = scaled(two[k], scale >> 16 | scale);
+  } else {
+    values_of<T>(w, byte, v);
+  }
   T* mine = staged[threadIdx.x >> 5].v + lane / G * (G * Staged<T>::kLane);
   uint4* own = reinterpret_cast<uint4*>(mine + Staged<T>::at(16 * in));
 #pragma unroll
   for (int i = 0; i < static_cast<int>(sizeof(T)); ++i)
     own[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
   __syncwarp();
-  T* y = static_cast<T*>(a.y) + row * a.ldy + c0 + in;
 #pragma unroll
-  for (int j = 0; j < 16; ++j)
-    if (j * G + in < left) y[j * G] = mine[Staged<T>::at(j * G + in)];
+  for (int j = 0; j < kWords; ++j) {
+    const int e = (j * G + in) * kOfWord;
+    if (c0 + e >= 0 && e + kOfWord <= left)
+      *reinterpret_cast<uint32_t*>(y + c0 + e) =
+          *reinterpret_cast<const uint32_t*>(mine + Staged<T>::at(e));
+  }
+  if (sizeof(T) == 2 && in == 0) {
+    if (c0 < 0 && left > 0) y[0] = mine[Staged<T>::at(1)];
+    if (left > 0 && left <= 16 * G && left % 2 != 0) y[a.K - 1] = mine[Staged<T>::at(left - 1)];
+  }
 }
 
 constexpr int64_t kMost = INT_MAX - 1024;
@@ -464,7 +493,9 @@ cudaError_t run_staged(QuantArgs a, cudaStream_t s) {
 }
 template <class T, int G>
 cudaError_t run_staged(DequantArgs a, cudaStream_t s) {
-  a.groups = (a.K + 16 * G - 1) / (16 * G);
+  // bf16 rows may begin between two words
+  const bool words = sizeof(T) == 4 || (is_aligned(a.y, 4) && (a.ldy % 2 == 0 || a.M == 1));
+  a.groups = (a.K + (words ? 0 : 1) + 16 * G - 1) / (16 * G);
   a.by = Divisor(static_cast<uint32_t>(a.groups));
   return launch(&dequantize_staged_kernel<T, G>,
                 dim3(grid_of(static_cast<int64_t>(a.M) * a.groups * G, kThreads)), kThreads, 0,
@@ -507,8 +538,8 @@ cudaError_t run_dequantize(DequantArgs a, cudaStream_t s) {
                     rows_by(a.y, a.ldy, sizeof(T), kVecOf<T>);
   if constexpr (sizeof(T) == 2) {
     // Where the pieces have half as many columns again as the row, a thread for each 32 bytes of
-    // y: 20 M elements by 63 columns 21.9 us (by pieces of 128: 28.1), by 257 18.1 (512: 26.8), by
-    // 13 41.5 (128: 108); but by 200 19.1 (256: 16.4) and by 1001 17.3 (1024: 14.5), for a
+    // y: 20 M elements by 63 columns 21.8 us (by pieces of 128: 31.7), by 257 18.1 (512: 26.8), by
+    // 13 41.5 (128: 145); but by 200 19.1 (256: 17.1) and by 1001 17.3 (1024: 14.1), for a
     // row's ends are single stores.
     const int64_t piece = 16 * lanes_of_piece(a.K);
     if (!wide && (a.K + piece - 1) / piece * piece * 2 > int64_t{3} * a.K) {
