@@ -101,7 +101,8 @@ class AdamWState(NamedTuple):
     ``torch.float8_e4m3fn`` and ``v`` uint8 codes of the second moment's root (the
     format is in ``dlrm_optim.h``), with f32 ``m_scale`` and ``v_scale`` for each
     block. ``master`` (f32, flat, or None) holds the weights of bf16 parameters.
-    ``step`` is int32 ``(2,)``: steps taken, and a word of the call's own (zero).
+    ``step`` is int32 ``(2,)``: steps taken, and a word of the call's own, which a step leaves at
+    zero and finds at any number from zero on (``state.step.fill_(t)`` goes on from step t).
     """
 
     m: torch.Tensor
