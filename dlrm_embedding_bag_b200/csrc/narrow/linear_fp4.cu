@@ -837,6 +837,8 @@ __global__ void __launch_bounds__(kOneThreads) linear_one_kernel(const OneArgs a
   if (lane < R && n0 + lane < a.N) by_kind(a, PutOne{a, n0 + lane, mine});
 }
 
+constexpr int64_t kMostPitch = int64_t{1} << 40;  // in bytes: tensor maps take less
+
 struct Operands {
   const uint8_t* x;
   const uint8_t* x_scale;
@@ -852,7 +854,8 @@ cudaError_t encode_codes(CUtensorMap* map, const uint8_t* base, int64_t K, int64
   const EncodeTiledFn enc = encode_tiled();
   if (enc == nullptr) return cudaErrorNotSupported;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>((K + 1) / 2), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld)};
+  // a single row's pitch leads nowhere, and may be more than a map takes
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(rows > 1 ? ld : (K + 31) / 32 * 16)};
   const cuuint32_t box[2] = {kBK, static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t estr[2] = {1, 1};
   const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims,
@@ -934,9 +937,7 @@ cudaError_t run_linear(const Operands& op, LinArgs args, int sms, cudaStream_t s
   args.tiles_b = (args.nb + BN - 1) / BN;
   args.tiles_a = (args.na + kUnitA - 1) / kUnitA;
   const int64_t tiles = static_cast<int64_t>(args.tiles_a) * args.tiles_b;
-  if (tiles > INT_MAX || static_cast<int64_t>(args.tiles_a) * kBand > INT_MAX)
-    return cudaErrorInvalidValue;
-  args.tiles = static_cast<int>(tiles);
+  args.tiles = static_cast<int>(tiles);  // no more than of the smallest tiles, which are counted below
   args.by_band = Divisor(static_cast<uint32_t>(args.tiles_a) * kBand);
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kThreads);
@@ -1021,7 +1022,8 @@ cudaError_t launch_linear(const Operands& op, const LinArgs& args, int sms, cuda
   }
   const int size = args.y_bf16 ? 2 : 4;
   // whole 16 bytes of a row: the copy engine's stores were seen to end on those, not on elements
-  const bool lines = is_aligned(args.y, 16) && args.ldy * size % 16 == 0 && op.N * size % 16 == 0;
+  const bool lines = is_aligned(args.y, 16) && args.ldy < kMostPitch / size &&
+                     args.ldy * size % 16 == 0 && op.N * size % 16 == 0;
   const Form* best = nullptr;
   double least = 0;
   for (const Form& f : kForms) {
@@ -1056,6 +1058,9 @@ int dlrm_linear_fp4(const uint8_t* x, int64_t ldx, const uint8_t* x_scale, const
   constexpr int64_t kMost = INT_MAX - 1024;
   if (M < 0 || M > kMost || N < 1 || N > kMost || K < 1 || K > kMost) return DLRM_ERR_SHAPE;
   if (ldx < (K + 1) / 2 || ldw < (K + 1) / 2 || ldy < N) return DLRM_ERR_SHAPE;
+  if ((M > 1 && ldx >= kMostPitch) || (N > 1 && ldw >= kMostPitch)) return DLRM_ERR_SHAPE;
+  // tiles of the smallest kind, 64 x 128
+  if ((M + 63) / 64 * ((N + 127) / 128) > INT_MAX) return DLRM_ERR_SHAPE;
   if (w == nullptr || w_scale == nullptr) return DLRM_ERR_NULL;
   if (M > 0 && (x == nullptr || x_scale == nullptr || y == nullptr)) return DLRM_ERR_NULL;
   if (ldx % 16 != 0 || ldw % 16 != 0 || !is_aligned(x, 16) || !is_aligned(w, 16) ||

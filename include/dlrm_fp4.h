@@ -71,7 +71,8 @@ DLRM_API int dlrm_dequantize_fp4(const uint8_t* q, int64_t ldq, const uint8_t* s
  * Products are exact, sums are f32 (in an order that the sizes fix: equal calls give equal
  * bits), the bias and the activation are applied in f32 and the result is rounded once.
  * Requirements (DLRM_ERR_SHAPE / DLRM_ERR_ALIGN otherwise): M >= 0 (with M == 0
- * nothing is enqueued), N >= 1, K >= 1, all below 2^31 - 1024; ldx, ldw >= (K + 1) / 2,
+ * nothing is enqueued), N >= 1, K >= 1, all below 2^31 - 1024, and no more than 2^31 - 1 tiles of 64
+ * rows of x by 128 of w; ldx, ldw >= (K + 1) / 2 and below 2^40 (where there is more than one row),
  * multiples of 16, ldy >= N; x, w and the scales 16-byte aligned (the TMA loads), the
  * others aligned to their elements. Bytes of x and w past (K + 1) / 2 are never
  * used; scale bytes past the matrix must be zero, and so must the last half byte of x or
