@@ -32,6 +32,7 @@
 #include <climits>
 
 #include "fp4_common.cuh"
+#include "fp4_forms.h"
 #include "ring_landing.h"
 #include "sectors.cuh"
 #include "tcgen05_common.cuh"
@@ -980,67 +981,38 @@ cudaError_t run_one(const OneArgs& a, cudaStream_t stream) {
                 kOneThreads, 0, true, stream, a);
 }
 
-// The forms of the tensor-core kernel, with what they take on a B200 in us besides a launch: a
-// stage of a tile (`step`: 256 columns of K), a tile besides (`tile`), and what comes
-// once (`once`: filling the ring, draining the last tile, joining a cluster's parts). Fitted
-// to all forms at 31 shapes from 2 x 4096 x 4096 to 65536 x 592 -> 512 in a graph, weights
-// from HBM; the choice was the fastest form, or within 3 % of it, at all of them.
-struct Form {
-  int rows_m, rows_n;  // of a tile: channels and tokens
-  int units;           // of 148 SMs that walk tiles: all, or pairs
-  int split;
-  bool lines;          // whether it needs rows of y that start and end on 16 bytes
-  double step, tile, once;
-  cudaError_t (*run)(const Operands&, LinArgs, int, cudaStream_t);
-};
-const Form kForms[] = {
-    {128, 64, 1, 1, false, 0.349, 0.6, 0.9, run_linear<64, false, 1, false>},
-    {128, 64, 1, 2, false, 0.328, 1.9, 1.7, run_linear<64, false, 2, false>},
-    {128, 64, 1, 4, false, 0.150, 2.2, 3.0, run_linear<64, false, 4, false>},
-    {128, 128, 1, 1, false, 0.350, 1.3, 0.7, run_linear<128, false, 1, false>},
-    {128, 128, 1, 2, false, 0.331, 2.9, 1.8, run_linear<128, false, 2, false>},
-    {128, 128, 1, 4, false, 0.150, 3.2, 2.8, run_linear<128, false, 4, false>},
-    {256, 256, 2, 1, false, 0.383, 2.6, 0.8, run_linear<256, true, 1, false>},
-    {256, 256, 2, 1, true, 0.371, 1.6, 2.5, run_linear<256, true, 1, true>},
-};
+// The kernels of the forms and variants in fp4_forms.h, in their order.
+template <int I>
+cudaError_t run_form(const Operands& op, const LinArgs& a, int sms, cudaStream_t s) {
+  constexpr Fp4Form f = kFp4FormOf[I];
+  static_assert(f.rows_m == f.units * kBM, "a CTA's channels, or a pair's");
+  return run_linear<f.rows_n, f.units == 2, f.split, f.lines>(op, a, sms, s);
+}
+template <int I>
+cudaError_t run_variant(const OneArgs& a, cudaStream_t s) {
+  return run_one<kFp4OneOf[I].blocks, kFp4OneOf[I].channels>(a, s);
+}
+constexpr decltype(&run_form<0>) kRunForm[] = {run_form<0>, run_form<1>, run_form<2>, run_form<3>,
+                                               run_form<4>, run_form<5>, run_form<6>, run_form<7>};
+constexpr decltype(&run_variant<0>) kRunVariant[] = {run_variant<0>, run_variant<1>, run_variant<2>,
+                                                     run_variant<3>, run_variant<4>};
+static_assert(sizeof(kRunForm) / sizeof(kRunForm[0]) == kFp4Forms &&
+                  sizeof(kRunVariant) / sizeof(kRunVariant[0]) == kFp4Ones,
+              "one for each");
 
-// One token and weights of up to 2^25 elements take the kernel for it (16.8 M elements 5.5 us
-// and 7.0 by tensor cores, 33.5 M 10 and 10, 67 M 13.6 and 11.5); the others the form that takes
-// the least time by the figures above.
 cudaError_t launch_linear(const Operands& op, const LinArgs& args, int sms, cudaStream_t s) {
-  if (op.M == 1 && op.N * op.K <= (int64_t{1} << 25)) {
+  if (fp4_one_token(op.M, op.N, op.K)) {
     const OneArgs a = {op.x, op.x_scale, op.w, op.w_scale, args.bias, args.y, op.ldw,
                        fp4_block_tiles(op.K), static_cast<int>(op.N),
                        static_cast<int>((op.K + 31) / 32), static_cast<int>((op.K + 1) / 2),
                        args.act, args.y_bf16};
-    // Four channels a warp where that leaves four warps an SM (1024 -> 8192 3.2 us, one channel
-    // 5.0; 8192 -> 1024 7.2 and 4.9), and as many blocks a lane as a row has, two or four.
-    const bool many = op.N >= 4 * 4 * sms;
-    if (a.blocks <= 32) return many ? run_one<1, 4>(a, s) : run_one<1, 1>(a, s);
-    if (a.blocks <= 64) return many ? run_one<2, 4>(a, s) : run_one<2, 1>(a, s);
-    return many ? run_one<2, 4>(a, s) : run_one<4, 1>(a, s);
+    return kRunVariant[fp4_one(op.N, a.blocks, sms)](a, s);
   }
   const int size = args.y_bf16 ? 2 : 4;
   // whole 16 bytes of a row: the copy engine's stores were seen to end on those, not on elements
   const bool lines = is_aligned(args.y, 16) && args.ldy < kMostPitch / size &&
                      args.ldy * size % 16 == 0 && op.N * size % 16 == 0;
-  const Form* best = nullptr;
-  double least = 0;
-  for (const Form& f : kForms) {
-    if (f.lines && !lines) continue;
-    const int64_t tiles =
-        (op.M + f.rows_n - 1) / f.rows_n * ((op.N + f.rows_m - 1) / f.rows_m);
-    // a cluster's CTAs run at the same time, and each has two K blocks at least
-    if (f.split > 1 && (tiles * f.split > 128 || args.nkb < 2 * f.split)) continue;
-    const int64_t units = sms / f.units;
-    const int64_t rounds = (tiles + units - 1) / units;
-    const double us = rounds * (f.step * args.nkb / f.split + f.tile) + f.once;
-    if (best == nullptr || us < least) {
-      best = &f;
-      least = us;
-    }
-  }
-  return best->run(op, args, sms, s);
+  return kRunForm[fp4_form(op.M, op.N, args.nkb, lines, sms)](op, args, sms, s);
 }
 
 }  // namespace
