@@ -6,7 +6,7 @@ import subprocess
 import pytest
 
 from test_gpu_fp4 import LAYERS
-from test_gpu_fp4_forms import FORMS, ONES
+from test_gpu_fp4_forms import FORMS, LINES, ONES
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 NARROW = os.path.join(ROOT, "dlrm_embedding_bag_b200", "csrc", "narrow")
@@ -53,6 +53,10 @@ def test_shapes_take_the_forms_that_they_stand_for(ask):
     for kind, table in (("tiles", FORMS), ("one", ONES)):
         for form, shapes in table.items():
             assert ask(shapes, False) == [(kind, *form, 0)] * len(shapes), form
+
+
+def test_outputs_that_leave_as_whole_lines(ask):
+    assert ask(LINES, True) == [("tiles", 256, 1, 1)] * len(LINES)
 
 
 def test_no_form_is_without_a_test(ask):

@@ -57,3 +57,27 @@ def test_every_form_on_whole_numbers(fp4, form, shape):  # noqa: F811
     b = torch.randint(-99, 100, (n,), device=DEV, generator=g).float()
     y = fp4.linear_fp4(xq, xs, wq, ws, b, out=torch.empty((m, n + 3), device=DEV)[:, :n])
     assert torch.equal(y.double(), x.double() @ w.double().T + b.double())
+
+
+# (tokens, columns, channels) whose outputs, pitched, leave as whole lines through the copy engine
+LINES = [(4099, 1300, 4072), (5003, 1301, 3000), (4100, 1500, 4008), (4225, 1111, 3976)]
+
+
+@pytest.mark.parametrize("start", [16, 48])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", LINES, ids=lambda s: "x".join(map(str, s)))
+def test_whole_lines_with_a_pitch(fp4, shape, dtype, start):  # noqa: F811
+    """What lies before, between, beside and behind the output's rows stays as it was. (Rows are
+    whole 16 bytes, that start on 16 but not on 128, and their last line is not full.)"""
+    g = _gen(43)
+    m, k, n = shape
+    ops = _layer(fp4, g, m, k, n, True)
+    size = 4 if dtype == F32 else 2
+    pitch, first = n + 2 * 16 // size + 48 // size, start // size
+    assert n * size % 16 == 0 and n * size % 128 != 0 and pitch * size % 16 == 0
+    flat = torch.full((first + m * pitch + 64,), 9.0, device=DEV, dtype=dtype)
+    rows = flat[first:first + m * pitch].view(m, pitch)
+    y = fp4.linear_fp4(*ops, "relu", out=rows[:, :n])
+    _check_layer(fp4, y, *ops, "relu")
+    assert (rows[:, n:] == 9).all() and (flat[:first] == 9).all() and (flat[first + m * pitch:] == 9).all()
+    assert torch.equal(y, fp4.linear_fp4(*ops, "relu", out_dtype=dtype))
