@@ -146,13 +146,14 @@ def adamw_state(params: Sequence[torch.Tensor], *, bits: int = 32,
         for o, p in zip(at, params):
             if p.dtype == torch.bfloat16:
                 copies[o:o + p.numel()].view(p.shape).copy_(p.detach())
+    kind = torch.float32  # whatever torch's default is
     if bits == 32:
-        return AdamWState(torch.zeros(total, device=dev), torch.zeros(total, device=dev), step,
-                          master=copies)
+        return AdamWState(torch.zeros(total, dtype=kind, device=dev),
+                          torch.zeros(total, dtype=kind, device=dev), step, master=copies)
     return AdamWState(torch.zeros(total, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn),
                       torch.zeros(total, dtype=torch.uint8, device=dev), step,
-                      torch.zeros(total // BLOCK, device=dev),
-                      torch.zeros(total // BLOCK, device=dev), copies)
+                      torch.zeros(total // BLOCK, dtype=kind, device=dev),
+                      torch.zeros(total // BLOCK, dtype=kind, device=dev), copies)
 
 
 _CODES = ops.TABLE_DTYPES
