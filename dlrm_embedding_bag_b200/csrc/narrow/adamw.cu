@@ -428,15 +428,20 @@ __device__ __forceinline__ void step_warp(const StepArgs& a, const Factors& f, c
     step_block<BITS, P, G, false>(a, f, t, e0, left < kBlock ? static_cast<int>(left) : kBlock);
 }
 
+// The word that chunks are counted in. (Taken from the arguments at each use: its address in two
+// registers for the whole walk cost 1 %.)
+__device__ __forceinline__ uint32_t* counter(const StepArgs& a) {
+  return reinterpret_cast<uint32_t*>(a.step + 1);
+}
+
 template <int BITS, int ROOM>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     adamw_kernel(const __grid_constant__ ListArgs<ROOM> args) {
   const StepArgs& a = args.step;
   __shared__ Factors shared;
   __shared__ int next[2];
-  uint32_t* word = reinterpret_cast<uint32_t*>(a.step + 1);
   if (threadIdx.x == 0) {
-    if (blockIdx.x == 0) atomicMax(word, kDrawing);
+    if (blockIdx.x == 0) atomicMax(counter(a), kDrawing);
     const uint32_t t = static_cast<uint32_t>(a.step[0]) + 1u;
     const double lr = a.lr_dev != nullptr ? static_cast<double>(*a.lr_dev) : a.lr;
     shared.b1 = static_cast<float>(a.beta1);
@@ -450,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     shared.t = t;
     shared.key = mixed(mixed(a.seed + 0x9E3779B9u) ^ t);
     // (Most find it raised by now: with one maximum for each of 577 CTAs 5.8 us, so 5.6.)
-    if (*static_cast<volatile uint32_t*>(word) < kDrawing) atomicMax(word, kDrawing);
+    if (*static_cast<volatile uint32_t*>(counter(a)) < kDrawing) atomicMax(counter(a), kDrawing);
     __threadfence();  // the count is read before this CTA draws a ticket
   }
   __syncthreads();
@@ -461,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   int ti = 0;
   for (int c = blockIdx.x, turn = 0;; turn ^= 1) {
     uint32_t drawn = 0;
-    if (threadIdx.x == 0) drawn = atomicAdd(word, 1u);
+    if (threadIdx.x == 0) drawn = atomicAdd(counter(a), 1u);
     if (c < a.chunks) {
       // the last tensor that starts at c or before it: near the last one, but for the first
       // chunk
@@ -489,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       next[turn] = next_chunk(drawn, a.chunks, static_cast<int>(gridDim.x));
       if (last_ticket(drawn, a.chunks)) {
         // every CTA has read the count and drawn its last ticket
-        *word = 0;
+        *counter(a) = 0;
         if (a.last) a.step[0] = static_cast<int32_t>(f.t);
       }
     }

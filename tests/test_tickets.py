@@ -91,10 +91,11 @@ def test_the_kernel_takes_its_chunks_so():
     src = open(os.path.join(NARROW, "adamw.cu")).read()
     body = src[src.index("adamw_kernel("):]
     body = body[:body.index("\n}\n")]
-    raised = re.search(r"if \(\*static_cast<volatile uint32_t\*>\(word\) < kDrawing\) "
-                       r"atomicMax\(word, kDrawing\);\s+__threadfence\(\)", body)
+    raised = re.search(r"if \(\*static_cast<volatile uint32_t\*>\(counter\(a\)\) < kDrawing\) "
+                       r"atomicMax\(counter\(a\), kDrawing\);\s+__threadfence\(\)", body)
     places = [body.index("a.step[0]"), raised.start(), raised.end()] + [body.index(s) for s in (
-        "atomicAdd(word, 1u)", "next_chunk(drawn, a.chunks", "last_ticket(drawn, a.chunks)",
-        "*word = 0")]
+        "atomicAdd(counter(a), 1u)", "next_chunk(drawn, a.chunks", "last_ticket(drawn, a.chunks)",
+        "*counter(a) = 0")]
     assert places == sorted(places)
-    assert body.count("atomicAdd(") == body.count("word = 0") == body.count("step + 1") == 1
+    assert body.count("atomicAdd(") == body.count("counter(a) = 0") == 1
+    assert src.count("step + 1") == 1 and "step[1]" not in src
