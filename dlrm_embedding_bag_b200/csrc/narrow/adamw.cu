@@ -2,17 +2,17 @@
 //
 // A step reads and writes every element once: 28 bytes an element for f32 with 32-bit
 // moments, 16 with 8-bit ones, 10 for bf16 with 8-bit ones. Bound by memory (10^6 x 64 in
-// a graph: f32 263 us of 273 by a copy's rate), but with 8-bit moments by instructions (f32
-// 170 of 156, bf16 167 of 98). Tensors travel as pointers by
-// value in the launch (up to kMaxTensors of them), so a network's dozens of small
-// tensors are one launch and need no copy in front of it.
+// a graph: f32 262 us of 273 by a copy's rate), but with 8-bit moments by instructions (f32
+// 166 of 156, bf16 167 of 98; the integer pipe at 58 and 64 %, 0.76 and 0.83 instructions a
+// scheduler and cycle). Tensors travel as pointers by value in the launch (up to kMaxTensors
+// of them), so a network's dozens of small tensors are one launch and need no copy in front of it.
 //
 // A warp takes a block of 256 elements, a lane eight neighbours, so that its accesses are
 // few and wide (16 bytes of bf16, 8 of codes) and a block's largest moment is one warp
 // reduction. Four warps take a chunk of 1024.
 // CTAs stay, and chunks are handed out in order by a counter: walking with a fixed
 // stride, CTAs drift apart and memory sees a wider and wider window of addresses (10^6 x
-// 64 f32 with 32-bit moments 294 us, with 8-bit ones 178; by tickets 262 and 156).
+// 64 f32 with 32-bit moments 282 us, with 8-bit ones 195; by tickets 261 and 167).
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
@@ -227,7 +227,7 @@ template <int BITS, class P, class G, bool ALL>
 __device__ __forceinline__ void step_block(const StepArgs& a, const Factors& f, const Tensor& t,
                                            int64_t e0, int left) {
   const int lane = threadIdx.x & 31;
-  const int q[2] = {lane * 8, lane * 8 + 4};  // the lane's places in the block
+  const int q = lane * 8;  // the lane's first place in the block
   const uint32_t block = t.block0 + static_cast<uint32_t>(e0 / kBlock);
   const int64_t at = static_cast<int64_t>(block) * kBlock;
   P* param = static_cast<P*>(t.param) + e0;
@@ -237,23 +237,23 @@ __device__ __forceinline__ void step_block(const StepArgs& a, const Factors& f, 
   Pair p[4], g[4], m[4], v[4];
   uint32_t mc[2], vc[2];
   float ms = 1.f, vs = 1.f;  // the scales of what was read
-  load8<G, ALL>(grad + q[0], left - q[0], g);
+  load8<G, ALL>(grad + q, left - q, g);
   if (whole)
-    load8<float, true>(a.master + at + q[0], 8, p);
+    load8<float, true>(a.master + at + q, 8, p);
   else
-    load8<P, ALL>(param + q[0], left - q[0], p);
+    load8<P, ALL>(param + q, left - q, p);
   if constexpr (BITS == 8) {
-    const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.m) + at + q[0]);
-    const uint2 y = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.v) + at + q[0]);
+    const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.m) + at + q);
+    const uint2 y = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.v) + at + q);
     mc[0] = x.x, mc[1] = x.y, vc[0] = y.x, vc[1] = y.y;
   } else {
-    load8<float, true>(static_cast<const float*>(a.m) + at + q[0], 8, m);
-    load8<float, true>(static_cast<const float*>(a.v) + at + q[0], 8, v);
+    load8<float, true>(static_cast<const float*>(a.m) + at + q, 8, m);
+    load8<float, true>(static_cast<const float*>(a.v) + at + q, 8, v);
   }
   // a random word for each element, while those are on their way
   uint32_t word[8];
   if constexpr (BITS == 8 || sizeof(P) == 2) {
-    const uint32_t base = mixed(f.key ^ block) + static_cast<uint32_t>(q[0]) * 0x9E3779B9u;
+    const uint32_t base = mixed(f.key ^ block) + static_cast<uint32_t>(q) * 0x9E3779B9u;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       word[i] = mixed(base + static_cast<uint32_t>(i) * 0x9E3779B9u);
@@ -269,9 +269,8 @@ __device__ __forceinline__ void step_block(const StepArgs& a, const Factors& f, 
   }
   // Moments round after every product and sum, as elementary operations do: where a code
   // goes up or down then hangs on the formula alone (and on the root below), not on what was fused.
-  // (10^6 x 64 with 8-bit moments:
-  // f32 155 -> 170 us, bf16 148 -> 167; a root off by a last place sent 1.5 of 10^6 codes the other
-  // way, and in the next step some weights with them.)
+  // (10^6 x 64 with 8-bit moments, fused and with a root off by a last place: f32 155 us, bf16 148, so
+  // 166 and 167; that sent 1.5 of 10^6 codes the other way, and in the next step some weights with them.)
   const Pair b1 = both(f.b1), b1c = both(f.b1c), b2 = both(f.b2), b2c = both(f.b2c);
   const Pair scale = both(f.grad_scale), keep = both(__fmaf_rn(-f.lr, t.decay, 1.f));
   const Pair alpha = both(-f.alpha), root = both(f.root), eps = both(a.eps);
@@ -319,7 +318,7 @@ __device__ __forceinline__ void step_block(const StepArgs& a, const Factors& f, 
     vf = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int e = q[0] + 2 * i;
+      const int e = q + 2 * i;
       const float2 pe = parts(p[i]), me = parts(m[i]), ve = parts(v[i]), re = parts(r[i]);
       const bool lo = e < left, hi = e + 1 < left;
       p[i] = pair(lo ? pe.x : 0.f, hi ? pe.y : 0.f);
@@ -372,9 +371,9 @@ __device__ __forceinline__ void step_block(const StepArgs& a, const Factors& f, 
         if (z.y > 0.f && (vc[h] & 0xff000000u) == 0) vc[h] |= 1u << 24;
       }
     }
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.m) + at + q[0]) =
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.m) + at + q) =
         live ? make_uint2(mc[0], mc[1]) : make_uint2(0u, 0u);
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v) + at + q[0]) =
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.v) + at + q) =
         vbad ? make_uint2(0u, 0u) : make_uint2(vc[0], vc[1]);
     if (lane == 0) {
       const float nan = __uint_as_float(0x7fc00000u);
@@ -382,11 +381,11 @@ __device__ __forceinline__ void step_block(const StepArgs& a, const Factors& f, 
       a.v_scale[block] = vbad ? nan : vf * (1.f / 1.9375f);
     }
   } else {
-    store8<float, true>(static_cast<float*>(a.m) + at + q[0], 8, m);
-    store8<float, true>(static_cast<float*>(a.v) + at + q[0], 8, v);
+    store8<float, true>(static_cast<float*>(a.m) + at + q, 8, m);
+    store8<float, true>(static_cast<float*>(a.v) + at + q, 8, v);
   }
   if (whole) {
-    store8<float, true>(a.master + at + q[0], 8, p);
+    store8<float, true>(a.master + at + q, 8, p);
   } else if constexpr (sizeof(P) == 2) {
     uint32_t b[4];
     float top = 0.f;
@@ -405,16 +404,16 @@ __device__ __forceinline__ void step_block(const StepArgs& a, const Factors& f, 
       }
     }
     if constexpr (ALL) {
-      *reinterpret_cast<uint4*>(param + q[0]) = make_uint4(b[0], b[1], b[2], b[3]);
+      *reinterpret_cast<uint4*>(param + q) = make_uint4(b[0], b[1], b[2], b[3]);
     } else {
-      uint16_t* at_p = reinterpret_cast<uint16_t*>(param + q[0]);
+      uint16_t* at_p = reinterpret_cast<uint16_t*>(param + q);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (q[0] + i < left) at_p[i] = static_cast<uint16_t>(b[i / 2] >> (16 * (i % 2)));
+        if (q + i < left) at_p[i] = static_cast<uint16_t>(b[i / 2] >> (16 * (i % 2)));
     }
     return;
   }
-  store8<P, ALL>(param + q[0], left - q[0], p);
+  store8<P, ALL>(param + q, left - q, p);
 }
 
 template <int BITS, class P, class G>

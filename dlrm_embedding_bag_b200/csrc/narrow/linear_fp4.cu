@@ -684,10 +684,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // One token: R channels a warp, a lane for each block of 32 columns, U of them at a time.
 // Codes become twice their values as 8-bit integers (a byte permutation looks four up in a
 // register pair), four products an instruction; a block's sum is exact in int32 and scaled
-// once. The token's codes are looked up once a warp and stay in registers, and all of a
-// warp's weights are on their way before the first is used. Bound by the pipe of those
-// permutations before memory is (4096 x 4096: 5.5 us with weights from HBM, 4.8 from L2; 1.4
-// by its bytes).
+// once. The token's codes are looked up once for the warp's channels. A trip over the row takes 32 U
+// blocks, and its weights are on their way before the first of them is used; the next trip's are not.
+// Bound by latency: 4096 x 4096 takes 4.9 us with weights in L2 and 5.7 with weights from HBM, 1.4 by
+// its bytes. It is two trips by 1.7 CTAs an SM; 0.31 instructions a scheduler and cycle of 1.7
+// warps, which wait for loads most, and the pipe of the permutations at 30 %.
 constexpr int kOneThreads = 128;
 
 struct OneArgs {

@@ -9,8 +9,9 @@
 // A thread takes half a block, 16 elements, and a block's two threads exchange their
 // maxima. Where rows start on 16 bytes it reads them in accesses of 16 or 32 bytes (16384 x
 // 4096 bf16 28.8 us of 25.9 by their bytes; values back 28.1 of 25.9). bf16 rows that start
-// anywhere it reads as the 64-bit words around them and moves those down (60000 x 1001 37.7 us of
-// 23.2; by neighbouring elements through shared memory 43.8). f32 rows that start anywhere lanes
+// anywhere it reads as the 64-bit words around them and moves those down (60000 x 1001 37.6 us of
+// 23.2, the integer pipe that moves them at 76 %; by neighbouring elements through shared memory
+// 43.8). f32 rows that start anywhere lanes
 // read by neighbouring elements, whole lines, and lay them out in shared memory from
 // where each takes its own 16 (45.3 us of 41.5); values go back the same way, or in
 // aligned words of the row (below).
@@ -405,7 +406,7 @@ __global__ void __launch_bounds__(kThreads) dequantize_anywhere_kernel(const Deq
 
 // G lanes take 16 G columns of a row, from one in front of it on where a bf16 row starts
 // between two words, so that all but its ends are stored as words (60000 x 1001
-// 40.1 us, by elements 41.4; 30000 x 1000 19.0 and 21.3).
+// 40.1 us, by elements 41.4; 30000 x 1000 18.8 and 21.3; the integer pipe at 78 %).
 template <class T, int G>
 __global__ void __launch_bounds__(kThreads) dequantize_staged_kernel(const DequantArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -11,9 +11,10 @@ is no fallback.
 
 :func:`adamw_state` makes the buffers of a list of parameters, :func:`adamw_step`
 takes one step in place, :func:`adamw_moments` reads 8-bit moments. The step stands
-beside :func:`.tokens.embedding_grad` with ``accumulate`` (sparse SGD) and takes
-the tensors that an :class:`.mlp.MLP` holds, bf16 weights and f32 biases in one list
-(weights whose rows are padded, as :func:`.mlp.bf16_empty` makes them, as contiguous copies).
+beside :func:`.tokens.embedding_grad` with ``accumulate`` (sparse SGD). It takes
+contiguous tensors, bf16 and f32 in one list: a table, an :class:`.mlp.MLP`'s biases and those
+of its weights whose columns are a multiple of 8. Weights of other widths have padded rows
+(:func:`.mlp.bf16_empty`) and are refused: a contiguous copy is stepped and copied back.
 """
 from __future__ import annotations
 

@@ -40,7 +40,8 @@ extern "C" {
 #define DLRM_FP4_BLOCK 32
 
 /* Bytes of the scales of an (M, K) matrix, or DLRM_ERR_SHAPE. M 0 .. 2^31 - 1025,
- * K 1 .. 2^31 - 1025. */
+ * K 1 .. 2^31 - 1025, and M K, both rounded up to multiples of 128, at most 2^38 (M K itself below
+ * it); so it is for the two calls below. */
 DLRM_API int64_t dlrm_fp4_scale_bytes(int64_t M, int64_t K);
 
 /* dlrm_quantize_fp4 -- (q, scale) of the rows of x.

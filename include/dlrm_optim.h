@@ -89,7 +89,9 @@ DLRM_API int dlrm_adamw_step(int64_t n, void* const* params, const void* const* 
                              dlrm_stream_t stream);
 
 /* dlrm_adamw_moments -- the 8-bit moments of `count` arena elements (a multiple of
- * DLRM_ADAMW_BLOCK) as values of dtype, rounded once: m_out and v_out dev, 32-byte aligned. */
+ * DLRM_ADAMW_BLOCK) as values of dtype: m_out and v_out dev, 32-byte aligned. The first is a code
+ * times its scale and the second the square of such a product, each product rounded to f32, as a
+ * step reads them; both are then rounded to dtype. */
 DLRM_API int dlrm_adamw_moments(int64_t count, const void* m, const void* v, const float* m_scale,
                                 const float* v_scale, void* m_out, void* v_out, int dtype,
                                 dlrm_stream_t stream);

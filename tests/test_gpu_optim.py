@@ -11,6 +11,10 @@ decay's factor, its product, the sum): 4 u. A result in bf16 from a master is 2^
 it; at random, it is one of the two neighbours: less than 2^-7. 8-bit moments are one of
 the two neighbours on their grid: within a step of the exact ones, 2^-3 (first) or 2^-4
 (root) relative, plus what f32 adds (16 u of the block's largest).
+
+Products and sums that round each by itself are within the same bounds: of the first moment b1 m
+rounds as a factor, a product and a sum (3 u), the gradient once as it is scaled besides (4 u); of the
+second b2 v 3 u, the square 2 u by its gradient, and by itself, its factor, product and sum 4 u.
 """
 from __future__ import annotations
 
