@@ -454,7 +454,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
     shared.t = t;
     shared.key = mixed(mixed(a.seed + 0x9E3779B9u) ^ t);
     // (Most find it raised by now: with one maximum for each of 577 CTAs 5.8 us, so 5.6.)
-    if (*static_cast<volatile uint32_t*>(counter(a)) < kDrawing) atomicMax(counter(a), kDrawing);
+    const uint32_t seen = *static_cast<volatile uint32_t*>(counter(a));
+    if (!raised(seen)) atomicCAS(counter(a), seen, kDrawing);
     __threadfence();  // the count is read before this CTA draws a ticket
   }
   __syncthreads();
@@ -573,7 +574,7 @@ int dlrm_adamw_step(int64_t n, void* const* params, const void* const* grads,
     if (counts[i] < 0 || counts[i] >= (int64_t{1} << 40)) return DLRM_ERR_SHAPE;
     blocks += (counts[i] + kBlock - 1) / kBlock;
     chunks += (counts[i] + kChunk - 1) / kChunk;
-    if (blocks >= (int64_t{1} << 32) || chunks > (1 << 30)) return DLRM_ERR_SHAPE;
+    if (blocks >= (int64_t{1} << 32) || chunks > int64_t{kMostTickets}) return DLRM_ERR_SHAPE;
     if (!known_dtype(param_dtypes[i]) || !known_dtype(grad_dtypes[i])) return DLRM_ERR_ARG;
     if (decays != nullptr && !std::isfinite(decays[i])) return DLRM_ERR_ARG;
     if (counts[i] == 0) continue;

@@ -103,7 +103,8 @@ class AdamWState(NamedTuple):
     format is in ``dlrm_optim.h``), with f32 ``m_scale`` and ``v_scale`` for each
     block. ``master`` (f32, flat, or None) holds the weights of bf16 parameters.
     ``step`` is int32 ``(2,)``: steps taken, and a word of the call's own, which a step leaves at
-    zero and finds at any number from zero on (``state.step.fill_(t)`` goes on from step t).
+    zero and finds at any number above -2^30 (``state.step.fill_(t)`` goes on from step t, and
+    ``state.step.sub_(1)`` from the one before).
     """
 
     m: torch.Tensor

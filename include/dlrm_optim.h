@@ -70,8 +70,8 @@ extern "C" {
  *                  bf16 parameter is rounded at random, as the moments are.
  *   step           dev int32[2]: steps taken so far (>= 0), and a word of the call's own, in which
  *                  its CTAs count what they take. t = step[0] + 1; the call writes it back,
- *                  and the word to 0. A word that is not negative may hold anything before
- *                  a call: both numbers may be set to a count.
+ *                  and the word to 0. The word may hold anything above -2^30 before a call:
+ *                  both numbers may be set to a count, or counted up or down.
  *   lr             learning rate, finite; lr_dev (dev f32) is taken instead if it is not NULL.
  *   beta1, beta2   in [0, 1); eps: a normal positive number of f32.
  *   grad_scale_dev dev f32 that every gradient is multiplied with (a clipping

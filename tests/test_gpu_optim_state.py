@@ -40,8 +40,8 @@ LISTS = [[(5,)], [(3000,), (0,), (1025, 3)], [(300, 1000)], [(4000, 1000), (17,)
 @pytest.mark.parametrize("sizes", LISTS, ids=["one", "few", "wave", "many", "launches"])
 @pytest.mark.parametrize("bits", [8, 32])
 def test_a_count_that_is_set(optim, bits, sizes):
-    """Both numbers filled with the count, or raised by one, or the word left at anything that is not
-    negative: every element is stepped once, and the word is zero again."""
+    """Both numbers filled with the count, or counted up or down, or the word left at anything above
+    -2^30: every element is stepped once, and the word is zero again."""
     g = _gen(1)
     params = [_normal(g, s, BF16 if i % 2 else F32) for i, s in enumerate(sizes)]
     grads = [_normal(g, s) for s in sizes]
@@ -74,7 +74,9 @@ def test_a_count_that_is_set(optim, bits, sizes):
         assert same(clean, filled) == t + 2
     # a step that is left out of the count's steps, by a sum over both numbers
     assert same(lambda step, i: step[0].add_(1), lambda step, i: step.add_(1)) == 6
-    for word in (1, 2, 3906, (1 << 31) - 1):
+    # a step taken back
+    assert same(lambda step, i: step[0].sub_(int(i > 0)), lambda step, i: step.sub_(int(i > 0))) == 1
+    for word in (1, 2, 3906, (1 << 31) - 1, -1, -2, -3907, 1 - (1 << 30)):
         assert same(lambda step, i: None, lambda step, i, w=word: step[1].fill_(w)) == 3
 
 

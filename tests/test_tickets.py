@@ -25,15 +25,19 @@ static long checks = 0;
   } while (0)
 
 // One launch by `ctas` threads: how often each chunk was taken, how often the word was put back.
-static void launch(uint32_t at, int chunks, int ctas, bool negative) {
+static void launch(uint32_t at, int chunks, int ctas, bool left_raised) {
   std::atomic<uint32_t> word(at);
   std::unique_ptr<std::atomic<int>[]> taken(new std::atomic<int>[chunks + 1]);
   for (int i = 0; i <= chunks; ++i) taken[i] = 0;
   std::atomic<int> ends(0), outside(0), draws(0);
   auto cta = [&](int number) {
-    uint32_t seen = word;
-    while (seen < dlrm::kDrawing && !word.compare_exchange_weak(seen, dlrm::kDrawing)) {
+    if (number == 0) {  // the first one's maximum
+      uint32_t was = word;
+      while (was < dlrm::kDrawing && !word.compare_exchange_weak(was, dlrm::kDrawing)) {
+      }
     }
+    uint32_t seen = word;
+    if (!dlrm::raised(seen)) word.compare_exchange_strong(seen, dlrm::kDrawing);
     for (int c = number;;) {
       const uint32_t drawn = word.fetch_add(1);
       ++draws;
@@ -53,7 +57,7 @@ static void launch(uint32_t at, int chunks, int ctas, bool negative) {
   for (int i = 0; i < ctas; ++i) all.emplace_back(cta, i);
   for (auto& t : all) t.join();
   CHECK(outside == 0);
-  if (negative) return;
+  if (left_raised) return;
   CHECK(ends == 1 && word == 0);
   CHECK(draws == (chunks > 0 ? chunks : 1));
   for (int i = 0; i < chunks; ++i) CHECK(taken[i] == 1);
@@ -63,10 +67,10 @@ int main() {
   for (int chunks : {0, 1, 2, 7, 8, 9, 100, 1000}) {
     for (int ctas : {1, 2, 8, 16}) {
       if (ctas > (chunks > 1 ? chunks : 1)) continue;  // a launch has no more of them
-      for (uint32_t at : {0u, 1u, 5u, 99u, 999u, 1000u, 1001u, 2000000000u, 0x7fffffffu})
+      for (uint32_t at : {0u, 1u, 5u, 99u, 999u, 1000u, 1001u, 2000000000u, 0x7fffffffu, 0xffffffffu, 0xfffffff0u, 0xfffffc00u, 0xc0000001u})
         for (int again = 0; again < 3; ++again) launch(at, chunks, ctas, false);
-      // negative ones: chunks may be missed, but none is taken that is not there
-      for (uint32_t at : {0x80000000u, 0x80000001u, 0xfffffff0u, 0xffffffffu}) launch(at, chunks, ctas, true);
+      // left raised: chunks may be missed, but none is taken that is not there
+      for (uint32_t at : {0x80000000u, 0x80000001u, 0x80000064u, 0xbfffffffu, 0xc0000000u}) launch(at, chunks, ctas, true);
     }
   }
   std::printf("%ld\n", checks);
@@ -91,8 +95,9 @@ def test_the_kernel_takes_its_chunks_so():
     src = open(os.path.join(NARROW, "adamw.cu")).read()
     body = src[src.index("adamw_kernel("):]
     body = body[:body.index("\n}\n")]
-    raised = re.search(r"if \(\*static_cast<volatile uint32_t\*>\(counter\(a\)\) < kDrawing\) "
-                       r"atomicMax\(counter\(a\), kDrawing\);\s+__threadfence\(\)", body)
+    raised = re.search(r"const uint32_t seen = \*static_cast<volatile uint32_t\*>\(counter\(a\)\);\s+"
+                       r"if \(!raised\(seen\)\) atomicCAS\(counter\(a\), seen, kDrawing\);\s+"
+                       r"__threadfence\(\)", body)
     places = [body.index("a.step[0]"), raised.start(), raised.end()] + [body.index(s) for s in (
         "atomicAdd(counter(a), 1u)", "next_chunk(drawn, a.chunks", "last_ticket(drawn, a.chunks)",
         "*counter(a) = 0")]
