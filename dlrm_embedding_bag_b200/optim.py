@@ -240,10 +240,13 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor], st
         raise ValueError(f"grads must have {n} entries (got {len(grads)})")
     pp, pc = _list(params, "params", index)
     pg, gc = _list(grads, "grads", index)
-    if len(set(pp)) != n:  # (empty ones have no address)
-        i = next((i for i in range(n) if pp[i] and pp[i] in pp[:i]), None)
-        if i is not None:
-            raise ValueError(f"params[{i}] is there twice")
+    if len(set(pp)) != n:
+        known = set()
+        for i, p in enumerate(pp):
+            if p in known:
+                raise ValueError(f"params[{i}] is there twice")
+            if p:  # (empty ones have no address)
+                known.add(p)
     if list(map(_shape_of, params)) != list(map(_shape_of, grads)):
         i = next(i for i in range(n) if params[i].shape != grads[i].shape)
         raise ValueError(f"grads[{i}] must be {tuple(params[i].shape)} (got {tuple(grads[i].shape)})")
