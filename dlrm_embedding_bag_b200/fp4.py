@@ -131,7 +131,8 @@ def linear_fp4(x_q: torch.Tensor, x_scale: torch.Tensor, w_q: torch.Tensor, w_sc
 
     ``(x_q, x_scale)`` is an ``(M, K)`` and ``(w_q, w_scale)`` an ``(N, K)`` matrix (pitch a
     multiple of 16; where K is odd the last half byte is zero, as
-    :func:`quantize_rows` leaves it), ``bias`` ``(N,)`` f32 or None. Products are
+    :func:`quantize_rows` leaves it, so that rows of an odd K pass for rows of one column
+    more, a zero), ``bias`` ``(N,)`` f32 or None. Products are
     exact, sums, bias and activation f32. The result is f32 or bf16: ``out``, or a new
     tensor of ``out_dtype``. ``status`` (one int32) gets ``FLAG_TIMEOUT`` OR-ed in if a
     wait of the kernel ran out.

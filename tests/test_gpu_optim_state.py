@@ -95,3 +95,34 @@ def test_a_captured_step_goes_on_from_a_count(optim):
         optim.adamw_step([q], [grad], want, lr=1e-3)
         assert torch.equal(p, q) and st.step.tolist() == want.step.tolist()
     assert st.step.tolist() == [43, 0]
+
+
+def test_elements_past_the_32_bit_count(optim):
+    """A tensor of 2^32 + 777 elements and one behind it in the arena: the first one's end has the scales
+    that it has alone, the other (f32, without random rounding) the weights."""
+    n, tail = (1 << 32) + 777, 3000
+    p, grad = (torch.zeros(n, device=DEV, dtype=BF16) for _ in range(2))
+    g = _gen(3)
+    p[-tail:], grad[-tail:] = _normal(g, (tail,), BF16), _normal(g, (tail,), BF16)
+    w, gw = _normal(g, (700,)), _normal(g, (700,))
+    at = (n - tail) // 256 * 256
+    q, gq, u = p[at:].clone(), grad[at:].clone(), w.clone()
+    st = optim.adamw_state([p, w], bits=8)
+    optim.adamw_step([p, w], [grad, gw], st, lr=1e-2)
+    alone = optim.adamw_state([q, u], bits=8)
+    optim.adamw_step([q, u], [gq, gw], alone, lr=1e-2)
+    assert torch.equal(w, u)
+    assert torch.equal(st.m_scale[at // 256:], alone.m_scale)
+    assert torch.equal(st.v_scale[at // 256:], alone.v_scale)
+    # each is one of the two neighbours
+    assert ((p[at:].float() - q.float()).abs() <= 2.0 ** -7 * q.float().abs()).all()
+    # a zero stays: its block has no moments. (Counted in parts.)
+    assert all((part == 0).all() for part in p[:at].split(1 << 30))
+    m, _ = optim.adamw_moments(st, dtype=BF16)
+    assert all((part == 0).all() for part in m[:at].split(1 << 30))
+    one, _ = optim.adamw_moments(alone, dtype=F32)
+    # Chance may take the other neighbour: a step, 2^-3 of the larger one (below the least normal code
+    # 2^-9 of the scale); and bf16 rounds by 2^-8.
+    size = one.abs().view(-1, 256).amax(1, keepdim=True).expand(-1, 256).reshape(-1)
+    far, last = (m[at:].float() - one).abs(), m[at:].float().abs()
+    assert (far <= (2.0 ** -3 + 2.0 ** -7) * torch.maximum(last, one.abs()) + 2.0 ** -9 * size / 448).all()
